@@ -63,7 +63,8 @@ typedef enum sp_status {
     SP_ERR_WORKSPACE = 3,     /* workspace null, misaligned (256 B) or smaller than required */
     SP_ERR_CUDA = 4,          /* a CUDA runtime call or launch failed */
     SP_ERR_TIMEOUT = 5,       /* (device status) a bounded device wait gave up */
-    SP_ERR_DEVICE = 6         /* (device status) the kernel found an inconsistent input */
+    SP_ERR_DEVICE = 6,        /* (device status) the kernel found an inconsistent input */
+    SP_ERR_CAPACITY = 7       /* (device status) the free list holds too few blocks */
 } sp_status;
 
 enum { SP_MODE_FIXED = 0, SP_MODE_MASS = 1 };
@@ -404,6 +405,173 @@ int sp_specprefill_score(const sp_shape* shape, const sp_params* params,
                          uint8_t* chunk_keep, int32_t* kept_idx, int32_t* kept_pos,
                          int32_t* kept_off, int32_t* n_kept, void* ws, size_t ws_bytes,
                          sp_stream_t stream, const sp_profile* prof);
+
+/* ---------------------------------------------------------------------
+ * Sparse prefill on a block-paged cache ("SpecPrefill — Implementation
+ * Guide", §How It Works / Sparse Prefill: the target prefills only the kept
+ * tokens, each at its original position ID, and then decodes). Three
+ * operators carry a step of the target from the kept lists above:
+ *
+ *   sp_block_tables     cache blocks and slots for the step's new tokens,
+ *                       from lengths that only the device knows (kept_off)
+ *   sp_append_kv        queries and keys rotated to their original positions
+ *                       (kept_pos), keys and values stored at those slots
+ *   sp_paged_attention  attention of the new tokens over their requests'
+ *                       cached tokens, the new ones included
+ *
+ * A cache layer is a key pool and a value pool of pool_tokens rows (blocks of
+ * block_size rows) in the layout of sp_kv_source; block_table (device,
+ * [n_seqs][table_stride] int32) maps logical block j of request b to pool
+ * block block_table[b * table_stride + j]. The pages have no counterpart of
+ * these operators; the paged layout is that of sp_kv_source.
+ *
+ * A request's cached tokens are its kept tokens in increasing original
+ * position, so causality over cache indices is causality over positions.
+ */
+enum { SP_DTYPE_BF16 = 0, SP_DTYPE_F16 = 1 };
+
+typedef struct sp_block_shape {
+    int32_t n_seqs;        /* 1 <= B <= 16384 requests (SP_ERR_UNSUPPORTED above) */
+    int32_t block_size;    /* >= 1 tokens of a block */
+    int32_t table_stride;  /* >= 1 table entries of a request */
+    int32_t n_tokens;      /* >= 0 entries of slot_map; the step's new tokens may be fewer */
+    int32_t free_capacity; /* >= 0 entries of free_blocks */
+    int32_t pool_blocks;   /* >= 1 blocks of the pool; pool_blocks * block_size <= 2^31 - 1 */
+} sp_block_shape;
+
+/* Block tables and slots of a step. Request b holds ctx_len[b] cached tokens
+ * (in ceil(ctx_len[b] / block_size) blocks, the first entries of its table
+ * row) and gets new_off[b+1] - new_off[b] new ones.
+ * - ctx_len (device, B int32), new_off (device, B+1 int32, from 0, at most
+ *   n_tokens; kept_off of the scoring call, or 0..B for a decode step).
+ * - free_blocks (device, free_capacity int32), n_free (device, one int32):
+ *   the free block ids are free_blocks[0, *n_free). Blocks are taken from
+ *   the end, request by request and in order within a request, so
+ *   free_blocks[0, *n_left) are the ones that stay free.
+ * - block_table (device, in/out): the entries of the blocks taken are
+ *   written, all others keep their values.
+ * - slot_map (device, n_tokens int32): pool row of every new token, in
+ *   order; -1 behind the last one.
+ * - kv_len (device, B int32): ctx_len plus the new tokens.
+ * - n_left (device, one int32): blocks that stay free.
+ * - status (device, one int32, nullable): raised to SP_ERR_CAPACITY when
+ *   n_free is too small, to SP_ERR_DEVICE when a length, an offset or n_free
+ *   is out of range or a request outgrows its table row; the call then takes
+ *   no block, leaves the table as it was, sets kv_len to 0 and every slot to
+ *   -1. A block id outside [0, pool_blocks) also raises SP_ERR_DEVICE; the
+ *   tokens of that block get slot -1. The word is never lowered: zero it
+ *   before the first call.
+ * Nothing is allocated and no other memory is used, so a captured call can
+ * be replayed. Outputs may not overlap inputs (block_table aside) or one
+ * another: equal pointers are SP_ERR_INVALID_ARG. */
+int sp_block_tables(const sp_block_shape* shape, const int32_t* ctx_len, const int32_t* new_off,
+                    const int32_t* free_blocks, const int32_t* n_free, int32_t* block_table,
+                    int32_t* slot_map, int32_t* kv_len, int32_t* n_left, int32_t* status,
+                    sp_stream_t stream);
+
+/* Shapes and strides (in elements, head_dim contiguous) of sp_append_kv. */
+typedef struct sp_append_shape {
+    int32_t n_tokens;      /* >= 1 rows of q, k, v and slot_map */
+    int32_t n_q_heads;     /* >= 1 with queries; ignored without */
+    int32_t n_kv_heads;    /* >= 1 */
+    int32_t head_dim;      /* a multiple of 16, at most 1024 */
+    int32_t rotary_dim;    /* 0 (no rotation) or a multiple of 16, at most head_dim */
+    int32_t max_pos;       /* rows of cos_sin (ignored when rotary_dim is 0) */
+    int32_t dtype;         /* SP_DTYPE_BF16 or SP_DTYPE_F16, of every tensor */
+    int32_t reserved;      /* 0 */
+    int64_t pool_tokens;   /* rows of each pool */
+    int64_t q_stride_token, q_stride_head, qo_stride_token, qo_stride_head;
+    int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
+    int64_t kp_stride_token, kp_stride_head, vp_stride_token, vp_stride_head;
+} sp_append_shape;
+
+/* Rotation and cache store of the new tokens of one layer. Row t of q and k
+ * is rotated to position positions[t] (rotate-half layout: elements j and
+ * j + rotary_dim/2, j < rotary_dim/2, become a cos - b sin and b cos + a sin,
+ * in 32 bits and rounded once; the others are copied); rotated queries go to
+ * row t of q_out, rotated keys and the values to pool row slot_map[t].
+ * - q, q_out (device, nullable together): [n_tokens][n_q_heads][head_dim];
+ *   q_out may be q itself with the same strides.
+ * - k, v (device): [n_tokens][n_kv_heads][head_dim]; k_pool, v_pool (device):
+ *   [pool_tokens][n_kv_heads][head_dim].
+ * - slot_map (device, n_tokens int32): -1 stores nothing (queries are still
+ *   rotated). Slots of different rows must differ, as sp_block_tables makes
+ *   them: a slot given twice holds a mixture of both rows.
+ * - positions (device, n_tokens int32) and cos_sin (device, fp32,
+ *   [max_pos][rotary_dim]: rotary_dim/2 cosines, then as many sines):
+ *   required when rotary_dim > 0.
+ * - n_new (device, one int32, nullable): the rows in use, clamped to
+ *   [0, n_tokens]; rows behind are neither read nor written.
+ * - status (device, one int32, nullable): raised to SP_ERR_DEVICE by a slot
+ *   at or past pool_tokens (nothing is stored for the row) or a position
+ *   outside [0, max_pos) (the row is skipped). Never lowered.
+ * Base pointers are 16-byte aligned and strides multiples of 8
+ * (SP_ERR_UNSUPPORTED otherwise). */
+int sp_append_kv(const sp_append_shape* shape, const uint16_t* q, const uint16_t* k,
+                 const uint16_t* v, const int32_t* slot_map, const int32_t* positions,
+                 const float* cos_sin, const int32_t* n_new, uint16_t* q_out, uint16_t* k_pool,
+                 uint16_t* v_pool, int32_t* status, sp_stream_t stream);
+
+/* Shapes and strides (in elements, head_dim contiguous) of
+ * sp_paged_attention. */
+typedef struct sp_paged_shape {
+    int32_t n_seqs;        /* 1 <= B <= 65536 requests */
+    int32_t n_q_heads;     /* Hq, Hq % Hk == 0, G = Hq / Hk <= 128 */
+    int32_t n_kv_heads;    /* Hk >= 1 */
+    int32_t head_dim;      /* d in {64, 128, 256} */
+    int32_t dtype;         /* SP_DTYPE_BF16 or SP_DTYPE_F16: q, pools and out */
+    int32_t block_size;    /* 8, 16, 32, 64 or a multiple of 128 */
+    int32_t table_stride;  /* >= 1 table entries of a request */
+    int32_t n_tokens;      /* >= 1 rows of q, out and lse; q_off[B] may be less */
+    int64_t pool_tokens;   /* rows of each pool, at most 2^31 - 1 */
+    int64_t q_stride_token, q_stride_head, o_stride_token, o_stride_head;
+    int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
+} sp_paged_shape;
+
+typedef struct sp_attn_params {
+    int32_t causal;        /* 1: a new token sees the cached tokens up to itself; 0: all of them */
+    int32_t window;        /* with causal: > 0 sees only the last `window` of those; 0: all */
+    float scale;           /* logit scale; 0 selects 1/sqrt(head_dim) */
+    int32_t spin_limit;    /* polls before a device wait gives up; <= 0 selects the default */
+} sp_attn_params;
+
+/* Bytes of device workspace of sp_paged_attention for this shape on the
+ * current device. The workspace is 256-byte aligned; prepare it once with
+ * sp_workspace_init, read its status with sp_get_device_status. Calls that
+ * share a workspace must be ordered (one stream, or events). */
+int sp_paged_attention_workspace(const sp_paged_shape* shape, size_t* bytes);
+
+/* Attention of new tokens over a block-paged cache: request b's new tokens
+ * are rows [q_off[b], q_off[b+1]) of q, the last of its kv_len[b] cached
+ * tokens (stored before this call). Row i of request b, at cache index
+ * p = kv_len[b] - (q_off[b+1] - q_off[b]) + i, sees the cached tokens j with
+ *   j <= p and (window == 0 or j > p - window)     when causal, else all,
+ * and every query head h of it gives, over the tokens it sees,
+ *   out = sum_j exp(s_j - m) v_j / sum_j exp(s_j - m),  s_j = scale <q, k_j>,
+ *   lse = m + log(sum_j exp(s_j - m)),                  m = max_j s_j,
+ * with keys and values of KV head h / G. A row that sees no token (p < 0, or
+ * a request without cached tokens) gives out = 0 and lse = -inf.
+ * - q_off (device, B+1 int32, from 0, at most n_tokens): lengths from one
+ *   token (a decode step) to a whole prompt, mixed in one call; 0 is allowed.
+ * - kv_len (device, B int32): from sp_block_tables. It may be smaller than
+ *   the number of new tokens (the first of them then see nothing).
+ * - q (device): [n_tokens][Hq][d]; out (device): the same shape; lse (device,
+ *   fp32 [n_tokens][Hq] dense, nullable). Rows at and behind q_off[B] are not
+ *   written.
+ * - Logits, softmax statistics and sums are held in 32 bits; the weights are
+ *   rounded to the tensors' type for the product with the values.
+ * - Cache rows at or behind kv_len[b], and blocks that no row of the request
+ *   can see, may hold anything, infinities and NaN included. Table entries
+ *   behind the request's last block are not read.
+ * - A bad q_off or kv_len (out of range, or more tokens than a table row
+ *   holds) sets the device status SP_ERR_DEVICE and nothing is computed; a
+ *   block id outside the pool sets it and reads pool row 0 instead.
+ * Strides times 2 bytes are multiples of 16 and base pointers 16-byte aligned
+ * (SP_ERR_UNSUPPORTED and SP_ERR_INVALID_ARG otherwise). */
+int sp_paged_attention(const sp_paged_shape* shape, const sp_attn_params* params,
+                       const int32_t* q_off, const int32_t* kv_len, const int32_t* block_table,
+                       const uint16_t* q, const uint16_t* k_pool, const uint16_t* v_pool,
+                       uint16_t* out, float* lse, void* ws, size_t ws_bytes, sp_stream_t stream);
 
 /* Synchronise `stream`, then read (and, when `clear` is non-zero, reset)
  * the workspace's sticky device status word into *status_host. */

@@ -42,6 +42,10 @@ __all__ = [
     "merge_windows",
     "specprefill_score",
     "device_status",
+    "block_tables",
+    "append_kv",
+    "make_attention_workspace",
+    "paged_attention",
     "STATUS",
 ]
 
@@ -49,7 +53,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libspecprefill.so")
 
 STATUS = {0: "SP_OK", 1: "SP_ERR_INVALID_ARG", 2: "SP_ERR_UNSUPPORTED", 3: "SP_ERR_WORKSPACE",
-          4: "SP_ERR_CUDA", 5: "SP_ERR_TIMEOUT", 6: "SP_ERR_DEVICE"}
+          4: "SP_ERR_CUDA", 5: "SP_ERR_TIMEOUT", 6: "SP_ERR_DEVICE", 7: "SP_ERR_CAPACITY"}
 MODES = {"fixed": 0, "mass": 1}
 RULES = {"exact": 0, "listing": 1}
 POOL_AT = {"token": 0, "head": 1}
@@ -179,6 +183,7 @@ def load(path: Optional[str] = None):
         fn = getattr(lib_, name)
         fn.argtypes = args
         fn.restype = i32
+    paged._bind(lib_)
     lib_.sp_status_string.argtypes = [i32]
     lib_.sp_status_string.restype = ctypes.c_char_p
     lib_.sp_build_info.argtypes = []
@@ -633,3 +638,7 @@ def device_status(ws, stream=None, clear: bool = True) -> int:
     _check(lib().sp_get_device_status(ws.data_ptr(), ws.numel(), _stream(stream), int(clear),
                                       ctypes.byref(v)), "sp_get_device_status")
     return int(v.value)
+
+
+from . import paged  # noqa: E402  (uses the helpers above)
+from .paged import append_kv, block_tables, make_attention_workspace, paged_attention  # noqa: E402

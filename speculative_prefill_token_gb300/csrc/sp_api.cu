@@ -557,6 +557,7 @@ const char* sp_status_string(int status) {
         case SP_ERR_CUDA: return "CUDA runtime or launch error";
         case SP_ERR_TIMEOUT: return "a bounded device wait gave up";
         case SP_ERR_DEVICE: return "device-side input check failed";
+        case SP_ERR_CAPACITY: return "the free list holds too few blocks";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,206 @@
+"""GPU parity of paged_attention against the float64 oracle: types, head
+layouts, page sizes, lengths from zero and one token to several tiles, masks
+that leave rows empty, NaN in every row that a request does not own."""
+
+import numpy as np
+import pytest
+
+from oracle import paged_oracle
+from tests.paged_cases import check_attention, host, paged_case
+
+pytestmark = pytest.mark.gpu
+
+
+def _run(sp, case, ref=True, lse=True, **kw):
+    import torch
+    q = case["q"]
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    ls = torch.full(q.shape[:2], 7.0, dtype=torch.float32, device="cuda") if lse else None
+    ws = sp.make_attention_workspace(q, case["kv_len"].numel(), case["k_pool"])
+    sp.paged_attention(q, case["q_off"], case["kv_len"], case["table"], case["k_pool"], case["v_pool"], out=out,
+                       lse=ls, ws=ws, **kw)
+    assert sp.device_status(ws) == 0
+    return out, ls
+
+
+def _check(sp, ctx, new, hq, hk, d, bs, dtype, seed=0, q_gain=1.0, spare=3, **kw):
+    case = paged_case(seed, ctx, new, hq, hk, d, bs, dtype, spare_rows=spare, q_gain=q_gain)
+    out, lse = _run(sp, case, **kw)
+    kv = host(case["kv_len"])
+    ref = paged_oracle.paged_attention(host(case["q"]), host(case["q_off"]), kv, host(case["table"]),
+                                       host(case["k_pool"]), host(case["v_pool"]), **kw)
+    n = sum(new)
+    check_attention(out, lse, ref, kv, d, dtype, n)
+    # rows behind the last request stay as they were
+    assert (host(out)[n:] == 7.0).all() and (host(lse)[n:] == 7.0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_single_tokens_over_ragged_contexts(cuda_lib, d, dtype):
+    ctx = [0, 1, 7, 8, 126, 127, 128, 129, 255, 256, 700, 1500]
+    _check(cuda_lib, ctx, [1] * len(ctx), 8, 2, d, 16, dtype, seed=d)
+
+
+@pytest.mark.parametrize("d,bs", [(64, 8), (64, 256), (128, 32), (128, 128), (256, 16), (256, 64)])
+def test_chunks_with_requests_of_no_and_one_token(cuda_lib, d, bs):
+    ctx = [300, 5, 0, 0, 64, 1000]
+    new = [130, 0, 1, 77, 64, 9]
+    _check(cuda_lib, ctx, new, 4, 2, d, bs, "bf16", seed=bs)
+
+
+@pytest.mark.parametrize("hq,hk", [(1, 1), (3, 1), (10, 2), (7, 1), (6, 2), (16, 1), (48, 1), (128, 1), (5, 5)])
+def test_groups_of_query_heads(cuda_lib, hq, hk):
+    _check(cuda_lib, [100, 0, 33], [40, 150, 1], hq, hk, 64, 32, "bf16", seed=hq)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 2, 64, 127, 128, 129, 500])
+def test_sliding_window(cuda_lib, d, window):
+    _check(cuda_lib, [400, 0, 1000, 129], [70, 300, 1, 130], 6, 2, d, 16, "fp16", seed=window, window=window)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_without_causality(cuda_lib, d):
+    _check(cuda_lib, [90, 0, 257], [40, 128, 1], 4, 4, d, 64, "bf16", seed=d, causal=False)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_longer_contexts_split_over_many_ctas(cuda_lib, d):
+    _check(cuda_lib, [9000, 200], [3, 1], 4, 1, d, 128, "bf16", seed=5)
+
+
+def test_prompt_of_several_query_tiles(cuda_lib):
+    _check(cuda_lib, [0], [1100], 4, 1, 128, 64, "bf16", seed=9)
+    _check(cuda_lib, [37], [700], 2, 1, 256, 16, "bf16", seed=10)
+    _check(cuda_lib, [37], [901], 3, 1, 64, 16, "fp16", seed=11)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_large_logits_move_the_running_maximum(cuda_lib, d):
+    """Logits of up to some hundreds: the maximum moves in most tiles, by far
+    more than any threshold, and most weights underflow."""
+    _check(cuda_lib, [1200, 0], [5, 260], 4, 2, d, 32, "bf16", seed=d, q_gain=30.0)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_rows_that_see_nothing(cuda_lib, causal):
+    """kv_len below the number of new tokens: the first tokens see nothing and
+    give 0 and -inf; kv_len = 0 gives that for all."""
+    import torch
+    sp = cuda_lib
+    case = paged_case(3, [0, 0, 10], [200, 30, 3], 4, 2, 128, 16, "bf16")
+    case["kv_len"] = torch.tensor([150, 0, 13], dtype=torch.int32, device="cuda")
+    out, lse = _run(sp, case, causal=causal)
+    kv = host(case["kv_len"])
+    ref = paged_oracle.paged_attention(host(case["q"]), host(case["q_off"]), kv, host(case["table"]),
+                                       host(case["k_pool"]), host(case["v_pool"]), causal=causal)
+    check_attention(out, lse, ref, kv, 128, "bf16", 233)
+    assert np.isneginf(host(lse)[200:230]).all() and (host(out)[200:230] == 0).all()
+
+
+def test_strided_queries_outputs_and_pools(cuda_lib):
+    """q as a view of fused projections, out as a view of a wider tensor, pools
+    whose heads and rows are views of wider rows."""
+    import torch
+    sp = cuda_lib
+    hq, hk, d, bs = 6, 2, 64, 16
+    case = paged_case(21, [50, 300], [20, 33], hq, hk, d, bs, "bf16")
+    want, _ = _run(sp, case)
+    n = case["q"].shape[0]
+    fused = torch.randn(n, hq + 2 * hk, d, device="cuda").to(torch.bfloat16)
+    fused[:, 1:1 + hq] = case["q"]
+    wide = torch.zeros(n, hq, 2 * d, dtype=torch.bfloat16, device="cuda")
+    nb = case["k_pool"].shape[0]
+    both = torch.full((nb, bs, 2, hk, d + 8), float("nan"), dtype=torch.bfloat16, device="cuda")
+    both[:, :, 0, :, :d] = case["k_pool"]
+    both[:, :, 1, :, :d] = case["v_pool"]
+    sp.paged_attention(fused[:, 1:1 + hq], case["q_off"], case["kv_len"], case["table"], both[:, :, 0, :, :d],
+                       both[:, :, 1, :, :d], out=wide[:, :, d:])
+    assert torch.equal(wide[:, :, d:], want)
+    assert (wide[:, :, :d] == 0).all()
+
+
+def test_bad_lengths_and_blocks_set_the_status(cuda_lib):
+    import torch
+    sp = cuda_lib
+    case = paged_case(4, [40, 60], [3, 2], 4, 2, 64, 16, "bf16", poison=False)
+    q = case["q"]
+
+    def call(**kw):
+        c = dict(case, **kw)
+        out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+        ws = sp.make_attention_workspace(q, 2, c["k_pool"])
+        sp.paged_attention(q, c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"], out=out, ws=ws)
+        return sp.device_status(ws), out
+
+    def i32(*v):
+        return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+    assert call()[0] == 0
+    for kw in (dict(q_off=i32(1, 3, 5)), dict(q_off=i32(0, 4, 3)), dict(q_off=i32(0, 3, 6)), dict(kv_len=i32(-1, 62)),
+               dict(kv_len=i32(43, 100000))):
+        status, out = call(**kw)
+        assert status == 6 and (out == 7.0).all(), kw
+    table = case["table"].clone()
+    table[1, 2] = 1 << 20
+    assert call(table=table)[0] == 6
+    table[1, 2] = -3
+    assert call(table=table)[0] == 6
+    # an entry behind the request's last block is not read
+    table = case["table"].clone()
+    table[:, -1] = 1 << 30
+    assert call(table=table)[0] == 0
+
+
+def test_calls_on_streams_and_a_captured_call(cuda_lib):
+    """Calls on three streams with workspaces of their own, a captured call
+    replayed on new inputs, and two captured calls that share a workspace."""
+    import torch
+    sp = cuda_lib
+    cases = [paged_case(30 + i, [700 * i, 10, 300], [60, 1, 5 + i], 8, 2, 128, 16, "bf16") for i in range(3)]
+    want = [_run(sp, c)[0] for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [torch.zeros_like(w) for w in want]
+    wss = [sp.make_attention_workspace(c["q"], 3, c["k_pool"]) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for c, st, o, ws in zip(cases, streams, outs, wss):
+            sp.paged_attention(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"], out=o, ws=ws,
+                               stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+    ws = wss[0]
+    graphs, goes = [], []
+    for c in cases[:2]:
+        o = torch.zeros_like(c["q"])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sp.paged_attention(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"], out=o, ws=ws)
+        graphs.append(g)
+        goes.append(o)
+    for _ in range(3):
+        for g, o, w in zip(graphs, goes, want):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, w)
+    # new lengths in place: fewer cached tokens of the first request
+    c = cases[1]
+    c["kv_len"][0] -= 100
+    again, _ = _run(sp, c)
+    graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(goes[1], again) and not torch.equal(again, want[1])
+
+
+def test_repeated_calls_give_the_same_bits(cuda_lib):
+    import torch
+    sp = cuda_lib
+    case = paged_case(50, [5000, 3, 900], [1, 300, 40], 16, 4, 128, 64, "bf16")
+    a = _run(sp, case)
+    for _ in range(5):
+        b = _run(sp, case)
+        n = 341
+        assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:n], b[1][:n])
