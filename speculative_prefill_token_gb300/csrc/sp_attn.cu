@@ -1,14 +1,43 @@
 // Attention of new tokens over a block-paged cache ("SpecPrefill —
 // Implementation Guide", §How It Works / Sparse Prefill: the target's
-// attention over the kept tokens, and its decode steps after them).
+// attention over the kept tokens, and its decode steps after them), on
+// fifth-generation tensor cores.
 //
 // For a query row (token i of request b, head h) with visible cache indices
 // [lo, hi), and KV head g = h / G,
 //   out = sum_j exp2(y_j - m) v_j / sum_j exp2(y_j - m),  y_j = scale log2(e) <q, k_j>,
-// in one pass over the keys: m is the running maximum, and the sum and the
-// accumulator are scaled by exp2(m_old - m_new) when it grows.
+// in one pass over the keys: m is a reference at most 8 below the running
+// maximum, and sum and accumulator are scaled by exp2(m_old - m_new) when it
+// moves.
 //
-// One warp per row, the head dimension spread over its lanes.
+// Work. The G heads that share a KV head are rows of one query tile: 128 / G
+// tokens x G heads, so a decode step reads each key once for all of them. An
+// item is the query tiles of one request and KV head that one CTA holds at a
+// time (two tiles of 128 rows for d <= 128, one for d = 256, whose
+// accumulator fills the tensor memory); its unit is a tile of 128 keys. All
+// units of all items are cut into equal contiguous ranges, one for each CTA
+// (one CTA per SM), whatever the mix of lengths; an item cut between CTAs is
+// joined by the last of them to finish, in the order of the parts, so results
+// do not depend on timing. The lengths live on the device: a one-CTA kernel
+// lays out the items and the ranges.
+//
+// Roles (352 threads):
+//   warps 0-7  two softmax warpgroups. A thread owns one row of a 128 x 128
+//              logits tile: reads it from tensor memory, takes the maximum,
+//              writes the weights back as 16-bit values in its place, keeps
+//              the sum, and writes or joins the result at the item's end.
+//   warp 8     K and V boxes by TMA (lane j issues box j of a 16 KB slot)
+//   warp 9     tcgen05.mma issuer (one thread) and TMEM owner
+//   warp 10    query tiles by TMA
+// Two streams keep the tensor cores busy while the other stream's softmax
+// runs: with two query tiles, one tile each; with one (decode steps, short
+// chunks), even and odd key tiles, with an accumulator each for d <= 128
+// (joined from tensor memory at the end) and one accumulator for d = 256.
+//
+// Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT
+// in the workspace status, and the CTA drains its copies and MMAs in flight
+// and frees its tensor memory before it returns.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -19,151 +48,1039 @@
 #include "sp_device.cuh"
 #include "sp_internal.h"
 #include "sp_paged.h"
+#include "sp_ptx.cuh"
 
 namespace sp {
 namespace {
 
-constexpr int kAttnThreads = 256;
+constexpr int kKeys = 128;                 // keys of a tile (a unit of work)
+constexpr int kRows = 128;                 // rows of a query tile
+constexpr uint32_t kSlot = 16384;          // bytes of a ring slot
+constexpr int kWarps = 11;
+constexpr int kAttnThreads = 32 * kWarps;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10;
+constexpr int kPlanThreads = 1024;
+constexpr int64_t kDrainSpin = int64_t(1) << 22;
+constexpr float kSlack = 8.0f;             // log2 units the reference may lag behind the maximum
+
+__host__ __device__ constexpr int tiles_per_item(int d) { return d <= 128 ? 2 : 1; }
+__host__ __device__ constexpr int ring_slots(int d) { return d == 64 ? 12 : 10; }
+
+// One item: rows of `ntok` tokens from row tok0 of q, the first at cache
+// index pos0; keys [klo, khi) are seen by some row, in tiles
+// [tile0, tile0 + ntiles).
+struct alignas(16) Item {
+    int32_t b, tok0, ntok, pos0, klo, khi, tile0, ntiles;
+};
+
+// Where a CTA's range starts: unit `off` of item `item` of KV head g.
+struct alignas(16) Start {
+    int32_t item, g, off, pad;
+    int64_t begin, end;   // units of all heads
+};
+
+struct PlanHead {
+    int64_t units;    // of one KV head (0: nothing to do)
+    int32_t items;    // of one KV head
+    int32_t ctas;     // CTAs with a range: at least one unit each
+};
 
 struct AttnArgs {
     const int32_t* q_off;
     const int32_t* kv_len;
     const int32_t* table;
-    const uint16_t* q;
-    const uint16_t* k;
-    const uint16_t* v;
     uint16_t* out;
     float* lse;
     int32_t* status;
-    int64_t q_st, q_sh, o_st, o_sh, k_st, k_sh, v_st, v_sh, pool_tokens;
-    int B, hq, hk, G, bs, table_stride, cap, causal, window;
+    PlanHead* head;
+    Item* items;
+    int64_t* pre;       // units before each item, [items + 1]
+    int32_t* req_item;  // first item of each request, [B + 1]
+    Start* starts;      // [grid]
+    unsigned* count;    // [grid][2] parts of the item first met by a CTA that are written
+    float* part_o;      // [grid * 2][tiles][128][d]
+    float2* part_ml;    // [grid * 2][tiles][128] (reference, sum)
+    int64_t o_st, o_sh, pool_tokens, spin;
+    int B, hk, G, tq, bs, table_stride, cap, causal, window, grid;
+    int hk_box, hv_box;  // rows of a K and of a V box
+    uint32_t q_bytes;    // of one 64-element chunk of a query tile
     float scale2;
 };
 
-template <bool kBf16>
-__device__ __forceinline__ float to_f32(uint16_t x) {
-    if constexpr (kBf16) return __uint_as_float(static_cast<uint32_t>(x) << 16);
-    return __half2float(__ushort_as_half(x));
+// ------------------------------------------------------------ plan
+
+__device__ __forceinline__ int64_t range_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sum, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = 0, all = 0;
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+    }
+    *total = all;
+    return before + incl - v;   // exclusive
 }
 
-template <bool kBf16>
-__device__ __forceinline__ uint16_t from_f32(float x) {
-    if constexpr (kBf16) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
-    return __half_as_ushort(__float2half_rn(x));
-}
-
-template <int D, bool kBf16>
-__global__ void __launch_bounds__(kAttnThreads) attn_rows_kernel(const AttnArgs a) {
+// Items, their units and the CTAs' ranges (one CTA).
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles) {
+    __shared__ int64_t warp_sum[kPlanThreads / 32];
     grid_dep_wait();
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    // (a request's lengths are checked by every row of the batch: nothing is
-    // computed for an inconsistent batch)
+    grid_dep_launch();
+    const int tid = threadIdx.x;
+    const int tpi = a.tq * tiles;   // tokens per item
+    for (int i = tid; i < a.grid * 2; i += kPlanThreads) a.count[i] = 0;
     int bad = a.q_off[0] != 0;
-    for (int b = threadIdx.x; b < a.B; b += kAttnThreads) {
-        const int lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_len[b];
-        bad |= hi < lo || hi > a.cap || kv < 0 || (static_cast<int64_t>(kv) + a.bs - 1) / a.bs > a.table_stride;
+    int64_t items = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int64_t n = 0;
+        if (b < a.B) {
+            const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_len[b];
+            if (hi < lo || hi > a.cap || kv < 0 || (kv + a.bs - 1) / a.bs > a.table_stride) bad = 1;
+            else n = (hi - lo + tpi - 1) / tpi;
+        }
+        int64_t total;
+        const int64_t at = items + block_scan(n, warp_sum, &total);
+        if (b < a.B) a.req_item[b] = static_cast<int32_t>(at);
+        items += total;
     }
     if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+        if (tid == 0) {
+            atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+            a.head->units = 0;
+        }
         return;
     }
-    const int64_t rows = static_cast<int64_t>(a.q_off[a.B]) * a.hq;
-    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kAttnThreads / 32);
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * (kAttnThreads / 32) + (threadIdx.x >> 5); w < rows;
-         w += warps) {
-        const int t = static_cast<int>(w / a.hq), h = static_cast<int>(w - static_cast<int64_t>(t) * a.hq);
-        int b = 0, e = a.B;
-        while (e - b > 1) {
-            const int mid = (b + e) >> 1;
-            if (a.q_off[mid] <= t) b = mid; else e = mid;
-        }
-        const int kv = a.kv_len[b];
-        int hi = kv, lo = 0;
-        if (a.causal) {
-            hi = kv - a.q_off[b + 1] + t + 1;
-            if (hi < 0) hi = 0;
-            if (a.window > 0 && hi > a.window) lo = hi - a.window;
-        }
-        float q[E], acc[E];
-        const uint16_t* qr = a.q + t * a.q_st + h * a.q_sh + lane * E;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            q[i] = to_f32<kBf16>(qr[i]);
-            acc[i] = 0.0f;
-        }
-        float m = -INFINITY, l = 0.0f;
-        const int g = h / a.G;
-        for (int j = lo; j < hi; ++j) {
-            const int id = a.table[static_cast<int64_t>(b) * a.table_stride + j / a.bs];
-            int64_t row = static_cast<int64_t>(id) * a.bs + j % a.bs;
-            if (id < 0 || row >= a.pool_tokens) {
-                atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
-                row = 0;
+    int64_t units = 0;
+    for (int64_t i0 = 0; i0 < items; i0 += kPlanThreads) {
+        const int64_t i = i0 + tid;
+        Item it = {};
+        int64_t n = 0;
+        if (i < items) {
+            // the last request whose first item is at or before i: requests
+            // without new tokens share the next one's first item
+            int lo = 0, hi = a.B;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (a.req_item[mid] <= i) lo = mid; else hi = mid;
             }
-            const uint16_t* kr = a.k + row * a.k_st + g * a.k_sh + lane * E;
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) s += q[i] * to_f32<kBf16>(kr[i]);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            s *= a.scale2;
-            const float mn = fmaxf(m, s), base = mn == -INFINITY ? 0.0f : mn;
-            const float f = exp2f(m - base), p = exp2f(s - base);
-            l = l * f + p;
-            const uint16_t* vr = a.v + row * a.v_st + g * a.v_sh + lane * E;
-#pragma unroll
-            for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + p * to_f32<kBf16>(vr[i]);
-            m = mn;
+            const int first = static_cast<int>(i - a.req_item[lo]) * tpi;
+            const int q0 = a.q_off[lo], nq = a.q_off[lo + 1] - q0, kv = a.kv_len[lo];
+            it.b = lo;
+            it.tok0 = q0 + first;
+            it.ntok = min(nq - first, tpi);
+            it.pos0 = kv - nq + first;
+            it.khi = a.causal ? max(0, min(kv, it.pos0 + it.ntok)) : kv;
+            it.klo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
+            it.tile0 = it.klo / kKeys;
+            it.ntiles = it.khi > it.klo ? (it.khi + kKeys - 1) / kKeys - it.tile0 : 0;
+            n = max(it.ntiles, 1);
+            a.items[i] = it;
         }
-        uint16_t* o = a.out + t * a.o_st + h * a.o_sh + lane * E;
-        const float inv = hi > lo ? 1.0f / l : 0.0f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] = from_f32<kBf16>(acc[i] * inv);
-        if (a.lse && lane == 0)
-            a.lse[w] = hi > lo ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        int64_t total;
+        const int64_t at = units + block_scan(n, warp_sum, &total);
+        if (i < items) a.pre[i] = at;
+        units += total;
     }
+    if (tid == 0) {
+        a.pre[items] = units;
+        a.head->units = units;
+        a.head->items = static_cast<int32_t>(items);
+        a.head->ctas = static_cast<int32_t>(min(static_cast<int64_t>(a.grid), units * a.hk));
+    }
+    __syncthreads();
+    const int64_t all = units * a.hk;
+    const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), all));
+    for (int c = tid; c < a.grid; c += kPlanThreads) {
+        Start s = {};
+        if (c < ctas) {
+            s.begin = range_start(all, ctas, c);
+            s.end = range_start(all, ctas, c + 1);
+            s.g = static_cast<int32_t>(s.begin / units);
+            const int64_t u = s.begin - s.g * units;
+            int64_t lo = 0, hi = items;
+            while (hi - lo > 1) {
+                const int64_t mid = (lo + hi) >> 1;
+                if (a.pre[mid] <= u) lo = mid; else hi = mid;
+            }
+            s.item = static_cast<int32_t>(lo);
+            s.off = static_cast<int32_t>(u - a.pre[lo]);
+        }
+        a.starts[c] = s;
+    }
+}
+
+// ------------------------------------------------------------ segments
+
+// A CTA's part of one item: key tiles [first, first + n) (n = 0 for an item
+// that sees no key), and whether other CTAs hold the rest.
+struct Segment {
+    Item it;
+    int g, item, first, n;
+    bool split, head;   // head: the CTA's first segment
+};
+
+// Walks a CTA's range; every role takes the same steps.
+struct Walk {
+    int item, g, off, items;
+    int64_t left;
+    bool head;
+    __device__ __forceinline__ explicit Walk(const AttnArgs& a) {
+        const Start s = a.starts[blockIdx.x];
+        item = s.item;
+        g = s.g;
+        off = s.off;
+        left = s.end - s.begin;
+        items = a.head->items;
+        head = true;
+    }
+    __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
+        if (left <= 0) return false;
+        s.it = a.items[item];
+        const int units = max(s.it.ntiles, 1);
+        const int take = static_cast<int>(min(static_cast<int64_t>(units - off), left));
+        s.g = g;
+        s.item = item;
+        s.first = s.it.tile0 + off;
+        s.n = s.it.ntiles == 0 ? 0 : take;
+        s.split = take < units;
+        s.head = head;
+        head = false;
+        left -= take;
+        off = 0;
+        if (++item == items) {
+            item = 0;
+            ++g;
+        }
+        return true;
+    }
+};
+
+// Two query tiles, each with its own stream, or one tile whose key tiles
+// alternate between the streams.
+__device__ __forceinline__ bool two_tiles(const AttnArgs& a, const Segment& s, int d) {
+    return d <= 128 && s.it.ntok > a.tq;
+}
+
+// Ring order of a segment's tiles: K0 V0 K1 V1 ... with two query tiles,
+// K0 K1 V0 K2 V1 ... with alternating key tiles. Position of V_j:
+__device__ __forceinline__ int v_position(bool two, int j, int n) {
+    return two ? 2 * j + 1 : min(2 * j + 2, 2 * n - 1);
+}
+
+// ------------------------------------------------------------ shared memory
+
+template <int D>
+struct Smem {
+    static constexpr int kTiles = tiles_per_item(D);
+    static constexpr int kChunks = D / 64;         // slots of a K or V tile
+    static constexpr int kSlots = ring_slots(D);
+    static constexpr uint32_t q = 0;
+    static constexpr uint32_t ring = kTiles * kChunks * kSlot;
+    static constexpr uint32_t stat = ring + kSlots * kSlot;   // [2][128] float2
+    static constexpr uint32_t bars = stat + 2 * kRows * 8;
+    static constexpr uint32_t full = bars;
+    static constexpr uint32_t empty = full + 8 * kSlots;
+    static constexpr uint32_t qfull = empty + 8 * kSlots;
+    static constexpr uint32_t qempty = qfull + 8;
+    static constexpr uint32_t sfull = qempty + 8;     // [2] logits written
+    static constexpr uint32_t pfull = sfull + 16;     // [2] weights written
+    static constexpr uint32_t odone = pfull + 16;     // [2] accumulator updated
+    static constexpr uint32_t oempty = odone + 16;    // [2] accumulator read
+    static constexpr uint32_t statfull = oempty + 16; // [2] second stream's sums written
+    static constexpr uint32_t drain = statfull + 16;
+    static constexpr uint32_t tmem = drain + 8;
+    static constexpr uint32_t abort = tmem + 8;
+    static constexpr uint32_t last = abort + 4;       // [2] this warpgroup joins the item
+    static constexpr uint32_t total = last + 12;
+};
+
+static_assert(Smem<64>::total <= 232448 && Smem<128>::total <= 232448 && Smem<256>::total <= 232448,
+              "shared memory of one CTA");
+
+struct Ctx {
+    uint8_t* smem;
+    uint32_t base;
+    volatile int* abort_flag;
+    int32_t* status;
+    int64_t spin;
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+        if (mbar_wait_bounded(base + bar, parity & 1, spin, abort_flag)) return true;
+        *abort_flag = 1;
+        atomicCAS(status, 0, static_cast<int32_t>(SP_ERR_TIMEOUT));
+        return false;
+    }
+};
+
+// ------------------------------------------------------------ loads
+
+// K and V boxes of the CTA's segments, by the whole warp. Boxes outside the
+// item's keys [klo, khi) are not loaded (their blocks may be gone); the
+// softmax warps zero the V rows outside before they are used.
+template <int D>
+__device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const CUtensorMap* mk,
+                                          const CUtensorMap* mv, int lane) {
+    using L = Smem<D>;
+    constexpr unsigned kAll = 0xffffffffu;
+    constexpr int kPer = kKeys / L::kChunks;   // keys of a V slot
+    const int nk = kKeys / a.hk_box;           // K boxes of a tile
+    const int sub = kPer / a.hv_box;           // V boxes of a slot and chunk
+    int slot = 0;
+    uint32_t turn = 0;
+    uint32_t used = 0, last_turn[L::kSlots];
+    bool ok = true;
+
+    // pool row of this lane's K box of a tile; -1 outside the item's keys
+    auto lookup = [&](const Segment& s, int tile) -> int {
+        const int key = tile * kKeys + lane * a.hk_box;
+        if (lane >= nk || key >= s.it.khi || key + a.hk_box <= s.it.klo) return -1;
+        const int blk = key / a.bs;
+        const int id = a.table[static_cast<int64_t>(s.it.b) * a.table_stride + blk];
+        const int64_t row = static_cast<int64_t>(id) * a.bs;
+        if (id < 0 || row + a.bs > a.pool_tokens) {
+            atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+            return 0;
+        }
+        return static_cast<int>(row) + key - blk * a.bs;
+    };
+    auto acquire = [&](uint32_t bytes) -> bool {
+        if (lane == 0) {
+            ok = c.wait(L::empty + 8 * slot, turn ^ 1);
+            if (ok) mbar_arrive_expect_tx(c.base + L::full + 8 * slot, bytes);
+        }
+        ok = __shfl_sync(kAll, ok, 0);
+        return ok;
+    };
+    auto advance = [&]() {
+        used |= 1u << slot;
+#pragma unroll
+        for (int i = 0; i < L::kSlots; ++i)
+            if (i == slot) last_turn[i] = turn;
+        if (++slot == L::kSlots) {
+            slot = 0;
+            turn ^= 1;
+        }
+    };
+    auto put_k = [&](const Segment& s, int row) {
+        const uint32_t bytes = __popc(__ballot_sync(kAll, row >= 0)) * a.hk_box * 128u;
+        for (int ch = 0; ch < L::kChunks; ++ch) {
+            if (!acquire(bytes)) return;
+            if (row >= 0)
+                tma_load_3d(c.base + L::ring + slot * kSlot + static_cast<uint32_t>(lane * a.hk_box) * 128u, mk,
+                            c.base + L::full + 8 * slot, ch * 64, row, s.g);
+            advance();
+        }
+    };
+    auto put_v = [&](const Segment& s, int tile, int row) {
+        for (int p = 0; p < L::kChunks; ++p) {
+            // lane: sub-box r of chunk ch; its K box holds the block's row
+            const int r = lane / L::kChunks, ch = lane % L::kChunks;
+            const int key = p * kPer + r * a.hv_box;       // of the tile
+            const int box = key / a.hk_box & 31;
+            const int base_row = __shfl_sync(kAll, row, box);
+            const int at = tile * kKeys + key;
+            const bool mine = r < sub && base_row >= 0 && at < s.it.khi && at + a.hv_box > s.it.klo;
+            const uint32_t bytes = __popc(__ballot_sync(kAll, mine)) * a.hv_box * 128u;
+            if (!acquire(bytes)) return;
+            if (mine)
+                tma_load_3d(c.base + L::ring + slot * kSlot + static_cast<uint32_t>(ch * kPer + r * a.hv_box) * 128u,
+                            mv, c.base + L::full + 8 * slot, ch * 64, base_row + key % a.hk_box, s.g);
+            advance();
+        }
+    };
+
+    Walk w(a);
+    Segment s;
+    while (ok && w.next(a, s)) {
+        if (s.n == 0) continue;
+        const bool two = two_tiles(a, s, D);
+        int row = lookup(s, s.first), next = -1;
+        if (s.n > 1) next = lookup(s, s.first + 1);
+        if (!two) put_k(s, row);
+        for (int j = 0; j < s.n && ok; ++j) {
+            const int after = j + 2 < s.n ? lookup(s, s.first + j + 2) : -1;
+            if (two) put_k(s, row);
+            else if (j + 1 < s.n) put_k(s, next);
+            if (ok) put_v(s, s.first + j, row);
+            row = next;
+            next = after;
+        }
+    }
+    // every copy this warp issued lands before it leaves
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < L::kSlots; ++i)
+            if (used >> i & 1) mbar_wait_spin(c.base + L::full + 8 * i, last_turn[i], kDrainSpin);
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, const CUtensorMap* mq) {
+    using L = Smem<D>;
+    Walk w(a);
+    Segment s;
+    uint32_t n = 0;
+    while (w.next(a, s)) {
+        if (s.n == 0) continue;
+        const int tiles = two_tiles(a, s, D) ? 2 : 1;
+        if (!c.wait(L::qempty, (n & 1) ^ 1)) break;
+        mbar_arrive_expect_tx(c.base + L::qfull, a.q_bytes * L::kChunks * tiles);
+        for (int t = 0; t < tiles; ++t)
+            for (int ch = 0; ch < L::kChunks; ++ch)
+                tma_load_3d(c.base + L::q + (t * L::kChunks + ch) * kSlot, mq, c.base + L::qfull, ch * 64, s.g * a.G,
+                            s.it.tok0 + t * a.tq);
+        ++n;
+    }
+    if (n) mbar_wait_spin(c.base + L::qfull, (n - 1) & 1, kDrainSpin);
+}
+
+// ------------------------------------------------------------ MMA
+
+template <int D, bool kBf16>
+__device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint32_t tmem) {
+    using L = Smem<D>;
+    constexpr uint32_t kIdQk = idesc_f16_f32(kRows, kKeys, kBf16, false);
+    constexpr uint32_t kIdPv = idesc_f16_f32(kRows, D, kBf16, true);
+    constexpr int kPer = kKeys / L::kChunks;
+    int slot = 0;
+    uint32_t turn = 0;
+    uint32_t nq = 0;                 // segments with keys so far
+    uint32_t np[2] = {0, 0};         // weight tiles consumed of each stream
+    uint32_t no[2] = {0, 0};         // segments that used each accumulator
+    bool ok = true, any = false;
+
+    // the ring position of the next tile is tracked by (slot, turn); a V tile
+    // that both query tiles use is walked twice from the same place
+    struct Place {
+        int slot;
+        uint32_t turn;
+    };
+    auto step = [&](Place& p) {
+        if (++p.slot == L::kSlots) {
+            p.slot = 0;
+            p.turn ^= 1;
+        }
+    };
+    // logits of query tile t and the K tile at p into stream buffer sb
+    auto qk = [&](Place p, int t, int sb, bool release) -> Place {
+#pragma unroll 1
+        for (int ch = 0; ch < L::kChunks; ++ch) {
+            if (ok) ok = c.wait(L::full + 8 * p.slot, p.turn);
+            if (!ok) return p;
+            tc_fence_after();
+            const uint32_t qa = c.base + L::q + (t * L::kChunks + ch) * kSlot;
+            const uint32_t ka = c.base + L::ring + p.slot * kSlot;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                tc_mma_bf16(tmem + sb * kKeys, smem_desc_sw128(qa + 32 * k), smem_desc_sw128(ka + 32 * k), kIdQk,
+                            (ch | k) != 0);
+            any = true;
+            if (release) tc_commit(c.base + L::empty + 8 * p.slot);
+            step(p);
+        }
+        tc_commit(c.base + L::sfull + 8 * sb);
+        return p;
+    };
+    // accumulator o (+)= weights of stream sb times the V tile at p
+    auto pv = [&](Place p, int sb, int o, bool first, bool release) -> Place {
+        if (ok) ok = c.wait(L::pfull + 8 * sb, np[sb] & 1);
+        if (!ok) return p;
+        ++np[sb];
+        if (first) {
+            ok = c.wait(L::oempty + 8 * o, (no[o] & 1) ^ 1);
+            if (!ok) return p;
+            ++no[o];
+        }
+#pragma unroll 1
+        for (int part = 0; part < L::kChunks; ++part) {
+            ok = c.wait(L::full + 8 * p.slot, p.turn);
+            if (!ok) return p;
+            tc_fence_after();
+            const uint32_t va = c.base + L::ring + p.slot * kSlot;
+#pragma unroll
+            for (int k = 0; k < kPer / 16; ++k)
+                tc_mma_f16_ts(tmem + 2 * kKeys + o * D, tmem + sb * kKeys + (part * (kPer / 16) + k) * 8,
+                              smem_desc_sw128_mn(va + 2048 * k, kPer * 128), kIdPv, !first || (part | k) != 0);
+            if (release) tc_commit(c.base + L::empty + 8 * p.slot);
+            step(p);
+        }
+        tc_commit(c.base + L::odone + 8 * o);
+        return p;
+    };
+
+    Walk w(a);
+    Segment s;
+    Place at{slot, turn};
+    while (ok && w.next(a, s)) {
+        if (s.n == 0) continue;
+        ok = c.wait(L::qfull, nq & 1);
+        if (!ok) break;
+        ++nq;
+        if (two_tiles(a, s, D)) {
+            qk(at, 0, 0, false);
+            at = qk(at, 1, 1, true);
+            if (s.n == 1) tc_commit(c.base + L::qempty);
+            for (int j = 0; j < s.n && ok; ++j) {
+                const Place v = at;
+                at = pv(v, 0, 0, j == 0, false);
+                const Place k = at;
+                if (j + 1 < s.n) qk(k, 0, 0, false);
+                pv(v, 1, 1, j == 0, true);
+                if (j + 1 < s.n) {
+                    at = qk(k, 1, 1, true);
+                    if (j + 2 == s.n) tc_commit(c.base + L::qempty);
+                }
+            }
+        } else {
+            at = qk(at, 0, 0, true);
+            if (s.n > 1) at = qk(at, 0, 1, true);
+            if (s.n <= 2) tc_commit(c.base + L::qempty);
+            // ring: V0 K2 V1 K3 ...
+            for (int j = 0; j < s.n && ok; ++j) {
+                const int sb = j & 1;
+                at = pv(at, sb, D <= 128 ? sb : 0, D <= 128 ? j < 2 : j == 0, true);
+                if (j + 2 < s.n) {
+                    at = qk(at, 0, sb, true);
+                    if (j + 3 == s.n) tc_commit(c.base + L::qempty);
+                }
+            }
+        }
+    }
+    if (any) {
+        tc_commit(c.base + L::drain);
+        mbar_wait_spin(c.base + L::drain, 0, kDrainSpin);
+    }
+}
+
+// ------------------------------------------------------------ softmax
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack_pair(float x, float y) {
+    if constexpr (kBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+__device__ __forceinline__ void bar_sync(int id, int count) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
+}
+
+// The CTA whose range holds unit u of `total`.
+__device__ __forceinline__ int range_owner(int64_t total, int ctas, int64_t u) {
+    return static_cast<int>(((u + 1) * ctas - 1) / total);
+}
+
+// One warpgroup (index wg) of softmax threads over the CTA's segments.
+template <int D, bool kBf16>
+__device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int wg) {
+    using L = Smem<D>;
+    constexpr unsigned kAll = 0xffffffffu;
+    // fp16 weights are scaled by 2^6: their subnormals then start 20 binary
+    // orders below the maximum, and the largest weight is 2^14
+    constexpr float kBias = kBf16 ? 0.0f : 6.0f;
+    constexpr float kLn2 = 0.6931471805599453f;
+    const int warp = threadIdx.x >> 5 & 3, lane = threadIdx.x & 31;
+    const int row = warp * 32 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const int tid = threadIdx.x & 127;
+    uint32_t cnt[2] = {0, 0};    // tiles of each stream buffer before this segment
+    uint32_t alt = 0;            // segments joined from two accumulators so far
+    int ring = 0;                // slot of the segment's first K tile
+    uint32_t turn = 0;           // and its turn
+    bool ok = true;
+    Walk w(a);
+    Segment s;
+    while (w.next(a, s)) {
+        const bool two = two_tiles(a, s, D);
+        const int tile = two ? wg : 0;                 // query tile of this warpgroup
+        const int ntok = min(max(s.it.ntok - tile * a.tq, 0), a.tq);
+        const int rows = ntok * a.G;
+        const bool live = warp * 32 < rows;            // (warp-uniform)
+        const int tok = row / a.G;                     // token of the tile
+        const bool valid = row < rows;
+        const int pos = s.it.pos0 + tile * a.tq + tok;
+        int hi = a.causal ? min(s.it.khi, pos + 1) : s.it.khi;
+        if (!valid) hi = 0;
+        const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        // tiles of this warpgroup: all with two query tiles or d = 256 (first
+        // warpgroup only), every second one otherwise
+        const bool whole = two || D > 128;
+        const int j0 = two ? 0 : wg, dj = whole ? 1 : 2;
+        const bool works = s.n > 0 && !(D > 128 && wg == 1);
+        float m = -INFINITY, l = 0.0f;
+        if (works) {
+            for (int j = j0; j < s.n; j += dj) {
+                const int sb = two ? wg : j & 1;
+                const uint32_t k = two ? j : j >> 1;
+                const uint32_t seen = cnt[sb] + k;     // tiles of this buffer before this one
+                if (ok) ok = __all_sync(kAll, c.wait(L::sfull + 8 * sb, seen & 1));
+                if (!ok) break;
+                tc_fence_after();
+                const int key0 = (s.first + j) * kKeys;
+                if (live) {
+                    float v[4][32];
+                    const uint32_t st = tmem + lanes + sb * kKeys;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(st + 32 * q, v[q]);
+                    tmem_ld_wait();
+                    const int h = hi - key0, b = lo - key0;
+                    if (__any_sync(kAll, h < kKeys || b > 0)) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) {
+                                const int col = q * 32 + i;
+                                if (col >= h || col < b) v[q][i] = -INFINITY;
+                            }
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        mx[q] = v[q][0];
+#pragma unroll
+                        for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], v[q][i]);
+                    }
+                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+                    const bool move = mt > m + kSlack;
+                    if (__any_sync(kAll, move)) {
+                        const float mn = move ? mt : m;
+                        const float f = mn == m ? 1.0f : exp2_ftz(m - mn);
+                        l *= f;
+                        m = mn;
+                        // the accumulator holds earlier tiles of this segment
+                        if (j > j0) {
+                            const int o = D > 128 ? 0 : sb;
+                            const uint32_t pvs = D > 128 ? cnt[0] + cnt[1] + j : seen;   // updates before this tile
+                            ok = __all_sync(kAll, c.wait(L::odone + 8 * o, (pvs - 1) & 1));
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t ot = tmem + lanes + 2 * kKeys + o * D;
+#pragma unroll 1
+                            for (int q = 0; q < D / 32; ++q) {
+                                float x[32];
+                                tmem_ld_32x32b_x32(ot + 32 * q, x);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 32; ++i) x[i] *= f;
+                                tmem_st_32x32b_x32(ot + 32 * q, x);
+                            }
+                        }
+                    }
+                    const float shift = (m == -INFINITY ? 0.0f : -m) + kBias;
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float x = exp2_ftz(fmaf(v[q][2 * i], a.scale2, shift));
+                            const float y = exp2_ftz(fmaf(v[q][2 * i + 1], a.scale2, shift));
+                            sum[i & 3] += x + y;
+                            pk[i] = pack_pair<kBf16>(x, y);
+                        }
+                        tmem_st_32x32b_x16(st + 16 * q, pk);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tmem_st_wait();
+                }
+                // V rows outside the item's keys are not loaded: zeros, so that
+                // their zero weights meet no NaN (with two query tiles the first
+                // warpgroup's zeros are in place before either product)
+                const int z0 = max(s.it.klo - key0, 0), z1 = min(s.it.khi - key0, kKeys);
+                if ((z0 > 0 || z1 < kKeys) && !(two && wg == 1)) {
+                    const int place = ring + v_position(two, j, s.n) * L::kChunks;
+                    int p = place % L::kSlots;
+                    uint32_t ph = turn ^ (place / L::kSlots & 1);
+                    constexpr int kPer = kKeys / L::kChunks;
+#pragma unroll 1
+                    for (int part = 0; part < L::kChunks && ok; ++part) {
+                        ok = __all_sync(kAll, c.wait(L::full + 8 * p, ph));
+                        if (!ok) break;
+                        // rows of this slot, 8 vectors a row and chunk
+                        uint4* v = reinterpret_cast<uint4*>(c.smem + L::ring + p * kSlot);
+                        for (int e = tid; e < kSlot / 16; e += 128) {
+                            const int key = part * kPer + (e >> 3) % kPer;
+                            if (key < z0 || key >= z1) v[e] = make_uint4(0, 0, 0, 0);
+                        }
+                        if (++p == L::kSlots) {
+                            p = 0;
+                            ph ^= 1;
+                        }
+                    }
+                    if (!ok) break;
+                    fence_proxy_async_smem();
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(c.base + L::pfull + 8 * sb);
+            }
+        }
+        // ---- the item's end. With alternating key tiles of d <= 128 the first
+        // warpgroup joins both accumulators.
+        const bool join = D <= 128 && !two && s.n > 1;
+        const uint32_t buf0 = two ? s.n : (s.n + 1) / 2, buf1 = two ? s.n : s.n / 2;
+        float2* stat = reinterpret_cast<float2*>(c.smem + L::stat) + (alt & 1) * kRows;
+        if (join && wg == 1) {
+            stat[row] = make_float2(m, l);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.base + L::statfull + 8 * (alt & 1));
+        }
+        cnt[0] += buf0;
+        cnt[1] += buf1;
+        const bool ends = two || wg == 0;   // this warpgroup writes rows
+        if (ends) {
+            const int o = two ? wg : 0;
+            float f0 = 1.0f, f1 = 0.0f;
+            if (s.n > 0) {
+                if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8 * o, ((D > 128 ? cnt[0] + cnt[1] : cnt[o]) - 1) & 1));
+                if (join) {
+                    if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8, (cnt[1] - 1) & 1) && c.wait(L::statfull + 8 * (alt & 1), alt >> 1 & 1));
+                    if (ok) {
+                        const float2 other = stat[row];
+                        const float mn = fmaxf(m, other.x);
+                        f0 = m == mn ? 1.0f : exp2_ftz(m - mn);
+                        f1 = other.x == mn ? 1.0f : exp2_ftz(other.x - mn);
+                        l = l * f0 + other.y * f1;
+                        m = mn;
+                    }
+                }
+                tc_fence_after();
+            }
+            const uint32_t ot = tmem + lanes + 2 * kKeys + o * D;
+            auto read = [&](int q, float (&x)[32]) {
+                tmem_ld_32x32b_x32(ot + 32 * q, x);
+                if (join) {
+                    float y[32];
+                    tmem_ld_32x32b_x32(ot + D + 32 * q, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = x[i] * f0 + y[i] * f1;
+                } else {
+                    tmem_ld_wait();
+                }
+            };
+            const int64_t t = s.it.tok0 + tile * a.tq + tok;
+            const int h = s.g * a.G + row - tok * a.G;
+            if (!s.split) {
+                if (ok && live) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    uint16_t* dst = a.out + t * a.o_st + h * a.o_sh;
+                    const bool none = s.n == 0 || l == 0.0f;
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        float x[32];
+                        if (s.n > 0) read(q, x);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            pk[i] = none ? 0u : pack_pair<kBf16>(x[2 * i] * inv, x[2 * i + 1] * inv);
+                        if (valid) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                reinterpret_cast<uint4*>(dst + q * 32)[i] =
+                                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                        }
+                    }
+                    if (valid && a.lse)
+                        a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2;
+                }
+            } else {
+                const int part = (blockIdx.x * 2 + (s.head ? 0 : 1)) * L::kTiles + tile;
+                if (ok && live) {
+                    float* dst = a.part_o + (static_cast<int64_t>(part) * kRows + row) * D;
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        float x[32];
+                        read(q, x);
+                        if (valid) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                reinterpret_cast<float4*>(dst + q * 32)[i] =
+                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        }
+                    }
+                    if (valid) a.part_ml[static_cast<int64_t>(part) * kRows + row] = make_float2(m, l);
+                }
+            }
+            if (s.n > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(c.base + L::oempty + 8 * o);
+                    if (join) mbar_arrive(c.base + L::oempty + 8);
+                }
+            }
+            if (s.split) {
+                // the last CTA to write its part of the item joins them all, in order
+                const int64_t per = a.head->units, all = per * a.hk;
+                const int64_t u0 = s.g * per + a.pre[s.item], u1 = u0 + max(s.it.ntiles, 1);
+                const int ctas = a.head->ctas;
+                const int c0 = range_owner(all, ctas, u0), c1 = range_owner(all, ctas, u1 - 1);
+                const int id = 1 + wg;
+                __threadfence();
+                ok = bar_sync_and(id, 128, ok);
+                volatile int* last = reinterpret_cast<volatile int*>(c.smem + L::last) + wg;
+                if (tid == 0) {
+                    const unsigned before = ok ? atomicAdd(a.count + c0 * 2 + tile, 1u) : 0u;
+                    *last = ok && before == static_cast<unsigned>(c1 - c0);
+                }
+                bar_sync(id, 128);
+                if (*last) {
+                    __threadfence();
+                    const bool c0_first = range_start(all, ctas, c0) >= u0;
+                    auto index = [&](int cta) {
+                        return static_cast<int64_t>((cta * 2 + (cta == c0 && !c0_first ? 1 : 0)) * L::kTiles + tile) * kRows;
+                    };
+                    for (int e = tid; e < rows * (D / 4); e += 128) {
+                        const int r = e / (D / 4), col = (e - r * (D / 4)) * 4;
+                        float mm = -INFINITY;
+                        for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, __ldcg(a.part_ml + index(p) + r).x);
+                        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        float ll = 0.0f;
+                        for (int p = c0; p <= c1; ++p) {
+                            const float2 ml = __ldcg(a.part_ml + index(p) + r);
+                            const float f = ml.x == mm ? 1.0f : exp2_ftz(ml.x - mm);
+                            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (index(p) + r) * D + col));
+                            ll += ml.y * f;
+                            acc.x += x.x * f;
+                            acc.y += x.y * f;
+                            acc.z += x.z * f;
+                            acc.w += x.w * f;
+                        }
+                        const bool none = ll == 0.0f;
+                        const float inv = none ? 0.0f : 1.0f / ll;
+                        const int tk = r / a.G;
+                        const int64_t tt = s.it.tok0 + tile * a.tq + tk;
+                        const int hh = s.g * a.G + r - tk * a.G;
+                        uint2 y;
+                        y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
+                        y.y = none ? 0u : pack_pair<kBf16>(acc.z * inv, acc.w * inv);
+                        *reinterpret_cast<uint2*>(a.out + tt * a.o_st + hh * a.o_sh + col) = y;
+                        if (a.lse && col == 0)
+                            a.lse[tt * a.G * a.hk + hh] = none ? -INFINITY : (mm - kBias + log2f(ll)) * kLn2;
+                    }
+                }
+                bar_sync(id, 128);   // the flag is free for the next item
+            }
+        }
+        if (join) ++alt;
+        // the ring moves on by the segment's 2 n tiles
+        ring += 2 * s.n * L::kChunks % (2 * L::kSlots);
+        while (ring >= L::kSlots) {
+            ring -= L::kSlots;
+            turn ^= 1;
+        }
+    }
+}
+
+// ------------------------------------------------------------ kernel
+
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+    using L = Smem<D>;
+    extern __shared__ __align__(1024) uint8_t attn_smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Ctx c;
+    c.smem = attn_smem;
+    c.base = smem_u32(attn_smem);
+    c.abort_flag = reinterpret_cast<volatile int*>(attn_smem + L::abort);
+    c.status = a.status;
+    c.spin = a.spin;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::kSlots; ++i) {
+            mbar_init(c.base + L::full + 8 * i, 1);
+            mbar_init(c.base + L::empty + 8 * i, 1);
+        }
+        mbar_init(c.base + L::qfull, 1);
+        mbar_init(c.base + L::qempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(c.base + L::sfull + 8 * i, 1);
+            mbar_init(c.base + L::pfull + 8 * i, 4);
+            mbar_init(c.base + L::odone + 8 * i, 1);
+            mbar_init(c.base + L::oempty + 8 * i, 4);
+            mbar_init(c.base + L::statfull + 8 * i, 4);
+        }
+        mbar_init(c.base + L::drain, 1);
+        *c.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(c.base + L::tmem, 512);
+        tmem_relinquish();
+    }
+    if (warp == kQWarp && lane == 0) {
+        prefetch_tmap(&mq);
+        prefetch_tmap(&mk);
+        prefetch_tmap(&mv);
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(attn_smem + L::tmem);
+    grid_dep_wait();
+    const bool aligned = (c.base & 1023u) == 0;   // the swizzle pattern starts at the slots
+    if (!aligned && threadIdx.x == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+    if (aligned && a.head->units > 0) {
+        if (warp == kLoadWarp) load_keys<D>(c, a, &mk, &mv, lane);
+        else if (warp == kMmaWarp) {
+            if (lane == 0) issue_mma<D, kBf16>(c, a, tmem);
+        } else if (warp == kQWarp) {
+            if (lane == 0) load_queries<D>(c, a, &mq);
+        } else {
+            softmax_rows<D, kBf16>(c, a, tmem, warp >> 2);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------ host
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &qr) !=
+                cudaSuccess ||
+            qr != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+// Map of rows of 64-element chunks, swizzled: dims (d, n1, n2) with element
+// strides s1 and s2, box (64, b1, b2). The stride of an axis of one entry
+// counts for nothing and is replaced.
+bool make_map(CUtensorMap* m, bool bf16, const void* p, int d, int64_t n1, int64_t s1, int64_t n2, int64_t s2,
+              int b1, int b2) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(n1), static_cast<cuuint64_t>(n2)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(n1 > 1 ? s1 : d) * 2, static_cast<cuuint64_t>(n2 > 1 ? s2 : d) * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
+    cuuint32_t es[3] = {1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(p),
+               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Layout {
+    int64_t items_max;
+    size_t head, items, pre, req, starts, count, ml, o, total;
+};
+
+Layout layout(const sp_paged_shape* s, int grid) {
+    Layout l;
+    const int tiles = tiles_per_item(s->head_dim), tq = kRows / (s->n_q_heads / s->n_kv_heads);
+    l.items_max = s->n_tokens / (tq * tiles) + s->n_seqs;
+    size_t off = sizeof(WsHeader);
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = (off + bytes + 255) & ~size_t(255);
+        return o;
+    };
+    l.head = take(sizeof(PlanHead));
+    l.items = take(sizeof(Item) * l.items_max);
+    l.pre = take(8 * (l.items_max + 1));
+    l.req = take(4 * (static_cast<size_t>(s->n_seqs) + 1));
+    l.starts = take(sizeof(Start) * grid);
+    l.count = take(8 * static_cast<size_t>(grid));
+    l.ml = take(8 * static_cast<size_t>(grid) * 2 * tiles * kRows);
+    l.o = take(4 * static_cast<size_t>(grid) * 2 * tiles * kRows * s->head_dim);
+    l.total = off;
+    return l;
+}
+
+template <int D>
+cudaError_t launch_d(const AttnArgs& a, bool bf16, const CUtensorMap& mq, const CUtensorMap& mk,
+                     const CUtensorMap& mv, cudaStream_t st) {
+    auto kern = bf16 ? attn_kernel<D, true> : attn_kernel<D, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(Smem<D>::total));
+    if (e != cudaSuccess) return e;
+    return launch_k(kern, static_cast<unsigned>(a.grid), kAttnThreads, Smem<D>::total, st, mq, mk, mv, a);
 }
 
 }  // namespace
 
-size_t attn_workspace(const sp_paged_shape*) { return sizeof(WsHeader); }
+size_t attn_workspace(const sp_paged_shape* s) { return layout(s, device_sms()).total; }
 
 cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params* p, const int32_t* q_off,
                                    const int32_t* kv_len, const int32_t* table, const uint16_t* q,
                                    const uint16_t* k_pool, const uint16_t* v_pool, uint16_t* out, float* lse,
                                    void* ws, cudaStream_t st) {
+    const int d = s->head_dim, bs = s->block_size;
+    const bool bf16 = s->dtype == SP_DTYPE_BF16;
     AttnArgs a;
+    a.grid = device_sms();
+    const Layout l = layout(s, a.grid);
     a.q_off = q_off;
     a.kv_len = kv_len;
     a.table = table;
-    a.q = q;
-    a.k = k_pool;
-    a.v = v_pool;
     a.out = out;
     a.lse = lse;
     a.status = &ws_ptr<WsHeader>(ws, 0)->status;
-    a.q_st = s->q_stride_token, a.q_sh = s->q_stride_head;
+    a.head = ws_ptr<PlanHead>(ws, l.head);
+    a.items = ws_ptr<Item>(ws, l.items);
+    a.pre = ws_ptr<int64_t>(ws, l.pre);
+    a.req_item = ws_ptr<int32_t>(ws, l.req);
+    a.starts = ws_ptr<Start>(ws, l.starts);
+    a.count = ws_ptr<unsigned>(ws, l.count);
+    a.part_o = ws_ptr<float>(ws, l.o);
+    a.part_ml = ws_ptr<float2>(ws, l.ml);
     a.o_st = s->o_stride_token, a.o_sh = s->o_stride_head;
-    a.k_st = s->k_stride_token, a.k_sh = s->k_stride_head;
-    a.v_st = s->v_stride_token, a.v_sh = s->v_stride_head;
     a.pool_tokens = s->pool_tokens;
+    a.spin = p->spin_limit > 0 ? p->spin_limit : kDefaultSpin;
     a.B = s->n_seqs;
-    a.hq = s->n_q_heads;
     a.hk = s->n_kv_heads;
-    a.G = a.hq / a.hk;
-    a.bs = s->block_size;
+    a.G = s->n_q_heads / s->n_kv_heads;
+    a.tq = kRows / a.G;
+    a.bs = bs;
     a.table_stride = s->table_stride;
     a.cap = s->n_tokens;
     a.causal = p->causal;
     a.window = p->window;
-    const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(s->head_dim));
+    a.hk_box = bs < kKeys ? bs : kKeys;
+    const int per = kKeys / (d / 64);
+    a.hv_box = bs < per ? bs : per;
+    a.q_bytes = static_cast<uint32_t>(a.G * a.tq) * 128u;
+    const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(d));
     a.scale2 = static_cast<float>(scale * 1.4426950408889634);
-    const bool bf = s->dtype == SP_DTYPE_BF16;
-    auto kern = s->head_dim == 64    ? (bf ? attn_rows_kernel<64, true> : attn_rows_kernel<64, false>)
-                : s->head_dim == 128 ? (bf ? attn_rows_kernel<128, true> : attn_rows_kernel<128, false>)
-                                     : (bf ? attn_rows_kernel<256, true> : attn_rows_kernel<256, false>);
-    return launch_k(kern, static_cast<unsigned>(8 * device_sms()), kAttnThreads, 0, st, a);
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, bf16, q, d, s->n_q_heads, s->q_stride_head, s->n_tokens, s->q_stride_token, a.G, a.tq) ||
+        !make_map(&mk, bf16, k_pool, d, s->pool_tokens, s->k_stride_token, a.hk, s->k_stride_head, a.hk_box, 1) ||
+        !make_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, a.hv_box, 1))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = launch_k(attn_plan_kernel, 1, kPlanThreads, 0, st, a, tiles_per_item(d));
+    if (e != cudaSuccess) return e;
+    return d == 64    ? launch_d<64>(a, bf16, mq, mk, mv, st)
+           : d == 128 ? launch_d<128>(a, bf16, mq, mk, mv, st)
+                      : launch_d<256>(a, bf16, mq, mk, mv, st);
 }
 
 }  // namespace sp
