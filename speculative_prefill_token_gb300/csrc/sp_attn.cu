@@ -294,7 +294,7 @@ struct Smem {
     static constexpr uint32_t qempty = qfull + 8;
     static constexpr uint32_t sfull = qempty + 8;     // [2] logits written
     static constexpr uint32_t pfull = sfull + 16;     // [2] weights written
-    static constexpr uint32_t odone = pfull + 16;     // [2] accumulator updated
+    static constexpr uint32_t odone = pfull + 16;     // [2] weights of a stream buffer in the accumulator
     static constexpr uint32_t oempty = odone + 16;    // [2] accumulator read
     static constexpr uint32_t statfull = oempty + 16; // [2] second stream's sums written
     static constexpr uint32_t drain = statfull + 16;
@@ -513,7 +513,7 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
             if (release) tc_commit(c.base + L::empty + 8 * p.slot);
             step(p);
         }
-        tc_commit(c.base + L::odone + 8 * o);
+        tc_commit(c.base + L::odone + 8 * sb);
         return p;
     };
 
@@ -621,6 +621,14 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
         const int j0 = two ? 0 : wg, dj = whole ? 1 : 2;
         const bool works = s.n > 0 && !(D > 128 && wg == 1);
         float m = -INFINITY, l = 0.0f;
+        // waits until the weights of tile j are in the accumulator. (Every
+        // stream buffer has a barrier of its own, also where both feed one
+        // accumulator: once the logits of a tile are there, all updates but
+        // the last of each buffer have ended, so one parity tells.)
+        auto updated = [&](int j) {
+            const int b = two ? wg : j & 1;
+            return __all_sync(kAll, c.wait(L::odone + 8 * b, (cnt[b] + (two ? j : j >> 1)) & 1)) != 0;
+        };
         if (works) {
             for (int j = j0; j < s.n; j += dj) {
                 const int sb = two ? wg : j & 1;
@@ -663,8 +671,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                         // the accumulator holds earlier tiles of this segment
                         if (j > j0) {
                             const int o = D > 128 ? 0 : sb;
-                            const uint32_t pvs = D > 128 ? cnt[0] + cnt[1] + j : seen;   // updates before this tile
-                            ok = __all_sync(kAll, c.wait(L::odone + 8 * o, (pvs - 1) & 1));
+                            ok = updated(j - dj);
                             if (!ok) break;
                             tc_fence_after();
                             const uint32_t ot = tmem + lanes + 2 * kKeys + o * D;
@@ -705,6 +712,9 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                     int p = place % L::kSlots;
                     uint32_t ph = turn ^ (place / L::kSlots & 1);
                     constexpr int kPer = kKeys / L::kChunks;
+                    // d = 256: the slots of V_j are those of V_{j-1} and K_j, ten
+                    // slots back; V_{j-1} is consumed before they are looked at
+                    if (D > 128 && j > 0) ok = updated(j - 1);
 #pragma unroll 1
                     for (int part = 0; part < L::kChunks && ok; ++part) {
                         ok = __all_sync(kAll, c.wait(L::full + 8 * p, ph));
@@ -745,7 +755,8 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             const int o = two ? wg : 0;
             float f0 = 1.0f, f1 = 0.0f;
             if (s.n > 0) {
-                if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8 * o, ((D > 128 ? cnt[0] + cnt[1] : cnt[o]) - 1) & 1));
+                const int b = D > 128 ? (s.n - 1) & 1 : o;   // buffer of the last update
+                if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8 * b, (cnt[b] - 1) & 1));
                 if (join) {
                     if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8, (cnt[1] - 1) & 1) && c.wait(L::statfull + 8 * (alt & 1), alt >> 1 & 1));
                     if (ok) {

@@ -70,10 +70,18 @@ def test_longer_contexts_split_over_many_ctas(cuda_lib, d):
     _check(cuda_lib, [9000, 200], [3, 1], 4, 1, d, 128, "bf16", seed=5)
 
 
+@pytest.mark.parametrize("d,hq,hk", [(64, 6, 2), (128, 16, 4), (256, 8, 2)])
+def test_last_keys_of_a_long_context_end_inside_a_tile(cuda_lib, d, hq, hk):
+    """Many key tiles for each CTA, the last one partly behind the end."""
+    _check(cuda_lib, [32768], [8], hq, hk, d, 16, "bf16", seed=12)
+    _check(cuda_lib, [6001, 12000, 16383, 4097, 8200, 777], [1, 1, 1, 1, 3, 1], hq, hk, d, 16, "bf16", seed=13)
+
+
 def test_prompt_of_several_query_tiles(cuda_lib):
     _check(cuda_lib, [0], [1100], 4, 1, 128, 64, "bf16", seed=9)
     _check(cuda_lib, [37], [700], 2, 1, 256, 16, "bf16", seed=10)
     _check(cuda_lib, [37], [901], 3, 1, 64, 16, "fp16", seed=11)
+    _check(cuda_lib, [0], [2500], 8, 2, 256, 64, "bf16", seed=14)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
