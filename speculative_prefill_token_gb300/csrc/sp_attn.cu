@@ -21,13 +21,13 @@
 // do not depend on timing. The lengths live on the device: a one-CTA kernel
 // lays out the items and the ranges.
 //
-// Roles (352 threads):
+// Roles (384 threads):
 //   warps 0-7  two softmax warpgroups. A thread owns one row of a 128 x 128
 //              logits tile: reads it from tensor memory, takes the maximum,
 //              writes the weights back as 16-bit values in its place, keeps
 //              the sum, and writes or joins the result at the item's end.
-//   warp 8     K and V boxes by TMA (lane j issues box j of a 16 KB slot)
-//   warp 9     tcgen05.mma issuer (one thread) and TMEM owner
+//   warp 8     K and V boxes by TMA (lane j issues box j of a slot)
+//   warp 9     tcgen05.mma issuer and TMEM owner
 //   warp 10    query tiles by TMA
 // Two streams keep the tensor cores busy while the other stream's softmax
 // runs: with two query tiles, one tile each; with one (decode steps, short
@@ -55,8 +55,8 @@ namespace {
 
 constexpr int kKeys = 128;                 // keys of a tile (a unit of work)
 constexpr int kRows = 128;                 // rows of a query tile
-constexpr uint32_t kSlot = 16384;          // bytes of a ring slot
-constexpr int kWarps = 11;
+constexpr uint32_t kChunk = 16384;         // bytes of 128 rows x 64 elements
+constexpr int kWarps = 12;                 // (the last one idle: registers move by warpgroup)
 constexpr int kAttnThreads = 32 * kWarps;
 constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10;
 constexpr int kPlanThreads = 1024;
@@ -64,7 +64,11 @@ constexpr int64_t kDrainSpin = int64_t(1) << 22;
 constexpr float kSlack = 8.0f;             // log2 units the reference may lag behind the maximum
 
 __host__ __device__ constexpr int tiles_per_item(int d) { return d <= 128 ? 2 : 1; }
-__host__ __device__ constexpr int ring_slots(int d) { return d == 64 ? 12 : 10; }
+// A ring slot holds a whole K or V tile (d = 256: half of one): the MMA warp
+// waits once for each. (16 KB slots at d = 128: a wait before every four MMAs,
+// 100 cycles that the MMA queue is too short to hide.)
+__host__ __device__ constexpr int slots_per_tile(int d) { return d == 256 ? 2 : 1; }
+__host__ __device__ constexpr int ring_slots(int d) { return d == 64 ? 12 : 5; }
 
 // One item: rows of `ntok` tokens from row tok0 of q, the first at cache
 // index pos0; keys [klo, khi) are seen by some row, in tiles
@@ -282,10 +286,14 @@ __device__ __forceinline__ int v_position(bool two, int j, int n) {
 template <int D>
 struct Smem {
     static constexpr int kTiles = tiles_per_item(D);
-    static constexpr int kChunks = D / 64;         // slots of a K or V tile
+    static constexpr int kChunks = D / 64;         // 64-element chunks of a row
+    static constexpr int kParts = slots_per_tile(D);
     static constexpr int kSlots = ring_slots(D);
+    static constexpr uint32_t kSlot = kChunks / kParts * kChunk;   // bytes
+    static constexpr int kSlotChunks = kChunks / kParts;           // of a K slot (128 keys)
+    static constexpr int kSlotKeys = kKeys / kParts;               // of a V slot (all chunks)
     static constexpr uint32_t q = 0;
-    static constexpr uint32_t ring = kTiles * kChunks * kSlot;
+    static constexpr uint32_t ring = kTiles * kChunks * kChunk;
     static constexpr uint32_t stat = ring + kSlots * kSlot;   // [2][128] float2
     static constexpr uint32_t bars = stat + 2 * kRows * 8;
     static constexpr uint32_t full = bars;
@@ -331,12 +339,11 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
                                           const CUtensorMap* mv, int lane) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
-    constexpr int kPer = kKeys / L::kChunks;   // keys of a V slot
-    const int nk = kKeys / a.hk_box;           // K boxes of a tile
+    constexpr int kPer = L::kSlotKeys;
+    const int nk = kKeys / a.hk_box;           // K boxes of a tile and chunk
     const int sub = kPer / a.hv_box;           // V boxes of a slot and chunk
     int slot = 0;
     uint32_t turn = 0;
-    uint32_t used = 0, last_turn[L::kSlots];
     bool ok = true;
 
     // pool row of this lane's K box of a tile; -1 outside the item's keys
@@ -361,27 +368,27 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
         return ok;
     };
     auto advance = [&]() {
-        used |= 1u << slot;
-#pragma unroll
-        for (int i = 0; i < L::kSlots; ++i)
-            if (i == slot) last_turn[i] = turn;
         if (++slot == L::kSlots) {
             slot = 0;
             turn ^= 1;
         }
     };
     auto put_k = [&](const Segment& s, int row) {
-        const uint32_t bytes = __popc(__ballot_sync(kAll, row >= 0)) * a.hk_box * 128u;
-        for (int ch = 0; ch < L::kChunks; ++ch) {
+        // lane: box r of chunk ch of the slot
+        const int r = lane / L::kSlotChunks, ch = lane % L::kSlotChunks;
+        const int mine = __shfl_sync(kAll, row, r);
+        const bool there = r < nk && mine >= 0;
+        const uint32_t bytes = __popc(__ballot_sync(kAll, there)) * a.hk_box * 128u;
+        for (int p = 0; p < L::kParts; ++p) {
             if (!acquire(bytes)) return;
-            if (row >= 0)
-                tma_load_3d(c.base + L::ring + slot * kSlot + static_cast<uint32_t>(lane * a.hk_box) * 128u, mk,
-                            c.base + L::full + 8 * slot, ch * 64, row, s.g);
+            if (there)
+                tma_load_3d(c.base + L::ring + slot * L::kSlot + ch * kChunk + static_cast<uint32_t>(r * a.hk_box) * 128u,
+                            mk, c.base + L::full + 8 * slot, (p * L::kSlotChunks + ch) * 64, mine, s.g);
             advance();
         }
     };
     auto put_v = [&](const Segment& s, int tile, int row) {
-        for (int p = 0; p < L::kChunks; ++p) {
+        for (int p = 0; p < L::kParts; ++p) {
             // lane: sub-box r of chunk ch; its K box holds the block's row
             const int r = lane / L::kChunks, ch = lane % L::kChunks;
             const int key = p * kPer + r * a.hv_box;       // of the tile
@@ -392,7 +399,7 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
             const uint32_t bytes = __popc(__ballot_sync(kAll, mine)) * a.hv_box * 128u;
             if (!acquire(bytes)) return;
             if (mine)
-                tma_load_3d(c.base + L::ring + slot * kSlot + static_cast<uint32_t>(ch * kPer + r * a.hv_box) * 128u,
+                tma_load_3d(c.base + L::ring + slot * L::kSlot + static_cast<uint32_t>(ch * kPer + r * a.hv_box) * 128u,
                             mv, c.base + L::full + 8 * slot, ch * 64, base_row + key % a.hk_box, s.g);
             advance();
         }
@@ -415,12 +422,12 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
             next = after;
         }
     }
-    // every copy this warp issued lands before it leaves
-    if (lane == 0) {
-#pragma unroll
+    // every copy this warp issued lands before it leaves: slots before `slot`
+    // were last used in this turn of the ring, the others in the one before
+    // (a wait on a first turn's parity 1 returns at once)
+    if (lane == 0)
         for (int i = 0; i < L::kSlots; ++i)
-            if (used >> i & 1) mbar_wait_spin(c.base + L::full + 8 * i, last_turn[i], kDrainSpin);
-    }
+            mbar_wait_spin(c.base + L::full + 8 * i, i < slot ? turn : turn ^ 1, kDrainSpin);
 }
 
 template <int D>
@@ -436,7 +443,7 @@ __device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, co
         mbar_arrive_expect_tx(c.base + L::qfull, a.q_bytes * L::kChunks * tiles);
         for (int t = 0; t < tiles; ++t)
             for (int ch = 0; ch < L::kChunks; ++ch)
-                tma_load_3d(c.base + L::q + (t * L::kChunks + ch) * kSlot, mq, c.base + L::qfull, ch * 64, s.g * a.G,
+                tma_load_3d(c.base + L::q + (t * L::kChunks + ch) * kChunk, mq, c.base + L::qfull, ch * 64, s.g * a.G,
                             s.it.tok0 + t * a.tq);
         ++n;
     }
@@ -445,21 +452,29 @@ __device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, co
 
 // ------------------------------------------------------------ MMA
 
+// Run by the whole warp: control flow and descriptors are the same in every
+// lane (broadcasts tell the compiler so: operands then stay in uniform
+// registers; issued by one diverged lane, eight MMAs took some 1,300 cycles),
+// and one elected lane issues.
 template <int D, bool kBf16>
-__device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint32_t tmem) {
+__device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint32_t tmem_base) {
     using L = Smem<D>;
+    constexpr unsigned kAll = 0xffffffffu;
     constexpr uint32_t kIdQk = idesc_f16_f32(kRows, kKeys, kBf16, false);
     constexpr uint32_t kIdPv = idesc_f16_f32(kRows, D, kBf16, true);
-    constexpr int kPer = kKeys / L::kChunks;
-    int slot = 0;
-    uint32_t turn = 0;
+    constexpr int kPer = L::kSlotKeys;
+    const uint32_t tmem = __shfl_sync(kAll, tmem_base, 0);
+    const uint32_t base = __shfl_sync(kAll, c.base, 0);
     uint32_t nq = 0;                 // segments with keys so far
-    uint32_t np[2] = {0, 0};         // weight tiles consumed of each stream
-    uint32_t no[2] = {0, 0};         // segments that used each accumulator
+    uint32_t np0 = 0, np1 = 0;       // weight tiles consumed of each stream
+    uint32_t no0 = 0, no1 = 0;       // segments that used each accumulator
     bool ok = true, any = false;
 
-    // the ring position of the next tile is tracked by (slot, turn); a V tile
-    // that both query tiles use is walked twice from the same place
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok) ok = __all_sync(kAll, c.wait(bar, parity));
+        return ok;
+    };
+    // a place in the ring; a tile that both query tiles use is walked twice
     struct Place {
         int slot;
         uint32_t turn;
@@ -470,94 +485,102 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
             p.turn ^= 1;
         }
     };
-    // logits of query tile t and the K tile at p into stream buffer sb
-    auto qk = [&](Place p, int t, int sb, bool release) -> Place {
+    // logits of query tile t and the K tile at p into stream buffer sb;
+    // `fresh`: its slots have not been waited for
+    auto qk = [&](Place p, int t, int sb, bool fresh, bool release) -> Place {
 #pragma unroll 1
-        for (int ch = 0; ch < L::kChunks; ++ch) {
-            if (ok) ok = c.wait(L::full + 8 * p.slot, p.turn);
-            if (!ok) return p;
+        for (int part = 0; part < L::kParts; ++part) {
+            if (fresh && !wait(L::full + 8 * p.slot, p.turn)) return p;
             tc_fence_after();
-            const uint32_t qa = c.base + L::q + (t * L::kChunks + ch) * kSlot;
-            const uint32_t ka = c.base + L::ring + p.slot * kSlot;
+            const int slot = __shfl_sync(kAll, p.slot, 0);
+            const uint64_t qd = smem_desc_sw128(base + L::q + t * L::kChunks * kChunk + part * L::kSlot);
+            const uint64_t kd = smem_desc_sw128(base + L::ring + slot * L::kSlot);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                tc_mma_bf16(tmem + sb * kKeys, smem_desc_sw128(qa + 32 * k), smem_desc_sw128(ka + 32 * k), kIdQk,
-                            (ch | k) != 0);
-            any = true;
-            if (release) tc_commit(c.base + L::empty + 8 * p.slot);
+                for (int k = 0; k < 4 * L::kSlotChunks; ++k)
+                    tc_mma_bf16(tmem + sb * kKeys, qd + (k / 4) * (kChunk / 16) + 2 * (k % 4),
+                                kd + (k / 4) * (kChunk / 16) + 2 * (k % 4), kIdQk, (part | k) != 0);
+                if (release) tc_commit(base + L::empty + 8 * slot);
+                if (part == L::kParts - 1) tc_commit(base + L::sfull + 8 * sb);
+            }
             step(p);
         }
-        tc_commit(c.base + L::sfull + 8 * sb);
+        any = true;
         return p;
     };
     // accumulator o (+)= weights of stream sb times the V tile at p
-    auto pv = [&](Place p, int sb, int o, bool first, bool release) -> Place {
-        if (ok) ok = c.wait(L::pfull + 8 * sb, np[sb] & 1);
-        if (!ok) return p;
-        ++np[sb];
-        if (first) {
-            ok = c.wait(L::oempty + 8 * o, (no[o] & 1) ^ 1);
-            if (!ok) return p;
-            ++no[o];
-        }
+    auto pv = [&](Place p, int sb, int o, bool fresh, bool first, bool release) -> Place {
+        if (first && !wait(L::oempty + 8 * o, (o ? no1++ : no0++) & 1 ^ 1)) return p;
+        if (!wait(L::pfull + 8 * sb, (sb ? np1++ : np0++) & 1)) return p;
 #pragma unroll 1
-        for (int part = 0; part < L::kChunks; ++part) {
-            ok = c.wait(L::full + 8 * p.slot, p.turn);
-            if (!ok) return p;
+        for (int part = 0; part < L::kParts; ++part) {
+            if (fresh && !wait(L::full + 8 * p.slot, p.turn)) return p;
             tc_fence_after();
-            const uint32_t va = c.base + L::ring + p.slot * kSlot;
+            const int slot = __shfl_sync(kAll, p.slot, 0);
+            const uint64_t vd = smem_desc_sw128_mn(base + L::ring + slot * L::kSlot, kPer * 128);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kPer / 16; ++k)
-                tc_mma_f16_ts(tmem + 2 * kKeys + o * D, tmem + sb * kKeys + (part * (kPer / 16) + k) * 8,
-                              smem_desc_sw128_mn(va + 2048 * k, kPer * 128), kIdPv, !first || (part | k) != 0);
-            if (release) tc_commit(c.base + L::empty + 8 * p.slot);
+                for (int k = 0; k < kPer / 16; ++k)
+                    tc_mma_f16_ts(tmem + 2 * kKeys + o * D, tmem + sb * kKeys + (part * (kPer / 16) + k) * 8,
+                                  vd + 128 * k, kIdPv, !first || (part | k) != 0);
+                if (release) tc_commit(base + L::empty + 8 * slot);
+                if (part == L::kParts - 1) tc_commit(base + L::odone + 8 * sb);
+            }
             step(p);
         }
-        tc_commit(c.base + L::odone + 8 * sb);
         return p;
+    };
+    auto queries_read = [&]() {
+        if (elect_one()) tc_commit(base + L::qempty);
     };
 
     Walk w(a);
     Segment s;
-    Place at{slot, turn};
+    Place at{0, 0};
     while (ok && w.next(a, s)) {
-        if (s.n == 0) continue;
-        ok = c.wait(L::qfull, nq & 1);
-        if (!ok) break;
+        const int n = __shfl_sync(kAll, s.n, 0);
+        if (n == 0) continue;
+        if (!wait(L::qfull, nq & 1)) break;
         ++nq;
-        if (two_tiles(a, s, D)) {
-            qk(at, 0, 0, false);
-            at = qk(at, 1, 1, true);
-            if (s.n == 1) tc_commit(c.base + L::qempty);
-            for (int j = 0; j < s.n && ok; ++j) {
+        if (__shfl_sync(kAll, static_cast<int>(two_tiles(a, s, D)), 0)) {
+            qk(at, 0, 0, true, false);
+            at = qk(at, 1, 1, false, true);
+            if (n == 1) queries_read();
+            for (int j = 0; j < n && ok; ++j) {
                 const Place v = at;
-                at = pv(v, 0, 0, j == 0, false);
-                const Place k = at;
-                if (j + 1 < s.n) qk(k, 0, 0, false);
-                pv(v, 1, 1, j == 0, true);
-                if (j + 1 < s.n) {
-                    at = qk(k, 1, 1, true);
-                    if (j + 2 == s.n) tc_commit(c.base + L::qempty);
+                const Place k = pv(v, 0, 0, true, j == 0, false);
+                if (j + 1 < n) qk(k, 0, 0, true, false);
+                at = pv(v, 1, 1, false, j == 0, true);
+                if (j + 1 < n) {
+                    at = qk(k, 1, 1, false, true);
+                    if (j + 2 == n) queries_read();
                 }
             }
         } else {
-            at = qk(at, 0, 0, true);
-            if (s.n > 1) at = qk(at, 0, 1, true);
-            if (s.n <= 2) tc_commit(c.base + L::qempty);
+            at = qk(at, 0, 0, true, true);
+            if (n > 1) at = qk(at, 0, 1, true, true);
+            if (n <= 2) queries_read();
             // ring: V0 K2 V1 K3 ...
-            for (int j = 0; j < s.n && ok; ++j) {
-                const int sb = j & 1;
-                at = pv(at, sb, D <= 128 ? sb : 0, D <= 128 ? j < 2 : j == 0, true);
-                if (j + 2 < s.n) {
-                    at = qk(at, 0, sb, true);
-                    if (j + 3 == s.n) tc_commit(c.base + L::qempty);
+            for (int j = 0; j < n && ok; j += 2) {
+                at = pv(at, 0, 0, true, j == 0, true);
+                if (j + 2 < n) {
+                    at = qk(at, 0, 0, true, true);
+                    if (j + 3 == n) queries_read();
+                }
+                if (j + 1 < n) {
+                    at = pv(at, 1, D <= 128 ? 1 : 0, true, D <= 128 && j == 0, true);
+                    if (j + 3 < n) {
+                        at = qk(at, 0, 1, true, true);
+                        if (j + 4 == n) queries_read();
+                    }
                 }
             }
         }
     }
     if (any) {
-        tc_commit(c.base + L::drain);
-        mbar_wait_spin(c.base + L::drain, 0, kDrainSpin);
+        if (elect_one()) tc_commit(base + L::drain);
+        __syncwarp();
+        mbar_wait_spin(base + L::drain, 0, kDrainSpin);
     }
 }
 
@@ -572,6 +595,32 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
         const __half2 v = __floats2half2_rn(x, y);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
 }
 
 __device__ __forceinline__ void bar_sync(int id, int count) {
@@ -596,7 +645,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
     const int row = warp * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const int tid = threadIdx.x & 127;
-    uint32_t cnt[2] = {0, 0};    // tiles of each stream buffer before this segment
+    uint32_t cnt0 = 0, cnt1 = 0; // tiles of each stream buffer before this segment
     uint32_t alt = 0;            // segments joined from two accumulators so far
     int ring = 0;                // slot of the segment's first K tile
     uint32_t turn = 0;           // and its turn
@@ -627,13 +676,13 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
         // the last of each buffer have ended, so one parity tells.)
         auto updated = [&](int j) {
             const int b = two ? wg : j & 1;
-            return __all_sync(kAll, c.wait(L::odone + 8 * b, (cnt[b] + (two ? j : j >> 1)) & 1)) != 0;
+            return __all_sync(kAll, c.wait(L::odone + 8 * b, ((b ? cnt1 : cnt0) + (two ? j : j >> 1)) & 1)) != 0;
         };
         if (works) {
             for (int j = j0; j < s.n; j += dj) {
                 const int sb = two ? wg : j & 1;
                 const uint32_t k = two ? j : j >> 1;
-                const uint32_t seen = cnt[sb] + k;     // tiles of this buffer before this one
+                const uint32_t seen = (sb ? cnt1 : cnt0) + k;     // tiles of this buffer before this one
                 if (ok) ok = __all_sync(kAll, c.wait(L::sfull + 8 * sb, seen & 1));
                 if (!ok) break;
                 tc_fence_after();
@@ -657,11 +706,11 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                     float mx[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        mx[q] = v[q][0];
+                        mx[q] = fmaxf(v[q][0], v[q][1]);
 #pragma unroll
-                        for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], v[q][i]);
+                        for (int i = 2; i < 32; i += 2) mx[q] = max3(mx[q], v[q][i], v[q][i + 1]);
                     }
-                    const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale2;
+                    const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale2;
                     const bool move = mt > m + kSlack;
                     if (__any_sync(kAll, move)) {
                         const float mn = move ? mt : m;
@@ -687,20 +736,23 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                         }
                     }
                     const float shift = (m == -INFINITY ? 0.0f : -m) + kBias;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float2 scale = make_float2(a.scale2, a.scale2), move2 = make_float2(shift, shift);
+                    float2 sum[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
                         uint32_t pk[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float x = exp2_ftz(fmaf(v[q][2 * i], a.scale2, shift));
-                            const float y = exp2_ftz(fmaf(v[q][2 * i + 1], a.scale2, shift));
-                            sum[i & 3] += x + y;
-                            pk[i] = pack_pair<kBf16>(x, y);
+                            float2 x = fma2(make_float2(v[q][2 * i], v[q][2 * i + 1]), scale, move2);
+                            x.x = exp2_ftz(x.x);
+                            x.y = exp2_ftz(x.y);
+                            sum[i & 3] = (q == 0 && i < 4) ? x : add2(sum[i & 3], x);
+                            pk[i] = pack_pair<kBf16>(x.x, x.y);
                         }
                         tmem_st_32x32b_x16(st + 16 * q, pk);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                    l += sum[0].x + sum[0].y;
                     tmem_st_wait();
                 }
                 // V rows outside the item's keys are not loaded: zeros, so that
@@ -708,20 +760,20 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                 // warpgroup's zeros are in place before either product)
                 const int z0 = max(s.it.klo - key0, 0), z1 = min(s.it.khi - key0, kKeys);
                 if ((z0 > 0 || z1 < kKeys) && !(two && wg == 1)) {
-                    const int place = ring + v_position(two, j, s.n) * L::kChunks;
+                    const int place = ring + v_position(two, j, s.n) * L::kParts;
                     int p = place % L::kSlots;
                     uint32_t ph = turn ^ (place / L::kSlots & 1);
-                    constexpr int kPer = kKeys / L::kChunks;
-                    // d = 256: the slots of V_j are those of V_{j-1} and K_j, ten
+                    constexpr int kPer = L::kSlotKeys;
+                    // d = 256: the slots of V_j are those of V_{j-1} and K_j, five
                     // slots back; V_{j-1} is consumed before they are looked at
                     if (D > 128 && j > 0) ok = updated(j - 1);
 #pragma unroll 1
-                    for (int part = 0; part < L::kChunks && ok; ++part) {
+                    for (int part = 0; part < L::kParts && ok; ++part) {
                         ok = __all_sync(kAll, c.wait(L::full + 8 * p, ph));
                         if (!ok) break;
                         // rows of this slot, 8 vectors a row and chunk
-                        uint4* v = reinterpret_cast<uint4*>(c.smem + L::ring + p * kSlot);
-                        for (int e = tid; e < kSlot / 16; e += 128) {
+                        uint4* v = reinterpret_cast<uint4*>(c.smem + L::ring + p * L::kSlot);
+                        for (int e = tid; e < static_cast<int>(L::kSlot / 16); e += 128) {
                             const int key = part * kPer + (e >> 3) % kPer;
                             if (key < z0 || key >= z1) v[e] = make_uint4(0, 0, 0, 0);
                         }
@@ -748,17 +800,17 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             __syncwarp();
             if (lane == 0) mbar_arrive(c.base + L::statfull + 8 * (alt & 1));
         }
-        cnt[0] += buf0;
-        cnt[1] += buf1;
+        cnt0 += buf0;
+        cnt1 += buf1;
         const bool ends = two || wg == 0;   // this warpgroup writes rows
         if (ends) {
             const int o = two ? wg : 0;
             float f0 = 1.0f, f1 = 0.0f;
             if (s.n > 0) {
                 const int b = D > 128 ? (s.n - 1) & 1 : o;   // buffer of the last update
-                if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8 * b, (cnt[b] - 1) & 1));
+                if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8 * b, ((b ? cnt1 : cnt0) - 1) & 1));
                 if (join) {
-                    if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8, (cnt[1] - 1) & 1) && c.wait(L::statfull + 8 * (alt & 1), alt >> 1 & 1));
+                    if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8, (cnt1 - 1) & 1) && c.wait(L::statfull + 8 * (alt & 1), alt >> 1 & 1));
                     if (ok) {
                         const float2 other = stat[row];
                         const float mn = fmaxf(m, other.x);
@@ -889,7 +941,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
         }
         if (join) ++alt;
         // the ring moves on by the segment's 2 n tiles
-        ring += 2 * s.n * L::kChunks % (2 * L::kSlots);
+        ring += 2 * s.n * L::kParts % (2 * L::kSlots);
         while (ring >= L::kSlots) {
             ring -= L::kSlots;
             turn ^= 1;
@@ -946,15 +998,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     grid_dep_wait();
     const bool aligned = (c.base & 1023u) == 0;   // the swizzle pattern starts at the slots
     if (!aligned && threadIdx.x == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
-    if (aligned && a.head->units > 0) {
-        if (warp == kLoadWarp) load_keys<D>(c, a, &mk, &mv, lane);
-        else if (warp == kMmaWarp) {
-            if (lane == 0) issue_mma<D, kBf16>(c, a, tmem);
-        } else if (warp == kQWarp) {
-            if (lane == 0) load_queries<D>(c, a, &mq);
-        } else {
-            softmax_rows<D, kBf16>(c, a, tmem, warp >> 2);
+    const bool work = aligned && a.head->units > 0;
+    // 384 threads x 168 registers at launch = 64,512; 128 x 80 + 256 x 208 = 63,488
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        if (work) {
+            if (warp == kLoadWarp) load_keys<D>(c, a, &mk, &mv, lane);
+            else if (warp == kMmaWarp) issue_mma<D, kBf16>(c, a, tmem);
+            else if (warp == kQWarp && lane == 0) load_queries<D>(c, a, &mq);
         }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (work) softmax_rows<D, kBf16>(c, a, tmem, warp >> 2);
     }
     tc_fence_before();
     __syncthreads();
