@@ -16,10 +16,13 @@
 // time (two tiles of 128 rows for d <= 128, one for d = 256, whose
 // accumulator fills the tensor memory); its unit is a tile of 128 keys. All
 // units of all items are cut into equal contiguous ranges, one for each CTA
-// (one CTA per SM), whatever the mix of lengths; an item cut between CTAs is
-// joined by the last of them to finish, in the order of the parts, so results
-// do not depend on timing. The lengths live on the device: a one-CTA kernel
-// lays out the items and the ranges.
+// (one CTA per SM), whatever the mix of lengths. The lengths live on the
+// device: a one-CTA kernel lays out the items and the ranges first. An item
+// cut between CTAs leaves a part in the workspace for each of them (reference,
+// sum and accumulator of each row), and a third kernel joins the parts in
+// their order, so results do not depend on timing. (Joined by the last CTA to
+// finish instead, the 76 parts of a single long chunk were read by two CTAs:
+// 245 us in place of 10 for 8 tokens over 32K.)
 //
 // Roles (384 threads):
 //   warps 0-7  two softmax warpgroups. A thread owns one row of a 128 x 128
@@ -63,6 +66,12 @@ constexpr int kPlanThreads = 1024;
 constexpr int64_t kDrainSpin = int64_t(1) << 22;
 constexpr float kSlack = 8.0f;             // log2 units the reference may lag behind the maximum
 
+constexpr float kLn2 = 0.6931471805599453f;
+
+// fp16 weights are scaled by 2^6: their subnormals then start 20 binary
+// orders below the maximum, and the largest weight is 2^14.
+__host__ __device__ constexpr float weight_bias(bool bf16) { return bf16 ? 0.0f : 6.0f; }
+
 __host__ __device__ constexpr int tiles_per_item(int d) { return d <= 128 ? 2 : 1; }
 // A ring slot holds a whole K or V tile (d = 256: half of one): the MMA warp
 // waits once for each. (16 KB slots at d = 128: a wait before every four MMAs,
@@ -101,7 +110,6 @@ struct AttnArgs {
     int64_t* pre;       // units before each item, [items + 1]
     int32_t* req_item;  // first item of each request, [B + 1]
     Start* starts;      // [grid]
-    unsigned* count;    // [grid][2] parts of the item first met by a CTA that are written
     float* part_o;      // [grid * 2][tiles][128][d]
     float2* part_ml;    // [grid * 2][tiles][128] (reference, sum)
     int64_t o_st, o_sh, pool_tokens, spin;
@@ -141,7 +149,6 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
     grid_dep_launch();
     const int tid = threadIdx.x;
     const int tpi = a.tq * tiles;   // tokens per item
-    for (int i = tid; i < a.grid * 2; i += kPlanThreads) a.count[i] = 0;
     int bad = a.q_off[0] != 0;
     int64_t items = 0;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
@@ -308,8 +315,7 @@ struct Smem {
     static constexpr uint32_t drain = statfull + 16;
     static constexpr uint32_t tmem = drain + 8;
     static constexpr uint32_t abort = tmem + 8;
-    static constexpr uint32_t last = abort + 4;       // [2] this warpgroup joins the item
-    static constexpr uint32_t total = last + 12;
+    static constexpr uint32_t total = abort + 8;
 };
 
 static_assert(Smem<64>::total <= 232448 && Smem<128>::total <= 232448 && Smem<256>::total <= 232448,
@@ -623,10 +629,6 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     return r;
 }
 
-__device__ __forceinline__ void bar_sync(int id, int count) {
-    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
-}
-
 // The CTA whose range holds unit u of `total`.
 __device__ __forceinline__ int range_owner(int64_t total, int ctas, int64_t u) {
     return static_cast<int>(((u + 1) * ctas - 1) / total);
@@ -637,10 +639,7 @@ template <int D, bool kBf16>
 __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int wg) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
-    // fp16 weights are scaled by 2^6: their subnormals then start 20 binary
-    // orders below the maximum, and the largest weight is 2^14
-    constexpr float kBias = kBf16 ? 0.0f : 6.0f;
-    constexpr float kLn2 = 0.6931471805599453f;
+    constexpr float kBias = weight_bias(kBf16);
     const int warp = threadIdx.x >> 5 & 3, lane = threadIdx.x & 31;
     const int row = warp * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
@@ -886,58 +885,6 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                     if (join) mbar_arrive(c.base + L::oempty + 8);
                 }
             }
-            if (s.split) {
-                // the last CTA to write its part of the item joins them all, in order
-                const int64_t per = a.head->units, all = per * a.hk;
-                const int64_t u0 = s.g * per + a.pre[s.item], u1 = u0 + max(s.it.ntiles, 1);
-                const int ctas = a.head->ctas;
-                const int c0 = range_owner(all, ctas, u0), c1 = range_owner(all, ctas, u1 - 1);
-                const int id = 1 + wg;
-                __threadfence();
-                ok = bar_sync_and(id, 128, ok);
-                volatile int* last = reinterpret_cast<volatile int*>(c.smem + L::last) + wg;
-                if (tid == 0) {
-                    const unsigned before = ok ? atomicAdd(a.count + c0 * 2 + tile, 1u) : 0u;
-                    *last = ok && before == static_cast<unsigned>(c1 - c0);
-                }
-                bar_sync(id, 128);
-                if (*last) {
-                    __threadfence();
-                    const bool c0_first = range_start(all, ctas, c0) >= u0;
-                    auto index = [&](int cta) {
-                        return static_cast<int64_t>((cta * 2 + (cta == c0 && !c0_first ? 1 : 0)) * L::kTiles + tile) * kRows;
-                    };
-                    for (int e = tid; e < rows * (D / 4); e += 128) {
-                        const int r = e / (D / 4), col = (e - r * (D / 4)) * 4;
-                        float mm = -INFINITY;
-                        for (int p = c0; p <= c1; ++p) mm = fmaxf(mm, __ldcg(a.part_ml + index(p) + r).x);
-                        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        float ll = 0.0f;
-                        for (int p = c0; p <= c1; ++p) {
-                            const float2 ml = __ldcg(a.part_ml + index(p) + r);
-                            const float f = ml.x == mm ? 1.0f : exp2_ftz(ml.x - mm);
-                            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (index(p) + r) * D + col));
-                            ll += ml.y * f;
-                            acc.x += x.x * f;
-                            acc.y += x.y * f;
-                            acc.z += x.z * f;
-                            acc.w += x.w * f;
-                        }
-                        const bool none = ll == 0.0f;
-                        const float inv = none ? 0.0f : 1.0f / ll;
-                        const int tk = r / a.G;
-                        const int64_t tt = s.it.tok0 + tile * a.tq + tk;
-                        const int hh = s.g * a.G + r - tk * a.G;
-                        uint2 y;
-                        y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
-                        y.y = none ? 0u : pack_pair<kBf16>(acc.z * inv, acc.w * inv);
-                        *reinterpret_cast<uint2*>(a.out + tt * a.o_st + hh * a.o_sh + col) = y;
-                        if (a.lse && col == 0)
-                            a.lse[tt * a.G * a.hk + hh] = none ? -INFINITY : (mm - kBias + log2f(ll)) * kLn2;
-                    }
-                }
-                bar_sync(id, 128);   // the flag is free for the next item
-            }
         }
         if (join) ++alt;
         // the ring moves on by the segment's 2 n tiles
@@ -1019,6 +966,97 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
 }
 
+// ------------------------------------------------------------ join
+
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 16;    // for each boundary between two ranges
+constexpr int kJoinFew = 4;        // parts that one thread walks by itself
+
+// out = sum_p w_p O_p / sum_p w_p l_p, w_p = exp2(m_p - max m). Blocks (x, y)
+// take the item that is cut for the first time at the end of CTA x's range.
+// A row's D / 4 vectors are one group of threads; with few parts every group
+// walks the parts of a row of its own, with many the groups share a row and
+// its parts (the L2 latency of 76 parts in turn would be the kernel's time).
+template <int D, bool kBf16>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+    using L = Smem<D>;
+    constexpr int kVecs = D / 4, kGroups = kJoinThreads / kVecs;
+    constexpr float kBias = weight_bias(kBf16);
+    __shared__ float4 acc_s[kGroups][kVecs];
+    __shared__ float sum_s[kGroups];
+    grid_dep_wait();
+    const int c0 = blockIdx.x;
+    if (a.head->units <= 0 || c0 + 1 >= a.head->ctas) return;
+    const Start st = a.starts[c0 + 1];
+    if (st.off == 0) return;   // the cut lies between two items
+    const int64_t per = a.head->units, all = per * a.hk;
+    const int ctas = a.head->ctas;
+    const int64_t u0 = st.g * per + a.pre[st.item], u1 = st.g * per + a.pre[st.item + 1];
+    if (range_owner(all, ctas, u0) != c0) return;   // an earlier cut has the item
+    const int parts = range_owner(all, ctas, u1 - 1) - c0 + 1;
+    const bool c0_head = range_start(all, ctas, c0) >= u0;
+    const Item it = a.items[st.item];
+    const int group = threadIdx.x / kVecs, vec = threadIdx.x % kVecs;
+    const int rows0 = min(it.ntok, a.tq) * a.G, rows = it.ntok * a.G;   // of the first tile, of both
+    const bool share = parts > kJoinFew;
+    const int stride = share ? kJoinBlocks : kJoinBlocks * kGroups;
+    for (int base = share ? blockIdx.y : blockIdx.y * kGroups; base < rows; base += stride) {
+        const int r = share ? base : base + group;
+        const bool mine = r < rows;
+        const int tile = mine && r >= rows0 ? 1 : 0, row = r - tile * rows0;
+        auto at = [&](int p) {
+            const int part = (c0 + p) * 2 + (p == 0 && !c0_head ? 1 : 0);
+            return (static_cast<int64_t>(part) * L::kTiles + tile) * kRows + row;
+        };
+        float top = -INFINITY, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (mine) {
+#pragma unroll 4
+            for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(a.part_ml + at(p)).x);
+#pragma unroll 4
+            for (int p = share ? group : 0; p < parts; p += share ? kGroups : 1) {
+                const float2 ml = __ldcg(a.part_ml + at(p));
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(p) * D) + vec);
+                const float f = ml.x == top ? 1.0f : exp2_ftz(ml.x - top);
+                sum += ml.y * f;
+                acc.x += x.x * f;
+                acc.y += x.y * f;
+                acc.z += x.z * f;
+                acc.w += x.w * f;
+            }
+        }
+        if (share) {
+            acc_s[group][vec] = acc;
+            if (vec == 0) sum_s[group] = sum;
+            __syncthreads();
+            if (group == 0) {
+#pragma unroll
+                for (int k = 1; k < kGroups; ++k) {
+                    const float4 x = acc_s[k][vec];
+                    acc.x += x.x;
+                    acc.y += x.y;
+                    acc.z += x.z;
+                    acc.w += x.w;
+                    sum += sum_s[k];
+                }
+            }
+            __syncthreads();
+            if (group != 0) continue;
+        }
+        if (!mine) continue;
+        const bool none = sum == 0.0f;
+        const float inv = none ? 0.0f : 1.0f / sum;
+        const int tok = row / a.G;
+        const int64_t t = it.tok0 + tile * a.tq + tok;
+        const int h = st.g * a.G + row - tok * a.G;
+        uint2 y;
+        y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
+        y.y = none ? 0u : pack_pair<kBf16>(acc.z * inv, acc.w * inv);
+        reinterpret_cast<uint2*>(a.out + t * a.o_st + h * a.o_sh)[vec] = y;
+        if (a.lse && vec == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (top - kBias + log2f(sum)) * kLn2;
+    }
+}
+
 // ------------------------------------------------------------ host
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
@@ -1057,7 +1095,7 @@ bool make_map(CUtensorMap* m, bool bf16, const void* p, int d, int64_t n1, int64
 
 struct Layout {
     int64_t items_max;
-    size_t head, items, pre, req, starts, count, ml, o, total;
+    size_t head, items, pre, req, starts, ml, o, total;
 };
 
 Layout layout(const sp_paged_shape* s, int grid) {
@@ -1075,7 +1113,6 @@ Layout layout(const sp_paged_shape* s, int grid) {
     l.pre = take(8 * (l.items_max + 1));
     l.req = take(4 * (static_cast<size_t>(s->n_seqs) + 1));
     l.starts = take(sizeof(Start) * grid);
-    l.count = take(8 * static_cast<size_t>(grid));
     l.ml = take(8 * static_cast<size_t>(grid) * 2 * tiles * kRows);
     l.o = take(4 * static_cast<size_t>(grid) * 2 * tiles * kRows * s->head_dim);
     l.total = off;
@@ -1089,7 +1126,10 @@ cudaError_t launch_d(const AttnArgs& a, bool bf16, const CUtensorMap& mq, const 
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(Smem<D>::total));
     if (e != cudaSuccess) return e;
-    return launch_k(kern, static_cast<unsigned>(a.grid), kAttnThreads, Smem<D>::total, st, mq, mk, mv, a);
+    const cudaError_t r = launch_k(kern, static_cast<unsigned>(a.grid), kAttnThreads, Smem<D>::total, st, mq, mk, mv, a);
+    if (r != cudaSuccess || a.grid < 2) return r;
+    return launch_k(bf16 ? attn_join_kernel<D, true> : attn_join_kernel<D, false>,
+                    dim3(static_cast<unsigned>(a.grid - 1), kJoinBlocks), kJoinThreads, 0, st, a);
 }
 
 }  // namespace
@@ -1116,7 +1156,6 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.pre = ws_ptr<int64_t>(ws, l.pre);
     a.req_item = ws_ptr<int32_t>(ws, l.req);
     a.starts = ws_ptr<Start>(ws, l.starts);
-    a.count = ws_ptr<unsigned>(ws, l.count);
     a.part_o = ws_ptr<float>(ws, l.o);
     a.part_ml = ws_ptr<float2>(ws, l.ml);
     a.o_st = s->o_stride_token, a.o_sh = s->o_stride_head;
