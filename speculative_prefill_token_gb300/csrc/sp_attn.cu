@@ -346,8 +346,8 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
     constexpr int kPer = L::kSlotKeys;
-    const int nk = kKeys / a.hk_box;           // K boxes of a tile and chunk
-    const int sub = kPer / a.hv_box;           // V boxes of a slot and chunk
+    const int nk = kKeys / a.hk_box;           // K boxes of a tile
+    const int sub = kPer / a.hv_box;           // V boxes of a slot
     int slot = 0;
     uint32_t turn = 0;
     bool ok = true;
@@ -380,33 +380,28 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
         }
     };
     auto put_k = [&](const Segment& s, int row) {
-        // lane: box r of chunk ch of the slot
-        const int r = lane / L::kSlotChunks, ch = lane % L::kSlotChunks;
-        const int mine = __shfl_sync(kAll, row, r);
-        const bool there = r < nk && mine >= 0;
-        const uint32_t bytes = __popc(__ballot_sync(kAll, there)) * a.hk_box * 128u;
+        const bool there = row >= 0;
+        const uint32_t bytes = __popc(__ballot_sync(kAll, there)) * a.hk_box * (L::kSlotChunks * 128u);
         for (int p = 0; p < L::kParts; ++p) {
             if (!acquire(bytes)) return;
             if (there)
-                tma_load_3d(c.base + L::ring + slot * L::kSlot + ch * kChunk + static_cast<uint32_t>(r * a.hk_box) * 128u,
-                            mk, c.base + L::full + 8 * slot, (p * L::kSlotChunks + ch) * 64, mine, s.g);
+                tma_load_5d(c.base + L::ring + slot * L::kSlot + static_cast<uint32_t>(lane * a.hk_box) * (L::kSlotChunks * 128u),
+                            mk, c.base + L::full + 8 * slot, 0, 0, p * L::kSlotChunks, row / 8, s.g);
             advance();
         }
     };
     auto put_v = [&](const Segment& s, int tile, int row) {
         for (int p = 0; p < L::kParts; ++p) {
-            // lane: sub-box r of chunk ch; its K box holds the block's row
-            const int r = lane / L::kChunks, ch = lane % L::kChunks;
-            const int key = p * kPer + r * a.hv_box;       // of the tile
-            const int box = key / a.hk_box & 31;
-            const int base_row = __shfl_sync(kAll, row, box);
+            // the rows of a V box lie in the block of a K box of the tile
+            const int key = p * kPer + lane * a.hv_box;    // of the tile
+            const int base_row = __shfl_sync(kAll, row, key / a.hk_box & 31);
             const int at = tile * kKeys + key;
-            const bool mine = r < sub && base_row >= 0 && at < s.it.khi && at + a.hv_box > s.it.klo;
-            const uint32_t bytes = __popc(__ballot_sync(kAll, mine)) * a.hv_box * 128u;
+            const bool there = lane < sub && base_row >= 0 && at < s.it.khi && at + a.hv_box > s.it.klo;
+            const uint32_t bytes = __popc(__ballot_sync(kAll, there)) * a.hv_box * (L::kChunks * 128u);
             if (!acquire(bytes)) return;
-            if (mine)
-                tma_load_3d(c.base + L::ring + slot * L::kSlot + static_cast<uint32_t>(ch * kPer + r * a.hv_box) * 128u,
-                            mv, c.base + L::full + 8 * slot, ch * 64, base_row + key % a.hk_box, s.g);
+            if (there)
+                tma_load_5d(c.base + L::ring + slot * L::kSlot + static_cast<uint32_t>(lane * a.hv_box) * (L::kChunks * 128u),
+                            mv, c.base + L::full + 8 * slot, 0, 0, 0, (base_row + key % a.hk_box) / 8, s.g);
             advance();
         }
     };
@@ -500,12 +495,12 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
             tc_fence_after();
             const int slot = __shfl_sync(kAll, p.slot, 0);
             const uint64_t qd = smem_desc_sw128(base + L::q + t * L::kChunks * kChunk + part * L::kSlot);
-            const uint64_t kd = smem_desc_sw128(base + L::ring + slot * L::kSlot);
+            const uint64_t kd = smem_desc_sw128(base + L::ring + slot * L::kSlot, 1024 * L::kSlotChunks);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4 * L::kSlotChunks; ++k)
                     tc_mma_bf16(tmem + sb * kKeys, qd + (k / 4) * (kChunk / 16) + 2 * (k % 4),
-                                kd + (k / 4) * (kChunk / 16) + 2 * (k % 4), kIdQk, (part | k) != 0);
+                                kd + (k / 4) * 64 + 2 * (k % 4), kIdQk, (part | k) != 0);
                 if (release) tc_commit(base + L::empty + 8 * slot);
                 if (part == L::kParts - 1) tc_commit(base + L::sfull + 8 * sb);
             }
@@ -523,12 +518,12 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
             if (fresh && !wait(L::full + 8 * p.slot, p.turn)) return p;
             tc_fence_after();
             const int slot = __shfl_sync(kAll, p.slot, 0);
-            const uint64_t vd = smem_desc_sw128_mn(base + L::ring + slot * L::kSlot, kPer * 128);
+            const uint64_t vd = smem_desc_sw128_mn(base + L::ring + slot * L::kSlot, 1024, 1024 * L::kChunks);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kPer / 16; ++k)
                     tc_mma_f16_ts(tmem + 2 * kKeys + o * D, tmem + sb * kKeys + (part * (kPer / 16) + k) * 8,
-                                  vd + 128 * k, kIdPv, !first || (part | k) != 0);
+                                  vd + 128 * L::kChunks * k, kIdPv, !first || (part | k) != 0);
                 if (release) tc_commit(base + L::empty + 8 * slot);
                 if (part == L::kParts - 1) tc_commit(base + L::odone + 8 * sb);
             }
@@ -770,10 +765,10 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                     for (int part = 0; part < L::kParts && ok; ++part) {
                         ok = __all_sync(kAll, c.wait(L::full + 8 * p, ph));
                         if (!ok) break;
-                        // rows of this slot, 8 vectors a row and chunk
+                        // vectors of this slot: [8 keys][chunk][key][8]
                         uint4* v = reinterpret_cast<uint4*>(c.smem + L::ring + p * L::kSlot);
                         for (int e = tid; e < static_cast<int>(L::kSlot / 16); e += 128) {
-                            const int key = part * kPer + (e >> 3) % kPer;
+                            const int key = part * kPer + e / (64 * L::kChunks) * 8 + (e >> 3) % 8;
                             if (key < z0 || key >= z1) v[e] = make_uint4(0, 0, 0, 0);
                         }
                         if (++p == L::kSlots) {
@@ -1093,6 +1088,25 @@ bool make_map(CUtensorMap* m, bool bf16, const void* p, int d, int64_t n1, int64
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Map of a pool for boxes of `rows` rows x `chunks` 64-element chunks of one
+// head: dims (64, 8 rows, chunk, group of 8 rows, head). A box lands as
+// [8-row group][chunk][8][64], the swizzle atoms of both products' operands at
+// fixed strides whatever the box's rows, so one copy brings a whole block.
+bool make_pool_map(CUtensorMap* m, bool bf16, const void* p, int d, int64_t pool_rows, int64_t row_stride, int heads,
+                   int64_t head_stride, int rows, int chunks) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(d / 64), static_cast<cuuint64_t>(pool_rows / 8),
+                          static_cast<cuuint64_t>(heads)};
+    cuuint64_t strides[4] = {static_cast<cuuint64_t>(row_stride) * 2, 128, static_cast<cuuint64_t>(row_stride) * 16,
+                             static_cast<cuuint64_t>(heads > 1 ? head_stride : d) * 2};
+    cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(chunks), static_cast<cuuint32_t>(rows / 8), 1};
+    cuuint32_t es[5] = {1, 1, 1, 1, 1};
+    return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5, const_cast<void*>(p),
+               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 struct Layout {
     int64_t items_max;
     size_t head, items, pre, req, starts, ml, o, total;
@@ -1171,15 +1185,17 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.causal = p->causal;
     a.window = p->window;
     a.hk_box = bs < kKeys ? bs : kKeys;
-    const int per = kKeys / (d / 64);
+    const int per = kKeys / slots_per_tile(d);
     a.hv_box = bs < per ? bs : per;
     a.q_bytes = static_cast<uint32_t>(a.G * a.tq) * 128u;
     const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(d));
     a.scale2 = static_cast<float>(scale * 1.4426950408889634);
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, bf16, q, d, s->n_q_heads, s->q_stride_head, s->n_tokens, s->q_stride_token, a.G, a.tq) ||
-        !make_map(&mk, bf16, k_pool, d, s->pool_tokens, s->k_stride_token, a.hk, s->k_stride_head, a.hk_box, 1) ||
-        !make_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, a.hv_box, 1))
+        !make_pool_map(&mk, bf16, k_pool, d, s->pool_tokens, s->k_stride_token, a.hk, s->k_stride_head, a.hk_box,
+                       d / 64 / slots_per_tile(d)) ||
+        !make_pool_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, a.hv_box,
+                       d / 64))
         return cudaErrorInvalidValue;
     const cudaError_t e = launch_k(attn_plan_kernel, 1, kPlanThreads, 0, st, a, tiles_per_item(d));
     if (e != cudaSuccess) return e;

@@ -288,25 +288,25 @@ __device__ __forceinline__ void tmem_ld_wait() {
 
 // Shared-memory matrix descriptor (tcgen05 format, version 1): K-major
 // operand stored as rows of 128 bytes with the 128-byte swizzle, 8-row
-// groups 1024 bytes apart. `addr` is the shared-space byte address.
-__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr) {
+// groups `stride` (1024) bytes apart. `addr` is the shared-space byte address.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t stride = 1024) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);          // start address
     d |= static_cast<uint64_t>(1u) << 16;                        // leading byte offset (unused)
-    d |= static_cast<uint64_t>((1024u >> 4) & 0x3FFFu) << 32;    // stride byte offset
+    d |= static_cast<uint64_t>((stride >> 4) & 0x3FFFu) << 32;   // stride byte offset
     d |= static_cast<uint64_t>(1u) << 46;                        // descriptor version
     d |= static_cast<uint64_t>(2u) << 61;                        // 128-byte swizzle
     return d;
 }
 
-// The same swizzle for an MN-major operand: rows (8-row groups 1024 bytes
-// apart) run along K, each 64 elements of M or N wide; the next 64 elements
-// are `lead` bytes further.
-__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t addr, uint32_t lead) {
+// The same swizzle for an MN-major operand: rows run along K, each 64
+// elements of M or N wide, in groups of 8 rows (1024 bytes) `stride` bytes
+// apart; the next 64 elements of M or N are `lead` bytes further.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t addr, uint32_t lead, uint32_t stride) {
     uint64_t d = 0;
     d |= static_cast<uint64_t>((addr >> 4) & 0x3FFFu);
     d |= static_cast<uint64_t>((lead >> 4) & 0x3FFFu) << 16;
-    d |= static_cast<uint64_t>((1024u >> 4) & 0x3FFFu) << 32;
+    d |= static_cast<uint64_t>((stride >> 4) & 0x3FFFu) << 32;
     d |= static_cast<uint64_t>(1u) << 46;
     d |= static_cast<uint64_t>(2u) << 61;
     return d;
