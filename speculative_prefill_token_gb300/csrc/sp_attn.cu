@@ -86,16 +86,23 @@ struct alignas(16) Item {
     int32_t b, tok0, ntok, pos0, klo, khi, tile0, ntiles;
 };
 
-// Where a CTA's range starts: unit `off` of item `item` of KV head g.
+// Where a CTA's range starts (and the one before it ends): key tile `off` of
+// item `item` of KV head g.
 struct alignas(16) Start {
     int32_t item, g, off, pad;
-    int64_t begin, end;   // units of all heads
+};
+
+// A cut item: its parts lie with CTAs c0 .. c0 + parts - 1.
+struct alignas(16) Job {
+    int32_t c0, parts, item, g;
+    int32_t task0;    // tasks of the join kernel before it
+    int32_t c0_head;  // CTA c0 starts with it
+    int32_t pad[2];
 };
 
 struct PlanHead {
-    int64_t units;    // of one KV head (0: nothing to do)
-    int32_t items;    // of one KV head
-    int32_t ctas;     // CTAs with a range: at least one unit each
+    int32_t items;    // of one KV head; 0: nothing to do
+    int32_t jobs, tasks, pad;
 };
 
 struct AttnArgs {
@@ -107,13 +114,16 @@ struct AttnArgs {
     int32_t* status;
     PlanHead* head;
     Item* items;
-    int64_t* pre;       // units before each item, [items + 1]
+    int64_t* pre;       // cost before each item, [items + 1]
     int32_t* req_item;  // first item of each request, [B + 1]
-    Start* starts;      // [grid]
+    Start* starts;      // [grid + 1]
+    Job* jobs;          // [grid]
     float* part_o;      // [grid * 2][tiles][128][d]
     float2* part_ml;    // [grid * 2][tiles][128] (reference, sum)
     int64_t o_st, o_sh, pool_tokens, spin;
     int B, hk, G, tq, bs, table_stride, cap, causal, window, grid;
+    int wide_out;        // 32-byte stores of out are aligned
+    int local_plan;      // every CTA lays out the batch itself
     int hk_box, hv_box;  // rows of a K and of a V box
     uint32_t q_bytes;    // of one 64-element chunk of a query tile
     float scale2;
@@ -121,60 +131,87 @@ struct AttnArgs {
 
 // ------------------------------------------------------------ plan
 
+constexpr int kMaxCtas = 256;
+constexpr int kLocalItems = 384;   // items and requests of a plan made by every CTA
+// Cost of an item besides its key tiles, in tiles: loading the queries,
+// filling the pipeline and writing the rows. (Without it the CTAs with the
+// shortest items of a prompt finish last.)
+constexpr int kItemCost = 2;
+constexpr int kJoinFew = 4;        // parts that one group of threads walks by itself
+constexpr int kJoinThreads = 256;
+constexpr int kJoinGroups = kJoinThreads / 16;   // of 16 threads: 64 columns of a row
+
+struct PlanScratch {
+    int64_t sums[32];
+    Start starts[kMaxCtas + 1];
+    int32_t req_item[kLocalItems + 1];
+    int64_t pre[kLocalItems + 1];
+};
+
 __device__ __forceinline__ int64_t range_start(int64_t total, int ctas, int c) { return total * c / ctas; }
 
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sum, int64_t* total) {
+// The CTA whose range holds unit u of `total`.
+__device__ __forceinline__ int range_owner(int64_t total, int ctas, int64_t u) {
+    return static_cast<int>(((u + 1) * ctas - 1) / total);
+}
+
+// Exclusive sums over the block's NT threads, and their total.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t incl = v;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
     __syncthreads();
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    int64_t before = 0, all = 0;
-    for (int w = 0; w < kPlanThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        all += warp_sum[w];
+    const int64_t mine = lane < NT / 32 ? sums[lane] : 0;
+    int64_t all = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += x;
     }
-    *total = all;
-    return before + incl - v;   // exclusive
+    *total = __shfl_sync(0xffffffffu, all, 31);
+    return __shfl_sync(0xffffffffu, all - mine, warp) + incl - v;
 }
 
-// Items, their units and the CTAs' ranges (one CTA).
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles) {
-    __shared__ int64_t warp_sum[kPlanThreads / 32];
-    grid_dep_wait();
-    grid_dep_launch();
+// Lays out the batch, by all NT threads of a block: items with their costs,
+// the CTAs' ranges of equal cost, and the cut items. A cut inside an item's
+// fixed cost falls on the item's start. Returns the number of items (0 for an
+// empty or inconsistent batch). With `local` the searched arrays lie in shared
+// memory (one item and one request per thread), else in the workspace.
+template <int NT, bool kLocal>
+__device__ __forceinline__ int plan_batch(const AttnArgs& a, int tiles, int chunks, PlanScratch& sc) {
     const int tid = threadIdx.x;
     const int tpi = a.tq * tiles;   // tokens per item
-    int bad = a.q_off[0] != 0;
+    int32_t* req_item = kLocal ? sc.req_item : a.req_item;
+    int64_t* pre = kLocal ? sc.pre : a.pre;
+    int bad = tid == 0 ? a.q_off[0] != 0 : 0;
     int64_t items = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
         const int b = b0 + tid;
         int64_t n = 0;
         if (b < a.B) {
             const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_len[b];
             if (hi < lo || hi > a.cap || kv < 0 || (kv + a.bs - 1) / a.bs > a.table_stride) bad = 1;
-            else n = (hi - lo + tpi - 1) / tpi;
+            else n = (static_cast<int>(hi - lo) + tpi - 1) / tpi;
         }
         int64_t total;
-        const int64_t at = items + block_scan(n, warp_sum, &total);
-        if (b < a.B) a.req_item[b] = static_cast<int32_t>(at);
+        const int64_t at = items + block_scan<NT>(n, sc.sums, &total);
+        if (b < a.B) req_item[b] = static_cast<int32_t>(at);
         items += total;
     }
     if (__syncthreads_or(bad)) {
-        if (tid == 0) {
-            atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
-            a.head->units = 0;
-        }
-        return;
+        if (tid == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+        items = 0;
     }
     int64_t units = 0;
-    for (int64_t i0 = 0; i0 < items; i0 += kPlanThreads) {
+    for (int64_t i0 = 0; i0 < items; i0 += NT) {
         const int64_t i = i0 + tid;
-        Item it = {};
         int64_t n = 0;
         if (i < items) {
             // the last request whose first item is at or before i: requests
@@ -182,9 +219,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
             int lo = 0, hi = a.B;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (a.req_item[mid] <= i) lo = mid; else hi = mid;
+                if (req_item[mid] <= i) lo = mid; else hi = mid;
             }
-            const int first = static_cast<int>(i - a.req_item[lo]) * tpi;
+            Item it;
+            const int first = static_cast<int>(i - req_item[lo]) * tpi;
             const int q0 = a.q_off[lo], nq = a.q_off[lo + 1] - q0, kv = a.kv_len[lo];
             it.b = lo;
             it.tok0 = q0 + first;
@@ -194,40 +232,80 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
             it.klo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
             it.tile0 = it.klo / kKeys;
             it.ntiles = it.khi > it.klo ? (it.khi + kKeys - 1) / kKeys - it.tile0 : 0;
-            n = max(it.ntiles, 1);
+            n = it.ntiles + kItemCost;
             a.items[i] = it;
         }
         int64_t total;
-        const int64_t at = units + block_scan(n, warp_sum, &total);
-        if (i < items) a.pre[i] = at;
+        const int64_t at = units + block_scan<NT>(n, sc.sums, &total);
+        if (i < items) pre[i] = at;
         units += total;
     }
-    if (tid == 0) {
-        a.pre[items] = units;
-        a.head->units = units;
-        a.head->items = static_cast<int32_t>(items);
-        a.head->ctas = static_cast<int32_t>(min(static_cast<int64_t>(a.grid), units * a.hk));
-    }
+    if (tid == 0) pre[items] = units;
     __syncthreads();
     const int64_t all = units * a.hk;
     const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), all));
-    for (int c = tid; c < a.grid; c += kPlanThreads) {
-        Start s = {};
+    for (int c = tid; c <= a.grid; c += NT) {
+        Start s{0, a.hk, 0, 0};
         if (c < ctas) {
-            s.begin = range_start(all, ctas, c);
-            s.end = range_start(all, ctas, c + 1);
-            s.g = static_cast<int32_t>(s.begin / units);
-            const int64_t u = s.begin - s.g * units;
-            int64_t lo = 0, hi = items;
+            const int64_t begin = range_start(all, ctas, c);
+            s.g = static_cast<int32_t>(begin / units);
+            const int64_t u = begin - s.g * units;
+            int lo = 0, hi = static_cast<int>(items);
             while (hi - lo > 1) {
-                const int64_t mid = (lo + hi) >> 1;
-                if (a.pre[mid] <= u) lo = mid; else hi = mid;
+                const int mid = (lo + hi) >> 1;
+                if (pre[mid] <= u) lo = mid; else hi = mid;
             }
-            s.item = static_cast<int32_t>(lo);
-            s.off = static_cast<int32_t>(u - a.pre[lo]);
+            s.item = lo;
+            s.off = static_cast<int32_t>(max(u - pre[lo] - kItemCost, static_cast<int64_t>(0)));
         }
+        sc.starts[c] = s;
         a.starts[c] = s;
     }
+    __syncthreads();
+    if (blockIdx.x == 0) {
+        int64_t jobs = 0, tasks = 0;
+        for (int x0 = 1; x0 < max(ctas, 2); x0 += NT) {
+            const int x = x0 + tid;
+            Job j = {};
+            int64_t mine = 0;
+            if (x < ctas) {
+                const Start s = sc.starts[x], b = sc.starts[x - 1];
+                // the first cut inside the item
+                if (s.off > 0 && !(b.item == s.item && b.g == s.g && b.off > 0)) {
+                    const int64_t u1 = s.g * units + pre[s.item + 1];
+                    j.c0 = x - 1;
+                    j.parts = range_owner(all, ctas, u1 - 1) - j.c0 + 1;
+                    j.item = s.item;
+                    j.g = s.g;
+                    j.c0_head = b.item == s.item && b.g == s.g;
+                    mine = static_cast<int64_t>(a.items[s.item].ntok) * a.G * chunks;
+                    if (j.parts <= kJoinFew) mine = (mine + kJoinGroups - 1) / kJoinGroups;
+                }
+            }
+            int64_t nj, nt;
+            const int64_t at = jobs + block_scan<NT>(j.parts > 0, sc.sums, &nj);
+            j.task0 = static_cast<int32_t>(tasks + block_scan<NT>(mine, sc.sums, &nt));
+            if (j.parts > 0) a.jobs[at] = j;
+            jobs += nj;
+            tasks += nt;
+        }
+        if (tid == 0) {
+            PlanHead h;
+            h.items = static_cast<int32_t>(items);
+            h.jobs = static_cast<int32_t>(jobs);
+            h.tasks = static_cast<int32_t>(tasks);
+            h.pad = 0;
+            *a.head = h;
+        }
+    }
+    return static_cast<int>(items);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles, int chunks) {
+    __shared__ PlanScratch sc;
+    grid_dep_wait();
+    grid_dep_launch();
+    plan_batch<kPlanThreads, false>(a, tiles, chunks, sc);
 }
 
 // ------------------------------------------------------------ segments
@@ -243,30 +321,33 @@ struct Segment {
 // Walks a CTA's range; every role takes the same steps.
 struct Walk {
     int item, g, off, items;
-    int64_t left;
+    int end_item, end_g, end_off;
     bool head;
-    __device__ __forceinline__ explicit Walk(const AttnArgs& a) {
-        const Start s = a.starts[blockIdx.x];
-        item = s.item;
-        g = s.g;
-        off = s.off;
-        left = s.end - s.begin;
-        items = a.head->items;
+    __device__ __forceinline__ Walk(const AttnArgs& a, int n_items) {
+        const int4 s = __ldcg(reinterpret_cast<const int4*>(a.starts + blockIdx.x));
+        const int4 e = __ldcg(reinterpret_cast<const int4*>(a.starts + blockIdx.x + 1));
+        item = s.x;
+        g = s.y;
+        off = s.z;
+        end_item = e.x;
+        end_g = e.y;
+        end_off = e.z;
+        items = n_items;
         head = true;
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
-        if (left <= 0) return false;
-        s.it = a.items[item];
-        const int units = max(s.it.ntiles, 1);
-        const int take = static_cast<int>(min(static_cast<int64_t>(units - off), left));
+        const bool last = g == end_g && item == end_item;
+        if (g > end_g || (g == end_g && item > end_item) || (last && off >= end_off)) return false;
+        const int4* p = reinterpret_cast<const int4*>(a.items + item);
+        const int4 x = __ldcg(p), y = __ldcg(p + 1);
+        s.it = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         s.g = g;
         s.item = item;
         s.first = s.it.tile0 + off;
-        s.n = s.it.ntiles == 0 ? 0 : take;
-        s.split = take < units;
+        s.n = (last ? end_off : s.it.ntiles) - off;
+        s.split = s.n < s.it.ntiles;
         s.head = head;
         head = false;
-        left -= take;
         off = 0;
         if (++item == items) {
             item = 0;
@@ -342,7 +423,7 @@ struct Ctx {
 // softmax warps zero the V rows outside before they are used.
 template <int D>
 __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const CUtensorMap* mk,
-                                          const CUtensorMap* mv, int lane) {
+                                          const CUtensorMap* mv, int items, int lane) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
     constexpr int kPer = L::kSlotKeys;
@@ -406,7 +487,7 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
         }
     };
 
-    Walk w(a);
+    Walk w(a, items);
     Segment s;
     while (ok && w.next(a, s)) {
         if (s.n == 0) continue;
@@ -432,9 +513,9 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
 }
 
 template <int D>
-__device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, const CUtensorMap* mq) {
+__device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, const CUtensorMap* mq, int items) {
     using L = Smem<D>;
-    Walk w(a);
+    Walk w(a, items);
     Segment s;
     uint32_t n = 0;
     while (w.next(a, s)) {
@@ -458,7 +539,7 @@ __device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, co
 // registers; issued by one diverged lane, eight MMAs took some 1,300 cycles),
 // and one elected lane issues.
 template <int D, bool kBf16>
-__device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint32_t tmem_base) {
+__device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint32_t tmem_base, int items) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
     constexpr uint32_t kIdQk = idesc_f16_f32(kRows, kKeys, kBf16, false);
@@ -535,7 +616,7 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
         if (elect_one()) tc_commit(base + L::qempty);
     };
 
-    Walk w(a);
+    Walk w(a, items);
     Segment s;
     Place at{0, 0};
     while (ok && w.next(a, s)) {
@@ -598,6 +679,13 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     }
 }
 
+// One 32-byte sector from one thread.
+__device__ __forceinline__ void store_32b(void* p, const uint32_t* x) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
+                 "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                 : "memory");
+}
+
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
@@ -624,14 +712,9 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
     return r;
 }
 
-// The CTA whose range holds unit u of `total`.
-__device__ __forceinline__ int range_owner(int64_t total, int ctas, int64_t u) {
-    return static_cast<int>(((u + 1) * ctas - 1) / total);
-}
-
 // One warpgroup (index wg) of softmax threads over the CTA's segments.
 template <int D, bool kBf16>
-__device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int wg) {
+__device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int items, int wg) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
     constexpr float kBias = weight_bias(kBf16);
@@ -644,7 +727,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
     int ring = 0;                // slot of the segment's first K tile
     uint32_t turn = 0;           // and its turn
     bool ok = true;
-    Walk w(a);
+    Walk w(a, items);
     Segment s;
     while (w.next(a, s)) {
         const bool two = two_tiles(a, s, D);
@@ -655,9 +738,10 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
         const int tok = row / a.G;                     // token of the tile
         const bool valid = row < rows;
         const int pos = s.it.pos0 + tile * a.tq + tok;
-        int hi = a.causal ? min(s.it.khi, pos + 1) : s.it.khi;
-        if (!valid) hi = 0;
-        const int lo = a.window > 0 ? max(pos - a.window + 1, 0) : 0;
+        // (unused rows of the tile compute on: masked, they would send every
+        // tile of their warp through the masking)
+        const int hi = a.causal && valid ? min(s.it.khi, pos + 1) : s.it.khi;
+        const int lo = a.window > 0 && valid ? max(pos - a.window + 1, 0) : 0;
         // tiles of this warpgroup: all with two query tiles or d = 256 (first
         // warpgroup only), every second one otherwise
         const bool whole = two || D > 128;
@@ -785,38 +869,47 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             }
         }
         // ---- the item's end. With alternating key tiles of d <= 128 the first
-        // warpgroup joins both accumulators.
+        // warpgroup joins both accumulators; with d = 256 the second one writes
+        // the upper half of the columns.
         const bool join = D <= 128 && !two && s.n > 1;
+        const bool halves = D > 128 && s.n > 0;
         const uint32_t buf0 = two ? s.n : (s.n + 1) / 2, buf1 = two ? s.n : s.n / 2;
         float2* stat = reinterpret_cast<float2*>(c.smem + L::stat) + (alt & 1) * kRows;
-        if (join && wg == 1) {
+        if ((join && wg == 1) || (halves && wg == 0)) {
             stat[row] = make_float2(m, l);
             __syncwarp();
             if (lane == 0) mbar_arrive(c.base + L::statfull + 8 * (alt & 1));
         }
         cnt0 += buf0;
         cnt1 += buf1;
-        const bool ends = two || wg == 0;   // this warpgroup writes rows
-        if (ends) {
+        if (two || wg == 0 || D > 128) {   // this warpgroup writes rows
             const int o = two ? wg : 0;
             float f0 = 1.0f, f1 = 0.0f;
-            if (s.n > 0) {
-                const int b = D > 128 ? (s.n - 1) & 1 : o;   // buffer of the last update
-                if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8 * b, ((b ? cnt1 : cnt0) - 1) & 1));
-                if (join) {
-                    if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8, (cnt1 - 1) & 1) && c.wait(L::statfull + 8 * (alt & 1), alt >> 1 & 1));
-                    if (ok) {
-                        const float2 other = stat[row];
+            if ((join && wg == 0) || (halves && wg == 1)) {
+                if (ok) ok = __all_sync(kAll, c.wait(L::statfull + 8 * (alt & 1), alt >> 1 & 1));
+                if (ok) {
+                    const float2 other = stat[row];
+                    if (join) {
                         const float mn = fmaxf(m, other.x);
                         f0 = m == mn ? 1.0f : exp2_ftz(m - mn);
                         f1 = other.x == mn ? 1.0f : exp2_ftz(other.x - mn);
                         l = l * f0 + other.y * f1;
                         m = mn;
+                    } else {
+                        m = other.x;
+                        l = other.y;
                     }
                 }
+            }
+            if (s.n > 0) {
+                const int b = D > 128 ? (s.n - 1) & 1 : o;   // buffer of the last update
+                if (ok) ok = __all_sync(kAll, c.wait(L::odone + 8 * b, ((b ? cnt1 : cnt0) - 1) & 1));
+                if (join && ok) ok = __all_sync(kAll, c.wait(L::odone + 8, (cnt1 - 1) & 1));
                 tc_fence_after();
             }
-            const uint32_t ot = tmem + lanes + 2 * kKeys + o * D;
+            constexpr int kCols = D > 128 ? D / 2 : D;    // columns of this warpgroup
+            const int col0 = D > 128 ? wg * kCols : 0;
+            const uint32_t ot = tmem + lanes + 2 * kKeys + o * D + col0;
             auto read = [&](int q, float (&x)[32]) {
                 tmem_ld_32x32b_x32(ot + 32 * q, x);
                 if (join) {
@@ -834,10 +927,10 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             if (!s.split) {
                 if (ok && live) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    uint16_t* dst = a.out + t * a.o_st + h * a.o_sh;
+                    uint16_t* dst = a.out + t * a.o_st + h * a.o_sh + col0;
                     const bool none = s.n == 0 || l == 0.0f;
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
+                    for (int q = 0; q < kCols / 32; ++q) {
                         float x[32];
                         if (s.n > 0) read(q, x);
                         uint32_t pk[16];
@@ -845,31 +938,35 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                         for (int i = 0; i < 16; ++i)
                             pk[i] = none ? 0u : pack_pair<kBf16>(x[2 * i] * inv, x[2 * i + 1] * inv);
                         if (valid) {
+                            if (a.wide_out) {
+                                store_32b(dst + q * 32, pk);
+                                store_32b(dst + q * 32 + 16, pk + 8);
+                            } else {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                reinterpret_cast<uint4*>(dst + q * 32)[i] =
-                                    make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                                for (int i = 0; i < 4; ++i)
+                                    reinterpret_cast<uint4*>(dst + q * 32)[i] =
+                                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+                            }
                         }
                     }
-                    if (valid && a.lse)
+                    if (valid && a.lse && col0 == 0)
                         a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2;
                 }
             } else {
                 const int part = (blockIdx.x * 2 + (s.head ? 0 : 1)) * L::kTiles + tile;
                 if (ok && live) {
-                    float* dst = a.part_o + (static_cast<int64_t>(part) * kRows + row) * D;
+                    float* dst = a.part_o + (static_cast<int64_t>(part) * kRows + row) * D + col0;
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
+                    for (int q = 0; q < kCols / 32; ++q) {
                         float x[32];
                         read(q, x);
                         if (valid) {
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                reinterpret_cast<float4*>(dst + q * 32)[i] =
-                                    make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                            for (int i = 0; i < 4; ++i)
+                                store_32b(dst + q * 32 + 8 * i, reinterpret_cast<const uint32_t*>(x + 8 * i));
                         }
                     }
-                    if (valid) a.part_ml[static_cast<int64_t>(part) * kRows + row] = make_float2(m, l);
+                    if (valid && col0 == 0) a.part_ml[static_cast<int64_t>(part) * kRows + row] = make_float2(m, l);
                 }
             }
             if (s.n > 0) {
@@ -881,7 +978,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                 }
             }
         }
-        if (join) ++alt;
+        if (join || halves) ++alt;
         // the ring moves on by the segment's 2 n tiles
         ring += 2 * s.n * L::kParts % (2 * L::kSlots);
         while (ring >= L::kSlots) {
@@ -917,7 +1014,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(c.base + L::sfull + 8 * i, 1);
             mbar_init(c.base + L::pfull + 8 * i, 4);
             mbar_init(c.base + L::odone + 8 * i, 1);
-            mbar_init(c.base + L::oempty + 8 * i, 4);
+            mbar_init(c.base + L::oempty + 8 * i, D > 128 ? 8 : 4);
             mbar_init(c.base + L::statfull + 8 * i, 4);
         }
         mbar_init(c.base + L::drain, 1);
@@ -940,18 +1037,30 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     grid_dep_wait();
     const bool aligned = (c.base & 1023u) == 0;   // the swizzle pattern starts at the slots
     if (!aligned && threadIdx.x == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
-    const bool work = aligned && a.head->units > 0;
+    int items = 0;
+    if (aligned) {
+        if (a.local_plan) {
+            // the ring is scratch until the first copy into it
+            items = plan_batch<kAttnThreads, true>(a, L::kTiles, L::kChunks,
+                                                   *reinterpret_cast<PlanScratch*>(attn_smem + L::ring));
+            fence_proxy_async_smem();
+            __syncthreads();
+        } else {
+            items = a.head->items;
+        }
+    }
+    const bool work = items > 0;
     // 384 threads x 168 registers at launch = 64,512; 128 x 80 + 256 x 208 = 63,488
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (work) {
-            if (warp == kLoadWarp) load_keys<D>(c, a, &mk, &mv, lane);
-            else if (warp == kMmaWarp) issue_mma<D, kBf16>(c, a, tmem);
-            else if (warp == kQWarp && lane == 0) load_queries<D>(c, a, &mq);
+            if (warp == kLoadWarp) load_keys<D>(c, a, &mk, &mv, items, lane);
+            else if (warp == kMmaWarp) issue_mma<D, kBf16>(c, a, tmem, items);
+            else if (warp == kQWarp && lane == 0) load_queries<D>(c, a, &mq, items);
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        if (work) softmax_rows<D, kBf16>(c, a, tmem, warp >> 2);
+        if (work) softmax_rows<D, kBf16>(c, a, tmem, items, warp >> 2);
     }
     tc_fence_before();
     __syncthreads();
@@ -963,70 +1072,68 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 // ------------------------------------------------------------ join
 
-constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 16;    // for each boundary between two ranges
-constexpr int kJoinFew = 4;        // parts that one thread walks by itself
-
-// out = sum_p w_p O_p / sum_p w_p l_p, w_p = exp2(m_p - max m). Blocks (x, y)
-// take the item that is cut for the first time at the end of CTA x's range.
-// A row's D / 4 vectors are one group of threads; with few parts every group
-// walks the parts of a row of its own, with many the groups share a row and
-// its parts (the L2 latency of 76 parts in turn would be the kernel's time).
+// out = sum_p w_p O_p / sum_p w_p l_p, w_p = exp2(m_p - max m), for the rows of
+// the cut items. A task is 64 columns of a row with many parts, which the 16
+// groups of a block share (the L2 latency of 76 parts in turn would be the
+// kernel's time), or of 16 rows with few, each walked by a group.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
     using L = Smem<D>;
-    constexpr int kVecs = D / 4, kGroups = kJoinThreads / kVecs;
     constexpr float kBias = weight_bias(kBf16);
-    __shared__ float4 acc_s[kGroups][kVecs];
-    __shared__ float sum_s[kGroups];
+    __shared__ int task0[kMaxCtas];
+    __shared__ float2 ml_s[kMaxCtas];
+    __shared__ float4 acc_s[kJoinGroups][16];
+    __shared__ float sum_s[kJoinGroups];
     grid_dep_wait();
-    const int c0 = blockIdx.x;
-    if (a.head->units <= 0 || c0 + 1 >= a.head->ctas) return;
-    const Start st = a.starts[c0 + 1];
-    if (st.off == 0) return;   // the cut lies between two items
-    const int64_t per = a.head->units, all = per * a.hk;
-    const int ctas = a.head->ctas;
-    const int64_t u0 = st.g * per + a.pre[st.item], u1 = st.g * per + a.pre[st.item + 1];
-    if (range_owner(all, ctas, u0) != c0) return;   // an earlier cut has the item
-    const int parts = range_owner(all, ctas, u1 - 1) - c0 + 1;
-    const bool c0_head = range_start(all, ctas, c0) >= u0;
-    const Item it = a.items[st.item];
-    const int group = threadIdx.x / kVecs, vec = threadIdx.x % kVecs;
-    const int rows0 = min(it.ntok, a.tq) * a.G, rows = it.ntok * a.G;   // of the first tile, of both
-    const bool share = parts > kJoinFew;
-    const int stride = share ? kJoinBlocks : kJoinBlocks * kGroups;
-    for (int base = share ? blockIdx.y : blockIdx.y * kGroups; base < rows; base += stride) {
-        const int r = share ? base : base + group;
+    const PlanHead head = *a.head;
+    if (static_cast<int>(blockIdx.x) >= head.tasks) return;
+    for (int i = threadIdx.x; i < head.jobs; i += kJoinThreads) task0[i] = a.jobs[i].task0;
+    __syncthreads();
+    const int group = threadIdx.x / 16, vec = threadIdx.x % 16, lane = threadIdx.x & 31;
+    for (int task = blockIdx.x; task < head.tasks; task += gridDim.x) {
+        int lo = 0, hi = head.jobs;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (task0[mid] <= task) lo = mid; else hi = mid;
+        }
+        const Job job = a.jobs[lo];
+        const Item it = a.items[job.item];
+        const int parts = job.parts;
+        const bool share = parts > kJoinFew;
+        const int rows0 = min(it.ntok, a.tq) * a.G, rows = it.ntok * a.G;   // of the first tile, of both
+        const int unit = share ? task - job.task0 : (task - job.task0) * kJoinGroups + group;
+        const int r = unit / L::kChunks, col = unit % L::kChunks * 64 + vec * 4;
         const bool mine = r < rows;
         const int tile = mine && r >= rows0 ? 1 : 0, row = r - tile * rows0;
         auto at = [&](int p) {
-            const int part = (c0 + p) * 2 + (p == 0 && !c0_head ? 1 : 0);
+            const int part = (job.c0 + p) * 2 + (p == 0 && !job.c0_head ? 1 : 0);
             return (static_cast<int64_t>(part) * L::kTiles + tile) * kRows + row;
         };
         float top = -INFINITY, sum = 0.0f;
         float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (mine) {
-#pragma unroll 4
-            for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(a.part_ml + at(p)).x);
-#pragma unroll 4
-            for (int p = share ? group : 0; p < parts; p += share ? kGroups : 1) {
-                const float2 ml = __ldcg(a.part_ml + at(p));
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + at(p) * D) + vec);
-                const float f = ml.x == top ? 1.0f : exp2_ftz(ml.x - top);
-                sum += ml.y * f;
-                acc.x += x.x * f;
-                acc.y += x.y * f;
-                acc.z += x.z * f;
-                acc.w += x.w * f;
-            }
-        }
+        auto add = [&](float2 ml, float4 x) {
+            const float f = ml.x == top ? 1.0f : exp2_ftz(ml.x - top);
+            sum += ml.y * f;
+            acc.x += x.x * f;
+            acc.y += x.y * f;
+            acc.z += x.z * f;
+            acc.w += x.w * f;
+        };
+        auto load = [&](int p) { return __ldcg(reinterpret_cast<const float4*>(a.part_o + at(p) * D + col)); };
         if (share) {
+            for (int p = threadIdx.x; p < parts; p += kJoinThreads) ml_s[p] = __ldcg(a.part_ml + at(p));
+            __syncthreads();
+            for (int p = lane; p < parts; p += 32) top = fmaxf(top, ml_s[p].x);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll 4
+            for (int p = group; p < parts; p += kJoinGroups) add(ml_s[p], load(p));
             acc_s[group][vec] = acc;
             if (vec == 0) sum_s[group] = sum;
             __syncthreads();
             if (group == 0) {
 #pragma unroll
-                for (int k = 1; k < kGroups; ++k) {
+                for (int k = 1; k < kJoinGroups; ++k) {
                     const float4 x = acc_s[k][vec];
                     acc.x += x.x;
                     acc.y += x.y;
@@ -1035,20 +1142,35 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
                     sum += sum_s[k];
                 }
             }
-            __syncthreads();
-            if (group != 0) continue;
+        } else if (mine) {
+            float2 ml[kJoinFew];
+            float4 x[kJoinFew];
+#pragma unroll
+            for (int p = 0; p < kJoinFew; ++p)
+                if (p < parts) {
+                    ml[p] = __ldcg(a.part_ml + at(p));
+                    x[p] = load(p);
+                }
+#pragma unroll
+            for (int p = 0; p < kJoinFew; ++p)
+                if (p < parts) top = fmaxf(top, ml[p].x);
+#pragma unroll
+            for (int p = 0; p < kJoinFew; ++p)
+                if (p < parts) add(ml[p], x[p]);
         }
-        if (!mine) continue;
-        const bool none = sum == 0.0f;
-        const float inv = none ? 0.0f : 1.0f / sum;
-        const int tok = row / a.G;
-        const int64_t t = it.tok0 + tile * a.tq + tok;
-        const int h = st.g * a.G + row - tok * a.G;
-        uint2 y;
-        y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
-        y.y = none ? 0u : pack_pair<kBf16>(acc.z * inv, acc.w * inv);
-        reinterpret_cast<uint2*>(a.out + t * a.o_st + h * a.o_sh)[vec] = y;
-        if (a.lse && vec == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (top - kBias + log2f(sum)) * kLn2;
+        if (mine && (!share || group == 0)) {
+            const bool none = sum == 0.0f;
+            const float inv = none ? 0.0f : 1.0f / sum;
+            const int tok = row / a.G;
+            const int64_t t = it.tok0 + tile * a.tq + tok;
+            const int h = job.g * a.G + row - tok * a.G;
+            uint2 y;
+            y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
+            y.y = none ? 0u : pack_pair<kBf16>(acc.z * inv, acc.w * inv);
+            *reinterpret_cast<uint2*>(a.out + t * a.o_st + h * a.o_sh + col) = y;
+            if (a.lse && col == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (top - kBias + log2f(sum)) * kLn2;
+        }
+        if (share) __syncthreads();   // (the shared arrays are free for the next task)
     }
 }
 
@@ -1109,7 +1231,7 @@ bool make_pool_map(CUtensorMap* m, bool bf16, const void* p, int d, int64_t pool
 
 struct Layout {
     int64_t items_max;
-    size_t head, items, pre, req, starts, ml, o, total;
+    size_t head, items, pre, req, starts, jobs, ml, o, total;
 };
 
 Layout layout(const sp_paged_shape* s, int grid) {
@@ -1126,7 +1248,8 @@ Layout layout(const sp_paged_shape* s, int grid) {
     l.items = take(sizeof(Item) * l.items_max);
     l.pre = take(8 * (l.items_max + 1));
     l.req = take(4 * (static_cast<size_t>(s->n_seqs) + 1));
-    l.starts = take(sizeof(Start) * grid);
+    l.starts = take(sizeof(Start) * (static_cast<size_t>(grid) + 1));
+    l.jobs = take(sizeof(Job) * grid);
     l.ml = take(8 * static_cast<size_t>(grid) * 2 * tiles * kRows);
     l.o = take(4 * static_cast<size_t>(grid) * 2 * tiles * kRows * s->head_dim);
     l.total = off;
@@ -1141,14 +1264,20 @@ cudaError_t launch_d(const AttnArgs& a, bool bf16, const CUtensorMap& mq, const 
                                                static_cast<int>(Smem<D>::total));
     if (e != cudaSuccess) return e;
     const cudaError_t r = launch_k(kern, static_cast<unsigned>(a.grid), kAttnThreads, Smem<D>::total, st, mq, mk, mv, a);
-    if (r != cudaSuccess || a.grid < 2) return r;
+    if (r != cudaSuccess) return r;
     return launch_k(bf16 ? attn_join_kernel<D, true> : attn_join_kernel<D, false>,
-                    dim3(static_cast<unsigned>(a.grid - 1), kJoinBlocks), kJoinThreads, 0, st, a);
+                    static_cast<unsigned>(8 * a.grid), kJoinThreads, 0, st, a);
 }
 
 }  // namespace
 
-size_t attn_workspace(const sp_paged_shape* s) { return layout(s, device_sms()).total; }
+// One CTA per SM (its shared memory fills one).
+int attn_grid() {
+    const int sms = device_sms();
+    return sms < kMaxCtas ? sms : kMaxCtas;
+}
+
+size_t attn_workspace(const sp_paged_shape* s) { return layout(s, attn_grid()).total; }
 
 cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params* p, const int32_t* q_off,
                                    const int32_t* kv_len, const int32_t* table, const uint16_t* q,
@@ -1157,7 +1286,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     const int d = s->head_dim, bs = s->block_size;
     const bool bf16 = s->dtype == SP_DTYPE_BF16;
     AttnArgs a;
-    a.grid = device_sms();
+    a.grid = attn_grid();
     const Layout l = layout(s, a.grid);
     a.q_off = q_off;
     a.kv_len = kv_len;
@@ -1170,6 +1299,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.pre = ws_ptr<int64_t>(ws, l.pre);
     a.req_item = ws_ptr<int32_t>(ws, l.req);
     a.starts = ws_ptr<Start>(ws, l.starts);
+    a.jobs = ws_ptr<Job>(ws, l.jobs);
     a.part_o = ws_ptr<float>(ws, l.o);
     a.part_ml = ws_ptr<float2>(ws, l.ml);
     a.o_st = s->o_stride_token, a.o_sh = s->o_stride_head;
@@ -1197,8 +1327,13 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
         !make_pool_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, a.hv_box,
                        d / 64))
         return cudaErrorInvalidValue;
-    const cudaError_t e = launch_k(attn_plan_kernel, 1, kPlanThreads, 0, st, a, tiles_per_item(d));
-    if (e != cudaSuccess) return e;
+    a.wide_out = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && (s->n_tokens == 1 || a.o_st % 16 == 0) &&
+                 (s->n_q_heads == 1 || a.o_sh % 16 == 0);
+    a.local_plan = l.items_max <= kLocalItems && a.B <= kLocalItems;
+    if (!a.local_plan) {
+        const cudaError_t e = launch_k(attn_plan_kernel, 1, kPlanThreads, 0, st, a, tiles_per_item(d), d / 64);
+        if (e != cudaSuccess) return e;
+    }
     return d == 64    ? launch_d<64>(a, bf16, mq, mk, mv, st)
            : d == 128 ? launch_d<128>(a, bf16, mq, mk, mv, st)
                       : launch_d<256>(a, bf16, mq, mk, mv, st);
