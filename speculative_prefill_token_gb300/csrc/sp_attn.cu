@@ -32,6 +32,7 @@
 //   warp 8     K and V boxes by TMA (lane j issues box j of a slot)
 //   warp 9     tcgen05.mma issuer and TMEM owner
 //   warp 10    query tiles by TMA
+//   warp 11    of CTA 0: the list of cut items for the join
 // Two streams keep the tensor cores busy while the other stream's softmax
 // runs: with two query tiles, one tile each; with one (decode steps, short
 // chunks), even and odd key tiles, with an accumulator each for d <= 128
@@ -59,9 +60,9 @@ namespace {
 constexpr int kKeys = 128;                 // keys of a tile (a unit of work)
 constexpr int kRows = 128;                 // rows of a query tile
 constexpr uint32_t kChunk = 16384;         // bytes of 128 rows x 64 elements
-constexpr int kWarps = 12;                 // (the last one idle: registers move by warpgroup)
+constexpr int kWarps = 12;
 constexpr int kAttnThreads = 32 * kWarps;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kQWarp = 10, kListWarp = 11;
 constexpr int kPlanThreads = 1024;
 constexpr int64_t kDrainSpin = int64_t(1) << 22;
 constexpr float kSlack = 8.0f;             // log2 units the reference may lag behind the maximum
@@ -94,15 +95,16 @@ struct alignas(16) Start {
 
 // A cut item: its parts lie with CTAs c0 .. c0 + parts - 1.
 struct alignas(16) Job {
-    int32_t c0, parts, item, g;
-    int32_t task0;    // tasks of the join kernel before it
-    int32_t c0_head;  // CTA c0 starts with it
-    int32_t pad[2];
+    int32_t c0, parts, g, c0_head;      // c0_head: CTA c0 starts with the item
+    int32_t tok0, ntok;
+    int32_t task0;                      // tasks of the join kernel before it
+    int32_t pad;
 };
 
 struct PlanHead {
     int32_t items;    // of one KV head; 0: nothing to do
     int32_t jobs, tasks, pad;
+    int64_t units;    // cost of one KV head
 };
 
 struct AttnArgs {
@@ -141,14 +143,8 @@ constexpr int kJoinFew = 4;        // parts that one group of threads walks by i
 constexpr int kJoinThreads = 256;
 constexpr int kJoinGroups = kJoinThreads / 16;   // of 16 threads: 64 columns of a row
 
-struct PlanScratch {
-    int64_t sums[32];
-    Start starts[kMaxCtas + 1];
-    int32_t req_item[kLocalItems + 1];
-    int64_t pre[kLocalItems + 1];
-};
-
-__device__ __forceinline__ int64_t range_start(int64_t total, int ctas, int c) { return total * c / ctas; }
+template <typename T>
+__device__ __forceinline__ T range_start(T total, int ctas, int c) { return total * c / ctas; }
 
 // The CTA whose range holds unit u of `total`.
 __device__ __forceinline__ int range_owner(int64_t total, int ctas, int64_t u) {
@@ -156,53 +152,96 @@ __device__ __forceinline__ int range_owner(int64_t total, int ctas, int64_t u) {
 }
 
 // Exclusive sums over the block's NT threads, and their total.
-template <int NT>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t* total) {
+template <int NT, typename T>
+__device__ __forceinline__ T block_scan(T v, T* sums, T* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t incl = v;
+    T incl = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        const T x = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += x;
     }
     __syncthreads();
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    const int64_t mine = lane < NT / 32 ? sums[lane] : 0;
-    int64_t all = mine;
+    const T mine = lane < NT / 32 ? sums[lane] : 0;
+    T all = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, all, o);
+        const T x = __shfl_up_sync(0xffffffffu, all, o);
         if (lane >= o) all += x;
     }
     *total = __shfl_sync(0xffffffffu, all, 31);
     return __shfl_sync(0xffffffffu, all - mine, warp) + incl - v;
 }
 
-// Lays out the batch, by all NT threads of a block: items with their costs,
-// the CTAs' ranges of equal cost, and the cut items. A cut inside an item's
-// fixed cost falls on the item's start. Returns the number of items (0 for an
-// empty or inconsistent batch). With `local` the searched arrays lie in shared
-// memory (one item and one request per thread), else in the workspace.
-template <int NT, bool kLocal>
-__device__ __forceinline__ int plan_batch(const AttnArgs& a, int tiles, int chunks, PlanScratch& sc) {
+// The item that begins at token `first` of a request's nq new ones.
+__device__ __forceinline__ Item make_item(const AttnArgs& a, int b, int q0, int nq, int kv, int first, int tpi) {
+    Item it;
+    it.b = b;
+    it.tok0 = q0 + first;
+    it.ntok = min(nq - first, tpi);
+    it.pos0 = kv - nq + first;
+    it.khi = a.causal ? max(0, min(kv, it.pos0 + it.ntok)) : kv;
+    it.klo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
+    it.tile0 = it.klo / kKeys;
+    it.ntiles = it.khi > it.klo ? (it.khi + kKeys - 1) / kKeys - it.tile0 : 0;
+    return it;
+}
+
+// Last index i in [0, n) with v[i] <= x (v[0] <= x).
+template <typename T, typename U>
+__device__ __forceinline__ int last_at_most(const T* v, int n, U x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Start of CTA c's range: ranges of equal cost; a cut inside an item's fixed
+// cost falls on the item's start.
+template <typename T>
+__device__ __forceinline__ Start make_start(const AttnArgs& a, const T* pre, int items, T units, int c) {
+    const T all = units * a.hk;
+    const int ctas = static_cast<int>(min(static_cast<T>(a.grid), all));
+    Start s{0, a.hk, 0, 0};   // the end of everything
+    if (c < ctas) {
+        const T begin = range_start(all, ctas, c);
+        s.g = static_cast<int32_t>(begin / units);
+        const T u = begin - s.g * units;
+        s.item = last_at_most(pre, items, u);
+        s.off = static_cast<int32_t>(max(u - pre[s.item] - kItemCost, static_cast<T>(0)));
+    }
+    return s;
+}
+
+__device__ __forceinline__ bool bad_request(const AttnArgs& a, int64_t lo, int64_t hi, int64_t kv) {
+    return hi < lo || hi > a.cap || kv < 0 || (kv + a.bs - 1) / a.bs > a.table_stride;
+}
+
+// Lays out a batch of any size, by one block of its own: items with their
+// costs, and the CTAs' ranges.
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles) {
+    __shared__ int64_t sums[32];
+    grid_dep_wait();
+    grid_dep_launch();
     const int tid = threadIdx.x;
     const int tpi = a.tq * tiles;   // tokens per item
-    int32_t* req_item = kLocal ? sc.req_item : a.req_item;
-    int64_t* pre = kLocal ? sc.pre : a.pre;
     int bad = tid == 0 ? a.q_off[0] != 0 : 0;
     int64_t items = 0;
-    for (int b0 = 0; b0 < a.B; b0 += NT) {
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int64_t n = 0;
         if (b < a.B) {
-            const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_len[b];
-            if (hi < lo || hi > a.cap || kv < 0 || (kv + a.bs - 1) / a.bs > a.table_stride) bad = 1;
-            else n = (static_cast<int>(hi - lo) + tpi - 1) / tpi;
+            const int64_t lo = a.q_off[b], hi = a.q_off[b + 1];
+            if (bad_request(a, lo, hi, a.kv_len[b])) bad = 1;
+            else n = (hi - lo + tpi - 1) / tpi;
         }
         int64_t total;
-        const int64_t at = items + block_scan<NT>(n, sc.sums, &total);
-        if (b < a.B) req_item[b] = static_cast<int32_t>(at);
+        const int64_t at = items + block_scan<kPlanThreads>(n, sums, &total);
+        if (b < a.B) a.req_item[b] = static_cast<int32_t>(at);
         items += total;
     }
     if (__syncthreads_or(bad)) {
@@ -210,102 +249,143 @@ __device__ __forceinline__ int plan_batch(const AttnArgs& a, int tiles, int chun
         items = 0;
     }
     int64_t units = 0;
-    for (int64_t i0 = 0; i0 < items; i0 += NT) {
+    for (int64_t i0 = 0; i0 < items; i0 += kPlanThreads) {
         const int64_t i = i0 + tid;
         int64_t n = 0;
         if (i < items) {
             // the last request whose first item is at or before i: requests
             // without new tokens share the next one's first item
-            int lo = 0, hi = a.B;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (req_item[mid] <= i) lo = mid; else hi = mid;
-            }
-            Item it;
-            const int first = static_cast<int>(i - req_item[lo]) * tpi;
-            const int q0 = a.q_off[lo], nq = a.q_off[lo + 1] - q0, kv = a.kv_len[lo];
-            it.b = lo;
-            it.tok0 = q0 + first;
-            it.ntok = min(nq - first, tpi);
-            it.pos0 = kv - nq + first;
-            it.khi = a.causal ? max(0, min(kv, it.pos0 + it.ntok)) : kv;
-            it.klo = a.window > 0 ? max(0, it.pos0 - a.window + 1) : 0;
-            it.tile0 = it.klo / kKeys;
-            it.ntiles = it.khi > it.klo ? (it.khi + kKeys - 1) / kKeys - it.tile0 : 0;
+            const int b = last_at_most(a.req_item, a.B, i);
+            const int q0 = a.q_off[b];
+            const Item it = make_item(a, b, q0, a.q_off[b + 1] - q0, a.kv_len[b],
+                                      static_cast<int>(i - a.req_item[b]) * tpi, tpi);
             n = it.ntiles + kItemCost;
             a.items[i] = it;
         }
         int64_t total;
-        const int64_t at = units + block_scan<NT>(n, sc.sums, &total);
-        if (i < items) pre[i] = at;
+        const int64_t at = units + block_scan<kPlanThreads>(n, sums, &total);
+        if (i < items) a.pre[i] = at;
         units += total;
     }
-    if (tid == 0) pre[items] = units;
-    __syncthreads();
-    const int64_t all = units * a.hk;
-    const int ctas = static_cast<int>(min(static_cast<int64_t>(a.grid), all));
-    for (int c = tid; c <= a.grid; c += NT) {
-        Start s{0, a.hk, 0, 0};
-        if (c < ctas) {
-            const int64_t begin = range_start(all, ctas, c);
-            s.g = static_cast<int32_t>(begin / units);
-            const int64_t u = begin - s.g * units;
-            int lo = 0, hi = static_cast<int>(items);
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (pre[mid] <= u) lo = mid; else hi = mid;
-            }
-            s.item = lo;
-            s.off = static_cast<int32_t>(max(u - pre[lo] - kItemCost, static_cast<int64_t>(0)));
-        }
-        sc.starts[c] = s;
-        a.starts[c] = s;
+    if (tid == 0) {
+        a.pre[items] = units;
+        PlanHead h = {};
+        h.items = static_cast<int32_t>(items);
+        h.units = units;
+        *a.head = h;
     }
     __syncthreads();
-    if (blockIdx.x == 0) {
-        int64_t jobs = 0, tasks = 0;
-        for (int x0 = 1; x0 < max(ctas, 2); x0 += NT) {
-            const int x = x0 + tid;
-            Job j = {};
-            int64_t mine = 0;
-            if (x < ctas) {
-                const Start s = sc.starts[x], b = sc.starts[x - 1];
-                // the first cut inside the item
-                if (s.off > 0 && !(b.item == s.item && b.g == s.g && b.off > 0)) {
-                    const int64_t u1 = s.g * units + pre[s.item + 1];
-                    j.c0 = x - 1;
-                    j.parts = range_owner(all, ctas, u1 - 1) - j.c0 + 1;
-                    j.item = s.item;
-                    j.g = s.g;
-                    j.c0_head = b.item == s.item && b.g == s.g;
-                    mine = static_cast<int64_t>(a.items[s.item].ntok) * a.G * chunks;
-                    if (j.parts <= kJoinFew) mine = (mine + kJoinGroups - 1) / kJoinGroups;
-                }
-            }
-            int64_t nj, nt;
-            const int64_t at = jobs + block_scan<NT>(j.parts > 0, sc.sums, &nj);
-            j.task0 = static_cast<int32_t>(tasks + block_scan<NT>(mine, sc.sums, &nt));
-            if (j.parts > 0) a.jobs[at] = j;
-            jobs += nj;
-            tasks += nt;
-        }
-        if (tid == 0) {
-            PlanHead h;
-            h.items = static_cast<int32_t>(items);
-            h.jobs = static_cast<int32_t>(jobs);
-            h.tasks = static_cast<int32_t>(tasks);
-            h.pad = 0;
-            *a.head = h;
-        }
-    }
-    return static_cast<int>(items);
+    for (int c = tid; c <= a.grid; c += kPlanThreads)
+        a.starts[c] = make_start(a, a.pre, static_cast<int>(items), units, c);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles, int chunks) {
-    __shared__ PlanScratch sc;
-    grid_dep_wait();
-    grid_dep_launch();
-    plan_batch<kPlanThreads, false>(a, tiles, chunks, sc);
+// The same of a small batch (at most kLocalItems items and requests, costs of
+// 32 bits), by every CTA of the attention kernel for itself: no launch before
+// it, and its own range and first item are at hand.
+struct LocalPlan {
+    int32_t sums[32];
+    int32_t q0[kLocalItems], nq[kLocalItems], kv[kLocalItems], req_item[kLocalItems], pre[kLocalItems + 1];
+};
+
+// What a CTA starts from.
+struct alignas(16) Range {
+    Start begin, end;
+};
+
+__device__ __forceinline__ int local_plan(const AttnArgs& a, int tiles, LocalPlan& p, Range* range) {
+    const int t = threadIdx.x;
+    const int tpi = a.tq * tiles;
+    int bad = 0, n = 0;
+    if (t < a.B) {
+        const int lo = a.q_off[t], hi = a.q_off[t + 1], kv = a.kv_len[t];
+        bad = bad_request(a, lo, hi, kv) || (t == 0 && lo != 0);
+        if (!bad) n = (hi - lo + tpi - 1) / tpi;
+        p.q0[t] = lo;
+        p.nq[t] = hi - lo;
+        p.kv[t] = kv;
+    }
+    if (__syncthreads_or(bad)) {
+        if (t == 0) {
+            atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+            if (blockIdx.x == 0) a.head->items = 0;
+        }
+        return 0;
+    }
+    int items, units;
+    const int at = block_scan<kAttnThreads>(n, p.sums, &items);
+    if (t < a.B) p.req_item[t] = at;
+    __syncthreads();
+    n = 0;
+    if (t < items) {
+        const int b = last_at_most(p.req_item, a.B, t);
+        const Item it = make_item(a, b, p.q0[b], p.nq[b], p.kv[b], (t - p.req_item[b]) * tpi, tpi);
+        n = it.ntiles + kItemCost;
+        a.items[t] = it;   // (every CTA writes the same; each reads what it wrote)
+    }
+    const int before = block_scan<kAttnThreads>(n, p.sums, &units);
+    if (t < items) p.pre[t] = before;
+    if (t == 0) p.pre[items] = units;
+    __syncthreads();
+    if (items > 0 && t < 2) {
+        const Start s = make_start(a, p.pre, items, units, static_cast<int>(blockIdx.x) + t);
+        if (t == 0) range->begin = s;
+        else range->end = s;
+    }
+    if (blockIdx.x == 0) {   // for the list of cut items
+        for (int c = t; c <= a.grid && items > 0; c += kAttnThreads) a.starts[c] = make_start(a, p.pre, items, units, c);
+        for (int i = t; i <= items; i += kAttnThreads) a.pre[i] = p.pre[i];
+        if (t == 0) {
+            a.head->items = items;
+            a.head->units = units;
+        }
+    }
+    return items;
+}
+
+// The cut items, listed for the join kernel by one warp of CTA 0 while the
+// others work.
+__device__ __forceinline__ void list_cuts(const AttnArgs& a, int chunks, int lane) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int items = __ldcg(&a.head->items);
+    const int64_t units = __ldcg(&a.head->units), all = units * a.hk;
+    const int ctas = items > 0 ? static_cast<int>(min(static_cast<int64_t>(a.grid), all)) : 0;
+    int jobs = 0, tasks = 0;
+    for (int x0 = 1; x0 < ctas; x0 += 32) {
+        const int x = x0 + lane;
+        Job j = {};
+        int mine = 0;
+        if (x < ctas) {
+            const int4 s = __ldcg(reinterpret_cast<const int4*>(a.starts + x));
+            const int4 b = __ldcg(reinterpret_cast<const int4*>(a.starts + x - 1));
+            const bool same = b.x == s.x && b.y == s.y;   // (item, g, off)
+            if (s.z > 0 && !(same && b.z > 0)) {          // the first cut inside the item
+                const int64_t last = s.y * units + __ldcg(a.pre + s.x + 1) - 1;
+                j.c0 = x - 1;
+                j.parts = range_owner(all, ctas, last) - j.c0 + 1;
+                j.g = s.y;
+                j.c0_head = same;
+                j.tok0 = __ldcg(&a.items[s.x].tok0);
+                j.ntok = __ldcg(&a.items[s.x].ntok);
+                mine = j.ntok * a.G * chunks;
+                if (j.parts <= kJoinFew) mine = (mine + kJoinGroups - 1) / kJoinGroups;
+            }
+        }
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const unsigned who = __ballot_sync(kAll, mine > 0);
+        j.task0 = tasks + incl - mine;
+        if (mine > 0) a.jobs[jobs + __popc(who & ((1u << lane) - 1))] = j;
+        jobs += __popc(who);
+        tasks += __shfl_sync(kAll, incl, 31);
+    }
+    if (lane == 0) {
+        a.head->jobs = jobs;
+        a.head->tasks = tasks;
+    }
 }
 
 // ------------------------------------------------------------ segments
@@ -314,7 +394,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
 // that sees no key), and whether other CTAs hold the rest.
 struct Segment {
     Item it;
-    int g, item, first, n;
+    int g, first, n;
     bool split, head;   // head: the CTA's first segment
 };
 
@@ -323,28 +403,24 @@ struct Walk {
     int item, g, off, items;
     int end_item, end_g, end_off;
     bool head;
-    __device__ __forceinline__ Walk(const AttnArgs& a, int n_items) {
-        const int4 s = __ldcg(reinterpret_cast<const int4*>(a.starts + blockIdx.x));
-        const int4 e = __ldcg(reinterpret_cast<const int4*>(a.starts + blockIdx.x + 1));
-        item = s.x;
-        g = s.y;
-        off = s.z;
-        end_item = e.x;
-        end_g = e.y;
-        end_off = e.z;
+    __device__ __forceinline__ Walk(const Range* r, int n_items) {
+        item = r->begin.item;
+        g = r->begin.g;
+        off = r->begin.off;
+        end_item = r->end.item;
+        end_g = r->end.g;
+        end_off = r->end.off;
         items = n_items;
         head = true;
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, Segment& s) {
-        const bool last = g == end_g && item == end_item;
-        if (g > end_g || (g == end_g && item > end_item) || (last && off >= end_off)) return false;
+        if (g > end_g || (g == end_g && (item > end_item || (item == end_item && off >= end_off)))) return false;
         const int4* p = reinterpret_cast<const int4*>(a.items + item);
         const int4 x = __ldcg(p), y = __ldcg(p + 1);
         s.it = Item{x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
         s.g = g;
-        s.item = item;
         s.first = s.it.tile0 + off;
-        s.n = (last ? end_off : s.it.ntiles) - off;
+        s.n = (g == end_g && item == end_item ? end_off : s.it.ntiles) - off;
         s.split = s.n < s.it.ntiles;
         s.head = head;
         head = false;
@@ -383,7 +459,8 @@ struct Smem {
     static constexpr uint32_t q = 0;
     static constexpr uint32_t ring = kTiles * kChunks * kChunk;
     static constexpr uint32_t stat = ring + kSlots * kSlot;   // [2][128] float2
-    static constexpr uint32_t bars = stat + 2 * kRows * 8;
+    static constexpr uint32_t range = stat + 2 * kRows * 8;
+    static constexpr uint32_t bars = range + sizeof(Range);
     static constexpr uint32_t full = bars;
     static constexpr uint32_t empty = full + 8 * kSlots;
     static constexpr uint32_t qfull = empty + 8 * kSlots;
@@ -408,6 +485,7 @@ struct Ctx {
     volatile int* abort_flag;
     int32_t* status;
     int64_t spin;
+    const Range* range;
     __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
         if (mbar_wait_bounded(base + bar, parity & 1, spin, abort_flag)) return true;
         *abort_flag = 1;
@@ -461,11 +539,10 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
         }
     };
     auto put_k = [&](const Segment& s, int row) {
-        const bool there = row >= 0;
-        const uint32_t bytes = __popc(__ballot_sync(kAll, there)) * a.hk_box * (L::kSlotChunks * 128u);
+        const uint32_t bytes = __popc(__ballot_sync(kAll, row >= 0)) * a.hk_box * (L::kSlotChunks * 128u);
         for (int p = 0; p < L::kParts; ++p) {
             if (!acquire(bytes)) return;
-            if (there)
+            if (row >= 0)
                 tma_load_5d(c.base + L::ring + slot * L::kSlot + static_cast<uint32_t>(lane * a.hk_box) * (L::kSlotChunks * 128u),
                             mk, c.base + L::full + 8 * slot, 0, 0, p * L::kSlotChunks, row / 8, s.g);
             advance();
@@ -487,7 +564,7 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
         }
     };
 
-    Walk w(a, items);
+    Walk w(c.range, items);
     Segment s;
     while (ok && w.next(a, s)) {
         if (s.n == 0) continue;
@@ -515,7 +592,7 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
 template <int D>
 __device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, const CUtensorMap* mq, int items) {
     using L = Smem<D>;
-    Walk w(a, items);
+    Walk w(c.range, items);
     Segment s;
     uint32_t n = 0;
     while (w.next(a, s)) {
@@ -616,7 +693,7 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
         if (elect_one()) tc_commit(base + L::qempty);
     };
 
-    Walk w(a, items);
+    Walk w(c.range, items);
     Segment s;
     Place at{0, 0};
     while (ok && w.next(a, s)) {
@@ -727,7 +804,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
     int ring = 0;                // slot of the segment's first K tile
     uint32_t turn = 0;           // and its turn
     bool ok = true;
-    Walk w(a, items);
+    Walk w(c.range, items);
     Segment s;
     while (w.next(a, s)) {
         const bool two = two_tiles(a, s, D);
@@ -1036,18 +1113,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(attn_smem + L::tmem);
     grid_dep_wait();
     const bool aligned = (c.base & 1023u) == 0;   // the swizzle pattern starts at the slots
-    if (!aligned && threadIdx.x == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+    if (!aligned && threadIdx.x == 0) {
+        atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+        if (blockIdx.x == 0) a.head->tasks = 0;
+    }
     int items = 0;
+    Range* range = reinterpret_cast<Range*>(attn_smem + L::range);
+    c.range = range;
     if (aligned) {
         if (a.local_plan) {
             // the ring is scratch until the first copy into it
-            items = plan_batch<kAttnThreads, true>(a, L::kTiles, L::kChunks,
-                                                   *reinterpret_cast<PlanScratch*>(attn_smem + L::ring));
+            items = local_plan(a, L::kTiles, *reinterpret_cast<LocalPlan*>(attn_smem + L::ring), range);
             fence_proxy_async_smem();
-            __syncthreads();
         } else {
             items = a.head->items;
+            if (threadIdx.x == 0 && items > 0) {
+                range->begin = a.starts[blockIdx.x];
+                range->end = a.starts[blockIdx.x + 1];
+            }
         }
+        __syncthreads();
     }
     const bool work = items > 0;
     // 384 threads x 168 registers at launch = 64,512; 128 x 80 + 256 x 208 = 63,488
@@ -1058,6 +1143,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             else if (warp == kMmaWarp) issue_mma<D, kBf16>(c, a, tmem, items);
             else if (warp == kQWarp && lane == 0) load_queries<D>(c, a, &mq, items);
         }
+        if (warp == kListWarp && blockIdx.x == 0 && aligned) list_cuts(a, L::kChunks, lane);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         if (work) softmax_rows<D, kBf16>(c, a, tmem, items, warp >> 2);
@@ -1080,27 +1166,27 @@ template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
     using L = Smem<D>;
     constexpr float kBias = weight_bias(kBf16);
-    __shared__ int task0[kMaxCtas];
+    __shared__ Job job_s[kMaxCtas];
     __shared__ float2 ml_s[kMaxCtas];
     __shared__ float4 acc_s[kJoinGroups][16];
     __shared__ float sum_s[kJoinGroups];
     grid_dep_wait();
     const PlanHead head = *a.head;
-    if (static_cast<int>(blockIdx.x) >= head.tasks) return;
-    for (int i = threadIdx.x; i < head.jobs; i += kJoinThreads) task0[i] = a.jobs[i].task0;
-    __syncthreads();
     const int group = threadIdx.x / 16, vec = threadIdx.x % 16, lane = threadIdx.x & 31;
+    // (requested along with the head: the list holds at most one job per CTA)
+    for (int i = threadIdx.x; i < a.grid; i += kJoinThreads) job_s[i] = a.jobs[i];
+    if (static_cast<int>(blockIdx.x) >= head.tasks) return;
+    __syncthreads();
     for (int task = blockIdx.x; task < head.tasks; task += gridDim.x) {
         int lo = 0, hi = head.jobs;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (task0[mid] <= task) lo = mid; else hi = mid;
+            if (job_s[mid].task0 <= task) lo = mid; else hi = mid;
         }
-        const Job job = a.jobs[lo];
-        const Item it = a.items[job.item];
+        const Job job = job_s[lo];
         const int parts = job.parts;
         const bool share = parts > kJoinFew;
-        const int rows0 = min(it.ntok, a.tq) * a.G, rows = it.ntok * a.G;   // of the first tile, of both
+        const int rows0 = min(job.ntok, a.tq) * a.G, rows = job.ntok * a.G;   // of the first tile, of both
         const int unit = share ? task - job.task0 : (task - job.task0) * kJoinGroups + group;
         const int r = unit / L::kChunks, col = unit % L::kChunks * 64 + vec * 4;
         const bool mine = r < rows;
@@ -1162,7 +1248,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
             const bool none = sum == 0.0f;
             const float inv = none ? 0.0f : 1.0f / sum;
             const int tok = row / a.G;
-            const int64_t t = it.tok0 + tile * a.tq + tok;
+            const int64_t t = job.tok0 + tile * a.tq + tok;
             const int h = job.g * a.G + row - tok * a.G;
             uint2 y;
             y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
@@ -1329,9 +1415,12 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
         return cudaErrorInvalidValue;
     a.wide_out = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && (s->n_tokens == 1 || a.o_st % 16 == 0) &&
                  (s->n_q_heads == 1 || a.o_sh % 16 == 0);
-    a.local_plan = l.items_max <= kLocalItems && a.B <= kLocalItems;
+    // costs (times CTAs) of a plan in 32 bits
+    const int64_t tiles = (static_cast<int64_t>(a.table_stride) * bs + kKeys - 1) / kKeys + kItemCost;
+    a.local_plan = l.items_max <= kLocalItems && a.B <= kLocalItems &&
+                   tiles < INT32_MAX / kLocalItems / kMaxCtas / a.hk;
     if (!a.local_plan) {
-        const cudaError_t e = launch_k(attn_plan_kernel, 1, kPlanThreads, 0, st, a, tiles_per_item(d), d / 64);
+        const cudaError_t e = launch_k(attn_plan_kernel, 1, kPlanThreads, 0, st, a, tiles_per_item(d));
         if (e != cudaSuccess) return e;
     }
     return d == 64    ? launch_d<64>(a, bf16, mq, mk, mv, st)
