@@ -15,7 +15,7 @@ after the scoring call that gave ``out``:
 
 import ctypes
 
-from . import _SZ, _check, _ptr, _stream, lib
+from . import _SZ, _check, lib
 
 
 class _BlockShape(ctypes.Structure):
@@ -47,6 +47,20 @@ class _AttnParams(ctypes.Structure):
 
 
 _INT32_MAX = 2 ** 31 - 1
+_int32 = _float32 = _codes = _raw_stream = _current_device = None
+
+
+def _init():
+    """torch's types and stream lookup, looked up once: a decode step makes
+    these calls for every layer, and the host's part of them is most of it
+    (torch.cuda.current_stream() alone takes 3 us, the raw handle 0.1)."""
+    global _int32, _float32, _codes, _raw_stream, _current_device
+    import torch
+    _int32, _float32 = torch.int32, torch.float32
+    _codes = {torch.bfloat16: 0, torch.float16: 1}
+    _current_device = torch.cuda.current_device
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _bind(lib_):
@@ -63,75 +77,65 @@ def _bind(lib_):
         fn.restype = ctypes.c_int
 
 
-def _on(device, t, name):
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-
-
-def _device_of(t, name):
+def _device_of(t, name) -> int:
     """The device of a call: that of its first tensor, which has to be the
     current CUDA device (the library launches there)."""
-    import torch
-    if not t.is_cuda:
+    if _int32 is None:
+        _init()
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if dev != _current_device():
         raise ValueError(f"{name} is on {t.device}, which is not the current CUDA device")
-    return t.device
+    return dev
 
 
-def _ints(t, n, name, device):
-    """An int32 vector of at least n entries, contiguous."""
-    import torch
-    if t.dtype is not torch.int32 or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} entries")
-    _on(device, t, name)
+def _ints(dev, *vectors):
+    """int32 vectors (tensor, entries at least, name), contiguous."""
+    for t, n, name in vectors:
+        if t.dtype is not _int32 or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n} entries on the call's device")
 
 
-def _dtype_code(t, name):
-    import torch
-    if t.dtype is torch.bfloat16:
-        return 0
-    if t.dtype is torch.float16:
-        return 1
-    raise ValueError(f"{name} must be bfloat16 or float16")
-
-
-def _rows(t, dtype, name, device, shape=None):
+def _rows(t, dtype, name, dev, shape=None):
     """Strides (token, head) of a [rows, heads, d] tensor, d contiguous."""
-    if t.dim() != 3 or t.dtype is not dtype or t.stride(2) != 1 or (shape is not None and t.shape != shape):
+    st = t.stride()
+    if len(st) != 3 or t.dtype is not dtype or st[2] != 1 or t.get_device() != dev or (
+            shape is not None and t.shape != shape):
         want = "[rows, heads, d]" if shape is None else str(list(shape))
-        raise ValueError(f"{name} must be a {want} tensor of type {dtype} with d contiguous")
-    _on(device, t, name)
-    return t.stride(0), t.stride(1)
+        raise ValueError(f"{name} must be a {want} tensor of type {dtype} on the call's device with d contiguous")
+    return st[0], st[1]
 
 
-def _pool(t, dtype, name, device):
-    """(blocks, block_size, Hk, d, token stride, head stride) of a pool."""
-    if t.dim() != 4 or t.dtype is not dtype or t.stride(3) != 1:
-        raise ValueError(f"{name} must be a [blocks, block_size, Hk, d] tensor of type {dtype} with d contiguous")
-    nb, bs, hk, d = t.shape
+def _pool(t, dtype, name, dev):
+    """(shape, token stride, head stride) of a [blocks, block_size, Hk, d] pool."""
+    st = t.stride()
+    if len(st) != 4 or t.dtype is not dtype or st[3] != 1 or t.get_device() != dev:
+        raise ValueError(f"{name} must be a [blocks, block_size, Hk, d] tensor of type {dtype} on the call's device "
+                         "with d contiguous")
+    shape = t.shape
     # (a block of one row has no token stride of its own)
-    st = t.stride(1) if bs > 1 else t.stride(0)
-    if nb > 1 and t.stride(0) != bs * st:
+    token = st[1] if shape[1] > 1 else st[0]
+    if shape[0] > 1 and st[0] != shape[1] * token:
         raise ValueError(f"the blocks of {name} must follow one another with the token stride")
-    _on(device, t, name)
-    return nb, bs, hk, d, st, t.stride(2)
+    return shape, token, st[2]
 
 
-def _table(t, n_seqs, device):
-    import torch
-    if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != n_seqs or t.shape[1] < 1 or not t.is_contiguous():
-        raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor")
-    _on(device, t, "block_table")
+def _table(t, n_seqs, dev) -> int:
+    shape = t.shape
+    if t.dtype is not _int32 or len(shape) != 2 or shape[0] != n_seqs or shape[1] < 1 or (
+            t.get_device() != dev or not t.is_contiguous()):
+        raise ValueError("block_table must be a contiguous int32 [B, max_blocks] tensor on the call's device")
+    return shape[1]
 
 
-def _new(shape, dtype, device, stream):
+def _new(shape, dtype, like, stream):
     """An output or workspace that belongs to the call's stream."""
     import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def block_tables(ctx_len, new_off, free_blocks, n_free, block_table, block_size: int, n_tokens=None, slot_map=None,
@@ -147,36 +151,32 @@ def block_tables(ctx_len, new_off, free_blocks, n_free, block_table, block_size:
     short (SP_ERR_CAPACITY) or a length is out of range (SP_ERR_DEVICE): the
     call then takes nothing, every slot is -1 and every kv_len 0.
     ``pool_blocks`` bounds the block ids."""
-    import torch
-    n_seqs = ctx_len.numel()
     dev = _device_of(ctx_len, "ctx_len")
-    _ints(ctx_len, 1, "ctx_len", dev)
-    _ints(new_off, n_seqs + 1, "new_off", dev)
-    _ints(free_blocks, 0, "free_blocks", dev)
-    _ints(n_free, 1, "n_free", dev)
-    _table(block_table, n_seqs, dev)
+    n_seqs = ctx_len.numel()
+    width = _table(block_table, n_seqs, dev)
     if slot_map is None:
         if n_tokens is None:
             raise ValueError("give slot_map or n_tokens")
-        slot_map = _new(int(n_tokens), torch.int32, dev, stream)
+        slot_map = _new(int(n_tokens), _int32, ctx_len, stream)
     elif n_tokens is None:
         n_tokens = slot_map.numel()
-    _ints(slot_map, n_tokens, "slot_map", dev)
     if kv_len is None:
-        kv_len = _new(n_seqs, torch.int32, dev, stream)
-    _ints(kv_len, n_seqs, "kv_len", dev)
+        kv_len = _new(n_seqs, _int32, ctx_len, stream)
     if n_left is None:
-        n_left = _new(1, torch.int32, dev, stream)
-    _ints(n_left, 1, "n_left", dev)
+        n_left = _new(1, _int32, ctx_len, stream)
+    _ints(dev, (ctx_len, 1, "ctx_len"), (new_off, n_seqs + 1, "new_off"), (free_blocks, 0, "free_blocks"),
+          (n_free, 1, "n_free"), (slot_map, n_tokens, "slot_map"), (kv_len, n_seqs, "kv_len"), (n_left, 1, "n_left"))
     if status is not None:
-        _ints(status, 1, "status", dev)
+        _ints(dev, (status, 1, "status"))
     if pool_blocks is None:
         pool_blocks = max(1, _INT32_MAX // max(1, int(block_size)))
-    shape = _BlockShape(n_seqs, int(block_size), block_table.shape[1], int(n_tokens), free_blocks.numel(),
-                        int(pool_blocks))
-    _check(lib().sp_block_tables(ctypes.byref(shape), ctx_len.data_ptr(), new_off.data_ptr(), free_blocks.data_ptr(),
-                                 n_free.data_ptr(), block_table.data_ptr(), slot_map.data_ptr(), kv_len.data_ptr(),
-                                 n_left.data_ptr(), _ptr(status), _stream(stream)), "sp_block_tables")
+    shape = _BlockShape(n_seqs, block_size, width, n_tokens, free_blocks.numel(), pool_blocks)
+    rc = lib().sp_block_tables(shape, ctx_len.data_ptr(), new_off.data_ptr(), free_blocks.data_ptr(),
+                               n_free.data_ptr(), block_table.data_ptr(), slot_map.data_ptr(), kv_len.data_ptr(),
+                               n_left.data_ptr(), None if status is None else status.data_ptr(),
+                               _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sp_block_tables")
     return slot_map, kv_len, n_left
 
 
@@ -189,70 +189,80 @@ def append_kv(k, v, slot_map, k_pool, v_pool, q=None, q_out=None, positions=None
     ``q_out`` [T, Hq, d], the rotated ``q`` (``q_out=q`` rotates in place), or
     None without queries. ``n_new`` (int32 [1], device) bounds the rows in
     use. Slots must differ from one another. ``status`` as in block_tables."""
-    n, hk, d = k.shape if k.dim() == 3 else (0, 0, 0)
     dev = _device_of(k, "k")
-    code = _dtype_code(k, "k")
     dt = k.dtype
+    code = _codes.get(dt)
+    if code is None:
+        raise ValueError("k must be bfloat16 or float16")
+    shape = k.shape
     k_st, k_sh = _rows(k, dt, "k", dev)
-    v_st, v_sh = _rows(v, dt, "v", dev, k.shape)
-    _ints(slot_map, n, "slot_map", dev)
-    nb, bs, khk, kd, kp_st, kp_sh = _pool(k_pool, dt, "k_pool", dev)
-    vnb, vbs, vhk, vd, vp_st, vp_sh = _pool(v_pool, dt, "v_pool", dev)
-    if (nb, bs, khk, kd) != (vnb, vbs, vhk, vd) or khk != hk or kd != d:
+    v_st, v_sh = _rows(v, dt, "v", dev, shape)
+    n, hk, d = shape
+    pool, kp_st, kp_sh = _pool(k_pool, dt, "k_pool", dev)
+    v_pool_shape, vp_st, vp_sh = _pool(v_pool, dt, "v_pool", dev)
+    if pool != v_pool_shape or pool[2] != hk or pool[3] != d:
         raise ValueError("k, v and the pools disagree on heads, head_dim or blocks")
+    _ints(dev, (slot_map, n, "slot_map"))
     rotary = max_pos = 0
     if cos_sin is not None:
-        import torch
-        if cos_sin.dtype is not torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous float32 [max_pos, rotary_dim] tensor")
-        _on(dev, cos_sin, "cos_sin")
         if positions is None:
             raise ValueError("cos_sin needs positions")
+        if cos_sin.dtype is not _float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or (
+                cos_sin.get_device() != dev):
+            raise ValueError("cos_sin must be a contiguous float32 [max_pos, rotary_dim] tensor on the call's device")
         max_pos, rotary = cos_sin.shape
-        _ints(positions, n, "positions", dev)
+        _ints(dev, (positions, n, "positions"))
     elif positions is not None:
         raise ValueError("positions need cos_sin")
     hq = q_st = q_sh = qo_st = qo_sh = 0
     if q is not None:
         q_st, q_sh = _rows(q, dt, "q", dev)
-        if q.shape[0] != n or q.shape[2] != d:
+        q_shape = q.shape
+        if q_shape[0] != n or q_shape[2] != d:
             raise ValueError("q and k disagree on tokens or head_dim")
-        hq = q.shape[1]
+        hq = q_shape[1]
         if q_out is None:
-            q_out = _new(q.shape, dt, dev, stream)
-        qo_st, qo_sh = _rows(q_out, dt, "q_out", dev, q.shape)
+            q_out = _new(q_shape, dt, k, stream)
+        qo_st, qo_sh = _rows(q_out, dt, "q_out", dev, q_shape)
     elif q_out is not None:
         raise ValueError("q_out needs q")
     if n_new is not None:
-        _ints(n_new, 1, "n_new", dev)
+        _ints(dev, (n_new, 1, "n_new"))
     if status is not None:
-        _ints(status, 1, "status", dev)
+        _ints(dev, (status, 1, "status"))
     if n == 0:
         return q_out
-    shape = _AppendShape(n, hq, hk, d, rotary, max_pos, code, 0, nb * bs, q_st, q_sh, qo_st, qo_sh, k_st, k_sh, v_st,
-                         v_sh, kp_st, kp_sh, vp_st, vp_sh)
-    _check(lib().sp_append_kv(ctypes.byref(shape), _ptr(q), k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
-                              _ptr(positions), _ptr(cos_sin), _ptr(n_new), _ptr(q_out), k_pool.data_ptr(),
-                              v_pool.data_ptr(), _ptr(status), _stream(stream)), "sp_append_kv")
+    rc = lib().sp_append_kv(
+        _AppendShape(n, hq, hk, d, rotary, max_pos, code, 0, pool[0] * pool[1], q_st, q_sh, qo_st, qo_sh, k_st, k_sh,
+                     v_st, v_sh, kp_st, kp_sh, vp_st, vp_sh),
+        None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), slot_map.data_ptr(),
+        None if positions is None else positions.data_ptr(), None if cos_sin is None else cos_sin.data_ptr(),
+        None if n_new is None else n_new.data_ptr(), None if q is None else q_out.data_ptr(), k_pool.data_ptr(),
+        v_pool.data_ptr(), None if status is None else status.data_ptr(),
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sp_append_kv")
     return q_out
 
 
-def _attention_shape(q, n_seqs, k_pool, device, table_stride=1, out=None, v_pool=None):
-    code = _dtype_code(q, "q")
+def _attention_shape(q, n_seqs, k_pool, dev, width=1, out=None, v_pool=None):
     dt = q.dtype
-    q_st, q_sh = _rows(q, dt, "q", device)
-    nb, bs, hk, d, k_st, k_sh = _pool(k_pool, dt, "k_pool", device)
-    n, hq, dq = q.shape
+    code = _codes.get(dt)
+    if code is None:
+        raise ValueError("q must be bfloat16 or float16")
+    q_st, q_sh = _rows(q, dt, "q", dev)
+    n, hq, dq = shape = q.shape
+    pool, k_st, k_sh = _pool(k_pool, dt, "k_pool", dev)
+    nb, bs, hk, d = pool
     if dq != d:
         raise ValueError("q and the pools disagree on head_dim")
-    o_st, o_sh = (hq * d, d) if out is None else _rows(out, dt, "out", device, q.shape)
+    o_st, o_sh = (hq * d, d) if out is None else _rows(out, dt, "out", dev, shape)
     v_st, v_sh = k_st, k_sh
     if v_pool is not None:
-        vnb, vbs, vhk, vd, v_st, v_sh = _pool(v_pool, dt, "v_pool", device)
-        if (vnb, vbs, vhk, vd) != (nb, bs, hk, d):
+        v_pool_shape, v_st, v_sh = _pool(v_pool, dt, "v_pool", dev)
+        if v_pool_shape != pool:
             raise ValueError("the pools disagree on heads, head_dim or blocks")
-    return _PagedShape(n_seqs, hq, hk, d, code, bs, table_stride, n, nb * bs, q_st, q_sh, o_st, o_sh, k_st, k_sh,
-                       v_st, v_sh)
+    return _PagedShape(n_seqs, hq, hk, d, code, bs, width, n, nb * bs, q_st, q_sh, o_st, o_sh, k_st, k_sh, v_st, v_sh)
 
 
 def make_attention_workspace(q, n_seqs: int, k_pool, stream=None):
@@ -263,11 +273,12 @@ def make_attention_workspace(q, n_seqs: int, k_pool, stream=None):
     dev = _device_of(q, "q")
     shape = _attention_shape(q, int(n_seqs), k_pool, dev)
     n = _SZ()
-    _check(lib().sp_paged_attention_workspace(ctypes.byref(shape), ctypes.byref(n)), "sp_paged_attention_workspace")
-    ws = _new(n.value + 256, torch.uint8, dev, stream)
+    _check(lib().sp_paged_attention_workspace(shape, ctypes.byref(n)), "sp_paged_attention_workspace")
+    ws = _new(n.value + 256, torch.uint8, q, stream)
     off = (-ws.data_ptr()) % 256
     ws = ws[off:off + n.value]
-    _check(lib().sp_workspace_init(ws.data_ptr(), n.value, _stream(stream)), "sp_workspace_init")
+    _check(lib().sp_workspace_init(ws.data_ptr(), n.value,
+                                   _raw_stream(dev) if stream is None else stream.cuda_stream), "sp_workspace_init")
     return ws
 
 
@@ -281,27 +292,26 @@ def paged_attention(q, q_off, kv_len, block_table, k_pool, v_pool, causal: bool 
     (fp32 [T, Hq], optional) receives the log-sum-exp of the scaled logits.
     A row that sees nothing gives 0 and -inf. ``ws`` from
     make_attention_workspace, with its status in device_status."""
-    import torch
-    n_seqs = kv_len.numel()
     dev = _device_of(q, "q")
-    _ints(kv_len, 1, "kv_len", dev)
-    _ints(q_off, n_seqs + 1, "q_off", dev)
-    _table(block_table, n_seqs, dev)
+    n_seqs = kv_len.numel()
+    _ints(dev, (kv_len, 1, "kv_len"), (q_off, n_seqs + 1, "q_off"))
+    width = _table(block_table, n_seqs, dev)
     if out is None:
-        out = _new(q.shape, q.dtype, dev, stream)
-    shape = _attention_shape(q, n_seqs, k_pool, dev, block_table.shape[1], out, v_pool)
-    if lse is not None:
-        if lse.dtype is not torch.float32 or not lse.is_contiguous() or lse.shape != q.shape[:2]:
-            raise ValueError("lse must be a contiguous float32 [T, Hq] tensor")
-        _on(dev, lse, "lse")
+        out = _new(q.shape, q.dtype, q, stream)
+    shape = _attention_shape(q, n_seqs, k_pool, dev, width, out, v_pool)
+    if lse is not None and (lse.dtype is not _float32 or not lse.is_contiguous() or lse.shape != q.shape[:2]
+                            or lse.get_device() != dev):
+        raise ValueError("lse must be a contiguous float32 [T, Hq] tensor on the call's device")
     if shape.n_tokens == 0:
         return out
     if ws is None:
         ws = make_attention_workspace(q, n_seqs, k_pool, stream)
-    _on(dev, ws, "ws")
-    params = _AttnParams(int(bool(causal)), int(window), float(scale), int(spin_limit))
-    _check(lib().sp_paged_attention(ctypes.byref(shape), ctypes.byref(params), q_off.data_ptr(), kv_len.data_ptr(),
-                                    block_table.data_ptr(), q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
-                                    out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel(), _stream(stream)),
-           "sp_paged_attention")
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must come from make_attention_workspace on the call's device")
+    rc = lib().sp_paged_attention(shape, _AttnParams(bool(causal), window, scale, spin_limit), q_off.data_ptr(),
+                                  kv_len.data_ptr(), block_table.data_ptr(), q.data_ptr(), k_pool.data_ptr(),
+                                  v_pool.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                  ws.data_ptr(), ws.nbytes, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if rc:
+        _check(rc, "sp_paged_attention")
     return out
