@@ -1352,7 +1352,7 @@ cudaError_t launch_d(const AttnArgs& a, bool bf16, const CUtensorMap& mq, const 
     const cudaError_t r = launch_k(kern, static_cast<unsigned>(a.grid), kAttnThreads, Smem<D>::total, st, mq, mk, mv, a);
     if (r != cudaSuccess) return r;
     return launch_k(bf16 ? attn_join_kernel<D, true> : attn_join_kernel<D, false>,
-                    static_cast<unsigned>(8 * a.grid), kJoinThreads, 0, st, a);
+                    static_cast<unsigned>(4 * a.grid), kJoinThreads, 0, st, a);
 }
 
 }  // namespace
