@@ -756,6 +756,22 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     }
 }
 
+// Lane c of a quad gives its w[j] to lane j: afterwards w[k] is what lane k
+// had for this lane.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
+    const bool odd = lane & 1, upper = lane & 2;
+#pragma unroll
+    for (int k = 0; k < 4; k += 2) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? w[k] : w[k + 1], 1);
+        if (odd) w[k] = r; else w[k + 1] = r;
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t r = __shfl_xor_sync(0xffffffffu, upper ? w[k] : w[k + 2], 2);
+        if (upper) w[k] = r; else w[k + 2] = r;
+    }
+}
+
 // One 32-byte sector from one thread.
 __device__ __forceinline__ void store_32b(void* p, const uint32_t* x) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
@@ -787,6 +803,113 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
         : "=f"(r.x), "=f"(r.y)
         : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
     return r;
+}
+
+// How a warp's rows of an item end: this lane's row (its place, factors of the
+// accumulators, reference and sum), and what all lanes share.
+struct RowEnd {
+    int64_t t;
+    int h, part;       // part < 0: the whole item is here
+    uint32_t ot;       // accumulator of the warp's rows
+    int rows, col0;    // rows in use from the warp's first, first column
+    float f0, f1, m, l;
+    bool join;
+};
+
+// Writes the rows of a warp: results, or a part for the join kernel. Not
+// inlined: the softmax loop keeps its registers. 16 rows x 64 columns at a
+// time, a quad of lanes on each of two rows, whose lanes exchange columns so
+// that each stores 32 bytes and the quad a whole line. (One row per lane: 32
+// lines an instruction, 1,100 cycles per 32 columns.)
+template <int D, bool kBf16>
+__device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
+    constexpr unsigned kAll = 0xffffffffu;
+    constexpr int kCols = D > 128 ? D / 2 : D;    // columns of a warpgroup
+    const int lane = threadIdx.x & 31;
+    const bool split = e.part >= 0;
+    const bool none = e.l == 0.0f && !split;
+    const float inv = split ? 1.0f : none ? 0.0f : 1.0f / e.l;
+    const float e0 = e.f0 * inv, e1 = e.f1 * inv;
+    char* dst = split ? reinterpret_cast<char*>(a.part_o + static_cast<int64_t>(e.part) * D + e.col0)
+                      : reinterpret_cast<char*>(a.out + e.t * a.o_st + e.h * a.o_sh + e.col0);
+    if (lane < e.rows && e.col0 == 0) {
+        if (split) a.part_ml[e.part] = make_float2(e.m, e.l);
+        else if (a.lse) a.lse[e.t * a.G * a.hk + e.h] = none ? -INFINITY : (e.m - weight_bias(kBf16) + log2f(e.l)) * kLn2;
+    }
+#pragma unroll 1
+    for (int half = 0; half < 2 && half * 16 < e.rows; ++half) {
+        const int r0 = half * 16 + lane / 4;
+        float x0[2], x1[2];
+        char* at[2];
+        bool mine[2], zero[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            x0[k] = __shfl_sync(kAll, e0, r0 + 8 * k);
+            x1[k] = __shfl_sync(kAll, e1, r0 + 8 * k);
+            at[k] = reinterpret_cast<char*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(dst), r0 + 8 * k));
+            zero[k] = __shfl_sync(kAll, none, r0 + 8 * k) != 0;
+            mine[k] = r0 + 8 * k < e.rows;
+        }
+#pragma unroll 1
+        for (int cb = 0; cb < kCols / 64; ++cb) {
+            float x[32];
+            const uint32_t src = e.ot + (static_cast<uint32_t>(half * 16) << 16) + cb * 64;
+            tmem_ld_16x256b_x8(src, x);
+            if (e.join) {
+                float y[32];
+                tmem_ld_16x256b_x8(src + D, y);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = x[i] * x0[i >> 1 & 1] + y[i] * x1[i >> 1 & 1];
+            } else {
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] *= x0[i >> 1 & 1];
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (split) {
+                    // groups of 8 columns j: lane c of the quad takes j = c, then 4 + c
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int p = 0; p < 2; ++p) {
+                            uint32_t y[4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) y[j] = __float_as_uint(x[4 * (4 * u + j) + 2 * k + p]);
+                            quad_transpose(y, lane);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) w[2 * j + p] = y[j];
+                        }
+                        if (mine[k]) store_32b(at[k] + cb * 256 + u * 128 + (lane & 3) * 32, w);
+                    }
+                } else {
+                    // lane c takes the groups 2 c and 2 c + 1
+                    uint32_t w[8];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            y[j] = zero[k] ? 0u : pack_pair<kBf16>(x[4 * (2 * j + u) + 2 * k], x[4 * (2 * j + u) + 2 * k + 1]);
+                        quad_transpose(y, lane);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) w[4 * u + j] = y[j];
+                    }
+                    if (mine[k]) {
+                        char* p = at[k] + cb * 128 + (lane & 3) * 32;
+                        if (a.wide_out) {
+                            store_32b(p, w);
+                        } else {
+                            reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    }
+                }
+            }
+        }
+    }
 }
 
 // One warpgroup (index wg) of softmax threads over the CTA's segments.
@@ -850,13 +973,17 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                     tmem_ld_wait();
                     const int h = hi - key0, b = lo - key0;
                     if (__any_sync(kAll, h < kKeys || b > 0)) {
+                        // 32 columns at a time: most are seen by all rows of the
+                        // warp or by none
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q) {
+                            const int hq = min(max(h - q * 32, 0), 32), bq = min(max(b - q * 32, 0), 32);
+                            if (!__any_sync(kAll, hq < 32 || bq > 0)) continue;
+                            const uint32_t seen_cols = static_cast<uint32_t>((1ull << hq) - (1ull << min(bq, hq)));
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const int col = q * 32 + i;
-                                if (col >= h || col < b) v[q][i] = -INFINITY;
-                            }
+                            for (int i = 0; i < 32; ++i)
+                                if (!(seen_cols & (1u << i))) v[q][i] = -INFINITY;
+                        }
                     }
                     float mx[4];
 #pragma unroll
@@ -986,65 +1113,20 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             }
             constexpr int kCols = D > 128 ? D / 2 : D;    // columns of this warpgroup
             const int col0 = D > 128 ? wg * kCols : 0;
-            const uint32_t ot = tmem + lanes + 2 * kKeys + o * D + col0;
-            auto read = [&](int q, float (&x)[32]) {
-                tmem_ld_32x32b_x32(ot + 32 * q, x);
-                if (join) {
-                    float y[32];
-                    tmem_ld_32x32b_x32(ot + D + 32 * q, y);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = x[i] * f0 + y[i] * f1;
-                } else {
-                    tmem_ld_wait();
-                }
-            };
-            const int64_t t = s.it.tok0 + tile * a.tq + tok;
-            const int h = s.g * a.G + row - tok * a.G;
-            if (!s.split) {
-                if (ok && live) {
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    uint16_t* dst = a.out + t * a.o_st + h * a.o_sh + col0;
-                    const bool none = s.n == 0 || l == 0.0f;
-#pragma unroll 1
-                    for (int q = 0; q < kCols / 32; ++q) {
-                        float x[32];
-                        if (s.n > 0) read(q, x);
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            pk[i] = none ? 0u : pack_pair<kBf16>(x[2 * i] * inv, x[2 * i + 1] * inv);
-                        if (valid) {
-                            if (a.wide_out) {
-                                store_32b(dst + q * 32, pk);
-                                store_32b(dst + q * 32 + 16, pk + 8);
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    reinterpret_cast<uint4*>(dst + q * 32)[i] =
-                                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
-                            }
-                        }
-                    }
-                    if (valid && a.lse && col0 == 0)
-                        a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2;
-                }
-            } else {
-                const int part = (blockIdx.x * 2 + (s.head ? 0 : 1)) * L::kTiles + tile;
-                if (ok && live) {
-                    float* dst = a.part_o + (static_cast<int64_t>(part) * kRows + row) * D + col0;
-#pragma unroll 1
-                    for (int q = 0; q < kCols / 32; ++q) {
-                        float x[32];
-                        read(q, x);
-                        if (valid) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                store_32b(dst + q * 32 + 8 * i, reinterpret_cast<const uint32_t*>(x + 8 * i));
-                        }
-                    }
-                    if (valid && col0 == 0) a.part_ml[static_cast<int64_t>(part) * kRows + row] = make_float2(m, l);
-                }
+            if (ok && live) {
+                RowEnd e;
+                e.ot = tmem + lanes + 2 * kKeys + o * D + col0;
+                e.rows = rows - warp * 32;
+                e.t = s.it.tok0 + tile * a.tq + tok;
+                e.h = s.g * a.G + row - tok * a.G;
+                e.part = s.split ? ((static_cast<int>(blockIdx.x) * 2 + (s.head ? 0 : 1)) * L::kTiles + tile) * kRows + row : -1;
+                e.col0 = col0;
+                e.f0 = s.n > 0 ? f0 : 0.0f;
+                e.f1 = f1;
+                e.m = m;
+                e.l = s.n > 0 ? l : 0.0f;
+                e.join = join;
+                write_rows<D, kBf16>(a, e);
             }
             if (s.n > 0) {
                 tc_fence_before();
@@ -1070,7 +1152,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                const __grid_constant__ CUtensorMap mv, const AttnArgs a) {
+                const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
     using L = Smem<D>;
     extern __shared__ __align__(1024) uint8_t attn_smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
