@@ -614,14 +614,20 @@ __device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, co
 // Run by the whole warp: control flow and descriptors are the same in every
 // lane (broadcasts tell the compiler so: operands then stay in uniform
 // registers; issued by one diverged lane, eight MMAs took some 1,300 cycles),
-// and one elected lane issues.
+// and one elected lane issues. A step of a stream is the product of its weights
+// with V_j and the product of the next keys with its queries. Its barriers are
+// polled together, one per lane: a wait costs some 200 cycles even when it is
+// over, and the MMA queue holds only a few instructions.
 template <int D, bool kBf16>
 __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint32_t tmem_base, int items) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
     constexpr uint32_t kIdQk = idesc_f16_f32(kRows, kKeys, kBf16, false);
     constexpr uint32_t kIdPv = idesc_f16_f32(kRows, D, kBf16, true);
-    constexpr int kPer = L::kSlotKeys;
+    constexpr int P = L::kParts, kPer = L::kSlotKeys;
+    // lane 0: weights; 1 .. P: V slots; P + 1 .. 2 P: K slots; then the accumulator
+    constexpr unsigned kNeedV = ((1u << P) - 1) << 1, kNeedK = kNeedV << P, kNeedO = 1u << (2 * P + 1);
+    const int lane = threadIdx.x & 31;
     const uint32_t tmem = __shfl_sync(kAll, tmem_base, 0);
     const uint32_t base = __shfl_sync(kAll, c.base, 0);
     uint32_t nq = 0;                 // segments with keys so far
@@ -629,29 +635,39 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
     uint32_t no0 = 0, no1 = 0;       // segments that used each accumulator
     bool ok = true, any = false;
 
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok) ok = __all_sync(kAll, c.wait(bar, parity));
-        return ok;
+    // Polls this lane's barrier until all lanes of `need` have theirs; the
+    // lanes that do, then.
+    auto poll = [&](uint32_t bar, uint32_t parity, unsigned need) -> unsigned {
+        for (int64_t it = 0; ok; ++it) {
+            const unsigned got = __ballot_sync(kAll, mbar_test_wait(base + bar, parity & 1));
+            if ((got & need) == need) return got;
+            if (__any_sync(kAll, *c.abort_flag != 0) || it > 16 * c.spin) ok = false;   // (16 polls to a suspended wait)
+        }
+        if (lane == 0) {
+            *c.abort_flag = 1;
+            atomicCAS(c.status, 0, static_cast<int32_t>(SP_ERR_TIMEOUT));
+        }
+        return 0;
     };
-    // a place in the ring; a tile that both query tiles use is walked twice
+    // a place in the ring: slot and turn
     struct Place {
         int slot;
         uint32_t turn;
     };
-    auto step = [&](Place& p) {
-        if (++p.slot == L::kSlots) {
-            p.slot = 0;
+    auto ahead = [&](Place p, int n) -> Place {
+        p.slot += n;
+        if (p.slot >= L::kSlots) {
+            p.slot -= L::kSlots;
             p.turn ^= 1;
         }
+        return p;
     };
-    // logits of query tile t and the K tile at p into stream buffer sb;
-    // `fresh`: its slots have not been waited for
-    auto qk = [&](Place p, int t, int sb, bool fresh, bool release) -> Place {
-#pragma unroll 1
-        for (int part = 0; part < L::kParts; ++part) {
-            if (fresh && !wait(L::full + 8 * p.slot, p.turn)) return p;
-            tc_fence_after();
-            const int slot = __shfl_sync(kAll, p.slot, 0);
+    // logits of query tile t and the K tile at p into stream buffer sb
+    auto qk = [&](Place p, int t, int sb, bool release) {
+        any = true;
+#pragma unroll(P == 1 ? 2 : 1)
+        for (int part = 0; part < P; ++part) {
+            const int slot = __shfl_sync(kAll, ahead(p, part).slot, 0);
             const uint64_t qd = smem_desc_sw128(base + L::q + t * L::kChunks * kChunk + part * L::kSlot);
             const uint64_t kd = smem_desc_sw128(base + L::ring + slot * L::kSlot, 1024 * L::kSlotChunks);
             if (elect_one()) {
@@ -660,22 +676,15 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
                     tc_mma_bf16(tmem + sb * kKeys, qd + (k / 4) * (kChunk / 16) + 2 * (k % 4),
                                 kd + (k / 4) * 64 + 2 * (k % 4), kIdQk, (part | k) != 0);
                 if (release) tc_commit(base + L::empty + 8 * slot);
-                if (part == L::kParts - 1) tc_commit(base + L::sfull + 8 * sb);
+                if (part == P - 1) tc_commit(base + L::sfull + 8 * sb);
             }
-            step(p);
         }
-        any = true;
-        return p;
     };
     // accumulator o (+)= weights of stream sb times the V tile at p
-    auto pv = [&](Place p, int sb, int o, bool fresh, bool first, bool release) -> Place {
-        if (first && !wait(L::oempty + 8 * o, (o ? no1++ : no0++) & 1 ^ 1)) return p;
-        if (!wait(L::pfull + 8 * sb, (sb ? np1++ : np0++) & 1)) return p;
-#pragma unroll 1
-        for (int part = 0; part < L::kParts; ++part) {
-            if (fresh && !wait(L::full + 8 * p.slot, p.turn)) return p;
-            tc_fence_after();
-            const int slot = __shfl_sync(kAll, p.slot, 0);
+    auto pv = [&](Place p, int sb, int o, bool first, bool release) {
+#pragma unroll(P == 1 ? 2 : 1)
+        for (int part = 0; part < P; ++part) {
+            const int slot = __shfl_sync(kAll, ahead(p, part).slot, 0);
             const uint64_t vd = smem_desc_sw128_mn(base + L::ring + slot * L::kSlot, 1024, 1024 * L::kChunks);
             if (elect_one()) {
 #pragma unroll
@@ -683,11 +692,42 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
                     tc_mma_f16_ts(tmem + 2 * kKeys + o * D, tmem + sb * kKeys + (part * (kPer / 16) + k) * 8,
                                   vd + 128 * L::kChunks * k, kIdPv, !first || (part | k) != 0);
                 if (release) tc_commit(base + L::empty + 8 * slot);
-                if (part == L::kParts - 1) tc_commit(base + L::odone + 8 * sb);
+                if (part == P - 1) tc_commit(base + L::odone + 8 * sb);
             }
-            step(p);
         }
-        return p;
+    };
+    // The next step of stream sb on query tile t: V at v, and K behind it when
+    // `more`. `fresh`: nobody has waited for their slots yet.
+    auto step = [&](Place v, int t, int sb, int o, bool first, bool more, bool fresh, bool release) {
+        const Place k = ahead(v, P);
+        const Place mine = lane <= P ? ahead(v, lane - 1 < 0 ? 0 : lane - 1) : ahead(k, (lane - 1) % P);
+        uint32_t bar = L::pfull + 8 * sb, parity = sb ? np1 : np0;
+        if (lane >= 1 && lane <= 2 * P) {
+            bar = L::full + 8 * mine.slot;
+            parity = mine.turn;
+        } else if (lane == 2 * P + 1) {
+            bar = L::oempty + 8 * o;
+            parity = (o ? no1 : no0) ^ 1;
+        }
+        const unsigned got = poll(bar, parity, 1u | (fresh ? kNeedV : 0u) | (first ? kNeedO : 0u));
+        if (!ok) return;
+        if (sb) ++np1; else ++np0;
+        if (first) { if (o) ++no1; else ++no0; }
+        tc_fence_after();
+        pv(v, sb, o, first, release);
+        if (more) {
+            if (fresh && (got & kNeedK) != kNeedK) {
+                poll(bar, parity, kNeedK);
+                if (!ok) return;
+            }
+            qk(k, t, sb, release);
+        }
+    };
+    auto keys_at = [&](Place p) {   // the K tile at p is there
+        const Place mine = ahead(p, lane % P);
+        poll(L::full + 8 * mine.slot, mine.turn, (1u << P) - 1);
+        tc_fence_after();
+        return ok;
     };
     auto queries_read = [&]() {
         if (elect_one()) tc_commit(base + L::qempty);
@@ -699,39 +739,41 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
     while (ok && w.next(a, s)) {
         const int n = __shfl_sync(kAll, s.n, 0);
         if (n == 0) continue;
-        if (!wait(L::qfull, nq & 1)) break;
+        const bool two = __shfl_sync(kAll, static_cast<int>(two_tiles(a, s, D)), 0) != 0;
+        poll(L::qfull, nq, 1);
+        if (!ok) break;
         ++nq;
-        if (__shfl_sync(kAll, static_cast<int>(two_tiles(a, s, D)), 0)) {
-            qk(at, 0, 0, true, false);
-            at = qk(at, 1, 1, false, true);
+        if (!keys_at(at)) break;
+        if (two) {
+            qk(at, 0, 0, false);
+            qk(at, 1, 1, true);
             if (n == 1) queries_read();
+            at = ahead(at, P);
             for (int j = 0; j < n && ok; ++j) {
-                const Place v = at;
-                const Place k = pv(v, 0, 0, true, j == 0, false);
-                if (j + 1 < n) qk(k, 0, 0, true, false);
-                at = pv(v, 1, 1, false, j == 0, true);
-                if (j + 1 < n) {
-                    at = qk(k, 1, 1, false, true);
-                    if (j + 2 == n) queries_read();
-                }
+                step(at, 0, 0, 0, j == 0, j + 1 < n, true, false);
+                if (!ok) break;
+                step(at, 1, 1, 1, j == 0, j + 1 < n, false, true);
+                if (j + 2 == n) queries_read();
+                at = ahead(ahead(at, P), j + 1 < n ? P : 0);
             }
         } else {
-            at = qk(at, 0, 0, true, true);
-            if (n > 1) at = qk(at, 0, 1, true, true);
+            // ring: K0 K1 V0 K2 V1 K3 ...
+            qk(at, 0, 0, true);
+            at = ahead(at, P);
+            if (n > 1) {
+                if (!keys_at(at)) break;
+                qk(at, 0, 1, true);
+                at = ahead(at, P);
+            }
             if (n <= 2) queries_read();
-            // ring: V0 K2 V1 K3 ...
             for (int j = 0; j < n && ok; j += 2) {
-                at = pv(at, 0, 0, true, j == 0, true);
-                if (j + 2 < n) {
-                    at = qk(at, 0, 0, true, true);
-                    if (j + 3 == n) queries_read();
-                }
-                if (j + 1 < n) {
-                    at = pv(at, 1, D <= 128 ? 1 : 0, true, D <= 128 && j == 0, true);
-                    if (j + 3 < n) {
-                        at = qk(at, 0, 1, true, true);
-                        if (j + 4 == n) queries_read();
-                    }
+                step(at, 0, 0, 0, j == 0, j + 2 < n, true, true);
+                if (j + 3 == n) queries_read();
+                at = ahead(ahead(at, P), j + 2 < n ? P : 0);
+                if (j + 1 < n && ok) {
+                    step(at, 0, 1, D <= 128 ? 1 : 0, D <= 128 && j == 0, j + 3 < n, true, true);
+                    if (j + 4 == n) queries_read();
+                    at = ahead(ahead(at, P), j + 3 < n ? P : 0);
                 }
             }
         }
