@@ -126,7 +126,7 @@ struct AttnArgs {
     int B, hk, G, tq, bs, table_stride, cap, causal, window, grid;
     int wide_out;        // 32-byte stores of out are aligned
     int local_plan;      // every CTA lays out the batch itself
-    int hk_box, hv_box;  // rows of a K and of a V box
+    int hk_shift, hv_shift;  // rows of a K and of a V box, as powers of two
     uint32_t q_bytes;    // of one 64-element chunk of a query tile
     float scale2;
 };
@@ -504,32 +504,38 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
                                           const CUtensorMap* mv, int items, int lane) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
-    constexpr int kPer = L::kSlotKeys;
-    const int nk = kKeys / a.hk_box;           // K boxes of a tile
-    const int sub = kPer / a.hv_box;           // V boxes of a slot
+    constexpr int P = L::kParts, kPer = L::kSlotKeys;
+    // (few instructions per slot: the warp shares its scheduler with two softmax
+    // warps, and at 120 instructions a slot its own arithmetic set the rate)
+    const int nk = kKeys >> a.hk_shift, hk = 1 << a.hk_shift;   // K boxes of a tile, their rows
+    const int sub = kPer >> a.hv_shift, hv = 1 << a.hv_shift;   // V boxes of a slot
+    const uint32_t k_dst = c.base + L::ring + static_cast<uint32_t>(lane << a.hk_shift) * (L::kSlotChunks * 128u);
+    const uint32_t v_dst = c.base + L::ring + static_cast<uint32_t>(lane << a.hv_shift) * (L::kChunks * 128u);
+    const int key_v = lane << a.hv_shift;    // this lane's V box, within its slot
+    const int per_block = a.bs >> 7;         // tiles of a block (0: blocks of a tile)
     int slot = 0;
     uint32_t turn = 0;
     bool ok = true;
 
-    // pool row of this lane's K box of a tile; -1 outside the item's keys
+    // pool row / 8 of this lane's K box of a tile; -1 outside the item's keys
     auto lookup = [&](const Segment& s, int tile) -> int {
-        const int key = tile * kKeys + lane * a.hk_box;
-        if (lane >= nk || key >= s.it.khi || key + a.hk_box <= s.it.klo) return -1;
-        const int blk = key / a.bs;
+        const int key = tile * kKeys + (lane << a.hk_shift);
+        if (lane >= nk || key >= s.it.khi || key + hk <= s.it.klo) return -1;
+        const int blk = per_block > 1 ? tile / per_block : per_block ? tile : tile * nk + lane;
+        const int within = per_block > 1 ? (tile - blk * per_block) * kKeys : 0;
         const int id = a.table[static_cast<int64_t>(s.it.b) * a.table_stride + blk];
         const int64_t row = static_cast<int64_t>(id) * a.bs;
         if (id < 0 || row + a.bs > a.pool_tokens) {
             atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
             return 0;
         }
-        return static_cast<int>(row) + key - blk * a.bs;
+        return static_cast<int>((row + within) >> 3);
     };
+    // the next slot, once it is empty, for `bytes`
     auto acquire = [&](uint32_t bytes) -> bool {
-        if (lane == 0) {
-            ok = c.wait(L::empty + 8 * slot, turn ^ 1);
-            if (ok) mbar_arrive_expect_tx(c.base + L::full + 8 * slot, bytes);
-        }
-        ok = __shfl_sync(kAll, ok, 0);
+        ok = __all_sync(kAll, c.wait(L::empty + 8 * slot, turn ^ 1));
+        if (ok && lane == 0) mbar_arrive_expect_tx(c.base + L::full + 8 * slot, bytes);
+        __syncwarp();
         return ok;
     };
     auto advance = [&]() {
@@ -538,28 +544,27 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
             turn ^= 1;
         }
     };
-    auto put_k = [&](const Segment& s, int row) {
-        const uint32_t bytes = __popc(__ballot_sync(kAll, row >= 0)) * a.hk_box * (L::kSlotChunks * 128u);
-        for (int p = 0; p < L::kParts; ++p) {
+    auto put_k = [&](const Segment& s, int group) {
+        const uint32_t bytes = __popc(__ballot_sync(kAll, group >= 0)) * (static_cast<uint32_t>(hk) * L::kSlotChunks * 128u);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
             if (!acquire(bytes)) return;
-            if (row >= 0)
-                tma_load_5d(c.base + L::ring + slot * L::kSlot + static_cast<uint32_t>(lane * a.hk_box) * (L::kSlotChunks * 128u),
-                            mk, c.base + L::full + 8 * slot, 0, 0, p * L::kSlotChunks, row / 8, s.g);
+            if (group >= 0)
+                tma_load_5d(k_dst + slot * L::kSlot, mk, c.base + L::full + 8 * slot, 0, 0, p * L::kSlotChunks, group, s.g);
             advance();
         }
     };
-    auto put_v = [&](const Segment& s, int tile, int row) {
-        for (int p = 0; p < L::kParts; ++p) {
+    auto put_v = [&](const Segment& s, int tile, int group) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
             // the rows of a V box lie in the block of a K box of the tile
-            const int key = p * kPer + lane * a.hv_box;    // of the tile
-            const int base_row = __shfl_sync(kAll, row, key / a.hk_box & 31);
-            const int at = tile * kKeys + key;
-            const bool there = lane < sub && base_row >= 0 && at < s.it.khi && at + a.hv_box > s.it.klo;
-            const uint32_t bytes = __popc(__ballot_sync(kAll, there)) * a.hv_box * (L::kChunks * 128u);
+            const int key = p * kPer + key_v, at = tile * kKeys + key;
+            const int first = __shfl_sync(kAll, group, key >> a.hk_shift & 31);
+            const bool there = lane < sub && first >= 0 && at < s.it.khi && at + hv > s.it.klo;
+            const uint32_t bytes = __popc(__ballot_sync(kAll, there)) * (static_cast<uint32_t>(hv) * L::kChunks * 128u);
             if (!acquire(bytes)) return;
             if (there)
-                tma_load_5d(c.base + L::ring + slot * L::kSlot + static_cast<uint32_t>(lane * a.hv_box) * (L::kChunks * 128u),
-                            mv, c.base + L::full + 8 * slot, 0, 0, 0, (base_row + key % a.hk_box) / 8, s.g);
+                tma_load_5d(v_dst + slot * L::kSlot, mv, c.base + L::full + 8 * slot, 0, 0, 0, first + ((key & (hk - 1)) >> 3), s.g);
             advance();
         }
     };
@@ -569,15 +574,15 @@ __device__ __forceinline__ void load_keys(const Ctx& c, const AttnArgs& a, const
     while (ok && w.next(a, s)) {
         if (s.n == 0) continue;
         const bool two = two_tiles(a, s, D);
-        int row = lookup(s, s.first), next = -1;
+        int group = lookup(s, s.first), next = -1;
         if (s.n > 1) next = lookup(s, s.first + 1);
-        if (!two) put_k(s, row);
+        if (!two) put_k(s, group);
         for (int j = 0; j < s.n && ok; ++j) {
             const int after = j + 2 < s.n ? lookup(s, s.first + j + 2) : -1;
-            if (two) put_k(s, row);
+            if (two) put_k(s, group);
             else if (j + 1 < s.n) put_k(s, next);
-            if (ok) put_v(s, s.first + j, row);
-            row = next;
+            if (ok) put_v(s, s.first + j, group);
+            group = next;
             next = after;
         }
     }
@@ -1524,17 +1529,18 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.cap = s->n_tokens;
     a.causal = p->causal;
     a.window = p->window;
-    a.hk_box = bs < kKeys ? bs : kKeys;
     const int per = kKeys / slots_per_tile(d);
-    a.hv_box = bs < per ? bs : per;
+    const int hk = bs < kKeys ? bs : kKeys, hv = bs < per ? bs : per;
+    a.hk_shift = __builtin_ctz(hk);
+    a.hv_shift = __builtin_ctz(hv);
     a.q_bytes = static_cast<uint32_t>(a.G * a.tq) * 128u;
     const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(d));
     a.scale2 = static_cast<float>(scale * 1.4426950408889634);
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, bf16, q, d, s->n_q_heads, s->q_stride_head, s->n_tokens, s->q_stride_token, a.G, a.tq) ||
-        !make_pool_map(&mk, bf16, k_pool, d, s->pool_tokens, s->k_stride_token, a.hk, s->k_stride_head, a.hk_box,
+        !make_pool_map(&mk, bf16, k_pool, d, s->pool_tokens, s->k_stride_token, a.hk, s->k_stride_head, hk,
                        d / 64 / slots_per_tile(d)) ||
-        !make_pool_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, a.hv_box,
+        !make_pool_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, hv,
                        d / 64))
         return cudaErrorInvalidValue;
     a.wide_out = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && (s->n_tokens == 1 || a.o_st % 16 == 0) &&
