@@ -803,22 +803,6 @@ __device__ __forceinline__ uint32_t pack_pair(float x, float y) {
     }
 }
 
-// Lane c of a quad gives its w[j] to lane j: afterwards w[k] is what lane k
-// had for this lane.
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int lane) {
-    const bool odd = lane & 1, upper = lane & 2;
-#pragma unroll
-    for (int k = 0; k < 4; k += 2) {
-        const uint32_t r = __shfl_xor_sync(0xffffffffu, odd ? w[k] : w[k + 1], 1);
-        if (odd) w[k] = r; else w[k + 1] = r;
-    }
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const uint32_t r = __shfl_xor_sync(0xffffffffu, upper ? w[k] : w[k + 2], 2);
-        if (upper) w[k] = r; else w[k + 2] = r;
-    }
-}
-
 // One 32-byte sector from one thread.
 __device__ __forceinline__ void store_32b(void* p, const uint32_t* x) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]),
@@ -863,97 +847,55 @@ struct RowEnd {
     bool join;
 };
 
-// Writes the rows of a warp: results, or a part for the join kernel. Not
-// inlined: the softmax loop keeps its registers. 16 rows x 64 columns at a
-// time, a quad of lanes on each of two rows, whose lanes exchange columns so
-// that each stores 32 bytes and the quad a whole line. (One row per lane: 32
-// lines an instruction, 1,100 cycles per 32 columns.)
+// Writes the rows of a warp, one per lane: results, or a part for the join
+// kernel. Not inlined: the softmax loop keeps its registers. (Whole lines after
+// an exchange between quads took 1.4 times as long: the shuffles cost more
+// than the 32 lines of a store.)
 template <int D, bool kBf16>
 __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
-    constexpr unsigned kAll = 0xffffffffu;
     constexpr int kCols = D > 128 ? D / 2 : D;    // columns of a warpgroup
-    const int lane = threadIdx.x & 31;
+    const bool mine = static_cast<int>(threadIdx.x & 31) < e.rows;
     const bool split = e.part >= 0;
     const bool none = e.l == 0.0f && !split;
-    const float inv = split ? 1.0f : none ? 0.0f : 1.0f / e.l;
+    const float inv = split ? 1.0f : none ? 0.0f : __fdividef(1.0f, e.l);
     const float e0 = e.f0 * inv, e1 = e.f1 * inv;
     char* dst = split ? reinterpret_cast<char*>(a.part_o + static_cast<int64_t>(e.part) * D + e.col0)
                       : reinterpret_cast<char*>(a.out + e.t * a.o_st + e.h * a.o_sh + e.col0);
-    if (lane < e.rows && e.col0 == 0) {
+    if (mine && e.col0 == 0) {
         if (split) a.part_ml[e.part] = make_float2(e.m, e.l);
-        else if (a.lse) a.lse[e.t * a.G * a.hk + e.h] = none ? -INFINITY : (e.m - weight_bias(kBf16) + log2f(e.l)) * kLn2;
+        else if (a.lse) a.lse[e.t * a.G * a.hk + e.h] = none ? -INFINITY : (e.m - weight_bias(kBf16) + __log2f(e.l)) * kLn2;
     }
 #pragma unroll 1
-    for (int half = 0; half < 2 && half * 16 < e.rows; ++half) {
-        const int r0 = half * 16 + lane / 4;
-        float x0[2], x1[2];
-        char* at[2];
-        bool mine[2], zero[2];
+    for (int q = 0; q < kCols / 32; ++q) {
+        float x[32];
+        tmem_ld_32x32b_x32(e.ot + 32 * q, x);
+        if (e.join) {
+            float y[32];
+            tmem_ld_32x32b_x32(e.ot + D + 32 * q, y);
+            tmem_ld_wait();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            x0[k] = __shfl_sync(kAll, e0, r0 + 8 * k);
-            x1[k] = __shfl_sync(kAll, e1, r0 + 8 * k);
-            at[k] = reinterpret_cast<char*>(__shfl_sync(kAll, reinterpret_cast<unsigned long long>(dst), r0 + 8 * k));
-            zero[k] = __shfl_sync(kAll, none, r0 + 8 * k) != 0;
-            mine[k] = r0 + 8 * k < e.rows;
+            for (int i = 0; i < 32; ++i) x[i] = x[i] * e0 + y[i] * e1;
+        } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] *= e0;
         }
-#pragma unroll 1
-        for (int cb = 0; cb < kCols / 64; ++cb) {
-            float x[32];
-            const uint32_t src = e.ot + (static_cast<uint32_t>(half * 16) << 16) + cb * 64;
-            tmem_ld_16x256b_x8(src, x);
-            if (e.join) {
-                float y[32];
-                tmem_ld_16x256b_x8(src + D, y);
-                tmem_ld_wait();
+        if (!mine) continue;
+        if (split) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = x[i] * x0[i >> 1 & 1] + y[i] * x1[i >> 1 & 1];
+            for (int i = 0; i < 4; ++i)
+                store_32b(dst + q * 128 + i * 32, reinterpret_cast<const uint32_t*>(x + 8 * i));
+        } else {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = none ? 0u : pack_pair<kBf16>(x[2 * i], x[2 * i + 1]);
+            if (a.wide_out) {
+                store_32b(dst + q * 64, w);
+                store_32b(dst + q * 64 + 32, w + 8);
             } else {
-                tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] *= x0[i >> 1 & 1];
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (split) {
-                    // groups of 8 columns j: lane c of the quad takes j = c, then 4 + c
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int p = 0; p < 2; ++p) {
-                            uint32_t y[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) y[j] = __float_as_uint(x[4 * (4 * u + j) + 2 * k + p]);
-                            quad_transpose(y, lane);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) w[2 * j + p] = y[j];
-                        }
-                        if (mine[k]) store_32b(at[k] + cb * 256 + u * 128 + (lane & 3) * 32, w);
-                    }
-                } else {
-                    // lane c takes the groups 2 c and 2 c + 1
-                    uint32_t w[8];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        uint32_t y[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            y[j] = zero[k] ? 0u : pack_pair<kBf16>(x[4 * (2 * j + u) + 2 * k], x[4 * (2 * j + u) + 2 * k + 1]);
-                        quad_transpose(y, lane);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) w[4 * u + j] = y[j];
-                    }
-                    if (mine[k]) {
-                        char* p = at[k] + cb * 128 + (lane & 3) * 32;
-                        if (a.wide_out) {
-                            store_32b(p, w);
-                        } else {
-                            reinterpret_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                            reinterpret_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
-                    }
-                }
+                for (int i = 0; i < 4; ++i)
+                    reinterpret_cast<uint4*>(dst + q * 64)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
             }
         }
     }
@@ -1383,7 +1325,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
             y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
             y.y = none ? 0u : pack_pair<kBf16>(acc.z * inv, acc.w * inv);
             *reinterpret_cast<uint2*>(a.out + t * a.o_st + h * a.o_sh + col) = y;
-            if (a.lse && col == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (top - kBias + log2f(sum)) * kLn2;
+            if (a.lse && col == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (top - kBias + __log2f(sum)) * kLn2;
         }
         if (share) __syncthreads();   // (the shared arrays are free for the next task)
     }
