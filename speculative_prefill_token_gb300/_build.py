@@ -1,7 +1,8 @@
-"""In-tree build of libspecprefill.so for sm_103a (nvcc, no cmake).
+"""In-tree build of libspecprefill.so for sm_103a (nvcc, no cmake) and of the
+torch side of its paged operators (g++ against torch's headers).
 
-Translation units compile in parallel; the shared library lands next to
-this file. Rebuilds only when a source or header is newer than the library.
+Translation units compile in parallel; both shared objects land next to
+this file. Rebuilds only when a source or header is newer than they are.
 """
 
 import os
@@ -15,6 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecprefill.so")
+TORCH_LIB = os.path.join(HERE, "_paged_torch.so")
+TORCH_SOURCE = "sp_paged_torch.cpp"
 SOURCES = ["sp_api.cu", "sp_stages.cu", "sp_logits_tc.cu", "sp_logits_simt.cu", "sp_noalloc.cu", "sp_post.cu",
            "sp_rows.cu", "sp_head_pool.cu", "sp_cache.cu", "sp_attn.cu", "sp_paged_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -34,9 +37,9 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(TORCH_LIB):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
@@ -56,8 +59,28 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {src}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_torch_side():
+        import sysconfig
+
+        import torch
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.isabs(nvcc) else "/usr/local/cuda"
+        obj = os.path.join(BUILD, TORCH_SOURCE.replace(".cpp", ".o"))
+        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE, "-I", os.path.join(root, "include"),
+               "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               "-I", sysconfig.get_paths()["include"], "-I", os.path.join(cuda, "include"),
+               "-c", os.path.join(CSRC, TORCH_SOURCE), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if verbose or r.returncode != 0:
+            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on {TORCH_SOURCE}")
+        return obj, os.path.join(root, "lib")
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        torch_side = ex.submit(compile_torch_side)
         objs = list(ex.map(compile_one, SOURCES))
+        torch_obj, torch_libs = torch_side.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -65,6 +88,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    # (the library is found beside it, torch's libraries are loaded already)
+    tmp = TORCH_LIB + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, torch_obj, "-L", HERE, "-l:libspecprefill.so", "-L", torch_libs, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        raise RuntimeError("link of the torch side failed")
+    os.replace(tmp, TORCH_LIB)
     return LIB
 
 

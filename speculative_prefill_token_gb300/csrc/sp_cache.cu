@@ -46,89 +46,119 @@ struct TabArgs {
     int32_t* n_left;
     int32_t* status;
     int B, bs, table_stride, cap, free_cap, pool_blocks;
+    int shift;   // log2(bs), or -1
 };
 
 __device__ __forceinline__ void raise_status(int32_t* status, int code) {
     if (status) atomicMax(status, code);
 }
 
+// x / d for x < 2^31: a shift where d is a power of two, as block sizes mostly are.
+__device__ __forceinline__ uint32_t blocks_below(const TabArgs& a, uint32_t x) {
+    return a.shift >= 0 ? x >> a.shift : x / static_cast<uint32_t>(a.bs);
+}
+
+__device__ __forceinline__ uint32_t blocks_for(const TabArgs& a, uint32_t tokens) {
+    const uint32_t full = blocks_below(a, tokens);
+    return full + (tokens - full * a.bs != 0);
+}
+
+// Last request b in [lo, hi) with off[b] <= t.
+__device__ __forceinline__ int request_of(const int32_t* off, int lo, int hi, int t) {
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= t) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
 __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs a) {
     extern __shared__ int32_t tab_smem[];
     int32_t* off = tab_smem;             // [B + 1] token offsets
-    int32_t* pre = tab_smem + a.B + 1;   // [B] blocks taken by earlier requests
+    int32_t* ctx = off + a.B + 1;        // [B] cached tokens
+    int32_t* pre = ctx + a.B;            // [B] blocks taken by earlier requests
     __shared__ int64_t warp_sum[kTabThreads / 32];
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    // each thread sums a contiguous run of requests
-    const int per = (a.B + kTabThreads - 1) / kTabThreads;
-    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    bool ok = true;
-    int64_t mine = 0;
-    if (tid == 0) {
-        if (a.new_off[0] != 0) ok = false;
-        off[a.B] = a.new_off[a.B];
+    for (int i = tid; i <= a.B; i += kTabThreads) {
+        off[i] = a.new_off[i];
+        if (i < a.B) ctx[i] = a.ctx_len[i];
     }
+    const int64_t n_free = *a.n_free;
+    __syncthreads();
+    // each thread takes a run of requests, of odd length (no bank conflicts)
+    const int per = (a.B + kTabThreads - 1) / kTabThreads | 1;
+    const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
+    bool ok = n_free >= 0 && n_free <= a.free_cap && off[0] == 0;
+    int64_t mine = 0;
     for (int b = b0; b < b1; ++b) {
-        const int64_t lo = a.new_off[b], hi = a.new_off[b + 1], ctx = a.ctx_len[b];
-        if (hi < lo || hi > a.cap || ctx < 0) ok = false;
-        const int64_t held = (ctx + a.bs - 1) / a.bs, need = (ctx + hi - lo + a.bs - 1) / a.bs;
-        if (need > a.table_stride || ctx + hi - lo > INT32_MAX) ok = false;
-        off[b] = static_cast<int32_t>(lo);
-        mine += need - held;
+        const int lo = off[b], hi = off[b + 1], c = ctx[b];
+        const int64_t all = static_cast<int64_t>(c) + hi - lo;
+        if (hi < lo || hi > a.cap || c < 0 || all > INT32_MAX) {
+            ok = false;
+            break;
+        }
+        const uint32_t need = blocks_for(a, static_cast<uint32_t>(all));
+        if (need > static_cast<uint32_t>(a.table_stride)) ok = false;
+        mine += need - blocks_for(a, c);
     }
     int64_t incl = mine;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += v;
     }
     if (lane == 31) warp_sum[warp] = incl;
     ok = __syncthreads_and(ok);
-    int64_t before = 0, total = 0;
-    for (int w = 0; w < kTabThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
+    int64_t sum = lane < kTabThreads / 32 ? warp_sum[lane] : 0;
+    const int64_t own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += v;
     }
-    const int64_t n_free = *a.n_free;
-    if (n_free < 0 || n_free > a.free_cap) ok = false;
-    const bool full = ok && total > n_free;   // (the same on every thread)
-    const bool go = ok && !full;
+    const int64_t total = __shfl_sync(0xffffffffu, sum, 31);
+    const int64_t before = __shfl_sync(0xffffffffu, sum - own, warp);
+    const bool go = ok && total <= n_free;   // (the same on every thread)
     if (go) {
-        int64_t run = before + incl - mine;
+        int run = static_cast<int>(before + incl - mine);
         for (int b = b0; b < b1; ++b) {
-            const int64_t ctx = a.ctx_len[b], n = a.new_off[b + 1] - off[b];
-            pre[b] = static_cast<int32_t>(run);
-            run += (ctx + n + a.bs - 1) / a.bs - (ctx + a.bs - 1) / a.bs;
+            pre[b] = run;
+            run += blocks_for(a, ctx[b] + (off[b + 1] - off[b])) - blocks_for(a, ctx[b]);
         }
     }
     if (blockIdx.x == 0 && tid == 0) {
         *a.n_left = static_cast<int32_t>(go ? n_free - total : n_free);
-        if (full) raise_status(a.status, SP_ERR_CAPACITY);
         if (!ok) raise_status(a.status, SP_ERR_DEVICE);
+        else if (!go) raise_status(a.status, SP_ERR_CAPACITY);
     }
     __syncthreads();
-    const int step = gridDim.x * kTabThreads, first = blockIdx.x * kTabThreads + tid;
-    for (int b = first; b < a.B; b += step)
-        a.kv_len[b] = go ? a.ctx_len[b] + (a.new_off[b + 1] - off[b]) : 0;
-    const int n_new = off[a.B];
-    for (int64_t t = first; t < a.cap; t += step) {
+    for (int b = blockIdx.x * kTabThreads + tid; b < a.B; b += gridDim.x * kTabThreads)
+        a.kv_len[b] = go ? ctx[b] + (off[b + 1] - off[b]) : 0;
+    // slots of this CTA's run of tokens
+    const int64_t per_cta = (static_cast<int64_t>(a.cap) + gridDim.x - 1) / gridDim.x;
+    const int t0 = static_cast<int>(min(per_cta * blockIdx.x, static_cast<int64_t>(a.cap)));
+    const int t1 = static_cast<int>(min(t0 + per_cta, static_cast<int64_t>(a.cap)));
+    const int n_new = go ? off[a.B] : 0;
+    const int live = min(t1, n_new);
+    int first = 0, last = 0;
+    if (t0 < live) {
+        first = request_of(off, 0, a.B, t0);
+        last = request_of(off, first, a.B, live - 1) + 1;
+    }
+    for (int t = t0 + tid; t < t1; t += kTabThreads) {
         int32_t slot = -1;
-        if (go && t < n_new) {
+        if (t < live) {
             // the request with off[b] <= t < off[b + 1]
-            int lo = 0, hi = a.B;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (off[mid] <= t) lo = mid; else hi = mid;
-            }
-            const int32_t ctx = a.ctx_len[lo];
-            const int32_t p = ctx + static_cast<int32_t>(t - off[lo]);
-            const int32_t k = p / a.bs, r = p - k * a.bs;
-            const int32_t held = ctx / a.bs + (ctx % a.bs != 0);
-            int32_t* entry = a.table + static_cast<int64_t>(lo) * a.table_stride + k;
-            const int32_t id = k < held ? *entry : a.free_blocks[n_free - 1 - (pre[lo] + (k - held))];
+            const int b = request_of(off, first, last, t);
+            const uint32_t c = ctx[b], p = c + (t - off[b]);
+            const uint32_t k = blocks_below(a, p), r = p - k * a.bs, held = blocks_for(a, c);
+            int32_t* entry = a.table + static_cast<int64_t>(b) * a.table_stride + k;
+            const int32_t id = k < held ? *entry : a.free_blocks[n_free - 1 - (pre[b] + static_cast<int64_t>(k - held))];
             if (k >= held && r == 0) *entry = id;
             if (id < 0 || id >= a.pool_blocks) raise_status(a.status, SP_ERR_DEVICE);
-            else slot = id * a.bs + r;
+            else slot = id * a.bs + static_cast<int32_t>(r);
         }
         a.slot_map[t] = slot;
     }
@@ -281,7 +311,8 @@ cudaError_t launch_block_tables(const sp_block_shape* s, const int32_t* ctx_len,
     a.cap = s->n_tokens;
     a.free_cap = s->free_capacity;
     a.pool_blocks = s->pool_blocks;
-    const size_t smem = (2 * static_cast<size_t>(a.B) + 1) * 4;
+    a.shift = (a.bs & (a.bs - 1)) == 0 ? __builtin_ctz(a.bs) : -1;
+    const size_t smem = (3 * static_cast<size_t>(a.B) + 1) * 4;
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    static_cast<int>(smem));
