@@ -167,6 +167,9 @@ __global__ void __launch_bounds__(kTabThreads) block_tables_kernel(const TabArgs
 // ------------------------------------------------------------ rotate and store
 
 constexpr int kAppThreads = 256;
+// Resident CTAs of an SM and the grid's: one full wave (five per SM, a second
+// wave of a quarter: 112 us in place of 84).
+constexpr int kAppCtas = 4;
 
 struct AppArgs {
     const uint16_t* q;
@@ -221,7 +224,7 @@ __device__ __forceinline__ void rotate(uint4& a, uint4& b, const float (&c)[8], 
 }
 
 template <bool kBf16>
-__global__ void __launch_bounds__(kAppThreads) append_kv_kernel(const AppArgs a) {
+__global__ void __launch_bounds__(kAppThreads, kAppCtas) append_kv_kernel(const AppArgs a) {
     grid_dep_wait();
     grid_dep_launch();
     int64_t n = a.cap;
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kAppThreads) append_kv_kernel(const AppArgs a)
             }
         }
         const int h1 = min((group + 1) * a.heads_per, heads);
-#pragma unroll 4
+#pragma unroll 2
         for (int h = group * a.heads_per; h < h1; ++h) {
             const uint16_t* src;
             uint16_t* dst;
@@ -355,11 +358,13 @@ cudaError_t launch_append_kv(const sp_append_shape* s, const uint16_t* q, const 
     a.half = s->rotary_dim / 2;
     a.max_pos = s->max_pos;
     const int heads = a.hq + 2 * a.hk, pairs = a.d / 16, sms = device_sms();
-    // four heads a thread once that still fills the GPU, else one
-    a.heads_per = static_cast<int64_t>(a.cap) * pairs * heads >= int64_t(4) * 2048 * sms ? 4 : 1;
+    // two heads a thread once that still fills the GPU (39,322 tokens of 16 + 4
+    // heads of 128: one 101 us, two 84, four 92), else one, so that a decode
+    // step's few rows are all in flight at once
+    a.heads_per = static_cast<int64_t>(a.cap) * pairs * heads >= int64_t(2) * kAppThreads * kAppCtas * sms ? 2 : 1;
     a.groups = (heads + a.heads_per - 1) / a.heads_per;
     int64_t grid = (static_cast<int64_t>(a.cap) * pairs * a.groups + kAppThreads - 1) / kAppThreads;
-    if (grid > int64_t(8) * sms) grid = int64_t(8) * sms;
+    if (grid > int64_t(kAppCtas) * sms) grid = int64_t(kAppCtas) * sms;
     auto kern = s->dtype == SP_DTYPE_BF16 ? append_kv_kernel<true> : append_kv_kernel<false>;
     return launch_k(kern, static_cast<unsigned>(grid), kAppThreads, 0, st, a);
 }
