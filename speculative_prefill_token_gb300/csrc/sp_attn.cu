@@ -32,7 +32,8 @@
 //   warp 8     K and V boxes by TMA (lane j issues box j of a slot)
 //   warp 9     tcgen05.mma issuer and TMEM owner
 //   warp 10    query tiles by TMA
-//   warp 11    of CTA 0: the list of cut items for the join
+//   warp 11    looks for infinities and NaN among values that some rows of an
+//              item are masked from; CTA 0: the list of cut items for the join
 // Two streams keep the tensor cores busy while the other stream's softmax
 // runs: with two query tiles, one tile each; with one (decode steps, short
 // chunks), even and odd key tiles, with an accumulator each for d <= 128
@@ -111,6 +112,9 @@ struct AttnArgs {
     const int32_t* q_off;
     const int32_t* kv_len;
     const int32_t* table;
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
     uint16_t* out;
     float* lse;
     int32_t* status;
@@ -122,7 +126,7 @@ struct AttnArgs {
     Job* jobs;          // [grid]
     float* part_o;      // [grid * 2][tiles][128][d]
     float2* part_ml;    // [grid * 2][tiles][128] (reference, sum)
-    int64_t o_st, o_sh, pool_tokens, spin;
+    int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh, pool_tokens, spin;
     int B, hk, G, tq, bs, table_stride, cap, causal, window, grid;
     int wide_out;        // 32-byte stores of out are aligned
     int local_plan;      // every CTA lays out the batch itself
@@ -473,7 +477,10 @@ struct Smem {
     static constexpr uint32_t drain = statfull + 16;
     static constexpr uint32_t tmem = drain + 8;
     static constexpr uint32_t abort = tmem + 8;
-    static constexpr uint32_t total = abort + 8;
+    static constexpr uint32_t odd = abort + 4;        // [2] a value of the segment is no number
+    static constexpr uint32_t checked = odd + 12;     // [2] that flag is written
+    static constexpr uint32_t seen = checked + 16;    // [2] and read
+    static constexpr uint32_t total = seen + 16;
 };
 
 static_assert(Smem<64>::total <= 232448 && Smem<128>::total <= 232448 && Smem<256>::total <= 232448,
@@ -612,6 +619,78 @@ __device__ __forceinline__ void load_queries(const Ctx& c, const AttnArgs& a, co
         ++n;
     }
     if (n) mbar_wait_spin(c.base + L::qfull, (n - 1) & 1, kDrainSpin);
+}
+
+// ------------------------------------------------------------ values
+
+// The values of keys that some rows of an item see and others are masked from
+// are looked at: a zero weight times infinity or NaN is NaN, and a tile's
+// product takes all its rows through all its keys. (Keys that no row sees are
+// never loaded, or zeroed.)
+__device__ __forceinline__ bool looked_at(const AttnArgs& a, const Segment& s) {
+    return a.causal && s.n > 0 && s.it.ntok > 1;
+}
+
+// Adds 0 * x of the eight values of x to acc: not zero once one is infinite or NaN.
+template <bool kBf16>
+__device__ __forceinline__ void add_zero_times(uint32_t& acc, uint4 x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (kBf16)
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0u));
+        else
+            asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0u));
+    }
+}
+
+// By one warp, from global memory (some 100 rows per item): one flag per
+// segment, after which the softmax warps take its rows again one by one. It
+// costs a prefill at d = 256 4 % of its time; by the softmax warps, from the
+// ring, it was 20 %.
+template <int D, bool kBf16>
+__device__ __forceinline__ void check_values(const Ctx& c, const AttnArgs& a, int items, int lane) {
+    using L = Smem<D>;
+    constexpr unsigned kAll = 0xffffffffu;
+    constexpr int kLanes = D / 8, kStep = 32 / kLanes;   // lanes of a row, rows at a time
+    uint32_t n = 0;
+    Walk w(c.range, items);
+    Segment s;
+    while (w.next(a, s)) {
+        if (!looked_at(a, s)) continue;
+        if (!__all_sync(kAll, c.wait(L::seen + 8 * (n & 1), (n >> 1 & 1) ^ 1))) return;
+        const int k0 = s.first * kKeys, k1 = (s.first + s.n) * kKeys;
+        const int last = s.it.pos0 + s.it.ntok - 1;
+        uint32_t acc = 0;
+        // keys behind the first row's position, keys before the last row's window
+#pragma unroll 1
+        for (int part = 0; part < (a.window > 0 ? 2 : 1); ++part) {
+            const int lo = max(part ? s.it.klo : max(s.it.klo, s.it.pos0 + 1), k0);
+            const int hi = min(part ? min(s.it.khi, last - a.window + 1) : s.it.khi, k1);
+            // block by block, a lane for each 16 bytes of a row
+            const int per = a.bs;
+            int blk = lo / per, in = lo - blk * per;
+            const int32_t* tab = a.table + static_cast<int64_t>(s.it.b) * a.table_stride;
+            for (int j = lo; j < hi; ++blk, in = 0) {
+                const int id = tab[blk];
+                int64_t row = static_cast<int64_t>(id) * per;
+                if (id < 0 || row + per > a.pool_tokens) row = 0;
+                const int n = min(per - in, hi - j);
+                const uint16_t* p = a.v + (row + in + lane / kLanes) * a.v_st + s.g * a.v_sh + lane % kLanes * 8;
+                const int64_t step = kStep * a.v_st;
+#pragma unroll 4
+                for (int i = lane / kLanes; i < n; i += kStep, p += step) add_zero_times<kBf16>(acc, *reinterpret_cast<const uint4*>(p));
+                j += n;
+            }
+        }
+        const bool odd = __any_sync(kAll, (acc & 0x7fff7fffu) != 0);
+        if (lane == 0) {
+            reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[n & 1] = odd;
+            mbar_arrive(c.base + L::checked + 8 * (n & 1));
+        }
+        __syncwarp();
+        ++n;
+    }
 }
 
 // ------------------------------------------------------------ MMA
@@ -901,6 +980,78 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
     }
 }
 
+// Rows [row0, min(row0 + 32, rows)) of query tile `tok0` tokens into the item,
+// over the segment's keys.
+struct RowsAgain {
+    Item it;
+    int g, first, n, tok0, row0, rows, part;   // part < 0: the whole item is here
+};
+
+// The same rows without the tensor cores, by one warp, a row at a time with
+// the head dimension over its lanes: for segments in which a row is masked from
+// a value that is infinite or NaN (its zero weight would make the product NaN).
+// Slow, and right for any input.
+template <int D, bool kBf16>
+__device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
+    constexpr int E = D / 32;
+    constexpr float kBias = weight_bias(kBf16);
+    const int lane = threadIdx.x & 31;
+    auto load = [&](const uint16_t* p, float (&x)[E]) {
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            if constexpr (kBf16) x[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+            else x[i] = __half2float(__ushort_as_half(p[i]));
+        }
+    };
+    for (int r = e.row0; r < min(e.rows, e.row0 + 32); ++r) {
+        const int tok = r / a.G, h = e.g * a.G + r - tok * a.G;
+        const int64_t t = e.it.tok0 + e.tok0 + tok;
+        const int pos = e.it.pos0 + e.tok0 + tok;
+        int hi = min(a.causal ? min(e.it.khi, pos + 1) : e.it.khi, (e.first + e.n) * kKeys);
+        int lo = max(a.window > 0 ? max(pos - a.window + 1, 0) : 0, e.first * kKeys);
+        float q[E], acc[E];
+        load(a.q + t * a.q_st + h * a.q_sh + lane * E, q);
+#pragma unroll
+        for (int i = 0; i < E; ++i) acc[i] = 0.0f;
+        float m = -INFINITY, l = 0.0f;
+        for (int j = lo; j < hi; ++j) {
+            const int blk = j / a.bs;
+            const int id = a.table[static_cast<int64_t>(e.it.b) * a.table_stride + blk];
+            int64_t row = static_cast<int64_t>(id) * a.bs;
+            row = id < 0 || row + a.bs > a.pool_tokens ? 0 : row + j - blk * a.bs;
+            float x[E], y = 0.0f;
+            load(a.k + row * a.k_st + e.g * a.k_sh + lane * E, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i) y += q[i] * x[i];
+#pragma unroll
+            for (int o = 16; o; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+            y *= a.scale2;
+            const float mn = fmaxf(m, y), base = mn == -INFINITY ? 0.0f : mn;
+            const float f = mn == m ? 1.0f : exp2_ftz(m - mn), p = exp2_ftz(y - base + kBias);
+            l = l * f + p;
+            load(a.v + row * a.v_st + e.g * a.v_sh + lane * E, x);
+#pragma unroll
+            for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + p * x[i];
+            m = mn;
+        }
+        if (e.part >= 0) {
+            float* o = a.part_o + static_cast<int64_t>(e.part + r) * D + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) o[i] = acc[i];
+            if (lane == 0) a.part_ml[e.part + r] = make_float2(m, l);
+        } else {
+            const bool none = l == 0.0f;
+            uint16_t* o = a.out + t * a.o_st + h * a.o_sh + lane * E;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const uint32_t w = none ? 0u : pack_pair<kBf16>(acc[i] / l, 0.0f);
+                o[i] = static_cast<uint16_t>(w & 0xffffu);
+            }
+            if (a.lse && lane == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (m - kBias + __log2f(l)) * kLn2;
+        }
+    }
+}
+
 // One warpgroup (index wg) of softmax threads over the CTA's segments.
 template <int D, bool kBf16>
 __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int items, int wg) {
@@ -916,6 +1067,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
     int ring = 0;                // slot of the segment's first K tile
     uint32_t turn = 0;           // and its turn
     bool ok = true;
+    uint32_t checks = 0;         // segments whose values are looked at so far
     Walk w(c.range, items);
     Segment s;
     while (w.next(a, s)) {
@@ -1075,6 +1227,14 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
         }
         cnt0 += buf0;
         cnt1 += buf1;
+        bool again = false;
+        if (looked_at(a, s)) {
+            if (ok) ok = __all_sync(kAll, c.wait(L::checked + 8 * (checks & 1), checks >> 1 & 1));
+            again = reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[checks & 1] != 0;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.base + L::seen + 8 * (checks & 1));
+            ++checks;
+        }
         if (two || wg == 0 || D > 128) {   // this warpgroup writes rows
             const int o = two ? wg : 0;
             float f0 = 1.0f, f1 = 0.0f;
@@ -1102,7 +1262,20 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             }
             constexpr int kCols = D > 128 ? D / 2 : D;    // columns of this warpgroup
             const int col0 = D > 128 ? wg * kCols : 0;
-            if (ok && live) {
+            if (ok && live && again) {
+                if (D <= 128 || wg == 0) {
+                    RowsAgain e;
+                    e.it = s.it;
+                    e.g = s.g;
+                    e.first = s.first;
+                    e.n = s.n;
+                    e.tok0 = tile * a.tq;
+                    e.row0 = warp * 32;
+                    e.rows = rows;
+                    e.part = s.split ? ((static_cast<int>(blockIdx.x) * 2 + (s.head ? 0 : 1)) * L::kTiles + tile) * kRows : -1;
+                    rows_again<D, kBf16>(a, e);
+                }
+            } else if (ok && live) {
                 RowEnd e;
                 e.ot = tmem + lanes + 2 * kKeys + o * D + col0;
                 e.rows = rows - warp * 32;
@@ -1164,6 +1337,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             mbar_init(c.base + L::odone + 8 * i, 1);
             mbar_init(c.base + L::oempty + 8 * i, D > 128 ? 8 : 4);
             mbar_init(c.base + L::statfull + 8 * i, 4);
+            mbar_init(c.base + L::checked + 8 * i, 1);
+            mbar_init(c.base + L::seen + 8 * i, 8);
         }
         mbar_init(c.base + L::drain, 1);
         *c.abort_flag = 0;
@@ -1214,7 +1389,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             else if (warp == kMmaWarp) issue_mma<D, kBf16>(c, a, tmem, items);
             else if (warp == kQWarp && lane == 0) load_queries<D>(c, a, &mq, items);
         }
-        if (warp == kListWarp && blockIdx.x == 0 && aligned) list_cuts(a, L::kChunks, lane);
+        if (warp == kListWarp) {
+            if (work) check_values<D, kBf16>(c, a, items, lane);
+            if (blockIdx.x == 0 && aligned) list_cuts(a, L::kChunks, lane);
+        }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         if (work) softmax_rows<D, kBf16>(c, a, tmem, items, warp >> 2);
@@ -1448,6 +1626,9 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.q_off = q_off;
     a.kv_len = kv_len;
     a.table = table;
+    a.q = q;
+    a.k = k_pool;
+    a.v = v_pool;
     a.out = out;
     a.lse = lse;
     a.status = &ws_ptr<WsHeader>(ws, 0)->status;
@@ -1459,6 +1640,9 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.jobs = ws_ptr<Job>(ws, l.jobs);
     a.part_o = ws_ptr<float>(ws, l.o);
     a.part_ml = ws_ptr<float2>(ws, l.ml);
+    a.q_st = s->q_stride_token, a.q_sh = s->q_stride_head;
+    a.k_st = s->k_stride_token, a.k_sh = s->k_stride_head;
+    a.v_st = s->v_stride_token, a.v_sh = s->v_stride_head;
     a.o_st = s->o_stride_token, a.o_sh = s->o_stride_head;
     a.pool_tokens = s->pool_tokens;
     a.spin = p->spin_limit > 0 ? p->spin_limit : kDefaultSpin;

@@ -212,3 +212,53 @@ def test_repeated_calls_give_the_same_bits(cuda_lib):
         b = _run(sp, case)
         n = 341
         assert torch.equal(a[0][:n], b[0][:n]) and torch.equal(a[1][:n], b[1][:n])
+
+
+@pytest.mark.parametrize("window", [0, 40])
+@pytest.mark.parametrize("d,hq,hk,dtype", [(64, 4, 2, "fp16"), (128, 4, 1, "bf16"), (256, 2, 1, "bf16"), (128, 1, 1, "bf16")])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_a_row_masked_from_a_bad_value_is_not_touched_by_it(cuda_lib, d, hq, hk, dtype, value, window):
+    """Infinity or NaN in two columns of one cached value, among the new tokens
+    of a request with 400 of them: rows that see the token have no number in
+    those columns, every other row and column is as without it. The same for a
+    request long enough to be cut between CTAs."""
+    import torch
+    sp = cuda_lib
+    ctx, new, bs = [30, 3000], [400, 130], 16
+    case = paged_case(60 + d, ctx, new, hq, hk, d, bs, dtype)
+    kv, table = host(case["kv_len"]), host(case["table"])
+    bad = [30 + 211, 3000 + 57]   # cache indices
+    cols = [3, d - 1]
+    for b, j in enumerate(bad):
+        case["v_pool"][int(table[b, j // bs]), j % bs][:, cols] = value
+    # the oracle's result without the bad columns' contribution of those tokens
+    clean = case["v_pool"].clone()
+    for b, j in enumerate(bad):
+        clean[int(table[b, j // bs]), j % bs][:, cols] = 0
+    ref = paged_oracle.paged_attention(host(case["q"]), host(case["q_off"]), kv, table, host(case["k_pool"]),
+                                       host(clean), window=window)
+    out, lse = _run(sp, case, window=window)
+    o = host(out)
+    sees = np.zeros(o.shape[0], bool)
+    for b, j in enumerate(bad):
+        pos = kv[b] - new[b] + np.arange(new[b])
+        lo = sum(new[:b])
+        sees[lo:lo + new[b]] = (pos >= j) & ((window == 0) | (pos < j + window))
+    assert sees.any() and not sees.all()
+    assert not np.isfinite(o[sees][:, :, cols]).any()
+    fixed = out.clone()
+    mask = torch.zeros(o.shape, dtype=torch.bool)
+    mask[torch.from_numpy(np.flatnonzero(sees))[:, None], :, torch.tensor(cols)] = True
+    fixed[mask.cuda()] = torch.from_numpy(ref[0])[mask].to(fixed.dtype).cuda()
+    check_attention(fixed, lse, ref, kv, d, dtype, sum(new))
+
+
+def test_keys_that_are_no_numbers_reach_only_the_rows_that_see_them(cuda_lib):
+    sp = cuda_lib
+    case = paged_case(70, [10], [300], 4, 2, 128, 32, "bf16")
+    table = host(case["table"])
+    j = 10 + 140
+    case["k_pool"][int(table[0, j // 32]), j % 32] = float("nan")
+    out, lse = _run(sp, case)
+    o = host(out)
+    assert np.isfinite(o[:140]).all() and np.isnan(o[140:]).all() and np.isnan(host(lse)[140:]).all()
