@@ -827,12 +827,15 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
         poll(L::qfull, nq, 1);
         if (!ok) break;
         ++nq;
-        if (!keys_at(at)) break;
+        // first logits: both query tiles with K0, or K0 and K1
+        for (int i = 0; i < (two || n > 1 ? 2 : 1); ++i) {
+            if ((i == 0 || !two) && !keys_at(at)) break;
+            qk(at, two ? i : 0, i, !two || i == 1);
+            if (!two || i == 1) at = ahead(at, P);
+        }
+        if (n <= (two ? 1 : 2)) queries_read();
         if (two) {
-            qk(at, 0, 0, false);
-            qk(at, 1, 1, true);
-            if (n == 1) queries_read();
-            at = ahead(at, P);
+            // ring: V0 K1 V1 K2 ..., each tile for both streams in turn
             for (int j = 0; j < n && ok; ++j) {
                 step(at, 0, 0, 0, j == 0, j + 1 < n, true, false);
                 if (!ok) break;
@@ -841,24 +844,12 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
                 at = ahead(ahead(at, P), j + 1 < n ? P : 0);
             }
         } else {
-            // ring: K0 K1 V0 K2 V1 K3 ...
-            qk(at, 0, 0, true);
-            at = ahead(at, P);
-            if (n > 1) {
-                if (!keys_at(at)) break;
-                qk(at, 0, 1, true);
-                at = ahead(at, P);
-            }
-            if (n <= 2) queries_read();
-            for (int j = 0; j < n && ok; j += 2) {
-                step(at, 0, 0, 0, j == 0, j + 2 < n, true, true);
+            // ring: V0 K2 V1 K3 ..., for one stream each
+            for (int j = 0; j < n && ok; ++j) {
+                const int sb = j & 1;
+                step(at, 0, sb, D <= 128 ? sb : 0, D <= 128 ? j < 2 : j == 0, j + 2 < n, true, true);
                 if (j + 3 == n) queries_read();
                 at = ahead(ahead(at, P), j + 2 < n ? P : 0);
-                if (j + 1 < n && ok) {
-                    step(at, 0, 1, D <= 128 ? 1 : 0, D <= 128 && j == 0, j + 3 < n, true, true);
-                    if (j + 4 == n) queries_read();
-                    at = ahead(ahead(at, P), j + 3 < n ? P : 0);
-                }
             }
         }
     }
