@@ -522,7 +522,7 @@ typedef struct sp_paged_shape {
     int32_t dtype;         /* SP_DTYPE_BF16 or SP_DTYPE_F16: q, pools and out */
     int32_t block_size;    /* 8, 16, 32, 64 or a multiple of 128 */
     int32_t table_stride;  /* >= 1 table entries of a request */
-    int32_t n_tokens;      /* >= 1 rows of q, out and lse; q_off[B] may be less */
+    int32_t n_tokens;      /* 1 to 2^30 rows of q, out and lse; q_off[B] may be less */
     int64_t pool_tokens;   /* rows of each pool, at most 2^31 - 1 */
     int64_t q_stride_token, q_stride_head, o_stride_token, o_stride_head;
     int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
@@ -560,11 +560,14 @@ int sp_paged_attention_workspace(const sp_paged_shape* shape, size_t* bytes);
  *   written.
  * - Logits, softmax statistics and sums are held in 32 bits; the weights are
  *   rounded to the tensors' type for the product with the values.
- * - Cache rows at or behind kv_len[b], and blocks that no row of the request
- *   can see, may hold anything, infinities and NaN included. Table entries
- *   behind the request's last block are not read.
- * - A bad q_off or kv_len (out of range, or more tokens than a table row
- *   holds) sets the device status SP_ERR_DEVICE and nothing is computed; a
+ * - Cache rows at or behind kv_len[b], and rows that a query is masked from,
+ *   may hold anything, infinities and NaN included: they do not reach its
+ *   result. (Where a value of the new tokens, or at the edge of the window, is
+ *   no number, the queries around it take a slow path: 0.1 s and more for a
+ *   context of 40,000 tokens.) Table entries behind the request's last block
+ *   are not read.
+ * - A bad q_off or kv_len (out of range, over 2^30, or more tokens than a
+ *   table row holds) sets the device status SP_ERR_DEVICE and nothing is computed; a
  *   block id outside the pool sets it and reads pool row 0 instead.
  * Strides times 2 bytes are multiples of 16 and base pointers 16-byte aligned
  * (SP_ERR_UNSUPPORTED and SP_ERR_INVALID_ARG otherwise). */

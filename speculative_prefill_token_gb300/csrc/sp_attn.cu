@@ -143,9 +143,17 @@ constexpr int kLocalItems = 384;   // items and requests of a plan made by every
 // filling the pipeline and writing the rows. (Without it the CTAs with the
 // shortest items of a prompt finish last.)
 constexpr int kItemCost = 2;
-constexpr int kJoinFew = 4;        // parts that one group of threads walks by itself
+constexpr int kJoinFew = 4;        // parts held in registers at once
 constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 4;     // of an SM, all resident
 constexpr int kJoinGroups = kJoinThreads / 16;   // of 16 threads: 64 columns of a row
+
+// Whether the groups of a join block share a row and its parts, or take a row
+// each: with few rows the parts' latency counts, with many (of some parts) the
+// blocks. (250 rows of 5 parts each in 30 items, a row at a time: 15 us.)
+__device__ __forceinline__ bool join_shares(int parts, int row_chunks) {
+    return parts > 16 || (parts > kJoinFew && row_chunks <= 128);
+}
 
 template <typename T>
 __device__ __forceinline__ T range_start(T total, int ctas, int c) { return total * c / ctas; }
@@ -221,8 +229,9 @@ __device__ __forceinline__ Start make_start(const AttnArgs& a, const T* pre, int
     return s;
 }
 
+// (cache indices stay below 2^30, so that no sum of two of them leaves 31 bits)
 __device__ __forceinline__ bool bad_request(const AttnArgs& a, int64_t lo, int64_t hi, int64_t kv) {
-    return hi < lo || hi > a.cap || kv < 0 || (kv + a.bs - 1) / a.bs > a.table_stride;
+    return hi < lo || hi > a.cap || kv < 0 || kv > kMaxCached || (kv + a.bs - 1) / a.bs > a.table_stride;
 }
 
 // Lays out a batch of any size, by one block of its own: items with their
@@ -371,7 +380,7 @@ __device__ __forceinline__ void list_cuts(const AttnArgs& a, int chunks, int lan
                 j.tok0 = __ldcg(&a.items[s.x].tok0);
                 j.ntok = __ldcg(&a.items[s.x].ntok);
                 mine = j.ntok * a.G * chunks;
-                if (j.parts <= kJoinFew) mine = (mine + kJoinGroups - 1) / kJoinGroups;
+                if (!join_shares(j.parts, mine)) mine = (mine + kJoinGroups - 1) / kJoinGroups;
             }
         }
         int incl = mine;
@@ -1403,7 +1412,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // groups of a block share (the L2 latency of 76 parts in turn would be the
 // kernel's time), or of 16 rows with few, each walked by a group.
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(const AttnArgs a) {
     using L = Smem<D>;
     constexpr float kBias = weight_bias(kBf16);
     __shared__ Job job_s[kMaxCtas];
@@ -1425,8 +1434,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
         }
         const Job job = job_s[lo];
         const int parts = job.parts;
-        const bool share = parts > kJoinFew;
         const int rows0 = min(job.ntok, a.tq) * a.G, rows = job.ntok * a.G;   // of the first tile, of both
+        const bool share = join_shares(parts, rows * L::kChunks);
         const int unit = share ? task - job.task0 : (task - job.task0) * kJoinGroups + group;
         const int r = unit / L::kChunks, col = unit % L::kChunks * 64 + vec * 4;
         const bool mine = r < rows;
@@ -1469,20 +1478,27 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const AttnArgs 
                 }
             }
         } else if (mine) {
-            float2 ml[kJoinFew];
-            float4 x[kJoinFew];
+            if (parts <= kJoinFew) {
+                float2 ml[kJoinFew];
+                float4 x[kJoinFew];
 #pragma unroll
-            for (int p = 0; p < kJoinFew; ++p)
-                if (p < parts) {
-                    ml[p] = __ldcg(a.part_ml + at(p));
-                    x[p] = load(p);
-                }
+                for (int p = 0; p < kJoinFew; ++p)
+                    if (p < parts) {
+                        ml[p] = __ldcg(a.part_ml + at(p));
+                        x[p] = load(p);
+                    }
 #pragma unroll
-            for (int p = 0; p < kJoinFew; ++p)
-                if (p < parts) top = fmaxf(top, ml[p].x);
+                for (int p = 0; p < kJoinFew; ++p)
+                    if (p < parts) top = fmaxf(top, ml[p].x);
 #pragma unroll
-            for (int p = 0; p < kJoinFew; ++p)
-                if (p < parts) add(ml[p], x[p]);
+                for (int p = 0; p < kJoinFew; ++p)
+                    if (p < parts) add(ml[p], x[p]);
+            } else {
+#pragma unroll 8
+                for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(a.part_ml + at(p)).x);
+#pragma unroll 8
+                for (int p = 0; p < parts; ++p) add(__ldcg(a.part_ml + at(p)), load(p));
+            }
         }
         if (mine && (!share || group == 0)) {
             const bool none = sum == 0.0f;
@@ -1592,7 +1608,7 @@ cudaError_t launch_d(const AttnArgs& a, bool bf16, const CUtensorMap& mq, const 
     const cudaError_t r = launch_k(kern, static_cast<unsigned>(a.grid), kAttnThreads, Smem<D>::total, st, mq, mk, mv, a);
     if (r != cudaSuccess) return r;
     return launch_k(bf16 ? attn_join_kernel<D, true> : attn_join_kernel<D, false>,
-                    static_cast<unsigned>(4 * a.grid), kJoinThreads, 0, st, a);
+                    static_cast<unsigned>(kJoinBlocks * a.grid), kJoinThreads, 0, st, a);
 }
 
 }  // namespace
@@ -1645,7 +1661,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.table_stride = s->table_stride;
     a.cap = s->n_tokens;
     a.causal = p->causal;
-    a.window = p->window;
+    a.window = p->window <= kMaxCached ? p->window : 0;   // (a longer one hides nothing)
     const int per = kKeys / slots_per_tile(d);
     const int hk = bs < kKeys ? bs : kKeys, hv = bs < per ? bs : per;
     a.hk_shift = __builtin_ctz(hk);

@@ -10,6 +10,7 @@
 
 namespace sp {
 
+constexpr int kMaxCached = 1 << 30;   // cached tokens of a request, and new tokens of an attention call
 constexpr int kMaxTableSeqs = 16384;  // requests whose scan fits a CTA's shared memory
 
 // Multiprocessors of the current device.

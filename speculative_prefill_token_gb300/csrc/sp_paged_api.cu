@@ -32,7 +32,8 @@ int check_paged(const sp_paged_shape* s) {
     if (s->n_q_heads % s->n_kv_heads != 0) return SP_ERR_INVALID_ARG;
     if (s->dtype != SP_DTYPE_BF16 && s->dtype != SP_DTYPE_F16) return SP_ERR_INVALID_ARG;
     if (s->head_dim != 64 && s->head_dim != 128 && s->head_dim != 256) return SP_ERR_UNSUPPORTED;
-    if (s->n_seqs > kMaxSeqs || s->n_q_heads / s->n_kv_heads > 128) return SP_ERR_UNSUPPORTED;
+    if (s->n_seqs > kMaxSeqs || s->n_q_heads / s->n_kv_heads > 128 || s->n_tokens > kMaxCached)
+        return SP_ERR_UNSUPPORTED;
     const int bs = s->block_size;
     if (!(bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs % 128 == 0)) return SP_ERR_UNSUPPORTED;
     if (s->pool_tokens < bs) return SP_ERR_INVALID_ARG;

@@ -262,3 +262,79 @@ def test_keys_that_are_no_numbers_reach_only_the_rows_that_see_them(cuda_lib):
     out, lse = _run(sp, case)
     o = host(out)
     assert np.isfinite(o[:140]).all() and np.isnan(o[140:]).all() and np.isnan(host(lse)[140:]).all()
+
+
+@pytest.mark.parametrize("bs,d", [(384, 128), (640, 64), (128, 256)])
+def test_blocks_of_several_tiles(cuda_lib, bs, d):
+    _check(cuda_lib, [1000, 3, 383], [5, 200, 2], 4, 2, d, bs, "bf16", seed=bs)
+
+
+def test_batches_of_thousands_of_requests_and_of_many_query_tiles(cuda_lib):
+    """More requests, and more query tiles, than a CTA lays out by itself."""
+    rng = np.random.default_rng(3)
+    new = (rng.random(3000) < 0.8).astype(int)
+    _check(cuda_lib, rng.integers(0, 40, 3000).tolist(), new.tolist(), 4, 2, 64, 16, "bf16", seed=31)
+    _check(cuda_lib, [5, 0, 90] * 150, [1, 3, 40] * 150, 8, 1, 128, 32, "fp16", seed=32)
+    _check(cuda_lib, [0], [7000], 64, 1, 64, 64, "bf16", seed=33, window=100)
+
+
+def test_no_new_tokens_and_no_cached_tokens(cuda_lib):
+    sp = cuda_lib
+    case = paged_case(5, [20, 0, 3], [0, 0, 0], 4, 2, 128, 16, "bf16", spare_rows=4)
+    out, lse = _run(sp, case)
+    assert (host(out) == 7.0).all() and (host(lse) == 7.0).all()
+
+
+def test_outputs_aligned_to_16_bytes_only(cuda_lib):
+    import torch
+    sp = cuda_lib
+    for d in (64, 128, 256):
+        case = paged_case(40 + d, [50, 700], [130, 3], 4, 2, d, 16, "bf16")
+        want, _ = _run(sp, case)
+        wide = torch.zeros(133, 4, d + 8, dtype=torch.bfloat16, device="cuda")
+        sp.paged_attention(case["q"], case["q_off"], case["kv_len"], case["table"], case["k_pool"], case["v_pool"],
+                           out=wide[:, :, 8:])
+        assert torch.equal(wide[:, :, 8:], want) and (wide[:, :, :8] == 0).all()
+
+
+def test_cache_rows_past_32_bit_offsets(cuda_lib):
+    """Pools of 2^31 elements and more, with the request's blocks at both ends;
+    the new tokens are stored there by append_kv."""
+    import torch
+    sp = cuda_lib
+    hk, d, bs = 8, 256, 64
+    blocks = 2 ** 31 // (hk * d * bs) + 40
+    assert blocks * bs * hk * d > 2 ** 31
+    pools = [torch.zeros(blocks, bs, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    ids = [blocks - 1, 0, blocks - 2, 1, blocks - 3]
+    n = 5 * bs - 7
+    rng = np.random.default_rng(9)
+    kv = [torch.from_numpy(rng.standard_normal((n, hk, d), dtype=np.float32)).cuda().bfloat16() for _ in range(2)]
+    slots = (np.asarray(ids)[:, None] * bs + np.arange(bs)).reshape(-1)[:n].astype(np.int32)
+    sp.append_kv(*kv, torch.from_numpy(slots).cuda(), *pools)
+    q = torch.from_numpy(rng.standard_normal((3, hk, d), dtype=np.float32)).cuda().bfloat16()
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    lse = torch.zeros(3, hk, device="cuda")
+    ws = sp.make_attention_workspace(q, 1, pools[0])
+    out = sp.paged_attention(q, i32(0, 3), i32(n), i32(*ids)[None], *pools, lse=lse, ws=ws)
+    assert sp.device_status(ws) == 0
+    small = [host(p[torch.tensor(ids, device="cuda")]) for p in pools]
+    ref = paged_oracle.paged_attention(host(q), [0, 3], [n], np.arange(5)[None], *small)
+    check_attention(out, lse, ref, [n], d, "bf16", 3)
+
+
+def test_waits_that_give_up_set_the_status_and_leave_the_workspace_usable(cuda_lib):
+    """With one poll for every wait the first one that has to wait gives up;
+    the call ends with SP_ERR_TIMEOUT and the next one is right."""
+    import torch
+    sp = cuda_lib
+    for d in (64, 128, 256):
+        case = paged_case(80 + d, [3000, 100], [1, 200], 4, 2, d, 16, "bf16")
+        want, _ = _run(sp, case)
+        ws = sp.make_attention_workspace(case["q"], 2, case["k_pool"])
+        out = torch.zeros_like(case["q"])
+        args = (case["q"], case["q_off"], case["kv_len"], case["table"], case["k_pool"], case["v_pool"])
+        sp.paged_attention(*args, out=out, ws=ws, spin_limit=1)
+        assert sp.device_status(ws) == 5
+        sp.paged_attention(*args, out=out, ws=ws)
+        assert sp.device_status(ws) == 0 and torch.equal(out, want)

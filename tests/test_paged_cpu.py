@@ -97,7 +97,7 @@ def test_paged_attention_refusals(lib):
                dict(q_stride_token=64), dict(k_stride_head=8), dict(block_size=512)):
         assert _attend(lib, kw) == 1, kw
         assert lib.sp_paged_attention_workspace(ctypes.byref(_paged(kw)), ctypes.byref(n)) == 1, kw
-    for kw in (dict(head_dim=96), dict(head_dim=512), dict(n_seqs=65537), dict(n_q_heads=258), dict(block_size=24),
+    for kw in (dict(head_dim=96), dict(head_dim=512), dict(n_seqs=65537), dict(n_q_heads=258), dict(n_tokens=(1 << 30) + 1), dict(block_size=24),
                dict(block_size=192), dict(block_size=4), dict(k_stride_token=260), dict(o_stride_head=132)):
         assert _attend(lib, kw) == 2, kw
     for kw in (dict(causal=2), dict(window=-1), dict(causal=0, window=4), dict(scale=-1.0), dict(scale=float("inf")),
