@@ -473,7 +473,7 @@ int sp_block_tables(const sp_block_shape* shape, const int32_t* ctx_len, const i
 typedef struct sp_append_shape {
     int32_t n_tokens;      /* >= 1 rows of q, k, v and slot_map */
     int32_t n_q_heads;     /* >= 1 with queries; ignored without */
-    int32_t n_kv_heads;    /* >= 1 */
+    int32_t n_kv_heads;    /* >= 1; queries, keys and values have at most 65536 heads together */
     int32_t head_dim;      /* a multiple of 16, at most 1024 */
     int32_t rotary_dim;    /* 0 (no rotation) or a multiple of 16, at most head_dim */
     int32_t max_pos;       /* rows of cos_sin (ignored when rotary_dim is 0) */
@@ -505,8 +505,9 @@ typedef struct sp_append_shape {
  * - status (device, one int32, nullable): raised to SP_ERR_DEVICE by a slot
  *   at or past pool_tokens (nothing is stored for the row) or a position
  *   outside [0, max_pos) (the row is skipped). Never lowered.
- * Base pointers are 16-byte aligned and strides multiples of 8
- * (SP_ERR_UNSUPPORTED otherwise). */
+ * Outputs may not overlap inputs (q_out = q aside) or one another; equal
+ * pointers are SP_ERR_INVALID_ARG. Base pointers are 16-byte aligned
+ * (SP_ERR_INVALID_ARG) and strides multiples of 8 (SP_ERR_UNSUPPORTED). */
 int sp_append_kv(const sp_append_shape* shape, const uint16_t* q, const uint16_t* k,
                  const uint16_t* v, const int32_t* slot_map, const int32_t* positions,
                  const float* cos_sin, const int32_t* n_new, uint16_t* q_out, uint16_t* k_pool,
@@ -516,7 +517,7 @@ int sp_append_kv(const sp_append_shape* shape, const uint16_t* q, const uint16_t
  * sp_paged_attention. */
 typedef struct sp_paged_shape {
     int32_t n_seqs;        /* 1 <= B <= 65536 requests */
-    int32_t n_q_heads;     /* Hq, Hq % Hk == 0, G = Hq / Hk <= 128 */
+    int32_t n_q_heads;     /* Hq <= 65536, Hq % Hk == 0, G = Hq / Hk <= 128 */
     int32_t n_kv_heads;    /* Hk >= 1 */
     int32_t head_dim;      /* d in {64, 128, 256} */
     int32_t dtype;         /* SP_DTYPE_BF16 or SP_DTYPE_F16: q, pools and out */
@@ -569,6 +570,7 @@ int sp_paged_attention_workspace(const sp_paged_shape* shape, size_t* bytes);
  * - A bad q_off or kv_len (out of range, over 2^30, or more tokens than a
  *   table row holds) sets the device status SP_ERR_DEVICE and nothing is computed; a
  *   block id outside the pool sets it and reads pool row 0 instead.
+ * out and lse may not overlap the inputs (equal pointers: SP_ERR_INVALID_ARG).
  * Strides times 2 bytes are multiples of 16 and base pointers 16-byte aligned
  * (SP_ERR_UNSUPPORTED and SP_ERR_INVALID_ARG otherwise). */
 int sp_paged_attention(const sp_paged_shape* shape, const sp_attn_params* params,

@@ -11,6 +11,7 @@
 namespace sp {
 
 constexpr int kMaxCached = 1 << 30;   // cached tokens of a request, and new tokens of an attention call
+constexpr int kMaxHeads = 1 << 16;    // heads of all kinds that one call walks
 constexpr int kMaxTableSeqs = 16384;  // requests whose scan fits a CTA's shared memory
 
 // Multiprocessors of the current device.

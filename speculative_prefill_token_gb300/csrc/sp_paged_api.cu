@@ -32,7 +32,8 @@ int check_paged(const sp_paged_shape* s) {
     if (s->n_q_heads % s->n_kv_heads != 0) return SP_ERR_INVALID_ARG;
     if (s->dtype != SP_DTYPE_BF16 && s->dtype != SP_DTYPE_F16) return SP_ERR_INVALID_ARG;
     if (s->head_dim != 64 && s->head_dim != 128 && s->head_dim != 256) return SP_ERR_UNSUPPORTED;
-    if (s->n_seqs > kMaxSeqs || s->n_q_heads / s->n_kv_heads > 128 || s->n_tokens > kMaxCached)
+    if (s->n_seqs > kMaxSeqs || s->n_q_heads / s->n_kv_heads > 128 || s->n_q_heads > kMaxHeads ||
+        s->n_tokens > kMaxCached)
         return SP_ERR_UNSUPPORTED;
     const int bs = s->block_size;
     if (!(bs == 8 || bs == 16 || bs == 32 || bs == 64 || bs % 128 == 0)) return SP_ERR_UNSUPPORTED;
@@ -94,7 +95,14 @@ int sp_append_kv(const sp_append_shape* s, const uint16_t* q, const uint16_t* k,
     if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(k_pool, 16) ||
         !aligned(v_pool, 16) || (s->rotary_dim > 0 && !aligned(cos_sin, 16)))
         return SP_ERR_INVALID_ARG;
-    if (k_pool == v_pool) return SP_ERR_INVALID_ARG;
+    if ((q ? static_cast<int64_t>(s->n_q_heads) : 0) + 2 * static_cast<int64_t>(s->n_kv_heads) > kMaxHeads)
+        return SP_ERR_UNSUPPORTED;
+    const uint16_t* out[3] = {k_pool, v_pool, q_out};
+    for (int i = 0; i < 3 && out[i]; ++i) {
+        if (out[i] == k || out[i] == v || (i < 2 && out[i] == q)) return SP_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (out[i] == out[j]) return SP_ERR_INVALID_ARG;
+    }
     if (q && q_out == q &&
         ((s->n_tokens > 1 && s->qo_stride_token != s->q_stride_token) ||
          (s->n_q_heads > 1 && s->qo_stride_head != s->q_stride_head)))
@@ -132,7 +140,8 @@ int sp_paged_attention(const sp_paged_shape* shape, const sp_attn_params* params
     if ((params->causal != 0 && params->causal != 1) || params->window < 0 ||
         (params->window > 0 && !params->causal) || !(std::isfinite(params->scale) && params->scale >= 0.0f))
         return SP_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) || out == q)
+    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) || out == q ||
+        out == k_pool || out == v_pool)
         return SP_ERR_INVALID_ARG;
     if (!ws || !aligned(ws, 256) || ws_bytes < attn_workspace(shape)) return SP_ERR_WORKSPACE;
     return to_status(launch_paged_attention(shape, params, q_off, kv_len, block_table, q, k_pool, v_pool, out, lse,

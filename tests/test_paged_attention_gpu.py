@@ -338,3 +338,28 @@ def test_waits_that_give_up_set_the_status_and_leave_the_workspace_usable(cuda_l
         assert sp.device_status(ws) == 5
         sp.paged_attention(*args, out=out, ws=ws)
         assert sp.device_status(ws) == 0 and torch.equal(out, want)
+
+
+def test_windows_longer_than_any_context_hide_nothing(cuda_lib):
+    import torch
+    sp = cuda_lib
+    case = paged_case(90, [2000, 0], [130, 60], 4, 2, 128, 32, "bf16")
+    want = _run(sp, case)
+    for window in (2131, 1 << 30, (1 << 30) + 1, 2 ** 31 - 1):
+        got = _run(sp, case, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), window
+
+
+def test_blocks_shared_by_requests(cuda_lib):
+    """Two requests whose tables name the same blocks for their common start."""
+    import torch
+    sp = cuda_lib
+    bs, d = 16, 64
+    case = paged_case(91, [64, 64], [5, 9], 4, 2, d, bs, "bf16")
+    case["table"][1, :4] = case["table"][0, :4]
+    out, lse = _run(sp, case)
+    kv = host(case["kv_len"])
+    ref = paged_oracle.paged_attention(host(case["q"]), host(case["q_off"]), kv, host(case["table"]),
+                                       host(case["k_pool"]), host(case["v_pool"]))
+    check_attention(out, lse, ref, kv, d, "bf16", 14)
+    assert torch.isfinite(out.float()).all()

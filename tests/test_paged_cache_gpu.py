@@ -233,3 +233,129 @@ def test_a_step_of_the_target_after_the_selection(cuda_lib, d, rotary, bs):
         ctx, n_free = kv, left
         new_off = _i32(np.arange(batch + 1))
         positions, n_new, cap = _i32([x + step for x in lengths]), _i32([batch]), batch
+
+
+def _step_state(lengths, ctx, hq, hk, d, bs, seed):
+    """Tensors of a step over a cache that holds ctx[b] tokens of each request,
+    for new tokens in a packed buffer of sum(lengths) + 5 rows."""
+    import torch
+    off, table, free, n_free = _tables_case(seed, ctx, lengths, bs, spare=3)
+    rng = np.random.default_rng(seed)
+    cap = int(off[-1]) + 5
+    blocks = int(max(table.max(), free.max())) + 1
+    pools = [torch.from_numpy(rng.standard_normal((blocks, bs, hk, d), dtype=np.float32)).cuda().bfloat16() for _ in range(2)]
+    qkv = torch.from_numpy(rng.standard_normal((cap, hq + 2 * hk, d), dtype=np.float32)).cuda().bfloat16()
+    pos = np.zeros(cap, np.int32)
+    for b, c in enumerate(ctx):
+        pos[off[b]:off[b + 1]] = 3 * c + 2 * np.arange(lengths[b])
+    ang = np.arange(4000)[:, None] * 1e4 ** (-np.arange(d // 4) * 4.0 / d)
+    cs = torch.from_numpy(np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)).cuda()
+    z = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    return dict(ctx=_i32(ctx), off=_i32(off), free=_i32(free), n_free=_i32([n_free]), table=_i32(table), pools=pools,
+                qkv=qkv, pos=_i32(pos), cs=cs, n_new=_i32([off[-1]]), slots=z(cap), kv=z(len(ctx)), left=z(1),
+                status=z(1), q=torch.zeros(cap, hq, d, dtype=torch.bfloat16, device="cuda"),
+                out=torch.zeros(cap, hq, d, dtype=torch.bfloat16, device="cuda"), hq=hq, hk=hk, bs=bs, cap=cap)
+
+
+def _step(sp, s, ws, stream=None):
+    hq, hk = s["hq"], s["hk"]
+    sp.block_tables(s["ctx"], s["off"], s["free"], s["n_free"], s["table"], s["bs"], slot_map=s["slots"], kv_len=s["kv"],
+                    n_left=s["left"], status=s["status"], stream=stream)
+    sp.append_kv(s["qkv"][:, hq:hq + hk], s["qkv"][:, hq + hk:], s["slots"], *s["pools"], q=s["qkv"][:, :hq], q_out=s["q"],
+                 positions=s["pos"], cos_sin=s["cs"], n_new=s["n_new"], status=s["status"], stream=stream)
+    sp.paged_attention(s["q"], s["off"], s["kv"], s["table"], *s["pools"], out=s["out"], ws=ws, stream=stream)
+
+
+def test_a_captured_step_replayed_with_other_lengths(cuda_lib):
+    """The three operators in one graph: replays give the eager call's bits,
+    also after the lengths, rows and free blocks were replaced in place."""
+    import torch
+    sp = cuda_lib
+    a = _step_state([40, 1, 0, 300], [100, 513, 7, 0], 8, 2, 128, 16, 1)
+    others = [_step_state(n, c, 8, 2, 128, 16, 2 + i) for i, (n, c) in enumerate(
+        [([0, 1, 339, 1], [64, 300, 15, 200]), ([341, 0, 0, 0], [90, 0, 600, 1]), ([1, 1, 1, 1], [0, 0, 0, 0])])]
+    wide = max(s["table"].shape[1] for s in [a] + others)
+    blocks = max(s["pools"][0].shape[0] for s in [a] + others)
+    free = max(s["free"].numel() for s in [a] + others)
+    for s in [a] + others:   # the capacities of one captured call
+        t = torch.full((4, wide), -9, dtype=torch.int32, device="cuda")
+        t[:, :s["table"].shape[1]] = s["table"]
+        s["table"] = t
+        f = torch.full((free,), -5, dtype=torch.int32, device="cuda")
+        f[:s["free"].numel()] = s["free"]
+        s["free"] = f
+        for i, p in enumerate(s["pools"]):
+            s["pools"][i] = torch.zeros(blocks, *p.shape[1:], dtype=p.dtype, device="cuda")
+            s["pools"][i][:p.shape[0]] = p
+        for name in ("qkv", "pos", "slots", "q", "out"):
+            x = s[name]
+            s[name] = torch.zeros(a["cap"], *x.shape[1:], dtype=x.dtype, device="cuda")
+            s[name][:x.shape[0]] = x
+    ws = sp.make_attention_workspace(a["q"], 4, a["pools"][0])
+    stage = {k: ([p.clone() for p in v] if isinstance(v, list) else v.clone() if torch.is_tensor(v) else v)
+             for k, v in a.items()}
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        _step(sp, stage, ws)
+    for s in [a] + others + [a]:
+        fresh = {k: ([p.clone() for p in v] if isinstance(v, list) else v.clone() if torch.is_tensor(v) else v)
+                 for k, v in s.items()}
+        for k, v in s.items():
+            if isinstance(v, list):
+                for x, y in zip(stage[k], v):
+                    x.copy_(y)
+            elif torch.is_tensor(v):
+                stage[k].copy_(v)
+        g.replay()
+        _step(sp, fresh, ws)
+        torch.cuda.synchronize()
+        assert sp.device_status(ws) == 0 and int(stage["status"]) == 0 and int(fresh["status"]) == 0
+        n = int(s["off"][-1])
+        for k in ("slots", "kv", "left", "table", "q", "out"):
+            assert torch.equal(stage[k], fresh[k]), k
+        for x, y in zip(stage["pools"], fresh["pools"]):
+            assert torch.equal(x, y)
+        assert n == 0 or stage["out"][:n].float().abs().sum() > 0
+
+
+def test_steps_on_two_streams_at_once(cuda_lib):
+    import torch
+    sp = cuda_lib
+    states = [_step_state([3, 1, 200], [1000, 20, 0], 8, 2, 256, 16, 7), _step_state([1] * 9, [700] * 9, 6, 3, 64, 32, 8)]
+    wss = [sp.make_attention_workspace(s["q"], s["ctx"].numel(), s["pools"][0]) for s in states]
+    for s, ws in zip(states, wss):
+        _step(sp, s, ws)
+    torch.cuda.synchronize()
+    want = [s["out"].clone() for s in states]
+    streams = [torch.cuda.Stream() for _ in states]
+    for s in states:
+        s["out"].zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):   # (the same step again takes the same blocks)
+        for s, ws, st in zip(states, wss, streams):
+            _step(sp, s, ws, stream=st)
+    torch.cuda.synchronize()
+    for s, ws, w in zip(states, wss, want):
+        assert torch.equal(s["out"], w) and sp.device_status(ws) == 0 and int(s["status"]) == 0
+
+
+@pytest.mark.parametrize("d,rotary", [(1024, 1024), (16, 16), (1024, 16)])
+def test_append_kv_smallest_and_largest_rows(cuda_lib, d, rotary):
+    import torch
+    sp = cuda_lib
+    rng = np.random.default_rng(d)
+    n, hk = 23, 2
+    k, v = [torch.from_numpy(rng.standard_normal((n, hk, d), dtype=np.float32)).cuda().bfloat16() for _ in range(2)]
+    pools = [torch.zeros(n, 1, hk, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]   # blocks of one token
+    slots, pos = rng.permutation(n).astype(np.int32), rng.integers(0, 100, n).astype(np.int32)
+    ang = np.arange(100)[:, None] * 1e4 ** (-np.arange(rotary // 2) * 2.0 / rotary)
+    cs = np.concatenate([np.cos(ang), np.sin(ang)], 1).astype(np.float32)
+    status = _i32([0])
+    sp.append_kv(k, v, _i32(slots), *pools, positions=_i32(pos), cos_sin=torch.from_numpy(cs).cuda(), status=status)
+    assert int(status) == 0
+    got, ref = host(pools[0])[slots, 0], paged_oracle.rotate(host(k), pos, cs)
+    # two products and a sum in fp32, one rounding
+    size = 2 * np.abs(host(k)).max(-1, keepdims=True)
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) * (1 + 2.0 ** -20) + 3 * 2.0 ** -24 * size + 2.0 ** -25).all()
+    assert torch.equal(pools[1][_i32(slots).long(), 0], v)

@@ -113,6 +113,17 @@ def test_paged_attention_refusals(lib):
     assert _attend(lib, ws=None) == 3 and _attend(lib, ws=P + 16) == 3 and _attend(lib, ws_bytes=n.value - 1) == 3
 
 
+def test_outputs_on_inputs_and_too_many_heads_are_refused(lib):
+    k, v, q, k_pool, v_pool = P + 4096, P + 8192, P, P + 8 * 4096, P + 9 * 4096
+    for kw in (dict(k_pool=k), dict(v_pool=v), dict(k_pool=v), dict(v_pool=q), dict(q_out=k), dict(q_out=v),
+               dict(q_out=k_pool), dict(q_out=v_pool)):
+        assert _append(lib, **kw) == 1, kw
+    for kw in (dict(n_q_heads=(1 << 16) - 3), dict(n_kv_heads=1 << 15), dict(n_kv_heads=1 << 30), dict(n_q_heads=2 ** 31 - 1)):
+        assert _append(lib, kw) == 2, kw
+    assert _attend(lib, out=P + 4 * 4096) == 1 and _attend(lib, out=P + 5 * 4096) == 1
+    assert _attend(lib, dict(n_q_heads=1 << 17, n_kv_heads=1 << 16)) == 2
+
+
 def test_status_string_of_the_free_list(lib):
     assert lib.sp_status_string(7) == b"the free list holds too few blocks"
     assert sp.STATUS[7] == "SP_ERR_CAPACITY"
