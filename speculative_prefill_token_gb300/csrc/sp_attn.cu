@@ -17,12 +17,12 @@
 // accumulator fills the tensor memory); its unit is a tile of 128 keys. All
 // units of all items are cut into equal contiguous ranges, one for each CTA
 // (one CTA per SM), whatever the mix of lengths. The lengths live on the
-// device: a one-CTA kernel lays out the items and the ranges first. An item
-// cut between CTAs leaves a part in the workspace for each of them (reference,
-// sum and accumulator of each row), and a third kernel joins the parts in
-// their order, so results do not depend on timing. (Joined by the last CTA to
-// finish instead, the 76 parts of a single long chunk were read by two CTAs:
-// 245 us in place of 10 for 8 tokens over 32K.)
+// device: every CTA lays out a small batch itself, a one-CTA kernel before it a
+// larger one. An item cut between CTAs leaves a part in the workspace for each
+// of them (reference, sum and accumulator of each row), and another kernel
+// joins the parts in their order, so results do not depend on timing. (Joined
+// by the last CTA to finish instead, the 76 parts of a single long chunk were
+// read by two CTAs: 244 us in place of 60 for 8 tokens over 32K, 25 now.)
 //
 // Roles (384 threads):
 //   warps 0-7  two softmax warpgroups. A thread owns one row of a 128 x 128
@@ -38,6 +38,21 @@
 // runs: with two query tiles, one tile each; with one (decode steps, short
 // chunks), even and odd key tiles, with an accumulator each for d <= 128
 // (joined from tensor memory at the end) and one accumulator for d = 256.
+//
+// What bounds it (of 6,693 GB/s and 1,908 TFLOP/s measured):
+//   decode steps    the stream of keys and values: 64 requests of 2K to 32K
+//                   tokens, 16 + 4 heads of 128, 375 us, 6.9 TB/s; 16 of 4K to
+//                   16K, 8 + 2 heads of 256, 57 us, 5.3 TB/s (of it 4.5 us until
+//                   the first copy, and 2 to 5 us of the join)
+//   d = 128, long   the chain logits -> softmax (some 1,700 cycles) -> weights
+//                   of a tile, which two streams do not hide in full: 4,096
+//                   tokens over 39K, 16 + 4 heads, 820 us, 1,530 TFLOP/s
+//   d = 256         shared memory: operands of both products and the copies
+//                   take 2,560 cycles of its bandwidth a tile, the products
+//                   2,048: 4,916 tokens, 8 + 2 heads, 100 us, 990 TFLOP/s (with
+//                   some 5 us of each of the few items to start and write)
+//   d = 64          the softmax: its instructions take twice the products' time
+//   single rows     latency: 9.5 us for a token over 512
 //
 // Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT
 // in the workspace status, and the CTA drains its copies and MMAs in flight
@@ -141,7 +156,8 @@ constexpr int kMaxCtas = 256;
 constexpr int kLocalItems = 384;   // items and requests of a plan made by every CTA
 // Cost of an item besides its key tiles, in tiles: loading the queries,
 // filling the pipeline and writing the rows. (Without it the CTAs with the
-// shortest items of a prompt finish last.)
+// shortest items of a prompt finish last. At 1, 2, 3 and 4: 4,916 tokens at
+// d = 256 118, 98, 98, 100 us; 24 mixed requests at d = 64 57, 53, 54, 55 us.)
 constexpr int kItemCost = 2;
 constexpr int kJoinFew = 4;        // parts held in registers at once
 constexpr int kJoinThreads = 256;
@@ -150,7 +166,8 @@ constexpr int kJoinGroups = kJoinThreads / 16;   // of 16 threads: 64 columns of
 
 // Whether the groups of a join block share a row and its parts, or take a row
 // each: with few rows the parts' latency counts, with many (of some parts) the
-// blocks. (250 rows of 5 parts each in 30 items, a row at a time: 15 us.)
+// blocks. (8 tokens over 32K, 76 parts: 25 us of the whole call shared, 45 a row
+// each; 702 tokens of one request, 5 parts: 18 us a row each, 23.5 shared.)
 __device__ __forceinline__ bool join_shares(int parts, int row_chunks) {
     return parts > 16 || (parts > kJoinFew && row_chunks <= 128);
 }
@@ -235,7 +252,7 @@ __device__ __forceinline__ bool bad_request(const AttnArgs& a, int64_t lo, int64
 }
 
 // Lays out a batch of any size, by one block of its own: items with their
-// costs, and the CTAs' ranges.
+// costs, and the CTAs' ranges. Bound by the latency of its scans.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles) {
     __shared__ int64_t sums[32];
     grid_dep_wait();
@@ -294,7 +311,9 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
 
 // The same of a small batch (at most kLocalItems items and requests, costs of
 // 32 bits), by every CTA of the attention kernel for itself: no launch before
-// it, and its own range and first item are at hand.
+// it, and its own range and first item are at hand. (By this and by the plan
+// kernel: one token 9.9 and 12.0 us, 16 decodes 57.6 and 60.2, 24 mixed requests
+// 52.6 and 55.7, a prompt of 4,916 tokens 102 and 102.)
 struct LocalPlan {
     int32_t sums[32];
     int32_t q0[kLocalItems], nq[kLocalItems], kv[kLocalItems], req_item[kLocalItems], pre[kLocalItems + 1];
@@ -1408,7 +1427,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ------------------------------------------------------------ join
 
 // out = sum_p w_p O_p / sum_p w_p l_p, w_p = exp2(m_p - max m), for the rows of
-// the cut items. A task is 64 columns of a row with many parts, which the 16
+// the cut items: 2 to 5 us, two chained reads of L2 and the launch. A task is 64 columns of a row with many parts, which the 16
 // groups of a block share (the L2 latency of 76 parts in turn would be the
 // kernel's time), or of 16 rows with few, each walked by a group.
 template <int D, bool kBf16>
@@ -1676,6 +1695,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
         !make_pool_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, hv,
                        d / 64))
         return cudaErrorInvalidValue;
+    // (a prompt of 4,916 tokens at d = 256: 102 us with 32-byte stores, 114 with 16)
     a.wide_out = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && (s->n_tokens == 1 || a.o_st % 16 == 0) &&
                  (s->n_q_heads == 1 || a.o_sh % 16 == 0);
     // costs (times CTAs) of a plan in 32 bits

@@ -12,12 +12,16 @@
 // writes the slots of its own tokens: one launch and no communication
 // between CTAs. The token at p % bs == 0 of a new block writes that block's
 // table entry; the other tokens of the block take its id from the free list,
-// so no CTA reads an entry that another one writes.
+// so no CTA reads an entry that another one writes. Latency bounds it (three
+// dependent reads and a scan): 16 requests 3 us, 4,000 requests with 270,000
+// tokens 8 us (11 with the lengths read from L2 in both passes).
 //
 // append_kv_kernel. A pure stream: each query, key and value row is read
 // once and written once. A thread owns one pair of 16-byte vectors of a
-// token's rows and walks the heads, so that the 64 bytes of cosines and
-// sines stay in its registers.
+// token's rows and walks one or two heads, so that the 64 bytes of cosines and
+// sines stay in its registers. Copy bandwidth bounds it: 39,322 tokens of 16 + 4
+// heads of 128 take 85 us, 5.93 TB/s of their own bytes (89 % of a measured
+// plain copy); 16 tokens 2.6 us, latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -360,7 +364,8 @@ cudaError_t launch_append_kv(const sp_append_shape* s, const uint16_t* q, const 
     const int heads = a.hq + 2 * a.hk, pairs = a.d / 16, sms = device_sms();
     // two heads a thread once that still fills the GPU (39,322 tokens of 16 + 4
     // heads of 128: one 101 us, two 84, four 92), else one, so that a decode
-    // step's few rows are all in flight at once
+    // step's few rows are all in flight at once (16 tokens of 8 + 2 heads of 256:
+    // one 2.1 us, two 2.6)
     a.heads_per = static_cast<int64_t>(a.cap) * pairs * heads >= int64_t(2) * kAppThreads * kAppCtas * sms ? 2 : 1;
     a.groups = (heads + a.heads_per - 1) / a.heads_per;
     int64_t grid = (static_cast<int64_t>(a.cap) * pairs * a.groups + kAppThreads - 1) / kAppThreads;
