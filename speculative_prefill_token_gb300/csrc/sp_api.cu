@@ -564,7 +564,7 @@ const char* sp_status_string(int status) {
 
 const char* sp_build_info(void) {
     return "specprefill sm_103a: tcgen05/TMA logits kernel, 16-bit fixed-point logits scratch, "
-           "slice-parallel chunk ranking, kept-row gathers";
+           "slice-parallel chunk ranking, kept-row gathers, paged cache store and attention";
 }
 
 }  // extern "C"
