@@ -161,8 +161,12 @@ constexpr int kLocalItems = 384;   // items and requests of a plan made by every
 constexpr int kItemCost = 2;
 constexpr int kJoinFew = 4;        // parts held in registers at once
 constexpr int kJoinThreads = 256;
-constexpr int kJoinBlocks = 4;     // of an SM, all resident
+constexpr int kJoinBlocks = 3;     // of an SM, all resident (80 registers a thread)
 constexpr int kJoinGroups = kJoinThreads / 16;   // of 16 threads: 64 columns of a row
+// Rows of two parts that a group has in flight: their latency is the join of a
+// prompt, whose items are mostly cut once. (4,916 tokens at d = 256, whole call:
+// one row and four blocks an SM 104 us, two and three 101, four and two 101.)
+constexpr int kJoinRows = 2;
 
 // Whether the groups of a join block share a row and its parts, or take a row
 // each: with few rows the parts' latency counts, with many (of some parts) the
@@ -399,7 +403,7 @@ __device__ __forceinline__ void list_cuts(const AttnArgs& a, int chunks, int lan
                 j.tok0 = __ldcg(&a.items[s.x].tok0);
                 j.ntok = __ldcg(&a.items[s.x].ntok);
                 mine = j.ntok * a.G * chunks;
-                if (!join_shares(j.parts, mine)) mine = (mine + kJoinGroups - 1) / kJoinGroups;
+                if (!join_shares(j.parts, mine)) mine = (mine + kJoinGroups * kJoinRows - 1) / (kJoinGroups * kJoinRows);
             }
         }
         int incl = mine;
@@ -1427,9 +1431,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ------------------------------------------------------------ join
 
 // out = sum_p w_p O_p / sum_p w_p l_p, w_p = exp2(m_p - max m), for the rows of
-// the cut items: 2 to 5 us, two chained reads of L2 and the launch. A task is 64 columns of a row with many parts, which the 16
-// groups of a block share (the L2 latency of 76 parts in turn would be the
-// kernel's time), or of 16 rows with few, each walked by a group.
+// the cut items: 2 to 5 us for decode steps, two chained reads of L2 and the
+// launch; some 10 us for a prompt at d = 256, whose 300 parts are 40 MB. A task is
+// 64 columns of a row with many parts, which the 16 groups of a block share (the
+// L2 latency of 76 parts in turn would be the kernel's time), or of 32 rows with
+// few, two for each group.
 template <int D, bool kBf16>
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(const AttnArgs a) {
     using L = Smem<D>;
@@ -1455,83 +1461,123 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
         const int parts = job.parts;
         const int rows0 = min(job.ntok, a.tq) * a.G, rows = job.ntok * a.G;   // of the first tile, of both
         const bool share = join_shares(parts, rows * L::kChunks);
-        const int unit = share ? task - job.task0 : (task - job.task0) * kJoinGroups + group;
-        const int r = unit / L::kChunks, col = unit % L::kChunks * 64 + vec * 4;
-        const bool mine = r < rows;
-        const int tile = mine && r >= rows0 ? 1 : 0, row = r - tile * rows0;
-        auto at = [&](int p) {
+        // 64 columns of a row, this thread's four of them
+        struct Place {
+            int tile, row, col;
+        };
+        auto place = [&](int unit) {
+            const int r = unit / L::kChunks, tile = r >= rows0 ? 1 : 0;
+            return Place{tile, r - tile * rows0, unit % L::kChunks * 64 + vec * 4};
+        };
+        auto at = [&](Place x, int p) {
             const int part = (job.c0 + p) * 2 + (p == 0 && !job.c0_head ? 1 : 0);
-            return (static_cast<int64_t>(part) * L::kTiles + tile) * kRows + row;
+            return (static_cast<int64_t>(part) * L::kTiles + x.tile) * kRows + x.row;
         };
-        float top = -INFINITY, sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        auto add = [&](float2 ml, float4 x) {
-            const float f = ml.x == top ? 1.0f : exp2_ftz(ml.x - top);
-            sum += ml.y * f;
-            acc.x += x.x * f;
-            acc.y += x.y * f;
-            acc.z += x.z * f;
-            acc.w += x.w * f;
+        auto load = [&](Place x, int p) { return __ldcg(reinterpret_cast<const float4*>(a.part_o + at(x, p) * D + x.col)); };
+        struct Row {
+            float top, sum;
+            float4 acc;
+            __device__ __forceinline__ void add(float2 ml, float4 x) {
+                const float f = ml.x == top ? 1.0f : exp2_ftz(ml.x - top);
+                sum += ml.y * f;
+                acc.x += x.x * f;
+                acc.y += x.y * f;
+                acc.z += x.z * f;
+                acc.w += x.w * f;
+            }
         };
-        auto load = [&](int p) { return __ldcg(reinterpret_cast<const float4*>(a.part_o + at(p) * D + col)); };
+        const Row zero{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
+        auto write = [&](Place x, const Row& y) {
+            const bool none = y.sum == 0.0f;
+            const float inv = none ? 0.0f : 1.0f / y.sum;
+            const int tok = x.row / a.G;
+            const int64_t t = job.tok0 + x.tile * a.tq + tok;
+            const int h = job.g * a.G + x.row - tok * a.G;
+            uint2 w;
+            w.x = none ? 0u : pack_pair<kBf16>(y.acc.x * inv, y.acc.y * inv);
+            w.y = none ? 0u : pack_pair<kBf16>(y.acc.z * inv, y.acc.w * inv);
+            *reinterpret_cast<uint2*>(a.out + t * a.o_st + h * a.o_sh + x.col) = w;
+            if (a.lse && x.col == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (y.top - kBias + __log2f(y.sum)) * kLn2;
+        };
         if (share) {
-            for (int p = threadIdx.x; p < parts; p += kJoinThreads) ml_s[p] = __ldcg(a.part_ml + at(p));
+            const Place x = place(task - job.task0);
+            Row y = zero;
+            for (int p = threadIdx.x; p < parts; p += kJoinThreads) ml_s[p] = __ldcg(a.part_ml + at(x, p));
             __syncthreads();
-            for (int p = lane; p < parts; p += 32) top = fmaxf(top, ml_s[p].x);
+            for (int p = lane; p < parts; p += 32) y.top = fmaxf(y.top, ml_s[p].x);
 #pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            for (int o = 16; o; o >>= 1) y.top = fmaxf(y.top, __shfl_xor_sync(0xffffffffu, y.top, o));
 #pragma unroll 4
-            for (int p = group; p < parts; p += kJoinGroups) add(ml_s[p], load(p));
-            acc_s[group][vec] = acc;
-            if (vec == 0) sum_s[group] = sum;
+            for (int p = group; p < parts; p += kJoinGroups) y.add(ml_s[p], load(x, p));
+            acc_s[group][vec] = y.acc;
+            if (vec == 0) sum_s[group] = y.sum;
             __syncthreads();
             if (group == 0) {
 #pragma unroll
                 for (int k = 1; k < kJoinGroups; ++k) {
-                    const float4 x = acc_s[k][vec];
-                    acc.x += x.x;
-                    acc.y += x.y;
-                    acc.z += x.z;
-                    acc.w += x.w;
-                    sum += sum_s[k];
+                    const float4 o = acc_s[k][vec];
+                    y.acc.x += o.x;
+                    y.acc.y += o.y;
+                    y.acc.z += o.z;
+                    y.acc.w += o.w;
+                    y.sum += sum_s[k];
+                }
+                write(x, y);
+            }
+            __syncthreads();   // (the shared arrays are free for the next task)
+            continue;
+        }
+        const int first = (task - job.task0) * (kJoinGroups * kJoinRows) + group, units = rows * L::kChunks;
+        if (parts == 2) {
+            Place x[kJoinRows];
+            float2 ml[kJoinRows][2];
+            float4 o[kJoinRows][2];
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k) {
+                x[k] = place(min(first + k * kJoinGroups, units - 1));
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    ml[k][p] = __ldcg(a.part_ml + at(x[k], p));
+                    o[k][p] = load(x[k], p);
                 }
             }
-        } else if (mine) {
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k) {
+                Row y = zero;
+                y.top = fmaxf(ml[k][0].x, ml[k][1].x);
+                y.add(ml[k][0], o[k][0]);
+                y.add(ml[k][1], o[k][1]);
+                if (first + k * kJoinGroups < units) write(x[k], y);
+            }
+            continue;
+        }
+#pragma unroll 1
+        for (int unit = first; unit < min(units, first + kJoinGroups * kJoinRows); unit += kJoinGroups) {
+            const Place x = place(unit);
+            Row y = zero;
             if (parts <= kJoinFew) {
                 float2 ml[kJoinFew];
-                float4 x[kJoinFew];
+                float4 o[kJoinFew];
 #pragma unroll
                 for (int p = 0; p < kJoinFew; ++p)
                     if (p < parts) {
-                        ml[p] = __ldcg(a.part_ml + at(p));
-                        x[p] = load(p);
+                        ml[p] = __ldcg(a.part_ml + at(x, p));
+                        o[p] = load(x, p);
                     }
 #pragma unroll
                 for (int p = 0; p < kJoinFew; ++p)
-                    if (p < parts) top = fmaxf(top, ml[p].x);
+                    if (p < parts) y.top = fmaxf(y.top, ml[p].x);
 #pragma unroll
                 for (int p = 0; p < kJoinFew; ++p)
-                    if (p < parts) add(ml[p], x[p]);
+                    if (p < parts) y.add(ml[p], o[p]);
             } else {
 #pragma unroll 8
-                for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(a.part_ml + at(p)).x);
+                for (int p = 0; p < parts; ++p) y.top = fmaxf(y.top, __ldcg(a.part_ml + at(x, p)).x);
 #pragma unroll 8
-                for (int p = 0; p < parts; ++p) add(__ldcg(a.part_ml + at(p)), load(p));
+                for (int p = 0; p < parts; ++p) y.add(__ldcg(a.part_ml + at(x, p)), load(x, p));
             }
+            write(x, y);
         }
-        if (mine && (!share || group == 0)) {
-            const bool none = sum == 0.0f;
-            const float inv = none ? 0.0f : 1.0f / sum;
-            const int tok = row / a.G;
-            const int64_t t = job.tok0 + tile * a.tq + tok;
-            const int h = job.g * a.G + row - tok * a.G;
-            uint2 y;
-            y.x = none ? 0u : pack_pair<kBf16>(acc.x * inv, acc.y * inv);
-            y.y = none ? 0u : pack_pair<kBf16>(acc.z * inv, acc.w * inv);
-            *reinterpret_cast<uint2*>(a.out + t * a.o_st + h * a.o_sh + col) = y;
-            if (a.lse && col == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (top - kBias + __log2f(sum)) * kLn2;
-        }
-        if (share) __syncthreads();   // (the shared arrays are free for the next task)
     }
 }
 
