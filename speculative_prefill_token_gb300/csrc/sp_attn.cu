@@ -142,7 +142,7 @@ struct AttnArgs {
     float* part_o;      // [grid * 2][tiles][128][d]
     float2* part_ml;    // [grid * 2][tiles][128] (reference, sum)
     int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, o_st, o_sh, pool_tokens, spin;
-    int B, hk, G, tq, bs, table_stride, cap, causal, window, grid;
+    int B, hk, G, tq, bs, table_stride, cap, causal, window, grid, item_cost;
     int wide_out;        // 32-byte stores of out are aligned
     int local_plan;      // every CTA lays out the batch itself
     int hk_shift, hv_shift;  // rows of a K and of a V box, as powers of two
@@ -156,9 +156,10 @@ constexpr int kMaxCtas = 256;
 constexpr int kLocalItems = 384;   // items and requests of a plan made by every CTA
 // Cost of an item besides its key tiles, in tiles: loading the queries,
 // filling the pipeline and writing the rows. (Without it the CTAs with the
-// shortest items of a prompt finish last. At 1, 2, 3 and 4: 4,916 tokens at
-// d = 256 118, 98, 98, 100 us; 24 mixed requests at d = 64 57, 53, 54, 55 us.)
-constexpr int kItemCost = 2;
+// shortest items of a prompt finish last: 8,200 cycles at d = 256, where a tile
+// takes 3,100, 5,300 at d = 64 and 2,700. At 1, 2, 3 and 4: 4,916 tokens at
+// d = 256 118, 101, 98, 100 us; 24 mixed requests at d = 64 57, 53, 54, 55 us.)
+constexpr int item_cost(int d) { return d == 256 ? 3 : 2; }
 constexpr int kJoinFew = 4;        // parts held in registers at once
 constexpr int kJoinThreads = 256;
 constexpr int kJoinBlocks = 3;     // of an SM, all resident (80 registers a thread)
@@ -245,7 +246,7 @@ __device__ __forceinline__ Start make_start(const AttnArgs& a, const T* pre, int
         s.g = static_cast<int32_t>(begin / units);
         const T u = begin - s.g * units;
         s.item = last_at_most(pre, items, u);
-        s.off = static_cast<int32_t>(max(u - pre[s.item] - kItemCost, static_cast<T>(0)));
+        s.off = static_cast<int32_t>(max(u - pre[s.item] - a.item_cost, static_cast<T>(0)));
     }
     return s;
 }
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
             const int q0 = a.q_off[b];
             const Item it = make_item(a, b, q0, a.q_off[b + 1] - q0, a.kv_len[b],
                                       static_cast<int>(i - a.req_item[b]) * tpi, tpi);
-            n = it.ntiles + kItemCost;
+            n = it.ntiles + a.item_cost;
             a.items[i] = it;
         }
         int64_t total;
@@ -355,7 +356,7 @@ __device__ __forceinline__ int local_plan(const AttnArgs& a, int tiles, LocalPla
     if (t < items) {
         const int b = last_at_most(p.req_item, a.B, t);
         const Item it = make_item(a, b, p.q0[b], p.nq[b], p.kv[b], (t - p.req_item[b]) * tpi, tpi);
-        n = it.ntiles + kItemCost;
+        n = it.ntiles + a.item_cost;
         a.items[t] = it;   // (every CTA writes the same; each reads what it wrote)
     }
     const int before = block_scan<kAttnThreads>(n, p.sums, &units);
@@ -1725,6 +1726,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.bs = bs;
     a.table_stride = s->table_stride;
     a.cap = s->n_tokens;
+    a.item_cost = item_cost(d);
     a.causal = p->causal;
     a.window = p->window <= kMaxCached ? p->window : 0;   // (a longer one hides nothing)
     const int per = kKeys / slots_per_tile(d);
@@ -1745,7 +1747,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.wide_out = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && (s->n_tokens == 1 || a.o_st % 16 == 0) &&
                  (s->n_q_heads == 1 || a.o_sh % 16 == 0);
     // costs (times CTAs) of a plan in 32 bits
-    const int64_t tiles = (static_cast<int64_t>(a.table_stride) * bs + kKeys - 1) / kKeys + kItemCost;
+    const int64_t tiles = (static_cast<int64_t>(a.table_stride) * bs + kKeys - 1) / kKeys + a.item_cost;
     a.local_plan = l.items_max <= kLocalItems && a.B <= kLocalItems &&
                    tiles < INT32_MAX / kLocalItems / kMaxCtas / a.hk;
     if (!a.local_plan) {
