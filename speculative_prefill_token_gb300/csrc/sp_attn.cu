@@ -69,6 +69,7 @@
 #include "sp_internal.h"
 #include "sp_paged.h"
 #include "sp_ptx.cuh"
+#include "sp_ptx_attn.cuh"
 
 namespace sp {
 namespace {
@@ -786,7 +787,7 @@ __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint3
         for (int part = 0; part < P; ++part) {
             const int slot = __shfl_sync(kAll, ahead(p, part).slot, 0);
             const uint64_t qd = smem_desc_sw128(base + L::q + t * L::kChunks * kChunk + part * L::kSlot);
-            const uint64_t kd = smem_desc_sw128(base + L::ring + slot * L::kSlot, 1024 * L::kSlotChunks);
+            const uint64_t kd = smem_desc_sw128_k(base + L::ring + slot * L::kSlot, 1024 * L::kSlotChunks);
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < 4 * L::kSlotChunks; ++k)
