@@ -22,7 +22,7 @@
 // of them (reference, sum and accumulator of each row), and another kernel
 // joins the parts in their order, so results do not depend on timing. (Joined
 // by the last CTA to finish instead, the 76 parts of a single long chunk were
-// read by two CTAs: 244 us in place of 60 for 8 tokens over 32K, 25 now.)
+// read by two CTAs: 244 us in place of 60 for 8 tokens over 32K, 24 now.)
 //
 // Roles (384 threads):
 //   warps 0-7  two softmax warpgroups. A thread owns one row of a 128 x 128
@@ -46,13 +46,14 @@
 //                   the first copy, and 2 to 5 us of the join)
 //   d = 128, long   the chain logits -> softmax (some 1,700 cycles) -> weights
 //                   of a tile, which two streams do not hide in full: 4,096
-//                   tokens over 39K, 16 + 4 heads, 820 us, 1,530 TFLOP/s
+//                   tokens over 39K, 16 + 4 heads, 805 to 864 us, 1,450 to
+//                   1,550 TFLOP/s
 //   d = 256         shared memory: operands of both products and the copies
 //                   take 2,560 cycles of its bandwidth a tile, the products
-//                   2,048: 4,916 tokens, 8 + 2 heads, 100 us, 990 TFLOP/s (with
-//                   some 5 us of each of the few items to start and write)
+//                   2,048: 4,916 tokens, 8 + 2 heads, 96 us, 1,030 TFLOP/s (10 of
+//                   them the join, some 4 each of a CTA's two items' ends)
 //   d = 64          the softmax: its instructions take twice the products' time
-//   single rows     latency: 9.5 us for a token over 512
+//   single rows     latency: 9.3 us for a token over 512
 //
 // Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT
 // in the workspace status, and the CTA drains its copies and MMAs in flight
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
 // 32 bits), by every CTA of the attention kernel for itself: no launch before
 // it, and its own range and first item are at hand. (By this and by the plan
 // kernel: one token 9.9 and 12.0 us, 16 decodes 57.6 and 60.2, 24 mixed requests
-// 52.6 and 55.7, a prompt of 4,916 tokens 102 and 102.)
+// 52.6 and 55.7; a prompt of 4,916 tokens the same.)
 struct LocalPlan {
     int32_t sums[32];
     int32_t q0[kLocalItems], nq[kLocalItems], kv[kLocalItems], req_item[kLocalItems], pre[kLocalItems + 1];
