@@ -565,8 +565,8 @@ int sp_paged_attention_workspace(const sp_paged_shape* shape, size_t* bytes);
  *   may hold anything, infinities and NaN included: they do not reach its
  *   result. (Where a value of the new tokens, or at the edge of the window, is
  *   no number, the queries around it take a slow path: 0.1 s and more for a
- *   context of 40,000 tokens.) Table entries behind the request's last block
- *   are not read.
+ *   context of 40,000 tokens, in proportion to it; device waits do not run out
+ *   meanwhile.) Table entries behind the request's last block are not read.
  * - A bad q_off or kv_len (out of range, over 2^30, or more tokens than a
  *   table row holds) sets the device status SP_ERR_DEVICE and nothing is computed; a
  *   block id outside the pool sets it and reads pool row 0 instead.

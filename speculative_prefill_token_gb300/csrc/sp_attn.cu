@@ -512,7 +512,7 @@ struct Smem {
     static constexpr uint32_t drain = statfull + 16;
     static constexpr uint32_t tmem = drain + 8;
     static constexpr uint32_t abort = tmem + 8;
-    static constexpr uint32_t odd = abort + 4;        // [2] a value of the segment is no number
+    static constexpr uint32_t odd = abort + 4;        // [3] a value of the segment is no number; of any segment
     static constexpr uint32_t checked = odd + 12;     // [2] that flag is written
     static constexpr uint32_t seen = checked + 16;    // [2] and read
     static constexpr uint32_t total = seen + 16;
@@ -679,48 +679,56 @@ __device__ __forceinline__ void add_zero_times(uint32_t& acc, uint4 x) {
     }
 }
 
-// By one warp, from global memory (some 100 rows per item): one flag per
-// segment, after which the softmax warps take its rows again one by one. It
+// Whether one of those values is infinite or NaN, by one warp from global
+// memory (some 100 rows per item).
+template <int D, bool kBf16>
+__device__ __forceinline__ bool odd_values(const AttnArgs& a, const Segment& s, int lane) {
+    constexpr int kLanes = D / 8, kStep = 32 / kLanes;   // lanes of a row, rows at a time
+    const int k0 = s.first * kKeys, k1 = (s.first + s.n) * kKeys;
+    const int last = s.it.pos0 + s.it.ntok - 1;
+    uint32_t acc = 0;
+    // keys behind the first row's position, keys before the last row's window
+#pragma unroll 1
+    for (int part = 0; part < (a.window > 0 ? 2 : 1); ++part) {
+        const int lo = max(part ? s.it.klo : max(s.it.klo, s.it.pos0 + 1), k0);
+        const int hi = min(part ? min(s.it.khi, last - a.window + 1) : s.it.khi, k1);
+        // block by block, a lane for each 16 bytes of a row
+        const int per = a.bs;
+        int blk = lo / per, in = lo - blk * per;
+        const int32_t* tab = a.table + static_cast<int64_t>(s.it.b) * a.table_stride;
+        for (int j = lo; j < hi; ++blk, in = 0) {
+            const int id = tab[blk];
+            int64_t row = static_cast<int64_t>(id) * per;
+            if (id < 0 || row + per > a.pool_tokens) row = 0;
+            const int n = min(per - in, hi - j);
+            const uint16_t* p = a.v + (row + in + lane / kLanes) * a.v_st + s.g * a.v_sh + lane % kLanes * 8;
+            const int64_t step = kStep * a.v_st;
+#pragma unroll 4
+            for (int i = lane / kLanes; i < n; i += kStep, p += step) add_zero_times<kBf16>(acc, *reinterpret_cast<const uint4*>(p));
+            j += n;
+        }
+    }
+    return __any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0);
+}
+
+// By a warp of its own: one flag per segment. The softmax warps write no rows of
+// a flagged segment; they take them one by one when their range is done. It
 // costs a prefill at d = 256 4 % of its time; by the softmax warps, from the
 // ring, it was 20 %.
 template <int D, bool kBf16>
 __device__ __forceinline__ void check_values(const Ctx& c, const AttnArgs& a, int items, int lane) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
-    constexpr int kLanes = D / 8, kStep = 32 / kLanes;   // lanes of a row, rows at a time
     uint32_t n = 0;
     Walk w(c.range, items);
     Segment s;
     while (w.next(a, s)) {
         if (!looked_at(a, s)) continue;
         if (!__all_sync(kAll, c.wait(L::seen + 8 * (n & 1), (n >> 1 & 1) ^ 1))) return;
-        const int k0 = s.first * kKeys, k1 = (s.first + s.n) * kKeys;
-        const int last = s.it.pos0 + s.it.ntok - 1;
-        uint32_t acc = 0;
-        // keys behind the first row's position, keys before the last row's window
-#pragma unroll 1
-        for (int part = 0; part < (a.window > 0 ? 2 : 1); ++part) {
-            const int lo = max(part ? s.it.klo : max(s.it.klo, s.it.pos0 + 1), k0);
-            const int hi = min(part ? min(s.it.khi, last - a.window + 1) : s.it.khi, k1);
-            // block by block, a lane for each 16 bytes of a row
-            const int per = a.bs;
-            int blk = lo / per, in = lo - blk * per;
-            const int32_t* tab = a.table + static_cast<int64_t>(s.it.b) * a.table_stride;
-            for (int j = lo; j < hi; ++blk, in = 0) {
-                const int id = tab[blk];
-                int64_t row = static_cast<int64_t>(id) * per;
-                if (id < 0 || row + per > a.pool_tokens) row = 0;
-                const int n = min(per - in, hi - j);
-                const uint16_t* p = a.v + (row + in + lane / kLanes) * a.v_st + s.g * a.v_sh + lane % kLanes * 8;
-                const int64_t step = kStep * a.v_st;
-#pragma unroll 4
-                for (int i = lane / kLanes; i < n; i += kStep, p += step) add_zero_times<kBf16>(acc, *reinterpret_cast<const uint4*>(p));
-                j += n;
-            }
-        }
-        const bool odd = __any_sync(kAll, (acc & 0x7fff7fffu) != 0);
+        const bool odd = odd_values<D, kBf16>(a, s, lane);
         if (lane == 0) {
             reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[n & 1] = odd;
+            if (odd) reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[2] = 1;
             mbar_arrive(c.base + L::checked + 8 * (n & 1));
         }
         __syncwarp();
@@ -1078,6 +1086,34 @@ __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
     }
 }
 
+// The rows of the flagged segments, when nothing of the CTA waits any more: their
+// time grows with the context (0.1 s and more at 40,000 keys), beyond what a
+// bounded wait may last. The segments are found by looking at their values once
+// more (as many flags as a range has segments have no place to stay).
+template <int D, bool kBf16>
+__device__ __noinline__ void flagged_rows(const AttnArgs& a, const Range* range, int items, int wg) {
+    const int warp = threadIdx.x >> 5 & 3, lane = threadIdx.x & 31;
+    Walk w(range, items);
+    Segment s;
+    while (w.next(a, s)) {
+        const bool two = two_tiles(a, s, D);
+        const int tile = two ? wg : 0;
+        const int rows = min(max(s.it.ntok - tile * a.tq, 0), a.tq) * a.G;
+        if (wg == 1 && !two) continue;   // (the first warpgroup's rows)
+        if (warp * 32 >= rows || !looked_at(a, s) || !odd_values<D, kBf16>(a, s, lane)) continue;
+        RowsAgain e;
+        e.it = s.it;
+        e.g = s.g;
+        e.first = s.first;
+        e.n = s.n;
+        e.tok0 = tile * a.tq;
+        e.row0 = warp * 32;
+        e.rows = rows;
+        e.part = s.split ? ((static_cast<int>(blockIdx.x) * 2 + (s.head ? 0 : 1)) * Smem<D>::kTiles + tile) * kRows : -1;
+        rows_again<D, kBf16>(a, e);
+    }
+}
+
 // One warpgroup (index wg) of softmax threads over the CTA's segments.
 template <int D, bool kBf16>
 __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int items, int wg) {
@@ -1288,20 +1324,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             }
             constexpr int kCols = D > 128 ? D / 2 : D;    // columns of this warpgroup
             const int col0 = D > 128 ? wg * kCols : 0;
-            if (ok && live && again) {
-                if (D <= 128 || wg == 0) {
-                    RowsAgain e;
-                    e.it = s.it;
-                    e.g = s.g;
-                    e.first = s.first;
-                    e.n = s.n;
-                    e.tok0 = tile * a.tq;
-                    e.row0 = warp * 32;
-                    e.rows = rows;
-                    e.part = s.split ? ((static_cast<int>(blockIdx.x) * 2 + (s.head ? 0 : 1)) * L::kTiles + tile) * kRows : -1;
-                    rows_again<D, kBf16>(a, e);
-                }
-            } else if (ok && live) {
+            if (ok && live && !again) {
                 RowEnd e;
                 e.ot = tmem + lanes + 2 * kKeys + o * D + col0;
                 e.rows = rows - warp * 32;
@@ -1333,6 +1356,8 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
             turn ^= 1;
         }
     }
+    // (this warp has seen the flag of every segment that is looked at)
+    if (ok && reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[2]) flagged_rows<D, kBf16>(a, c.range, items, wg);
 }
 
 // ------------------------------------------------------------ kernel
@@ -1368,6 +1393,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
         mbar_init(c.base + L::drain, 1);
         *c.abort_flag = 0;
+        reinterpret_cast<volatile uint32_t*>(attn_smem + L::odd)[2] = 0;
         fence_mbar_init();
     }
     if (warp == kMmaWarp) {
