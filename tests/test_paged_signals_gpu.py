@@ -10,11 +10,14 @@ from tests.paged_signals import TILE, check_signals, signal_arrays
 pytestmark = pytest.mark.gpu
 
 
-def _check(sp, ctx, new, hq, hk, d, bs, dtype, seed, **kw):
+def _check(sp, ctx, new, hq, hk, d, bs, dtype, seed, scale=0.0, **kw):
     import torch
 
     from tests.paged_cases import torch_dtype
     a = signal_arrays(seed, ctx, new, hq, hk, d, bs, dtype)
+    if scale:   # the same logits by another way
+        a["q"] = a["q"] * 0.5
+        kw["scale"] = scale
     t = {n: torch.from_numpy(x).cuda() for n, x in a.items()}
     q, k_pool, v_pool = [t[n].to(torch_dtype(dtype)) for n in ("q", "k_pool", "v_pool")]
     out = torch.zeros_like(q)
@@ -55,3 +58,9 @@ def test_a_batch_laid_out_by_its_own_kernel(cuda_lib):
     ctx = [7 * (i % 90) for i in range(500)]
     ctx[3] = ctx[250] = ctx[499] = 9001
     _check(cuda_lib, ctx, [1 + (i % 7 == 0) for i in range(500)], 4, 2, 64, 16, "bf16", 5)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, "fp16"), (128, "bf16"), (256, "bf16")])
+def test_a_scale_of_the_callers(cuda_lib, d, dtype):
+    _check(cuda_lib, [5000, 3], [4, 150], 4, 2, d, 16, dtype, d, scale=2.0 * d ** -0.5)
+    _check(cuda_lib, [700], [60], 4, 2, d, 16, dtype, d, scale=0.01)
