@@ -463,7 +463,8 @@ typedef struct sp_block_shape {
  *   before the first call.
  * Nothing is allocated and no other memory is used, so a captured call can
  * be replayed. Outputs may not overlap inputs (block_table aside) or one
- * another: equal pointers are SP_ERR_INVALID_ARG. */
+ * another: equal pointers are SP_ERR_INVALID_ARG, and so are pointers that
+ * are not 4-byte aligned. */
 int sp_block_tables(const sp_block_shape* shape, const int32_t* ctx_len, const int32_t* new_off,
                     const int32_t* free_blocks, const int32_t* n_free, int32_t* block_table,
                     int32_t* slot_map, int32_t* kv_len, int32_t* n_left, int32_t* status,
@@ -506,8 +507,9 @@ typedef struct sp_append_shape {
  *   at or past pool_tokens (nothing is stored for the row) or a position
  *   outside [0, max_pos) (the row is skipped). Never lowered.
  * Outputs may not overlap inputs (q_out = q aside) or one another; equal
- * pointers are SP_ERR_INVALID_ARG. Base pointers are 16-byte aligned
- * (SP_ERR_INVALID_ARG) and strides multiples of 8 (SP_ERR_UNSUPPORTED). */
+ * pointers are SP_ERR_INVALID_ARG. Base pointers of the 16-bit tensors and
+ * cos_sin are 16-byte aligned, the others 4-byte aligned
+ * (SP_ERR_INVALID_ARG), and strides multiples of 8 (SP_ERR_UNSUPPORTED). */
 int sp_append_kv(const sp_append_shape* shape, const uint16_t* q, const uint16_t* k,
                  const uint16_t* v, const int32_t* slot_map, const int32_t* positions,
                  const float* cos_sin, const int32_t* n_new, uint16_t* q_out, uint16_t* k_pool,
@@ -570,9 +572,10 @@ int sp_paged_attention_workspace(const sp_paged_shape* shape, size_t* bytes);
  * - A bad q_off or kv_len (out of range, over 2^30, or more tokens than a
  *   table row holds) sets the device status SP_ERR_DEVICE and nothing is computed; a
  *   block id outside the pool sets it and reads pool row 0 instead.
- * out and lse may not overlap the inputs (equal pointers: SP_ERR_INVALID_ARG).
- * Strides times 2 bytes are multiples of 16 and base pointers 16-byte aligned
- * (SP_ERR_UNSUPPORTED and SP_ERR_INVALID_ARG otherwise). */
+ * out and lse may not overlap the inputs or one another (equal pointers:
+ * SP_ERR_INVALID_ARG). Strides times 2 bytes are multiples of 16
+ * (SP_ERR_UNSUPPORTED otherwise); base pointers of the 16-bit tensors are
+ * 16-byte aligned, the others 4-byte aligned (SP_ERR_INVALID_ARG otherwise). */
 int sp_paged_attention(const sp_paged_shape* shape, const sp_attn_params* params,
                        const int32_t* q_off, const int32_t* kv_len, const int32_t* block_table,
                        const uint16_t* q, const uint16_t* k_pool, const uint16_t* v_pool,

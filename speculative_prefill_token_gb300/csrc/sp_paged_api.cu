@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "sp_internal.h"
 #include "sp_paged.h"
@@ -13,6 +14,27 @@ namespace sp {
 namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+using Pointers = std::initializer_list<const void*>;
+
+// Whether all of them (null or not) are aligned to their 32-bit entries.
+bool words(Pointers all) {
+    for (const void* p : all)
+        if (!aligned(p, 4)) return false;
+    return true;
+}
+
+// Whether an output is one of the inputs, or another output.
+bool shared(Pointers outs, Pointers ins) {
+    for (const void* const* o = outs.begin(); o != outs.end(); ++o) {
+        if (!*o) continue;
+        for (const void* i : ins)
+            if (i == *o) return true;
+        for (const void* const* other = outs.begin(); other != o; ++other)
+            if (*other == *o) return true;
+    }
+    return false;
+}
 
 int to_status(cudaError_t e) { return e == cudaSuccess ? SP_OK : SP_ERR_CUDA; }
 
@@ -66,15 +88,9 @@ int sp_block_tables(const sp_block_shape* s, const int32_t* ctx_len, const int32
         return SP_ERR_INVALID_ARG;
     if ((s->n_tokens > 0 && !slot_map) || (s->free_capacity > 0 && !free_blocks)) return SP_ERR_INVALID_ARG;
     if (s->n_seqs > kMaxTableSeqs) return SP_ERR_UNSUPPORTED;
-    const int32_t* in[4] = {ctx_len, new_off, free_blocks, n_free};
-    const int32_t* out[5] = {block_table, slot_map, kv_len, n_left, status};
-    for (int i = 0; i < 5; ++i) {
-        if (!out[i]) continue;
-        for (int j = 0; j < 4; ++j)
-            if (out[i] == in[j]) return SP_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (out[i] == out[j]) return SP_ERR_INVALID_ARG;
-    }
+    if (!words({ctx_len, new_off, free_blocks, n_free, block_table, slot_map, kv_len, n_left, status}) ||
+        shared({block_table, slot_map, kv_len, n_left, status}, {ctx_len, new_off, free_blocks, n_free}))
+        return SP_ERR_INVALID_ARG;
     return to_status(launch_block_tables(s, ctx_len, new_off, free_blocks, n_free, block_table, slot_map, kv_len,
                                          n_left, status, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -97,12 +113,10 @@ int sp_append_kv(const sp_append_shape* s, const uint16_t* q, const uint16_t* k,
         return SP_ERR_INVALID_ARG;
     if ((q ? static_cast<int64_t>(s->n_q_heads) : 0) + 2 * static_cast<int64_t>(s->n_kv_heads) > kMaxHeads)
         return SP_ERR_UNSUPPORTED;
-    const uint16_t* out[3] = {k_pool, v_pool, q_out};
-    for (int i = 0; i < 3 && out[i]; ++i) {
-        if (out[i] == k || out[i] == v || (i < 2 && out[i] == q)) return SP_ERR_INVALID_ARG;
-        for (int j = 0; j < i; ++j)
-            if (out[i] == out[j]) return SP_ERR_INVALID_ARG;
-    }
+    if (!words({slot_map, positions, n_new, status}) ||
+        shared({k_pool, v_pool, q_out, status}, {k, v, slot_map, positions, cos_sin, n_new}) ||
+        shared({k_pool, v_pool, status}, {q}))
+        return SP_ERR_INVALID_ARG;
     if (q && q_out == q &&
         ((s->n_tokens > 1 && s->qo_stride_token != s->q_stride_token) ||
          (s->n_q_heads > 1 && s->qo_stride_head != s->q_stride_head)))
@@ -140,8 +154,9 @@ int sp_paged_attention(const sp_paged_shape* shape, const sp_attn_params* params
     if ((params->causal != 0 && params->causal != 1) || params->window < 0 ||
         (params->window > 0 && !params->causal) || !(std::isfinite(params->scale) && params->scale >= 0.0f))
         return SP_ERR_INVALID_ARG;
-    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) || out == q ||
-        out == k_pool || out == v_pool)
+    if (!aligned(q, 16) || !aligned(k_pool, 16) || !aligned(v_pool, 16) || !aligned(out, 16) ||
+        !words({q_off, kv_len, block_table, lse}) ||
+        shared({out, lse}, {q_off, kv_len, block_table, q, k_pool, v_pool, ws}))
         return SP_ERR_INVALID_ARG;
     if (!ws || !aligned(ws, 256) || ws_bytes < attn_workspace(shape)) return SP_ERR_WORKSPACE;
     return to_status(launch_paged_attention(shape, params, q_off, kv_len, block_table, q, k_pool, v_pool, out, lse,
