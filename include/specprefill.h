@@ -461,6 +461,13 @@ typedef struct sp_block_shape {
  *   -1. A block id outside [0, pool_blocks) also raises SP_ERR_DEVICE; the
  *   tokens of that block get slot -1. The word is never lowered: zero it
  *   before the first call.
+ * A step that took nothing has to leave the lengths as they are: its kv_len is
+ * no length of the cache, and as the next call's ctx_len it would have every
+ * request begin anew over the blocks that it holds. Where steps are chained on
+ * the device, let kv_len and n_left become ctx_len and n_free only where status
+ * is still 0 (ctx_len and n_free themselves are inputs, so they hold what was
+ * before the step, and the same step can be taken again). A block that a
+ * request fills further belongs to it alone; full ones may be shared.
  * Nothing is allocated and no other memory is used, so a captured call can
  * be replayed. Outputs may not overlap inputs (block_table aside) or one
  * another: equal pointers are SP_ERR_INVALID_ARG, and so are pointers that

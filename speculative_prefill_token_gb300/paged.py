@@ -110,8 +110,10 @@ def block_tables(ctx_len, new_off, free_blocks, n_free, block_table, block_size:
     token; ``n_left`` [1] counts the blocks that stay free. ``status`` [1],
     zeroed by the caller, is raised to a STATUS code when the free list is too
     short (SP_ERR_CAPACITY) or a length is out of range (SP_ERR_DEVICE): the
-    call then takes nothing, every slot is -1 and every kv_len 0.
-    ``pool_blocks`` bounds the block ids."""
+    call then takes nothing, every slot is -1 and every kv_len 0. Where steps
+    are chained on the device, kv_len and n_left become ctx_len and n_free only
+    where status is still 0: ``ctx_len.copy_(torch.where(status == 0, kv_len,
+    ctx_len))``, and n_free alike. ``pool_blocks`` bounds the block ids."""
     if slot_map is None:
         if n_tokens is None:
             raise ValueError("give slot_map or n_tokens")
