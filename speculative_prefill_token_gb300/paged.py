@@ -21,7 +21,7 @@ import importlib.machinery
 import importlib.util
 import os
 
-from . import LIB_PATH, _check, lib
+from . import LIB_PATH, _build, _check, lib
 
 
 class _BlockShape(ctypes.Structure):
@@ -76,8 +76,9 @@ def torch_side():
         import torch  # noqa: F401  (its libraries are loaded before the extension that uses them)
         lib()
         path = os.path.join(os.path.dirname(LIB_PATH), "_paged_torch.so")
-        if not os.path.exists(path):
-            raise RuntimeError(f"_paged_torch.so not built ({path}); run __graft_entry__.build()")
+        if not _build.torch_side_fits():
+            raise RuntimeError(f"_paged_torch.so not built for this torch and Python ({path}); "
+                               "run __graft_entry__.build()")
         loader = importlib.machinery.ExtensionFileLoader("_paged_torch", path)
         spec = importlib.util.spec_from_file_location("_paged_torch", path, loader=loader)
         side = importlib.util.module_from_spec(spec)
