@@ -143,8 +143,8 @@ float* floats(const at::Tensor* t, const char* name, int dev) {
 }
 
 // (ctx_len, new_off, free_blocks, n_free, block_table, block_size, n_tokens,
-//  slot_map, kv_len, n_left, status, pool_blocks, stream); n_tokens < 0: all
-// of slot_map, pool_blocks <= 0: as many as 31-bit slots allow.
+//  slot_map, kv_len, n_left, status, pool_blocks, stream); n_tokens None: all
+// of slot_map, pool_blocks None: as many as 31-bit slots allow.
 int call_block_tables(PyObject* const* a) {
     const at::Tensor &ctx = need(a[0], "ctx_len"), &slots = need(a[7], "slot_map");
     const int dev = device_of(ctx, "ctx_len");
@@ -152,12 +152,10 @@ int call_block_tables(PyObject* const* a) {
     s.n_seqs = count(ctx.numel(), "ctx_len");
     s.block_size = int32(a[5], "block_size");
     int32_t* tab = table(need(a[4], "block_table"), s.n_seqs, dev, &s.table_stride);
-    const int64_t n = integer(a[6]);
-    s.n_tokens = count(n < 0 ? slots.numel() : n, "slot_map");
+    s.n_tokens = a[6] == Py_None ? count(slots.numel(), "slot_map") : int32(a[6], "n_tokens");
     const at::Tensor& free = need(a[2], "free_blocks");
     s.free_capacity = count(free.numel(), "free_blocks");
-    const int32_t bound = int32(a[11], "pool_blocks");
-    s.pool_blocks = bound > 0 ? bound : INT32_MAX / (s.block_size > 0 ? s.block_size : 1);
+    s.pool_blocks = a[11] == Py_None ? INT32_MAX / (s.block_size > 0 ? s.block_size : 1) : int32(a[11], "pool_blocks");
     return sp_block_tables(&s, ints(&ctx, 1, "ctx_len", dev), ints(&need(a[1], "new_off"), s.n_seqs + 1ll, "new_off", dev),
                            ints(&free, 0, "free_blocks", dev), ints(&need(a[3], "n_free"), 1, "n_free", dev), tab,
                            ints(&slots, s.n_tokens, "slot_map", dev),

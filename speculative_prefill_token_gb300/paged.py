@@ -124,8 +124,8 @@ def block_tables(ctx_len, new_off, free_blocks, n_free, block_table, block_size:
     if n_left is None:
         n_left = _new(1, ctx_len.dtype, ctx_len, stream)
     rc = (_side or torch_side()).block_tables(
-        ctx_len, new_off, free_blocks, n_free, block_table, block_size, -1 if n_tokens is None else n_tokens, slot_map,
-        kv_len, n_left, status, pool_blocks or 0, _handle(stream))
+        ctx_len, new_off, free_blocks, n_free, block_table, block_size, n_tokens, slot_map, kv_len, n_left, status,
+        pool_blocks, _handle(stream))
     if rc:
         _check(rc, "sp_block_tables")
     return slot_map, kv_len, n_left

@@ -75,3 +75,18 @@ def test_a_step_that_is_not_served_leaves_the_chain_as_it_was(cuda_lib, captured
         step()
         want = paged_oracle.block_tables(want[2], off, free, want[3], want[0], bs, batch)
         assert int(s["status"]) == 0 and unchanged() and np.array_equal(host(s["slots"]), want[1])
+
+
+def test_bounds_that_bound_nothing_are_refused(cuda_lib):
+    """pool_blocks and n_tokens below their range are errors, not 'no bound'."""
+    import torch
+    sp = cuda_lib
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = (i32(0), i32(0, 2), i32(0, 1), i32(2), i32(-1, -1)[None], 4)
+    for kw in (dict(pool_blocks=0), dict(pool_blocks=-1), dict(n_tokens=-1)):
+        slots = i32(5, 5)
+        with pytest.raises(sp.SpecPrefillError):
+            sp.block_tables(*args, slot_map=slots, **kw)
+        assert slots.tolist() == [5, 5]
+    assert sp.block_tables(*args, slot_map=i32(5, 5), pool_blocks=2)[0].tolist() == [4, 5]
+    assert sp.block_tables(*args, slot_map=i32(5, 5, 5), n_tokens=2)[0].tolist() == [4, 5, 5]
