@@ -39,21 +39,26 @@
 // chunks), even and odd key tiles, with an accumulator each for d <= 128
 // (joined from tensor memory at the end) and one accumulator for d = 256.
 //
-// What bounds it (of 6,693 GB/s and 1,908 TFLOP/s measured):
+// What bounds it (of 6,693 GB/s of a copy, 7,200 of a plain read of 2.6 GB and
+// 1,908 TFLOP/s measured):
 //   decode steps    the stream of keys and values: 64 requests of 2K to 32K
-//                   tokens, 16 + 4 heads of 128, 375 us, 6.9 TB/s; 16 of 4K to
-//                   16K, 8 + 2 heads of 256, 57 us, 5.3 TB/s (of it 4.5 us until
-//                   the first copy, and 2 to 5 us of the join)
+//                   tokens, 16 + 4 heads of 128, 366 to 376 us, 6.9 to 7.1 TB/s;
+//                   16 of 4K to 16K, 8 + 2 heads of 256, 57 us, 5.3 TB/s (of it
+//                   4.5 us until the first copy, and 2 to 5 us of the join)
 //   d = 128, long   the chain logits -> softmax (some 1,700 cycles) -> weights
 //                   of a tile, which two streams do not hide in full: 4,096
-//                   tokens over 39K, 16 + 4 heads, 805 to 864 us, 1,450 to
-//                   1,550 TFLOP/s
+//                   tokens over 39K, 16 + 4 heads, 860 to 870 us, 1,440 to
+//                   1,455 TFLOP/s
 //   d = 256         shared memory: operands of both products and the copies
 //                   take 2,560 cycles of its bandwidth a tile, the products
-//                   2,048: 4,916 tokens, 8 + 2 heads, 96 us, 1,030 TFLOP/s (10 of
+//                   2,048: 4,916 tokens, 8 + 2 heads, 95 us, 1,045 TFLOP/s (10 of
 //                   them the join, some 4 each of a CTA's two items' ends)
-//   d = 64          the softmax: its instructions take twice the products' time
-//   single rows     latency: 9.3 us for a token over 512
+//   d = 64          latency of the softmax's chain: two of its warps on each
+//                   scheduler, each tensor-memory load, maximum, exponentials and
+//                   store in turn. No pipe is full: a prompt of 2,700 tokens, 8 +
+//                   2 heads, has an instruction in 24 % of the issue slots, the
+//                   tensor and exponential pipes busy 15 % each
+//   single rows     latency: 9.5 us for a token over 512
 //
 // Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT
 // in the workspace status, and the CTA drains its copies and MMAs in flight
@@ -970,6 +975,10 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
     const bool mine = static_cast<int>(threadIdx.x & 31) < e.rows;
     const bool split = e.part >= 0;
     const bool none = e.l == 0.0f && !split;
+    // (the approximate reciprocal and, for lse, logarithm are off by 2^-22: with
+    // the exact ones out is the same to four digits of its error, lse is 0.5e-6 in
+    // place of 0.7e-6 off at 8.5, where a step of 32 bits is 1e-6, and a prompt at
+    // d = 256 and the mixed batch take 1 % longer)
     const float inv = split ? 1.0f : none ? 0.0f : __fdividef(1.0f, e.l);
     const float e0 = e.f0 * inv, e1 = e.f1 * inv;
     char* dst = split ? reinterpret_cast<char*>(a.part_o + static_cast<int64_t>(e.part) * D + e.col0)
@@ -1220,6 +1229,12 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                             }
                         }
                     }
+                    // The weights are rounded to 16 bits, the type of the tensor
+                    // cores' operands (half a step each, not their sum, which stays
+                    // as it is): beside the rounding of the result, which any form
+                    // has, that takes the relative error over long contexts from
+                    // 0.0017 to 0.0023 (bf16). Their exponentials are off by 2^-22
+                    // at most, results below 2^-126 are 0.
                     const float shift = (m == -INFINITY ? 0.0f : -m) + kBias;
                     const float2 scale = make_float2(a.scale2, a.scale2), move2 = make_float2(shift, shift);
                     float2 sum[4];

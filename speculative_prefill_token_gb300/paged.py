@@ -14,6 +14,9 @@ after the scoring call that gave ``out``:
   # for each layer:
   q = append_kv(k, v, slots, k_pool, v_pool, q=q, positions=out.kept_pos, cos_sin=cos_sin, n_new=out.n_kept)
   o = paged_attention(q, out.kept_off, kv_len, table, k_pool, v_pool, ws=ws)
+
+Forward only: no gradient is recorded, and tensors are written without moving
+their version counters.
 """
 
 import ctypes
@@ -174,7 +177,8 @@ def paged_attention(q, q_off, kv_len, block_table, k_pool, v_pool, causal: bool 
     Returns ``out`` (like q; rows behind q_off[B] are not written); ``lse``
     (fp32 [T, Hq], optional) receives the log-sum-exp of the scaled logits.
     A row that sees nothing gives 0 and -inf. ``ws`` from
-    make_attention_workspace, with its status in device_status."""
+    make_attention_workspace, with its status in device_status; without it
+    the call allocates one (20 to 40 MB), whose status is lost."""
     if out is None:
         out = _new(q.shape, q.dtype, q, stream)
     if q.shape[0] == 0:
