@@ -47,8 +47,8 @@
 //                   4.5 us until the first copy, and 2 to 5 us of the join)
 //   d = 128, long   the chain logits -> softmax (some 1,700 cycles) -> weights
 //                   of a tile, which two streams do not hide in full: 4,096
-//                   tokens over 39K, 16 + 4 heads, 860 to 870 us, 1,440 to
-//                   1,455 TFLOP/s
+//                   tokens over 39K, 16 + 4 heads, 860 to 897 us, 1,395 to
+//                   1,455 TFLOP/s by the machine's clock under power
 //   d = 256         shared memory: operands of both products and the copies
 //                   take 2,560 cycles of its bandwidth a tile, the products
 //                   2,048: 4,916 tokens, 8 + 2 heads, 95 us, 1,045 TFLOP/s (10 of
