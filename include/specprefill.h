@@ -588,6 +588,234 @@ int sp_paged_attention(const sp_paged_shape* shape, const sp_attn_params* params
                        const uint16_t* q, const uint16_t* k_pool, const uint16_t* v_pool,
                        uint16_t* out, float* lse, void* ws, size_t ws_bytes, sp_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * A cache in 4 bits
+ *
+ * The paged cache of the target's step ("SpecPrefill — Implementation Guide",
+ * §How It Works / Sparse Prefill) held in 4.5 bits an element: a value is an
+ * e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 or a negative of them) times an e4m3
+ * scale shared by 16 neighbours of a row, times a factor that the caller gives
+ * for the whole pool. Number times scale is exact in bf16 and fp16.
+ *
+ * A pool holds, for block b and KV head h, block_size / 8 records of 9 d / 2
+ * bytes: 8 tokens' codes (d / 2 bytes each, element 2 i in the low and 2 i + 1 in
+ * the high four bits of byte i; bit 3 of a code is the sign), then their scales
+ * (d / 16 bytes each). The records of a block and head follow one another; blocks
+ * and heads are `stride_block` and `stride_head` bytes apart, multiples of 16.
+ * head_dim is 64, 128 or 256, block_size 8, 16, 32, 64 or a multiple of 128. */
+
+/* Shapes and strides of sp_append_kv_fp4 (16-bit tensors in elements, pools in
+ * bytes). */
+typedef struct sp_append_fp4_shape {
+    int32_t n_tokens;      /* >= 1 rows of q, k, v and slot_map */
+    int32_t n_q_heads;     /* >= 1 with queries; ignored without */
+    int32_t n_kv_heads;    /* >= 1; queries, keys and values have at most 65536 heads together */
+    int32_t head_dim;      /* 64, 128 or 256 */
+    int32_t rotary_dim;    /* 0 (no rotation) or a multiple of 16, at most head_dim */
+    int32_t max_pos;       /* rows of cos_sin (ignored when rotary_dim is 0) */
+    int32_t dtype;         /* SP_DTYPE_BF16 or SP_DTYPE_F16, of q, k, v and q_out */
+    int32_t block_size;
+    int64_t pool_blocks;   /* blocks of each pool; pool_blocks * block_size < 2^31 */
+    int64_t q_stride_token, q_stride_head, qo_stride_token, qo_stride_head;
+    int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
+    int64_t kp_stride_block, kp_stride_head, vp_stride_block, vp_stride_head;
+    float k_scale, v_scale;  /* factors of the pools, finite and > 0 */
+} sp_append_fp4_shape;
+
+/* sp_append_kv into pools of 4 bits. Queries are rotated as there; a row x of
+ * a rotated key (in 32 bits, not rounded before) or of a value is stored as
+ *   y = x / factor,   s_g = max(e4m3(min(max |y_g| / 6, 448)), 2^-9),
+ *   code_i = e2m1(y_i / s_g)   for each group g of 16 neighbours,
+ * every operation in 32 bits and rounded to nearest, e4m3() and e2m1() to the
+ * nearest number with ties to even, e2m1 saturating at 6. A group that holds
+ * an infinity or NaN gets the scale NaN, and reads back as NaN. The rest is as
+ * for sp_append_kv: slot -1 stores nothing, slots of different rows must differ,
+ * a bad slot or position raises SP_ERR_DEVICE in `status`, equal pointers and
+ * misaligned ones are SP_ERR_INVALID_ARG, strides off 16 bytes
+ * SP_ERR_UNSUPPORTED. */
+int sp_append_kv_fp4(const sp_append_fp4_shape* shape, const uint16_t* q, const uint16_t* k,
+                     const uint16_t* v, const int32_t* slot_map, const int32_t* positions,
+                     const float* cos_sin, const int32_t* n_new, uint16_t* q_out, uint8_t* k_pool,
+                     uint8_t* v_pool, int32_t* status, sp_stream_t stream);
+
+typedef struct sp_unpack_fp4_shape {
+    int32_t n_kv_heads;    /* >= 1, at most 65536 */
+    int32_t head_dim;      /* 64, 128 or 256 */
+    int32_t block_size;
+    int32_t dtype;         /* of out */
+    int64_t pool_blocks;
+    int64_t stride_block, stride_head;          /* of the pool, in bytes */
+    int64_t n_rows;        /* rows of out */
+    int64_t o_stride_token, o_stride_head;      /* of out, in elements */
+    float scale;           /* factor of the pool, finite */
+    int32_t reserved;      /* 0 */
+} sp_unpack_fp4_shape;
+
+/* Rows of a 4-bit pool as 16-bit values (number * scale * factor in 32 bits,
+ * rounded once; without a rounding when factor is a power of two and nothing
+ * leaves the type's range). Row r of out is the pool's row slots[r]
+ * (device, int32), or row r itself when slots is null (n_rows is then
+ * pool_blocks * block_size). A slot of -1 gives zeros; one outside the pool
+ * raises SP_ERR_DEVICE in `status` (device, one int32, nullable) and gives
+ * zeros too. The values are what sp_attn_importance_kv, sp_paged_attention and
+ * the gathers take as a 16-bit cache. */
+int sp_unpack_fp4(const sp_unpack_fp4_shape* shape, const uint8_t* pool, const int32_t* slots,
+                  uint16_t* out, int32_t* status, sp_stream_t stream);
+
+/* Shapes and strides of sp_paged_attention_fp4 (q and out in elements, pools
+ * in bytes). */
+typedef struct sp_fp4_shape {
+    int32_t n_seqs;        /* 1 <= B <= 65536 requests */
+    int32_t n_q_heads;     /* Hq <= 65536, Hq % Hk == 0, G = Hq / Hk <= 128 */
+    int32_t n_kv_heads;    /* Hk >= 1 */
+    int32_t head_dim;      /* d in {64, 128, 256} */
+    int32_t dtype;         /* SP_DTYPE_BF16 or SP_DTYPE_F16: q and out */
+    int32_t block_size;    /* 8, 16, 32, 64 or a multiple of 128 */
+    int32_t table_stride;  /* >= 1 table entries of a request */
+    int32_t n_tokens;      /* 1 to 2^30 rows of q, out and lse; n_tokens * Hq < 2^31 */
+    int32_t max_new;       /* most new tokens of a request, at most n_tokens; 0: n_tokens */
+    int32_t reserved;      /* 0 */
+    int64_t dense_tokens;  /* cached tokens that requests with many new ones may have together to be
+                              read through 16 bits (below); 0: none */
+    int64_t pool_blocks;   /* blocks of each pool; pool_blocks * block_size < 2^31 */
+    int64_t q_stride_token, q_stride_head, o_stride_token, o_stride_head;
+    int64_t k_stride_block, k_stride_head, v_stride_block, v_stride_head;
+} sp_fp4_shape;
+
+typedef struct sp_fp4_params {
+    int32_t causal;        /* as in sp_attn_params */
+    int32_t window;
+    float scale;           /* logit scale; 0 selects 1/sqrt(head_dim) */
+    float k_scale;         /* factors of the pools, finite and > 0 */
+    float v_scale;
+    int32_t spin_limit;    /* polls before a device wait gives up; <= 0 selects the default */
+} sp_fp4_params;
+
+/* Bytes of device workspace of sp_paged_attention_fp4 for this shape on the
+ * current device (prepared and read as that of sp_paged_attention). It holds
+ * 4 * Hk * head_dim bytes for each of dense_tokens. */
+int sp_paged_attention_fp4_workspace(const sp_fp4_shape* shape, size_t* bytes);
+
+/* sp_paged_attention over 4-bit pools: the same rows, masks, outputs and error
+ * behaviour, with s_j = scale k_scale <q, k_j> and out = v_scale sum p v / sum p.
+ * Logits, statistics and sums are held in 32 bits; weights are rounded to fp16
+ * (scaled so that the largest is 2^6 to 2^14) for the product with the values, or to the
+ * tensors' type where the values are read through 16 bits. bf16 queries are
+ * scaled by a power of two for each row and head and taken as fp16, which is
+ * exact for elements down to 2^-31 of the row's largest.
+ * Requests whose new tokens make many rows are computed over a 16-bit copy of
+ * their cached tokens, in the workspace, as long as those of all such requests
+ * of the call fit into dense_tokens (in the requests' order); the others, and
+ * all decode steps, are computed from the 4-bit rows. A request with more new
+ * tokens than max_new sets SP_ERR_DEVICE, and nothing is computed.
+ * Cached rows that a query is masked from may hold anything, scales that are
+ * NaN included. */
+int sp_paged_attention_fp4(const sp_fp4_shape* shape, const sp_fp4_params* params,
+                           const int32_t* q_off, const int32_t* kv_len, const int32_t* block_table,
+                           const uint16_t* q, const uint8_t* k_pool, const uint8_t* v_pool,
+                           uint16_t* out, float* lse, void* ws, size_t ws_bytes, sp_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of the cache
+ *
+ * A block may belong to several requests. `shared` (device, int32 [pool_blocks])
+ * counts its holders beyond the first: 0 for a block of one request and for a
+ * free one, so that blocks that sp_block_tables takes need no entry. */
+
+typedef struct sp_copy_shape {
+    int32_t n_pools;       /* 1 to SP_MAX_COPY_POOLS pools of one shape */
+    int32_t n_entries;     /* entries of src and dst */
+    int32_t rows;          /* consecutive slots of an entry: 1, or block_size */
+    int32_t block_size;
+    int32_t n_kv_heads;
+    int32_t head_dim;      /* 16-bit pools: a multiple of 8; 4-bit pools: 64, 128 or 256 */
+    int32_t fp4;           /* 0: 16-bit pools [blocks][block_size][Hk][d]; 1: 4-bit pools */
+    int32_t n_seqs;        /* with block_table: its rows */
+    int32_t table_stride;  /* with block_table: entries of a row */
+    int32_t reserved;      /* 0 */
+    int64_t pool_blocks;
+    int64_t stride_block, stride_token, stride_head;   /* of every pool, in bytes (4-bit: no token stride) */
+} sp_copy_shape;
+
+#define SP_MAX_COPY_POOLS 256
+
+/* Copies rows of the cache in every pool (keys and values of all layers).
+ * Entry i copies the `rows` slots from src[i] * rows on to those from dst[i] * rows on:
+ * single tokens, or whole blocks (the copies that sp_fork_blocks asks for). With
+ * block_table and src_off (int32 [n_seqs + 1], from 0, non-decreasing; rows = 1),
+ * entry i of request b, src_off[b] <= i < src_off[b + 1], copies the request's cached
+ * token src[i], which lies in block block_table[b][src[i] / block_size]: with a
+ * scoring call's kept_pos and kept_off, and slots that sp_block_tables gave for
+ * new rows of the table, this moves the kept tokens of cached prompts to blocks
+ * of their own.
+ * - src, dst (device, n_entries int32): an entry with a negative src or dst
+ *   copies nothing. The slots written differ from one another and from all that are
+ *   read.
+ * - n_used (device, one int32, nullable): the entries in use, clamped to
+ *   [0, n_entries] (and to src_off[n_seqs] with block_table).
+ * - status (device, one int32, nullable): raised to SP_ERR_DEVICE by a slot, a
+ *   token or a block id out of range; that entry copies nothing.
+ * - pools (host array of n_pools device pointers), 16-byte aligned. */
+int sp_copy_kv(const sp_copy_shape* shape, void* const* pools, const int32_t* src, const int32_t* dst,
+               const int32_t* block_table, const int32_t* src_off, const int32_t* n_used,
+               int32_t* status, sp_stream_t stream);
+
+typedef struct sp_pages_shape {
+    int32_t n_seqs;        /* 1 <= B <= 16384 rows of the table */
+    int32_t n_forks;       /* sp_fork_blocks: entries of src and dst, 1 to 16384 */
+    int32_t block_size;    /* >= 1 */
+    int32_t table_stride;  /* >= 1 entries of a table row */
+    int32_t pool_blocks;   /* entries of shared; pool_blocks * block_size < 2^31 */
+    int32_t free_capacity; /* entries of free_blocks */
+} sp_pages_shape;
+
+/* Forks requests: row dst[i] of the table becomes a request with the cached
+ * tokens of row src[i]. Its full blocks are src's own, each with one holder more;
+ * a begun last block is taken anew, from the end of the free list, in the order
+ * of i, and left to be copied: copy_src[i] and copy_dst[i] name the blocks (-1
+ * where there is none), as sp_copy_kv takes them with rows = block_size.
+ * - src, dst (device, n_forks int32): src[i] < 0 forks nothing. The rows dst of
+ *   the others differ from one another and from all of src, and hold nothing
+ *   (ctx_len 0).
+ * - ctx_len (device, B int32): cached tokens of every row; kv_len (device, B
+ *   int32, written): the same after the forks.
+ * - block_table (device, int32 [B][table_stride]), shared (device, int32
+ *   [pool_blocks]): written in place.
+ * - free_blocks, n_free, n_left: as in sp_block_tables.
+ * - status (device, one int32, nullable): raised to SP_ERR_CAPACITY when the free
+ *   list is too short, to SP_ERR_DEVICE when an entry, a length or n_free is out of
+ *   range or a dst breaks the rule above. The call then forks nothing: table and
+ *   counts stay, kv_len is ctx_len, n_left is n_free and all copies are -1. A block
+ *   id outside [0, pool_blocks) also raises SP_ERR_DEVICE, and is counted nowhere.
+ * Outputs may not be inputs or one another (SP_ERR_INVALID_ARG). */
+int sp_fork_blocks(const sp_pages_shape* shape, const int32_t* src, const int32_t* dst,
+                   const int32_t* ctx_len, int32_t* block_table, int32_t* shared,
+                   const int32_t* free_blocks, const int32_t* n_free, int32_t* kv_len,
+                   int32_t* copy_src, int32_t* copy_dst, int32_t* n_left, int32_t* status,
+                   sp_stream_t stream);
+
+/* Cuts every request from ctx_len[b] to new_len[b] <= ctx_len[b] cached tokens
+ * (0: the request ends) and lets go of the blocks behind them: a block's count of
+ * holders goes down by the requests that let it go, and the blocks that nobody
+ * holds any more are put behind the n_free free ones, in increasing order of
+ * their ids, whatever the order of the requests.
+ * - ctx_len, new_len (device, B int32); kv_len (device, B int32, written): new_len.
+ * - block_table (device, int32 [B][table_stride]): read only; entries behind a
+ *   request's last block count for nothing afterwards.
+ * - shared, free_blocks (device): written in place; n_left (device, one int32,
+ *   written): the blocks that are free after the call.
+ * - status (device, one int32, nullable): raised to SP_ERR_DEVICE when a length or
+ *   n_free is out of range, or a block is let go more often than it is held (as
+ *   far as `shared`, whose entries are 0 or more, shows it); to SP_ERR_CAPACITY when
+ *   free_blocks is too short. The call then frees nothing: counts and list stay,
+ *   kv_len is ctx_len, n_left is n_free. A block id outside [0, pool_blocks) also
+ *   raises SP_ERR_DEVICE, and is counted nowhere.
+ * Outputs may not be inputs or one another (SP_ERR_INVALID_ARG). */
+int sp_free_blocks(const sp_pages_shape* shape, const int32_t* ctx_len, const int32_t* new_len,
+                   const int32_t* block_table, int32_t* shared, int32_t* free_blocks,
+                   const int32_t* n_free, int32_t* kv_len, int32_t* n_left, int32_t* status,
+                   sp_stream_t stream);
+
 /* Synchronise `stream`, then read (and, when `clear` is non-zero, reset)
  * the workspace's sticky device status word into *status_host. */
 int sp_get_device_status(void* ws, size_t ws_bytes, sp_stream_t stream, int clear,

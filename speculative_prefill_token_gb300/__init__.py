@@ -46,6 +46,14 @@ __all__ = [
     "append_kv",
     "make_attention_workspace",
     "paged_attention",
+    "make_pool_fp4",
+    "append_kv_fp4",
+    "unpack_fp4",
+    "make_attention_fp4_workspace",
+    "paged_attention_fp4",
+    "copy_kv",
+    "fork_blocks",
+    "free_blocks",
     "STATUS",
 ]
 
@@ -642,3 +650,6 @@ def device_status(ws, stream=None, clear: bool = True) -> int:
 
 from . import paged  # noqa: E402  (uses the helpers above)
 from .paged import append_kv, block_tables, make_attention_workspace, paged_attention  # noqa: E402
+from . import fp4, pages  # noqa: E402
+from .fp4 import append_kv_fp4, make_attention_fp4_workspace, make_pool_fp4, paged_attention_fp4, unpack_fp4  # noqa: E402
+from .pages import copy_kv, fork_blocks, free_blocks  # noqa: E402

@@ -23,7 +23,8 @@ TORCH_LIB = os.path.join(HERE, "_paged_torch.so")
 TORCH_SOURCE = "sp_paged_torch.cpp"
 TORCH_STAMP = os.path.join(BUILD, "paged_torch.stamp")
 SOURCES = ["sp_api.cu", "sp_stages.cu", "sp_logits_tc.cu", "sp_logits_simt.cu", "sp_noalloc.cu", "sp_post.cu",
-           "sp_rows.cu", "sp_head_pool.cu", "sp_cache.cu", "sp_attn.cu", "sp_paged_api.cu"]
+           "sp_rows.cu", "sp_head_pool.cu", "sp_cache.cu", "sp_attn.cu", "sp_paged_api.cu", "sp_fp4_cache.cu",
+           "sp_fp4_attn.cu", "sp_pages.cu", "sp_fp4_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

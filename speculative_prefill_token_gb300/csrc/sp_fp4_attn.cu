@@ -1,0 +1,1012 @@
+// Attention of new tokens over a block-paged cache in 4 bits ("SpecPrefill —
+// Implementation Guide", §How It Works / Sparse Prefill: the target's decode
+// steps and short chunks over the kept tokens' cache).
+//
+// For a query row (token i of request b, head h) with visible cache indices
+// [lo, hi), and KV head g = h / G,
+//   out = v_scale sum_j exp2(y_j - m) v_j / sum_j exp2(y_j - m),
+//   y_j = scale k_scale log2(e) <q, k_j>,
+// where k_j and v_j are numbers times their group's scale, exact in fp16.
+//
+// The codes never exist as 16-bit values outside registers. A warp takes a tile
+// of 64 keys alone: it converts the key codes into the left operand of an
+// m16n8k16 product (16 keys x 16 elements; the right operand are 8 query rows),
+// keeps the logits in registers, and converts the value codes into the left
+// operand of the second product (16 elements x 16 keys), whose right operand
+// are the transposed weights. The elements of a row are dealt to the lanes so
+// that every lane's codes are consecutive bytes of one load: the sum over the
+// elements, and the order of the result's elements, may be permuted freely.
+// (Operands of tcgen05.mma lie in shared or tensor memory: writing 16-bit values there
+// and reading them again takes 4 of the 3.6 times more bytes than the codes
+// themselves from the shared memory's 128 bytes a cycle, where HBM delivers 23.5
+// bytes of codes a cycle and SM. From registers, mma.sync needs 0.32 of its rate.)
+//
+// Work. The new tokens x the G heads of a KV head are rows; an item is up to
+// 8 or 16 rows of a request and KV head, its unit a tile of 64 keys. All units
+// of all items are cut into equal contiguous ranges, one for each CTA (one CTA an
+// SM). A warp loads the codes of the CTA's tiles into a ring of stages by bulk
+// copies (a run of 8-token records each); tile i of the CTA goes to warp i mod 8.
+// The warps' results are joined at the end of an item, those of CTAs that share
+// an item by another kernel, in their order: results do not depend on timing.
+//
+// Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT in
+// the workspace status, and the CTA's copies in flight land before it returns.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "sp_device.cuh"
+#include "sp_fp4.cuh"
+#include "sp_fp4.h"
+#include "sp_internal.h"
+#include "sp_paged.h"
+#include "sp_ptx.cuh"
+
+namespace sp {
+namespace {
+
+constexpr int kTileKeys = 64;
+constexpr int kTileRecs = kTileKeys / kFp4Rows;
+constexpr int kWarps = 8;                    // that compute
+constexpr int kThreads = 32 * (kWarps + 1);  // and the one that loads
+constexpr int kItemCost = 8;                 // of an item besides its tiles, in tiles
+constexpr int kLocalSeqs = 1024;             // requests of a plan made by every CTA
+constexpr int kPlanThreads = 1024;
+constexpr int kMaxGrid = 256;
+constexpr int64_t kDrainSpin = int64_t(1) << 22;
+constexpr float kSlack = 8.0f;               // log2 units the reference may lag behind the maximum
+constexpr float kBias = 6.0f;                // fp16 weights are scaled by 2^6: normal down to 2^-20 of the reference
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kJoinThreads = 128;
+
+// Where a CTA's range starts: key tile `off` of item `gj` (KV head, row tile) of
+// request b. b = n_seqs: the end of everything.
+struct alignas(16) Start {
+    int32_t b, gj, off, pad;
+};
+
+struct Args {
+    const int32_t* q_off;
+    const int32_t* kv_len;
+    const int32_t* table;
+    const int32_t* dense;      // [B] or null: requests computed elsewhere (>= 0)
+    const uint16_t* q;
+    const uint8_t* k;
+    const uint8_t* v;
+    uint16_t* out;
+    float* lse;
+    int32_t* status;
+    int64_t* pre;              // units before each request [B + 1]; pre[B] < 0: nothing to do
+    Start* starts;             // [grid + 1]
+    float* part_o;             // [2 grid][rows][d]
+    float2* part_ml;           // [2 grid][rows] (reference, sum)
+    int64_t q_st, q_sh, o_st, o_sh, k_sb, k_sh, v_sb, v_sh, pool_blocks, spin;
+    int B, hk, G, bs, table_stride, cap, max_new, causal, window, grid;
+    int piece_shift;           // log2 of a copy's tokens: a block's, at most a tile's
+    int local_plan, bf16;
+    float scale2, v_scale;
+};
+
+template <typename T, typename U>
+__device__ __forceinline__ int last_at_most(const T* v, int n, U x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (v[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+// Exclusive sum over the block's NT threads, and the total.
+template <int NT>
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    const int64_t mine = lane < NT / 32 ? sums[lane] : 0;
+    int64_t all = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, all, o);
+        if (lane >= o) all += x;
+    }
+    *total = __shfl_sync(0xffffffffu, all, 31);
+    return __shfl_sync(0xffffffffu, all - mine, warp) + incl - v;
+}
+
+// Key tiles that some row of a request sees, and its tiles of rows.
+struct Span {
+    int tile0, tiles, row_tiles;
+};
+
+__device__ __forceinline__ Span span_of(const Args& a, int nq, int kv, int rows) {
+    Span s;
+    const int lo = a.window > 0 ? max(0, kv - nq - a.window + 1) : 0;
+    s.tile0 = lo / kTileKeys;
+    s.tiles = kv > lo ? (kv + kTileKeys - 1) / kTileKeys - s.tile0 : 0;
+    s.row_tiles = static_cast<int>((static_cast<int64_t>(nq) * a.G + rows - 1) / rows);
+    return s;
+}
+
+__device__ __forceinline__ bool bad_request(const Args& a, int64_t lo, int64_t hi, int64_t kv) {
+    return hi < lo || hi > a.cap || hi - lo > a.max_new || kv < 0 || kv > kMaxCached ||
+           (kv + a.bs - 1) / a.bs > a.table_stride;
+}
+
+// Units before each request, by the block's NT threads; the total, or -1 when a
+// length is out of range.
+template <int NT>
+__device__ __forceinline__ int64_t plan_requests(const Args& a, int rows, int64_t* pre, int64_t* sums) {
+    const int tid = threadIdx.x;
+    int bad = tid == 0 ? a.q_off[0] != 0 : 0;
+    int64_t units = 0;
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
+        const int b = b0 + tid;
+        int64_t n = 0;
+        if (b < a.B) {
+            const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_len[b];
+            if (bad_request(a, lo, hi, kv)) bad = 1;
+            else if (!a.dense || a.dense[b] < 0) {
+                const Span s = span_of(a, static_cast<int>(hi - lo), static_cast<int>(kv), rows);
+                n = static_cast<int64_t>(a.hk) * s.row_tiles * (s.tiles + kItemCost);
+            }
+        }
+        int64_t total;
+        const int64_t at = units + block_scan<NT>(n, sums, &total);
+        if (b < a.B) pre[b] = at;
+        units += total;
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+        units = -1;
+    }
+    return units;
+}
+
+// Lays out a batch of more than kLocalSeqs requests, by one block of its own.
+__global__ void __launch_bounds__(kPlanThreads) fp4_plan_kernel(const Args a, int rows) {
+    __shared__ int64_t sums[32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t units = plan_requests<kPlanThreads>(a, rows, a.pre, sums);
+    if (threadIdx.x == 0) a.pre[a.B] = units;
+}
+
+// The start of CTA c's range of `units`; a cut inside an item's fixed cost falls
+// on the item's start.
+__device__ __forceinline__ Start make_start(const Args& a, const int64_t* pre, int64_t units, int c, int rows) {
+    const int64_t ctas = min(static_cast<int64_t>(a.grid), units);
+    Start s{a.B, 0, 0, 0};
+    if (c < ctas) {
+        int64_t u = units * c / ctas;
+        s.b = last_at_most(pre, a.B, u);
+        u -= pre[s.b];
+        const Span sp = span_of(a, a.q_off[s.b + 1] - a.q_off[s.b], a.kv_len[s.b], rows);
+        const int64_t per = sp.tiles + kItemCost;
+        s.gj = static_cast<int32_t>(u / per);
+        s.off = static_cast<int32_t>(max(u - s.gj * per - kItemCost, static_cast<int64_t>(0)));
+    }
+    return s;
+}
+
+// ------------------------------------------------------------ segments
+
+// A CTA's part of one item: rows [row0, row0 + rows) of request b and KV head g
+// over key tiles [first, first + n).
+struct Segment {
+    int b, g, q0, pos0, kv, row0, rows, first, n;
+    int lo, hi;             // cache indices that some row sees
+    int all_lo, all_hi;     // and that all rows see
+    bool split, head;       // other CTAs hold the rest; the CTA's first segment
+};
+
+// Walks a CTA's range; every warp takes the same steps.
+struct Walk {
+    Start at, end;
+    bool head;
+    __device__ __forceinline__ Walk(const Start* r) : at(r[0]), end(r[1]), head(true) {}
+    __device__ __forceinline__ bool next(const Args& a, int tile_rows, Segment& s) {
+        for (;;) {
+            if (at.b > end.b || at.b >= a.B ||
+                (at.b == end.b && (at.gj > end.gj || (at.gj == end.gj && at.off >= end.off))))
+                return false;
+            const int q0 = a.q_off[at.b], nq = a.q_off[at.b + 1] - q0, kv = a.kv_len[at.b];
+            const Span sp = span_of(a, nq, kv, tile_rows);
+            if (sp.row_tiles == 0 || (a.dense && a.dense[at.b] >= 0) || at.gj >= a.hk * sp.row_tiles) {
+                ++at.b;
+                at.gj = at.off = 0;
+                continue;
+            }
+            s.b = at.b;
+            s.g = at.gj / sp.row_tiles;
+            s.q0 = q0;
+            s.kv = kv;
+            s.pos0 = kv - nq;
+            s.row0 = (at.gj - s.g * sp.row_tiles) * tile_rows;
+            s.rows = min(tile_rows, nq * a.G - s.row0);
+            const int i0 = s.row0 / a.G, i1 = (s.row0 + s.rows - 1) / a.G;
+            s.hi = a.causal ? max(0, min(kv, s.pos0 + i1 + 1)) : kv;
+            s.lo = a.window > 0 ? max(0, s.pos0 + i0 - a.window + 1) : 0;
+            s.all_hi = a.causal ? min(kv, s.pos0 + i0 + 1) : kv;
+            s.all_lo = a.window > 0 ? max(0, s.pos0 + i1 - a.window + 1) : 0;
+            const int last = at.b == end.b && at.gj == end.gj ? end.off : sp.tiles;
+            s.split = at.off > 0 || last < sp.tiles;
+            // (the first row tiles of a chunk see less than its last)
+            s.first = max(sp.tile0 + at.off, s.lo / kTileKeys);
+            s.n = s.hi > s.lo ? max(0, min(sp.tile0 + last, (s.hi + kTileKeys - 1) / kTileKeys) - s.first) : 0;
+            s.head = head;
+            head = false;
+            at.off = 0;
+            ++at.gj;
+            return true;
+        }
+    }
+};
+
+// ------------------------------------------------------------ shared memory
+
+template <int D, int NT>
+struct Smem {
+    static constexpr int kRows = 8 * NT;
+    static constexpr uint32_t kRec = fp4_record(D);
+    static constexpr uint32_t kHalf = kTileRecs * kRec;   // K or V of a tile
+    static constexpr uint32_t kStage = 2 * kHalf;
+    static constexpr int kAcc = D / 16 * NT * 4;          // accumulator registers of a lane
+    static constexpr int kVals = kAcc + NT * 4;           // and references and sums
+    static constexpr uint32_t join = 0;                   // [kWarps / 2][kVals][32] floats
+    static constexpr uint32_t ring = kWarps / 2 * kVals * 32 * 4;
+    static constexpr int kStages = (200 * 1024 - ring) / kStage < 32 ? (200 * 1024 - ring) / kStage : 32;
+    static constexpr uint32_t bars = ring + kStages * kStage;
+    static constexpr uint32_t full = bars;
+    static constexpr uint32_t empty = full + 8 * kStages;
+    static constexpr uint32_t range = empty + 8 * kStages;  // [2] Start
+    static constexpr uint32_t sums = range + 2 * 16;
+    static constexpr uint32_t abort = sums + 32 * 8;
+    static constexpr uint32_t pre = abort + 16;
+    static constexpr uint32_t total = pre + 8 * kLocalSeqs;
+};
+
+struct Ctx {
+    uint8_t* smem;
+    uint32_t base;
+    volatile int* abort_flag;
+    int32_t* status;
+    int64_t spin;
+    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
+        if (mbar_wait_bounded(base + bar, parity & 1, spin, abort_flag)) return true;
+        *abort_flag = 1;
+        atomicCAS(status, 0, static_cast<int32_t>(SP_ERR_TIMEOUT));
+        return false;
+    }
+};
+
+// ------------------------------------------------------------ loads
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+        "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
+        : "memory");
+}
+
+// The tiles of the CTA's segments, by one warp. A tile is cut into pieces (runs of
+// tokens of one block); lane t * pieces + p looks up and copies piece p of the
+// t-th tile of a batch of 32 / pieces tiles. Pieces outside the item's keys are
+// not loaded (their blocks may be gone).
+template <int D, int NT>
+__device__ __forceinline__ void load_tiles(const Ctx& c, const Args& a, int lane) {
+    using L = Smem<D, NT>;
+    constexpr unsigned kAll = 0xffffffffu;
+    const int piece = 1 << a.piece_shift, pieces = kTileKeys >> a.piece_shift;
+    const int per_batch = 32 / pieces, ti = lane / pieces, p = lane - ti * pieces;
+    const uint32_t bytes = (piece / kFp4Rows) * L::kRec;
+    const uint32_t dst = c.base + L::ring + p * bytes;
+    struct Batch {
+        int g, count;
+        const uint8_t *k, *v;   // of this lane's piece; null: not loaded
+    };
+    Walk w(reinterpret_cast<const Start*>(c.smem + L::range));
+    Segment s;
+    s.n = 0;
+    int done = 0;   // tiles of the segment handed out
+    auto next = [&](Batch& x) -> bool {
+        while (done >= s.n) {
+            if (!w.next(a, L::kRows, s)) return false;
+            done = 0;
+        }
+        x.count = min(per_batch, s.n - done);
+        const int key = (s.first + done + ti) * kTileKeys + (p << a.piece_shift);
+        x.k = x.v = nullptr;
+        if (ti < x.count && key < s.hi && key + piece > s.lo) {
+            const int blk = key / a.bs, within = key - blk * a.bs;
+            int id = a.table[static_cast<int64_t>(s.b) * a.table_stride + blk];
+            if (id < 0 || id >= a.pool_blocks) {
+                atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+                id = 0;
+            }
+            const int64_t rec = static_cast<int64_t>(within / kFp4Rows) * L::kRec;
+            x.k = a.k + id * a.k_sb + s.g * a.k_sh + rec;
+            x.v = a.v + id * a.v_sb + s.g * a.v_sh + rec;
+        }
+        done += x.count;
+        return true;
+    };
+    int slot = 0;
+    uint32_t turn = 0;
+    bool ok = true;
+    Batch cur, after;
+    bool have = next(cur);
+    while (have && ok) {
+        const bool more = next(after);   // (looked up while this batch waits for its stages)
+        for (int i = 0; i < cur.count; ++i) {
+            ok = __all_sync(kAll, c.wait(L::empty + 8 * slot, turn ^ 1));
+            if (!ok) break;
+            const bool mine = ti == i && cur.k;
+            const uint32_t n = __popc(__ballot_sync(kAll, mine)) * bytes * 2;
+            const uint32_t bar = c.base + L::full + 8 * slot;
+            if (lane == 0) mbar_arrive_expect_tx(bar, n);
+            __syncwarp();
+            if (mine) {
+                bulk_load(dst + slot * L::kStage, cur.k, bytes, bar);
+                bulk_load(dst + slot * L::kStage + L::kHalf, cur.v, bytes, bar);
+            }
+            if (++slot == L::kStages) {
+                slot = 0;
+                turn ^= 1;
+            }
+        }
+        cur = after;
+        have = more;
+    }
+    // every copy lands before the warp leaves: slots before `slot` were last used in
+    // this turn of the ring, the others in the one before (a wait on a first turn's
+    // parity 1 returns at once)
+    if (lane == 0)
+        for (int i = 0; i < L::kStages; ++i)
+            mbar_wait_spin(c.base + L::full + 8 * i, i < slot ? turn : turn ^ 1, kDrainSpin);
+    __syncwarp();
+}
+
+// ------------------------------------------------------------ products
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Transpose of an 8 x 8 matrix of 16-bit values held two in each lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// (low half x, high half y; rounded to nearest)
+__device__ __forceinline__ uint32_t half2_of(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+    static_assert(N == 1 || N == 2 || N % 4 == 0, "words of a lane");
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (N == 2) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 x = *reinterpret_cast<const uint4*>(p + 4 * i);
+            w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
+        }
+    }
+}
+
+// ------------------------------------------------------------ one warp's share
+
+// Lane (gid, tig) = (lane / 4, lane % 4). It holds
+//   of a key row       elements [tig D/4, (tig + 1) D/4): four of them a product
+//   of a value row     elements [gid D/8, (gid + 1) D/8): two a product
+//   of the logits      keys gid and gid + 8 of 16, query rows 2 tig and 2 tig + 1 of 8
+//   of the result      its elements of a value row, query rows 2 tig and 2 tig + 1
+template <int D, int NT>
+struct Worker {
+    using L = Smem<D, NT>;
+    static constexpr int kM = D / 16;
+    uint32_t q[D / 16][NT][2];
+    float acc[kM][NT][4];
+    float m[NT][2], l[NT][2];      // reference (log2 units), sum of this lane's keys
+    float sc[NT][2];               // scale of a row's logits, log2 units
+    int gid, tig;
+
+    __device__ __forceinline__ void reset() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) m[n][c] = -INFINITY, l[n][c] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kM; ++i)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[i][n][c] = 0.0f;
+        }
+    }
+
+    // Query rows as the products' right operand. bf16 rows are scaled by a power of
+    // two that takes their largest element to [2^14, 2^15): exact in fp16 down to
+    // 2^-31 of it (8 significant bits above the last subnormal).
+    __device__ __forceinline__ void load_q(const Args& a, const Segment& s) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int r = s.row0 + 8 * n + gid, tok = r / a.G;
+            uint4 x[D / 32];
+            const bool live = 8 * n + gid < s.rows;
+            const uint16_t* p = a.q + (s.q0 + static_cast<int64_t>(tok)) * a.q_st +
+                                (static_cast<int64_t>(s.g) * a.G + r - tok * a.G) * a.q_sh + tig * (D / 4);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+                x[i] = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+            float back = 1.0f;
+            if (a.bf16) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) top = max(top, max(w[u] & 0x7fff0000u, (w[u] << 16) & 0x7fff0000u));
+                }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                // exponent field of the factor and of its inverse, both kept normal
+                const int e = min(max(268 - static_cast<int>(top >> 23), 1), 253);
+                const float f = __uint_as_float(static_cast<uint32_t>(e) << 23);
+                back = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        w[u] = half2_of(__uint_as_float(w[u] << 16) * f, __uint_as_float(w[u] & 0xffff0000u) * f);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                q[2 * i][n][0] = x[i].x, q[2 * i][n][1] = x[i].y;
+                q[2 * i + 1][n][0] = x[i].z, q[2 * i + 1][n][1] = x[i].w;
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) sc[n][c] = a.scale2 * __shfl_sync(0xffffffffu, back, (2 * tig + c) * 4);
+        }
+    }
+
+    // Cache indices [lo, hi) that query row n, c sees.
+    __device__ __forceinline__ void sees(const Args& a, const Segment& s, int n, int c, int* lo, int* hi) const {
+        const int r = min(8 * n + 2 * tig + c, s.rows - 1);   // (rows behind the last are like it)
+        const int pos = s.pos0 + (s.row0 + r) / a.G;
+        *hi = a.causal ? min(s.kv, pos + 1) : s.kv;
+        *lo = a.window > 0 ? pos - a.window + 1 : 0;
+    }
+
+    // A tile whose copies have landed, its first key at cache index key0.
+    __device__ __forceinline__ void tile(const Args& a, const Segment& s, const uint8_t* kt, int key0) {
+        const uint8_t* vt = kt + L::kHalf;
+        const bool edge = key0 < s.all_lo || key0 + kTileKeys > s.all_hi;
+        float y[4][NT][4];
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[mt][n][c] = 0.0f;
+            const uint8_t *r0 = kt + 2 * mt * L::kRec, *r1 = r0 + L::kRec;
+            uint32_t w0[D / 32], w1[D / 32];
+            load_words(r0 + gid * (D / 2) + tig * (D / 8), w0);
+            load_words(r1 + gid * (D / 2) + tig * (D / 8), w1);
+            const uint32_t at = fp4_codes(D) + gid * (D / 16) + tig * (D / 64);
+            uint32_t f0, f1;
+            if constexpr (D == 64) f0 = r0[at], f1 = r1[at];
+            else if constexpr (D == 128)
+                f0 = *reinterpret_cast<const uint16_t*>(r0 + at), f1 = *reinterpret_cast<const uint16_t*>(r1 + at);
+            else f0 = *reinterpret_cast<const uint32_t*>(r0 + at), f1 = *reinterpret_cast<const uint32_t*>(r1 + at);
+            uint32_t s0 = 0, s1 = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                if (i % 2 == 0) {   // the scale of the next 16 elements, in both halves
+                    const uint32_t pick = (i / 2) * 0x11u;
+                    s0 = fp8_unpack(__byte_perm(f0, 0, pick));
+                    s1 = fp8_unpack(__byte_perm(f1, 0, pick));
+                }
+                uint32_t x0[4], x1[4];
+                fp4_unpack(w0[i], x0);
+                fp4_unpack(w1[i], x1);
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const uint32_t op[4] = {mul_f16x2(x0[2 * u], s0), mul_f16x2(x1[2 * u], s1),
+                                            mul_f16x2(x0[2 * u + 1], s0), mul_f16x2(x1[2 * u + 1], s1)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(y[mt][n], op, q[2 * i + u][n][0], q[2 * i + u][n][1]);
+                }
+            }
+        }
+        // logits in log2 units, masked at the edges of what the rows see
+        float top[NT][2];
+        bool above = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                int lo = 0, hi = INT32_MAX;
+                if (edge) sees(a, s, n, c, &lo, &hi);
+                float t = -INFINITY;
+#pragma unroll
+                for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float& x = y[mt][n][2 * h + c];
+                        x *= sc[n][c];
+                        if (edge) {
+                            const int j = key0 + 16 * mt + 8 * h + gid;
+                            if (j < lo || j >= hi) x = -INFINITY;
+                        }
+                        t = fmaxf(t, x);
+                    }
+                top[n][c] = t;
+                // (a first value is above a reference of minus infinity)
+                above |= t > m[n][c] + kSlack;
+            }
+        if (__any_sync(0xffffffffu, above)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float t = top[n][c];
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                    if (t > m[n][c] + kSlack) {
+                        const float f = ex2(m[n][c] - t);   // (0 for a first value)
+                        m[n][c] = t;
+                        l[n][c] *= f;
+#pragma unroll
+                        for (int i = 0; i < kM; ++i) acc[i][n][c] *= f, acc[i][n][2 + c] *= f;
+                    }
+                }
+        }
+        // weights, transposed to the right operand of the second product
+        uint32_t w[4][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float shift[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) shift[c] = kBias - (m[n][c] == -INFINITY ? 0.0f : m[n][c]);
+#pragma unroll
+            for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float p0 = ex2(y[mt][n][2 * h] + shift[0]), p1 = ex2(y[mt][n][2 * h + 1] + shift[1]);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    w[mt][n][h] = transpose8(half2_of(p0, p1));
+                }
+        }
+        bool odd = false;
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+            const uint8_t *r0 = vt + 2 * mt * L::kRec, *r1 = r0 + L::kRec;
+            constexpr int N = D / 64;
+            uint32_t w00[N], w01[N], w10[N], w11[N];   // record, row 2 tig and 2 tig + 1
+            const uint32_t at = 2 * tig * (D / 2) + gid * (D / 16);
+            load_words(r0 + at, w00);
+            load_words(r0 + at + D / 2, w01);
+            load_words(r1 + at, w10);
+            load_words(r1 + at + D / 2, w11);
+            // scales of both rows' groups: low byte row 2 tig, high byte row 2 tig + 1
+            constexpr int kGroups = D == 256 ? 2 : 1;
+            uint32_t f0[kGroups], f1[kGroups];
+            const uint32_t fat = fp4_codes(D) + 2 * tig * (D / 16) + gid * (D / 8) / kFp4Group;
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                uint32_t b[4] = {r0[fat + k], r0[fat + k + D / 16], r1[fat + k], r1[fat + k + D / 16]};
+                if (edge) {
+                    // a scale that is no number counts for the rows that see its key only
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (scale_is_nan(b[u])) b[u] = 0, odd = true;
+                }
+                f0[k] = fp8_unpack(b[0] | b[1] << 8);
+                f1[k] = fp8_unpack(b[2] | b[3] << 8);
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                // the same element of two neighbouring rows in one byte
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t e0[4], o0[4], e1[4], o1[4];
+                fp4_unpack((w00[i] & kLow) | (w01[i] << 4 & ~kLow), e0);
+                fp4_unpack((w00[i] >> 4 & kLow) | (w01[i] & ~kLow), o0);
+                fp4_unpack((w10[i] & kLow) | (w11[i] << 4 & ~kLow), e1);
+                fp4_unpack((w10[i] >> 4 & kLow) | (w11[i] & ~kLow), o1);
+                const uint32_t s0 = f0[kGroups == 2 ? i / 2 : 0], s1 = f1[kGroups == 2 ? i / 2 : 0];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t op[4] = {mul_f16x2(e0[u], s0), mul_f16x2(o0[u], s0), mul_f16x2(e1[u], s1),
+                                            mul_f16x2(o1[u], s1)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_f16(acc[4 * i + u][n], op, w[mt][n][0], w[mt][n][1]);
+                }
+            }
+        }
+        if (edge && __any_sync(0xffffffffu, odd)) spread_nan(a, s, vt, key0);
+    }
+
+    // Values that are no number, at the edge of what the rows see: the elements of
+    // their group become NaN in the rows that see them, whatever their weight.
+    __device__ __forceinline__ void spread_nan(const Args& a, const Segment& s, const uint8_t* vt, int key0) {
+        constexpr int kGroups = D == 256 ? 2 : 1;
+#pragma unroll 1
+        for (int k = 0; k < kTileKeys; ++k) {
+            const int j = key0 + k;
+            if (j < s.lo || j >= s.hi) continue;
+            const uint8_t* f = vt + k / kFp4Rows * L::kRec + fp4_codes(D) + k % kFp4Rows * (D / 16) + gid * (D / 8) / kFp4Group;
+#pragma unroll
+            for (int x = 0; x < kGroups; ++x) {
+                if (!scale_is_nan(f[x])) continue;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        int lo, hi;
+                        sees(a, s, n, c, &lo, &hi);
+                        if (j < lo || j >= hi) continue;
+#pragma unroll
+                        for (int i = 0; i < kM; ++i)
+                            if (i / 8 == x || kGroups == 1) acc[i][n][c] = acc[i][n][2 + c] = NAN;
+                    }
+            }
+        }
+    }
+
+    // This lane's share of a partial result, to and from `p` (32 lanes interleaved).
+    __device__ __forceinline__ void put(float* p) const {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) p[(n * 4 + c) * 32] = m[n][c], p[(n * 4 + 2 + c) * 32] = l[n][c];
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) p[(NT * 4 + (i * NT + n) * 4 + c) * 32] = acc[i][n][c];
+    }
+    __device__ __forceinline__ void add(const float* p) {
+        float mine[NT][2], theirs[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float o = p[(n * 4 + c) * 32], t = fmaxf(m[n][c], o);
+                mine[n][c] = m[n][c] == t ? 1.0f : ex2(m[n][c] - t);
+                theirs[n][c] = o == t ? 1.0f : ex2(o - t);
+                m[n][c] = t;
+                l[n][c] = l[n][c] * mine[n][c] + p[(n * 4 + 2 + c) * 32] * theirs[n][c];
+            }
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    acc[i][n][c] = acc[i][n][c] * mine[n][c & 1] + p[(NT * 4 + (i * NT + n) * 4 + c) * 32] * theirs[n][c & 1];
+    }
+
+    // Sums over the lanes' keys; then the rows of the result, or of a part of it.
+    __device__ __forceinline__ void write(const Args& a, const Segment& s) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float t = l[n][c];
+                t += __shfl_xor_sync(0xffffffffu, t, 4);
+                t += __shfl_xor_sync(0xffffffffu, t, 8);
+                t += __shfl_xor_sync(0xffffffffu, t, 16);
+                const int row = 8 * n + 2 * tig + c;
+                if (row >= s.rows) continue;
+                if (s.split) {
+                    const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (s.head ? 0 : 1)) * L::kRows + row;
+                    float* o = a.part_o + part * D + gid * (D / 8);
+#pragma unroll
+                    for (int i = 0; i < kM; i += 2)
+                        *reinterpret_cast<float4*>(o + 2 * i) = make_float4(acc[i][n][c], acc[i][n][2 + c], acc[i + 1][n][c],
+                                                                            acc[i + 1][n][2 + c]);
+                    if (gid == 0) a.part_ml[part] = make_float2(m[n][c], t);
+                    continue;
+                }
+                const int r = s.row0 + row, tok = r / a.G;
+                const int64_t h = static_cast<int64_t>(s.g) * a.G + r - tok * a.G, at = s.q0 + static_cast<int64_t>(tok);
+                const float inv = t == 0.0f ? 0.0f : a.v_scale / t;
+                uint16_t* o = a.out + at * a.o_st + h * a.o_sh + gid * (D / 8);
+                uint32_t x[kM];
+#pragma unroll
+                for (int i = 0; i < kM; ++i) {
+                    const float lo = acc[i][n][c] * inv, hi = acc[i][n][2 + c] * inv;
+                    if (a.bf16) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+                        x[i] = *reinterpret_cast<const uint32_t*>(&b);
+                    } else {
+                        x[i] = half2_of(lo, hi);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kM; i += 4)
+                    *reinterpret_cast<uint4*>(o + 2 * i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+                if (a.lse && gid == 0)
+                    a.lse[at * a.G * a.hk + h] = t == 0.0f ? -INFINITY : (m[n][c] - kBias + __log2f(t)) * kLn2;
+            }
+    }
+};
+
+// Rendezvous of the warps that compute (waits of theirs are bounded, so all come).
+__device__ __forceinline__ void workers_sync() { asm volatile("barrier.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, 1) fp4_attn_kernel(const Args a) {
+    using L = Smem<D, NT>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Ctx c{smem, smem_u32(smem), reinterpret_cast<volatile int*>(smem + L::abort), a.status, a.spin};
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::kStages; ++i) {
+            mbar_init(c.base + L::full + 8 * i, 1);
+            mbar_init(c.base + L::empty + 8 * i, 1);
+        }
+        *c.abort_flag = 0;
+        fence_mbar_init();
+    }
+    grid_dep_wait();
+    grid_dep_launch();
+    int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
+    int64_t units;
+    if (a.local_plan) {
+        units = plan_requests<kThreads>(a, L::kRows, pre, reinterpret_cast<int64_t*>(smem + L::sums));
+    } else {
+        pre = a.pre;
+        units = __ldcg(a.pre + a.B);
+    }
+    __syncthreads();   // (sums and barriers)
+    if (threadIdx.x < 2) {
+        const Start s = make_start(a, pre, units, static_cast<int>(blockIdx.x) + threadIdx.x, L::kRows);
+        reinterpret_cast<Start*>(smem + L::range)[threadIdx.x] = s;
+        if (threadIdx.x == 0 || static_cast<int>(blockIdx.x) == a.grid - 1) a.starts[blockIdx.x + threadIdx.x] = s;
+    }
+    __syncthreads();
+    if (warp == kWarps) {
+        load_tiles<D, NT>(c, a, lane);
+        return;
+    }
+    Worker<D, NT> me;
+    me.gid = lane >> 2;
+    me.tig = lane & 3;
+    Walk walk(reinterpret_cast<const Start*>(smem + L::range));
+    Segment s;
+    int seq = 0;       // tiles of earlier segments
+    while (walk.next(a, L::kRows, s)) {
+        me.load_q(a, s);
+        me.reset();
+        for (int k = (warp - seq) & (kWarps - 1); k < s.n; k += kWarps) {
+            const int i = seq + k, turn = i / L::kStages, slot = i - turn * L::kStages;
+            const bool ok = __all_sync(0xffffffffu, c.wait(L::full + 8 * slot, turn));
+            if (ok) me.tile(a, s, smem + L::ring + slot * L::kStage, (s.first + k) * kTileKeys);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(c.base + L::empty + 8 * slot);
+        }
+        seq += s.n;
+        // the warps' results, joined in pairs
+        float* join = reinterpret_cast<float*>(smem + L::join) + lane;
+#pragma unroll 1
+        for (int half = kWarps / 2; half; half /= 2) {
+            if (warp >= half && warp < 2 * half) me.put(join + (warp - half) * L::kVals * 32);
+            workers_sync();
+            if (warp < half) me.add(join + warp * L::kVals * 32);
+            workers_sync();
+        }
+        if (warp == 0) me.write(a, s);
+    }
+}
+
+// ------------------------------------------------------------ join
+
+// Parts of the items that were cut between CTAs. Block (x, r) joins row r of the
+// item that is cut first between CTAs x and x + 1, if one is.
+template <int D, int NT>
+__global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const Args a) {
+    constexpr int kRows = 8 * NT, kCols = D / 32, kJoinWarps = kJoinThreads / 32;
+    __shared__ float acc_s[kJoinWarps][D], sum_s[kJoinWarps];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int x = blockIdx.x + 1, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    auto start = [&](int c) {
+        const int4 v = __ldcg(reinterpret_cast<const int4*>(a.starts + c));
+        return Start{v.x, v.y, v.z, v.w};
+    };
+    const Start s = start(x), before = start(x - 1);
+    const bool same = before.b == s.b && before.gj == s.gj;
+    if (s.b >= a.B || s.off == 0 || (same && before.off > 0)) return;
+    const int q0 = a.q_off[s.b], nq = a.q_off[s.b + 1] - q0;
+    const int row_tiles = static_cast<int>((static_cast<int64_t>(nq) * a.G + kRows - 1) / kRows);
+    const int g = s.gj / row_tiles, r = (s.gj - g * row_tiles) * kRows + row;
+    if (r >= nq * a.G) return;
+    // CTAs x .. x + parts - 2 begin inside the item
+    int parts = 2;
+    for (int c0 = x + 1; c0 < a.grid; c0 += 32) {
+        bool more = false;
+        if (c0 + lane < a.grid) {
+            const Start o = start(c0 + lane);
+            more = o.b == s.b && o.gj == s.gj;
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, more);
+        parts += who == 0xffffffffu ? 32 : __ffs(~who) - 1;
+        if (who != 0xffffffffu) break;
+    }
+    auto at = [&](int p) {
+        return (2 * static_cast<int64_t>(x - 1 + p) + (p == 0 && !same ? 1 : 0)) * kRows + row;
+    };
+    float top = -INFINITY;
+    for (int p = lane; p < parts; p += 32) top = fmaxf(top, __ldcg(a.part_ml + at(p)).x);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float acc[kCols] = {}, sum = 0.0f;
+#pragma unroll 4
+    for (int p = warp; p < parts; p += kJoinWarps) {
+        const float2 ml = __ldcg(a.part_ml + at(p));
+        const float f = ml.x == top ? 1.0f : ex2(ml.x - top);
+        sum += ml.y * f;
+        const float* o = a.part_o + at(p) * D + lane * kCols;
+#pragma unroll
+        for (int i = 0; i < kCols; i += 2) {
+            const float2 v = __ldcg(reinterpret_cast<const float2*>(o + i));
+            acc[i] += v.x * f;
+            acc[i + 1] += v.y * f;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) acc_s[warp][lane * kCols + i] = acc[i];
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    sum = 0.0f;
+    for (int k = 0; k < kJoinWarps; ++k) sum += sum_s[k];
+    const int tok = r / a.G;
+    const int64_t h = static_cast<int64_t>(g) * a.G + r - tok * a.G, t = q0 + static_cast<int64_t>(tok);
+    const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+    for (int i = 2 * threadIdx.x; i < D; i += 2 * kJoinThreads) {
+        float lo = 0.0f, hi = 0.0f;
+        for (int k = 0; k < kJoinWarps; ++k) lo += acc_s[k][i], hi += acc_s[k][i + 1];
+        lo *= inv, hi *= inv;
+        uint32_t w;
+        if (a.bf16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+            w = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+            w = half2_of(lo, hi);
+        }
+        *reinterpret_cast<uint32_t*>(a.out + t * a.o_st + h * a.o_sh + i) = w;
+    }
+    if (a.lse && threadIdx.x == 0) a.lse[t * a.G * a.hk + h] = sum == 0.0f ? -INFINITY : (top - kBias + __log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------ host
+
+constexpr int kMostRows = 16;
+
+struct Layout {
+    size_t pre, starts, ml, o, total;
+};
+
+int grid_of() {
+    const int sms = device_sms();
+    return sms < kMaxGrid ? sms : kMaxGrid;
+}
+
+Layout layout(const sp_fp4_shape* s, int grid) {
+    Layout l;
+    size_t off = sizeof(WsHeader);
+    auto take = [&](size_t bytes) {
+        const size_t o = off;
+        off = (off + bytes + 255) & ~size_t(255);
+        return o;
+    };
+    l.pre = take(8 * (static_cast<size_t>(s->n_seqs) + 1));
+    l.starts = take(sizeof(Start) * (static_cast<size_t>(grid) + 1));
+    l.ml = take(8 * static_cast<size_t>(grid) * 2 * kMostRows);
+    l.o = take(4 * static_cast<size_t>(grid) * 2 * kMostRows * s->head_dim);
+    l.total = off;
+    return l;
+}
+
+template <int D, int NT>
+cudaError_t launch_rows(const Args& a, cudaStream_t st) {
+    using L = Smem<D, NT>;
+    static_assert(L::total <= 232448 && L::kStages >= kWarps, "shared memory of one CTA");
+    if (!a.local_plan) {
+        const cudaError_t e = launch_k(fp4_plan_kernel, 1, kPlanThreads, 0, st, a, L::kRows);
+        if (e != cudaSuccess) return e;
+    }
+    auto kern = fp4_attn_kernel<D, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::total));
+    if (e != cudaSuccess) return e;
+    e = launch_k(kern, static_cast<unsigned>(a.grid), kThreads, L::total, st, a);
+    if (e != cudaSuccess || a.grid < 2) return e;
+    return launch_k(fp4_join_kernel<D, NT>, dim3(a.grid - 1, L::kRows), kJoinThreads, 0, st, a);
+}
+
+}  // namespace
+
+size_t attn_fp4_workspace(const sp_fp4_shape* s) { return layout(s, grid_of()).total; }
+
+cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_params* p, const int32_t* q_off,
+                                       const int32_t* kv_len, const int32_t* table, const uint16_t* q,
+                                       const uint8_t* k_pool, const uint8_t* v_pool, uint16_t* out, float* lse,
+                                       void* ws, cudaStream_t st) {
+    const int d = s->head_dim;
+    Args a;
+    a.grid = grid_of();
+    const Layout l = layout(s, a.grid);
+    a.q_off = q_off;
+    a.kv_len = kv_len;
+    a.table = table;
+    a.dense = nullptr;
+    a.q = q;
+    a.k = k_pool;
+    a.v = v_pool;
+    a.out = out;
+    a.lse = lse;
+    a.status = &ws_ptr<WsHeader>(ws, 0)->status;
+    a.pre = ws_ptr<int64_t>(ws, l.pre);
+    a.starts = ws_ptr<Start>(ws, l.starts);
+    a.part_o = ws_ptr<float>(ws, l.o);
+    a.part_ml = ws_ptr<float2>(ws, l.ml);
+    a.q_st = s->q_stride_token, a.q_sh = s->q_stride_head;
+    a.o_st = s->o_stride_token, a.o_sh = s->o_stride_head;
+    a.k_sb = s->k_stride_block, a.k_sh = s->k_stride_head;
+    a.v_sb = s->v_stride_block, a.v_sh = s->v_stride_head;
+    a.pool_blocks = s->pool_blocks;
+    a.spin = p->spin_limit > 0 ? p->spin_limit : kDefaultSpin;
+    a.B = s->n_seqs;
+    a.hk = s->n_kv_heads;
+    a.G = s->n_q_heads / s->n_kv_heads;
+    a.bs = s->block_size;
+    a.table_stride = s->table_stride;
+    a.cap = s->n_tokens;
+    a.max_new = s->max_new > 0 ? s->max_new : s->n_tokens;
+    a.causal = p->causal;
+    a.window = p->window <= kMaxCached ? p->window : 0;   // (a longer one hides nothing)
+    a.piece_shift = __builtin_ctz(a.bs < kTileKeys ? a.bs : kTileKeys);
+    a.local_plan = a.B <= kLocalSeqs;
+    a.bf16 = s->dtype == SP_DTYPE_BF16;
+    const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(d));
+    a.scale2 = static_cast<float>(scale * p->k_scale * 1.4426950408889634);
+    a.v_scale = p->v_scale;
+    const bool one = static_cast<int64_t>(a.max_new) * a.G <= 8;
+    if (d == 64) return one ? launch_rows<64, 1>(a, st) : launch_rows<64, 2>(a, st);
+    if (d == 128) return one ? launch_rows<128, 1>(a, st) : launch_rows<128, 2>(a, st);
+    return launch_rows<256, 1>(a, st);
+}
+
+}  // namespace sp

@@ -1,0 +1,333 @@
+// Rows of the 4-bit cache ("SpecPrefill — Implementation Guide", §How It
+// Works / Sparse Prefill: the target prefills the kept tokens, each at its
+// original position): the store of a step's rotated keys and values, and rows
+// read back as 16-bit values.
+//
+// append_kv_fp4_kernel. A thread owns one pair of 16-byte vectors of a query row,
+// or one group of 16 elements of a key or value row: it needs no other thread
+// for the group's largest element, its scale and its 8 bytes of codes. (A key
+// group that is rotated reads its partners too, the same lines as another thread
+// of the warp.) Every operation of the stored value is a single 32-bit one, none
+// contracted, so that the bits are those of the definition in specprefill.h.
+//
+// unpack_fp4_kernel. A thread turns 8 bytes of codes and a scale into 32 bytes.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sp_device.cuh"
+#include "sp_fp4.cuh"
+#include "sp_fp4.h"
+#include "sp_internal.h"
+#include "sp_paged.h"
+
+namespace sp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCtas = 4;   // resident CTAs of an SM and the grid's
+
+__device__ __forceinline__ void raise_status(int32_t* status, int code) {
+    if (status) atomicMax(status, code);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+    if constexpr (kBf16) {
+        return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+    } else {
+        return __half22float2(*reinterpret_cast<const __half2*>(&x));
+    }
+}
+
+// (rounded to nearest even, the one rounding of the value)
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    if constexpr (kBf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack8(uint4 v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<kBf16>(w[i]);
+        x[2 * i] = f.x, x[2 * i + 1] = f.y;
+    }
+}
+
+// ------------------------------------------------------------ rotate and store
+
+struct AppArgs {
+    const uint16_t* q;
+    const uint16_t* k;
+    const uint16_t* v;
+    const int32_t* slot_map;
+    const int32_t* positions;
+    const float* cos_sin;
+    const int32_t* n_new;
+    uint16_t* q_out;
+    uint8_t* k_pool;
+    uint8_t* v_pool;
+    int32_t* status;
+    int64_t q_st, q_sh, qo_st, qo_sh, k_st, k_sh, v_st, v_sh, kp_sb, kp_sh, vp_sb, vp_sh;
+    int64_t pool_tokens;
+    int cap, hq, hk, d, half, max_pos, bs;
+    int heads_per, groups;  // heads walked by one thread, and groups of them
+    float k_scale, v_scale;
+};
+
+// cos and sin of 8 neighbouring elements.
+__device__ __forceinline__ void angles(const float* row, int half, float (&c)[8], float (&s)[8]) {
+#pragma unroll
+    for (int u = 0; u < 8; u += 4) {
+        const float4 x = __ldg(reinterpret_cast<const float4*>(row + u));
+        const float4 y = __ldg(reinterpret_cast<const float4*>(row + half + u));
+        c[u] = x.x, c[u + 1] = x.y, c[u + 2] = x.z, c[u + 3] = x.w;
+        s[u] = y.x, s[u + 1] = y.y, s[u + 2] = y.z, s[u + 3] = y.w;
+    }
+}
+
+// The codes (8 bytes) and scale of a group of 16 values, their factor taken out.
+__device__ __forceinline__ uint2 encode(float (&x)[16], float factor, uint32_t* scale_byte) {
+    uint32_t top = 0;
+    // (a division by 1 changes nothing)
+    if (factor != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], factor);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    if (top >= 0x7f800000u) {   // an infinity or NaN among them
+        *scale_byte = kFp4NoNumber;
+        return make_uint2(0u, 0u);
+    }
+    // (at most 448, and at least the smallest scale: 2^-9, code 1)
+    const uint32_t byte = max(fp8_pack(__fdiv_rn(__uint_as_float(top), 6.0f)), 1u);
+    *scale_byte = byte;
+    const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(fp8_unpack(byte))));
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i / 4] |= fp4_pack2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) << (8 * (i % 4));
+    return make_uint2(w[0], w[1]);
+}
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const AppArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    int64_t n = a.cap;
+    if (a.n_new) {
+        const int64_t given = *a.n_new;
+        n = given < 0 ? 0 : (given < n ? given : n);
+    }
+    const int pairs = a.d / 16;            // pairs of vectors, or groups, of a row
+    const int per_token = pairs * a.groups;
+    const int heads = a.hq + 2 * a.hk;
+    const int64_t total = n * per_token;
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; w < total;
+         w += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t t = w / per_token;
+        const int rest = static_cast<int>(w - t * per_token);
+        const int group = rest / pairs, i = rest - group * pairs;
+        const int64_t slot = a.slot_map[t];
+        const bool stored = slot >= 0 && slot < a.pool_tokens;
+        if (slot >= a.pool_tokens && rest == 0) raise_status(a.status, SP_ERR_DEVICE);
+        const float* row = nullptr;
+        if (a.half) {
+            const int64_t pos = a.positions[t];
+            if (pos < 0 || pos >= a.max_pos) {
+                if (rest == 0) raise_status(a.status, SP_ERR_DEVICE);
+                continue;
+            }
+            row = a.cos_sin + pos * 2 * a.half;
+        }
+        const int64_t blk = stored ? slot / a.bs : 0;
+        const int within = stored ? static_cast<int>(slot - blk * a.bs) : 0;
+        const int64_t rec = static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
+        const int r = within % kFp4Rows;
+        const int h1 = min((group + 1) * a.heads_per, heads);
+        for (int h = group * a.heads_per; h < h1; ++h) {
+            if (h < a.hq) {
+                // vectors (e0, e1) in elements: a rotated pair, or two neighbours behind it
+                const bool turn = i < a.half / 8;
+                const int e0 = turn ? i * 8 : 2 * a.half + (i - a.half / 8) * 16, e1 = turn ? e0 + a.half : e0 + 8;
+                const uint16_t* src = a.q + t * a.q_st + h * a.q_sh;
+                uint16_t* dst = a.q_out + t * a.qo_st + h * a.qo_sh;
+                uint4 x = __ldcs(reinterpret_cast<const uint4*>(src + e0));
+                uint4 y = __ldcs(reinterpret_cast<const uint4*>(src + e1));
+                if (turn) {
+                    float c[8], s[8];
+                    angles(row + e0, a.half, c, s);
+                    uint32_t* px = reinterpret_cast<uint32_t*>(&x);
+                    uint32_t* py = reinterpret_cast<uint32_t*>(&y);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float2 f = unpack2<kBf16>(px[u]), g = unpack2<kBf16>(py[u]);
+                        px[u] = pack2<kBf16>(f.x * c[2 * u] - g.x * s[2 * u], f.y * c[2 * u + 1] - g.y * s[2 * u + 1]);
+                        py[u] = pack2<kBf16>(g.x * c[2 * u] + f.x * s[2 * u], g.y * c[2 * u + 1] + f.y * s[2 * u + 1]);
+                    }
+                }
+                *reinterpret_cast<uint4*>(dst + e0) = x;
+                *reinterpret_cast<uint4*>(dst + e1) = y;
+                continue;
+            }
+            if (!stored) continue;
+            const bool is_v = h >= a.hq + a.hk;
+            const int g = is_v ? h - a.hq - a.hk : h - a.hq;
+            const uint16_t* src = is_v ? a.v + t * a.v_st + g * a.v_sh : a.k + t * a.k_st + g * a.k_sh;
+            uint8_t* dst = is_v ? a.v_pool + blk * a.vp_sb + g * a.vp_sh : a.k_pool + blk * a.kp_sb + g * a.kp_sh;
+            float x[16];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int e = 16 * i + 8 * u;
+                float f[8];
+                unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(src + e)), f);
+                if (!is_v && e < 2 * a.half) {
+                    // a cos - b sin in the first half, b cos + a sin in the second
+                    const bool second = e >= a.half;
+                    const int j = second ? e - a.half : e;
+                    float o[8], c[8], s[8];
+                    unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(src + (second ? j : e + a.half))), o);
+                    angles(row + j, a.half, c, s);
+#pragma unroll
+                    for (int v = 0; v < 8; ++v)
+                        f[v] = __fadd_rn(__fmul_rn(f[v], c[v]), __fmul_rn(second ? o[v] : -o[v], s[v]));
+                }
+#pragma unroll
+                for (int v = 0; v < 8; ++v) x[8 * u + v] = f[v];
+            }
+            uint32_t byte;
+            const uint2 codes = encode(x, is_v ? a.v_scale : a.k_scale, &byte);
+            *reinterpret_cast<uint2*>(dst + rec + r * (a.d / 2) + 8 * i) = codes;
+            dst[rec + fp4_codes(a.d) + r * (a.d / 16) + i] = static_cast<uint8_t>(byte);
+        }
+    }
+}
+
+// ------------------------------------------------------------ read back
+
+struct UnpackArgs {
+    const uint8_t* pool;
+    const int32_t* slots;
+    uint16_t* out;
+    int32_t* status;
+    int64_t rows, sb, sh, o_st, o_sh, pool_tokens;
+    int hk, d, bs;
+    float scale;
+};
+
+template <bool kBf16>
+__global__ void __launch_bounds__(kThreads) unpack_fp4_kernel(const UnpackArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int groups = a.d / 16, per_row = groups * a.hk;
+    const int64_t total = a.rows * per_row;
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; w < total;
+         w += static_cast<int64_t>(gridDim.x) * kThreads) {
+        const int64_t t = w / per_row;
+        const int rest = static_cast<int>(w - t * per_row);
+        const int h = rest / groups, i = rest - h * groups;
+        const int64_t slot = a.slots ? a.slots[t] : t;
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (slot >= 0 && slot < a.pool_tokens) {
+            const int64_t blk = slot / a.bs;
+            const int within = static_cast<int>(slot - blk * a.bs), r = within % kFp4Rows;
+            const uint8_t* rec = a.pool + blk * a.sb + h * a.sh + static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
+            const uint2 codes = __ldg(reinterpret_cast<const uint2*>(rec + r * (a.d / 2) + 8 * i));
+            const uint32_t s = fp8_unpack(rec[fp4_codes(a.d) + r * groups + i] * 0x101u);
+            uint32_t n[8], o[8];
+            fp4_unpack(codes.x, *reinterpret_cast<uint32_t(*)[4]>(n));
+            fp4_unpack(codes.y, *reinterpret_cast<uint32_t(*)[4]>(n + 4));
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float2 f = unpack2<false>(mul_f16x2(n[u], s));
+                o[u] = pack2<kBf16>(f.x * a.scale, f.y * a.scale);
+            }
+            x = make_uint4(o[0], o[1], o[2], o[3]);
+            y = make_uint4(o[4], o[5], o[6], o[7]);
+        } else if (slot != -1 && rest == 0) {
+            raise_status(a.status, SP_ERR_DEVICE);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(a.out + t * a.o_st + h * a.o_sh + 16 * i);
+        dst[0] = x;
+        dst[1] = y;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append_kv_fp4(const sp_append_fp4_shape* s, const uint16_t* q, const uint16_t* k,
+                                 const uint16_t* v, const int32_t* slot_map, const int32_t* positions,
+                                 const float* cos_sin, const int32_t* n_new, uint16_t* q_out, uint8_t* k_pool,
+                                 uint8_t* v_pool, int32_t* status, cudaStream_t st) {
+    AppArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.slot_map = slot_map;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.n_new = n_new;
+    a.q_out = q_out;
+    a.k_pool = k_pool;
+    a.v_pool = v_pool;
+    a.status = status;
+    a.q_st = s->q_stride_token, a.q_sh = s->q_stride_head;
+    a.qo_st = s->qo_stride_token, a.qo_sh = s->qo_stride_head;
+    a.k_st = s->k_stride_token, a.k_sh = s->k_stride_head;
+    a.v_st = s->v_stride_token, a.v_sh = s->v_stride_head;
+    a.kp_sb = s->kp_stride_block, a.kp_sh = s->kp_stride_head;
+    a.vp_sb = s->vp_stride_block, a.vp_sh = s->vp_stride_head;
+    a.pool_tokens = s->pool_blocks * s->block_size;
+    a.cap = s->n_tokens;
+    a.hq = q ? s->n_q_heads : 0;
+    a.hk = s->n_kv_heads;
+    a.d = s->head_dim;
+    a.half = s->rotary_dim / 2;
+    a.max_pos = s->max_pos;
+    a.bs = s->block_size;
+    a.k_scale = s->k_scale;
+    a.v_scale = s->v_scale;
+    const int heads = a.hq + 2 * a.hk, pairs = a.d / 16, sms = device_sms();
+    a.heads_per = static_cast<int64_t>(a.cap) * pairs * heads >= int64_t(2) * kThreads * kCtas * sms ? 2 : 1;
+    a.groups = (heads + a.heads_per - 1) / a.heads_per;
+    int64_t grid = (static_cast<int64_t>(a.cap) * pairs * a.groups + kThreads - 1) / kThreads;
+    if (grid > int64_t(kCtas) * sms) grid = int64_t(kCtas) * sms;
+    auto kern = s->dtype == SP_DTYPE_BF16 ? append_kv_fp4_kernel<true> : append_kv_fp4_kernel<false>;
+    return launch_k(kern, static_cast<unsigned>(grid), kThreads, 0, st, a);
+}
+
+cudaError_t launch_unpack_fp4(const sp_unpack_fp4_shape* s, const uint8_t* pool, const int32_t* slots, uint16_t* out,
+                              int32_t* status, cudaStream_t st) {
+    UnpackArgs a;
+    a.pool = pool;
+    a.slots = slots;
+    a.out = out;
+    a.status = status;
+    a.rows = s->n_rows;
+    a.sb = s->stride_block, a.sh = s->stride_head;
+    a.o_st = s->o_stride_token, a.o_sh = s->o_stride_head;
+    a.pool_tokens = s->pool_blocks * s->block_size;
+    a.hk = s->n_kv_heads;
+    a.d = s->head_dim;
+    a.bs = s->block_size;
+    a.scale = s->scale;
+    const int64_t work = a.rows * a.hk * (a.d / 16);
+    int64_t grid = (work + kThreads - 1) / kThreads;
+    const int64_t most = int64_t(8) * device_sms();
+    if (grid > most) grid = most;
+    auto kern = s->dtype == SP_DTYPE_BF16 ? unpack_fp4_kernel<true> : unpack_fp4_kernel<false>;
+    return launch_k(kern, static_cast<unsigned>(grid), kThreads, 0, st, a);
+}
+
+}  // namespace sp

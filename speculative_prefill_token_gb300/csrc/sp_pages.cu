@@ -1,0 +1,540 @@
+// Pages of the block-paged cache ("SpecPrefill — Implementation Guide", §How It
+// Works / Sparse Prefill: what the target holds of a prompt; several
+// continuations of one prompt share its blocks, kept tokens of a cached prompt
+// move to blocks of their own, ended requests give theirs back).
+//
+// copy_kv_kernel. A warp copies one row of all heads (or, for whole blocks of a
+// 4-bit pool, one head's records) of one pool: it issues up to four 16-byte loads
+// a lane before their stores.
+//
+// fork_blocks_kernel. With len_i the cached tokens of src_i, full_i = len_i / bs and
+// pre_i the begun blocks of the forks before i,
+//   table[dst_i][k] = table[src_i][k],  shared[table[src_i][k]] += 1,  k < full_i
+//   table[dst_i][full_i] = free[n_free - 1 - pre_i]          if len_i % bs != 0.
+// Every CTA checks and scans all forks itself (no communication between CTAs),
+// and then takes its share of runs of 256 table entries. Counts go up by atomic
+// additions, whose order changes nothing.
+//
+// free_blocks. One kernel takes a holder off every block that a request lets go
+// (shared[id] -= 1, so that a block that nobody holds any more is at -1); a
+// second, one cluster of 8 CTAs, walks the counts in the order of the ids, each
+// CTA a slice, and puts the blocks at -1 behind the free ones. The order of the
+// list is that of the ids, so it does not depend on timing; a count below -1 is a
+// block let go too often, and everything is put back.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "sp_device.cuh"
+#include "sp_fp4.cuh"
+#include "sp_fp4.h"
+#include "sp_internal.h"
+#include "sp_paged.h"
+
+namespace sp {
+namespace {
+
+__device__ __forceinline__ void raise_status(int32_t* status, int code) {
+    if (status) atomicMax(status, code);
+}
+
+// ------------------------------------------------------------ copies
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyWarps = kCopyThreads / 32;
+constexpr int kCopyCtas = 8;      // of an SM
+constexpr int kCopyUnroll = 4;
+
+struct CopyArgs {
+    void* pools[SP_MAX_COPY_POOLS];
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* table;
+    const int32_t* src_off;
+    const int32_t* n_used;
+    int32_t* status;
+    int64_t sb, st, sh;
+    int pool_blocks, n_pools, entries, rows, bs, hk, d, fp4, B, table_stride;
+};
+
+// The last b with off[b] <= i < off[b + 1] of B + 1 offsets, by a whole warp: 32
+// pivots a step.
+__device__ __forceinline__ int request_of(const int32_t* off, int B, int i, int lane) {
+    int lo = 0, hi = B;   // off[lo] <= i (off[0] = 0)
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const bool below = at < hi && off[at] <= i;
+        const unsigned who = __ballot_sync(0xffffffffu, below);
+        const int last = who ? 31 - __clz(who) : 0;
+        lo += last * step;
+        hi = min(hi, lo + step);
+    }
+    return lo;
+}
+
+// A slot: its block and its row there.
+struct Place {
+    int block, row;
+};
+
+// Where entry i's first row comes from and goes to; false where it copies nothing.
+// (slots stay below 2^31)
+__device__ __forceinline__ bool places_of(const CopyArgs& a, int i, int lane, Place* from, Place* to) {
+    const int s = a.src[i], t = a.dst[i];
+    if (s < 0 || t < 0) return false;
+    bool ok = true;
+    if (a.rows > 1) {
+        *from = Place{s, 0};
+        *to = Place{t, 0};
+    } else {
+        const int k = s / a.bs;
+        *from = Place{k, s - k * a.bs};
+        to->block = t / a.bs;
+        to->row = t - to->block * a.bs;
+        if (a.table) {
+            const int b = request_of(a.src_off, a.B, i, lane);
+            from->block = k < a.table_stride ? a.table[static_cast<int64_t>(b) * a.table_stride + k] : -1;
+            ok = from->block >= 0;
+        }
+    }
+    ok = ok && from->block < a.pool_blocks && to->block < a.pool_blocks;
+    if (!ok && lane == 0) raise_status(a.status, SP_ERR_DEVICE);
+    return ok;
+}
+
+// `n` vectors of 16 bytes by a warp; `at` gives a vector's offset in its row.
+template <typename F>
+__device__ __forceinline__ void copy_vectors(const uint8_t* from, uint8_t* to, int n, int lane, F at) {
+    for (int v0 = lane; v0 < n; v0 += 32 * kCopyUnroll) {
+        uint4 x[kCopyUnroll];
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if (v0 + 32 * u < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(from + at(v0 + 32 * u)));
+#pragma unroll
+        for (int u = 0; u < kCopyUnroll; ++u)
+            if (v0 + 32 * u < n) *reinterpret_cast<uint4*>(to + at(v0 + 32 * u)) = x[u];
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas / 2) copy_kv_kernel(const __grid_constant__ CopyArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31;
+    int64_t n = a.entries;
+    if (a.table) n = min(n, static_cast<int64_t>(max(a.src_off[a.B], 0)));
+    if (a.n_used) n = min(n, static_cast<int64_t>(max(*a.n_used, 0)));
+    // parts of an entry: its rows, or the heads of a 4-bit block
+    const int parts = a.fp4 && a.rows > 1 ? a.hk : a.rows;
+    const int64_t per_pool = n * parts, total = per_pool * a.n_pools;
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); w < total;
+         w += static_cast<int64_t>(gridDim.x) * kCopyWarps) {
+        const int pool = static_cast<int>(w / per_pool);
+        const int64_t rest = w - pool * per_pool;
+        const int i = static_cast<int>(rest / parts), part = static_cast<int>(rest - static_cast<int64_t>(i) * parts);
+        Place from, to;
+        if (!places_of(a, i, lane, &from, &to)) continue;
+        const uint8_t* x = static_cast<const uint8_t*>(a.pools[pool]) + from.block * a.sb;
+        uint8_t* y = static_cast<uint8_t*>(a.pools[pool]) + to.block * a.sb;
+        if (!a.fp4) {
+            const int per_head = a.d / 8;
+            x += (from.row + part) * a.st;
+            y += (to.row + part) * a.st;
+            if (a.sh == 2 * a.d) copy_vectors(x, y, a.hk * per_head, lane, [](int v) { return static_cast<int64_t>(v) * 16; });
+            else copy_vectors(x, y, a.hk * per_head, lane, [&](int v) { return v / per_head * a.sh + v % per_head * 16; });
+        } else if (a.rows > 1) {
+            copy_vectors(x + part * a.sh, y + part * a.sh, a.bs / kFp4Rows * (fp4_record(a.d) / 16), lane,
+                         [](int v) { return static_cast<int64_t>(v) * 16; });
+        } else {
+            // a token: d / 2 bytes of codes and d / 16 of scales for each head, in words
+            const int r0 = from.row % kFp4Rows, r1 = to.row % kFp4Rows;
+            x += from.row / kFp4Rows * fp4_record(a.d);
+            y += to.row / kFp4Rows * fp4_record(a.d);
+            const int codes = a.d / 8, words = codes + a.d / 64;   // of a head
+            for (int v = lane; v < a.hk * words; v += 32) {
+                const int h = v / words, u = v - h * words;
+                const bool c = u < codes;
+                const int in = c ? 4 * u : fp4_codes(a.d) + 4 * (u - codes), row = c ? a.d / 2 : a.d / 16;
+                *reinterpret_cast<uint32_t*>(y + h * a.sh + in + r1 * row) =
+                    *reinterpret_cast<const uint32_t*>(x + h * a.sh + in + r0 * row);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ forks
+
+constexpr int kForkThreads = 512;
+constexpr int kRun = 256;         // table entries of a unit of work: 8 a lane
+
+struct PageArgs {
+    const int32_t* src;
+    const int32_t* dst;
+    const int32_t* ctx_len;
+    const int32_t* new_len;
+    int32_t* table;
+    int32_t* shared;
+    const int32_t* free_in;
+    int32_t* free_out;
+    const int32_t* n_free;
+    int32_t* kv_len;
+    int32_t* copy_src;
+    int32_t* copy_dst;
+    int32_t* n_left;
+    int32_t* status;
+    int B, F, bs, table_stride, pool_blocks, free_cap;
+};
+
+__device__ __forceinline__ int blocks_for(int tokens, int bs) { return tokens / bs + (tokens % bs != 0); }
+
+__global__ void __launch_bounds__(kForkThreads) fork_blocks_kernel(const PageArgs a) {
+    extern __shared__ int32_t fork_smem[];
+    int32_t* len = fork_smem;            // [F] tokens of the fork, -1: none
+    int32_t* pre = len + a.F;            // [F] begun blocks before it
+    uint32_t* taken = reinterpret_cast<uint32_t*>(pre + a.F);   // a bit for each row that becomes a fork
+    __shared__ int warp_sum[kForkThreads / 32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int words = (a.B + 31) / 32;
+    for (int i = tid; i < words; i += kForkThreads) taken[i] = 0;
+    const int n_free = *a.n_free;
+    __syncthreads();
+    bool ok = n_free >= 0 && n_free <= a.free_cap;
+    for (int i = tid; i < a.F; i += kForkThreads) {
+        const int s = a.src[i], t = a.dst[i];
+        int n = -1;
+        if (s >= 0) {
+            if (s >= a.B || t < 0 || t >= a.B) {
+                ok = false;
+            } else {
+                n = a.ctx_len[s];
+                if (n < 0 || blocks_for(n, a.bs) > a.table_stride || a.ctx_len[t] != 0) ok = false;
+                if (atomicOr(taken + t / 32, 1u << (t % 32)) >> (t % 32) & 1) ok = false;   // a row forked into twice
+            }
+        }
+        len[i] = n;
+    }
+    ok = __syncthreads_and(ok);
+    // (a row that is forked from and into)
+    if (ok)
+        for (int i = tid; i < a.F; i += kForkThreads)
+            if (len[i] >= 0 && taken[a.src[i] / 32] >> (a.src[i] % 32) & 1) ok = false;
+    // each thread takes a run of forks, of odd length (no bank conflicts)
+    const int per = (a.F + kForkThreads - 1) / kForkThreads | 1;
+    const int i0 = min(tid * per, a.F), i1 = min(i0 + per, a.F);
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) mine += len[i] > 0 && len[i] % a.bs != 0;
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    ok = __syncthreads_and(ok);
+    int before = 0, total = 0;
+    for (int k = 0; k < kForkThreads / 32; ++k) {
+        if (k < warp) before += warp_sum[k];
+        total += warp_sum[k];
+    }
+    before += incl - mine;
+    for (int i = i0; i < i1; ++i) {
+        pre[i] = before;
+        before += len[i] > 0 && len[i] % a.bs != 0;
+    }
+    const bool go = ok && total <= n_free;   // (the same on every thread)
+    if (blockIdx.x == 0 && tid == 0) {
+        *a.n_left = go ? n_free - total : n_free;
+        if (!ok) raise_status(a.status, SP_ERR_DEVICE);
+        else if (!go) raise_status(a.status, SP_ERR_CAPACITY);
+    }
+    __syncthreads();
+    for (int b = blockIdx.x * kForkThreads + tid; b < a.B; b += gridDim.x * kForkThreads)
+        if (!go || !(taken[b / 32] >> (b % 32) & 1)) a.kv_len[b] = a.ctx_len[b];
+    // units: runs of kRun table entries of a fork, its begun block with the run that holds it
+    const int runs = (a.table_stride + kRun - 1) / kRun;
+    const int64_t units = static_cast<int64_t>(a.F) * runs;
+    for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kForkThreads / 32) + warp; u < units;
+         u += static_cast<int64_t>(gridDim.x) * (kForkThreads / 32)) {
+        const int i = static_cast<int>(u / runs), k0 = static_cast<int>(u - static_cast<int64_t>(i) * runs) * kRun;
+        const int n = go ? len[i] : -1;
+        const int full = n > 0 ? n / a.bs : 0;
+        const bool begun = n > 0 && n % a.bs != 0;
+        if (k0 == 0 && lane == 0) {
+            if (!begun) a.copy_src[i] = a.copy_dst[i] = -1;
+            if (n >= 0) a.kv_len[a.dst[i]] = n;
+        }
+        if (n <= 0 || k0 > full) continue;
+        const int32_t* from = a.table + static_cast<int64_t>(a.src[i]) * a.table_stride;
+        int32_t* to = a.table + static_cast<int64_t>(a.dst[i]) * a.table_stride;
+        int id[kRun / 32];
+#pragma unroll
+        for (int x = 0; x < kRun / 32; ++x) {
+            const int k = k0 + 32 * x + lane;
+            id[x] = k < full ? from[k] : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < kRun / 32; ++x) {
+            const int k = k0 + 32 * x + lane;
+            if (k >= full) continue;
+            to[k] = id[x];
+            if (id[x] < 0 || id[x] >= a.pool_blocks) raise_status(a.status, SP_ERR_DEVICE);
+            else atomicAdd(a.shared + id[x], 1);
+        }
+        if (begun && full - k0 < kRun && lane == 0) {
+            const int fresh = a.free_in[n_free - 1 - pre[i]];
+            to[full] = fresh;
+            a.copy_src[i] = from[full];
+            a.copy_dst[i] = fresh;
+            if (fresh < 0 || fresh >= a.pool_blocks) raise_status(a.status, SP_ERR_DEVICE);
+        }
+    }
+}
+
+// ------------------------------------------------------------ frees
+
+constexpr int kDropThreads = 256;
+constexpr int kSweepThreads = 1024;
+constexpr int kSweepCtas = 8;     // one cluster
+constexpr int kSweepPer = 4 * kSweepThreads;   // counts of a step: 4 a thread
+
+// Whether every length is in range (by the whole block; both kernels take the
+// same way).
+__device__ __forceinline__ bool lengths_fit(const PageArgs& a) {
+    const int n_free = *a.n_free;
+    bool ok = n_free >= 0 && n_free <= a.free_cap;
+    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+        const int ctx = a.ctx_len[b], left = a.new_len[b];
+        ok = ok && left >= 0 && left <= ctx && blocks_for(ctx, a.bs) <= a.table_stride;
+    }
+    return __syncthreads_and(ok);
+}
+
+// Adds `by` to the count of every block that a request lets go: runs of kRun
+// entries of a row, from warp w of `warps`.
+__device__ __forceinline__ void count_drops(const PageArgs& a, int by, int64_t w, int64_t warps, int32_t* status) {
+    const int lane = threadIdx.x & 31, runs = (a.table_stride + kRun - 1) / kRun;
+    const int64_t units = static_cast<int64_t>(a.B) * runs;
+    for (int64_t u = w; u < units; u += warps) {
+        const int b = static_cast<int>(u / runs), k0 = static_cast<int>(u - static_cast<int64_t>(b) * runs) * kRun;
+        const int keep = blocks_for(a.new_len[b], a.bs), held = blocks_for(a.ctx_len[b], a.bs);
+        if (k0 >= held || k0 + kRun <= keep) continue;
+        const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
+        int id[kRun / 32];
+#pragma unroll
+        for (int x = 0; x < kRun / 32; ++x) {
+            const int k = k0 + 32 * x + lane;
+            id[x] = k >= keep && k < held ? row[k] : -1;
+        }
+#pragma unroll
+        for (int x = 0; x < kRun / 32; ++x) {
+            const int k = k0 + 32 * x + lane;
+            if (k < keep || k >= held) continue;
+            if (id[x] < 0 || id[x] >= a.pool_blocks) raise_status(status, SP_ERR_DEVICE);
+            else atomicAdd(a.shared + id[x], by);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kDropThreads) drop_blocks_kernel(const PageArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    if (!lengths_fit(a)) return;
+    count_drops(a, -1, static_cast<int64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5),
+                static_cast<int64_t>(gridDim.x) * (kDropThreads / 32), a.status);
+}
+
+// Counts [4 i, 4 i + 4) of the pool's (0 behind its end).
+__device__ __forceinline__ int4 counts_at(const PageArgs& a, int64_t i) {
+    int4 v = make_int4(0, 0, 0, 0);
+    if (i < a.pool_blocks) v.x = a.shared[i];
+    if (i + 1 < a.pool_blocks) v.y = a.shared[i + 1];
+    if (i + 2 < a.pool_blocks) v.z = a.shared[i + 2];
+    if (i + 3 < a.pool_blocks) v.w = a.shared[i + 3];
+    return v;
+}
+
+__global__ void __cluster_dims__(kSweepCtas, 1, 1) __launch_bounds__(kSweepThreads) sweep_blocks_kernel(const PageArgs a) {
+    namespace cg = cooperative_groups;
+    __shared__ int sums[32];
+    __shared__ int told[2];     // blocks freed in the CTA's slice; a count below -1
+    const cg::cluster_group cluster = cg::this_cluster();
+    const int rank = static_cast<int>(cluster.block_rank());
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool fit = lengths_fit(a);
+    const int n_free = *a.n_free;
+    // a slice of whole steps for each CTA
+    const int64_t steps = (static_cast<int64_t>(a.pool_blocks) + kSweepPer - 1) / kSweepPer;
+    const int64_t first = steps * rank / kSweepCtas, last = steps * (rank + 1) / kSweepCtas;
+    int freed = 0;
+    bool low = false;
+    for (int64_t s = first; s < last && fit; ++s) {
+        const int4 v = counts_at(a, s * kSweepPer + 4 * tid);
+        freed += (v.x == -1) + (v.y == -1) + (v.z == -1) + (v.w == -1);
+        low |= min(min(v.x, v.y), min(v.z, v.w)) < -1;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) freed += __shfl_xor_sync(0xffffffffu, freed, o);
+    if (lane == 0) sums[warp] = freed;
+    low = __syncthreads_or(low);
+    if (tid == 0) {
+        int all = 0;
+        for (int k = 0; k < 32; ++k) all += sums[k];
+        told[0] = all;
+        told[1] = low;
+    }
+    cluster.sync();
+    int64_t base = n_free, total = 0;
+    bool bad = !fit;
+    for (int k = 0; k < kSweepCtas; ++k) {
+        const int* o = cluster.map_shared_rank(told, k);
+        if (k < rank) base += o[0];
+        total += o[0];
+        bad |= o[1] != 0;
+    }
+    const bool room = n_free + total <= a.free_cap;
+    const bool go = !bad && room;
+    cluster.sync();   // (every count is read before a block changes its own again)
+    for (int b = rank * kSweepThreads + tid; b < a.B; b += kSweepCtas * kSweepThreads)
+        a.kv_len[b] = go ? a.new_len[b] : a.ctx_len[b];
+    if (rank == 0 && tid == 0) {
+        *a.n_left = static_cast<int32_t>(go ? n_free + total : n_free);
+        if (bad) raise_status(a.status, SP_ERR_DEVICE);
+        else if (!room) raise_status(a.status, SP_ERR_CAPACITY);
+    }
+    if (!go) {   // every holder back
+        if (fit) count_drops(a, 1, static_cast<int64_t>(rank) * 32 + warp, int64_t(32) * kSweepCtas, nullptr);
+        return;
+    }
+    if (told[0] == 0) return;
+    for (int64_t s = first; s < last; ++s) {
+        const int64_t i = s * kSweepPer + 4 * tid;
+        const int4 v = counts_at(a, i);
+        const int mine = (v.x == -1) + (v.y == -1) + (v.z == -1) + (v.w == -1);
+        int incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        __syncthreads();   // (the sums of the step before are read)
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        int own = sums[lane], run = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += x;
+        }
+        const int all = __shfl_sync(0xffffffffu, run, 31);
+        int64_t at = base + __shfl_sync(0xffffffffu, run - own, warp) + incl - mine;
+        const int c[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (c[k] == -1) {
+                a.free_out[at++] = static_cast<int32_t>(i + k);
+                a.shared[i + k] = 0;
+            }
+        base += all;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_copy_kv(const sp_copy_shape* s, void* const* pools, const int32_t* src, const int32_t* dst,
+                           const int32_t* block_table, const int32_t* src_off, const int32_t* n_used,
+                           int32_t* status, cudaStream_t st) {
+    CopyArgs a = {};
+    for (int i = 0; i < s->n_pools; ++i) a.pools[i] = pools[i];
+    a.src = src;
+    a.dst = dst;
+    a.table = block_table;
+    a.src_off = src_off;
+    a.n_used = n_used;
+    a.status = status;
+    a.sb = s->stride_block, a.st = s->stride_token, a.sh = s->stride_head;
+    a.pool_blocks = static_cast<int>(s->pool_blocks);
+    a.n_pools = s->n_pools;
+    a.entries = s->n_entries;
+    a.rows = s->rows;
+    a.bs = s->block_size;
+    a.hk = s->n_kv_heads;
+    a.d = s->head_dim;
+    a.fp4 = s->fp4;
+    a.B = s->n_seqs;
+    a.table_stride = s->table_stride;
+    const int64_t parts = a.fp4 && a.rows > 1 ? a.hk : a.rows;
+    int64_t grid = (static_cast<int64_t>(a.entries) * parts * a.n_pools + kCopyWarps - 1) / kCopyWarps;
+    const int64_t most = int64_t(kCopyCtas) * device_sms();
+    if (grid > most) grid = most;
+    return launch_k(copy_kv_kernel, static_cast<unsigned>(grid), kCopyThreads, 0, st, a);
+}
+
+cudaError_t launch_fork_blocks(const sp_pages_shape* s, const int32_t* src, const int32_t* dst,
+                               const int32_t* ctx_len, int32_t* table, int32_t* shared, const int32_t* free_blocks,
+                               const int32_t* n_free, int32_t* kv_len, int32_t* copy_src, int32_t* copy_dst,
+                               int32_t* n_left, int32_t* status, cudaStream_t st) {
+    PageArgs a = {};
+    a.src = src;
+    a.dst = dst;
+    a.ctx_len = ctx_len;
+    a.table = table;
+    a.shared = shared;
+    a.free_in = free_blocks;
+    a.n_free = n_free;
+    a.kv_len = kv_len;
+    a.copy_src = copy_src;
+    a.copy_dst = copy_dst;
+    a.n_left = n_left;
+    a.status = status;
+    a.B = s->n_seqs;
+    a.F = s->n_forks;
+    a.bs = s->block_size;
+    a.table_stride = s->table_stride;
+    a.pool_blocks = s->pool_blocks;
+    a.free_cap = s->free_capacity;
+    const size_t smem = 8 * static_cast<size_t>(a.F) + 4 * ((static_cast<size_t>(a.B) + 31) / 32);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(fork_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    const int64_t units = static_cast<int64_t>(a.F) * ((a.table_stride + kRun - 1) / kRun);
+    const int64_t work = units * 32 > a.B ? units * 32 : a.B;
+    int64_t grid = (work + kForkThreads - 1) / kForkThreads;
+    const int sms = device_sms();
+    if (grid > sms) grid = sms;
+    return launch_k(fork_blocks_kernel, static_cast<unsigned>(grid), kForkThreads, smem, st, a);
+}
+
+cudaError_t launch_free_blocks(const sp_pages_shape* s, const int32_t* ctx_len, const int32_t* new_len,
+                               const int32_t* table, int32_t* shared, int32_t* free_blocks, const int32_t* n_free,
+                               int32_t* kv_len, int32_t* n_left, int32_t* status, cudaStream_t st) {
+    PageArgs a = {};
+    a.ctx_len = ctx_len;
+    a.new_len = new_len;
+    a.table = const_cast<int32_t*>(table);
+    a.shared = shared;
+    a.free_out = free_blocks;
+    a.n_free = n_free;
+    a.kv_len = kv_len;
+    a.n_left = n_left;
+    a.status = status;
+    a.B = s->n_seqs;
+    a.bs = s->block_size;
+    a.table_stride = s->table_stride;
+    a.pool_blocks = s->pool_blocks;
+    a.free_cap = s->free_capacity;
+    const int64_t units = static_cast<int64_t>(a.B) * ((a.table_stride + kRun - 1) / kRun);
+    int64_t grid = (units + kDropThreads / 32 - 1) / (kDropThreads / 32);
+    const int64_t most = int64_t(2) * device_sms();
+    if (grid > most) grid = most;
+    const cudaError_t e = launch_k(drop_blocks_kernel, static_cast<unsigned>(grid), kDropThreads, 0, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_k(sweep_blocks_kernel, kSweepCtas, kSweepThreads, 0, st, a);
+}
+
+}  // namespace sp

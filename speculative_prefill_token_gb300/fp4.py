@@ -1,0 +1,128 @@
+"""A block-paged cache held in 4 bits: store, attention, rows read back.
+Argument checks and marshalling only, as in paged.py, whose operators these
+stand beside: block tables and slots are those of block_tables.
+
+A pool is ``uint8 [num_blocks, Hk, block_size / 8, 9 d / 2]`` (make_pool_fp4): a
+value is an e2m1 number times an e4m3 scale that 16 neighbours of a row share,
+times a factor of the whole pool, 4.5 bits an element. Number times scale is
+exact in bf16 and fp16. A step of the target:
+
+  slots, kv_len, n_left = block_tables(ctx_len, out.kept_off, free, n_free, table, block_size, n_tokens=T)
+  # for each layer, its pools and their factors:
+  q = append_kv_fp4(k, v, slots, k_pool, v_pool, q=q, positions=out.kept_pos, cos_sin=cos_sin, n_new=out.n_kept)
+  o = paged_attention_fp4(q, out.kept_off, kv_len, table, k_pool, v_pool, ws=ws)
+
+Forward only: no gradient is recorded, and tensors are written without moving
+their version counters.
+"""
+
+from . import _check, lib
+from . import paged
+from .paged import _handle, _new, torch_side
+
+
+def make_pool_fp4(num_blocks: int, block_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
+    """A zeroed 4-bit pool of keys or of values (block_size a multiple of 8,
+    head_dim 64, 128 or 256)."""
+    import torch
+    if head_dim not in (64, 128, 256) or block_size < 8 or block_size % 8:
+        raise ValueError("head_dim must be 64, 128 or 256 and block_size a multiple of 8")
+    return torch.zeros(num_blocks, n_kv_heads, block_size // 8, 9 * head_dim // 2, dtype=torch.uint8, device=device)
+
+
+def append_kv_fp4(k, v, slot_map, k_pool, v_pool, q=None, q_out=None, positions=None, cos_sin=None, n_new=None,
+                  k_scale: float = 1.0, v_scale: float = 1.0, status=None, stream=None):
+    """append_kv into 4-bit pools: keys (rotated in 32 bits) and values are
+    divided by the pools' factors and stored; queries as there. The largest of 16
+    neighbours is stored as 6 times their scale, which reaches from 2^-9 to 448:
+    factors that bring the rows to between 0.1 and 1000 keep all of its bits. A
+    group with an infinity or NaN reads back as NaN."""
+    if q is not None and q_out is None:
+        q_out = _new(q.shape, q.dtype, q, stream)
+    rc = (paged._side or torch_side()).append_kv_fp4(k, v, slot_map, k_pool, v_pool, q, q_out, positions, cos_sin,
+                                                     n_new, status, k_scale, v_scale, _handle(stream))
+    if rc:
+        _check(rc, "sp_append_kv_fp4")
+    return q_out
+
+
+def unpack_fp4(pool, dtype=None, slots=None, scale: float = 1.0, out=None, status=None, stream=None):
+    """Rows of a 4-bit pool as bf16 (or fp16) values: all of them, [num_blocks,
+    block_size, Hk, d] as specprefill_score_kv and paged_attention take a pool, or
+    those at ``slots`` (int32, device; -1 gives zeros), [T, Hk, d]. ``scale`` is
+    the pool's factor."""
+    import torch
+    if out is None:
+        if pool.dim() != 4:
+            raise ValueError("pool must be a 4-bit pool (make_pool_fp4)")
+        blocks, hk, groups, width = pool.shape
+        shape = (blocks, groups * 8, hk, width * 2 // 9) if slots is None else (slots.numel(), hk, width * 2 // 9)
+        out = _new(shape, dtype or torch.bfloat16, pool, stream)
+    # (a view, so that the rows are written in place)
+    rows = out.view(-1, *out.shape[2:]) if slots is None else out
+    rc = (paged._side or torch_side()).unpack_fp4(pool, slots, rows, scale, status, _handle(stream))
+    if rc:
+        _check(rc, "sp_unpack_fp4")
+    return out
+
+
+def _dense(kv_tokens, k_pool):
+    return k_pool.shape[0] * k_pool.shape[2] * 8 if kv_tokens is None else int(kv_tokens)
+
+
+class _Workspace:
+    """Device workspace of paged_attention_fp4 and what it was made for."""
+
+    def __init__(self, buffer, dense):
+        self.buffer = buffer
+        self.dense = dense
+
+    def data_ptr(self):
+        return self.buffer.data_ptr()
+
+    def numel(self):
+        return self.buffer.numel()
+
+
+def make_attention_fp4_workspace(q, n_seqs: int, k_pool, max_new=None, kv_tokens=None, stream=None):
+    """Workspace of paged_attention_fp4 for queries of q's shape (its rows bound
+    the new tokens of a call) of ``n_seqs`` requests over pools like ``k_pool``;
+    calls that share one must be ordered. Requests with many new tokens are
+    computed over a 16-bit copy of their cached tokens in the workspace:
+    ``kv_tokens`` bounds those tokens (default: as many as the pool has;
+    requests that do not fit are computed from the 4-bit rows, more slowly).
+    With a small ``max_new``, the most new tokens of a request, none is needed."""
+    import torch
+    dense = _dense(kv_tokens, k_pool)
+    n = torch_side().workspace_fp4(q, n_seqs, k_pool, max_new, dense)
+    if n < 0:
+        _check(-n, "sp_paged_attention_fp4_workspace")
+    ws = _new(n + 256, torch.uint8, q, stream)
+    off = (-ws.data_ptr()) % 256
+    ws = ws[off:off + n]
+    handle = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+    _check(lib().sp_workspace_init(ws.data_ptr(), n, handle), "sp_workspace_init")
+    return _Workspace(ws, dense)
+
+
+def paged_attention_fp4(q, q_off, kv_len, block_table, k_pool, v_pool, causal: bool = True, window: int = 0,
+                        scale: float = 0.0, k_scale: float = 1.0, v_scale: float = 1.0, out=None, lse=None,
+                        max_new=None, ws=None, stream=None, spin_limit: int = 0):
+    """paged_attention over 4-bit pools with the factors ``k_scale`` and
+    ``v_scale``: the attention over the values that unpack_fp4 gives, with
+    the same arguments, masks and outputs. ``max_new`` (default: the rows of q) is the most
+    new tokens of a request; a decode step that says 1 launches less. ``ws`` from
+    make_attention_fp4_workspace, with its status in device_status; without
+    it the call allocates one, whose status is lost."""
+    if out is None:
+        out = _new(q.shape, q.dtype, q, stream)
+    if q.shape[0] == 0:
+        return out
+    if ws is None:
+        ws = make_attention_fp4_workspace(q, kv_len.numel(), k_pool, max_new, None, stream)
+    rc = (paged._side or torch_side()).paged_attention_fp4(
+        q, q_off, kv_len, block_table, k_pool, v_pool, causal, window, scale, k_scale, v_scale, out, lse, max_new,
+        ws.buffer, ws.dense, spin_limit, _handle(stream))
+    if rc:
+        _check(rc, "sp_paged_attention_fp4")
+    return out
