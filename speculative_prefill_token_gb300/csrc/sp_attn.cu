@@ -134,6 +134,7 @@ struct AttnArgs {
     const int32_t* q_off;
     const int32_t* kv_len;
     const int32_t* table;
+    const int32_t* only;   // [B] or null: requests below 0 are left out
     const uint16_t* q;
     const uint16_t* k;
     const uint16_t* v;
@@ -155,6 +156,7 @@ struct AttnArgs {
     int hk_shift, hv_shift;  // rows of a K and of a V box, as powers of two
     uint32_t q_bytes;    // of one 64-element chunk of a query tile
     float scale2;
+    float out_scale;     // factor of the result
 };
 
 // ------------------------------------------------------------ plan
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
         if (b < a.B) {
             const int64_t lo = a.q_off[b], hi = a.q_off[b + 1];
             if (bad_request(a, lo, hi, a.kv_len[b])) bad = 1;
-            else n = (hi - lo + tpi - 1) / tpi;
+            else if (!a.only || a.only[b] >= 0) n = (hi - lo + tpi - 1) / tpi;
         }
         int64_t total;
         const int64_t at = items + block_scan<kPlanThreads>(n, sums, &total);
@@ -343,7 +345,7 @@ __device__ __forceinline__ int local_plan(const AttnArgs& a, int tiles, LocalPla
     if (t < a.B) {
         const int lo = a.q_off[t], hi = a.q_off[t + 1], kv = a.kv_len[t];
         bad = bad_request(a, lo, hi, kv) || (t == 0 && lo != 0);
-        if (!bad) n = (hi - lo + tpi - 1) / tpi;
+        if (!bad && (!a.only || a.only[t] >= 0)) n = (hi - lo + tpi - 1) / tpi;
         p.q0[t] = lo;
         p.nq[t] = hi - lo;
         p.kv[t] = kv;
@@ -979,7 +981,7 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
     // the exact ones out is the same to four digits of its error, lse is 0.5e-6 in
     // place of 0.7e-6 off at 8.5, where a step of 32 bits is 1e-6, and a prompt at
     // d = 256 and the mixed batch take 1 % longer)
-    const float inv = split ? 1.0f : none ? 0.0f : __fdividef(1.0f, e.l);
+    const float inv = split ? 1.0f : none ? 0.0f : __fdividef(1.0f, e.l) * a.out_scale;
     const float e0 = e.f0 * inv, e1 = e.f1 * inv;
     char* dst = split ? reinterpret_cast<char*>(a.part_o + static_cast<int64_t>(e.part) * D + e.col0)
                       : reinterpret_cast<char*>(a.out + e.t * a.o_st + e.h * a.o_sh + e.col0);
@@ -1087,7 +1089,7 @@ __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
             uint16_t* o = a.out + t * a.o_st + h * a.o_sh + lane * E;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const uint32_t w = none ? 0u : pack_pair<kBf16>(acc[i] / l, 0.0f);
+                const uint32_t w = none ? 0u : pack_pair<kBf16>(acc[i] / l * a.out_scale, 0.0f);
                 o[i] = static_cast<uint16_t>(w & 0xffffu);
             }
             if (a.lse && lane == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (m - kBias + __log2f(l)) * kLn2;
@@ -1533,7 +1535,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
         const Row zero{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
         auto write = [&](Place x, const Row& y) {
             const bool none = y.sum == 0.0f;
-            const float inv = none ? 0.0f : 1.0f / y.sum;
+            const float inv = none ? 0.0f : 1.0f / y.sum * a.out_scale;
             const int tok = x.row / a.G;
             const int64_t t = job.tok0 + x.tile * a.tq + tok;
             const int h = job.g * a.G + x.row - tok * a.G;
@@ -1733,7 +1735,7 @@ size_t attn_workspace(const sp_paged_shape* s) { return layout(s, attn_grid()).t
 cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params* p, const int32_t* q_off,
                                    const int32_t* kv_len, const int32_t* table, const uint16_t* q,
                                    const uint16_t* k_pool, const uint16_t* v_pool, uint16_t* out, float* lse,
-                                   void* ws, cudaStream_t st) {
+                                   void* ws, cudaStream_t st, const AttnMore* more) {
     const int d = s->head_dim, bs = s->block_size;
     const bool bf16 = s->dtype == SP_DTYPE_BF16;
     AttnArgs a;
@@ -1747,7 +1749,9 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     a.v = v_pool;
     a.out = out;
     a.lse = lse;
-    a.status = &ws_ptr<WsHeader>(ws, 0)->status;
+    a.status = more ? more->status : &ws_ptr<WsHeader>(ws, 0)->status;
+    a.only = more ? more->only : nullptr;
+    a.out_scale = more ? more->out_scale : 1.0f;
     a.head = ws_ptr<PlanHead>(ws, l.head);
     a.items = ws_ptr<Item>(ws, l.items);
     a.pre = ws_ptr<int64_t>(ws, l.pre);

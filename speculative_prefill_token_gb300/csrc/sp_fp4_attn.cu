@@ -29,6 +29,11 @@
 // The warps' results are joined at the end of an item, those of CTAs that share
 // an item by another kernel, in their order: results do not depend on timing.
 //
+// Requests with many rows are bound by the products, not by the cache: their keys
+// and values are written once as 16-bit values into the workspace (exactly), and
+// computed by the attention over a 16-bit cache (sp_attn.cu), on
+// fifth-generation tensor cores, 128 rows at a time.
+//
 // Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT in
 // the workspace status, and the CTA's copies in flight land before it returns.
 #include <cuda_bf16.h>
@@ -911,13 +916,159 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const Args a) {
     if (a.lse && threadIdx.x == 0) a.lse[t * a.G * a.hk + h] = sum == 0.0f ? -INFINITY : (top - kBias + __log2f(sum)) * kLn2;
 }
 
+// ------------------------------------------------------------ requests with many rows
+
+constexpr int kDenseRows = 64;        // rows from which a request is read through 16 bits
+constexpr int kDenseBlock = 128;      // tokens of a block of the copy
+constexpr int kDenseThreads = 256;
+
+struct DenseArgs {
+    const int32_t* q_off;
+    const int32_t* kv_len;
+    const int32_t* table;
+    const uint8_t* k;
+    const uint8_t* v;
+    uint16_t* k_out;       // [hk][cap * kDenseBlock][d]
+    uint16_t* v_out;
+    int32_t* status;
+    int32_t* base;         // [B] first block of a request's copy, or -1
+    int32_t* dense_table;  // [B][width]
+    int2* owner;           // [cap] request and table column of a block
+    int32_t* used;         // blocks in use
+    int64_t k_sb, k_sh, v_sb, v_sh, pool_blocks;
+    int B, hk, G, d, bs, table_stride, width, max_new, window, cap;
+};
+
+// Which requests are read through 16 bits, and where their copies lie: those of
+// kDenseRows rows and more, in order, as long as their blocks fit. By one block.
+__global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const DenseArgs a) {
+    __shared__ int64_t sums[32];
+    __shared__ int most;
+    grid_dep_wait();
+    grid_dep_launch();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) most = 0;
+    auto first_of = [&](int nq, int kv) { return a.window > 0 ? max(0, kv - nq - a.window + 1) / kDenseBlock : 0; };
+    int64_t blocks = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+        const int b = b0 + tid;
+        int64_t n = 0;
+        if (b < a.B) {
+            // (lengths that are out of range are told by the kernels that follow)
+            const int64_t nq = static_cast<int64_t>(a.q_off[b + 1]) - a.q_off[b], kv = a.kv_len[b];
+            if (nq * a.G >= kDenseRows && nq <= a.max_new && kv > 0 && kv <= static_cast<int64_t>(a.width) * kDenseBlock &&
+                (kv + a.bs - 1) / a.bs <= a.table_stride)
+                n = (kv + kDenseBlock - 1) / kDenseBlock - first_of(static_cast<int>(nq), static_cast<int>(kv));
+        }
+        int64_t total;
+        const int64_t at = blocks + block_scan<kPlanThreads>(n, sums, &total);
+        if (b < a.B) a.base[b] = n > 0 && at + n <= a.cap ? static_cast<int32_t>(at) : -1;
+        if (n > 0 && at + n <= a.cap) atomicMax(&most, static_cast<int>(at + n));
+        blocks += total;
+    }
+    __syncthreads();
+    for (int b0 = 32 * warp; b0 < a.B; b0 += kPlanThreads) {
+        const int mine = b0 + lane < a.B ? a.base[b0 + lane] : -1;
+        for (unsigned who = __ballot_sync(0xffffffffu, mine >= 0); who; who &= who - 1) {
+            const int b = b0 + __ffs(who) - 1, base = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+            const int kv = a.kv_len[b], first = first_of(a.q_off[b + 1] - a.q_off[b], kv);
+            for (int i = first + lane; i < (kv + kDenseBlock - 1) / kDenseBlock; i += 32) {
+                a.dense_table[static_cast<int64_t>(b) * a.width + i] = base + i - first;
+                a.owner[base + i - first] = make_int2(b, i);
+            }
+        }
+    }
+    if (tid == 0) *a.used = most;
+}
+
+// The copies: a block of tokens of one head by a CTA, 16 elements a thread.
+template <bool kBf16>
+__global__ void __launch_bounds__(kDenseThreads) fp4_dense_kernel(const DenseArgs a) {
+    grid_dep_wait();
+    grid_dep_launch();
+    const int groups = a.d / kFp4Group, units = *a.used * a.hk;
+    const int64_t head = static_cast<int64_t>(a.cap) * kDenseBlock * a.d;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        const int blk = u / a.hk, h = u - blk * a.hk;
+        const int2 own = a.owner[blk];
+        const int kv = a.kv_len[own.x];
+        for (int x = threadIdx.x; x < kDenseBlock * groups; x += kDenseThreads) {
+            const int r = x / groups, g = x - r * groups, j = own.y * kDenseBlock + r;
+            if (j >= kv) continue;
+            const int col = j / a.bs, within = j - col * a.bs;
+            int id = a.table[static_cast<int64_t>(own.x) * a.table_stride + col];
+            if (id < 0 || id >= a.pool_blocks) {
+                atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+                id = 0;
+            }
+            const int64_t rec = static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
+            const int code = within % kFp4Rows * (a.d / 2) + 8 * g, scale = fp4_codes(a.d) + within % kFp4Rows * groups + g;
+            const int64_t to = h * head + (static_cast<int64_t>(blk) * kDenseBlock + r) * a.d + 16 * g;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint8_t* src = (v ? a.v + id * a.v_sb + h * a.v_sh : a.k + id * a.k_sb + h * a.k_sh) + rec;
+                const uint2 c = *reinterpret_cast<const uint2*>(src + code);
+                const uint32_t s = fp8_unpack(src[scale] * 0x101u);
+                uint32_t n[8], o[8];
+                fp4_unpack(c.x, *reinterpret_cast<uint32_t(*)[4]>(n));
+                fp4_unpack(c.y, *reinterpret_cast<uint32_t(*)[4]>(n + 4));
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    o[i] = mul_f16x2(n[i], s);
+                    if constexpr (kBf16) {   // (exact: 6 significant bits)
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
+                        const __nv_bfloat162 w = __floats2bfloat162_rn(f.x, f.y);
+                        o[i] = *reinterpret_cast<const uint32_t*>(&w);
+                    }
+                }
+                uint4* dst = reinterpret_cast<uint4*>((v ? a.v_out : a.k_out) + to);
+                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        }
+    }
+}
+
 // ------------------------------------------------------------ host
 
 constexpr int kMostRows = 16;
 
 struct Layout {
-    size_t pre, starts, ml, o, total;
+    size_t pre, starts, ml, o;
+    int dense_cap, dense_width;   // blocks of the copy (0: none), entries of a row of its table
+    size_t base, table, owner, used, k, v, inner, total;
 };
+
+int most_new(const sp_fp4_shape* s) { return s->max_new > 0 ? s->max_new : s->n_tokens; }
+
+// Entries of a row of the copy's table: as many as the pool's tokens fill (the
+// workspace is made before a table is there; a longer request, which has blocks
+// twice, is read from the 4-bit rows). More of them than kMaxDenseTable in all:
+// there is no copy.
+constexpr int64_t kMaxDenseTable = int64_t(1) << 28;
+
+int dense_width(const sp_fp4_shape* s) {
+    return static_cast<int>((s->pool_blocks * s->block_size + kDenseBlock - 1) / kDenseBlock);
+}
+
+// The call over the copy.
+sp_paged_shape dense_shape(const sp_fp4_shape* s, int cap, int width) {
+    sp_paged_shape p = {};
+    p.n_seqs = s->n_seqs;
+    p.n_q_heads = s->n_q_heads;
+    p.n_kv_heads = s->n_kv_heads;
+    p.head_dim = s->head_dim;
+    p.dtype = s->dtype;
+    p.block_size = kDenseBlock;
+    p.table_stride = width;
+    p.n_tokens = s->n_tokens;
+    p.pool_tokens = static_cast<int64_t>(cap) * kDenseBlock;
+    p.q_stride_token = s->q_stride_token, p.q_stride_head = s->q_stride_head;
+    p.o_stride_token = s->o_stride_token, p.o_stride_head = s->o_stride_head;
+    p.k_stride_token = p.v_stride_token = s->head_dim;
+    p.k_stride_head = p.v_stride_head = p.pool_tokens * s->head_dim;
+    return p;
+}
 
 int grid_of() {
     const int sms = device_sms();
@@ -936,6 +1087,24 @@ Layout layout(const sp_fp4_shape* s, int grid) {
     l.starts = take(sizeof(Start) * (static_cast<size_t>(grid) + 1));
     l.ml = take(8 * static_cast<size_t>(grid) * 2 * kMostRows);
     l.o = take(4 * static_cast<size_t>(grid) * 2 * kMostRows * s->head_dim);
+    const int64_t rows = static_cast<int64_t>(s->n_tokens) * (s->n_q_heads / s->n_kv_heads);
+    const int64_t most = static_cast<int64_t>(most_new(s)) * (s->n_q_heads / s->n_kv_heads);
+    l.dense_cap = 0;
+    if (s->dense_tokens > 0 && most >= kDenseRows && static_cast<int64_t>(dense_width(s)) * s->n_seqs <= kMaxDenseTable) {
+        // (a request's last block may be begun)
+        const int64_t begun = rows / kDenseRows < s->n_seqs ? rows / kDenseRows : s->n_seqs;
+        l.dense_cap = static_cast<int>(s->dense_tokens / kDenseBlock + begun);
+        l.dense_width = dense_width(s);
+        const size_t copy = static_cast<size_t>(l.dense_cap) * kDenseBlock * s->n_kv_heads * s->head_dim * 2;
+        l.base = take(4 * static_cast<size_t>(s->n_seqs));
+        l.table = take(4 * static_cast<size_t>(s->n_seqs) * l.dense_width);
+        l.owner = take(8 * static_cast<size_t>(l.dense_cap));
+        l.used = take(4);
+        l.k = take(copy);
+        l.v = take(copy);
+        const sp_paged_shape p = dense_shape(s, l.dense_cap, l.dense_width);
+        l.inner = take(attn_workspace(&p));
+    }
     l.total = off;
     return l;
 }
@@ -1003,6 +1172,50 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(d));
     a.scale2 = static_cast<float>(scale * p->k_scale * 1.4426950408889634);
     a.v_scale = p->v_scale;
+    if (l.dense_cap > 0) {
+        DenseArgs e;
+        e.q_off = q_off;
+        e.kv_len = kv_len;
+        e.table = table;
+        e.k = k_pool;
+        e.v = v_pool;
+        e.k_out = ws_ptr<uint16_t>(ws, l.k);
+        e.v_out = ws_ptr<uint16_t>(ws, l.v);
+        e.status = a.status;
+        e.base = ws_ptr<int32_t>(ws, l.base);
+        e.dense_table = ws_ptr<int32_t>(ws, l.table);
+        e.owner = ws_ptr<int2>(ws, l.owner);
+        e.used = ws_ptr<int32_t>(ws, l.used);
+        e.k_sb = a.k_sb, e.k_sh = a.k_sh, e.v_sb = a.v_sb, e.v_sh = a.v_sh;
+        e.pool_blocks = a.pool_blocks;
+        e.B = a.B;
+        e.hk = a.hk;
+        e.G = a.G;
+        e.d = d;
+        e.bs = a.bs;
+        e.table_stride = a.table_stride;
+        e.width = l.dense_width;
+        e.max_new = a.max_new;
+        e.window = a.window;
+        e.cap = l.dense_cap;
+        cudaError_t rc = launch_k(fp4_dense_plan_kernel, 1, kPlanThreads, 0, st, e);
+        if (rc != cudaSuccess) return rc;
+        const int64_t units = static_cast<int64_t>(l.dense_cap) * a.hk, most = int64_t(8) * a.grid;
+        rc = launch_k(a.bf16 ? fp4_dense_kernel<true> : fp4_dense_kernel<false>,
+                      static_cast<unsigned>(units < most ? units : most), kDenseThreads, 0, st, e);
+        if (rc != cudaSuccess) return rc;
+        const sp_paged_shape shape = dense_shape(s, l.dense_cap, l.dense_width);
+        sp_attn_params params;
+        params.causal = p->causal;
+        params.window = p->window;
+        params.scale = static_cast<float>(scale * p->k_scale);
+        params.spin_limit = p->spin_limit;
+        const AttnMore more{e.base, a.status, a.v_scale};
+        rc = launch_paged_attention(&shape, &params, q_off, kv_len, e.dense_table, q, e.k_out, e.v_out, out, lse,
+                                    ws_ptr<char>(ws, l.inner), st, &more);
+        if (rc != cudaSuccess) return rc;
+        a.dense = e.base;
+    }
     const bool one = static_cast<int64_t>(a.max_new) * a.G <= 8;
     if (d == 64) return one ? launch_rows<64, 1>(a, st) : launch_rows<64, 2>(a, st);
     if (d == 128) return one ? launch_rows<128, 1>(a, st) : launch_rows<128, 2>(a, st);

@@ -35,9 +35,16 @@ cudaError_t launch_append_kv(const sp_append_shape* s, const uint16_t* q, const 
 // Bytes of workspace of the attention (header included).
 size_t attn_workspace(const sp_paged_shape* s);
 
+// What a caller inside the library may ask for besides (sp_fp4_attn.cu).
+struct AttnMore {
+    const int32_t* only;   // device [B]: requests below 0 are left out
+    int32_t* status;       // in place of the workspace's
+    float out_scale;       // factor of the result
+};
+
 cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params* p, const int32_t* q_off,
                                    const int32_t* kv_len, const int32_t* table, const uint16_t* q,
                                    const uint16_t* k_pool, const uint16_t* v_pool, uint16_t* out, float* lse,
-                                   void* ws, cudaStream_t st);
+                                   void* ws, cudaStream_t st, const AttnMore* more = nullptr);
 
 }  // namespace sp
