@@ -24,18 +24,16 @@
 // Work. The new tokens x the G heads of a KV head are rows; an item is up to
 // 8 or 16 rows of a request and KV head, its unit a tile of 64 keys. All units
 // of all items are cut into equal contiguous ranges, one for each CTA (one CTA an
-// SM). A warp loads the codes of the CTA's tiles into a ring of stages by bulk
-// copies (a run of 8-token records each); tile i of the CTA goes to warp i mod 8.
-// The warps' results are joined at the end of an item, those of CTAs that share
+// SM); tile i of the CTA goes to warp i mod 12, which copies it into its own part
+// of shared memory while it works on the one before: no warp waits for another
+// one before the item's end. (One warp that loaded for all by bulk copies: some
+// 120 cycles a copy, two to sixteen of them a tile.) The warps' results are joined at the end of an item, those of CTAs that share
 // an item by another kernel, in their order: results do not depend on timing.
 //
 // Requests with many rows are bound by the products, not by the cache: their keys
 // and values are written once as 16-bit values into the workspace (exactly), and
 // computed by the attention over a 16-bit cache (sp_attn.cu), on
 // fifth-generation tensor cores, 128 rows at a time.
-//
-// Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT in
-// the workspace status, and the CTA's copies in flight land before it returns.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -53,15 +51,12 @@
 namespace sp {
 namespace {
 
-constexpr int kTileKeys = 64;
-constexpr int kTileRecs = kTileKeys / kFp4Rows;
-constexpr int kWarps = 8;                    // that compute
-constexpr int kThreads = 32 * (kWarps + 1);  // and the one that loads
+// Keys of a tile, the unit of work of a warp.
+__host__ __device__ constexpr int tile_keys(int d) { return d <= 128 ? 64 : 32; }
 constexpr int kItemCost = 8;                 // of an item besides its tiles, in tiles
 constexpr int kLocalSeqs = 1024;             // requests of a plan made by every CTA
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxGrid = 256;
-constexpr int64_t kDrainSpin = int64_t(1) << 22;
 constexpr float kSlack = 8.0f;               // log2 units the reference may lag behind the maximum
 constexpr float kBias = 6.0f;                // fp16 weights are scaled by 2^6: normal down to 2^-20 of the reference
 constexpr float kLn2 = 0.6931471805599453f;
@@ -88,8 +83,9 @@ struct Args {
     Start* starts;             // [grid + 1]
     float* part_o;             // [2 grid][rows][d]
     float2* part_ml;           // [2 grid][rows] (reference, sum)
-    int64_t q_st, q_sh, o_st, o_sh, k_sb, k_sh, v_sb, v_sh, pool_blocks, spin;
+    int64_t q_st, q_sh, o_st, o_sh, k_sb, k_sh, v_sb, v_sh, pool_blocks;
     int B, hk, G, bs, table_stride, cap, max_new, causal, window, grid;
+    int tile_shift;            // log2 of a tile's keys
     int piece_shift;           // log2 of a copy's tokens: a block's, at most a tile's
     int local_plan, bf16;
     float scale2, v_scale;
@@ -129,6 +125,11 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* sums, int64_t*
     return __shfl_sync(0xffffffffu, all - mine, warp) + incl - v;
 }
 
+// Tiles that the keys below cache index n touch (n <= 2^30).
+__device__ __forceinline__ int tiles_below(const Args& a, int n) {
+    return (n + (1 << a.tile_shift) - 1) >> a.tile_shift;
+}
+
 // Key tiles that some row of a request sees, and its tiles of rows.
 struct Span {
     int tile0, tiles, row_tiles;
@@ -137,8 +138,8 @@ struct Span {
 __device__ __forceinline__ Span span_of(const Args& a, int nq, int kv, int rows) {
     Span s;
     const int lo = a.window > 0 ? max(0, kv - nq - a.window + 1) : 0;
-    s.tile0 = lo / kTileKeys;
-    s.tiles = kv > lo ? (kv + kTileKeys - 1) / kTileKeys - s.tile0 : 0;
+    s.tile0 = lo >> a.tile_shift;
+    s.tiles = kv > lo ? tiles_below(a, kv) - s.tile0 : 0;
     s.row_tiles = static_cast<int>((static_cast<int64_t>(nq) * a.G + rows - 1) / rows);
     return s;
 }
@@ -247,8 +248,8 @@ struct Walk {
             const int last = at.b == end.b && at.gj == end.gj ? end.off : sp.tiles;
             s.split = at.off > 0 || last < sp.tiles;
             // (the first row tiles of a chunk see less than its last)
-            s.first = max(sp.tile0 + at.off, s.lo / kTileKeys);
-            s.n = s.hi > s.lo ? max(0, min(sp.tile0 + last, (s.hi + kTileKeys - 1) / kTileKeys) - s.first) : 0;
+            s.first = max(sp.tile0 + at.off, s.lo >> a.tile_shift);
+            s.n = s.hi > s.lo ? max(0, min(sp.tile0 + last, tiles_below(a, s.hi)) - s.first) : 0;
             s.head = head;
             head = false;
             at.off = 0;
@@ -260,127 +261,104 @@ struct Walk {
 
 // ------------------------------------------------------------ shared memory
 
+// Warps of a CTA: 12 of 168 registers.
+constexpr int kWarps = 12;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 2;      // tiles of a warp in shared memory: one in work, the next on its way
+
 template <int D, int NT>
 struct Smem {
     static constexpr int kRows = 8 * NT;
     static constexpr uint32_t kRec = fp4_record(D);
-    static constexpr uint32_t kHalf = kTileRecs * kRec;   // K or V of a tile
-    static constexpr uint32_t kStage = 2 * kHalf;
+    static constexpr int kKeys = tile_keys(D);
+    static constexpr int kMt = kKeys / 16;                       // products over a tile's keys
+    static constexpr uint32_t kHalf = kKeys / kFp4Rows * kRec;   // K or V of a tile
     static constexpr int kAcc = D / 16 * NT * 4;          // accumulator registers of a lane
     static constexpr int kVals = kAcc + NT * 4;           // and references and sums
-    static constexpr uint32_t join = 0;                   // [kWarps / 2][kVals][32] floats
-    static constexpr uint32_t ring = kWarps / 2 * kVals * 32 * 4;
-    static constexpr int kStages = (200 * 1024 - ring) / kStage < 32 ? (200 * 1024 - ring) / kStage : 32;
-    static constexpr uint32_t bars = ring + kStages * kStage;
-    static constexpr uint32_t full = bars;
-    static constexpr uint32_t empty = full + 8 * kStages;
-    static constexpr uint32_t range = empty + 8 * kStages;  // [2] Start
-    static constexpr uint32_t sums = range + 2 * 16;
-    static constexpr uint32_t abort = sums + 32 * 8;
-    static constexpr uint32_t pre = abort + 16;
-    static constexpr uint32_t total = pre + 8 * kLocalSeqs;
-};
-
-struct Ctx {
-    uint8_t* smem;
-    uint32_t base;
-    volatile int* abort_flag;
-    int32_t* status;
-    int64_t spin;
-    __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) const {
-        if (mbar_wait_bounded(base + bar, parity & 1, spin, abort_flag)) return true;
-        *abort_flag = 1;
-        atomicCAS(status, 0, static_cast<int32_t>(SP_ERR_TIMEOUT));
-        return false;
-    }
+    // (a share for the join lies in the stage that its warp has just used)
+    static constexpr uint32_t kStage = 2 * kHalf > 128 * kVals ? 2 * kHalf : 128 * kVals;
+    static constexpr uint32_t ring = 0;                   // [kWarps][kStages] stages
+    static constexpr uint32_t range = kWarps * kStages * kStage;   // [2] Start
+    static constexpr uint32_t where = range + 2 * 16;     // [kWarps] where a warp left its share for the join
+    static constexpr uint32_t total = where + 4 * kWarps;
+    // the plan, before the first tile
+    static constexpr uint32_t sums = 0;
+    static constexpr uint32_t pre = 32 * 8;
+    static_assert(pre + 8 * (kLocalSeqs + 1) <= range && total <= 232448, "shared memory of one CTA");
 };
 
 // ------------------------------------------------------------ loads
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-        "l"(__cvta_generic_to_global(src)), "r"(bytes), "r"(bar)
-        : "memory");
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
 }
 
-// The tiles of the CTA's segments, by one warp. A tile is cut into pieces (runs of
-// tokens of one block); lane t * pieces + p looks up and copies piece p of the
-// t-th tile of a batch of 32 / pieces tiles. Pieces outside the item's keys are
-// not loaded (their blocks may be gone).
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Waits until all but the last N groups of this lane have landed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The tiles of one warp, every kWarps-th of the CTA's, on their way into its
+// stages. A tile is cut into pieces (runs of tokens of one block); lane p looks
+// piece p up. Pieces outside the item's keys are not loaded (their blocks may be
+// gone).
 template <int D, int NT>
-__device__ __forceinline__ void load_tiles(const Ctx& c, const Args& a, int lane) {
+struct Feed {
     using L = Smem<D, NT>;
-    constexpr unsigned kAll = 0xffffffffu;
-    const int piece = 1 << a.piece_shift, pieces = kTileKeys >> a.piece_shift;
-    const int per_batch = 32 / pieces, ti = lane / pieces, p = lane - ti * pieces;
-    const uint32_t bytes = (piece / kFp4Rows) * L::kRec;
-    const uint32_t dst = c.base + L::ring + p * bytes;
-    struct Batch {
-        int g, count;
-        const uint8_t *k, *v;   // of this lane's piece; null: not loaded
-    };
-    Walk w(reinterpret_cast<const Start*>(c.smem + L::range));
+    Walk w;
     Segment s;
-    s.n = 0;
-    int done = 0;   // tiles of the segment handed out
-    auto next = [&](Batch& x) -> bool {
-        while (done >= s.n) {
-            if (!w.next(a, L::kRows, s)) return false;
-            done = 0;
+    int k, id, row;   // the warp's next tile in the segment; this lane's block (-1: none) and row in it
+    bool live;
+
+    __device__ __forceinline__ Feed(const Args& a, const Start* range, int warp) : w(range), k(warp), id(-1), row(0), live(true) {
+        s.n = 0;
+        settle(a);
+    }
+    __device__ __forceinline__ void settle(const Args& a) {
+        while (live && k >= s.n) {
+            k -= s.n;
+            live = w.next(a, L::kRows, s);
         }
-        x.count = min(per_batch, s.n - done);
-        const int key = (s.first + done + ti) * kTileKeys + (p << a.piece_shift);
-        x.k = x.v = nullptr;
-        if (ti < x.count && key < s.hi && key + piece > s.lo) {
-            const int blk = key / a.bs, within = key - blk * a.bs;
-            int id = a.table[static_cast<int64_t>(s.b) * a.table_stride + blk];
+    }
+    __device__ __forceinline__ void next(const Args& a) {
+        k += kWarps;
+        settle(a);
+    }
+    __device__ __forceinline__ void look_up(const Args& a, int lane) {
+        const int key = (s.first + k) * L::kKeys + (lane << a.piece_shift);
+        id = -1;
+        if (lane < L::kKeys >> a.piece_shift && key < s.hi && key + (1 << a.piece_shift) > s.lo) {
+            const int blk = key / a.bs;
+            row = key - blk * a.bs;
+            id = __ldg(a.table + static_cast<int64_t>(s.b) * a.table_stride + blk);
             if (id < 0 || id >= a.pool_blocks) {
                 atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
                 id = 0;
             }
-            const int64_t rec = static_cast<int64_t>(within / kFp4Rows) * L::kRec;
-            x.k = a.k + id * a.k_sb + s.g * a.k_sh + rec;
-            x.v = a.v + id * a.v_sb + s.g * a.v_sh + rec;
         }
-        done += x.count;
-        return true;
-    };
-    int slot = 0;
-    uint32_t turn = 0;
-    bool ok = true;
-    Batch cur, after;
-    bool have = next(cur);
-    while (have && ok) {
-        const bool more = next(after);   // (looked up while this batch waits for its stages)
-        for (int i = 0; i < cur.count; ++i) {
-            ok = __all_sync(kAll, c.wait(L::empty + 8 * slot, turn ^ 1));
-            if (!ok) break;
-            const bool mine = ti == i && cur.k;
-            const uint32_t n = __popc(__ballot_sync(kAll, mine)) * bytes * 2;
-            const uint32_t bar = c.base + L::full + 8 * slot;
-            if (lane == 0) mbar_arrive_expect_tx(bar, n);
-            __syncwarp();
-            if (mine) {
-                bulk_load(dst + slot * L::kStage, cur.k, bytes, bar);
-                bulk_load(dst + slot * L::kStage + L::kHalf, cur.v, bytes, bar);
-            }
-            if (++slot == L::kStages) {
-                slot = 0;
-                turn ^= 1;
-            }
-        }
-        cur = after;
-        have = more;
     }
-    // every copy lands before the warp leaves: slots before `slot` were last used in
-    // this turn of the ring, the others in the one before (a wait on a first turn's
-    // parity 1 returns at once)
-    if (lane == 0)
-        for (int i = 0; i < L::kStages; ++i)
-            mbar_wait_spin(c.base + L::full + 8 * i, i < slot ? turn : turn ^ 1, kDrainSpin);
-    __syncwarp();
-}
+    __device__ __forceinline__ void issue(const Args& a, uint32_t dst, int lane) const {
+        const int pieces = L::kKeys >> a.piece_shift;
+        const uint32_t bytes = (L::kRec / kFp4Rows) << a.piece_shift;
+        dst += 16 * lane;
+        for (int p = 0; p < pieces; ++p, dst += bytes) {
+            const int blk = __shfl_sync(0xffffffffu, id, p);
+            if (blk < 0) continue;
+            const int64_t rec = static_cast<int64_t>(__shfl_sync(0xffffffffu, row, p) / kFp4Rows) * L::kRec + 16 * lane;
+            const uint8_t* k_src = a.k + blk * a.k_sb + s.g * a.k_sh + rec;
+            const uint8_t* v_src = a.v + blk * a.v_sb + s.g * a.v_sh + rec;
+#pragma unroll
+            for (uint32_t o = 0; o < L::kHalf; o += 512) {
+                if (o + 16 * lane >= bytes) break;
+                copy16(dst + o, k_src + o);
+                copy16(dst + L::kHalf + o, v_src + o);
+            }
+        }
+    }
+};
 
 // ------------------------------------------------------------ products
 
@@ -409,20 +387,32 @@ __device__ __forceinline__ uint32_t half2_of(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Loads from shared memory: a byte, two bytes, N words.
+__device__ __forceinline__ uint32_t lds_u8(uint32_t at) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(at));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at) {
+    uint16_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(at));
+    return r;
+}
+
 template <int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+__device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
     static_assert(N == 1 || N == 2 || N % 4 == 0, "words of a lane");
     if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t*>(p);
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(at));
     } else if constexpr (N == 2) {
-        const uint2 x = *reinterpret_cast<const uint2*>(p);
-        w[0] = x.x, w[1] = x.y;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
     } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(p + 4 * i);
-            w[i] = x.x, w[i + 1] = x.y, w[i + 2] = x.z, w[i + 3] = x.w;
-        }
+        for (int i = 0; i < N; i += 4)
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                         : "r"(at + 4 * i));
     }
 }
 
@@ -511,33 +501,38 @@ struct Worker {
     }
 
     // A tile whose copies have landed, its first key at cache index key0.
-    __device__ __forceinline__ void tile(const Args& a, const Segment& s, const uint8_t* kt, int key0) {
-        const uint8_t* vt = kt + L::kHalf;
-        const bool edge = key0 < s.all_lo || key0 + kTileKeys > s.all_hi;
-        float y[4][NT][4];
+    __device__ __forceinline__ void tile(const Args& a, const Segment& s, uint32_t kt, int key0) {
+        const uint32_t vt = kt + L::kHalf;
+        const uint32_t k_at = kt + gid * (D / 2) + tig * (D / 8);
+        const uint32_t kf_at = kt + fp4_codes(D) + gid * (D / 16) + tig * (D / 64);
+        const uint32_t v_at = vt + 2 * tig * (D / 2) + gid * (D / 16);
+        const uint32_t vf_at = vt + fp4_codes(D) + 2 * tig * (D / 16) + gid * (D / 8) / kFp4Group;
+        const bool edge = key0 < s.all_lo || key0 + L::kKeys > s.all_hi;
+        float y[L::kMt][NT][4];
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = 0; mt < L::kMt; ++mt) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) y[mt][n][c] = 0.0f;
-            const uint8_t *r0 = kt + 2 * mt * L::kRec, *r1 = r0 + L::kRec;
             uint32_t w0[D / 32], w1[D / 32];
-            load_words(r0 + gid * (D / 2) + tig * (D / 8), w0);
-            load_words(r1 + gid * (D / 2) + tig * (D / 8), w1);
-            const uint32_t at = fp4_codes(D) + gid * (D / 16) + tig * (D / 64);
-            uint32_t f0, f1;
-            if constexpr (D == 64) f0 = r0[at], f1 = r1[at];
-            else if constexpr (D == 128)
-                f0 = *reinterpret_cast<const uint16_t*>(r0 + at), f1 = *reinterpret_cast<const uint16_t*>(r1 + at);
-            else f0 = *reinterpret_cast<const uint32_t*>(r0 + at), f1 = *reinterpret_cast<const uint32_t*>(r1 + at);
+            lds_words(k_at + 2 * mt * L::kRec, w0);
+            lds_words(k_at + (2 * mt + 1) * L::kRec, w1);
+            uint32_t f[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t at = kf_at + (2 * mt + h) * L::kRec;
+                if constexpr (D == 64) f[h] = lds_u8(at);
+                else if constexpr (D == 128) f[h] = lds_u16(at);
+                else lds_words(at, *reinterpret_cast<uint32_t(*)[1]>(f + h));
+            }
             uint32_t s0 = 0, s1 = 0;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 if (i % 2 == 0) {   // the scale of the next 16 elements, in both halves
                     const uint32_t pick = (i / 2) * 0x11u;
-                    s0 = fp8_unpack(__byte_perm(f0, 0, pick));
-                    s1 = fp8_unpack(__byte_perm(f1, 0, pick));
+                    s0 = fp8_unpack(__byte_perm(f[0], 0, pick));
+                    s1 = fp8_unpack(__byte_perm(f[1], 0, pick));
                 }
                 uint32_t x0[4], x1[4];
                 fp4_unpack(w0[i], x0);
@@ -562,7 +557,7 @@ struct Worker {
                 if (edge) sees(a, s, n, c, &lo, &hi);
                 float t = -INFINITY;
 #pragma unroll
-                for (int mt = 0; mt < 4; ++mt)
+                for (int mt = 0; mt < L::kMt; ++mt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         float& x = y[mt][n][2 * h + c];
@@ -596,14 +591,14 @@ struct Worker {
                 }
         }
         // weights, transposed to the right operand of the second product
-        uint32_t w[4][NT][2];
+        uint32_t w[L::kMt][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float shift[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) shift[c] = kBias - (m[n][c] == -INFINITY ? 0.0f : m[n][c]);
 #pragma unroll
-            for (int mt = 0; mt < 4; ++mt)
+            for (int mt = 0; mt < L::kMt; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float p0 = ex2(y[mt][n][2 * h] + shift[0]), p1 = ex2(y[mt][n][2 * h + 1] + shift[1]);
@@ -614,22 +609,21 @@ struct Worker {
         }
         bool odd = false;
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
-            const uint8_t *r0 = vt + 2 * mt * L::kRec, *r1 = r0 + L::kRec;
+        for (int mt = 0; mt < L::kMt; ++mt) {
             constexpr int N = D / 64;
+            const uint32_t r0 = v_at + 2 * mt * L::kRec, r1 = r0 + L::kRec;
             uint32_t w00[N], w01[N], w10[N], w11[N];   // record, row 2 tig and 2 tig + 1
-            const uint32_t at = 2 * tig * (D / 2) + gid * (D / 16);
-            load_words(r0 + at, w00);
-            load_words(r0 + at + D / 2, w01);
-            load_words(r1 + at, w10);
-            load_words(r1 + at + D / 2, w11);
+            lds_words(r0, w00);
+            lds_words(r0 + D / 2, w01);
+            lds_words(r1, w10);
+            lds_words(r1 + D / 2, w11);
             // scales of both rows' groups: low byte row 2 tig, high byte row 2 tig + 1
             constexpr int kGroups = D == 256 ? 2 : 1;
             uint32_t f0[kGroups], f1[kGroups];
-            const uint32_t fat = fp4_codes(D) + 2 * tig * (D / 16) + gid * (D / 8) / kFp4Group;
+            const uint32_t g0 = vf_at + 2 * mt * L::kRec, g1 = g0 + L::kRec;
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
-                uint32_t b[4] = {r0[fat + k], r0[fat + k + D / 16], r1[fat + k], r1[fat + k + D / 16]};
+                uint32_t b[4] = {lds_u8(g0 + k), lds_u8(g0 + k + D / 16), lds_u8(g1 + k), lds_u8(g1 + k + D / 16)};
                 if (edge) {
                     // a scale that is no number counts for the rows that see its key only
 #pragma unroll
@@ -663,16 +657,16 @@ struct Worker {
 
     // Values that are no number, at the edge of what the rows see: the elements of
     // their group become NaN in the rows that see them, whatever their weight.
-    __device__ __forceinline__ void spread_nan(const Args& a, const Segment& s, const uint8_t* vt, int key0) {
+    __device__ __forceinline__ void spread_nan(const Args& a, const Segment& s, uint32_t vt, int key0) {
         constexpr int kGroups = D == 256 ? 2 : 1;
 #pragma unroll 1
-        for (int k = 0; k < kTileKeys; ++k) {
+        for (int k = 0; k < L::kKeys; ++k) {
             const int j = key0 + k;
             if (j < s.lo || j >= s.hi) continue;
-            const uint8_t* f = vt + k / kFp4Rows * L::kRec + fp4_codes(D) + k % kFp4Rows * (D / 16) + gid * (D / 8) / kFp4Group;
+            const uint32_t f = vt + k / kFp4Rows * L::kRec + fp4_codes(D) + k % kFp4Rows * (D / 16) + gid * (D / 8) / kFp4Group;
 #pragma unroll
             for (int x = 0; x < kGroups; ++x) {
-                if (!scale_is_nan(f[x])) continue;
+                if (!scale_is_nan(lds_u8(f + x))) continue;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -768,72 +762,83 @@ struct Worker {
     }
 };
 
-// Rendezvous of the warps that compute (waits of theirs are bounded, so all come).
-__device__ __forceinline__ void workers_sync() { asm volatile("barrier.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
-
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) fp4_attn_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1) fp4_attn_kernel(const __grid_constant__ Args a) {
     using L = Smem<D, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Ctx c{smem, smem_u32(smem), reinterpret_cast<volatile int*>(smem + L::abort), a.status, a.spin};
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < L::kStages; ++i) {
-            mbar_init(c.base + L::full + 8 * i, 1);
-            mbar_init(c.base + L::empty + 8 * i, 1);
-        }
-        *c.abort_flag = 0;
-        fence_mbar_init();
-    }
+    const uint32_t base = smem_u32(smem);
     grid_dep_wait();
     grid_dep_launch();
     int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
     int64_t units;
     if (a.local_plan) {
         units = plan_requests<kThreads>(a, L::kRows, pre, reinterpret_cast<int64_t*>(smem + L::sums));
+        __syncthreads();
     } else {
         pre = a.pre;
         units = __ldcg(a.pre + a.B);
     }
-    __syncthreads();   // (sums and barriers)
+    const Start* range = reinterpret_cast<const Start*>(smem + L::range);
     if (threadIdx.x < 2) {
         const Start s = make_start(a, pre, units, static_cast<int>(blockIdx.x) + threadIdx.x, L::kRows);
         reinterpret_cast<Start*>(smem + L::range)[threadIdx.x] = s;
         if (threadIdx.x == 0 || static_cast<int>(blockIdx.x) == a.grid - 1) a.starts[blockIdx.x + threadIdx.x] = s;
     }
     __syncthreads();
-    if (warp == kWarps) {
-        load_tiles<D, NT>(c, a, lane);
-        return;
+    volatile uint32_t* where = reinterpret_cast<volatile uint32_t*>(smem + L::where);
+    const uint32_t mine = base + L::ring + warp * (kStages * L::kStage);
+    Feed<D, NT> feed(a, range, warp);
+    if (feed.live) {
+        feed.look_up(a, lane);
+        feed.issue(a, mine, lane);
+        feed.next(a);
+        if (feed.live) feed.look_up(a, lane);
     }
+    cp_async_commit();
     Worker<D, NT> me;
     me.gid = lane >> 2;
     me.tig = lane & 3;
-    Walk walk(reinterpret_cast<const Start*>(smem + L::range));
+    Walk walk(range);
     Segment s;
-    int seq = 0;       // tiles of earlier segments
+    int k = warp;       // the warp's next tile in the segment
+    uint32_t stage = 0; // and its stage
     while (walk.next(a, L::kRows, s)) {
         me.load_q(a, s);
         me.reset();
-        for (int k = (warp - seq) & (kWarps - 1); k < s.n; k += kWarps) {
-            const int i = seq + k, turn = i / L::kStages, slot = i - turn * L::kStages;
-            const bool ok = __all_sync(0xffffffffu, c.wait(L::full + 8 * slot, turn));
-            if (ok) me.tile(a, s, smem + L::ring + slot * L::kStage, (s.first + k) * kTileKeys);
+        for (; k < s.n; k += kWarps) {
+            const uint32_t at = mine + stage * L::kStage;
+            stage ^= 1;
+            __syncwarp();   // (every lane has read the tile before)
+            if (feed.live) {
+                feed.issue(a, mine + stage * L::kStage, lane);
+                feed.next(a);
+                if (feed.live) feed.look_up(a, lane);
+            }
+            cp_async_commit();
+            cp_async_wait<1>();
             __syncwarp();
-            if (lane == 0) mbar_arrive(c.base + L::empty + 8 * slot);
+            me.tile(a, s, at, (s.first + k) * L::kKeys);
         }
-        seq += s.n;
-        // the warps' results, joined in pairs
-        float* join = reinterpret_cast<float*>(smem + L::join) + lane;
+        k -= s.n;
+        // the warps' results, joined in pairs; shares lie in the stages that are free
+        const uint32_t free_at = warp * (kStages * L::kStage) + (stage ^ 1) * L::kStage;
+        if (lane == 0) where[warp] = free_at;
 #pragma unroll 1
-        for (int half = kWarps / 2; half; half /= 2) {
-            if (warp >= half && warp < 2 * half) me.put(join + (warp - half) * L::kVals * 32);
-            workers_sync();
-            if (warp < half) me.add(join + warp * L::kVals * 32);
-            workers_sync();
+        for (int left = kWarps; left > 1;) {
+            const int half = (left + 1) / 2;
+            if (warp >= half && warp < left) {
+                __syncwarp();
+                me.put(reinterpret_cast<float*>(smem + free_at) + lane);
+            }
+            __syncthreads();
+            if (warp < left - half) me.add(reinterpret_cast<const float*>(smem + where[warp + half]) + lane);
+            left = half;
         }
+        __syncthreads();   // (the shares are read, and the stages free again)
         if (warp == 0) me.write(a, s);
     }
+    cp_async_wait<0>();
 }
 
 // ------------------------------------------------------------ join
@@ -1112,7 +1117,6 @@ Layout layout(const sp_fp4_shape* s, int grid) {
 template <int D, int NT>
 cudaError_t launch_rows(const Args& a, cudaStream_t st) {
     using L = Smem<D, NT>;
-    static_assert(L::total <= 232448 && L::kStages >= kWarps, "shared memory of one CTA");
     if (!a.local_plan) {
         const cudaError_t e = launch_k(fp4_plan_kernel, 1, kPlanThreads, 0, st, a, L::kRows);
         if (e != cudaSuccess) return e;
@@ -1156,7 +1160,6 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     a.k_sb = s->k_stride_block, a.k_sh = s->k_stride_head;
     a.v_sb = s->v_stride_block, a.v_sh = s->v_stride_head;
     a.pool_blocks = s->pool_blocks;
-    a.spin = p->spin_limit > 0 ? p->spin_limit : kDefaultSpin;
     a.B = s->n_seqs;
     a.hk = s->n_kv_heads;
     a.G = s->n_q_heads / s->n_kv_heads;
@@ -1166,7 +1169,8 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     a.max_new = s->max_new > 0 ? s->max_new : s->n_tokens;
     a.causal = p->causal;
     a.window = p->window <= kMaxCached ? p->window : 0;   // (a longer one hides nothing)
-    a.piece_shift = __builtin_ctz(a.bs < kTileKeys ? a.bs : kTileKeys);
+    a.tile_shift = __builtin_ctz(tile_keys(d));
+    a.piece_shift = a.bs < tile_keys(d) ? __builtin_ctz(a.bs) : a.tile_shift;
     a.local_plan = a.B <= kLocalSeqs;
     a.bf16 = s->dtype == SP_DTYPE_BF16;
     const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(d));
