@@ -60,12 +60,11 @@ constexpr int kMaxGrid = 256;
 constexpr float kSlack = 8.0f;               // log2 units the reference may lag behind the maximum
 constexpr float kBias = 6.0f;                // fp16 weights are scaled by 2^6: normal down to 2^-20 of the reference
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kJoinThreads = 128;
-
 // Where a CTA's range starts: key tile `off` of item `gj` (KV head, row tile) of
-// request b. b = n_seqs: the end of everything.
+// request b, an item that CTAs c0 .. c0 + parts - 1 work on. b = n_seqs: the end of
+// everything.
 struct alignas(16) Start {
-    int32_t b, gj, off, pad;
+    int32_t b, gj, off, c0, parts, pad[3];
 };
 
 struct Args {
@@ -87,6 +86,7 @@ struct Args {
     int B, hk, G, bs, table_stride, cap, max_new, causal, window, grid;
     int tile_shift;            // log2 of a tile's keys
     int piece_shift;           // log2 of a copy's tokens: a block's, at most a tile's
+    int bs_shift;              // log2(bs), or -1
     int local_plan, bf16;
     float scale2, v_scale;
 };
@@ -188,19 +188,27 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_plan_kernel(const Args a, in
     if (threadIdx.x == 0) a.pre[a.B] = units;
 }
 
+// The CTA whose range holds unit u of `units`.
+__device__ __forceinline__ int range_owner(int64_t units, int64_t ctas, int64_t u) {
+    return static_cast<int>(((u + 1) * ctas - 1) / units);
+}
+
 // The start of CTA c's range of `units`; a cut inside an item's fixed cost falls
 // on the item's start.
 __device__ __forceinline__ Start make_start(const Args& a, const int64_t* pre, int64_t units, int c, int rows) {
     const int64_t ctas = min(static_cast<int64_t>(a.grid), units);
-    Start s{a.B, 0, 0, 0};
+    Start s{a.B, 0, 0, 0, 1, {0, 0, 0}};
     if (c < ctas) {
-        int64_t u = units * c / ctas;
+        const int64_t u = units * c / ctas;
         s.b = last_at_most(pre, a.B, u);
-        u -= pre[s.b];
+        const int64_t in = u - pre[s.b];
         const Span sp = span_of(a, a.q_off[s.b + 1] - a.q_off[s.b], a.kv_len[s.b], rows);
         const int64_t per = sp.tiles + kItemCost;
-        s.gj = static_cast<int32_t>(u / per);
-        s.off = static_cast<int32_t>(max(u - s.gj * per - kItemCost, static_cast<int64_t>(0)));
+        s.gj = static_cast<int32_t>(in / per);
+        const int64_t item = pre[s.b] + s.gj * per;
+        s.off = static_cast<int32_t>(max(u - item - kItemCost, static_cast<int64_t>(0)));
+        s.c0 = range_owner(units, ctas, item + kItemCost);
+        s.parts = range_owner(units, ctas, item + per - 1) - s.c0 + 1;
     }
     return s;
 }
@@ -213,47 +221,51 @@ struct Segment {
     int b, g, q0, pos0, kv, row0, rows, first, n;
     int lo, hi;             // cache indices that some row sees
     int all_lo, all_hi;     // and that all rows see
-    bool split, head;       // other CTAs hold the rest; the CTA's first segment
+    int c0, parts;          // the CTAs that share the item; parts = 0: the whole item is here
 };
 
 // Walks a CTA's range; every warp takes the same steps.
 struct Walk {
-    Start at, end;
-    bool head;
-    __device__ __forceinline__ Walk(const Start* r) : at(r[0]), end(r[1]), head(true) {}
+    const Start* range;     // in shared memory
+    int at_b, at_gj, at_off;
+    __device__ __forceinline__ Walk(const Start* r) : range(r), at_b(r->b), at_gj(r->gj), at_off(r->off) {}
     __device__ __forceinline__ bool next(const Args& a, int tile_rows, Segment& s) {
+        const Start &begin = range[0], &end = range[1];
         for (;;) {
-            if (at.b > end.b || at.b >= a.B ||
-                (at.b == end.b && (at.gj > end.gj || (at.gj == end.gj && at.off >= end.off))))
+            if (at_b > end.b || at_b >= a.B ||
+                (at_b == end.b && (at_gj > end.gj || (at_gj == end.gj && at_off >= end.off))))
                 return false;
-            const int q0 = a.q_off[at.b], nq = a.q_off[at.b + 1] - q0, kv = a.kv_len[at.b];
+            const int q0 = a.q_off[at_b], nq = a.q_off[at_b + 1] - q0, kv = a.kv_len[at_b];
             const Span sp = span_of(a, nq, kv, tile_rows);
-            if (sp.row_tiles == 0 || (a.dense && a.dense[at.b] >= 0) || at.gj >= a.hk * sp.row_tiles) {
-                ++at.b;
-                at.gj = at.off = 0;
+            if (sp.row_tiles == 0 || (a.dense && a.dense[at_b] >= 0) || at_gj >= a.hk * sp.row_tiles) {
+                ++at_b;
+                at_gj = at_off = 0;
                 continue;
             }
-            s.b = at.b;
-            s.g = at.gj / sp.row_tiles;
+            s.b = at_b;
+            s.g = at_gj / sp.row_tiles;
             s.q0 = q0;
             s.kv = kv;
             s.pos0 = kv - nq;
-            s.row0 = (at.gj - s.g * sp.row_tiles) * tile_rows;
+            s.row0 = (at_gj - s.g * sp.row_tiles) * tile_rows;
             s.rows = min(tile_rows, nq * a.G - s.row0);
             const int i0 = s.row0 / a.G, i1 = (s.row0 + s.rows - 1) / a.G;
             s.hi = a.causal ? max(0, min(kv, s.pos0 + i1 + 1)) : kv;
             s.lo = a.window > 0 ? max(0, s.pos0 + i0 - a.window + 1) : 0;
             s.all_hi = a.causal ? min(kv, s.pos0 + i0 + 1) : kv;
             s.all_lo = a.window > 0 ? max(0, s.pos0 + i1 - a.window + 1) : 0;
-            const int last = at.b == end.b && at.gj == end.gj ? end.off : sp.tiles;
-            s.split = at.off > 0 || last < sp.tiles;
+            const int last = at_b == end.b && at_gj == end.gj ? end.off : sp.tiles;
+            s.parts = 0;
+            if (at_off > 0 || last < sp.tiles) {   // (cut: the CTA's first item, or its last)
+                const Start& x = at_off > 0 ? begin : end;
+                s.c0 = x.c0;
+                s.parts = x.parts;
+            }
             // (the first row tiles of a chunk see less than its last)
-            s.first = max(sp.tile0 + at.off, s.lo >> a.tile_shift);
+            s.first = max(sp.tile0 + at_off, s.lo >> a.tile_shift);
             s.n = s.hi > s.lo ? max(0, min(sp.tile0 + last, tiles_below(a, s.hi)) - s.first) : 0;
-            s.head = head;
-            head = false;
-            at.off = 0;
-            ++at.gj;
+            at_off = 0;
+            ++at_gj;
             return true;
         }
     }
@@ -261,26 +273,31 @@ struct Walk {
 
 // ------------------------------------------------------------ shared memory
 
-// Warps of a CTA: 12 of 168 registers.
-constexpr int kWarps = 12;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 2;      // tiles of a warp in shared memory: one in work, the next on its way
+// Warps of a CTA: 16 of 128 registers, or 12 of 168.
+constexpr int warps_of(int d, int nt) { return 12; }
 
 template <int D, int NT>
 struct Smem {
+    static constexpr int kWarps = warps_of(D, NT);
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kRows = 8 * NT;
     static constexpr uint32_t kRec = fp4_record(D);
     static constexpr int kKeys = tile_keys(D);
     static constexpr int kMt = kKeys / 16;                       // products over a tile's keys
     static constexpr uint32_t kHalf = kKeys / kFp4Rows * kRec;   // K or V of a tile
+    // halves of a warp in shared memory: one in work, two on their way
+    static constexpr int kHalves = 3;
     static constexpr int kAcc = D / 16 * NT * 4;          // accumulator registers of a lane
     static constexpr int kVals = kAcc + NT * 4;           // and references and sums
-    // (a share for the join lies in the stage that its warp has just used)
-    static constexpr uint32_t kStage = 2 * kHalf > 128 * kVals ? 2 * kHalf : 128 * kVals;
-    static constexpr uint32_t ring = 0;                   // [kWarps][kStages] stages
-    static constexpr uint32_t range = kWarps * kStages * kStage;   // [2] Start
-    static constexpr uint32_t where = range + 2 * 16;     // [kWarps] where a warp left its share for the join
-    static constexpr uint32_t total = where + 4 * kWarps;
+    static constexpr uint32_t kShare = kVals * 32 * 4;    // a warp's share for the join at an item's end
+    // (in the half that its warp has just used, if it fits)
+    static constexpr bool kShareInRing = kShare <= kHalf;
+    static constexpr uint32_t ring = 0;                   // [kWarps][kHalves]
+    static constexpr uint32_t shares = kWarps * kHalves * kHalf;
+    static constexpr uint32_t range = shares + (kShareInRing ? 0 : kWarps / 2 * kShare);   // [2] Start
+    static constexpr uint32_t where = range + 2 * sizeof(Start);   // [kWarps] a warp's share
+    static constexpr uint32_t seg = (where + 4 * kWarps + 15) / 16 * 16;   // [kWarps][2] Segment in work, on its way
+    static constexpr uint32_t total = seg + 2 * kWarps * sizeof(Segment);
     // the plan, before the first tile
     static constexpr uint32_t sums = 0;
     static constexpr uint32_t pre = 32 * 8;
@@ -302,61 +319,80 @@ __device__ __forceinline__ void cp_async_wait() {
 }
 
 // The tiles of one warp, every kWarps-th of the CTA's, on their way into its
-// stages. A tile is cut into pieces (runs of tokens of one block); lane p looks
+// halves. A tile is cut into pieces (runs of tokens of one block); lane p looks
 // piece p up. Pieces outside the item's keys are not loaded (their blocks may be
 // gone).
 template <int D, int NT>
 struct Feed {
     using L = Smem<D, NT>;
     Walk w;
-    Segment s;
-    int k, id, row;   // the warp's next tile in the segment; this lane's block (-1: none) and row in it
+    Segment* s;       // in shared memory
+    int k, n;         // the warp's next tile in the segment; its tiles
+    int id, row;      // this lane's block (-1: none) and row in it
     bool live;
 
-    __device__ __forceinline__ Feed(const Args& a, const Start* range, int warp) : w(range), k(warp), id(-1), row(0), live(true) {
-        s.n = 0;
-        settle(a);
+    __device__ __forceinline__ Feed(const Args& a, const Start* range, Segment* seg, int warp, int lane)
+        : w(range), s(seg), k(warp), n(0), id(-1), row(0), live(true) {
+        settle(a, lane);
     }
-    __device__ __forceinline__ void settle(const Args& a) {
-        while (live && k >= s.n) {
-            k -= s.n;
-            live = w.next(a, L::kRows, s);
+    __device__ __forceinline__ void settle(const Args& a, int lane) {
+        while (live && k >= n) {
+            k -= n;
+            Segment t;
+            live = w.next(a, L::kRows, t);
+            if (!live) break;
+            __syncwarp();
+            if (lane == 0) *s = t;
+            __syncwarp();
+            n = t.n;
         }
+        if (live) look_up(a, lane);
     }
-    __device__ __forceinline__ void next(const Args& a) {
-        k += kWarps;
-        settle(a);
+    __device__ __forceinline__ void next(const Args& a, int lane) {
+        k += L::kWarps;
+        settle(a, lane);
     }
     __device__ __forceinline__ void look_up(const Args& a, int lane) {
-        const int key = (s.first + k) * L::kKeys + (lane << a.piece_shift);
+        const int key = (s->first + k) * L::kKeys + (lane << a.piece_shift);
         id = -1;
-        if (lane < L::kKeys >> a.piece_shift && key < s.hi && key + (1 << a.piece_shift) > s.lo) {
-            const int blk = key / a.bs;
+        if (lane < L::kKeys >> a.piece_shift && key < s->hi && key + (1 << a.piece_shift) > s->lo) {
+            const int blk = a.bs_shift >= 0 ? key >> a.bs_shift : key / a.bs;
             row = key - blk * a.bs;
-            id = __ldg(a.table + static_cast<int64_t>(s.b) * a.table_stride + blk);
+            id = __ldg(a.table + static_cast<int64_t>(s->b) * a.table_stride + blk);
             if (id < 0 || id >= a.pool_blocks) {
                 atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
                 id = 0;
             }
         }
     }
+    // Keys or values of the tile to `dst`, as a group of copies.
+    template <bool kValues>
     __device__ __forceinline__ void issue(const Args& a, uint32_t dst, int lane) const {
-        const int pieces = L::kKeys >> a.piece_shift;
-        const uint32_t bytes = (L::kRec / kFp4Rows) << a.piece_shift;
-        dst += 16 * lane;
-        for (int p = 0; p < pieces; ++p, dst += bytes) {
-            const int blk = __shfl_sync(0xffffffffu, id, p);
-            if (blk < 0) continue;
-            const int64_t rec = static_cast<int64_t>(__shfl_sync(0xffffffffu, row, p) / kFp4Rows) * L::kRec + 16 * lane;
-            const uint8_t* k_src = a.k + blk * a.k_sb + s.g * a.k_sh + rec;
-            const uint8_t* v_src = a.v + blk * a.v_sb + s.g * a.v_sh + rec;
+        if (live) {
+            const int pieces = L::kKeys >> a.piece_shift;
+            const uint32_t bytes = (L::kRec / kFp4Rows) << a.piece_shift;
+            const uint8_t* pool = (kValues ? a.v + s->g * a.v_sh : a.k + s->g * a.k_sh) + 16 * lane;
+            dst += 16 * lane;
+            if (pieces == 1) {   // (one run of tokens, copied whole)
+                const int blk = __shfl_sync(0xffffffffu, id, 0), r = __shfl_sync(0xffffffffu, row, 0);
+                if (blk >= 0) {
+                    const uint8_t* src = pool + blk * (kValues ? a.v_sb : a.k_sb) + r * static_cast<int64_t>(L::kRec / kFp4Rows);
 #pragma unroll
-            for (uint32_t o = 0; o < L::kHalf; o += 512) {
-                if (o + 16 * lane >= bytes) break;
-                copy16(dst + o, k_src + o);
-                copy16(dst + L::kHalf + o, v_src + o);
+                    for (uint32_t o = 0; o < L::kHalf; o += 512)
+                        if (o + 512 <= L::kHalf || o + 16 * lane < L::kHalf) copy16(dst + o, src + o);
+                }
+            } else for (int p = 0; p < pieces; ++p, dst += bytes) {
+                const int blk = __shfl_sync(0xffffffffu, id, p), r = __shfl_sync(0xffffffffu, row, p);
+                if (blk < 0) continue;
+                const uint8_t* src = pool + blk * (kValues ? a.v_sb : a.k_sb) + r * static_cast<int64_t>(L::kRec / kFp4Rows);
+#pragma unroll
+                for (uint32_t o = 0; o < L::kHalf; o += 512) {
+                    if (o + 16 * lane >= bytes) break;
+                    copy16(dst + o, src + o);
+                }
             }
         }
+        cp_async_commit();
     }
 };
 
@@ -366,6 +402,13 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// The same from zero.
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // Transpose of an 8 x 8 matrix of 16-bit values held two in each lane.
@@ -416,6 +459,10 @@ __device__ __forceinline__ void lds_words(uint32_t at, uint32_t (&w)[N]) {
     }
 }
 
+// The place of CTA c's part of an item that is cut first in CTA c0's range: c0's
+// second one (its first may be the end of an earlier item), the others' first.
+__device__ __forceinline__ int64_t part_of(int c0, int c) { return 2 * static_cast<int64_t>(c) + (c == c0); }
+
 // ------------------------------------------------------------ one warp's share
 
 // Lane (gid, tig) = (lane / 4, lane % 4). It holds
@@ -428,6 +475,7 @@ struct Worker {
     using L = Smem<D, NT>;
     static constexpr int kM = D / 16;
     uint32_t q[D / 16][NT][2];
+    uint32_t w[L::kMt][NT][2];     // the tile's weights
     float acc[kM][NT][4];
     float m[NT][2], l[NT][2];      // reference (log2 units), sum of this lane's keys
     float sc[NT][2];               // scale of a row's logits, log2 units
@@ -500,21 +548,31 @@ struct Worker {
         *lo = a.window > 0 ? pos - a.window + 1 : 0;
     }
 
-    // A tile whose copies have landed, its first key at cache index key0.
-    __device__ __forceinline__ void tile(const Args& a, const Segment& s, uint32_t kt, int key0) {
-        const uint32_t vt = kt + L::kHalf;
+    // Minus infinity where a row does not see a key. (A branch of its own: as selects in
+    // the loops above and below it took a tenth of the tile's instructions.)
+    __device__ __forceinline__ void mask(const Args& a, const Segment& s, float (&y)[L::kMt][NT][4], int key0) const {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                int lo, hi;
+                sees(a, s, n, c, &lo, &hi);
+                lo -= key0 + gid;
+                hi -= key0 + gid;
+#pragma unroll
+                for (int i = 0; i < 2 * L::kMt; ++i)
+                    if (8 * i < lo || 8 * i >= hi) y[i / 2][n][i % 2 * 2 + c] = -INFINITY;
+            }
+    }
+
+    // A tile's keys, the first at cache index key0, to the weights of its values;
+    // `edge`: not every row sees every key.
+    __device__ __forceinline__ void keys(const Args& a, const Segment& s, uint32_t kt, int key0, bool edge) {
         const uint32_t k_at = kt + gid * (D / 2) + tig * (D / 8);
         const uint32_t kf_at = kt + fp4_codes(D) + gid * (D / 16) + tig * (D / 64);
-        const uint32_t v_at = vt + 2 * tig * (D / 2) + gid * (D / 16);
-        const uint32_t vf_at = vt + fp4_codes(D) + 2 * tig * (D / 16) + gid * (D / 8) / kFp4Group;
-        const bool edge = key0 < s.all_lo || key0 + L::kKeys > s.all_hi;
         float y[L::kMt][NT][4];
 #pragma unroll
         for (int mt = 0; mt < L::kMt; ++mt) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) y[mt][n][c] = 0.0f;
             uint32_t w0[D / 32], w1[D / 32];
             lds_words(k_at + 2 * mt * L::kRec, w0);
             lds_words(k_at + (2 * mt + 1) * L::kRec, w1);
@@ -542,32 +600,30 @@ struct Worker {
                     const uint32_t op[4] = {mul_f16x2(x0[2 * u], s0), mul_f16x2(x1[2 * u], s1),
                                             mul_f16x2(x0[2 * u + 1], s0), mul_f16x2(x1[2 * u + 1], s1)};
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16(y[mt][n], op, q[2 * i + u][n][0], q[2 * i + u][n][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        if (i == 0 && u == 0) mma_f16_first(y[mt][n], op, q[0][n][0], q[0][n][1]);
+                        else mma_f16(y[mt][n], op, q[2 * i + u][n][0], q[2 * i + u][n][1]);
+                    }
                 }
             }
         }
         // logits in log2 units, masked at the edges of what the rows see
+#pragma unroll
+        for (int mt = 0; mt < L::kMt; ++mt)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) y[mt][n][c] *= sc[n][c & 1];
+        if (edge) mask(a, s, y, key0);
         float top[NT][2];
         bool above = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                int lo = 0, hi = INT32_MAX;
-                if (edge) sees(a, s, n, c, &lo, &hi);
-                float t = -INFINITY;
+                float t = y[0][n][c];
 #pragma unroll
-                for (int mt = 0; mt < L::kMt; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float& x = y[mt][n][2 * h + c];
-                        x *= sc[n][c];
-                        if (edge) {
-                            const int j = key0 + 16 * mt + 8 * h + gid;
-                            if (j < lo || j >= hi) x = -INFINITY;
-                        }
-                        t = fmaxf(t, x);
-                    }
+                for (int i = 1; i < 2 * L::kMt; ++i) t = fmaxf(t, y[i / 2][n][i % 2 * 2 + c]);
                 top[n][c] = t;
                 // (a first value is above a reference of minus infinity)
                 above |= t > m[n][c] + kSlack;
@@ -591,7 +647,6 @@ struct Worker {
                 }
         }
         // weights, transposed to the right operand of the second product
-        uint32_t w[L::kMt][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float shift[2];
@@ -607,7 +662,13 @@ struct Worker {
                     w[mt][n][h] = transpose8(half2_of(p0, p1));
                 }
         }
-        bool odd = false;
+    }
+
+    // The tile's values, times its weights.
+    __device__ __forceinline__ void values(const Args& a, const Segment& s, uint32_t vt, int key0, bool edge) {
+        const uint32_t v_at = vt + 2 * tig * (D / 2) + gid * (D / 16);
+        const uint32_t vf_at = vt + fp4_codes(D) + 2 * tig * (D / 16) + gid * (D / 8) / kFp4Group;
+        if (edge) take_nan(a, s, vt, key0);
 #pragma unroll
         for (int mt = 0; mt < L::kMt; ++mt) {
             constexpr int N = D / 64;
@@ -623,15 +684,8 @@ struct Worker {
             const uint32_t g0 = vf_at + 2 * mt * L::kRec, g1 = g0 + L::kRec;
 #pragma unroll
             for (int k = 0; k < kGroups; ++k) {
-                uint32_t b[4] = {lds_u8(g0 + k), lds_u8(g0 + k + D / 16), lds_u8(g1 + k), lds_u8(g1 + k + D / 16)};
-                if (edge) {
-                    // a scale that is no number counts for the rows that see its key only
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (scale_is_nan(b[u])) b[u] = 0, odd = true;
-                }
-                f0[k] = fp8_unpack(b[0] | b[1] << 8);
-                f1[k] = fp8_unpack(b[2] | b[3] << 8);
+                f0[k] = fp8_unpack(lds_u8(g0 + k) | lds_u8(g0 + k + D / 16) << 8);
+                f1[k] = fp8_unpack(lds_u8(g1 + k) | lds_u8(g1 + k + D / 16) << 8);
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
@@ -652,11 +706,30 @@ struct Worker {
                 }
             }
         }
-        if (edge && __any_sync(0xffffffffu, odd)) spread_nan(a, s, vt, key0);
     }
 
-    // Values that are no number, at the edge of what the rows see: the elements of
-    // their group become NaN in the rows that see them, whatever their weight.
+    // Value scales that are no number, at the edge of what the rows see: a weight of
+    // zero does not take such a value away. The elements of its group become NaN in
+    // the rows that see it, whatever their weight, and the scale zero.
+    __device__ __forceinline__ void take_nan(const Args& a, const Segment& s, uint32_t vt, int key0) {
+        const int lane = 4 * gid + tig;
+        constexpr int kWords = L::kKeys * (D / 16) / 4, kPerRec = D / 8;   // words of scales of a tile, of a record
+        bool odd = false;
+        for (int i = lane; i < kWords; i += 32) {
+            uint32_t w[1];
+            lds_words(vt + i / kPerRec * L::kRec + fp4_codes(D) + i % kPerRec * 4, w);
+            odd |= scale_is_nan(w[0]) || scale_is_nan(w[0] >> 8) || scale_is_nan(w[0] >> 16) || scale_is_nan(w[0] >> 24);
+        }
+        if (!__any_sync(0xffffffffu, odd)) return;
+        spread_nan(a, s, vt, key0);
+        __syncwarp();
+        for (int i = lane; i < 4 * kWords; i += 32) {
+            const uint32_t at = vt + i / (4 * kPerRec) * L::kRec + fp4_codes(D) + i % (4 * kPerRec);
+            if (scale_is_nan(lds_u8(at))) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(0) : "memory");
+        }
+        __syncwarp();
+    }
+
     __device__ __forceinline__ void spread_nan(const Args& a, const Segment& s, uint32_t vt, int key0) {
         constexpr int kGroups = D == 256 ? 2 : 1;
 #pragma unroll 1
@@ -728,8 +801,8 @@ struct Worker {
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
                 const int row = 8 * n + 2 * tig + c;
                 if (row >= s.rows) continue;
-                if (s.split) {
-                    const int64_t part = (2 * static_cast<int64_t>(blockIdx.x) + (s.head ? 0 : 1)) * L::kRows + row;
+                if (s.parts) {
+                    const int64_t part = part_of(s.c0, blockIdx.x) * L::kRows + row;
                     float* o = a.part_o + part * D + gid * (D / 8);
 #pragma unroll
                     for (int i = 0; i < kM; i += 2)
@@ -763,8 +836,9 @@ struct Worker {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, 1) fp4_attn_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(const __grid_constant__ Args a) {
     using L = Smem<D, NT>;
+    constexpr int kWarps = L::kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
@@ -773,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attn_kernel(const __grid_cons
     int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
     int64_t units;
     if (a.local_plan) {
-        units = plan_requests<kThreads>(a, L::kRows, pre, reinterpret_cast<int64_t*>(smem + L::sums));
+        units = plan_requests<L::kThreads>(a, L::kRows, pre, reinterpret_cast<int64_t*>(smem + L::sums));
         __syncthreads();
     } else {
         pre = a.pre;
@@ -787,55 +861,68 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attn_kernel(const __grid_cons
     }
     __syncthreads();
     volatile uint32_t* where = reinterpret_cast<volatile uint32_t*>(smem + L::where);
-    const uint32_t mine = base + L::ring + warp * (kStages * L::kStage);
-    Feed<D, NT> feed(a, range, warp);
-    if (feed.live) {
-        feed.look_up(a, lane);
-        feed.issue(a, mine, lane);
-        feed.next(a);
-        if (feed.live) feed.look_up(a, lane);
-    }
-    cp_async_commit();
+    // (what only the edges and ends of an item need stays out of the registers)
+    Segment* seg = reinterpret_cast<Segment*>(smem + L::seg) + 2 * warp;
+    const uint32_t mine = base + L::ring + warp * (L::kHalves * L::kHalf);
+    Feed<D, NT> feed(a, range, seg + 1, warp, lane);
+    feed.template issue<false>(a, mine, lane);
+    feed.template issue<true>(a, mine + L::kHalf, lane);
+    if (feed.live) feed.next(a, lane);
     Worker<D, NT> me;
     me.gid = lane >> 2;
     me.tig = lane & 3;
     Walk walk(range);
-    Segment s;
+    Segment& s = *seg;
     int k = warp;       // the warp's next tile in the segment
-    uint32_t stage = 0; // and its stage
-    while (walk.next(a, L::kRows, s)) {
+    uint32_t half = 0;  // and the half that it begins in
+    for (;;) {
+        Segment t;
+        if (!walk.next(a, L::kRows, t)) break;
+        __syncwarp();
+        if (lane == 0) s = t;
+        __syncwarp();
         me.load_q(a, s);
         me.reset();
-        for (; k < s.n; k += kWarps) {
-            const uint32_t at = mine + stage * L::kStage;
-            stage ^= 1;
+        const int n = t.n, first = t.first, all_lo = t.all_lo, all_hi = t.all_hi;
+        for (; k < n; k += kWarps) {
+            const int key0 = (first + k) * L::kKeys;
+            const bool edge = key0 < all_lo || key0 + L::kKeys > all_hi;
+            // halves in turn: this tile's keys, its values, the next tile's keys (copied
+            // over the values of the tile before)
+            const uint32_t k_at = mine + half * L::kHalf;
+            half = half == 2 ? 0 : half + 1;
+            const uint32_t v_at = mine + half * L::kHalf;
+            half = half == 2 ? 0 : half + 1;
             __syncwarp();   // (every lane has read the tile before)
-            if (feed.live) {
-                feed.issue(a, mine + stage * L::kStage, lane);
-                feed.next(a);
-                if (feed.live) feed.look_up(a, lane);
-            }
-            cp_async_commit();
-            cp_async_wait<1>();
+            feed.template issue<false>(a, mine + half * L::kHalf, lane);
+            cp_async_wait<2>();
             __syncwarp();
-            me.tile(a, s, at, (s.first + k) * L::kKeys);
+            me.keys(a, s, k_at, key0, edge);
+            __syncwarp();
+            feed.template issue<true>(a, k_at, lane);
+            if (feed.live) feed.next(a, lane);
+            cp_async_wait<2>();
+            __syncwarp();
+            me.values(a, s, v_at, key0, edge);
         }
-        k -= s.n;
-        // the warps' results, joined in pairs; shares lie in the stages that are free
-        const uint32_t free_at = warp * (kStages * L::kStage) + (stage ^ 1) * L::kStage;
-        if (lane == 0) where[warp] = free_at;
+        k -= n;
+        // the warps' results, joined in pairs
+        uint32_t share = L::ring + warp * (L::kHalves * L::kHalf) + (half == 0 ? 2 : half - 1) * L::kHalf;
+        if constexpr (!L::kShareInRing) share = L::shares + (warp % (kWarps / 2)) * L::kShare;
+        if (lane == 0) where[warp] = share;
 #pragma unroll 1
         for (int left = kWarps; left > 1;) {
-            const int half = (left + 1) / 2;
-            if (warp >= half && warp < left) {
+            const int upper = (left + 1) / 2;
+            if (warp >= upper && warp < left) {
                 __syncwarp();
-                me.put(reinterpret_cast<float*>(smem + free_at) + lane);
+                me.put(reinterpret_cast<float*>(smem + share) + lane);
             }
             __syncthreads();
-            if (warp < left - half) me.add(reinterpret_cast<const float*>(smem + where[warp + half]) + lane);
-            left = half;
+            if (warp < left - upper) me.add(reinterpret_cast<const float*>(smem + where[warp + upper]) + lane);
+            left = upper;
+            if constexpr (!L::kShareInRing) __syncthreads();   // (the next round's shares take the place of these)
         }
-        __syncthreads();   // (the shares are read, and the stages free again)
+        __syncthreads();   // (the shares are read)
         if (warp == 0) me.write(a, s);
     }
     cp_async_wait<0>();
@@ -843,41 +930,26 @@ __global__ void __launch_bounds__(kThreads, 1) fp4_attn_kernel(const __grid_cons
 
 // ------------------------------------------------------------ join
 
-// Parts of the items that were cut between CTAs. Block (x, r) joins row r of the
-// item that is cut first between CTAs x and x + 1, if one is.
+constexpr int kJoinThreads = 128;
+
+// Parts of the items that were cut between CTAs, in the order of the CTAs. Block
+// (c, r) joins row r of the item that is cut first at the end of CTA c's range, if
+// one is.
 template <int D, int NT>
-__global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const Args a) {
+__global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const __grid_constant__ Args a) {
     constexpr int kRows = 8 * NT, kCols = D / 32, kJoinWarps = kJoinThreads / 32;
     __shared__ float acc_s[kJoinWarps][D], sum_s[kJoinWarps];
     grid_dep_wait();
     grid_dep_launch();
-    const int x = blockIdx.x + 1, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    auto start = [&](int c) {
-        const int4 v = __ldcg(reinterpret_cast<const int4*>(a.starts + c));
-        return Start{v.x, v.y, v.z, v.w};
-    };
-    const Start s = start(x), before = start(x - 1);
-    const bool same = before.b == s.b && before.gj == s.gj;
-    if (s.b >= a.B || s.off == 0 || (same && before.off > 0)) return;
-    const int q0 = a.q_off[s.b], nq = a.q_off[s.b + 1] - q0;
+    const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Start* next = a.starts + c + 1;
+    if (__ldcg(&next->off) == 0 || __ldcg(&next->c0) != c) return;
+    const int b = __ldcg(&next->b), gj = __ldcg(&next->gj), parts = __ldcg(&next->parts);
+    const int q0 = a.q_off[b], nq = a.q_off[b + 1] - q0;
     const int row_tiles = static_cast<int>((static_cast<int64_t>(nq) * a.G + kRows - 1) / kRows);
-    const int g = s.gj / row_tiles, r = (s.gj - g * row_tiles) * kRows + row;
+    const int g = gj / row_tiles, r = (gj - g * row_tiles) * kRows + row;
     if (r >= nq * a.G) return;
-    // CTAs x .. x + parts - 2 begin inside the item
-    int parts = 2;
-    for (int c0 = x + 1; c0 < a.grid; c0 += 32) {
-        bool more = false;
-        if (c0 + lane < a.grid) {
-            const Start o = start(c0 + lane);
-            more = o.b == s.b && o.gj == s.gj;
-        }
-        const unsigned who = __ballot_sync(0xffffffffu, more);
-        parts += who == 0xffffffffu ? 32 : __ffs(~who) - 1;
-        if (who != 0xffffffffu) break;
-    }
-    auto at = [&](int p) {
-        return (2 * static_cast<int64_t>(x - 1 + p) + (p == 0 && !same ? 1 : 0)) * kRows + row;
-    };
+    auto at = [&](int p) { return part_of(c, c + p) * kRows + row; };
     float top = -INFINITY;
     for (int p = lane; p < parts; p += 32) top = fmaxf(top, __ldcg(a.part_ml + at(p)).x);
 #pragma unroll
@@ -911,8 +983,8 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const Args a) {
         lo *= inv, hi *= inv;
         uint32_t w;
         if (a.bf16) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-            w = *reinterpret_cast<const uint32_t*>(&b);
+            const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+            w = *reinterpret_cast<const uint32_t*>(&x);
         } else {
             w = half2_of(lo, hi);
         }
@@ -1124,7 +1196,7 @@ cudaError_t launch_rows(const Args& a, cudaStream_t st) {
     auto kern = fp4_attn_kernel<D, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::total));
     if (e != cudaSuccess) return e;
-    e = launch_k(kern, static_cast<unsigned>(a.grid), kThreads, L::total, st, a);
+    e = launch_k(kern, static_cast<unsigned>(a.grid), L::kThreads, L::total, st, a);
     if (e != cudaSuccess || a.grid < 2) return e;
     return launch_k(fp4_join_kernel<D, NT>, dim3(a.grid - 1, L::kRows), kJoinThreads, 0, st, a);
 }
@@ -1169,6 +1241,7 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     a.max_new = s->max_new > 0 ? s->max_new : s->n_tokens;
     a.causal = p->causal;
     a.window = p->window <= kMaxCached ? p->window : 0;   // (a longer one hides nothing)
+    a.bs_shift = (a.bs & (a.bs - 1)) == 0 ? __builtin_ctz(a.bs) : -1;
     a.tile_shift = __builtin_ctz(tile_keys(d));
     a.piece_shift = a.bs < tile_keys(d) ? __builtin_ctz(a.bs) : a.tile_shift;
     a.local_plan = a.B <= kLocalSeqs;
