@@ -82,7 +82,7 @@ struct Args {
     Start* starts;             // [grid + 1]
     float* part_o;             // [2 grid][rows][d]
     float2* part_ml;           // [2 grid][rows] (reference, sum)
-    int64_t q_st, q_sh, o_st, o_sh, k_sb, k_sh, v_sb, v_sh, pool_blocks;
+    int64_t q_st, q_sh, o_st, o_sh, k_sb, k_sh, v_sb, v_sh, pool_blocks, spin;
     int B, hk, G, bs, table_stride, cap, max_new, causal, window, grid;
     int tile_shift;            // log2 of a tile's keys
     int piece_shift;           // log2 of a copy's tokens: a block's, at most a tile's
@@ -188,29 +188,54 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_plan_kernel(const Args a, in
     if (threadIdx.x == 0) a.pre[a.B] = units;
 }
 
-// The CTA whose range holds unit u of `units`.
-__device__ __forceinline__ int range_owner(int64_t units, int64_t ctas, int64_t u) {
-    return static_cast<int>(((u + 1) * ctas - 1) / units);
+// x / y for x >= 0, y > 0: in 32 bits where both fit.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    return x / y;
 }
 
-// The start of CTA c's range of `units`; a cut inside an item's fixed cost falls
-// on the item's start.
-__device__ __forceinline__ Start make_start(const Args& a, const int64_t* pre, int64_t units, int c, int rows) {
-    const int64_t ctas = min(static_cast<int64_t>(a.grid), units);
-    Start s{a.B, 0, 0, 0, 1, {0, 0, 0}};
-    if (c < ctas) {
-        const int64_t u = units * c / ctas;
-        s.b = last_at_most(pre, a.B, u);
-        const int64_t in = u - pre[s.b];
-        const Span sp = span_of(a, a.q_off[s.b + 1] - a.q_off[s.b], a.kv_len[s.b], rows);
-        const int64_t per = sp.tiles + kItemCost;
-        s.gj = static_cast<int32_t>(in / per);
-        const int64_t item = pre[s.b] + s.gj * per;
-        s.off = static_cast<int32_t>(max(u - item - kItemCost, static_cast<int64_t>(0)));
-        s.c0 = range_owner(units, ctas, item + kItemCost);
-        s.parts = range_owner(units, ctas, item + per - 1) - s.c0 + 1;
-    }
+// The CTA whose range holds unit u of `units`.
+__device__ __forceinline__ int range_owner(int64_t units, int64_t ctas, int64_t u) {
+    return static_cast<int>(quotient((u + 1) * ctas - 1, units));
+}
+
+// Unit u of `units`, of request b whose units begin at `at`, as a start; a cut inside
+// an item's fixed cost falls on the item's start.
+__device__ __forceinline__ Start make_start(const Args& a, int b, int64_t at, int64_t units, int64_t ctas, int64_t u, int rows) {
+    Start s{b, 0, 0, 0, 1, {0, 0, 0}};
+    const Span sp = span_of(a, a.q_off[b + 1] - a.q_off[b], a.kv_len[b], rows);
+    const int64_t per = sp.tiles + kItemCost;
+    s.gj = static_cast<int32_t>(quotient(u - at, per));
+    const int64_t item = at + s.gj * per;
+    s.off = static_cast<int32_t>(max(u - item - kItemCost, static_cast<int64_t>(0)));
+    s.c0 = range_owner(units, ctas, item + kItemCost);
+    s.parts = range_owner(units, ctas, item + per - 1) - s.c0 + 1;
     return s;
+}
+
+// The starts of this CTA's range and of the next one's, to `range`. Every thread
+// looks whether one of them falls into a request of its own.
+__device__ __forceinline__ void find_range(const Args& a, const int64_t* pre, int64_t units, int rows, Start* range) {
+    const int64_t ctas = min(static_cast<int64_t>(a.grid), units);
+    const int c = blockIdx.x, t = threadIdx.x;
+    auto tell = [&](int i, const Start& s) {
+        range[i] = s;
+        if (i == 0 || c == a.grid - 1) a.starts[c + i] = s;
+    };
+    if (t < 2 && c + t >= ctas) tell(t, Start{a.B, 0, 0, 0, 1, {0, 0, 0}});
+    if (c >= ctas) return;
+    const int64_t u[2] = {quotient(units * c, ctas), quotient(units * (c + 1), ctas)};
+    if (a.local_plan) {
+        for (int b = t; b < a.B; b += blockDim.x) {
+            const int64_t at = pre[b], end = b + 1 < a.B ? pre[b + 1] : units;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i)
+                if (u[i] >= at && u[i] < end) tell(i, make_start(a, b, at, units, ctas, u[i], rows));
+        }
+    } else if (t < 2 && c + t < ctas) {
+        const int b = last_at_most(pre, a.B, u[t]);
+        tell(t, make_start(a, b, pre[b], units, ctas, u[t], rows));
+    }
 }
 
 // ------------------------------------------------------------ segments
@@ -273,8 +298,8 @@ struct Walk {
 
 // ------------------------------------------------------------ shared memory
 
-// Warps of a CTA: 16 of 128 registers, or 12 of 168.
-constexpr int warps_of(int d, int nt) { return 12; }
+// Warps of a CTA: as many as their registers and shares of shared memory allow.
+constexpr int warps_of(int d, int nt) { return d == 64 ? 16 : d * nt <= 128 ? 12 : 8; }
 
 template <int D, int NT>
 struct Smem {
@@ -290,14 +315,12 @@ struct Smem {
     static constexpr int kAcc = D / 16 * NT * 4;          // accumulator registers of a lane
     static constexpr int kVals = kAcc + NT * 4;           // and references and sums
     static constexpr uint32_t kShare = kVals * 32 * 4;    // a warp's share for the join at an item's end
-    // (in the half that its warp has just used, if it fits)
-    static constexpr bool kShareInRing = kShare <= kHalf;
     static constexpr uint32_t ring = 0;                   // [kWarps][kHalves]
-    static constexpr uint32_t shares = kWarps * kHalves * kHalf;
-    static constexpr uint32_t range = shares + (kShareInRing ? 0 : kWarps / 2 * kShare);   // [2] Start
-    static constexpr uint32_t where = range + 2 * sizeof(Start);   // [kWarps] a warp's share
-    static constexpr uint32_t seg = (where + 4 * kWarps + 15) / 16 * 16;   // [kWarps][2] Segment in work, on its way
-    static constexpr uint32_t total = seg + 2 * kWarps * sizeof(Segment);
+    static constexpr uint32_t shares = kWarps * kHalves * kHalf;   // [kWarps]
+    static constexpr uint32_t range = shares + kWarps * kShare;    // [2] Start
+    static constexpr uint32_t bars = range + 2 * sizeof(Start);    // shares written, shares read
+    static constexpr uint32_t seg = bars + 16;                     // [kWarps][3] Segment in work, on its way, to be joined
+    static constexpr uint32_t total = seg + 3 * kWarps * sizeof(Segment);
     // the plan, before the first tile
     static constexpr uint32_t sums = 0;
     static constexpr uint32_t pre = 32 * 8;
@@ -755,42 +778,9 @@ struct Worker {
         }
     }
 
-    // This lane's share of a partial result, to and from `p` (32 lanes interleaved).
+    // This lane's share of the item's result to `p` (32 lanes interleaved): references
+    // and sums (over the lanes' keys), then the accumulators.
     __device__ __forceinline__ void put(float* p) const {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) p[(n * 4 + c) * 32] = m[n][c], p[(n * 4 + 2 + c) * 32] = l[n][c];
-#pragma unroll
-        for (int i = 0; i < kM; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) p[(NT * 4 + (i * NT + n) * 4 + c) * 32] = acc[i][n][c];
-    }
-    __device__ __forceinline__ void add(const float* p) {
-        float mine[NT][2], theirs[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float o = p[(n * 4 + c) * 32], t = fmaxf(m[n][c], o);
-                mine[n][c] = m[n][c] == t ? 1.0f : ex2(m[n][c] - t);
-                theirs[n][c] = o == t ? 1.0f : ex2(o - t);
-                m[n][c] = t;
-                l[n][c] = l[n][c] * mine[n][c] + p[(n * 4 + 2 + c) * 32] * theirs[n][c];
-            }
-#pragma unroll
-        for (int i = 0; i < kM; ++i)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    acc[i][n][c] = acc[i][n][c] * mine[n][c & 1] + p[(NT * 4 + (i * NT + n) * 4 + c) * 32] * theirs[n][c & 1];
-    }
-
-    // Sums over the lanes' keys; then the rows of the result, or of a part of it.
-    __device__ __forceinline__ void write(const Args& a, const Segment& s) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -799,41 +789,66 @@ struct Worker {
                 t += __shfl_xor_sync(0xffffffffu, t, 4);
                 t += __shfl_xor_sync(0xffffffffu, t, 8);
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
-                const int row = 8 * n + 2 * tig + c;
-                if (row >= s.rows) continue;
-                if (s.parts) {
-                    const int64_t part = part_of(s.c0, blockIdx.x) * L::kRows + row;
-                    float* o = a.part_o + part * D + gid * (D / 8);
-#pragma unroll
-                    for (int i = 0; i < kM; i += 2)
-                        *reinterpret_cast<float4*>(o + 2 * i) = make_float4(acc[i][n][c], acc[i][n][2 + c], acc[i + 1][n][c],
-                                                                            acc[i + 1][n][2 + c]);
-                    if (gid == 0) a.part_ml[part] = make_float2(m[n][c], t);
-                    continue;
-                }
-                const int r = s.row0 + row, tok = r / a.G;
-                const int64_t h = static_cast<int64_t>(s.g) * a.G + r - tok * a.G, at = s.q0 + static_cast<int64_t>(tok);
-                const float inv = t == 0.0f ? 0.0f : a.v_scale / t;
-                uint16_t* o = a.out + at * a.o_st + h * a.o_sh + gid * (D / 8);
-                uint32_t x[kM];
-#pragma unroll
-                for (int i = 0; i < kM; ++i) {
-                    const float lo = acc[i][n][c] * inv, hi = acc[i][n][2 + c] * inv;
-                    if (a.bf16) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-                        x[i] = *reinterpret_cast<const uint32_t*>(&b);
-                    } else {
-                        x[i] = half2_of(lo, hi);
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < kM; i += 4)
-                    *reinterpret_cast<uint4*>(o + 2 * i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-                if (a.lse && gid == 0)
-                    a.lse[at * a.G * a.hk + h] = t == 0.0f ? -INFINITY : (m[n][c] - kBias + __log2f(t)) * kLn2;
+                p[(n * 4 + c) * 32] = m[n][c];
+                p[(n * 4 + 2 + c) * 32] = t;
             }
+#pragma unroll
+        for (int i = 0; i < kM; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) p[(NT * 4 + (i * NT + n) * 4 + c) * 32] = acc[i][n][c];
     }
 };
+
+// This warp's part of joining the warps' shares of an item, in their order: units of
+// two neighbouring elements of four rows.
+template <int D, int NT>
+__device__ __forceinline__ void join_shares(const Args& a, const Segment& s, const float* shares, int warp, int lane) {
+    using L = Smem<D, NT>;
+    constexpr int kUnits = D / 16 * NT * 2, kStep = L::kShare / 4;
+    const int gid = lane >> 2, tig = lane & 3;
+    shares += lane;
+    for (int u = warp; u < kUnits; u += L::kWarps) {
+        const int c = u & 1, n = (u >> 1) % NT, i = (u >> 1) / NT;
+        const int row = 8 * n + 2 * tig + c;
+        float m[L::kWarps], top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < L::kWarps; ++w) {
+            m[w] = shares[w * kStep + (n * 4 + c) * 32];
+            top = fmaxf(top, m[w]);
+        }
+        float sum = 0.0f, lo = 0.0f, hi = 0.0f;
+#pragma unroll
+        for (int w = 0; w < L::kWarps; ++w) {
+            const float f = m[w] == top ? 1.0f : ex2(m[w] - top);
+            const float* p = shares + w * kStep;
+            sum += p[(n * 4 + 2 + c) * 32] * f;
+            lo += p[(NT * 4 + (i * NT + n) * 4 + c) * 32] * f;
+            hi += p[(NT * 4 + (i * NT + n) * 4 + 2 + c) * 32] * f;
+        }
+        if (row >= s.rows) continue;
+        const int col = gid * (D / 8) + 2 * i;
+        if (s.parts) {
+            const int64_t part = part_of(s.c0, blockIdx.x) * L::kRows + row;
+            *reinterpret_cast<float2*>(a.part_o + part * D + col) = make_float2(lo, hi);
+            if (col == 0) a.part_ml[part] = make_float2(top, sum);
+            continue;
+        }
+        const int r = s.row0 + row, tok = r / a.G;
+        const int64_t h = static_cast<int64_t>(s.g) * a.G + r - tok * a.G, at = s.q0 + static_cast<int64_t>(tok);
+        const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        uint32_t x;
+        if (a.bf16) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(lo * inv, hi * inv);
+            x = *reinterpret_cast<const uint32_t*>(&b);
+        } else {
+            x = half2_of(lo * inv, hi * inv);
+        }
+        *reinterpret_cast<uint32_t*>(a.out + at * a.o_st + h * a.o_sh + col) = x;
+        if (a.lse && col == 0) a.lse[at * a.G * a.hk + h] = sum == 0.0f ? -INFINITY : (top - kBias + __log2f(sum)) * kLn2;
+    }
+}
 
 template <int D, int NT>
 __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(const __grid_constant__ Args a) {
@@ -842,6 +857,11 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem);
+    if (threadIdx.x == 0) {
+        mbar_init(base + L::bars, kWarps);
+        mbar_init(base + L::bars + 8, kWarps);
+        fence_mbar_init();
+    }
     grid_dep_wait();
     grid_dep_launch();
     int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
@@ -854,16 +874,13 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
         units = __ldcg(a.pre + a.B);
     }
     const Start* range = reinterpret_cast<const Start*>(smem + L::range);
-    if (threadIdx.x < 2) {
-        const Start s = make_start(a, pre, units, static_cast<int>(blockIdx.x) + threadIdx.x, L::kRows);
-        reinterpret_cast<Start*>(smem + L::range)[threadIdx.x] = s;
-        if (threadIdx.x == 0 || static_cast<int>(blockIdx.x) == a.grid - 1) a.starts[blockIdx.x + threadIdx.x] = s;
-    }
+    find_range(a, pre, units, L::kRows, reinterpret_cast<Start*>(smem + L::range));
     __syncthreads();
-    volatile uint32_t* where = reinterpret_cast<volatile uint32_t*>(smem + L::where);
     // (what only the edges and ends of an item need stays out of the registers)
-    Segment* seg = reinterpret_cast<Segment*>(smem + L::seg) + 2 * warp;
+    Segment* seg = reinterpret_cast<Segment*>(smem + L::seg) + 3 * warp;
+    float* shares = reinterpret_cast<float*>(smem + L::shares);
     const uint32_t mine = base + L::ring + warp * (L::kHalves * L::kHalf);
+    const uint32_t written = base + L::bars, read = written + 8;
     Feed<D, NT> feed(a, range, seg + 1, warp, lane);
     feed.template issue<false>(a, mine, lane);
     feed.template issue<true>(a, mine + L::kHalf, lane);
@@ -875,6 +892,21 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     Segment& s = *seg;
     int k = warp;       // the warp's next tile in the segment
     uint32_t half = 0;  // and the half that it begins in
+    // The warps do not wait for one another at an item's end: each leaves its share and
+    // goes on, and takes its part of the join once all shares are there. Every warp
+    // sees every phase of both barriers, one after the other.
+    uint32_t ends = 0;  // items whose share this warp has left
+    bool owed = false;  // its part of the last one's join is still to do
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        int never = 0;
+        if (!mbar_wait_bounded(bar, parity & 1, a.spin, &never)) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_TIMEOUT));
+    };
+    auto join = [&]() {
+        join_shares<D, NT>(a, seg[2], shares, warp, lane);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(read);
+        owed = false;
+    };
     for (;;) {
         Segment t;
         if (!walk.next(a, L::kRows, t)) break;
@@ -885,6 +917,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
         me.reset();
         const int n = t.n, first = t.first, all_lo = t.all_lo, all_hi = t.all_hi;
         for (; k < n; k += kWarps) {
+            if (owed && __all_sync(0xffffffffu, mbar_test_wait(written, (ends - 1) & 1))) join();
             const int key0 = (first + k) * L::kKeys;
             const bool edge = key0 < all_lo || key0 + L::kKeys > all_hi;
             // halves in turn: this tile's keys, its values, the next tile's keys (copied
@@ -906,24 +939,21 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
             me.values(a, s, v_at, key0, edge);
         }
         k -= n;
-        // the warps' results, joined in pairs
-        uint32_t share = L::ring + warp * (L::kHalves * L::kHalf) + (half == 0 ? 2 : half - 1) * L::kHalf;
-        if constexpr (!L::kShareInRing) share = L::shares + (warp % (kWarps / 2)) * L::kShare;
-        if (lane == 0) where[warp] = share;
-#pragma unroll 1
-        for (int left = kWarps; left > 1;) {
-            const int upper = (left + 1) / 2;
-            if (warp >= upper && warp < left) {
-                __syncwarp();
-                me.put(reinterpret_cast<float*>(smem + share) + lane);
-            }
-            __syncthreads();
-            if (warp < left - upper) me.add(reinterpret_cast<const float*>(smem + where[warp + upper]) + lane);
-            left = upper;
-            if constexpr (!L::kShareInRing) __syncthreads();   // (the next round's shares take the place of these)
+        if (owed) {
+            wait(written, ends - 1);
+            join();
         }
-        __syncthreads();   // (the shares are read)
-        if (warp == 0) me.write(a, s);
+        if (ends) wait(read, ends - 1);   // (the shares' places are free)
+        me.put(shares + warp * (L::kShare / 4) + lane);
+        if (lane == 0) seg[2] = s;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(written);
+        ++ends;
+        owed = true;
+    }
+    if (owed) {
+        wait(written, ends - 1);
+        join();
     }
     cp_async_wait<0>();
 }
@@ -1232,6 +1262,7 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     a.k_sb = s->k_stride_block, a.k_sh = s->k_stride_head;
     a.v_sb = s->v_stride_block, a.v_sh = s->v_stride_head;
     a.pool_blocks = s->pool_blocks;
+    a.spin = p->spin_limit > 0 ? p->spin_limit : kDefaultSpin;
     a.B = s->n_seqs;
     a.hk = s->n_kv_heads;
     a.G = s->n_q_heads / s->n_kv_heads;
