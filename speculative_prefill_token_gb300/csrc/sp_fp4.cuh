@@ -36,11 +36,11 @@ __device__ __forceinline__ void fp4_unpack(uint32_t w, uint32_t (&r)[4]) {
         : "r"(w));
 }
 
-// Two e4m3 numbers (low byte first) as fp16.
+// Two e4m3 numbers (the low 16 bits, low byte first) as fp16.
 __device__ __forceinline__ uint32_t fp8_unpack(uint32_t two) {
     uint32_t r;
-    asm("{\n\t.reg .b16 x;\n\t"
-        "cvt.u16.u32 x, %1;\n\t"
+    asm("{\n\t.reg .b16 x, y;\n\t"
+        "mov.b32 {x, y}, %1;\n\t"
         "cvt.rn.f16x2.e4m3x2 %0, x;\n\t}"
         : "=r"(r)
         : "r"(two));

@@ -188,6 +188,13 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_plan_kernel(const Args a, in
     if (threadIdx.x == 0) a.pre[a.B] = units;
 }
 
+// CTAs that share `units`: few of them get less than a tile for every other warp.
+constexpr int kLeastUnits = 8;
+
+__device__ __forceinline__ int64_t ctas_for(const Args& a, int64_t units) {
+    return min(static_cast<int64_t>(a.grid), (units + kLeastUnits - 1) / kLeastUnits);
+}
+
 // x / y for x >= 0, y > 0: in 32 bits where both fit.
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
     if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
@@ -216,7 +223,7 @@ __device__ __forceinline__ Start make_start(const Args& a, int b, int64_t at, in
 // The starts of this CTA's range and of the next one's, to `range`. Every thread
 // looks whether one of them falls into a request of its own.
 __device__ __forceinline__ void find_range(const Args& a, const int64_t* pre, int64_t units, int rows, Start* range) {
-    const int64_t ctas = min(static_cast<int64_t>(a.grid), units);
+    const int64_t ctas = units > 0 ? ctas_for(a, units) : 0;
     const int c = blockIdx.x, t = threadIdx.x;
     auto tell = [&](int i, const Start& s) {
         range[i] = s;
@@ -329,8 +336,12 @@ struct Smem {
 
 // ------------------------------------------------------------ loads
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(__cvta_generic_to_global(src)) : "memory");
+// (the stream is the first to leave L2: what it pushes out otherwise are the lengths,
+// the tables and the code of the next launches)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(src)),
+                 "l"(policy)
+                 : "memory");
 }
 
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -353,9 +364,10 @@ struct Feed {
     int k, n;         // the warp's next tile in the segment; its tiles
     int id, row;      // this lane's block (-1: none) and row in it
     bool live;
+    uint64_t policy;
 
     __device__ __forceinline__ Feed(const Args& a, const Start* range, Segment* seg, int warp, int lane)
-        : w(range), s(seg), k(warp), n(0), id(-1), row(0), live(true) {
+        : w(range), s(seg), k(warp), n(0), id(-1), row(0), live(true), policy(policy_evict_first()) {
         settle(a, lane);
     }
     __device__ __forceinline__ void settle(const Args& a, int lane) {
@@ -402,7 +414,7 @@ struct Feed {
                     const uint8_t* src = pool + blk * (kValues ? a.v_sb : a.k_sb) + r * static_cast<int64_t>(L::kRec / kFp4Rows);
 #pragma unroll
                     for (uint32_t o = 0; o < L::kHalf; o += 512)
-                        if (o + 512 <= L::kHalf || o + 16 * lane < L::kHalf) copy16(dst + o, src + o);
+                        if (o + 512 <= L::kHalf || o + 16 * lane < L::kHalf) copy16(dst + o, src + o, policy);
                 }
             } else for (int p = 0; p < pieces; ++p, dst += bytes) {
                 const int blk = __shfl_sync(0xffffffffu, id, p), r = __shfl_sync(0xffffffffu, row, p);
@@ -411,7 +423,7 @@ struct Feed {
 #pragma unroll
                 for (uint32_t o = 0; o < L::kHalf; o += 512) {
                     if (o + 16 * lane >= bytes) break;
-                    copy16(dst + o, src + o);
+                    copy16(dst + o, src + o, policy);
                 }
             }
         }
@@ -607,13 +619,20 @@ struct Worker {
                 else if constexpr (D == 128) f[h] = lds_u16(at);
                 else lds_words(at, *reinterpret_cast<uint32_t(*)[1]>(f + h));
             }
+            // scales of neighbouring groups, two in a register
+            uint32_t g0[(D + 127) / 128], g1[(D + 127) / 128];
+#pragma unroll
+            for (int j = 0; j < (D + 127) / 128; ++j) {
+                g0[j] = fp8_unpack(f[0] >> (16 * j));
+                g1[j] = fp8_unpack(f[1] >> (16 * j));
+            }
             uint32_t s0 = 0, s1 = 0;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 if (i % 2 == 0) {   // the scale of the next 16 elements, in both halves
-                    const uint32_t pick = (i / 2) * 0x11u;
-                    s0 = fp8_unpack(__byte_perm(f[0], 0, pick));
-                    s1 = fp8_unpack(__byte_perm(f[1], 0, pick));
+                    const uint32_t pick = i / 2 % 2 ? 0x3232u : 0x1010u;
+                    s0 = __byte_perm(g0[i / 4], 0, pick);
+                    s1 = __byte_perm(g1[i / 4], 0, pick);
                 }
                 uint32_t x0[4], x1[4];
                 fp4_unpack(w0[i], x0);
