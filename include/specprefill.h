@@ -601,7 +601,8 @@ int sp_paged_attention(const sp_paged_shape* shape, const sp_attn_params* params
  * bytes: 8 tokens' codes (d / 2 bytes each, element 2 i in the low and 2 i + 1 in
  * the high four bits of byte i; bit 3 of a code is the sign), then their scales
  * (d / 16 bytes each). The records of a block and head follow one another; blocks
- * and heads are `stride_block` and `stride_head` bytes apart, multiples of 16.
+ * and heads are `stride_block` and `stride_head` bytes apart, multiples of 16 below
+ * 2^32 (SP_ERR_UNSUPPORTED).
  * head_dim is 64, 128 or 256, block_size 8, 16, 32, 64 or a multiple of 128. */
 
 /* Shapes and strides of sp_append_kv_fp4 (16-bit tensors in elements, pools in

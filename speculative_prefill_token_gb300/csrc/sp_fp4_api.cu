@@ -58,8 +58,10 @@ int check_stride(int64_t extent, int64_t stride, int64_t width, int64_t step) {
 // Blocks and heads of a 4-bit pool, in either order.
 int check_pool(int64_t blocks, int hk, int bs, int d, int64_t sb, int64_t sh) {
     const int64_t page = static_cast<int64_t>(bs) / kFp4Rows * fp4_record(d);
-    const int rc = check_stride(blocks, sb, page, 16);
-    return rc == SP_OK ? check_stride(hk, sh, page, 16) : rc;
+    int rc = check_stride(blocks, sb, page, 16);
+    if (rc == SP_OK) rc = check_stride(hk, sh, page, 16);
+    if (rc == SP_OK && ((blocks > 1 && sb > UINT32_MAX) || (hk > 1 && sh > UINT32_MAX))) rc = SP_ERR_UNSUPPORTED;
+    return rc;
 }
 
 int check_fp4(const sp_fp4_shape* s) {

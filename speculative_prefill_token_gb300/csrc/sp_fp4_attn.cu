@@ -82,7 +82,8 @@ struct Args {
     Start* starts;             // [grid + 1]
     float* part_o;             // [2 grid][rows][d]
     float2* part_ml;           // [2 grid][rows] (reference, sum)
-    int64_t q_st, q_sh, o_st, o_sh, k_sb, k_sh, v_sb, v_sh, pool_blocks, spin;
+    int64_t q_st, q_sh, o_st, o_sh, spin;
+    uint32_t k_sb, k_sh, v_sb, v_sh, pool_blocks;   // (bytes)
     int B, hk, G, bs, table_stride, cap, max_new, causal, window, grid;
     int tile_shift;            // log2 of a tile's keys
     int piece_shift;           // log2 of a copy's tokens: a block's, at most a tile's
@@ -360,14 +361,16 @@ template <int D, int NT>
 struct Feed {
     using L = Smem<D, NT>;
     Walk w;
-    Segment* s;       // in shared memory
-    int k, n;         // the warp's next tile in the segment; its tiles
-    int id, row;      // this lane's block (-1: none) and row in it
+    Segment* s;              // in shared memory
+    const int32_t* table;    // of the segment's request
+    const uint8_t *k_head, *v_head;   // the segment's KV head, this lane's 16 bytes
+    int k, n;                // the warp's next tile in the segment; its tiles
+    int64_t k_at, v_at;      // this lane's piece (-1: not loaded)
     bool live;
     uint64_t policy;
 
     __device__ __forceinline__ Feed(const Args& a, const Start* range, Segment* seg, int warp, int lane)
-        : w(range), s(seg), k(warp), n(0), id(-1), row(0), live(true), policy(policy_evict_first()) {
+        : w(range), s(seg), k(warp), n(0), k_at(-1), v_at(-1), live(true), policy(policy_evict_first()) {
         settle(a, lane);
     }
     __device__ __forceinline__ void settle(const Args& a, int lane) {
@@ -380,6 +383,9 @@ struct Feed {
             if (lane == 0) *s = t;
             __syncwarp();
             n = t.n;
+            table = a.table + static_cast<int64_t>(t.b) * a.table_stride;
+            k_head = a.k + static_cast<uint64_t>(t.g) * a.k_sh + 16 * lane;
+            v_head = a.v + static_cast<uint64_t>(t.g) * a.v_sh + 16 * lane;
         }
         if (live) look_up(a, lane);
     }
@@ -388,16 +394,19 @@ struct Feed {
         settle(a, lane);
     }
     __device__ __forceinline__ void look_up(const Args& a, int lane) {
-        const int key = (s->first + k) * L::kKeys + (lane << a.piece_shift);
-        id = -1;
-        if (lane < L::kKeys >> a.piece_shift && key < s->hi && key + (1 << a.piece_shift) > s->lo) {
-            const int blk = a.bs_shift >= 0 ? key >> a.bs_shift : key / a.bs;
-            row = key - blk * a.bs;
-            id = __ldg(a.table + static_cast<int64_t>(s->b) * a.table_stride + blk);
-            if (id < 0 || id >= a.pool_blocks) {
+        const int pieces = L::kKeys >> a.piece_shift, p = lane & (pieces - 1);   // (one piece: every lane's)
+        const int key = (s->first + k) * L::kKeys + (p << a.piece_shift);
+        k_at = -1;
+        if (key < s->hi && key + (1 << a.piece_shift) > s->lo) {
+            const uint32_t blk = a.bs_shift >= 0 ? key >> a.bs_shift : key / a.bs;
+            const uint32_t row = key - blk * a.bs;
+            uint32_t id = __ldg(table + blk);
+            if (id >= a.pool_blocks) {
                 atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
                 id = 0;
             }
+            k_at = static_cast<uint64_t>(id) * a.k_sb + row * (L::kRec / kFp4Rows);
+            v_at = static_cast<uint64_t>(id) * a.v_sb + row * (L::kRec / kFp4Rows);
         }
     }
     // Keys or values of the tile to `dst`, as a group of copies.
@@ -405,25 +414,26 @@ struct Feed {
     __device__ __forceinline__ void issue(const Args& a, uint32_t dst, int lane) const {
         if (live) {
             const int pieces = L::kKeys >> a.piece_shift;
-            const uint32_t bytes = (L::kRec / kFp4Rows) << a.piece_shift;
-            const uint8_t* pool = (kValues ? a.v + s->g * a.v_sh : a.k + s->g * a.k_sh) + 16 * lane;
+            const uint8_t* head = kValues ? v_head : k_head;
             dst += 16 * lane;
-            if (pieces == 1) {   // (one run of tokens, copied whole)
-                const int blk = __shfl_sync(0xffffffffu, id, 0), r = __shfl_sync(0xffffffffu, row, 0);
-                if (blk >= 0) {
-                    const uint8_t* src = pool + blk * (kValues ? a.v_sb : a.k_sb) + r * static_cast<int64_t>(L::kRec / kFp4Rows);
+            if (pieces == 1) {   // (one run of tokens)
+                if (k_at >= 0) {
+                    const uint8_t* src = head + (kValues ? v_at : k_at);
 #pragma unroll
                     for (uint32_t o = 0; o < L::kHalf; o += 512)
                         if (o + 512 <= L::kHalf || o + 16 * lane < L::kHalf) copy16(dst + o, src + o, policy);
                 }
-            } else for (int p = 0; p < pieces; ++p, dst += bytes) {
-                const int blk = __shfl_sync(0xffffffffu, id, p), r = __shfl_sync(0xffffffffu, row, p);
-                if (blk < 0) continue;
-                const uint8_t* src = pool + blk * (kValues ? a.v_sb : a.k_sb) + r * static_cast<int64_t>(L::kRec / kFp4Rows);
+            } else {
+                const uint32_t bytes = (L::kRec / kFp4Rows) << a.piece_shift;
+                for (int p = 0; p < pieces; ++p, dst += bytes) {
+                    const int64_t at = __shfl_sync(0xffffffffu, kValues && k_at >= 0 ? v_at : k_at, p);
+                    if (at < 0) continue;
+                    const uint8_t* src = head + at;
 #pragma unroll
-                for (uint32_t o = 0; o < L::kHalf; o += 512) {
-                    if (o + 16 * lane >= bytes) break;
-                    copy16(dst + o, src + o, policy);
+                    for (uint32_t o = 0; o < L::kHalf; o += 512) {
+                        if (o + 16 * lane >= bytes) break;
+                        copy16(dst + o, src + o, policy);
+                    }
                 }
             }
         }
@@ -450,6 +460,27 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+// Two fp32 values at a time.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
 
@@ -512,7 +543,7 @@ struct Worker {
     uint32_t q[D / 16][NT][2];
     uint32_t w[L::kMt][NT][2];     // the tile's weights
     float acc[kM][NT][4];
-    float m[NT][2], l[NT][2];      // reference (log2 units), sum of this lane's keys
+    float m[NT][2], l[NT][2];      // reference (a logit before its scale), sum of this lane's keys
     float sc[NT][2];               // scale of a row's logits, log2 units
     int gid, tig;
 
@@ -571,7 +602,8 @@ struct Worker {
                 q[2 * i + 1][n][0] = x[i].z, q[2 * i + 1][n][1] = x[i].w;
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) sc[n][c] = a.scale2 * __shfl_sync(0xffffffffu, back, (2 * tig + c) * 4);
+            for (int c = 0; c < 2; ++c)   // (not zero, which times a masked logit is no number)
+                sc[n][c] = fmaxf(a.scale2 * __shfl_sync(0xffffffffu, back, (2 * tig + c) * 4), 1.1754944e-38f);
         }
     }
 
@@ -649,13 +681,7 @@ struct Worker {
                 }
             }
         }
-        // logits in log2 units, masked at the edges of what the rows see
-#pragma unroll
-        for (int mt = 0; mt < L::kMt; ++mt)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) y[mt][n][c] *= sc[n][c & 1];
+        // masked at the edges of what the rows see; the largest
         if (edge) mask(a, s, y, key0);
         float top[NT][2];
         bool above = false;
@@ -668,7 +694,7 @@ struct Worker {
                 for (int i = 1; i < 2 * L::kMt; ++i) t = fmaxf(t, y[i / 2][n][i % 2 * 2 + c]);
                 top[n][c] = t;
                 // (a first value is above a reference of minus infinity)
-                above |= t > m[n][c] + kSlack;
+                above |= (t - m[n][c]) * sc[n][c] > kSlack;
             }
         if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
@@ -679,8 +705,8 @@ struct Worker {
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    if (t > m[n][c] + kSlack) {
-                        const float f = ex2(m[n][c] - t);   // (0 for a first value)
+                    if ((t - m[n][c]) * sc[n][c] > kSlack) {
+                        const float f = ex2((m[n][c] - t) * sc[n][c]);   // (0 for a first value)
                         m[n][c] = t;
                         l[n][c] *= f;
 #pragma unroll
@@ -691,18 +717,21 @@ struct Worker {
         // weights, transposed to the right operand of the second product
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float shift[2];
-#pragma unroll
-            for (int c = 0; c < 2; ++c) shift[c] = kBias - (m[n][c] == -INFINITY ? 0.0f : m[n][c]);
+            const float2 f = make_float2(sc[n][0], sc[n][1]);
+            // (the difference before the scale: the largest logit gives 2^kBias whatever its size)
+            const float2 less = make_float2(m[n][0] == -INFINITY ? 0.0f : -m[n][0], m[n][1] == -INFINITY ? 0.0f : -m[n][1]);
+            float2 sum = make_float2(l[n][0], l[n][1]);
 #pragma unroll
             for (int mt = 0; mt < L::kMt; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float p0 = ex2(y[mt][n][2 * h] + shift[0]), p1 = ex2(y[mt][n][2 * h + 1] + shift[1]);
-                    l[n][0] += p0;
-                    l[n][1] += p1;
-                    w[mt][n][h] = transpose8(half2_of(p0, p1));
+                    const float2 x = fma2(add2(make_float2(y[mt][n][2 * h], y[mt][n][2 * h + 1]), less), f, make_float2(kBias, kBias));
+                    const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                    sum = add2(sum, p);
+                    w[mt][n][h] = transpose8(half2_of(p.x, p.y));
                 }
+            l[n][0] = sum.x;
+            l[n][1] = sum.y;
         }
     }
 
@@ -808,7 +837,7 @@ struct Worker {
                 t += __shfl_xor_sync(0xffffffffu, t, 4);
                 t += __shfl_xor_sync(0xffffffffu, t, 8);
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
-                p[(n * 4 + c) * 32] = m[n][c];
+                p[(n * 4 + c) * 32] = m[n][c] * sc[n][c];   // (in log2 units from here on)
                 p[(n * 4 + 2 + c) * 32] = t;
             }
 #pragma unroll
@@ -1235,6 +1264,9 @@ Layout layout(const sp_fp4_shape* s, int grid) {
     return l;
 }
 
+// A stride of a pool (below 2^32 where it counts).
+uint32_t stride32(int64_t extent, int64_t stride) { return extent > 1 ? static_cast<uint32_t>(stride) : 0u; }
+
 template <int D, int NT>
 cudaError_t launch_rows(const Args& a, cudaStream_t st) {
     using L = Smem<D, NT>;
@@ -1278,9 +1310,9 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     a.part_ml = ws_ptr<float2>(ws, l.ml);
     a.q_st = s->q_stride_token, a.q_sh = s->q_stride_head;
     a.o_st = s->o_stride_token, a.o_sh = s->o_stride_head;
-    a.k_sb = s->k_stride_block, a.k_sh = s->k_stride_head;
-    a.v_sb = s->v_stride_block, a.v_sh = s->v_stride_head;
-    a.pool_blocks = s->pool_blocks;
+    a.k_sb = stride32(s->pool_blocks, s->k_stride_block), a.k_sh = stride32(s->n_kv_heads, s->k_stride_head);
+    a.v_sb = stride32(s->pool_blocks, s->v_stride_block), a.v_sh = stride32(s->n_kv_heads, s->v_stride_head);
+    a.pool_blocks = static_cast<uint32_t>(s->pool_blocks);
     a.spin = p->spin_limit > 0 ? p->spin_limit : kDefaultSpin;
     a.B = s->n_seqs;
     a.hk = s->n_kv_heads;
