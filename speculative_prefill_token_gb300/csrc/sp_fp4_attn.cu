@@ -209,9 +209,10 @@ __device__ __forceinline__ int range_owner(int64_t units, int64_t ctas, int64_t 
 
 // Unit u of `units`, of request b whose units begin at `at`, as a start; a cut inside
 // an item's fixed cost falls on the item's start.
-__device__ __forceinline__ Start make_start(const Args& a, int b, int64_t at, int64_t units, int64_t ctas, int64_t u, int rows) {
+__device__ __forceinline__ Start make_start(const Args& a, int b, int nq, int kv, int64_t at, int64_t units, int64_t ctas,
+                                            int64_t u, int rows) {
     Start s{b, 0, 0, 0, 1, {0, 0, 0}};
-    const Span sp = span_of(a, a.q_off[b + 1] - a.q_off[b], a.kv_len[b], rows);
+    const Span sp = span_of(a, nq, kv, rows);
     const int64_t per = sp.tiles + kItemCost;
     s.gj = static_cast<int32_t>(quotient(u - at, per));
     const int64_t item = at + s.gj * per;
@@ -238,12 +239,83 @@ __device__ __forceinline__ void find_range(const Args& a, const int64_t* pre, in
             const int64_t at = pre[b], end = b + 1 < a.B ? pre[b + 1] : units;
 #pragma unroll 1
             for (int i = 0; i < 2; ++i)
-                if (u[i] >= at && u[i] < end) tell(i, make_start(a, b, at, units, ctas, u[i], rows));
+                if (u[i] >= at && u[i] < end) tell(i, make_start(a, b, a.q_off[b + 1] - a.q_off[b], a.kv_len[b], at, units, ctas, u[i], rows));
         }
     } else if (t < 2 && c + t < ctas) {
         const int b = last_at_most(pre, a.B, u[t]);
-        tell(t, make_start(a, b, pre[b], units, ctas, u[t], rows));
+        tell(t, make_start(a, b, a.q_off[b + 1] - a.q_off[b], a.kv_len[b], pre[b], units, ctas, u[t], rows));
     }
+}
+
+// The same for a batch of at most 64 requests, by every warp for itself, two requests
+// a lane: no rendezvous, and one read of the lengths. False where costs leave 24
+// bits (the others decide so too): the block lays it out. (A decode step of 16: the
+// first tile's copies begin 5,900 cycles into the kernel by the block's plan.)
+constexpr int kWarpSeqs = 64;
+
+__device__ __forceinline__ bool warp_plan(const Args& a, int rows, Start* range, int lane, bool writes) {
+    constexpr unsigned kAll = 0xffffffffu;
+    int q0[2], nq[2] = {0, 0}, kv[2] = {0, 0}, n[2] = {0, 0};
+    bool bad = false, large = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int b = lane + 32 * i;
+        if (b < a.B) {
+            q0[i] = a.q_off[b];
+            nq[i] = a.q_off[b + 1];
+            kv[i] = a.kv_len[b];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int b = lane + 32 * i;
+        if (b >= a.B) continue;
+        bad |= bad_request(a, q0[i], nq[i], kv[i]) || (b == 0 && q0[i] != 0);
+        nq[i] -= q0[i];
+        if (bad || (a.dense && a.dense[b] >= 0)) continue;
+        const Span s = span_of(a, nq[i], kv[i], rows);
+        const int64_t cost = static_cast<int64_t>(a.hk) * s.row_tiles * (s.tiles + kItemCost);
+        large |= cost >> 24 != 0;
+        n[i] = static_cast<int>(cost);
+    }
+    const bool none = __any_sync(kAll, bad);
+    if (none && writes && lane == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+    if (!none && __any_sync(kAll, large)) return false;
+    int pre[2], run = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int incl = n[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += x;
+        }
+        pre[i] = run + incl - n[i];
+        run += __shfl_sync(kAll, incl, 31);
+    }
+    const int64_t units = none ? 0 : run, ctas = ctas_for(a, units);
+    // lanes 0 to 15: this CTA's start; the others: the next one's
+    const int c = blockIdx.x + (lane >> 4);
+    Start s{a.B, 0, 0, 0, 1, {0, 0, 0}};
+    const int64_t u = c < ctas ? quotient(units * c, ctas) : 0;
+    int b = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        // the last request with a cost that begins at or before the unit
+        const int64_t v = __shfl_sync(kAll, u, 16 * h);
+        const unsigned lo = __ballot_sync(kAll, n[0] > 0 && pre[0] <= v), hi = __ballot_sync(kAll, n[1] > 0 && pre[1] <= v);
+        if (lane >> 4 == h) b = hi ? 63 - __clz(hi) : lo ? 31 - __clz(lo) : 0;
+    }
+    const int at0 = __shfl_sync(kAll, pre[0], b & 31), at1 = __shfl_sync(kAll, pre[1], b & 31);
+    const int nq0 = __shfl_sync(kAll, nq[0], b & 31), nq1 = __shfl_sync(kAll, nq[1], b & 31);
+    const int kv0 = __shfl_sync(kAll, kv[0], b & 31), kv1 = __shfl_sync(kAll, kv[1], b & 31);
+    if (c < ctas) s = make_start(a, b, b < 32 ? nq0 : nq1, b < 32 ? kv0 : kv1, b < 32 ? at0 : at1, units, ctas, u, rows);
+    if ((lane & 15) == 0) {
+        range[lane >> 4] = s;
+        if (writes && (lane == 0 || static_cast<int>(blockIdx.x) == a.grid - 1)) a.starts[c] = s;
+    }
+    __syncwarp();
+    return true;
 }
 
 // ------------------------------------------------------------ segments
@@ -276,13 +348,13 @@ struct Walk {
                 continue;
             }
             s.b = at_b;
-            s.g = at_gj / sp.row_tiles;
+            s.g = sp.row_tiles == 1 ? at_gj : at_gj / sp.row_tiles;
             s.q0 = q0;
             s.kv = kv;
             s.pos0 = kv - nq;
             s.row0 = (at_gj - s.g * sp.row_tiles) * tile_rows;
             s.rows = min(tile_rows, nq * a.G - s.row0);
-            const int i0 = s.row0 / a.G, i1 = (s.row0 + s.rows - 1) / a.G;
+            const int i0 = nq == 1 ? 0 : s.row0 / a.G, i1 = nq == 1 ? 0 : (s.row0 + s.rows - 1) / a.G;
             s.hi = a.causal ? max(0, min(kv, s.pos0 + i1 + 1)) : kv;
             s.lo = a.window > 0 ? max(0, s.pos0 + i0 - a.window + 1) : 0;
             s.all_hi = a.causal ? min(kv, s.pos0 + i0 + 1) : kv;
@@ -307,7 +379,7 @@ struct Walk {
 // ------------------------------------------------------------ shared memory
 
 // Warps of a CTA: as many as their registers and shares of shared memory allow.
-constexpr int warps_of(int d, int nt) { return d == 64 ? 16 : d * nt <= 128 ? 12 : 8; }
+constexpr int warps_of(int d, int nt) { return d * nt == 64 ? 16 : d * nt == 128 ? 12 : 8; }
 
 template <int D, int NT>
 struct Smem {
@@ -325,8 +397,8 @@ struct Smem {
     static constexpr uint32_t kShare = kVals * 32 * 4;    // a warp's share for the join at an item's end
     static constexpr uint32_t ring = 0;                   // [kWarps][kHalves]
     static constexpr uint32_t shares = kWarps * kHalves * kHalf;   // [kWarps]
-    static constexpr uint32_t range = shares + kWarps * kShare;    // [2] Start
-    static constexpr uint32_t bars = range + 2 * sizeof(Start);    // shares written, shares read
+    static constexpr uint32_t range = shares + kWarps * kShare;    // [kWarps][2] Start
+    static constexpr uint32_t bars = range + kWarps * 2 * sizeof(Start);    // shares written, shares read
     static constexpr uint32_t seg = bars + 16;                     // [kWarps][3] Segment in work, on its way, to be joined
     static constexpr uint32_t total = seg + 3 * kWarps * sizeof(Segment);
     // the plan, before the first tile
@@ -559,29 +631,35 @@ struct Worker {
         }
     }
 
-    // Query rows as the products' right operand. bf16 rows are scaled by a power of
+    // Query rows, and then their scaling, as the products' right operand. bf16 rows are scaled by a power of
     // two that takes their largest element to [2^14, 2^15): exact in fp16 down to
     // 2^-31 of it (8 significant bits above the last subnormal).
-    __device__ __forceinline__ void load_q(const Args& a, const Segment& s) {
+    __device__ __forceinline__ void fetch_q(const Args& a, const Segment& s) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const int r = s.row0 + 8 * n + gid, tok = r / a.G;
-            uint4 x[D / 32];
+            const int r = s.row0 + 8 * n + gid, tok = a.G == 1 ? r : r / a.G;
             const bool live = 8 * n + gid < s.rows;
             const uint16_t* p = a.q + (s.q0 + static_cast<int64_t>(tok)) * a.q_st +
                                 (static_cast<int64_t>(s.g) * a.G + r - tok * a.G) * a.q_sh + tig * (D / 4);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                x[i] = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < D / 32; ++i) {
+                const uint4 x = live ? __ldg(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0, 0, 0, 0);
+                q[2 * i][n][0] = x.x, q[2 * i][n][1] = x.y;
+                q[2 * i + 1][n][0] = x.z, q[2 * i + 1][n][1] = x.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void scale_q(const Args& a) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
             float back = 1.0f;
             if (a.bf16) {
                 uint32_t top = 0;
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) top = max(top, max(w[u] & 0x7fff0000u, (w[u] << 16) & 0x7fff0000u));
-                }
+                    for (int u = 0; u < 2; ++u)
+                        top = max(top, max(q[i][n][u] & 0x7fff0000u, (q[i][n][u] << 16) & 0x7fff0000u));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                 // exponent field of the factor and of its inverse, both kept normal
@@ -589,17 +667,10 @@ struct Worker {
                 const float f = __uint_as_float(static_cast<uint32_t>(e) << 23);
                 back = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&x[i]);
+                for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        w[u] = half2_of(__uint_as_float(w[u] << 16) * f, __uint_as_float(w[u] & 0xffff0000u) * f);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                q[2 * i][n][0] = x[i].x, q[2 * i][n][1] = x[i].y;
-                q[2 * i + 1][n][0] = x[i].z, q[2 * i + 1][n][1] = x[i].w;
+                    for (int u = 0; u < 2; ++u)
+                        q[i][n][u] = half2_of(__uint_as_float(q[i][n][u] << 16) * f, __uint_as_float(q[i][n][u] & 0xffff0000u) * f);
             }
 #pragma unroll
             for (int c = 0; c < 2; ++c)   // (not zero, which times a masked logit is no number)
@@ -912,32 +983,50 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     }
     grid_dep_wait();
     grid_dep_launch();
-    int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
-    int64_t units;
-    if (a.local_plan) {
-        units = plan_requests<L::kThreads>(a, L::kRows, pre, reinterpret_cast<int64_t*>(smem + L::sums));
-        __syncthreads();
+    Start* range = reinterpret_cast<Start*>(smem + L::range) + 2 * warp;
+    if (a.B <= kWarpSeqs && warp_plan(a, L::kRows, range, lane, warp == 0)) {
+        __syncthreads();   // (the barriers are there)
     } else {
-        pre = a.pre;
-        units = __ldcg(a.pre + a.B);
+        int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
+        int64_t units;
+        if (a.local_plan) {
+            units = plan_requests<L::kThreads>(a, L::kRows, pre, reinterpret_cast<int64_t*>(smem + L::sums));
+            __syncthreads();
+        } else {
+            pre = a.pre;
+            units = __ldcg(a.pre + a.B);
+        }
+        range = reinterpret_cast<Start*>(smem + L::range);
+        find_range(a, pre, units, L::kRows, range);
+        __syncthreads();
     }
-    const Start* range = reinterpret_cast<const Start*>(smem + L::range);
-    find_range(a, pre, units, L::kRows, reinterpret_cast<Start*>(smem + L::range));
-    __syncthreads();
     // (what only the edges and ends of an item need stays out of the registers)
     Segment* seg = reinterpret_cast<Segment*>(smem + L::seg) + 3 * warp;
     float* shares = reinterpret_cast<float*>(smem + L::shares);
     const uint32_t mine = base + L::ring + warp * (L::kHalves * L::kHalf);
     const uint32_t written = base + L::bars, read = written + 8;
     Feed<D, NT> feed(a, range, seg + 1, warp, lane);
-    feed.template issue<false>(a, mine, lane);
-    feed.template issue<true>(a, mine + L::kHalf, lane);
-    if (feed.live) feed.next(a, lane);
     Worker<D, NT> me;
     me.gid = lane >> 2;
     me.tig = lane & 3;
     Walk walk(range);
     Segment& s = *seg;
+    int n, first, all_lo, all_hi;
+    // the next segment, its queries on their way
+    auto advance = [&]() -> bool {
+        Segment t;
+        if (!walk.next(a, L::kRows, t)) return false;
+        __syncwarp();
+        if (lane == 0) s = t;
+        __syncwarp();
+        n = t.n, first = t.first, all_lo = t.all_lo, all_hi = t.all_hi;
+        me.fetch_q(a, s);
+        return true;
+    };
+    bool more = advance();   // (while the first block id is looked up)
+    feed.template issue<false>(a, mine, lane);
+    feed.template issue<true>(a, mine + L::kHalf, lane);
+    if (feed.live) feed.next(a, lane);
     int k = warp;       // the warp's next tile in the segment
     uint32_t half = 0;  // and the half that it begins in
     // The warps do not wait for one another at an item's end: each leaves its share and
@@ -955,15 +1044,9 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
         if (lane == 0) mbar_arrive(read);
         owed = false;
     };
-    for (;;) {
-        Segment t;
-        if (!walk.next(a, L::kRows, t)) break;
-        __syncwarp();
-        if (lane == 0) s = t;
-        __syncwarp();
-        me.load_q(a, s);
+    for (; more; more = advance()) {
+        me.scale_q(a);
         me.reset();
-        const int n = t.n, first = t.first, all_lo = t.all_lo, all_hi = t.all_hi;
         for (; k < n; k += kWarps) {
             if (owed && __all_sync(0xffffffffu, mbar_test_wait(written, (ends - 1) & 1))) join();
             const int key0 = (first + k) * L::kKeys;
