@@ -247,13 +247,14 @@ __device__ __forceinline__ void find_range(const Args& a, const int64_t* pre, in
     }
 }
 
-// The same for a batch of at most 64 requests, by every warp for itself, two requests
-// a lane: no rendezvous, and one read of the lengths. False where costs leave 24
-// bits (the others decide so too): the block lays it out. (A decode step of 16: the
-// first tile's copies begin 5,900 cycles into the kernel by the block's plan.)
+// The same for a batch of at most 64 requests, by one warp, two requests a lane: one
+// read of the lengths and one rendezvous. Costs that leave 24 bits are left to the block:
+// the first start is then of request -1. (A decode step of 16: the first tile's
+// copies begin 5,900 cycles into the kernel by the block's plan, 4,000 by every warp
+// for itself.)
 constexpr int kWarpSeqs = 64;
 
-__device__ __forceinline__ bool warp_plan(const Args& a, int rows, Start* range, int lane, bool writes) {
+__device__ __forceinline__ void warp_plan(const Args& a, int rows, Start* range, int lane) {
     constexpr unsigned kAll = 0xffffffffu;
     int q0[2], nq[2] = {0, 0}, kv[2] = {0, 0}, n[2] = {0, 0};
     bool bad = false, large = false;
@@ -279,8 +280,11 @@ __device__ __forceinline__ bool warp_plan(const Args& a, int rows, Start* range,
         n[i] = static_cast<int>(cost);
     }
     const bool none = __any_sync(kAll, bad);
-    if (none && writes && lane == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
-    if (!none && __any_sync(kAll, large)) return false;
+    if (none && lane == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
+    if (!none && __any_sync(kAll, large)) {
+        if (lane == 0) range->b = -1;
+        return;
+    }
     int pre[2], run = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -312,10 +316,8 @@ __device__ __forceinline__ bool warp_plan(const Args& a, int rows, Start* range,
     if (c < ctas) s = make_start(a, b, b < 32 ? nq0 : nq1, b < 32 ? kv0 : kv1, b < 32 ? at0 : at1, units, ctas, u, rows);
     if ((lane & 15) == 0) {
         range[lane >> 4] = s;
-        if (writes && (lane == 0 || static_cast<int>(blockIdx.x) == a.grid - 1)) a.starts[c] = s;
+        if (lane == 0 || static_cast<int>(blockIdx.x) == a.grid - 1) a.starts[c] = s;
     }
-    __syncwarp();
-    return true;
 }
 
 // ------------------------------------------------------------ segments
@@ -397,8 +399,8 @@ struct Smem {
     static constexpr uint32_t kShare = kVals * 32 * 4;    // a warp's share for the join at an item's end
     static constexpr uint32_t ring = 0;                   // [kWarps][kHalves]
     static constexpr uint32_t shares = kWarps * kHalves * kHalf;   // [kWarps]
-    static constexpr uint32_t range = shares + kWarps * kShare;    // [kWarps][2] Start
-    static constexpr uint32_t bars = range + kWarps * 2 * sizeof(Start);    // shares written, shares read
+    static constexpr uint32_t range = shares + kWarps * kShare;    // [2] Start
+    static constexpr uint32_t bars = range + 2 * sizeof(Start);    // shares written, shares read
     static constexpr uint32_t seg = bars + 16;                     // [kWarps][3] Segment in work, on its way, to be joined
     static constexpr uint32_t total = seg + 3 * kWarps * sizeof(Segment);
     // the plan, before the first tile
@@ -441,23 +443,27 @@ struct Feed {
     bool live;
     uint64_t policy;
 
-    __device__ __forceinline__ Feed(const Args& a, const Start* range, Segment* seg, int warp, int lane)
-        : w(range), s(seg), k(warp), n(0), k_at(-1), v_at(-1), live(true), policy(policy_evict_first()) {
+    // (the walk has taken its first step, to `t`)
+    __device__ __forceinline__ Feed(const Args& a, const Walk& walk, const Segment& t, bool some, Segment* seg, int warp, int lane)
+        : w(walk), s(seg), k(warp), n(0), k_at(-1), v_at(-1), live(some), policy(policy_evict_first()) {
+        if (live) take(a, t, lane);
         settle(a, lane);
+    }
+    __device__ __forceinline__ void take(const Args& a, const Segment& t, int lane) {
+        __syncwarp();
+        if (lane == 0) *s = t;
+        __syncwarp();
+        n = t.n;
+        table = a.table + static_cast<int64_t>(t.b) * a.table_stride;
+        k_head = a.k + static_cast<uint64_t>(t.g) * a.k_sh + 16 * lane;
+        v_head = a.v + static_cast<uint64_t>(t.g) * a.v_sh + 16 * lane;
     }
     __device__ __forceinline__ void settle(const Args& a, int lane) {
         while (live && k >= n) {
             k -= n;
             Segment t;
             live = w.next(a, L::kRows, t);
-            if (!live) break;
-            __syncwarp();
-            if (lane == 0) *s = t;
-            __syncwarp();
-            n = t.n;
-            table = a.table + static_cast<int64_t>(t.b) * a.table_stride;
-            k_head = a.k + static_cast<uint64_t>(t.g) * a.k_sh + 16 * lane;
-            v_head = a.v + static_cast<uint64_t>(t.g) * a.v_sh + 16 * lane;
+            if (live) take(a, t, lane);
         }
         if (live) look_up(a, lane);
     }
@@ -983,20 +989,22 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     }
     grid_dep_wait();
     grid_dep_launch();
-    Start* range = reinterpret_cast<Start*>(smem + L::range) + 2 * warp;
-    if (a.B <= kWarpSeqs && warp_plan(a, L::kRows, range, lane, warp == 0)) {
-        __syncthreads();   // (the barriers are there)
-    } else {
+    Start* range = reinterpret_cast<Start*>(smem + L::range);
+    const bool few = a.B <= kWarpSeqs;
+    if (few) {
+        if (warp == 0) warp_plan(a, L::kRows, range, lane);
+        __syncthreads();
+    }
+    if (!few || range->b < 0) {
         int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
         int64_t units;
         if (a.local_plan) {
             units = plan_requests<L::kThreads>(a, L::kRows, pre, reinterpret_cast<int64_t*>(smem + L::sums));
-            __syncthreads();
         } else {
             pre = a.pre;
             units = __ldcg(a.pre + a.B);
         }
-        range = reinterpret_cast<Start*>(smem + L::range);
+        __syncthreads();   // (the first start is read)
         find_range(a, pre, units, L::kRows, range);
         __syncthreads();
     }
@@ -1005,25 +1013,30 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     float* shares = reinterpret_cast<float*>(smem + L::shares);
     const uint32_t mine = base + L::ring + warp * (L::kHalves * L::kHalf);
     const uint32_t written = base + L::bars, read = written + 8;
-    Feed<D, NT> feed(a, range, seg + 1, warp, lane);
     Worker<D, NT> me;
     me.gid = lane >> 2;
     me.tig = lane & 3;
     Walk walk(range);
     Segment& s = *seg;
     int n, first, all_lo, all_hi;
-    // the next segment, its queries on their way
-    auto advance = [&]() -> bool {
-        Segment t;
-        if (!walk.next(a, L::kRows, t)) return false;
+    // a segment in work, its queries on their way
+    auto begin = [&](const Segment& t) {
         __syncwarp();
         if (lane == 0) s = t;
         __syncwarp();
         n = t.n, first = t.first, all_lo = t.all_lo, all_hi = t.all_hi;
         me.fetch_q(a, s);
+    };
+    auto advance = [&]() -> bool {
+        Segment t;
+        if (!walk.next(a, L::kRows, t)) return false;
+        begin(t);
         return true;
     };
-    bool more = advance();   // (while the first block id is looked up)
+    Segment one;
+    const bool some = walk.next(a, L::kRows, one);
+    Feed<D, NT> feed(a, walk, one, some, seg + 1, warp, lane);
+    if (some) begin(one);   // (while the first block id is looked up)
     feed.template issue<false>(a, mine, lane);
     feed.template issue<true>(a, mine + L::kHalf, lane);
     if (feed.live) feed.next(a, lane);
@@ -1044,7 +1057,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
         if (lane == 0) mbar_arrive(read);
         owed = false;
     };
-    for (; more; more = advance()) {
+    for (bool more = some; more; more = advance()) {
         me.scale_q(a);
         me.reset();
         for (; k < n; k += kWarps) {

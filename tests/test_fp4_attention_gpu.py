@@ -103,7 +103,7 @@ def test_large_logits_and_sinks():
     check(c, "bf16")
 
 
-@pytest.mark.parametrize("batch", [1100, 3000])
+@pytest.mark.parametrize("batch", [65, 200, 1100, 3000])
 def test_many_requests(batch):
     rng = np.random.default_rng(batch)
     ctx = rng.integers(0, 60, batch).tolist()
