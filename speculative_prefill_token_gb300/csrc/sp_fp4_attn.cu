@@ -53,7 +53,7 @@ namespace {
 
 // Keys of a tile, the unit of work of a warp.
 __host__ __device__ constexpr int tile_keys(int d) { return d <= 128 ? 64 : 32; }
-constexpr int kItemCost = 8;                 // of an item besides its tiles, in tiles
+constexpr int kItemCost = 16;                // of an item besides its tiles, in tiles
 constexpr int kLocalSeqs = 1024;             // requests of a plan made by every CTA
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxGrid = 256;
@@ -1169,7 +1169,11 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const __grid_con
 
 // ------------------------------------------------------------ requests with many rows
 
-constexpr int kDenseRows = 64;        // rows from which a request is read through 16 bits
+// Rows from which a request is read through 16 bits. (4 requests of 8K tokens, groups of
+// 4, 16 bits and 4: 96 rows 36 and 22 us at d = 64, 63 and 45 at 128, 67 and 60 at
+// 256; 192 rows 44 and 31, 69 and 76, 66 and 104; 512 rows 48 and 61, 92 and 175, 85
+// and 249.)
+__host__ __device__ constexpr int dense_rows(int d) { return d == 64 ? 256 : 128; }
 constexpr int kDenseBlock = 128;      // tokens of a block of the copy
 constexpr int kDenseThreads = 256;
 
@@ -1191,7 +1195,7 @@ struct DenseArgs {
 };
 
 // Which requests are read through 16 bits, and where their copies lie: those of
-// kDenseRows rows and more, in order, as long as their blocks fit. By one block.
+// dense_rows() rows and more, in order, as long as their blocks fit. By one block.
 __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const DenseArgs a) {
     __shared__ int64_t sums[32];
     __shared__ int most;
@@ -1207,7 +1211,7 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const Dens
         if (b < a.B) {
             // (lengths that are out of range are told by the kernels that follow)
             const int64_t nq = static_cast<int64_t>(a.q_off[b + 1]) - a.q_off[b], kv = a.kv_len[b];
-            if (nq * a.G >= kDenseRows && nq <= a.max_new && kv > 0 && kv <= static_cast<int64_t>(a.width) * kDenseBlock &&
+            if (nq * a.G >= dense_rows(a.d) && nq <= a.max_new && kv > 0 && kv <= static_cast<int64_t>(a.width) * kDenseBlock &&
                 (kv + a.bs - 1) / a.bs <= a.table_stride)
                 n = (kv + kDenseBlock - 1) / kDenseBlock - first_of(static_cast<int>(nq), static_cast<int>(kv));
         }
@@ -1341,9 +1345,9 @@ Layout layout(const sp_fp4_shape* s, int grid) {
     const int64_t rows = static_cast<int64_t>(s->n_tokens) * (s->n_q_heads / s->n_kv_heads);
     const int64_t most = static_cast<int64_t>(most_new(s)) * (s->n_q_heads / s->n_kv_heads);
     l.dense_cap = 0;
-    if (s->dense_tokens > 0 && most >= kDenseRows && static_cast<int64_t>(dense_width(s)) * s->n_seqs <= kMaxDenseTable) {
+    if (s->dense_tokens > 0 && most >= dense_rows(s->head_dim) && static_cast<int64_t>(dense_width(s)) * s->n_seqs <= kMaxDenseTable) {
         // (a request's last block may be begun)
-        const int64_t begun = rows / kDenseRows < s->n_seqs ? rows / kDenseRows : s->n_seqs;
+        const int64_t begun = rows / dense_rows(s->head_dim) < s->n_seqs ? rows / dense_rows(s->head_dim) : s->n_seqs;
         l.dense_cap = static_cast<int>(s->dense_tokens / kDenseBlock + begun);
         l.dense_width = dense_width(s);
         const size_t copy = static_cast<size_t>(l.dense_cap) * kDenseBlock * s->n_kv_heads * s->head_dim * 2;
