@@ -3,12 +3,16 @@
 // original position): the store of a step's rotated keys and values, and rows
 // read back as 16-bit values.
 //
-// append_kv_fp4_kernel. A thread owns one pair of 16-byte vectors of a query row,
-// or one group of 16 elements of a key or value row: it needs no other thread
-// for the group's largest element, its scale and its 8 bytes of codes. (A key
-// group that is rotated reads its partners too, the same lines as another thread
-// of the warp.) Every operation of the stored value is a single 32-bit one, none
-// contracted, so that the bits are those of the definition in specprefill.h.
+// append_kv_fp4_kernel. A thread owns pairs of 16-byte vectors of query rows, or two
+// groups of 16 elements of a key or value row: the groups that are rotated with one
+// another, or neighbours. It needs no other thread for a group's largest element, its
+// scale and its 8 bytes of codes. (Where half the rotated elements are no whole
+// number of groups, a key's threads read the partners of their neighbours' groups.)
+// Every operation of the stored value is one of 32 bits, rounded as the definition in
+// specprefill.h has it: the division by the scale as r = 1 / s, q = y r, q + (y - q s) r
+// with fused operations, which is the rounded quotient (Markstein: r is rounded
+// correctly, and no quotient here overflows; one that underflows is far below the
+// smallest code's border).
 //
 // unpack_fp4_kernel. A thread turns 8 bytes of codes and a scale into 32 bytes.
 #include <cuda_bf16.h>
@@ -27,7 +31,7 @@ namespace sp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCtas = 4;   // resident CTAs of an SM and the grid's
+constexpr int kCtas = 3;   // resident CTAs of an SM and the grid's
 
 __device__ __forceinline__ void raise_status(int32_t* status, int code) {
     if (status) atomicMax(status, code);
@@ -96,14 +100,9 @@ __device__ __forceinline__ void angles(const float* row, int half, float (&c)[8]
     }
 }
 
-// The codes (8 bytes) and scale of a group of 16 values, their factor taken out.
-__device__ __forceinline__ uint2 encode(float (&x)[16], float factor, uint32_t* scale_byte) {
+// The codes (8 bytes) and scale of a group of 16 values.
+__device__ __forceinline__ uint2 encode(const float (&x)[16], uint32_t* scale_byte) {
     uint32_t top = 0;
-    // (a division by 1 changes nothing)
-    if (factor != 1.0f) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], factor);
-    }
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
     if (top >= 0x7f800000u) {   // an infinity or NaN among them
@@ -114,11 +113,48 @@ __device__ __forceinline__ uint2 encode(float (&x)[16], float factor, uint32_t* 
     const uint32_t byte = max(fp8_pack(__fdiv_rn(__uint_as_float(top), 6.0f)), 1u);
     *scale_byte = byte;
     const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(fp8_unpack(byte))));
+    const float r = __frcp_rn(s);
+    auto over = [&](float y) {
+        const float q = __fmul_rn(y, r);
+        return copysignf(__fmaf_rn(__fmaf_rn(-q, s, y), r, q), y);   // (the sign of a zero)
+    };
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w[i / 4] |= fp4_pack2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s)) << (8 * (i % 4));
+    for (int i = 0; i < 8; ++i) w[i / 4] |= fp4_pack2(over(x[2 * i]), over(x[2 * i + 1])) << (8 * (i % 4));
     return make_uint2(w[0], w[1]);
+}
+
+// A group of a row to its record, its pool's factor taken out.
+__device__ __forceinline__ void store_group(float (&x)[16], float factor, uint8_t* rec, int d, int r, int group) {
+    // (a division by 1 changes nothing)
+    if (factor != 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], factor);
+    }
+    uint32_t byte;
+    const uint2 codes = encode(x, &byte);
+    *reinterpret_cast<uint2*>(rec + r * (d / 2) + 8 * group) = codes;
+    rec[fp4_codes(d) + r * (d / 16) + group] = static_cast<uint8_t>(byte);
+}
+
+// 8 elements of x and of their partners y: (x cos - y sin, y cos + x sin), each
+// product and sum rounded.
+__device__ __forceinline__ void turn8(const float* row, int half, float* x, float* y) {
+    float c[8], s[8];
+    angles(row, half, c, s);
+#pragma unroll
+    for (int v = 0; v < 8; ++v) {
+        const float a = x[v], b = y[v];
+        x[v] = __fadd_rn(__fmul_rn(a, c[v]), __fmul_rn(-b, s[v]));
+        y[v] = __fadd_rn(__fmul_rn(b, c[v]), __fmul_rn(a, s[v]));
+    }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void load16(const uint16_t* p, float (&x)[16]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(p) + u), *reinterpret_cast<float(*)[8]>(x + 8 * u));
 }
 
 template <bool kBf16>
@@ -130,19 +166,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const Ap
         const int64_t given = *a.n_new;
         n = given < 0 ? 0 : (given < n ? given : n);
     }
-    const int pairs = a.d / 16;            // pairs of vectors, or groups, of a row
-    const int per_token = pairs * a.groups;
-    const int heads = a.hq + 2 * a.hk;
+    // threads of a token: those of the queries, then of the keys, then of the values
+    const int pairs = a.d / 16, halves = a.d / 32;
+    const int of_q = pairs * a.groups, of_k = a.hk * halves, per_token = of_q + 2 * of_k;
     const int64_t total = n * per_token;
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; w < total;
          w += static_cast<int64_t>(gridDim.x) * kThreads) {
         const int64_t t = w / per_token;
         const int rest = static_cast<int>(w - t * per_token);
-        const int group = rest / pairs, i = rest - group * pairs;
-        const int64_t slot = a.slot_map[t];
-        const bool stored = slot >= 0 && slot < a.pool_tokens;
-        if (slot >= a.pool_tokens && rest == 0) raise_status(a.status, SP_ERR_DEVICE);
         const float* row = nullptr;
+        const int64_t slot = a.slot_map[t];
+        if (slot >= a.pool_tokens && rest == 0) raise_status(a.status, SP_ERR_DEVICE);
         if (a.half) {
             const int64_t pos = a.positions[t];
             if (pos < 0 || pos >= a.max_pos) {
@@ -151,23 +185,21 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const Ap
             }
             row = a.cos_sin + pos * 2 * a.half;
         }
-        const int64_t blk = stored ? slot / a.bs : 0;
-        const int within = stored ? static_cast<int>(slot - blk * a.bs) : 0;
-        const int64_t rec = static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
-        const int r = within % kFp4Rows;
-        const int h1 = min((group + 1) * a.heads_per, heads);
-        for (int h = group * a.heads_per; h < h1; ++h) {
-            if (h < a.hq) {
-                // vectors (e0, e1) in elements: a rotated pair, or two neighbours behind it
-                const bool turn = i < a.half / 8;
-                const int e0 = turn ? i * 8 : 2 * a.half + (i - a.half / 8) * 16, e1 = turn ? e0 + a.half : e0 + 8;
+        if (rest < of_q) {
+            // vectors (e0, e1) in elements: a rotated pair, or two neighbours behind it
+            const int group = rest / pairs, i = rest - group * pairs;
+            const bool turn = i < a.half / 8;
+            const int e0 = turn ? i * 8 : 2 * a.half + (i - a.half / 8) * 16, e1 = turn ? e0 + a.half : e0 + 8;
+            float c[8], s[8];
+            if (turn) angles(row + e0, a.half, c, s);
+            const int h0 = group * a.heads_per, h1 = min(h0 + a.heads_per, a.hq);
+#pragma unroll 2
+            for (int h = h0; h < h1; ++h) {
                 const uint16_t* src = a.q + t * a.q_st + h * a.q_sh;
                 uint16_t* dst = a.q_out + t * a.qo_st + h * a.qo_sh;
                 uint4 x = __ldcs(reinterpret_cast<const uint4*>(src + e0));
                 uint4 y = __ldcs(reinterpret_cast<const uint4*>(src + e1));
                 if (turn) {
-                    float c[8], s[8];
-                    angles(row + e0, a.half, c, s);
                     uint32_t* px = reinterpret_cast<uint32_t*>(&x);
                     uint32_t* py = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
@@ -179,38 +211,47 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const Ap
                 }
                 *reinterpret_cast<uint4*>(dst + e0) = x;
                 *reinterpret_cast<uint4*>(dst + e1) = y;
-                continue;
             }
-            if (!stored) continue;
-            const bool is_v = h >= a.hq + a.hk;
-            const int g = is_v ? h - a.hq - a.hk : h - a.hq;
-            const uint16_t* src = is_v ? a.v + t * a.v_st + g * a.v_sh : a.k + t * a.k_st + g * a.k_sh;
-            uint8_t* dst = is_v ? a.v_pool + blk * a.vp_sb + g * a.vp_sh : a.k_pool + blk * a.kp_sb + g * a.kp_sh;
-            float x[16];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int e = 16 * i + 8 * u;
-                float f[8];
-                unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(src + e)), f);
-                if (!is_v && e < 2 * a.half) {
-                    // a cos - b sin in the first half, b cos + a sin in the second
-                    const bool second = e >= a.half;
-                    const int j = second ? e - a.half : e;
-                    float o[8], c[8], s[8];
-                    unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(src + (second ? j : e + a.half))), o);
-                    angles(row + j, a.half, c, s);
-#pragma unroll
-                    for (int v = 0; v < 8; ++v)
-                        f[v] = __fadd_rn(__fmul_rn(f[v], c[v]), __fmul_rn(second ? o[v] : -o[v], s[v]));
-                }
-#pragma unroll
-                for (int v = 0; v < 8; ++v) x[8 * u + v] = f[v];
-            }
-            uint32_t byte;
-            const uint2 codes = encode(x, is_v ? a.v_scale : a.k_scale, &byte);
-            *reinterpret_cast<uint2*>(dst + rec + r * (a.d / 2) + 8 * i) = codes;
-            dst[rec + fp4_codes(a.d) + r * (a.d / 16) + i] = static_cast<uint8_t>(byte);
+            continue;
         }
+        if (slot < 0 || slot >= a.pool_tokens) continue;
+        const bool is_v = rest >= of_q + of_k;
+        const int unit = rest - of_q - (is_v ? of_k : 0), g = unit / halves, j = unit - g * halves;
+        const uint32_t at = static_cast<uint32_t>(slot), blk = at / static_cast<uint32_t>(a.bs);
+        const int within = static_cast<int>(at - blk * a.bs), r = within % kFp4Rows;
+        const uint16_t* src = is_v ? a.v + t * a.v_st + g * a.v_sh : a.k + t * a.k_st + g * a.k_sh;
+        uint8_t* rec = (is_v ? a.v_pool + blk * a.vp_sb + g * a.vp_sh : a.k_pool + blk * a.kp_sb + g * a.kp_sh) +
+                       static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
+        const float factor = is_v ? a.v_scale : a.k_scale;
+        const int half = is_v ? 0 : a.half, turned = half / kFp4Group;
+        const bool whole = half % kFp4Group == 0;   // rotated groups have groups as partners
+        int g0 = 2 * j, g1 = 2 * j + 1;
+        const bool pair = whole && j < turned;
+        if (whole) g0 = pair ? j : 2 * turned + 2 * (j - turned), g1 = pair ? j + turned : g0 + 1;
+        float x[16], y[16];
+        load16<kBf16>(src + 16 * g0, x);
+        load16<kBf16>(src + 16 * g1, y);
+        if (pair) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) turn8(row + 16 * g0 + 8 * u, half, x + 8 * u, y + 8 * u);
+        } else if (!whole) {
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {
+                const int e = 32 * j + 8 * u;
+                if (e >= 2 * half) break;
+                const bool second = e >= half;
+                const int k = second ? e - half : e;
+                float o[8];
+                unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(src + (second ? k : e + half))), o);
+                // (four places, so that the elements stay in registers)
+                if (u == 0) second ? turn8(row + k, half, o, x) : turn8(row + k, half, x, o);
+                if (u == 1) second ? turn8(row + k, half, o, x + 8) : turn8(row + k, half, x + 8, o);
+                if (u == 2) second ? turn8(row + k, half, o, y) : turn8(row + k, half, y, o);
+                if (u == 3) second ? turn8(row + k, half, o, y + 8) : turn8(row + k, half, y + 8, o);
+            }
+        }
+        store_group(x, factor, rec, a.d, r, g0);
+        store_group(y, factor, rec, a.d, r, g1);
     }
 }
 
@@ -298,10 +339,10 @@ cudaError_t launch_append_kv_fp4(const sp_append_fp4_shape* s, const uint16_t* q
     a.bs = s->block_size;
     a.k_scale = s->k_scale;
     a.v_scale = s->v_scale;
-    const int heads = a.hq + 2 * a.hk, pairs = a.d / 16, sms = device_sms();
-    a.heads_per = static_cast<int64_t>(a.cap) * pairs * heads >= int64_t(2) * kThreads * kCtas * sms ? 2 : 1;
-    a.groups = (heads + a.heads_per - 1) / a.heads_per;
-    int64_t grid = (static_cast<int64_t>(a.cap) * pairs * a.groups + kThreads - 1) / kThreads;
+    const int pairs = a.d / 16, sms = device_sms();
+    a.heads_per = static_cast<int64_t>(a.cap) * pairs * a.hq >= int64_t(2) * kThreads * kCtas * sms ? 2 : 1;
+    a.groups = (a.hq + a.heads_per - 1) / a.heads_per;
+    int64_t grid = (static_cast<int64_t>(a.cap) * (pairs * a.groups + 2 * a.hk * (a.d / 32)) + kThreads - 1) / kThreads;
     if (grid > int64_t(kCtas) * sms) grid = int64_t(kCtas) * sms;
     auto kern = s->dtype == SP_DTYPE_BF16 ? append_kv_fp4_kernel<true> : append_kv_fp4_kernel<false>;
     return launch_k(kern, static_cast<unsigned>(grid), kThreads, 0, st, a);

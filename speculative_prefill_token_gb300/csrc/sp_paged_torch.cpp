@@ -354,17 +354,25 @@ int call_append_kv_fp4(PyObject* const* a) {
     return sp_append_kv_fp4(&s, q.p, k.p, v.p, slots, at_pos, turn, n_new, qo.p, kp.p, vp.p, status, stream_of(a[13], dev));
 }
 
-// (pool, slots, out, scale, status, stream); out is [rows, Hk, d]
+// (pool, slots, out, scale, status, stream); out is [rows, Hk, d], or without slots
+// [blocks, block_size, Hk, d] with the blocks following one another
 int call_unpack_fp4(PyObject* const* a) {
     const at::Tensor &pt = need(a[0], "pool"), &ot = need(a[2], "out");
     const int dev = device_of(pt, "pool");
     const Pool4 p = pool4(pt, "pool", dev);
     sp_unpack_fp4_shape s = {};
     s.dtype = dtype_code(ot, "out");
-    const Rows out = rows(ot, ot.scalar_type(), "out", dev);
+    const at::Tensor* st = maybe(a[1], "slots");
+    Rows out;
+    if (st) {
+        out = rows(ot, ot.scalar_type(), "out", dev);
+    } else {
+        const Pool o = pool(ot, ot.scalar_type(), "out", dev);
+        if (o.blocks != p.blocks || o.bs != p.bs) refuse("out must hold every row of the pool");
+        out = {o.p, o.blocks * o.bs, o.heads, o.d, o.token, o.head};
+    }
     if (out.heads != p.heads || out.d != p.d) refuse("out and the pool disagree on heads or head_dim");
-    const int32_t* slots = ints(maybe(a[1], "slots"), out.n, "slots", dev);
-    if (!slots && out.n != p.blocks * p.bs) refuse("out must hold every row of the pool");
+    const int32_t* slots = ints(st, out.n, "slots", dev);
     s.n_kv_heads = count(p.heads, "pool");
     s.head_dim = count(p.d, "pool");
     s.block_size = count(p.bs, "pool");

@@ -3,9 +3,10 @@
 // continuations of one prompt share its blocks, kept tokens of a cached prompt
 // move to blocks of their own, ended requests give theirs back).
 //
-// copy_kv_kernel. A warp copies one row of all heads (or, for whole blocks of a
-// 4-bit pool, one head's records) of one pool: it issues up to four 16-byte loads
-// a lane before their stores.
+// copy_kv_kernel. A warp takes up to 32 tasks of one pool: a task is a row of all heads
+// (or, for whole blocks of a 4-bit pool, one head's records). Its lanes look the tasks'
+// places up side by side, and the warp copies four of them at a time, every load issued
+// before the first store.
 //
 // fork_blocks_kernel. With len_i the cached tokens of src_i, full_i = len_i / bs and
 // pre_i the begun blocks of the forks before i,
@@ -16,11 +17,12 @@
 // additions, whose order changes nothing.
 //
 // free_blocks. One kernel takes a holder off every block that a request lets go
-// (shared[id] -= 1, so that a block that nobody holds any more is at -1); a
-// second, one cluster of 8 CTAs, walks the counts in the order of the ids, each
-// CTA a slice, and puts the blocks at -1 behind the free ones. The order of the
-// list is that of the ids, so it does not depend on timing; a count below -1 is a
-// block let go too often, and everything is put back.
+// (shared[id] -= 1, so that a block that nobody holds any more is at -1), leaving
+// requests with lengths out of range alone; a second, one cluster of 8 CTAs, checks all
+// lengths, walks the counts in the order of the ids, each CTA a slice, and puts the
+// blocks at -1 behind the free ones. The order of the list is that of the ids, so it
+// does not depend on timing. After a length out of range, or a count below -1 (a block
+// let go too often), everything is put back.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -43,8 +45,7 @@ __device__ __forceinline__ void raise_status(int32_t* status, int code) {
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyWarps = kCopyThreads / 32;
-constexpr int kCopyCtas = 8;      // of an SM
-constexpr int kCopyUnroll = 4;
+constexpr int kCopyCtas = 4;      // of an SM
 
 struct CopyArgs {
     void* pools[SP_MAX_COPY_POOLS];
@@ -56,19 +57,15 @@ struct CopyArgs {
     int32_t* status;
     int64_t sb, st, sh;
     int pool_blocks, n_pools, entries, rows, bs, hk, d, fp4, B, table_stride;
+    int per_warp;   // tasks of a warp's step
 };
 
-// The last b with off[b] <= i < off[b + 1] of B + 1 offsets, by a whole warp: 32
-// pivots a step.
-__device__ __forceinline__ int request_of(const int32_t* off, int B, int i, int lane) {
-    int lo = 0, hi = B;   // off[lo] <= i (off[0] = 0)
+// The last b of B with off[b] <= i (off[0] = 0).
+__device__ __forceinline__ int request_of(const int32_t* off, int B, int i) {
+    int lo = 0, hi = B;
     while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool below = at < hi && off[at] <= i;
-        const unsigned who = __ballot_sync(0xffffffffu, below);
-        const int last = who ? 31 - __clz(who) : 0;
-        lo += last * step;
-        hi = min(hi, lo + step);
+        const int mid = (lo + hi) >> 1;
+        if (off[mid] <= i) lo = mid; else hi = mid;
     }
     return lo;
 }
@@ -80,7 +77,7 @@ struct Place {
 
 // Where entry i's first row comes from and goes to; false where it copies nothing.
 // (slots stay below 2^31)
-__device__ __forceinline__ bool places_of(const CopyArgs& a, int i, int lane, Place* from, Place* to) {
+__device__ __forceinline__ bool places_of(const CopyArgs& a, int i, Place* from, Place* to) {
     const int s = a.src[i], t = a.dst[i];
     if (s < 0 || t < 0) return false;
     bool ok = true;
@@ -93,70 +90,101 @@ __device__ __forceinline__ bool places_of(const CopyArgs& a, int i, int lane, Pl
         to->block = t / a.bs;
         to->row = t - to->block * a.bs;
         if (a.table) {
-            const int b = request_of(a.src_off, a.B, i, lane);
+            const int b = request_of(a.src_off, a.B, i);
             from->block = k < a.table_stride ? a.table[static_cast<int64_t>(b) * a.table_stride + k] : -1;
             ok = from->block >= 0;
         }
     }
     ok = ok && from->block < a.pool_blocks && to->block < a.pool_blocks;
-    if (!ok && lane == 0) raise_status(a.status, SP_ERR_DEVICE);
+    if (!ok) raise_status(a.status, SP_ERR_DEVICE);
     return ok;
 }
 
-// `n` vectors of 16 bytes by a warp; `at` gives a vector's offset in its row.
+// Copies `count` runs of n vectors of 16 bytes, by a warp; lane r holds where run r
+// comes from and goes to, in bytes into the pool (from -1: nothing), and `at` gives a
+// vector's offset in its run. Four vectors of a lane are in flight.
 template <typename F>
-__device__ __forceinline__ void copy_vectors(const uint8_t* from, uint8_t* to, int n, int lane, F at) {
-    for (int v0 = lane; v0 < n; v0 += 32 * kCopyUnroll) {
-        uint4 x[kCopyUnroll];
+__device__ __forceinline__ void copy_runs(uint8_t* pool, int64_t in, int64_t out, int count, int n, int lane, F at) {
+    constexpr int kAhead = 4;
+    // (vector v of run r is number r * n + v: short runs share a step)
+    const int all = count * n;
+    for (int v0 = 0; v0 < all; v0 += 32 * kAhead) {
+        uint4 x[kAhead];
+        int64_t to[kAhead];
+        bool live[kAhead];
 #pragma unroll
-        for (int u = 0; u < kCopyUnroll; ++u)
-            if (v0 + 32 * u < n) x[u] = __ldcs(reinterpret_cast<const uint4*>(from + at(v0 + 32 * u)));
+        for (int u = 0; u < kAhead; ++u) {
+            const int v = min(v0 + 32 * u + lane, all - 1), r = v / n;
+            const int64_t o = at(v - r * n), from = __shfl_sync(0xffffffffu, in, r);
+            to[u] = __shfl_sync(0xffffffffu, out, r) + o;
+            live[u] = v0 + 32 * u + lane < all && from >= 0;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (live[u]) x[u] = __ldcs(reinterpret_cast<const uint4*>(pool + from + o));
+        }
 #pragma unroll
-        for (int u = 0; u < kCopyUnroll; ++u)
-            if (v0 + 32 * u < n) *reinterpret_cast<uint4*>(to + at(v0 + 32 * u)) = x[u];
+        for (int u = 0; u < kAhead; ++u)
+            if (live[u]) *reinterpret_cast<uint4*>(pool + to[u]) = x[u];
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads, kCopyCtas / 2) copy_kv_kernel(const __grid_constant__ CopyArgs a) {
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kv_kernel(const __grid_constant__ CopyArgs a) {
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31;
     int64_t n = a.entries;
     if (a.table) n = min(n, static_cast<int64_t>(max(a.src_off[a.B], 0)));
     if (a.n_used) n = min(n, static_cast<int64_t>(max(*a.n_used, 0)));
-    // parts of an entry: its rows, or the heads of a 4-bit block
-    const int parts = a.fp4 && a.rows > 1 ? a.hk : a.rows;
-    const int64_t per_pool = n * parts, total = per_pool * a.n_pools;
-    for (int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); w < total;
+    // tasks of an entry: its rows, or the heads of a 4-bit block
+    const bool records = a.fp4 && a.rows > 1;
+    const int parts = records ? a.hk : a.rows;
+    const int64_t tasks = n * parts, steps = (tasks + a.per_warp - 1) / a.per_warp;   // of a pool
+    for (int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); w < steps * a.n_pools;
          w += static_cast<int64_t>(gridDim.x) * kCopyWarps) {
-        const int pool = static_cast<int>(w / per_pool);
-        const int64_t rest = w - pool * per_pool;
-        const int i = static_cast<int>(rest / parts), part = static_cast<int>(rest - static_cast<int64_t>(i) * parts);
-        Place from, to;
-        if (!places_of(a, i, lane, &from, &to)) continue;
-        const uint8_t* x = static_cast<const uint8_t*>(a.pools[pool]) + from.block * a.sb;
-        uint8_t* y = static_cast<uint8_t*>(a.pools[pool]) + to.block * a.sb;
+        const int p = static_cast<int>(w / steps);
+        const int64_t task = (w - p * steps) * a.per_warp + lane;
+        const bool mine = lane < a.per_warp && task < tasks;
+        const int i = mine ? static_cast<int>(task / parts) : 0, part = static_cast<int>(task - static_cast<int64_t>(i) * parts);
+        Place from = {0, 0}, to = {0, 0};
+        const bool live = mine && places_of(a, i, &from, &to);
+        uint8_t* pool = static_cast<uint8_t*>(a.pools[p]);
+        int64_t in, out;
         if (!a.fp4) {
-            const int per_head = a.d / 8;
-            x += (from.row + part) * a.st;
-            y += (to.row + part) * a.st;
-            if (a.sh == 2 * a.d) copy_vectors(x, y, a.hk * per_head, lane, [](int v) { return static_cast<int64_t>(v) * 16; });
-            else copy_vectors(x, y, a.hk * per_head, lane, [&](int v) { return v / per_head * a.sh + v % per_head * 16; });
-        } else if (a.rows > 1) {
-            copy_vectors(x + part * a.sh, y + part * a.sh, a.bs / kFp4Rows * (fp4_record(a.d) / 16), lane,
-                         [](int v) { return static_cast<int64_t>(v) * 16; });
+            in = from.block * a.sb + (from.row + part) * a.st;
+            out = to.block * a.sb + (to.row + part) * a.st;
+        } else if (records) {
+            in = from.block * a.sb + part * a.sh;
+            out = to.block * a.sb + part * a.sh;
         } else {
-            // a token: d / 2 bytes of codes and d / 16 of scales for each head, in words
-            const int r0 = from.row % kFp4Rows, r1 = to.row % kFp4Rows;
-            x += from.row / kFp4Rows * fp4_record(a.d);
-            y += to.row / kFp4Rows * fp4_record(a.d);
-            const int codes = a.d / 8, words = codes + a.d / 64;   // of a head
+            in = from.block * a.sb + from.row / kFp4Rows * fp4_record(a.d);
+            out = to.block * a.sb + to.row / kFp4Rows * fp4_record(a.d);
+        }
+        if (!a.fp4 || records) {
+            if (!live) in = -1;
+            const int count = static_cast<int>(min(static_cast<int64_t>(a.per_warp), tasks - (w - p * steps) * a.per_warp));
+            const int per_head = a.d / 8;
+            if (records)
+                copy_runs(pool, in, out, count, a.bs / kFp4Rows * (fp4_record(a.d) / 16), lane, [](int v) { return static_cast<int64_t>(v) * 16; });
+            else if (a.sh == 2 * a.d || a.hk == 1)
+                copy_runs(pool, in, out, count, a.hk * per_head, lane, [](int v) { return static_cast<int64_t>(v) * 16; });
+            else
+                copy_runs(pool, in, out, count, a.hk * per_head, lane, [&](int v) { return v / per_head * a.sh + v % per_head * 16; });
+            continue;
+        }
+        // tokens of a 4-bit pool: d / 2 bytes of codes and d / 16 of scales for each head, in words
+        const int codes = a.d / 8, words = codes + a.d / 64;   // of a head
+        const int r_in = from.row % kFp4Rows, r_out = to.row % kFp4Rows;
+        for (unsigned who = __ballot_sync(0xffffffffu, live); who; who &= who - 1) {
+            const int t = __ffs(who) - 1;
+            const uint8_t* x = pool + __shfl_sync(0xffffffffu, in, t);
+            uint8_t* y = pool + __shfl_sync(0xffffffffu, out, t);
+            const int r0 = __shfl_sync(0xffffffffu, r_in, t), r1 = __shfl_sync(0xffffffffu, r_out, t);
+#pragma unroll 2
             for (int v = lane; v < a.hk * words; v += 32) {
                 const int h = v / words, u = v - h * words;
                 const bool c = u < codes;
-                const int in = c ? 4 * u : fp4_codes(a.d) + 4 * (u - codes), row = c ? a.d / 2 : a.d / 16;
-                *reinterpret_cast<uint32_t*>(y + h * a.sh + in + r1 * row) =
-                    *reinterpret_cast<const uint32_t*>(x + h * a.sh + in + r0 * row);
+                const int off = c ? 4 * u : fp4_codes(a.d) + 4 * (u - codes), row = c ? a.d / 2 : a.d / 16;
+                *reinterpret_cast<uint32_t*>(y + h * a.sh + off + r1 * row) =
+                    *reinterpret_cast<const uint32_t*>(x + h * a.sh + off + r0 * row);
             }
         }
     }
@@ -201,19 +229,34 @@ __global__ void __launch_bounds__(kForkThreads) fork_blocks_kernel(const PageArg
     const int n_free = *a.n_free;
     __syncthreads();
     bool ok = n_free >= 0 && n_free <= a.free_cap;
-    for (int i = tid; i < a.F; i += kForkThreads) {
-        const int s = a.src[i], t = a.dst[i];
-        int n = -1;
-        if (s >= 0) {
-            if (s >= a.B || t < 0 || t >= a.B) {
+    constexpr int kAhead = 4;   // entries of a thread whose reads are under way together
+    for (int i0 = tid; i0 < a.F; i0 += kAhead * kForkThreads) {
+        int s[kAhead], t[kAhead], n[kAhead], held[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kForkThreads;
+            s[u] = i < a.F ? a.src[i] : -1;
+            t[u] = i < a.F ? a.dst[i] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            n[u] = -1, held[u] = 0;
+            if (s[u] < 0) continue;
+            if (s[u] >= a.B || t[u] < 0 || t[u] >= a.B) {
                 ok = false;
             } else {
-                n = a.ctx_len[s];
-                if (n < 0 || blocks_for(n, a.bs) > a.table_stride || a.ctx_len[t] != 0) ok = false;
-                if (atomicOr(taken + t / 32, 1u << (t % 32)) >> (t % 32) & 1) ok = false;   // a row forked into twice
+                n[u] = a.ctx_len[s[u]];
+                held[u] = a.ctx_len[t[u]];
             }
         }
-        len[i] = n;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + u * kForkThreads;
+            if (i < a.F) len[i] = n[u];
+            if (s[u] < 0 || s[u] >= a.B || t[u] < 0 || t[u] >= a.B) continue;
+            if (n[u] < 0 || blocks_for(n[u], a.bs) > a.table_stride || held[u] != 0) ok = false;
+            if (atomicOr(taken + t[u] / 32, 1u << (t[u] % 32)) >> (t[u] % 32) & 1) ok = false;   // a row forked into twice
+        }
     }
     ok = __syncthreads_and(ok);
     // (a row that is forked from and into)
@@ -299,16 +342,9 @@ constexpr int kSweepThreads = 1024;
 constexpr int kSweepCtas = 8;     // one cluster
 constexpr int kSweepPer = 4 * kSweepThreads;   // counts of a step: 4 a thread
 
-// Whether every length is in range (by the whole block; both kernels take the
-// same way).
-__device__ __forceinline__ bool lengths_fit(const PageArgs& a) {
-    const int n_free = *a.n_free;
-    bool ok = n_free >= 0 && n_free <= a.free_cap;
-    for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-        const int ctx = a.ctx_len[b], left = a.new_len[b];
-        ok = ok && left >= 0 && left <= ctx && blocks_for(ctx, a.bs) <= a.table_stride;
-    }
-    return __syncthreads_and(ok);
+// Whether a request may be cut like this.
+__device__ __forceinline__ bool cut_fits(const PageArgs& a, int ctx, int left) {
+    return left >= 0 && left <= ctx && blocks_for(ctx, a.bs) <= a.table_stride;
 }
 
 // Adds `by` to the count of every block that a request lets go: runs of kRun
@@ -318,7 +354,9 @@ __device__ __forceinline__ void count_drops(const PageArgs& a, int by, int64_t w
     const int64_t units = static_cast<int64_t>(a.B) * runs;
     for (int64_t u = w; u < units; u += warps) {
         const int b = static_cast<int>(u / runs), k0 = static_cast<int>(u - static_cast<int64_t>(b) * runs) * kRun;
-        const int keep = blocks_for(a.new_len[b], a.bs), held = blocks_for(a.ctx_len[b], a.bs);
+        const int ctx = a.ctx_len[b], left = a.new_len[b];
+        if (!cut_fits(a, ctx, left)) continue;
+        const int keep = blocks_for(left, a.bs), held = blocks_for(ctx, a.bs);
         if (k0 >= held || k0 + kRun <= keep) continue;
         const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
         int id[kRun / 32];
@@ -340,7 +378,6 @@ __device__ __forceinline__ void count_drops(const PageArgs& a, int by, int64_t w
 __global__ void __launch_bounds__(kDropThreads) drop_blocks_kernel(const PageArgs a) {
     grid_dep_wait();
     grid_dep_launch();
-    if (!lengths_fit(a)) return;
     count_drops(a, -1, static_cast<int64_t>(blockIdx.x) * (kDropThreads / 32) + (threadIdx.x >> 5),
                 static_cast<int64_t>(gridDim.x) * (kDropThreads / 32), a.status);
 }
@@ -358,20 +395,21 @@ __device__ __forceinline__ int4 counts_at(const PageArgs& a, int64_t i) {
 __global__ void __cluster_dims__(kSweepCtas, 1, 1) __launch_bounds__(kSweepThreads) sweep_blocks_kernel(const PageArgs a) {
     namespace cg = cooperative_groups;
     __shared__ int sums[32];
-    __shared__ int told[2];     // blocks freed in the CTA's slice; a count below -1
+    __shared__ int told[2];     // blocks freed in the CTA's slice; something is wrong there
     const cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
     grid_dep_wait();
     grid_dep_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const bool fit = lengths_fit(a);
     const int n_free = *a.n_free;
+    bool low = n_free < 0 || n_free > a.free_cap;   // something is wrong
+    for (int b = rank * kSweepThreads + tid; b < a.B; b += kSweepCtas * kSweepThreads)
+        low |= !cut_fits(a, a.ctx_len[b], a.new_len[b]);
     // a slice of whole steps for each CTA
     const int64_t steps = (static_cast<int64_t>(a.pool_blocks) + kSweepPer - 1) / kSweepPer;
     const int64_t first = steps * rank / kSweepCtas, last = steps * (rank + 1) / kSweepCtas;
     int freed = 0;
-    bool low = false;
-    for (int64_t s = first; s < last && fit; ++s) {
+    for (int64_t s = first; s < last; ++s) {
         const int4 v = counts_at(a, s * kSweepPer + 4 * tid);
         freed += (v.x == -1) + (v.y == -1) + (v.z == -1) + (v.w == -1);
         low |= min(min(v.x, v.y), min(v.z, v.w)) < -1;
@@ -388,7 +426,7 @@ __global__ void __cluster_dims__(kSweepCtas, 1, 1) __launch_bounds__(kSweepThrea
     }
     cluster.sync();
     int64_t base = n_free, total = 0;
-    bool bad = !fit;
+    bool bad = false;
     for (int k = 0; k < kSweepCtas; ++k) {
         const int* o = cluster.map_shared_rank(told, k);
         if (k < rank) base += o[0];
@@ -406,7 +444,7 @@ __global__ void __cluster_dims__(kSweepCtas, 1, 1) __launch_bounds__(kSweepThrea
         else if (!room) raise_status(a.status, SP_ERR_CAPACITY);
     }
     if (!go) {   // every holder back
-        if (fit) count_drops(a, 1, static_cast<int64_t>(rank) * 32 + warp, int64_t(32) * kSweepCtas, nullptr);
+        count_drops(a, 1, static_cast<int64_t>(rank) * 32 + warp, int64_t(32) * kSweepCtas, nullptr);
         return;
     }
     if (told[0] == 0) return;
@@ -466,9 +504,12 @@ cudaError_t launch_copy_kv(const sp_copy_shape* s, void* const* pools, const int
     a.fp4 = s->fp4;
     a.B = s->n_seqs;
     a.table_stride = s->table_stride;
-    const int64_t parts = a.fp4 && a.rows > 1 ? a.hk : a.rows;
-    int64_t grid = (static_cast<int64_t>(a.entries) * parts * a.n_pools + kCopyWarps - 1) / kCopyWarps;
-    const int64_t most = int64_t(kCopyCtas) * device_sms();
+    // as many tasks a step as leave every warp of the GPU one
+    const int64_t tasks = static_cast<int64_t>(a.entries) * (a.fp4 && a.rows > 1 ? a.hk : a.rows);
+    const int64_t most = int64_t(kCopyCtas) * device_sms(), per = tasks * a.n_pools / (most * kCopyWarps);
+    a.per_warp = static_cast<int>(per < 1 ? 1 : per > 32 ? 32 : per);
+    const int64_t steps = (tasks + a.per_warp - 1) / a.per_warp * a.n_pools;
+    int64_t grid = (steps + kCopyWarps - 1) / kCopyWarps;
     if (grid > most) grid = most;
     return launch_k(copy_kv_kernel, static_cast<unsigned>(grid), kCopyThreads, 0, st, a);
 }

@@ -51,19 +51,21 @@ def unpack_fp4(pool, dtype=None, slots=None, scale: float = 1.0, out=None, statu
     block_size, Hk, d] as specprefill_score_kv and paged_attention take a pool, or
     those at ``slots`` (int32, device; -1 gives zeros), [T, Hk, d]. ``scale`` is
     the pool's factor."""
-    import torch
     if out is None:
         if pool.dim() != 4:
             raise ValueError("pool must be a 4-bit pool (make_pool_fp4)")
         blocks, hk, groups, width = pool.shape
         shape = (blocks, groups * 8, hk, width * 2 // 9) if slots is None else (slots.numel(), hk, width * 2 // 9)
-        out = _new(shape, dtype or torch.bfloat16, pool, stream)
-    # (a view, so that the rows are written in place)
-    rows = out.view(-1, *out.shape[2:]) if slots is None else out
-    rc = (paged._side or torch_side()).unpack_fp4(pool, slots, rows, scale, status, _handle(stream))
+        out = _new(shape, dtype or _bfloat16(), pool, stream)
+    rc = (paged._side or torch_side()).unpack_fp4(pool, slots, out, scale, status, _handle(stream))
     if rc:
         _check(rc, "sp_unpack_fp4")
     return out
+
+
+def _bfloat16():
+    import torch
+    return torch.bfloat16
 
 
 def _dense(kv_tokens, k_pool):
