@@ -45,7 +45,7 @@ __device__ __forceinline__ void raise_status(int32_t* status, int code) {
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyWarps = kCopyThreads / 32;
-constexpr int kCopyCtas = 4;      // of an SM
+constexpr int kCopyCtas = 5;      // of an SM
 
 struct CopyArgs {
     void* pools[SP_MAX_COPY_POOLS];

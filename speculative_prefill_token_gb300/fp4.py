@@ -51,21 +51,33 @@ def unpack_fp4(pool, dtype=None, slots=None, scale: float = 1.0, out=None, statu
     block_size, Hk, d] as specprefill_score_kv and paged_attention take a pool, or
     those at ``slots`` (int32, device; -1 gives zeros), [T, Hk, d]. ``scale`` is
     the pool's factor."""
+    side = paged._side or torch_side()
+    if out is None and stream is None:
+        out = side.new_unpack_fp4(pool, slots, _is_half(dtype), scale, status)
+        if isinstance(out, int):
+            _check(out, "sp_unpack_fp4")
+        return out
     if out is None:
         if pool.dim() != 4:
             raise ValueError("pool must be a 4-bit pool (make_pool_fp4)")
         blocks, hk, groups, width = pool.shape
         shape = (blocks, groups * 8, hk, width * 2 // 9) if slots is None else (slots.numel(), hk, width * 2 // 9)
-        out = _new(shape, dtype or _bfloat16(), pool, stream)
-    rc = (paged._side or torch_side()).unpack_fp4(pool, slots, out, scale, status, _handle(stream))
+        import torch
+        out = _new(shape, torch.float16 if _is_half(dtype) else torch.bfloat16, pool, stream)
+    rc = side.unpack_fp4(pool, slots, out, scale, status, _handle(stream))
     if rc:
         _check(rc, "sp_unpack_fp4")
     return out
 
 
-def _bfloat16():
-    import torch
-    return torch.bfloat16
+_HALF = {"None": False, "torch.bfloat16": False, "torch.float16": True}
+
+
+def _is_half(dtype):
+    try:
+        return _HALF[str(dtype)]
+    except KeyError:
+        raise ValueError("dtype must be bfloat16 or float16") from None
 
 
 def _dense(kv_tokens, k_pool):
