@@ -620,7 +620,7 @@ typedef struct sp_append_fp4_shape {
     int64_t q_stride_token, q_stride_head, qo_stride_token, qo_stride_head;
     int64_t k_stride_token, k_stride_head, v_stride_token, v_stride_head;
     int64_t kp_stride_block, kp_stride_head, vp_stride_block, vp_stride_head;
-    float k_scale, v_scale;  /* factors of the pools, finite and > 0 */
+    float k_scale, v_scale;  /* factors of the pools, from 2^-60 to 2^60 */
 } sp_append_fp4_shape;
 
 /* sp_append_kv into pools of 4 bits. Queries are rotated as there; a row x of
@@ -687,7 +687,7 @@ typedef struct sp_fp4_params {
     int32_t causal;        /* as in sp_attn_params */
     int32_t window;
     float scale;           /* logit scale; 0 selects 1/sqrt(head_dim) */
-    float k_scale;         /* factors of the pools, finite and > 0 */
+    float k_scale;         /* factors of the pools, from 2^-60 to 2^60 */
     float v_scale;
     int32_t spin_limit;    /* polls before a device wait gives up; <= 0 selects the default */
 } sp_fp4_params;

@@ -44,7 +44,8 @@ int to_status(cudaError_t e) { return e == cudaSuccess ? SP_OK : SP_ERR_CUDA; }
 
 bool fp4_head_dim(int d) { return d == 64 || d == 128 || d == 256; }
 bool fp4_block_size(int bs) { return bs == 8 || bs == 16 || bs == 32 || bs == 64 || (bs > 0 && bs % 128 == 0); }
-bool factor(float f) { return std::isfinite(f) && f > 0.0f; }
+// (a NaN is in no range)
+bool factor(float f) { return f >= 0x1p-60f && f <= 0x1p60f; }
 bool is_type(int dtype) { return dtype == SP_DTYPE_BF16 || dtype == SP_DTYPE_F16; }
 
 // An axis whose entries are at least `width` apart, in steps of `step`: a stride

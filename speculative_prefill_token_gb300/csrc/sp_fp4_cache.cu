@@ -31,7 +31,6 @@ namespace sp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kCtas = 3;   // resident CTAs of an SM and the grid's
 
 __device__ __forceinline__ void raise_status(int32_t* status, int code) {
     if (status) atomicMax(status, code);
@@ -126,10 +125,16 @@ __device__ __forceinline__ uint2 encode(const float (&x)[16], uint32_t* scale_by
 
 // A group of a row to its record, its pool's factor taken out.
 __device__ __forceinline__ void store_group(float (&x)[16], float factor, uint8_t* rec, int d, int r, int group) {
-    // (a division by 1 changes nothing)
+    // (a division by 1 changes nothing; quotients as above: factors lie between 2^-60 and
+    // 2^60, and a quotient that overflows gives no number, which is as good as an
+    // infinity here)
     if (factor != 1.0f) {
+        const float inv = __frcp_rn(factor);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = __fdiv_rn(x[i], factor);
+        for (int i = 0; i < 16; ++i) {
+            const float q = __fmul_rn(x[i], inv);
+            x[i] = copysignf(__fmaf_rn(__fmaf_rn(-q, factor, x[i]), inv, q), x[i]);
+        }
     }
     uint32_t byte;
     const uint2 codes = encode(x, &byte);
@@ -157,8 +162,14 @@ __device__ __forceinline__ void load16(const uint16_t* p, float (&x)[16]) {
         unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(p) + u), *reinterpret_cast<float(*)[8]>(x + 8 * u));
 }
 
-template <bool kBf16>
-__global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const AppArgs a) {
+// Which rows a launch takes. Many tokens go in two launches, queries and then keys and
+// values: a thread of a query row needs 64 registers, one that encodes 80, and the
+// queries' stream wants more warps than those leave room for.
+enum Part { kAllRows, kQueryRows, kCacheRows };
+constexpr int ctas_of(Part part) { return part == kQueryRows ? 4 : 3; }   // resident, of an SM
+
+template <bool kBf16, Part kPart>
+__global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel(const AppArgs a) {
     grid_dep_wait();
     grid_dep_launch();
     int64_t n = a.cap;
@@ -168,14 +179,20 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const Ap
     }
     // threads of a token: those of the queries, then of the keys, then of the values
     const int pairs = a.d / 16, halves = a.d / 32;
-    const int of_q = pairs * a.groups, of_k = a.hk * halves, per_token = of_q + 2 * of_k;
+    const int of_q = kPart == kCacheRows ? 0 : pairs * a.groups, of_k = kPart == kQueryRows ? 0 : a.hk * halves;
+    const int per_token = of_q + 2 * of_k;
     const int64_t total = n * per_token;
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; w < total;
          w += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t t = w / per_token;
-        const int rest = static_cast<int>(w - t * per_token);
+        // (keys and values of a token take other ways through the code: where they are many,
+        // those of all tokens follow one another)
+        const bool late = kPart == kCacheRows && w >= n * of_k;
+        const int64_t v = late ? w - n * of_k : w;
+        const int of_t = kPart == kCacheRows ? of_k : per_token;
+        const int64_t t = v / of_t;
+        const int rest = static_cast<int>(v - t * of_t) + (late ? of_k : 0);
         const float* row = nullptr;
-        const int64_t slot = a.slot_map[t];
+        const int64_t slot = kPart == kQueryRows ? -1 : a.slot_map[t];
         if (slot >= a.pool_tokens && rest == 0) raise_status(a.status, SP_ERR_DEVICE);
         if (a.half) {
             const int64_t pos = a.positions[t];
@@ -185,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const Ap
             }
             row = a.cos_sin + pos * 2 * a.half;
         }
-        if (rest < of_q) {
+        if (kPart != kCacheRows && rest < of_q) {
             // vectors (e0, e1) in elements: a rotated pair, or two neighbours behind it
             const int group = rest / pairs, i = rest - group * pairs;
             const bool turn = i < a.half / 8;
@@ -214,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_kv_fp4_kernel(const Ap
             }
             continue;
         }
-        if (slot < 0 || slot >= a.pool_tokens) continue;
+        if (kPart == kQueryRows || slot < 0 || slot >= a.pool_tokens) continue;
         const bool is_v = rest >= of_q + of_k;
         const int unit = rest - of_q - (is_v ? of_k : 0), g = unit / halves, j = unit - g * halves;
         const uint32_t at = static_cast<uint32_t>(slot), blk = at / static_cast<uint32_t>(a.bs);
@@ -339,13 +356,24 @@ cudaError_t launch_append_kv_fp4(const sp_append_fp4_shape* s, const uint16_t* q
     a.bs = s->block_size;
     a.k_scale = s->k_scale;
     a.v_scale = s->v_scale;
-    const int pairs = a.d / 16, sms = device_sms();
-    a.heads_per = static_cast<int64_t>(a.cap) * pairs * a.hq >= int64_t(2) * kThreads * kCtas * sms ? 2 : 1;
+    const bool bf16 = s->dtype == SP_DTYPE_BF16;
+    const int pairs = a.d / 16;
+    const int64_t of_q = static_cast<int64_t>(a.cap) * pairs * a.hq, of_kv = static_cast<int64_t>(a.cap) * 2 * a.hk * (a.d / 32);
+    const int sms = device_sms();
+    auto launch = [&](Part part, int64_t work, void (*kern)(const AppArgs)) {
+        const int64_t most = int64_t(ctas_of(part)) * sms, need = (work + kThreads - 1) / kThreads;
+        return launch_k(kern, static_cast<unsigned>(need < most ? need : most), kThreads, 0, st, a);
+    };
+    // two heads a thread and two launches once either fills the GPU
+    const bool many = of_q / 2 >= int64_t(kThreads) * ctas_of(kQueryRows) * sms;
+    a.heads_per = many ? 2 : 1;
     a.groups = (a.hq + a.heads_per - 1) / a.heads_per;
-    int64_t grid = (static_cast<int64_t>(a.cap) * (pairs * a.groups + 2 * a.hk * (a.d / 32)) + kThreads - 1) / kThreads;
-    if (grid > int64_t(kCtas) * sms) grid = int64_t(kCtas) * sms;
-    auto kern = s->dtype == SP_DTYPE_BF16 ? append_kv_fp4_kernel<true> : append_kv_fp4_kernel<false>;
-    return launch_k(kern, static_cast<unsigned>(grid), kThreads, 0, st, a);
+    const int64_t units = static_cast<int64_t>(a.cap) * pairs * a.groups;
+    if (!many)
+        return launch(kAllRows, units + of_kv, bf16 ? append_kv_fp4_kernel<true, kAllRows> : append_kv_fp4_kernel<false, kAllRows>);
+    const cudaError_t e = launch(kQueryRows, units, bf16 ? append_kv_fp4_kernel<true, kQueryRows> : append_kv_fp4_kernel<false, kQueryRows>);
+    if (e != cudaSuccess) return e;
+    return launch(kCacheRows, of_kv, bf16 ? append_kv_fp4_kernel<true, kCacheRows> : append_kv_fp4_kernel<false, kCacheRows>);
 }
 
 cudaError_t launch_unpack_fp4(const sp_unpack_fp4_shape* s, const uint8_t* pool, const int32_t* slots, uint16_t* out,
