@@ -625,7 +625,7 @@ typedef struct sp_append_fp4_shape {
 
 /* sp_append_kv into pools of 4 bits. Queries are rotated as there; a row x of
  * a rotated key (in 32 bits, not rounded before) or of a value is stored as
- *   y = x / factor,   s_g = max(e4m3(min(max |y_g| / 6, 448)), 2^-9),
+ *   y = x (1 / factor),   s_g = max(e4m3(min(max |y_g| / 6, 448)), 2^-9),
  *   code_i = e2m1(y_i / s_g)   for each group g of 16 neighbours,
  * every operation in 32 bits and rounded to nearest, e4m3() and e2m1() to the
  * nearest number with ties to even, e2m1 saturating at 6. A group that holds

@@ -32,7 +32,7 @@ def encode(x, factor=1.0):
     """(codes, scale bytes) of fp32 rows [..., d]: codes [..., d] with bit 3 the
     sign, scales [..., d / 16]."""
     x = np.asarray(x, dtype=np.float32)
-    y = (x / np.float32(factor)).reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
+    y = (x * (np.float32(1) / np.float32(factor))).reshape(*x.shape[:-1], x.shape[-1] // 16, 16)
     with np.errstate(invalid="ignore"):
         top = np.abs(y).max(-1)
         bad = ~np.isfinite(y).all(-1)

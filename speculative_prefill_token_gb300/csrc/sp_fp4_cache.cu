@@ -85,7 +85,7 @@ struct AppArgs {
     int64_t pool_tokens;
     int cap, hq, hk, d, half, max_pos, bs;
     int heads_per, groups;  // heads walked by one thread, and groups of them
-    float k_scale, v_scale;
+    float k_inverse, v_inverse;   // of the pools' factors
 };
 
 // cos and sin of 8 neighbouring elements.
@@ -124,18 +124,9 @@ __device__ __forceinline__ uint2 encode(const float (&x)[16], uint32_t* scale_by
 }
 
 // A group of a row to its record, its pool's factor taken out.
-__device__ __forceinline__ void store_group(float (&x)[16], float factor, uint8_t* rec, int d, int r, int group) {
-    // (a division by 1 changes nothing; quotients as above: factors lie between 2^-60 and
-    // 2^60, and a quotient that overflows gives no number, which is as good as an
-    // infinity here)
-    if (factor != 1.0f) {
-        const float inv = __frcp_rn(factor);
+__device__ __forceinline__ void store_group(float (&x)[16], float inverse, uint8_t* rec, int d, int r, int group) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float q = __fmul_rn(x[i], inv);
-            x[i] = copysignf(__fmaf_rn(__fmaf_rn(-q, factor, x[i]), inv, q), x[i]);
-        }
-    }
+    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], inverse);
     uint32_t byte;
     const uint2 codes = encode(x, &byte);
     *reinterpret_cast<uint2*>(rec + r * (d / 2) + 8 * group) = codes;
@@ -239,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel
         const uint16_t* src = is_v ? a.v + t * a.v_st + g * a.v_sh : a.k + t * a.k_st + g * a.k_sh;
         uint8_t* rec = (is_v ? a.v_pool + blk * a.vp_sb + g * a.vp_sh : a.k_pool + blk * a.kp_sb + g * a.kp_sh) +
                        static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
-        const float factor = is_v ? a.v_scale : a.k_scale;
+        const float inverse = is_v ? a.v_inverse : a.k_inverse;
         const int half = is_v ? 0 : a.half, turned = half / kFp4Group;
         const bool whole = half % kFp4Group == 0;   // rotated groups have groups as partners
         int g0 = 2 * j, g1 = 2 * j + 1;
@@ -267,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel
                 if (u == 3) second ? turn8(row + k, half, o, y + 8) : turn8(row + k, half, y + 8, o);
             }
         }
-        store_group(x, factor, rec, a.d, r, g0);
-        store_group(y, factor, rec, a.d, r, g1);
+        store_group(x, inverse, rec, a.d, r, g0);
+        store_group(y, inverse, rec, a.d, r, g1);
     }
 }
 
@@ -354,8 +345,8 @@ cudaError_t launch_append_kv_fp4(const sp_append_fp4_shape* s, const uint16_t* q
     a.half = s->rotary_dim / 2;
     a.max_pos = s->max_pos;
     a.bs = s->block_size;
-    a.k_scale = s->k_scale;
-    a.v_scale = s->v_scale;
+    a.k_inverse = 1.0f / s->k_scale;
+    a.v_inverse = 1.0f / s->v_scale;
     const bool bf16 = s->dtype == SP_DTYPE_BF16;
     const int pairs = a.d / 16;
     const int64_t of_q = static_cast<int64_t>(a.cap) * pairs * a.hq, of_kv = static_cast<int64_t>(a.cap) * 2 * a.hk * (a.d / 32);
