@@ -192,6 +192,8 @@ def load(path: Optional[str] = None):
         fn.argtypes = args
         fn.restype = i32
     paged._bind(lib_)
+    fp4._bind(lib_)
+    pages._bind(lib_)
     lib_.sp_status_string.argtypes = [i32]
     lib_.sp_status_string.restype = ctypes.c_char_p
     lib_.sp_build_info.argtypes = []

@@ -16,9 +16,55 @@ Forward only: no gradient is recorded, and tensors are written without moving
 their version counters.
 """
 
+import ctypes
+
 from . import _check, lib
 from . import paged
 from .paged import _handle, _new, torch_side
+
+
+class _AppendShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_tokens", "n_q_heads", "n_kv_heads", "head_dim", "rotary_dim",
+                                               "max_pos", "dtype", "block_size")]
+                + [(n, ctypes.c_int64) for n in (
+                    "pool_blocks", "q_stride_token", "q_stride_head", "qo_stride_token", "qo_stride_head",
+                    "k_stride_token", "k_stride_head", "v_stride_token", "v_stride_head", "kp_stride_block",
+                    "kp_stride_head", "vp_stride_block", "vp_stride_head")]
+                + [("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)])
+
+
+class _UnpackShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_kv_heads", "head_dim", "block_size", "dtype")]
+                + [(n, ctypes.c_int64) for n in ("pool_blocks", "stride_block", "stride_head", "n_rows",
+                                                 "o_stride_token", "o_stride_head")]
+                + [("scale", ctypes.c_float), ("reserved", ctypes.c_int32)])
+
+
+class _Shape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_seqs", "n_q_heads", "n_kv_heads", "head_dim", "dtype",
+                                               "block_size", "table_stride", "n_tokens", "max_new", "reserved")]
+                + [(n, ctypes.c_int64) for n in (
+                    "dense_tokens", "pool_blocks", "q_stride_token", "q_stride_head", "o_stride_token",
+                    "o_stride_head", "k_stride_block", "k_stride_head", "v_stride_block", "v_stride_head")])
+
+
+class _Params(ctypes.Structure):
+    _fields_ = [("causal", ctypes.c_int32), ("window", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float), ("spin_limit", ctypes.c_int32)]
+
+
+def _bind(lib_):
+    P, SZ, ref = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER
+    sigs = {
+        "sp_append_kv_fp4": [ref(_AppendShape)] + [P] * 12,
+        "sp_unpack_fp4": [ref(_UnpackShape)] + [P] * 5,
+        "sp_paged_attention_fp4_workspace": [ref(_Shape), ref(SZ)],
+        "sp_paged_attention_fp4": [ref(_Shape), ref(_Params)] + [P] * 9 + [SZ, P],
+    }
+    for name, args in sigs.items():
+        fn = getattr(lib_, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int
 
 
 def make_pool_fp4(num_blocks: int, block_size: int, n_kv_heads: int, head_dim: int, device="cuda"):
@@ -33,10 +79,10 @@ def make_pool_fp4(num_blocks: int, block_size: int, n_kv_heads: int, head_dim: i
 def append_kv_fp4(k, v, slot_map, k_pool, v_pool, q=None, q_out=None, positions=None, cos_sin=None, n_new=None,
                   k_scale: float = 1.0, v_scale: float = 1.0, status=None, stream=None):
     """append_kv into 4-bit pools: keys (rotated in 32 bits) and values are
-    divided by the pools' factors and stored; queries as there. The largest of 16
-    neighbours is stored as 6 times their scale, which reaches from 2^-9 to 448:
-    factors that bring the rows to between 0.1 and 1000 keep all of its bits. A
-    group with an infinity or NaN reads back as NaN."""
+    stored without the pools' factors (from 2^-60 to 2^60); queries as there. The
+    largest of 16 neighbours is stored as 6 times their scale, which reaches from
+    2^-9 to 448: factors that bring it to between 0.1 and 2,688 keep all of the
+    scale's bits. A group with an infinity or NaN reads back as NaN."""
     if q is not None and q_out is None:
         q_out = _new(q.shape, q.dtype, q, stream)
     rc = (paged._side or torch_side()).append_kv_fp4(k, v, slot_map, k_pool, v_pool, q, q_out, positions, cos_sin,

@@ -17,9 +17,35 @@ has a row for each prompt, empty before):
   copy_kv(pools, out.kept_pos, slots, block_table=table, src_off=out.kept_off, n=out.n_kept)
 """
 
+import ctypes
+
 from . import _check
 from . import paged
 from .paged import _handle, _new, torch_side
+
+
+class _CopyShape(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int32) for n in ("n_pools", "n_entries", "rows", "block_size", "n_kv_heads",
+                                               "head_dim", "fp4", "n_seqs", "table_stride", "reserved")]
+                + [(n, ctypes.c_int64) for n in ("pool_blocks", "stride_block", "stride_token", "stride_head")])
+
+
+class _PagesShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_forks", "block_size", "table_stride", "pool_blocks",
+                                              "free_capacity")]
+
+
+def _bind(lib_):
+    P, ref = ctypes.c_void_p, ctypes.POINTER
+    sigs = {
+        "sp_copy_kv": [ref(_CopyShape), ref(P)] + [P] * 7,
+        "sp_fork_blocks": [ref(_PagesShape)] + [P] * 13,
+        "sp_free_blocks": [ref(_PagesShape)] + [P] * 10,
+    }
+    for name, args in sigs.items():
+        fn = getattr(lib_, name)
+        fn.argtypes = args
+        fn.restype = ctypes.c_int
 
 
 def copy_kv(pools, src, dst, rows: int = 1, block_table=None, src_off=None, n=None, status=None, stream=None):

@@ -1,0 +1,160 @@
+"""The operators as they are used together: prompts scored, their kept tokens
+stored in 4 bits, decoded, forked, compacted and freed, with the lengths on the
+device."""
+
+import numpy as np
+import pytest
+
+from oracle import fp4_oracle, paged_oracle
+from synth import get_workload, make_inputs
+from tests.fp4_cases import check_attention, dev
+from tests.gpu_helpers import to_device
+from tests.paged_cases import host
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(*v):
+    return dev(np.array(v, dtype=np.int32))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_score_store_decode_fork_and_free(cuda_lib, captured):
+    import torch
+    sp = cuda_lib
+    w = get_workload("tiny")
+    q, k, off = to_device(make_inputs(w))
+    out = sp.specprefill_score(q, k, off, sp.SelectionParams(**w.selection_kwargs()))
+    n = int(out.n_kept)
+    bs, hq, hk, d, cap, rows = 16, 8, 2, 128, w.lengths[0], 4
+    blocks = 3 * (cap // bs) + 8
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    pools = [sp.make_pool_fp4(blocks, bs, hk, d) for _ in range(2)]
+    table = torch.full((rows, cap // bs + 2), -1, dtype=torch.int32, device="cuda")
+    free, shared = torch.arange(blocks, dtype=torch.int32, device="cuda"), torch.zeros(blocks, dtype=torch.int32, device="cuda")
+    ctx, n_free, status = i32(0, 0, 0, 0), i32(blocks), i32(0)
+    angle = torch.arange(cap + 8, device="cuda")[:, None] * 1e4 ** (-torch.arange(d // 2, device="cuda") * 2.0 / d)
+    turn = torch.cat([angle.cos(), angle.sin()], 1).contiguous()
+    # the kept tokens of the prompt, request 0 (the others have none)
+    qkv = torch.randn(cap, hq + 2 * hk, d, device="cuda", generator=gen).bfloat16()
+    new_off = torch.cat([out.kept_off, out.kept_off[-1:].expand(rows - 1)]).contiguous()
+    slots, kv, left = sp.block_tables(ctx, new_off, free, n_free, table, bs, n_tokens=cap, status=status)
+    qr = sp.append_kv_fp4(qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, *pools, q=qkv[:, :hq], positions=out.kept_pos,
+                          cos_sin=turn, n_new=out.n_kept, k_scale=0.5, v_scale=0.25, status=status)
+    ws = sp.make_attention_fp4_workspace(qr, rows, pools[0])
+    o = sp.paged_attention_fp4(qr, new_off, kv, table, *pools, k_scale=0.5, v_scale=0.25, ws=ws)
+
+    def reference(q, off, kv):
+        k, v = (fp4_oracle.values(host(p), f) for p, f in zip(pools, (0.5, 0.25)))
+        return paged_oracle.paged_attention(host(q), host(off), host(kv), host(table), np.nan_to_num(k), np.nan_to_num(v))
+
+    check_attention(o, None, reference(qr, new_off, kv), host(kv), d, "bf16", n, 30.0)
+    # the keys are what the definition makes of the rotated rows
+    codes, scales = fp4_oracle.encode(fp4_oracle.rotate32(host(qkv[:n, hq:hq + hk]).astype(np.float32), host(out.kept_pos)[:n],
+                                                          host(turn).astype(np.float32)), 0.5)
+    at = host(slots)[:n]
+    got = fp4_oracle.unpack(host(pools[0]))
+    assert np.array_equal(got[0][at // bs, at % bs], codes) and np.array_equal(got[1][at // bs, at % bs], scales)
+    # three continuations
+    kv, cs, cd, left = sp.fork_blocks(i32(0, 0, 0), i32(2, 1, 3), kv, table, shared, free, left, bs, status=status)
+    sp.copy_kv(pools, cs, cd, rows=bs, status=status)
+    assert int(status) == 0 and host(kv).tolist() == [n] * 4
+    # decode steps of all four, each with tokens of its own
+    one = i32(0, 1, 2, 3, 4)
+    s = dict(ctx=kv.clone(), n_free=left.clone(), slots=i32(0, 0, 0, 0), kv=i32(0, 0, 0, 0), left=i32(0),
+             qkv=torch.zeros(rows, hq + 2 * hk, d, dtype=torch.bfloat16, device="cuda"), pos=i32(0, 0, 0, 0))
+    outs = dict(q=torch.zeros(rows, hq, d, dtype=torch.bfloat16, device="cuda"),
+                o=torch.zeros(rows, hq, d, dtype=torch.bfloat16, device="cuda"))
+    ws1 = sp.make_attention_fp4_workspace(outs["q"], rows, pools[0], max_new=1)
+
+    def step():
+        sp.block_tables(s["ctx"], one, free, s["n_free"], table, bs, slot_map=s["slots"], kv_len=s["kv"], n_left=s["left"],
+                        status=status)
+        sp.append_kv_fp4(s["qkv"][:, hq:hq + hk], s["qkv"][:, hq + hk:], s["slots"], *pools, q=s["qkv"][:, :hq],
+                         q_out=outs["q"], positions=s["pos"], cos_sin=turn, k_scale=0.5, v_scale=0.25, status=status)
+        sp.paged_attention_fp4(outs["q"], one, s["kv"], table, *pools, k_scale=0.5, v_scale=0.25, out=outs["o"], max_new=1, ws=ws1)
+        s["ctx"].copy_(torch.where(status == 0, s["kv"], s["ctx"]))
+        s["n_free"].copy_(torch.where(status == 0, s["left"], s["n_free"]))
+
+    run = step
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        run = graph.replay
+    for i in range(20):
+        s["qkv"].copy_(torch.randn(rows, hq + 2 * hk, d, device="cuda", generator=gen).bfloat16())
+        s["pos"].fill_(cap - 20 + i)
+        run()
+        check_attention(outs["o"], None, reference(outs["q"], one, s["kv"]), host(s["kv"]), d, "bf16", rows, 30.0)
+    assert int(status) == 0 and sp.device_status(ws1) == 0 and host(s["ctx"]).tolist() == [n + 20] * 4
+    # every second cached token of request 1 moves to blocks of its own, in 4 bits; the old row is freed
+    keep = torch.arange(0, n + 20, 2, dtype=torch.int32, device="cuda")
+    m = keep.numel()
+    table2 = torch.full((1, table.shape[1]), -1, dtype=torch.int32, device="cuda")
+    slots2, kv2, left = sp.block_tables(i32(0), i32(0, m), free, s["n_free"], table2, bs, n_tokens=m, status=status)
+    sp.copy_kv(pools, keep, slots2, block_table=table[1:2], src_off=i32(0, m), status=status)
+    both = host(sp.unpack_fp4(pools[1], slots=slots2))
+    row = host(table)[1]
+    old = (row[host(keep) // bs] * bs + host(keep) % bs).astype(np.int32)
+    assert np.array_equal(both, host(sp.unpack_fp4(pools[1], slots=dev(old))))
+    ctx2, left = sp.free_blocks(s["ctx"], i32(n + 20, 0, n + 20, 0), table, shared, free, left, bs, status=status)
+    ctx2, left = sp.free_blocks(ctx2, i32(0, 0, 0, 0), table, shared, free, left, bs, status=status)
+    ctx2, left = sp.free_blocks(kv2, i32(0), table2, shared, free, left, bs, status=status)
+    assert int(status) == 0 and int(left) == blocks and not shared.any()
+    assert sorted(host(free).tolist()) == list(range(blocks))
+
+
+def test_scoring_over_keys_read_back(cuda_lib):
+    """A draft's cache in 4 bits: its keys read back are scored like any 16-bit cache."""
+    import torch
+    sp = cuda_lib
+    w = get_workload("tiny")
+    q, k, off = to_device(make_inputs(w))
+    bs, n = 16, w.lengths[0]
+    hk, d = w.n_kv_heads, w.head_dim
+    p = sp.SelectionParams(**w.selection_kwargs())
+    table = torch.randperm(n // bs, device="cuda").to(torch.int32)[None].contiguous()
+    slot = (table[0].long().repeat_interleave(bs) * bs + torch.arange(bs, device="cuda").repeat(n // bs)).to(torch.int32)
+    layers, dense = [], []
+    for layer in range(k.shape[0]):
+        pools = [sp.make_pool_fp4(n // bs, bs, hk, d) for _ in range(2)]
+        rows = k[layer].view(torch.bfloat16)
+        sp.append_kv_fp4(rows, rows, slot, *pools)
+        layers.append(sp.unpack_fp4(pools[0]))
+        dense.append(sp.unpack_fp4(pools[0], slots=slot))
+    a = sp.specprefill_score_kv(q, layers, off, n, p, block_table=table)
+    b = sp.specprefill_score(q, torch.stack(dense).view(torch.int16), off, p)
+    assert torch.equal(a.imp, b.imp) and int(a.n_kept) == int(b.n_kept)
+
+
+def test_calls_on_two_streams(cuda_lib):
+    """Two steps at once, a workspace each."""
+    import torch
+    from tests.fp4_cases import fp4_case
+    sp = cuda_lib
+    cases = [fp4_case(i, [5000 + i, 40], [1, 1], 8, 2, 128, 16, "bf16") for i in range(2)]
+    args = [(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"]) for c in cases]
+    want = [sp.paged_attention_fp4(*a) for a in args]
+    ws = [sp.make_attention_fp4_workspace(c["q"], 2, c["k_pool"]) for c in cases]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(sp.paged_attention_fp4(*args[i], ws=ws[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
+
+
+def test_a_small_workspace_is_refused(cuda_lib):
+    from tests.fp4_cases import fp4_case
+    sp = cuda_lib
+    c = fp4_case(3, [50], [300], 8, 2, 64, 16, "bf16")
+    ws = sp.make_attention_fp4_workspace(c["q"], 1, c["k_pool"], max_new=1)
+    with pytest.raises(sp.SpecPrefillError):
+        sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"], ws=ws)
+    with pytest.raises(ValueError):
+        sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"][:, :1], ws=ws)
+    with pytest.raises(ValueError):
+        sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"], max_new=0, ws=ws)
