@@ -686,7 +686,8 @@ typedef struct sp_fp4_shape {
 typedef struct sp_fp4_params {
     int32_t causal;        /* as in sp_attn_params */
     int32_t window;
-    float scale;           /* logit scale; 0 selects 1/sqrt(head_dim) */
+    float scale;           /* logit scale; 0 selects 1/sqrt(head_dim). scale * k_scale lies between
+                              2^-126 and 2^126 */
     float k_scale;         /* factors of the pools, from 2^-60 to 2^60 */
     float v_scale;
     int32_t spin_limit;    /* polls before a device wait gives up; <= 0 selects the default */

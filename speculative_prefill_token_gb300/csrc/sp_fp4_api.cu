@@ -179,6 +179,8 @@ int sp_paged_attention_fp4(const sp_fp4_shape* shape, const sp_fp4_params* param
         (params->window > 0 && !params->causal) || !(std::isfinite(params->scale) && params->scale >= 0.0f) ||
         !factor(params->k_scale) || !factor(params->v_scale))
         return SP_ERR_INVALID_ARG;
+    const double logit = params->scale * static_cast<double>(params->k_scale);
+    if (params->scale > 0.0f && (logit < 0x1p-126 || logit > 0x1p126)) return SP_ERR_INVALID_ARG;
     if (!all_aligned({q, k_pool, v_pool, out}, 16) || !all_aligned({q_off, kv_len, block_table, lse}, 4) ||
         shared({out, lse}, {q_off, kv_len, block_table, q, k_pool, v_pool, ws}))
         return SP_ERR_INVALID_ARG;

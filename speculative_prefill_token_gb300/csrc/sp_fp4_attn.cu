@@ -145,8 +145,10 @@ __device__ __forceinline__ Span span_of(const Args& a, int nq, int kv, int rows)
     return s;
 }
 
-__device__ __forceinline__ bool bad_request(const Args& a, int64_t lo, int64_t hi, int64_t kv) {
-    return hi < lo || hi > a.cap || hi - lo > a.max_new || kv < 0 || kv > kMaxCached ||
+// (of Args or DenseArgs, with its rows of q)
+template <typename A>
+__device__ __forceinline__ bool bad_request(const A& a, int tokens, int64_t lo, int64_t hi, int64_t kv) {
+    return hi < lo || hi > tokens || hi - lo > a.max_new || kv < 0 || kv > kMaxCached ||
            (kv + a.bs - 1) / a.bs > a.table_stride;
 }
 
@@ -162,7 +164,7 @@ __device__ __forceinline__ int64_t plan_requests(const Args& a, int rows, int64_
         int64_t n = 0;
         if (b < a.B) {
             const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], kv = a.kv_len[b];
-            if (bad_request(a, lo, hi, kv)) bad = 1;
+            if (bad_request(a, a.cap, lo, hi, kv)) bad = 1;
             else if (!a.dense || a.dense[b] < 0) {
                 const Span s = span_of(a, static_cast<int>(hi - lo), static_cast<int>(kv), rows);
                 n = static_cast<int64_t>(a.hk) * s.row_tiles * (s.tiles + kItemCost);
@@ -271,7 +273,7 @@ __device__ __forceinline__ void warp_plan(const Args& a, int rows, Start* range,
     for (int i = 0; i < 2; ++i) {
         const int b = lane + 32 * i;
         if (b >= a.B) continue;
-        bad |= bad_request(a, q0[i], nq[i], kv[i]) || (b == 0 && q0[i] != 0);
+        bad |= bad_request(a, a.cap, q0[i], nq[i], kv[i]) || (b == 0 && q0[i] != 0);
         nq[i] -= q0[i];
         if (bad || (a.dense && a.dense[b] >= 0)) continue;
         const Span s = span_of(a, nq[i], kv[i], rows);
@@ -1191,7 +1193,7 @@ struct DenseArgs {
     int2* owner;           // [cap] request and table column of a block
     int32_t* used;         // blocks in use
     int64_t k_sb, k_sh, v_sb, v_sh, pool_blocks;
-    int B, hk, G, d, bs, table_stride, width, max_new, window, cap;
+    int B, hk, G, d, bs, table_stride, width, tokens, max_new, window, cap;
 };
 
 // Which requests are read through 16 bits, and where their copies lie: those of
@@ -1205,14 +1207,14 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const Dens
     if (tid == 0) most = 0;
     auto first_of = [&](int nq, int kv) { return a.window > 0 ? max(0, kv - nq - a.window + 1) / kDenseBlock : 0; };
     int64_t blocks = 0;
+    int bad = tid == 0 ? a.q_off[0] != 0 : 0;   // (told by the kernels that follow)
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int64_t n = 0;
         if (b < a.B) {
-            // (lengths that are out of range are told by the kernels that follow)
-            const int64_t nq = static_cast<int64_t>(a.q_off[b + 1]) - a.q_off[b], kv = a.kv_len[b];
-            if (nq * a.G >= dense_rows(a.d) && nq <= a.max_new && kv > 0 && kv <= static_cast<int64_t>(a.width) * kDenseBlock &&
-                (kv + a.bs - 1) / a.bs <= a.table_stride)
+            const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], nq = hi - lo, kv = a.kv_len[b];
+            if (bad_request(a, a.tokens, lo, hi, kv)) bad = 1;
+            else if (nq * a.G >= dense_rows(a.d) && kv > 0 && kv <= static_cast<int64_t>(a.width) * kDenseBlock)
                 n = (kv + kDenseBlock - 1) / kDenseBlock - first_of(static_cast<int>(nq), static_cast<int>(kv));
         }
         int64_t total;
@@ -1221,7 +1223,11 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const Dens
         if (n > 0 && at + n <= a.cap) atomicMax(&most, static_cast<int>(at + n));
         blocks += total;
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) {   // nothing is computed
+        for (int b = tid; b < a.B; b += kPlanThreads) a.base[b] = -1;
+        if (tid == 0) *a.used = 0;
+        return;
+    }
     for (int b0 = 32 * warp; b0 < a.B; b0 += kPlanThreads) {
         const int mine = b0 + lane < a.B ? a.base[b0 + lane] : -1;
         for (unsigned who = __ballot_sync(0xffffffffu, mine >= 0); who; who &= who - 1) {
@@ -1454,6 +1460,7 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
         e.bs = a.bs;
         e.table_stride = a.table_stride;
         e.width = l.dense_width;
+        e.tokens = a.cap;
         e.max_new = a.max_new;
         e.window = a.window;
         e.cap = l.dense_cap;

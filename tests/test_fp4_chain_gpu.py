@@ -158,3 +158,63 @@ def test_a_small_workspace_is_refused(cuda_lib):
         sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"][:, :1], ws=ws)
     with pytest.raises(ValueError):
         sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"], max_new=0, ws=ws)
+
+
+@pytest.mark.parametrize("fault", ["max_new", "kv_len", "q_off"])
+def test_a_length_out_of_range_stops_the_chunks_of_the_others(cuda_lib, fault):
+    """Nothing is written, by the kernels over 16 bits neither."""
+    import torch
+    from tests.fp4_cases import fp4_case
+    sp = cuda_lib
+    c = fp4_case(5, [500, 0, 90], [200, 130, 1], 8, 2, 128, 16, "bf16")
+    off, kv = c["q_off"].clone(), c["kv_len"].clone()
+    ws = sp.make_attention_fp4_workspace(c["q"], 3, c["k_pool"], kv_tokens=3000)
+    args = dict(k_scale=1.0, v_scale=1.0, ws=ws)
+    want = sp.paged_attention_fp4(c["q"], off, kv, c["table"], c["k_pool"], c["v_pool"], **args)
+    assert sp.device_status(ws) == 0
+    if fault == "max_new":
+        ws = sp.make_attention_fp4_workspace(c["q"], 3, c["k_pool"], max_new=150, kv_tokens=3000)
+        args.update(ws=ws, max_new=150)
+    elif fault == "kv_len":
+        kv[2] = 16 * c["table"].shape[1] + 1
+    else:
+        off[3] = off[2] - 1
+    out = torch.full_like(want, 7.0)
+    sp.paged_attention_fp4(c["q"], off, kv, c["table"], c["k_pool"], c["v_pool"], out=out, **args)
+    assert sp.device_status(ws) == 6 and (out == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("n,hq,d,rot", [(1300, 32, 128, 128), (5001, 8, 64, 48), (700, 33, 256, 64)])
+def test_many_rows_in_place(cuda_lib, dtype, n, hq, d, rot):
+    """Queries that go in a launch of their own, in place, some rows not in use."""
+    import torch
+    from tests.paged_cases import torch_dtype
+    sp = cuda_lib
+    hk, bs, used = 2, 16, n - 3
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    qkv = torch.randn(n, hq + 2 * hk, d, device="cuda", generator=gen).to(torch_dtype(dtype))
+    turn = torch.randn(64, rot, device="cuda", generator=gen)
+    pos = torch.randint(0, 64, (n,), device="cuda", generator=gen, dtype=torch.int32)
+    blocks = -(-n // bs) + 1
+    slots = torch.randperm(blocks * bs, device="cuda", generator=gen)[:n].to(torch.int32)
+    slots[5] = -1
+    pools = [sp.make_pool_fp4(blocks, bs, hk, d) for _ in range(2)]
+    ref = [torch.zeros(blocks, bs, hk, d, dtype=torch_dtype(dtype), device="cuda") for _ in range(2)]
+    want = sp.append_kv(qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, *ref, q=qkv[:, :hq], positions=pos, cos_sin=turn)
+    before, status = qkv.clone(), i32(0)
+    sp.append_kv_fp4(qkv[:, hq:hq + hk], qkv[:, hq + hk:], slots, *pools, q=qkv[:, :hq], q_out=qkv[:, :hq], positions=pos,
+                     cos_sin=turn, n_new=i32(used), k_scale=0.5, status=status)
+    assert int(status) == 0
+    assert torch.equal(qkv[:used, :hq], want[:used]) and torch.equal(qkv[used:], before[used:])
+    assert torch.equal(qkv[:, hq:], before[:, hq:])
+    x = host(before)
+    rows = [fp4_oracle.rotate32(x[:, hq:hq + hk].astype(np.float32), host(pos), host(turn)), x[:, hq + hk:].astype(np.float32)]
+    at = host(slots)
+    live = (np.arange(n) < used) & (at >= 0)
+    for pool, row, factor in zip(pools, rows, (0.5, 1.0)):
+        codes, scales = fp4_oracle.encode(row[live], factor)
+        full = [np.zeros((blocks * bs, hk, d), dtype=np.uint8), np.zeros((blocks * bs, hk, d // 16), dtype=np.uint8)]
+        full[0][at[live]], full[1][at[live]] = codes, scales
+        want_pool = fp4_oracle.pack(full[0].reshape(blocks, bs, hk, d), full[1].reshape(blocks, bs, hk, d // 16))
+        assert np.array_equal(host(pool), want_pool)

@@ -110,7 +110,8 @@ def test_attention_refusals(lib):
                dict(dense_tokens=1 << 31), dict(k_stride_block=1 << 33)):
         assert _attend(lib, kw) == 2, kw
     for kw in (dict(causal=2), dict(window=-1), dict(causal=0, window=4), dict(scale=-1.0), dict(scale=float("nan")),
-               dict(k_scale=0.0), dict(v_scale=float("inf")), dict(k_scale=2.0 ** 70)):
+               dict(k_scale=0.0), dict(v_scale=float("inf")), dict(k_scale=2.0 ** 70), dict(scale=2.0 ** -100, k_scale=2.0 ** -60),
+               dict(scale=2.0 ** 100, k_scale=2.0 ** 60)):
         assert _attend(lib, params=kw) == 1, kw
     for name in ("q_off", "kv_len", "table", "q", "k_pool", "v_pool", "out"):
         assert _attend(lib, **{name: None}) == 1, name
