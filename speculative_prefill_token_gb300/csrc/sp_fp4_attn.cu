@@ -149,7 +149,7 @@ __device__ __forceinline__ Span span_of(const Args& a, int nq, int kv, int rows)
 template <typename A>
 __device__ __forceinline__ bool bad_request(const A& a, int tokens, int64_t lo, int64_t hi, int64_t kv) {
     return hi < lo || hi > tokens || hi - lo > a.max_new || kv < 0 || kv > kMaxCached ||
-           (kv + a.bs - 1) / a.bs > a.table_stride;
+           kv > static_cast<int64_t>(a.table_stride) * a.bs;
 }
 
 // Units before each request, by the block's NT threads; the total, or -1 when a
@@ -198,27 +198,23 @@ __device__ __forceinline__ int64_t ctas_for(const Args& a, int64_t units) {
     return min(static_cast<int64_t>(a.grid), (units + kLeastUnits - 1) / kLeastUnits);
 }
 
-// x / y for x >= 0, y > 0: in 32 bits where both fit.
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
-    if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
-    return x / y;
-}
-
-// The CTA whose range holds unit u of `units`.
-__device__ __forceinline__ int range_owner(int64_t units, int64_t ctas, int64_t u) {
-    return static_cast<int>(quotient((u + 1) * ctas - 1, units));
+// The CTA whose range holds unit u of `units`. (T: int64_t, or uint32_t where units
+// are below 2^24.)
+template <typename T>
+__device__ __forceinline__ int range_owner(T units, T ctas, T u) {
+    return static_cast<int>(((u + 1) * ctas - 1) / units);
 }
 
 // Unit u of `units`, of request b whose units begin at `at`, as a start; a cut inside
 // an item's fixed cost falls on the item's start.
-__device__ __forceinline__ Start make_start(const Args& a, int b, int nq, int kv, int64_t at, int64_t units, int64_t ctas,
-                                            int64_t u, int rows) {
+template <typename T>
+__device__ __forceinline__ Start make_start(const Args& a, int b, int nq, int kv, T at, T units, T ctas, T u, int rows) {
     Start s{b, 0, 0, 0, 1, {0, 0, 0}};
     const Span sp = span_of(a, nq, kv, rows);
-    const int64_t per = sp.tiles + kItemCost;
-    s.gj = static_cast<int32_t>(quotient(u - at, per));
-    const int64_t item = at + s.gj * per;
-    s.off = static_cast<int32_t>(max(u - item - kItemCost, static_cast<int64_t>(0)));
+    const T per = sp.tiles + kItemCost;
+    s.gj = static_cast<int32_t>((u - at) / per);
+    const T item = at + s.gj * per;
+    s.off = max(static_cast<int32_t>(u - item) - kItemCost, 0);
     s.c0 = range_owner(units, ctas, item + kItemCost);
     s.parts = range_owner(units, ctas, item + per - 1) - s.c0 + 1;
     return s;
@@ -235,7 +231,7 @@ __device__ __forceinline__ void find_range(const Args& a, const int64_t* pre, in
     };
     if (t < 2 && c + t >= ctas) tell(t, Start{a.B, 0, 0, 0, 1, {0, 0, 0}});
     if (c >= ctas) return;
-    const int64_t u[2] = {quotient(units * c, ctas), quotient(units * (c + 1), ctas)};
+    const int64_t u[2] = {units * c / ctas, units * (c + 1) / ctas};
     if (a.local_plan) {
         for (int b = t; b < a.B; b += blockDim.x) {
             const int64_t at = pre[b], end = b + 1 < a.B ? pre[b + 1] : units;
@@ -250,15 +246,17 @@ __device__ __forceinline__ void find_range(const Args& a, const int64_t* pre, in
 }
 
 // The same for a batch of at most 64 requests, by one warp, two requests a lane: one
-// read of the lengths and one rendezvous. Costs that leave 24 bits are left to the block:
-// the first start is then of request -1. (A decode step of 16: the first tile's
-// copies begin 5,900 cycles into the kernel by the block's plan, 4,000 by every warp
-// for itself.)
+// read of the lengths and one rendezvous, all in 32 bits. A batch of 2^24 units or more
+// is left to the block: the first start is then of request -1. (A decode step of 16:
+// the first tile's copies begin 5,900 cycles into the kernel by the block's plan, 4,000
+// by every warp for itself.)
 constexpr int kWarpSeqs = 64;
 
 __device__ __forceinline__ void warp_plan(const Args& a, int rows, Start* range, int lane) {
     constexpr unsigned kAll = 0xffffffffu;
-    int q0[2], nq[2] = {0, 0}, kv[2] = {0, 0}, n[2] = {0, 0};
+    const bool two = a.B > 32;
+    int q0[2], nq[2] = {0, 0}, kv[2] = {0, 0};
+    uint32_t n[2] = {0, 0};
     bool bad = false, large = false;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -277,45 +275,53 @@ __device__ __forceinline__ void warp_plan(const Args& a, int rows, Start* range,
         nq[i] -= q0[i];
         if (bad || (a.dense && a.dense[b] >= 0)) continue;
         const Span s = span_of(a, nq[i], kv[i], rows);
-        const int64_t cost = static_cast<int64_t>(a.hk) * s.row_tiles * (s.tiles + kItemCost);
+        // (the first product is below 2^32: max_new Hq is)
+        const int64_t cost = static_cast<int64_t>(static_cast<uint32_t>(a.hk) * static_cast<uint32_t>(s.row_tiles)) * (s.tiles + kItemCost);
         large |= cost >> 24 != 0;
-        n[i] = static_cast<int>(cost);
+        n[i] = static_cast<uint32_t>(cost);
     }
     const bool none = __any_sync(kAll, bad);
     if (none && lane == 0) atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
-    if (!none && __any_sync(kAll, large)) {
-        if (lane == 0) range->b = -1;
-        return;
-    }
-    int pre[2], run = 0;
+    large = __any_sync(kAll, large);
+    uint32_t pre[2] = {0, 0}, run = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        int incl = n[i];
+        if (i && !two) break;
+        uint32_t incl = n[i];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(kAll, incl, o);
+            const uint32_t x = __shfl_up_sync(kAll, incl, o);
             if (lane >= o) incl += x;
         }
         pre[i] = run + incl - n[i];
         run += __shfl_sync(kAll, incl, 31);
     }
-    const int64_t units = none ? 0 : run, ctas = ctas_for(a, units);
+    if (!none && (large || run >> 24 != 0)) {
+        if (lane == 0) range->b = -1;
+        return;
+    }
+    const uint32_t units = none ? 0 : run, ctas = static_cast<uint32_t>(ctas_for(a, units));
     // lanes 0 to 15: this CTA's start; the others: the next one's
-    const int c = blockIdx.x + (lane >> 4);
+    const uint32_t c = blockIdx.x + (lane >> 4);
     Start s{a.B, 0, 0, 0, 1, {0, 0, 0}};
-    const int64_t u = c < ctas ? quotient(units * c, ctas) : 0;
+    const uint32_t u = c < ctas ? units * c / ctas : 0;
     int b = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         // the last request with a cost that begins at or before the unit
-        const int64_t v = __shfl_sync(kAll, u, 16 * h);
-        const unsigned lo = __ballot_sync(kAll, n[0] > 0 && pre[0] <= v), hi = __ballot_sync(kAll, n[1] > 0 && pre[1] <= v);
+        const uint32_t v = __shfl_sync(kAll, u, 16 * h);
+        const unsigned lo = __ballot_sync(kAll, n[0] > 0 && pre[0] <= v);
+        const unsigned hi = two ? __ballot_sync(kAll, n[1] > 0 && pre[1] <= v) : 0u;
         if (lane >> 4 == h) b = hi ? 63 - __clz(hi) : lo ? 31 - __clz(lo) : 0;
     }
-    const int at0 = __shfl_sync(kAll, pre[0], b & 31), at1 = __shfl_sync(kAll, pre[1], b & 31);
-    const int nq0 = __shfl_sync(kAll, nq[0], b & 31), nq1 = __shfl_sync(kAll, nq[1], b & 31);
-    const int kv0 = __shfl_sync(kAll, kv[0], b & 31), kv1 = __shfl_sync(kAll, kv[1], b & 31);
-    if (c < ctas) s = make_start(a, b, b < 32 ? nq0 : nq1, b < 32 ? kv0 : kv1, b < 32 ? at0 : at1, units, ctas, u, rows);
+    uint32_t at = __shfl_sync(kAll, pre[0], b & 31);
+    int my_nq = __shfl_sync(kAll, nq[0], b & 31), my_kv = __shfl_sync(kAll, kv[0], b & 31);
+    if (two) {
+        const uint32_t at1 = __shfl_sync(kAll, pre[1], b & 31);
+        const int nq1 = __shfl_sync(kAll, nq[1], b & 31), kv1 = __shfl_sync(kAll, kv[1], b & 31);
+        if (b >= 32) at = at1, my_nq = nq1, my_kv = kv1;
+    }
+    if (c < ctas) s = make_start<uint32_t>(a, b, my_nq, my_kv, at, units, ctas, u, rows);
     if ((lane & 15) == 0) {
         range[lane >> 4] = s;
         if (lane == 0 || static_cast<int>(blockIdx.x) == a.grid - 1) a.starts[c] = s;
@@ -337,7 +343,7 @@ struct Segment {
 struct Walk {
     const Start* range;     // in shared memory
     int at_b, at_gj, at_off;
-    __device__ __forceinline__ Walk(const Start* r) : range(r), at_b(r->b), at_gj(r->gj), at_off(r->off) {}
+    __device__ __forceinline__ Walk(const Start* r, int b, int gj, int off) : range(r), at_b(b), at_gj(gj), at_off(off) {}
     __device__ __forceinline__ bool next(const Args& a, int tile_rows, Segment& s) {
         const Start &begin = range[0], &end = range[1];
         for (;;) {
@@ -380,6 +386,12 @@ struct Walk {
     }
 };
 
+// A CTA's first segment, and where the walk goes on; at_b < 0: there is none.
+struct alignas(16) First {
+    Segment s;
+    int at_b, at_gj;
+};
+
 // ------------------------------------------------------------ shared memory
 
 // Warps of a CTA: as many as their registers and shares of shared memory allow.
@@ -402,13 +414,14 @@ struct Smem {
     static constexpr uint32_t ring = 0;                   // [kWarps][kHalves]
     static constexpr uint32_t shares = kWarps * kHalves * kHalf;   // [kWarps]
     static constexpr uint32_t range = shares + kWarps * kShare;    // [2] Start
-    static constexpr uint32_t bars = range + 2 * sizeof(Start);    // shares written, shares read
+    static constexpr uint32_t first = range + 2 * sizeof(Start);   // First
+    static constexpr uint32_t bars = first + sizeof(First);        // shares written, shares read
     static constexpr uint32_t seg = bars + 16;                     // [kWarps][3] Segment in work, on its way, to be joined
     static constexpr uint32_t total = seg + 3 * kWarps * sizeof(Segment);
     // the plan, before the first tile
     static constexpr uint32_t sums = 0;
     static constexpr uint32_t pre = 32 * 8;
-    static_assert(pre + 8 * (kLocalSeqs + 1) <= range && total <= 232448, "shared memory of one CTA");
+    static_assert(pre + 8 * (kLocalSeqs + 1) <= range && bars % 16 == 0 && total <= 232448, "shared memory of one CTA");
 };
 
 // ------------------------------------------------------------ loads
@@ -992,6 +1005,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     grid_dep_wait();
     grid_dep_launch();
     Start* range = reinterpret_cast<Start*>(smem + L::range);
+    First* start = reinterpret_cast<First*>(smem + L::first);
     const bool few = a.B <= kWarpSeqs;
     if (few) {
         if (warp == 0) warp_plan(a, L::kRows, range, lane);
@@ -1010,6 +1024,17 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
         find_range(a, pre, units, L::kRows, range);
         __syncthreads();
     }
+    if (warp == 0) {
+        Walk w(range, range->b, range->gj, range->off);
+        Segment t;
+        const bool some = w.next(a, L::kRows, t);
+        if (lane == 0) {
+            if (some) start->s = t;
+            start->at_b = some ? w.at_b : -1;
+            start->at_gj = w.at_gj;
+        }
+    }
+    __syncthreads();
     // (what only the edges and ends of an item need stays out of the registers)
     Segment* seg = reinterpret_cast<Segment*>(smem + L::seg) + 3 * warp;
     float* shares = reinterpret_cast<float*>(smem + L::shares);
@@ -1018,7 +1043,8 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     Worker<D, NT> me;
     me.gid = lane >> 2;
     me.tig = lane & 3;
-    Walk walk(range);
+    const bool some = start->at_b >= 0;
+    Walk walk(range, start->at_b, start->at_gj, 0);
     Segment& s = *seg;
     int n, first, all_lo, all_hi;
     // a segment in work, its queries on their way
@@ -1035,8 +1061,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
         begin(t);
         return true;
     };
-    Segment one;
-    const bool some = walk.next(a, L::kRows, one);
+    const Segment one = start->s;
     Feed<D, NT> feed(a, walk, one, some, seg + 1, warp, lane);
     if (some) begin(one);   // (while the first block id is looked up)
     feed.template issue<false>(a, mine, lane);
