@@ -9,7 +9,7 @@
 // scale and its 8 bytes of codes. (Where half the rotated elements are no whole
 // number of groups, a key's threads read the partners of their neighbours' groups.)
 // Every operation of the stored value is one of 32 bits, rounded as the definition in
-// specprefill.h has it: the division by the scale as r = 1 / s, q = y r, q + (y - q s) r
+// specprefill.h has it: the division by the scale as r = 1 / s, q = y r, q - (q s - y) r
 // with fused operations, which is the rounded quotient (Markstein: r is rounded
 // correctly, and no quotient here overflows; one that underflows is far below the
 // smallest code's border).
@@ -99,11 +99,19 @@ __device__ __forceinline__ void angles(const float* row, int half, float (&c)[8]
     }
 }
 
+// The largest magnitude, or NaN where one of them is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // The codes (8 bytes) and scale of a group of 16 values.
 __device__ __forceinline__ uint2 encode(const float (&x)[16], uint32_t* scale_byte) {
-    uint32_t top = 0;
+    float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < 16; i += 2) most = max_abs3(most, x[i], x[i + 1]);
+    const uint32_t top = __float_as_uint(most);
     if (top >= 0x7f800000u) {   // an infinity or NaN among them
         *scale_byte = kFp4NoNumber;
         return make_uint2(0u, 0u);
@@ -113,9 +121,9 @@ __device__ __forceinline__ uint2 encode(const float (&x)[16], uint32_t* scale_by
     *scale_byte = byte;
     const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(fp8_unpack(byte))));
     const float r = __frcp_rn(s);
-    auto over = [&](float y) {
+    auto over = [&](float y) {   // (the error negated: a zero keeps its sign)
         const float q = __fmul_rn(y, r);
-        return copysignf(__fmaf_rn(__fmaf_rn(-q, s, y), r, q), y);   // (the sign of a zero)
+        return __fmaf_rn(-__fmaf_rn(q, s, -y), r, q);
     };
     uint32_t w[2] = {0u, 0u};
 #pragma unroll
@@ -180,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel
         const bool late = kPart == kCacheRows && w >= n * of_k;
         const int64_t v = late ? w - n * of_k : w;
         const int of_t = kPart == kCacheRows ? of_k : per_token;
-        const int64_t t = v / of_t;
+        const int64_t t = total >> 32 ? v / of_t : static_cast<uint32_t>(v) / static_cast<uint32_t>(of_t);
         const int rest = static_cast<int>(v - t * of_t) + (late ? of_k : 0);
         const float* row = nullptr;
         const int64_t slot = kPart == kQueryRows ? -1 : a.slot_map[t];
