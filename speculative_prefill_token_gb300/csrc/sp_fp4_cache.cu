@@ -14,7 +14,15 @@
 // correctly, and no quotient here overflows; one that underflows is far below the
 // smallest code's border).
 //
-// unpack_fp4_kernel. A thread turns 8 bytes of codes and a scale into 32 bytes.
+// Bound: 39,322 tokens of 16/4 heads of 128 (bf16) are 322 MB of queries and 81 + 23 MB of
+// keys and values; the queries take 54 us (6.0 TB/s, the memory), keys and values 36 us: 17
+// instructions an element and the loads' latency before them (issue slots 55 % busy at 24
+// warps an SM; a thread's elements are under way before its slot and position are known,
+// 93 to 90 us in all; the next row's read ahead as well: no gain). 16 tokens of 8/2 heads of
+// 256: 2.3 us, a launch and three reads that follow one another.
+//
+// unpack_fp4_kernel. A thread turns 8 bytes of codes and a scale into 32 bytes (39,424 rows of 4 heads
+// of 128, 52 MB: 11.7 us, 4.4 TB/s, most of it writes).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -154,18 +162,26 @@ __device__ __forceinline__ void turn8(const float* row, int half, float* x, floa
     }
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void load16(const uint16_t* p, float (&x)[16]) {
+// 16 elements, as they are.
+__device__ __forceinline__ void load16(const uint16_t* p, uint4* raw) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-        unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(p) + u), *reinterpret_cast<float(*)[8]>(x + 8 * u));
+    for (int u = 0; u < 2; ++u) raw[u] = __ldg(reinterpret_cast<const uint4*>(p) + u);
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void unpack16(const uint4* raw, float (&x)[16]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) unpack8<kBf16>(raw[u], *reinterpret_cast<float(*)[8]>(x + 8 * u));
 }
 
 // Which rows a launch takes. Many tokens go in two launches, queries and then keys and
 // values: a thread of a query row needs 64 registers, one that encodes 80, and the
-// queries' stream wants more warps than those leave room for.
+// queries' stream wants more warps than those leave room for (39,322 tokens of 16/4 heads of
+// 128: one launch 103 us, two 96). Few tokens are one wave of blocks: they take the registers
+// that spare them all spills (16 tokens of 8/2 heads of 256: 2.3 us, 2.5 with three blocks
+// an SM; many tokens by two blocks: 97 us, by three 90, by 640 threads an SM 92).
 enum Part { kAllRows, kQueryRows, kCacheRows };
-constexpr int ctas_of(Part part) { return part == kQueryRows ? 4 : 3; }   // resident, of an SM
+constexpr int ctas_of(Part part) { return part == kQueryRows ? 4 : part == kCacheRows ? 3 : 2; }   // resident, of an SM
 
 template <bool kBf16, Part kPart>
 __global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel(const AppArgs a) {
@@ -190,18 +206,32 @@ __global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel
         const int of_t = kPart == kCacheRows ? of_k : per_token;
         const int64_t t = total >> 32 ? v / of_t : static_cast<uint32_t>(v) / static_cast<uint32_t>(of_t);
         const int rest = static_cast<int>(v - t * of_t) + (late ? of_k : 0);
+        const bool is_q = kPart != kCacheRows && rest < of_q;
+        // a key's or value's 32 elements, under way before its slot and position are known
+        const bool is_v = rest >= of_q + of_k;
+        const int unit = rest - of_q - (is_v ? of_k : 0), g = unit / halves, j = unit - g * halves;
+        const int half = is_v ? 0 : a.half, turned = half / kFp4Group;
+        const bool whole = half % kFp4Group == 0;   // rotated groups have groups as partners
+        const bool pair = whole && j < turned;
+        const int g0 = !whole ? 2 * j : pair ? j : 2 * turned + 2 * (j - turned), g1 = pair ? j + turned : g0 + 1;
+        const uint16_t* from = is_v ? a.v + t * a.v_st + g * a.v_sh : a.k + t * a.k_st + g * a.k_sh;
+        uint4 raw[4] = {};
+        if (kPart != kQueryRows && !is_q) {
+            load16(from + 16 * g0, raw);
+            load16(from + 16 * g1, raw + 2);
+        }
         const float* row = nullptr;
         const int64_t slot = kPart == kQueryRows ? -1 : a.slot_map[t];
+        const int64_t pos = a.half ? a.positions[t] : 0;
         if (slot >= a.pool_tokens && rest == 0) raise_status(a.status, SP_ERR_DEVICE);
         if (a.half) {
-            const int64_t pos = a.positions[t];
             if (pos < 0 || pos >= a.max_pos) {
                 if (rest == 0) raise_status(a.status, SP_ERR_DEVICE);
                 continue;
             }
             row = a.cos_sin + pos * 2 * a.half;
         }
-        if (kPart != kCacheRows && rest < of_q) {
+        if (is_q) {
             // vectors (e0, e1) in elements: a rotated pair, or two neighbours behind it
             const int group = rest / pairs, i = rest - group * pairs;
             const bool turn = i < a.half / 8;
@@ -231,22 +261,14 @@ __global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel
             continue;
         }
         if (kPart == kQueryRows || slot < 0 || slot >= a.pool_tokens) continue;
-        const bool is_v = rest >= of_q + of_k;
-        const int unit = rest - of_q - (is_v ? of_k : 0), g = unit / halves, j = unit - g * halves;
         const uint32_t at = static_cast<uint32_t>(slot), blk = at / static_cast<uint32_t>(a.bs);
         const int within = static_cast<int>(at - blk * a.bs), r = within % kFp4Rows;
-        const uint16_t* src = is_v ? a.v + t * a.v_st + g * a.v_sh : a.k + t * a.k_st + g * a.k_sh;
         uint8_t* rec = (is_v ? a.v_pool + blk * a.vp_sb + g * a.vp_sh : a.k_pool + blk * a.kp_sb + g * a.kp_sh) +
                        static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
         const float inverse = is_v ? a.v_inverse : a.k_inverse;
-        const int half = is_v ? 0 : a.half, turned = half / kFp4Group;
-        const bool whole = half % kFp4Group == 0;   // rotated groups have groups as partners
-        int g0 = 2 * j, g1 = 2 * j + 1;
-        const bool pair = whole && j < turned;
-        if (whole) g0 = pair ? j : 2 * turned + 2 * (j - turned), g1 = pair ? j + turned : g0 + 1;
         float x[16], y[16];
-        load16<kBf16>(src + 16 * g0, x);
-        load16<kBf16>(src + 16 * g1, y);
+        unpack16<kBf16>(raw, x);
+        unpack16<kBf16>(raw + 2, y);
         if (pair) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) turn8(row + 16 * g0 + 8 * u, half, x + 8 * u, y + 8 * u);
@@ -258,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, ctas_of(kPart)) append_kv_fp4_kernel
                 const bool second = e >= half;
                 const int k = second ? e - half : e;
                 float o[8];
-                unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(src + (second ? k : e + half))), o);
+                unpack8<kBf16>(__ldg(reinterpret_cast<const uint4*>(from + (second ? k : e + half))), o);
                 // (four places, so that the elements stay in registers)
                 if (u == 0) second ? turn8(row + k, half, o, x) : turn8(row + k, half, x, o);
                 if (u == 1) second ? turn8(row + k, half, o, x + 8) : turn8(row + k, half, x + 8, o);
