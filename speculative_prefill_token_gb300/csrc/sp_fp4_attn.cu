@@ -1218,7 +1218,7 @@ struct DenseArgs {
     int2* owner;           // [cap] request and table column of a block
     int32_t* used;         // blocks in use
     int64_t k_sb, k_sh, v_sb, v_sh, pool_blocks;
-    int B, hk, G, d, bs, table_stride, width, tokens, max_new, window, cap;
+    int B, hk, G, d, bs, bs_shift, table_stride, width, tokens, max_new, window, cap;
 };
 
 // Which requests are read through 16 bits, and where their copies lie: those of
@@ -1272,16 +1272,16 @@ template <bool kBf16>
 __global__ void __launch_bounds__(kDenseThreads) fp4_dense_kernel(const DenseArgs a) {
     grid_dep_wait();
     grid_dep_launch();
-    const int groups = a.d / kFp4Group, units = *a.used * a.hk;
+    const int shift = 31 - __clz(a.d / kFp4Group), groups = 1 << shift, units = *a.used * a.hk;
     const int64_t head = static_cast<int64_t>(a.cap) * kDenseBlock * a.d;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const int blk = u / a.hk, h = u - blk * a.hk;
         const int2 own = a.owner[blk];
         const int kv = a.kv_len[own.x];
         for (int x = threadIdx.x; x < kDenseBlock * groups; x += kDenseThreads) {
-            const int r = x / groups, g = x - r * groups, j = own.y * kDenseBlock + r;
+            const int r = x >> shift, g = x & (groups - 1), j = own.y * kDenseBlock + r;
             if (j >= kv) continue;
-            const int col = j / a.bs, within = j - col * a.bs;
+            const int col = a.bs_shift >= 0 ? j >> a.bs_shift : j / a.bs, within = j - col * a.bs;
             int id = a.table[static_cast<int64_t>(own.x) * a.table_stride + col];
             if (id < 0 || id >= a.pool_blocks) {
                 atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
@@ -1483,6 +1483,7 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
         e.G = a.G;
         e.d = d;
         e.bs = a.bs;
+        e.bs_shift = a.bs_shift;
         e.table_stride = a.table_stride;
         e.width = l.dense_width;
         e.tokens = a.cap;

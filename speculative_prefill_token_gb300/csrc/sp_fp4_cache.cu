@@ -313,14 +313,14 @@ __global__ void __launch_bounds__(kThreads) unpack_fp4_kernel(const UnpackArgs a
     const int64_t total = a.rows * per_row;
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; w < total;
          w += static_cast<int64_t>(gridDim.x) * kThreads) {
-        const int64_t t = w / per_row;
+        const int64_t t = total >> 32 ? w / per_row : static_cast<uint32_t>(w) / static_cast<uint32_t>(per_row);
         const int rest = static_cast<int>(w - t * per_row);
         const int h = rest / groups, i = rest - h * groups;
         const int64_t slot = a.slots ? a.slots[t] : t;
         uint4 x = make_uint4(0, 0, 0, 0), y = x;
         if (slot >= 0 && slot < a.pool_tokens) {
-            const int64_t blk = slot / a.bs;
-            const int within = static_cast<int>(slot - blk * a.bs), r = within % kFp4Rows;
+            const uint32_t at = static_cast<uint32_t>(slot), blk = at / static_cast<uint32_t>(a.bs);
+            const int within = static_cast<int>(at - blk * a.bs), r = within % kFp4Rows;
             const uint8_t* rec = a.pool + blk * a.sb + h * a.sh + static_cast<int64_t>(within / kFp4Rows) * fp4_record(a.d);
             const uint2 codes = __ldg(reinterpret_cast<const uint2*>(rec + r * (a.d / 2) + 8 * i));
             const uint32_t s = fp8_unpack(rec[fp4_codes(a.d) + r * groups + i] * 0x101u);
