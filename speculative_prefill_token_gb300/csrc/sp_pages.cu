@@ -5,8 +5,9 @@
 //
 // copy_kv_kernel. A warp takes up to 32 tasks of one pool: a task is a row of all heads
 // (or, for whole blocks of a 4-bit pool, one head's records). Its lanes look the tasks'
-// places up side by side, and the warp copies four of them at a time, every load issued
-// before the first store.
+// places up side by side, and the warp copies 2 KB of them at a time, every load issued
+// before the first store. Bound by memory: 39,322 rows of 1 KB in two pools, a third of
+// a prompt's, 161 MB, 32.9 us, 4.9 TB/s; rows in order by the same kernel 5.2 TB/s.
 //
 // fork_blocks_kernel. With len_i the cached tokens of src_i, full_i = len_i / bs and
 // pre_i the begun blocks of the forks before i,
@@ -45,7 +46,13 @@ __device__ __forceinline__ void raise_status(int32_t* status, int code) {
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyWarps = kCopyThreads / 32;
-constexpr int kCopyCtas = 5;      // of an SM
+// Resident, of an SM. (Rows of 1 KB 32.9 us by five, 33.7 by four, 33.9 by six; tokens in 4 bits,
+// 288 bytes in four pools, 33.2 us by four, 36.4 by five, 32.0 by three.)
+constexpr int copy_ctas(int tokens) { return tokens ? 4 : 5; }
+// Of a warp's step: what the GPU copies at a time lies close together. (Rows of 1 KB: 12 a
+// step 37.5 us, 8 or 4 32.6, 2 33.8, 1 49.8; of 256 bytes: 32 22.1, 16 18.8, 8 20.3; records of
+// 4.6 KB: 12 63, 4 57, 1 54.)
+constexpr int kStepBytes = 4096;
 
 struct CopyArgs {
     void* pools[SP_MAX_COPY_POOLS];
@@ -127,7 +134,49 @@ __device__ __forceinline__ void copy_runs(uint8_t* pool, int64_t in, int64_t out
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kv_kernel(const __grid_constant__ CopyArgs a) {
+// The same for tokens of a 4-bit pool of head size D: of each head D / 2 bytes of codes, 16
+// a lane, and D / 16 of scales, a lane's. Lane r holds the records of token r and, in
+// `rows`, its rows there.
+template <int D>
+__device__ __forceinline__ void copy_tokens_fp4(uint8_t* pool, int64_t in, int64_t out, int rows, int count, int hk,
+                                                int64_t sh, int lane) {
+    constexpr int kAhead = 4, kCodes = D / 32, kUnits = kCodes + 1, kScales = D / 16;
+    const int n = hk * kUnits, all = count * n;
+    for (int v0 = 0; v0 < all; v0 += 32 * kAhead) {
+        uint4 x[kAhead];
+        int64_t to[kAhead];
+        bool live[kAhead], codes[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int v = min(v0 + 32 * u + lane, all - 1), r = v / n, o = v - r * n, h = o / kUnits, w = o - h * kUnits;
+            const int64_t from = __shfl_sync(0xffffffffu, in, r);
+            const int both = __shfl_sync(0xffffffffu, rows, r);
+            codes[u] = w < kCodes;
+            const int64_t at = h * sh + (codes[u] ? 16 * w : fp4_codes(D));
+            const int row = codes[u] ? D / 2 : D / 16;
+            to[u] = __shfl_sync(0xffffffffu, out, r) + at + (both >> 8) * row;
+            live[u] = v0 + 32 * u + lane < all && from >= 0;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (!live[u]) continue;
+            const uint8_t* src = pool + from + at + (both & 255) * row;
+            if (codes[u] || kScales == 16) x[u] = __ldcs(reinterpret_cast<const uint4*>(src));
+            else if constexpr (kScales == 8) *reinterpret_cast<uint2*>(&x[u]) = __ldcs(reinterpret_cast<const uint2*>(src));
+            else x[u].x = __ldcs(reinterpret_cast<const uint32_t*>(src));
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (!live[u]) continue;
+            uint8_t* dst = pool + to[u];
+            if (codes[u] || kScales == 16) *reinterpret_cast<uint4*>(dst) = x[u];
+            else if constexpr (kScales == 8) *reinterpret_cast<uint2*>(dst) = make_uint2(x[u].x, x[u].y);
+            else *reinterpret_cast<uint32_t*>(dst) = x[u].x;
+        }
+    }
+}
+
+// kTokens: the head size where tokens of 4-bit pools are copied, 0 where runs of bytes.
+template <int kTokens>
+__global__ void __launch_bounds__(kCopyThreads, copy_ctas(kTokens)) copy_kv_kernel(const __grid_constant__ CopyArgs a) {
     grid_dep_wait();
     grid_dep_launch();
     const int lane = threadIdx.x & 31;
@@ -135,7 +184,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kv_kernel(const 
     if (a.table) n = min(n, static_cast<int64_t>(max(a.src_off[a.B], 0)));
     if (a.n_used) n = min(n, static_cast<int64_t>(max(*a.n_used, 0)));
     // tasks of an entry: its rows, or the heads of a 4-bit block
-    const bool records = a.fp4 && a.rows > 1;
+    const bool records = !kTokens && a.fp4;
     const int parts = records ? a.hk : a.rows;
     const int64_t tasks = n * parts, steps = (tasks + a.per_warp - 1) / a.per_warp;   // of a pool
     for (int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5); w < steps * a.n_pools;
@@ -148,7 +197,7 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kv_kernel(const 
         const bool live = mine && places_of(a, i, &from, &to);
         uint8_t* pool = static_cast<uint8_t*>(a.pools[p]);
         int64_t in, out;
-        if (!a.fp4) {
+        if (!kTokens && !a.fp4) {
             in = from.block * a.sb + (from.row + part) * a.st;
             out = to.block * a.sb + (to.row + part) * a.st;
         } else if (records) {
@@ -158,34 +207,17 @@ __global__ void __launch_bounds__(kCopyThreads, kCopyCtas) copy_kv_kernel(const 
             in = from.block * a.sb + from.row / kFp4Rows * fp4_record(a.d);
             out = to.block * a.sb + to.row / kFp4Rows * fp4_record(a.d);
         }
-        if (!a.fp4 || records) {
-            if (!live) in = -1;
-            const int count = static_cast<int>(min(static_cast<int64_t>(a.per_warp), tasks - (w - p * steps) * a.per_warp));
+        if (!live) in = -1;
+        const int count = static_cast<int>(min(static_cast<int64_t>(a.per_warp), tasks - (w - p * steps) * a.per_warp));
+        [[maybe_unused]] auto plain = [](int v) { return static_cast<int64_t>(v) * 16; };
+        if constexpr (kTokens != 0) {
+            copy_tokens_fp4<kTokens>(pool, in, out, from.row % kFp4Rows | to.row % kFp4Rows << 8, count, a.hk, a.sh, lane);
+        } else if (records) {
+            copy_runs(pool, in, out, count, a.bs / kFp4Rows * (fp4_record(a.d) / 16), lane, plain);
+        } else {
             const int per_head = a.d / 8;
-            if (records)
-                copy_runs(pool, in, out, count, a.bs / kFp4Rows * (fp4_record(a.d) / 16), lane, [](int v) { return static_cast<int64_t>(v) * 16; });
-            else if (a.sh == 2 * a.d || a.hk == 1)
-                copy_runs(pool, in, out, count, a.hk * per_head, lane, [](int v) { return static_cast<int64_t>(v) * 16; });
-            else
-                copy_runs(pool, in, out, count, a.hk * per_head, lane, [&](int v) { return v / per_head * a.sh + v % per_head * 16; });
-            continue;
-        }
-        // tokens of a 4-bit pool: d / 2 bytes of codes and d / 16 of scales for each head, in words
-        const int codes = a.d / 8, words = codes + a.d / 64;   // of a head
-        const int r_in = from.row % kFp4Rows, r_out = to.row % kFp4Rows;
-        for (unsigned who = __ballot_sync(0xffffffffu, live); who; who &= who - 1) {
-            const int t = __ffs(who) - 1;
-            const uint8_t* x = pool + __shfl_sync(0xffffffffu, in, t);
-            uint8_t* y = pool + __shfl_sync(0xffffffffu, out, t);
-            const int r0 = __shfl_sync(0xffffffffu, r_in, t), r1 = __shfl_sync(0xffffffffu, r_out, t);
-#pragma unroll 2
-            for (int v = lane; v < a.hk * words; v += 32) {
-                const int h = v / words, u = v - h * words;
-                const bool c = u < codes;
-                const int off = c ? 4 * u : fp4_codes(a.d) + 4 * (u - codes), row = c ? a.d / 2 : a.d / 16;
-                *reinterpret_cast<uint32_t*>(y + h * a.sh + off + r1 * row) =
-                    *reinterpret_cast<const uint32_t*>(x + h * a.sh + off + r0 * row);
-            }
+            if (a.sh == 2 * a.d || a.hk == 1) copy_runs(pool, in, out, count, a.hk * per_head, lane, plain);
+            else copy_runs(pool, in, out, count, a.hk * per_head, lane, [&](int v) { return v / per_head * a.sh + v % per_head * 16; });
         }
     }
 }
@@ -504,14 +536,18 @@ cudaError_t launch_copy_kv(const sp_copy_shape* s, void* const* pools, const int
     a.fp4 = s->fp4;
     a.B = s->n_seqs;
     a.table_stride = s->table_stride;
-    // as many tasks a step as leave every warp of the GPU one
+    // as many tasks a step as leave every warp of the GPU one, and kStepBytes
     const int64_t tasks = static_cast<int64_t>(a.entries) * (a.fp4 && a.rows > 1 ? a.hk : a.rows);
-    const int64_t most = int64_t(kCopyCtas) * device_sms(), per = tasks * a.n_pools / (most * kCopyWarps);
+    const int tokens = a.fp4 && a.rows == 1 ? a.d : 0;
+    const int64_t most = int64_t(copy_ctas(tokens)) * device_sms(), all = tasks * a.n_pools / (most * kCopyWarps);
+    const int64_t bytes = !a.fp4 ? 2 * int64_t(a.hk) * a.d : a.rows > 1 ? a.bs / kFp4Rows * int64_t(fp4_record(a.d)) : a.hk * (9 * int64_t(a.d) / 16);
+    const int64_t few = kStepBytes / bytes, per = all < few ? all : few;
     a.per_warp = static_cast<int>(per < 1 ? 1 : per > 32 ? 32 : per);
     const int64_t steps = (tasks + a.per_warp - 1) / a.per_warp * a.n_pools;
     int64_t grid = (steps + kCopyWarps - 1) / kCopyWarps;
     if (grid > most) grid = most;
-    return launch_k(copy_kv_kernel, static_cast<unsigned>(grid), kCopyThreads, 0, st, a);
+    auto kern = tokens == 0 ? copy_kv_kernel<0> : tokens == 64 ? copy_kv_kernel<64> : tokens == 128 ? copy_kv_kernel<128> : copy_kv_kernel<256>;
+    return launch_k(kern, static_cast<unsigned>(grid), kCopyThreads, 0, st, a);
 }
 
 cudaError_t launch_fork_blocks(const sp_pages_shape* s, const int32_t* src, const int32_t* dst,
