@@ -16,24 +16,36 @@
 // are the transposed weights. The elements of a row are dealt to the lanes so
 // that every lane's codes are consecutive bytes of one load: the sum over the
 // elements, and the order of the result's elements, may be permuted freely.
-// (Operands of tcgen05.mma lie in shared or tensor memory: writing 16-bit values there
-// and reading them again takes 4 of the 3.6 times more bytes than the codes
-// themselves from the shared memory's 128 bytes a cycle, where HBM delivers 23.5
-// bytes of codes a cycle and SM. From registers, mma.sync needs 0.32 of its rate.)
+// (Operands of tcgen05.mma lie in shared or tensor memory: 16-bit values written there
+// and read again are 7 bytes for each byte of codes, 167 a cycle and SM where HBM delivers
+// 23.5 of codes and shared memory moves 128. From registers, mma.sync needs 0.3 of its rate.)
 //
 // Work. The new tokens x the G heads of a KV head are rows; an item is up to
-// 8 or 16 rows of a request and KV head, its unit a tile of 64 keys. All units
+// 8 or 16 rows of a request and KV head, its unit a tile of 64 keys (32 at d = 256). All units
 // of all items are cut into equal contiguous ranges, one for each CTA (one CTA an
-// SM); tile i of the CTA goes to warp i mod 12, which copies it into its own part
-// of shared memory while it works on the one before: no warp waits for another
-// one before the item's end. (One warp that loaded for all by bulk copies: some
-// 120 cycles a copy, two to sixteen of them a tile.) The warps' results are joined at the end of an item, those of CTAs that share
-// an item by another kernel, in their order: results do not depend on timing.
+// SM); tile i of the CTA goes to warp i mod W, which copies it into its own part
+// of shared memory, keys and values in turn, while it works on what came before: no warp
+// waits for another one inside an item. (One warp that loaded for all by bulk copies: some
+// 120 cycles a copy, two to sixteen of them a tile: 174 us in place of 155 with blocks of 64
+// tokens, 455 in place of 207 with blocks of 8.) At an item's end each warp leaves its share in shared memory and
+// goes on; it takes its part of the join when all shares are there. Results of CTAs that share
+// an item are joined by another kernel, in their order: results do not depend on timing.
 //
 // Requests with many rows are bound by the products, not by the cache: their keys
 // and values are written once as 16-bit values into the workspace (exactly), and
 // computed by the attention over a 16-bit cache (sp_attn.cu), on
 // fifth-generation tensor cores, 128 rows at a time.
+//
+// Measured (bf16): 64 requests of 2K to 32K tokens, a token of each, 16/4 heads of 128, 728 MB: 127.5
+// us, 5.7 TB/s, 84 % of a copy's rate; its loads alone 116. Issue slots 56 % busy at 12 warps, ALU and fp16 pipes
+// 47 and 38 %, tensor pipe 27 %, DRAM 69 %: no pipe is full, the rest is the chain convert - multiply
+// - softmax of a warp, of which registers and shared memory hold no more than 12. The same bytes at
+// d = 256 (8 warps) 151 us, at d = 64, half of them, 96. A token of 16 requests of 4K to 16K, 8/2 heads of 256, 86 MB:
+// 35 us, of which 5 are the start (lengths, ranges, table, first tile: reads that follow one
+// another) and 3 the join. One token over 512: 10 us, all of it latency. 8 tokens over 32K, d =
+// 256: 32 us, four items of 8 rows that convert the same codes (16 rows would take 128
+// accumulators a lane, beside 64 registers of queries). 4,096 tokens over 39,322 in all: 0.83 to 0.86
+// ms, of which the copy is 0.03.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -51,9 +63,10 @@
 namespace sp {
 namespace {
 
-// Keys of a tile, the unit of work of a warp.
+// Keys of a tile, the unit of work of a warp. (d = 128: 32 keys 167 us in place of 137; d = 256:
+// 64 do not fit into a warp's registers.)
 __host__ __device__ constexpr int tile_keys(int d) { return d <= 128 ? 64 : 32; }
-constexpr int kItemCost = 16;                // of an item besides its tiles, in tiles
+constexpr int kItemCost = 16;                // of an item besides its tiles, in tiles (64 long decodes 127.8 us; 4: 134.2, 8: 129.7, 24: 128.7)
 constexpr int kLocalSeqs = 1024;             // requests of a plan made by every CTA
 constexpr int kPlanThreads = 1024;
 constexpr int kMaxGrid = 256;
@@ -191,7 +204,9 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_plan_kernel(const Args a, in
     if (threadIdx.x == 0) a.pre[a.B] = units;
 }
 
-// CTAs that share `units`: few of them get less than a tile for every other warp.
+// CTAs that share `units`: few of them get less than a tile for every other warp. (4 tokens
+// over 8K in 4 requests, d = 64: 14.3 us; 16 15.3, 32 17.9. One token over 512: 10.2 us; 2 and 4, where
+// more CTAs share it, 11.0 and 10.9.)
 constexpr int kLeastUnits = 8;
 
 __device__ __forceinline__ int64_t ctas_for(const Args& a, int64_t units) {
@@ -247,9 +262,8 @@ __device__ __forceinline__ void find_range(const Args& a, const int64_t* pre, in
 
 // The same for a batch of at most 64 requests, by one warp, two requests a lane: one
 // read of the lengths and one rendezvous, all in 32 bits. A batch of 2^24 units or more
-// is left to the block: the first start is then of request -1. (A decode step of 16:
-// the first tile's copies begin 5,900 cycles into the kernel by the block's plan, 4,000
-// by every warp for itself.)
+// is left to the block: the first start is then of request -1. (16 decode steps 36.4 to 35.5
+// us against 64-bit quotients, with the first segment worked out by that warp alone.)
 constexpr int kWarpSeqs = 64;
 
 __device__ __forceinline__ void warp_plan(const Args& a, int rows, Start* range, int lane) {
@@ -394,7 +408,8 @@ struct alignas(16) First {
 
 // ------------------------------------------------------------ shared memory
 
-// Warps of a CTA: as many as their registers and shares of shared memory allow.
+// Warps of a CTA: as many as their registers and shares of shared memory allow (d = 128: 12 of 168
+// registers 145 us for 64 long decodes when 16 of 128, which spill, took 151; d = 256: 10 are slower than 8).
 constexpr int warps_of(int d, int nt) { return d * nt == 64 ? 16 : d * nt == 128 ? 12 : 8; }
 
 template <int D, int NT>
