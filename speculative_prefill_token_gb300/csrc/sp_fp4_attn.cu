@@ -410,7 +410,7 @@ struct alignas(16) First {
 
 // Warps of a CTA: as many as their registers and shares of shared memory allow (d = 128: 12 of 168
 // registers 145 us for 64 long decodes when 16 of 128, which spill, took 151; d = 256: 10 are slower than 8).
-constexpr int warps_of(int d, int nt) { return d * nt == 64 ? 16 : d * nt == 128 ? 12 : 8; }
+constexpr int warps_of(int d, int nt) { return d * nt == 64 ? 16 : d * nt == 128 || d == 256 ? 12 : 8; }
 
 template <int D, int NT>
 struct Smem {
@@ -422,7 +422,7 @@ struct Smem {
     static constexpr int kMt = kKeys / 16;                       // products over a tile's keys
     static constexpr uint32_t kHalf = kKeys / kFp4Rows * kRec;   // K or V of a tile
     // halves of a warp in shared memory: one in work, two on their way
-    static constexpr int kHalves = 3;
+    static constexpr int kHalves = D == 256 ? 2 : 3;
     static constexpr int kAcc = D / 16 * NT * 4;          // accumulator registers of a lane
     static constexpr int kVals = kAcc + NT * 4;           // and references and sums
     static constexpr uint32_t kShare = kVals * 32 * 4;    // a warp's share for the join at an item's end
@@ -1106,6 +1106,20 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
             if (owed && __all_sync(0xffffffffu, mbar_test_wait(written, (ends - 1) & 1))) join();
             const int key0 = (first + k) * L::kKeys;
             const bool edge = key0 < all_lo || key0 + L::kKeys > all_hi;
+            if constexpr (L::kHalves == 2) {
+                cp_async_wait<1>();
+                __syncwarp();
+                me.keys(a, s, mine, key0, edge);
+                __syncwarp();
+                feed.template issue<false>(a, mine, lane);
+                cp_async_wait<1>();
+                __syncwarp();
+                me.values(a, s, mine + L::kHalf, key0, edge);
+                __syncwarp();
+                feed.template issue<true>(a, mine + L::kHalf, lane);
+                if (feed.live) feed.next(a, lane);
+                continue;
+            }
             // halves in turn: this tile's keys, its values, the next tile's keys (copied
             // over the values of the tile before)
             const uint32_t k_at = mine + half * L::kHalf;
