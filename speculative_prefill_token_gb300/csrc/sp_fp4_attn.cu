@@ -40,10 +40,10 @@
 // us, 5.7 TB/s, 84 % of a copy's rate; its loads alone 116. Issue slots 56 % busy at 12 warps, ALU and fp16 pipes
 // 47 and 38 %, tensor pipe 27 %, DRAM 69 %: no pipe is full, the rest is the chain convert - multiply
 // - softmax of a warp, of which registers and shared memory hold no more than 12. The same bytes at
-// d = 256 (8 warps) 151 us, at d = 64, half of them, 96. A token of 16 requests of 4K to 16K, 8/2 heads of 256, 86 MB:
-// 35 us, of which 5 are the start (lengths, ranges, table, first tile: reads that follow one
+// d = 256 135 us, at d = 64, half of them, 96. A token of 16 requests of 4K to 16K, 8/2 heads of 256, 86 MB:
+// 33.6 us, of which 5 are the start (lengths, ranges, table, first tile: reads that follow one
 // another) and 3 the join. One token over 512: 10 us, all of it latency. 8 tokens over 32K, d =
-// 256: 32 us, four items of 8 rows that convert the same codes (16 rows would take 128
+// 256: 31 us, four items of 8 rows that convert the same codes (16 rows would take 128
 // accumulators a lane, beside 64 registers of queries). 4,096 tokens over 39,322 in all: 0.83 to 0.86
 // ms, of which the copy is 0.03.
 #include <cuda_bf16.h>
@@ -409,7 +409,7 @@ struct alignas(16) First {
 // ------------------------------------------------------------ shared memory
 
 // Warps of a CTA: as many as their registers and shares of shared memory allow (d = 128: 12 of 168
-// registers 145 us for 64 long decodes when 16 of 128, which spill, took 151; d = 256: 10 are slower than 8).
+// registers 145 us for 64 long decodes when 16 of 128, which spill, took 151).
 constexpr int warps_of(int d, int nt) { return d * nt == 64 ? 16 : d * nt == 128 || d == 256 ? 12 : 8; }
 
 template <int D, int NT>
@@ -421,7 +421,10 @@ struct Smem {
     static constexpr int kKeys = tile_keys(D);
     static constexpr int kMt = kKeys / 16;                       // products over a tile's keys
     static constexpr uint32_t kHalf = kKeys / kFp4Rows * kRec;   // K or V of a tile
-    // halves of a warp in shared memory: one in work, two on their way
+    // Halves of a warp in shared memory: one in work and two on their way, or, at d = 256, the
+    // other one on its way, which leaves room for 12 warps (three halves and 8 warps: 64 long
+    // decodes 151 us in place of 135; at d = 128, where registers hold 12 at most, two halves
+    // 129.1 in place of 127.8, with blocks of 8 tokens 200 in place of 197).
     static constexpr int kHalves = D == 256 ? 2 : 3;
     static constexpr int kAcc = D / 16 * NT * 4;          // accumulator registers of a lane
     static constexpr int kVals = kAcc + NT * 4;           // and references and sums
