@@ -1081,9 +1081,9 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     };
     const Segment one = start->s;
     Feed<D, NT> feed(a, walk, one, some, seg + 1, warp, lane);
-    if (some) begin(one);   // (while the first block id is looked up)
     feed.template issue<false>(a, mine, lane);
     feed.template issue<true>(a, mine + L::kHalf, lane);
+    if (some) begin(one);   // (while they are on their way)
     if (feed.live) feed.next(a, lane);
     int k = warp;       // the warp's next tile in the segment
     uint32_t half = 0;  // and the half that it begins in
