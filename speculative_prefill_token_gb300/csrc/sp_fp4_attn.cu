@@ -346,7 +346,7 @@ __device__ __forceinline__ void warp_plan(const Args& a, int rows, Start* range,
 
 // A CTA's part of one item: rows [row0, row0 + rows) of request b and KV head g
 // over key tiles [first, first + n).
-struct Segment {
+struct alignas(16) Segment {
     int b, g, q0, pos0, kv, row0, rows, first, n;
     int lo, hi;             // cache indices that some row sees
     int all_lo, all_hi;     // and that all rows see
@@ -1024,12 +1024,24 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
     grid_dep_launch();
     Start* range = reinterpret_cast<Start*>(smem + L::range);
     First* start = reinterpret_cast<First*>(smem + L::first);
-    const bool few = a.B <= kWarpSeqs;
-    if (few) {
-        if (warp == 0) warp_plan(a, L::kRows, range, lane);
-        __syncthreads();
+    bool planned = a.B <= kWarpSeqs;
+    if (planned && warp == 0) {
+        warp_plan(a, L::kRows, range, lane);
+        __syncwarp();
     }
-    if (!few || range->b < 0) {
+    for (;;) {
+        if (planned && warp == 0 && range->b >= 0) {
+            Walk w(range, range->b, range->gj, range->off);
+            Segment t;
+            const bool some = w.next(a, L::kRows, t);
+            if (lane == 0) {
+                if (some) start->s = t;
+                start->at_b = some ? w.at_b : -1;
+                start->at_gj = w.at_gj;
+            }
+        }
+        __syncthreads();
+        if (planned && range->b >= 0) break;
         int64_t* pre = reinterpret_cast<int64_t*>(smem + L::pre);
         int64_t units;
         if (a.local_plan) {
@@ -1041,18 +1053,8 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) fp4_attn_kernel(cons
         __syncthreads();   // (the first start is read)
         find_range(a, pre, units, L::kRows, range);
         __syncthreads();
+        planned = true;
     }
-    if (warp == 0) {
-        Walk w(range, range->b, range->gj, range->off);
-        Segment t;
-        const bool some = w.next(a, L::kRows, t);
-        if (lane == 0) {
-            if (some) start->s = t;
-            start->at_b = some ? w.at_b : -1;
-            start->at_gj = w.at_gj;
-        }
-    }
-    __syncthreads();
     // (what only the edges and ends of an item need stays out of the registers)
     Segment* seg = reinterpret_cast<Segment*>(smem + L::seg) + 3 * warp;
     float* shares = reinterpret_cast<float*>(smem + L::shares);
