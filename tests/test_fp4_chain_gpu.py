@@ -218,3 +218,76 @@ def test_many_rows_in_place(cuda_lib, dtype, n, hq, d, rot):
         full[0][at[live]], full[1][at[live]] = codes, scales
         want_pool = fp4_oracle.pack(full[0].reshape(blocks, bs, hk, d), full[1].reshape(blocks, bs, hk, d // 16))
         assert np.array_equal(host(pool), want_pool)
+
+
+def test_pools_of_more_than_32_bits(cuda_lib):
+    """Every operator on the last blocks of pools of 5 GB, decode steps and a chunk through 16 bits."""
+    import torch
+    sp = cuda_lib
+    bs, d, hk, blocks = 128, 128, 4, 140000
+    pools = [torch.zeros(blocks, hk, bs // 8, 9 * d // 2, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    assert pools[0].numel() > 1 << 32
+    n = 300
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    qkv = torch.randn(n, 12, d, device="cuda", generator=gen).bfloat16()
+    ids = np.array([blocks - 1, 0, blocks - 3], dtype=np.int32)
+    at = dev((ids[:, None].astype(np.int64) * bs + np.arange(bs)).reshape(-1)[:n].astype(np.int32))
+    sp.append_kv_fp4(qkv[:, 4:8], qkv[:, 8:], at, *pools)
+    back = [sp.unpack_fp4(p, slots=at) for p in pools]
+    for x, rows in zip(back, (qkv[:, 4:8], qkv[:, 8:])):
+        assert np.array_equal(host(x), fp4_oracle.decode(*fp4_oracle.encode(host(rows).astype(np.float32))))
+    sp.copy_kv(pools, i32(blocks - 3, blocks - 1), i32(5, blocks - 7), rows=bs)
+    sp.copy_kv(pools, i32(blocks * bs - 1), i32((blocks - 20) * bs + 9))
+    assert torch.equal(sp.unpack_fp4(pools[0], slots=i32(blocks * bs - 1)), sp.unpack_fp4(pools[0], slots=i32((blocks - 20) * bs + 9)))
+    q, table = qkv[:, :4].contiguous(), dev(np.array([ids, [blocks - 7, 0, 5]], dtype=np.int32))
+    pad = [np.concatenate([host(x), np.zeros((3 * bs - n, hk, d))]).reshape(3, bs, hk, d) for x in back]
+    for new in (1, 150):
+        off = i32(0, new, 2 * new)
+        out = sp.paged_attention_fp4(q[:2 * new], off, i32(n, n), table, *pools, max_new=new)
+        ref = paged_oracle.paged_attention(host(q[:2 * new]), host(off), [n, n], np.tile(np.arange(3), (2, 1)), *pad)
+        check_attention(out, None, ref, [n, n], d, "bf16", 2 * new, 30.0)
+
+
+def test_a_workspace_serves_smaller_calls(cuda_lib):
+    """The largest of several, used for all of them in turn."""
+    import torch
+    from tests.fp4_cases import fp4_case
+    sp = cuda_lib
+    cases = [fp4_case(20 + i, ctx, new, 8, 2, d, 16, "fp16") for i, (ctx, new, d) in enumerate(
+        [([700, 30], [400, 1], 128), ([2000], [1], 128), ([100, 9], [90, 3], 64), ([40], [40], 256)])]
+    ws = max((sp.make_attention_fp4_workspace(c["q"], 3, c["k_pool"], kv_tokens=1 << 16) for c in cases), key=lambda w: w.numel())
+    args = [(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"]) for c in cases]
+    want = [sp.paged_attention_fp4(*a) for a in args]
+    for _ in range(3):
+        for a, w in zip(args, want):
+            ws.buffer[256:].fill_(0xff)   # (what earlier calls left there counts for nothing)
+            assert torch.equal(sp.paged_attention_fp4(*a, ws=ws), w)
+    assert sp.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("fp4", [False, True])
+def test_copies_within_a_captured_step(cuda_lib, fp4):
+    """The count, the entries and the tables are read when the graph runs."""
+    import torch
+    sp = cuda_lib
+    bs, hk, d, blocks = 16, 2, 64, 12
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    if fp4:
+        pools = [torch.randint(0, 256, (blocks, hk, bs // 8, 9 * d // 2), dtype=torch.uint8, device="cuda", generator=gen)]
+    else:
+        pools = [torch.randn(blocks, bs, hk, d, device="cuda", generator=gen).bfloat16()]
+    src, dst, n = i32(0, 0, 0), i32(0, 0, 0), i32(0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sp.copy_kv(pools, src, dst, n=n)
+    look = (lambda p: fp4_oracle.unpack(host(p))) if fp4 else (lambda p: (host(p),))
+    want = [x.reshape(blocks * bs, *x.shape[2:]).copy() for x in look(pools[0])]
+    for s, t, m in (([3, 40, 5], [100, 17, 8], 2), ([9, -1, 7], [101, 120, -1], 3), ([1, 2, 3], [150, 151, 152], 0),
+                    ([50, 51, 52], [180, 181, 182], 99)):
+        src.copy_(i32(*s)), dst.copy_(i32(*t)), n.fill_(m)
+        graph.replay()
+        for i in range(min(m, 3)):
+            if s[i] >= 0 and t[i] >= 0:
+                for x in want:
+                    x[t[i]] = x[s[i]]
+        assert all(np.array_equal(x.reshape(y.shape), y, equal_nan=True) for x, y in zip(want, look(pools[0])))
