@@ -707,8 +707,9 @@ int sp_paged_attention_fp4_workspace(const sp_fp4_shape* shape, size_t* bytes);
  * exact for elements down to 2^-31 of the row's largest.
  * Requests whose new tokens make many rows are computed over a 16-bit copy of
  * their cached tokens, in the workspace, as long as those of all such requests
- * of the call fit into dense_tokens (in the requests' order); the others, and
- * all decode steps, are computed from the 4-bit rows. A request with more new
+ * of the call fit into dense_tokens (in the requests' order); the others,
+ * all decode steps, and calls that n_tokens and the table's rows bound to little work are
+ * computed from the 4-bit rows. A request with more new
  * tokens than max_new sets SP_ERR_DEVICE, and nothing is computed.
  * Cached rows that a query is masked from may hold anything, scales that are
  * NaN included. */

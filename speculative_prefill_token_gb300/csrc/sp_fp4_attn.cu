@@ -101,6 +101,7 @@ struct Args {
     int tile_shift;            // log2 of a tile's keys
     int piece_shift;           // log2 of a copy's tokens: a block's, at most a tile's
     int bs_shift;              // log2(bs), or -1
+    int whole;                 // tiles of an item up to which it is not cut
     int local_plan, bf16;
     float scale2, v_scale;
 };
@@ -221,7 +222,9 @@ __device__ __forceinline__ int range_owner(T units, T ctas, T u) {
 }
 
 // Unit u of `units`, of request b whose units begin at `at`, as a start; a cut inside
-// an item's fixed cost falls on the item's start.
+// an item's fixed cost, or an item that has a tile for each warp at most, falls on the
+// item's start. (Cut as the others: a token of 16 requests of 900, 2 heads of 64, 14.9 us in place of
+// 10.9; a prompt of 70, 4 heads of 128, 19.5 in place of 13.9; long contexts have no such items.)
 template <typename T>
 __device__ __forceinline__ Start make_start(const Args& a, int b, int nq, int kv, T at, T units, T ctas, T u, int rows) {
     Start s{b, 0, 0, 0, 1, {0, 0, 0}};
@@ -229,7 +232,7 @@ __device__ __forceinline__ Start make_start(const Args& a, int b, int nq, int kv
     const T per = sp.tiles + kItemCost;
     s.gj = static_cast<int32_t>((u - at) / per);
     const T item = at + s.gj * per;
-    s.off = max(static_cast<int32_t>(u - item) - kItemCost, 0);
+    s.off = sp.tiles > a.whole ? max(static_cast<int32_t>(u - item) - kItemCost, 0) : 0;
     s.c0 = range_owner(units, ctas, item + kItemCost);
     s.parts = range_owner(units, ctas, item + per - 1) - s.c0 + 1;
     return s;
@@ -1235,6 +1238,13 @@ __global__ void __launch_bounds__(kJoinThreads) fp4_join_kernel(const __grid_con
 // 256; 192 rows 44 and 31, 69 and 76, 66 and 104; 512 rows 48 and 61, 92 and 175, 85
 // and 249.)
 __host__ __device__ constexpr int dense_rows(int d) { return d == 64 ? 256 : 128; }
+
+// Units (tiles of keys and items' starts, as the ranges count them) of a call up to which every
+// request is computed from the 4-bit rows, by a bound of them from the call's shape: the copy and the kernels
+// over it take 22 us at the least. (The 4-bit rows, and the copy, at units: d = 64, 8 heads: 5.8K 16 and 23 us, 11.5K 29
+// and 35, 12.6K 39 and 25; 2 heads: 10K 31 to 39 and 33, 17K 47 and 28. d = 128, 4 heads: 2.9K 14 and 25, 6.3K 28 and
+// 27, 10.4K 41 and 31. d = 256, 2 heads: 3.2K 20 and 29, 7.8K 28 and 29, 10.8K 32 and 35, 14K 42 and 32.)
+constexpr int dense_units(int d) { return d == 128 ? 6000 : 9000; }
 constexpr int kDenseBlock = 128;      // tokens of a block of the copy
 constexpr int kDenseThreads = 256;
 
@@ -1255,8 +1265,26 @@ struct DenseArgs {
     int B, hk, G, d, bs, bs_shift, table_stride, width, tokens, max_new, window, cap;
 };
 
+// First block of 128 tokens that a request's rows see.
+__device__ __forceinline__ int dense_first(const DenseArgs& a, int nq, int kv) {
+    return a.window > 0 ? max(0, kv - nq - a.window + 1) / kDenseBlock : 0;
+}
+
+// Blocks of request b's copy, from `first` on; 0: it is read from the 4-bit rows.
+// Lengths that are out of range are noted, and told by the kernels that follow.
+__device__ __forceinline__ int dense_blocks(const DenseArgs& a, int b, int* first, int* bad) {
+    const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], nq = hi - lo, kv = a.kv_len[b];
+    if (bad_request(a, a.tokens, lo, hi, kv) || (b == 0 && lo != 0)) *bad = 1;
+    else if (nq * a.G >= dense_rows(a.d) && kv > 0 && kv <= static_cast<int64_t>(a.width) * kDenseBlock) {
+        *first = dense_first(a, static_cast<int>(nq), static_cast<int>(kv));
+        return static_cast<int>((kv + kDenseBlock - 1) / kDenseBlock) - *first;
+    }
+    return 0;
+}
+
 // Which requests are read through 16 bits, and where their copies lie: those of
-// dense_rows() rows and more, in order, as long as their blocks fit. By one block.
+// dense_rows() rows and more, in order, as long as their blocks fit. By one block, for
+// more requests than a warp of each of the copying blocks lays out for itself.
 __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const DenseArgs a) {
     __shared__ int64_t sums[32];
     __shared__ int most;
@@ -1264,18 +1292,12 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const Dens
     grid_dep_launch();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) most = 0;
-    auto first_of = [&](int nq, int kv) { return a.window > 0 ? max(0, kv - nq - a.window + 1) / kDenseBlock : 0; };
     int64_t blocks = 0;
-    int bad = tid == 0 ? a.q_off[0] != 0 : 0;   // (told by the kernels that follow)
+    int bad = 0;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
-        int64_t n = 0;
-        if (b < a.B) {
-            const int64_t lo = a.q_off[b], hi = a.q_off[b + 1], nq = hi - lo, kv = a.kv_len[b];
-            if (bad_request(a, a.tokens, lo, hi, kv)) bad = 1;
-            else if (nq * a.G >= dense_rows(a.d) && kv > 0 && kv <= static_cast<int64_t>(a.width) * kDenseBlock)
-                n = (kv + kDenseBlock - 1) / kDenseBlock - first_of(static_cast<int>(nq), static_cast<int>(kv));
-        }
+        int first;
+        const int64_t n = b < a.B ? dense_blocks(a, b, &first, &bad) : 0;
         int64_t total;
         const int64_t at = blocks + block_scan<kPlanThreads>(n, sums, &total);
         if (b < a.B) a.base[b] = n > 0 && at + n <= a.cap ? static_cast<int32_t>(at) : -1;
@@ -1291,7 +1313,7 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const Dens
         const int mine = b0 + lane < a.B ? a.base[b0 + lane] : -1;
         for (unsigned who = __ballot_sync(0xffffffffu, mine >= 0); who; who &= who - 1) {
             const int b = b0 + __ffs(who) - 1, base = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
-            const int kv = a.kv_len[b], first = first_of(a.q_off[b + 1] - a.q_off[b], kv);
+            const int kv = a.kv_len[b], first = dense_first(a, a.q_off[b + 1] - a.q_off[b], kv);
             for (int i = first + lane; i < (kv + kDenseBlock - 1) / kDenseBlock; i += 32) {
                 a.dense_table[static_cast<int64_t>(b) * a.width + i] = base + i - first;
                 a.owner[base + i - first] = make_int2(b, i);
@@ -1301,16 +1323,65 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_dense_plan_kernel(const Dens
     if (tid == 0) *a.used = most;
 }
 
-// The copies: a block of tokens of one head by a CTA, 16 elements a thread.
+// The same for at most 64 requests, by one warp, two a lane: each request's blocks of the
+// copy, [base, last), and the blocks in use.
+__device__ __forceinline__ void plan_copy(const DenseArgs& a, int* base, int* last, int* first, int* used, int lane) {
+    constexpr unsigned kAll = 0xffffffffu;
+    int n[2] = {0, 0}, from[2] = {0, 0}, bad = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (lane + 32 * i < a.B) n[i] = dense_blocks(a, lane + 32 * i, from + i, &bad);
+    const bool none = __any_sync(kAll, bad != 0);
+    int64_t run = 0;
+    int most = 0;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        int64_t incl = n[i];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(kAll, incl, o);
+            if (lane >= o) incl += x;
+        }
+        const int64_t end = run + incl;
+        const bool fits = !none && n[i] > 0 && end <= a.cap;
+        base[32 * i + lane] = fits ? static_cast<int>(end - n[i]) : -1;
+        last[32 * i + lane] = fits ? static_cast<int>(end) : -1;
+        first[32 * i + lane] = from[i];
+        if (fits) most = max(most, static_cast<int>(end));
+        run += __shfl_sync(kAll, incl, 31);
+    }
+    most = __reduce_max_sync(kAll, most);
+    if (lane == 0) *used = most;
+}
+
+// The copies: a block of tokens of one head by a CTA, 16 elements a thread. (The layout with them, in
+// place of a launch before: a chunk of 60 tokens 27.6 to 25.6 us, the mixed batch 78.4 to 74.7.)
 template <bool kBf16>
 __global__ void __launch_bounds__(kDenseThreads) fp4_dense_kernel(const DenseArgs a) {
     grid_dep_wait();
     grid_dep_launch();
-    const int shift = 31 - __clz(a.d / kFp4Group), groups = 1 << shift, units = *a.used * a.hk;
+    __shared__ int base_s[kWarpSeqs], last_s[kWarpSeqs], first_s[kWarpSeqs], used_s;
+    const int lane = threadIdx.x & 31;
+    const bool local = a.B <= kWarpSeqs;
+    if (local) {
+        if (threadIdx.x < 32) plan_copy(a, base_s, last_s, first_s, &used_s, lane);
+        __syncthreads();
+        if (blockIdx.x == 0 && threadIdx.x < a.B) a.base[threadIdx.x] = base_s[threadIdx.x];
+    }
+    const int shift = 31 - __clz(a.d / kFp4Group), groups = 1 << shift, units = (local ? used_s : *a.used) * a.hk;
     const int64_t head = static_cast<int64_t>(a.cap) * kDenseBlock * a.d;
     for (int u = blockIdx.x; u < units; u += gridDim.x) {
         const int blk = u / a.hk, h = u - blk * a.hk;
-        const int2 own = a.owner[blk];
+        int2 own;
+        if (local) {
+            const unsigned in0 = __ballot_sync(0xffffffffu, base_s[lane] >= 0 && base_s[lane] <= blk && blk < last_s[lane]);
+            const unsigned in1 = __ballot_sync(0xffffffffu, base_s[32 + lane] >= 0 && base_s[32 + lane] <= blk && blk < last_s[32 + lane]);
+            own.x = in0 ? __ffs(in0) - 1 : 31 + __ffs(in1);
+            own.y = first_s[own.x] + blk - base_s[own.x];
+            if (h == 0 && threadIdx.x == 0) a.dense_table[static_cast<int64_t>(own.x) * a.width + own.y] = blk;
+        } else {
+            own = a.owner[blk];
+        }
         const int kv = a.kv_len[own.x];
         for (int x = threadIdx.x; x < kDenseBlock * groups; x += kDenseThreads) {
             const int r = x >> shift, g = x & (groups - 1), j = own.y * kDenseBlock + r;
@@ -1429,6 +1500,9 @@ Layout layout(const sp_fp4_shape* s, int grid) {
     return l;
 }
 
+// Rows of an item.
+int rows_of(int d, int max_new, int G) { return d == 256 || static_cast<int64_t>(max_new) * G <= 8 ? 8 : 16; }
+
 // A stride of a pool (below 2^32 where it counts).
 uint32_t stride32(int64_t extent, int64_t stride) { return extent > 1 ? static_cast<uint32_t>(stride) : 0u; }
 
@@ -1496,7 +1570,11 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     const double scale = p->scale > 0.0f ? static_cast<double>(p->scale) : 1.0 / std::sqrt(static_cast<double>(d));
     a.scale2 = static_cast<float>(scale * p->k_scale * 1.4426950408889634);
     a.v_scale = p->v_scale;
-    if (l.dense_cap > 0) {
+    const int rows = rows_of(d, a.max_new, a.G);
+    a.whole = warps_of(d, rows / 8);
+    const int64_t items = a.hk * (static_cast<int64_t>(a.cap) * a.G / rows + a.B);
+    const int64_t keys = static_cast<int64_t>(a.table_stride) * a.bs >> a.tile_shift;
+    if (l.dense_cap > 0 && items * (keys + kItemCost) > dense_units(d)) {
         DenseArgs e;
         e.q_off = q_off;
         e.kv_len = kv_len;
@@ -1524,7 +1602,8 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
         e.max_new = a.max_new;
         e.window = a.window;
         e.cap = l.dense_cap;
-        cudaError_t rc = launch_k(fp4_dense_plan_kernel, 1, kPlanThreads, 0, st, e);
+        cudaError_t rc = cudaSuccess;
+        if (a.B > kWarpSeqs) rc = launch_k(fp4_dense_plan_kernel, 1, kPlanThreads, 0, st, e);
         if (rc != cudaSuccess) return rc;
         const int64_t units = static_cast<int64_t>(l.dense_cap) * a.hk, most = int64_t(8) * a.grid;
         rc = launch_k(a.bf16 ? fp4_dense_kernel<true> : fp4_dense_kernel<false>,
@@ -1542,9 +1621,8 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
         if (rc != cudaSuccess) return rc;
         a.dense = e.base;
     }
-    const bool one = static_cast<int64_t>(a.max_new) * a.G <= 8;
-    if (d == 64) return one ? launch_rows<64, 1>(a, st) : launch_rows<64, 2>(a, st);
-    if (d == 128) return one ? launch_rows<128, 1>(a, st) : launch_rows<128, 2>(a, st);
+    if (d == 64) return rows == 8 ? launch_rows<64, 1>(a, st) : launch_rows<64, 2>(a, st);
+    if (d == 128) return rows == 8 ? launch_rows<128, 1>(a, st) : launch_rows<128, 2>(a, st);
     return launch_rows<256, 1>(a, st);
 }
 

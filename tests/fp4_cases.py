@@ -20,7 +20,9 @@ def fp4_case(seed, ctx, new, hq, hk, d, bs, dtype, spare_rows=0, q_gain=1.0, fac
     used = [-(-n // bs) for n in kv]
     blocks = sum(used) + 2
     perm = rng.permutation(blocks)
-    table = np.full((len(kv), max(max(used), 1) + 1), -1, dtype=np.int32)   # (unused entries are invalid ids)
+    # (unused entries are invalid ids; by rows this wide the call may be a long one, so that requests with many new
+    # tokens go through 16 bits)
+    table = np.full((len(kv), max(max(used), 1) + 90000 // bs), -1, dtype=np.int32)
     pools = []
     for f in factor:
         codes = rng.integers(0, 16, (blocks, bs, hk, d), dtype=np.uint8)

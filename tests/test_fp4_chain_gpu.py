@@ -291,3 +291,43 @@ def test_copies_within_a_captured_step(cuda_lib, fp4):
                 for x in want:
                     x[t[i]] = x[s[i]]
         assert all(np.array_equal(x.reshape(y.shape), y, equal_nan=True) for x, y in zip(want, look(pools[0])))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("narrow", [False, True])
+def test_short_prompts_by_either_way(cuda_lib, d, narrow):
+    """Prompts and chunks of little work: by the table's width from the 4-bit rows or through 16 bits."""
+    import torch
+    from tests.fp4_cases import fp4_case
+    sp = cuda_lib
+    c = fp4_case(31, [0, 60, 3], [300, 150, 1], 8, 2, d, 16, "bf16")
+    table = c["table"][:, :24].contiguous() if narrow else c["table"]
+    lse = torch.full((451, 8), 7.0, device="cuda")
+    ws = sp.make_attention_fp4_workspace(c["q"], 3, c["k_pool"])
+    out = sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], table, c["k_pool"], c["v_pool"], window=100, lse=lse, ws=ws)
+    ref = paged_oracle.paged_attention(host(c["q"]), host(c["q_off"]), host(c["kv_len"]), host(table), np.nan_to_num(c["k"]),
+                                       np.nan_to_num(c["v"]), window=100)
+    check_attention(out, lse, ref, host(c["kv_len"]), d, "bf16", 451, 30.0)
+    assert sp.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("batch", [64, 65, 130])
+@pytest.mark.parametrize("room", [None, 900])
+def test_chunks_among_many_requests(cuda_lib, batch, room):
+    """Layouts of the 16-bit copies by a warp and by a block, with and without room for all of them."""
+    import torch
+    from tests.fp4_cases import fp4_case
+    sp = cuda_lib
+    rng = np.random.default_rng(batch)
+    new = [int(x) for x in rng.choice([0, 1, 1, 2, 70], batch)]
+    for i in (0, 33, batch - 1):
+        new[i] = 100 + i
+    ctx = [int(x) for x in rng.integers(0, 300, batch)]
+    c = fp4_case(batch, ctx, new, 4, 1, 64, 32, "fp16")
+    ws = sp.make_attention_fp4_workspace(c["q"], batch, c["k_pool"], kv_tokens=room)
+    for _ in range(2):
+        out = sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], c["table"], c["k_pool"], c["v_pool"], ws=ws)
+    ref = paged_oracle.paged_attention(host(c["q"]), host(c["q_off"]), host(c["kv_len"]), host(c["table"]), np.nan_to_num(c["k"]),
+                                       np.nan_to_num(c["v"]))
+    check_attention(out, None, ref, host(c["kv_len"]), 64, "fp16", sum(new), 30.0)
+    assert sp.device_status(ws) == 0
