@@ -223,8 +223,12 @@ __device__ __forceinline__ int range_owner(T units, T ctas, T u) {
 
 // Unit u of `units`, of request b whose units begin at `at`, as a start; a cut inside
 // an item's fixed cost, or an item that has a tile for each warp at most, falls on the
-// item's start. (Cut as the others: a token of 16 requests of 900, 2 heads of 64, 14.9 us in place of
-// 10.9; a prompt of 70, 4 heads of 128, 19.5 in place of 13.9; long contexts have no such items.)
+// item's start: a warp's time there is that of one tile, and pieces of items cost their ends and
+// the second join. (Cut as the others: a token of 16 requests of 900, 2 heads of 64, 14.9 us in
+// place of 10.9; a prompt of 70, 4 heads of 128, 19.5 in place of 13.9.) Items of two tiles a warp are not cut
+// either where there are 64 or more of them and no CTA gets two while most get one: a token of
+// 16, 32 and 64 requests of 900, 4 heads of 128, 17.3, 19.9 and 26.0 us cut, 14.0, 14.1 and 21.5 whole; of 8 16.4
+// and 13.9, but of 4 12.0 and 13.7; of 40 requests of 1,400 19.7 and 24.0.
 template <typename T>
 __device__ __forceinline__ Start make_start(const Args& a, int b, int nq, int kv, T at, T units, T ctas, T u, int rows) {
     Start s{b, 0, 0, 0, 1, {0, 0, 0}};
@@ -1571,8 +1575,9 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     a.scale2 = static_cast<float>(scale * p->k_scale * 1.4426950408889634);
     a.v_scale = p->v_scale;
     const int rows = rows_of(d, a.max_new, a.G);
-    a.whole = warps_of(d, rows / 8);
-    const int64_t items = a.hk * (static_cast<int64_t>(a.cap) * a.G / rows + a.B);
+    // (as many as there may be, without those that a padded batch does not have)
+    const int64_t items = a.hk * (static_cast<int64_t>(a.max_new) * a.G <= rows ? a.B : static_cast<int64_t>(a.cap) * a.G / rows + a.B);
+    a.whole = warps_of(d, rows / 8) * (items >= 64 && (items <= a.grid || 2 * items >= 3 * a.grid) ? 2 : 1);
     const int64_t keys = static_cast<int64_t>(a.table_stride) * a.bs >> a.tile_shift;
     if (l.dense_cap > 0 && items * (keys + kItemCost) > dense_units(d)) {
         DenseArgs e;
