@@ -36,14 +36,14 @@
 // computed by the attention over a 16-bit cache (sp_attn.cu), on
 // fifth-generation tensor cores, 128 rows at a time.
 //
-// Measured (bf16): 64 requests of 2K to 32K tokens, a token of each, 16/4 heads of 128, 728 MB: 127.5
-// us, 5.7 TB/s, 84 % of a copy's rate; its loads alone 116. Issue slots 56 % busy at 12 warps, ALU and fp16 pipes
+// Measured (bf16): 64 requests of 2K to 32K tokens, a token of each, 16/4 heads of 128, 728 MB: 125 to
+// 127 us, 5.8 TB/s, 85 % of a copy's rate; its loads alone 116. Issue slots 56 % busy at 12 warps, ALU and fp16 pipes
 // 47 and 38 %, tensor pipe 27 %, DRAM 69 %: no pipe is full, the rest is the chain convert - multiply
 // - softmax of a warp, of which registers and shared memory hold no more than 12. The same bytes at
 // d = 256 135 us, at d = 64, half of them, 96. A token of 16 requests of 4K to 16K, 8/2 heads of 256, 86 MB:
-// 33.6 us, of which 5 are the start (lengths, ranges, table, first tile: reads that follow one
+// 33 us, of which 5 are the start (lengths, ranges, table, first tile: reads that follow one
 // another) and 3 the join. One token over 512: 10 us, all of it latency. 8 tokens over 32K, d =
-// 256: 31 us, four items of 8 rows that convert the same codes (16 rows would take 128
+// 256: 30.5 us, four items of 8 rows that convert the same codes (16 rows would take 128
 // accumulators a lane, beside 64 registers of queries). 4,096 tokens over 39,322 in all: 0.83 to 0.86
 // ms, of which the copy is 0.03.
 #include <cuda_bf16.h>
