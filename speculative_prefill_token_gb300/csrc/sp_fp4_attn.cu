@@ -42,7 +42,7 @@
 // - softmax of a warp, of which registers and shared memory hold no more than 12. The same bytes at
 // d = 256 135 us, at d = 64, half of them, 96. A token of 16 requests of 4K to 16K, 8/2 heads of 256, 86 MB:
 // 33 us, of which 5 are the start (lengths, ranges, table, first tile: reads that follow one
-// another) and 3 the join. One token over 512: 10 us, all of it latency. 8 tokens over 32K, d =
+// another) and 3 the join. One token over 512: 8 us, all of it latency. 8 tokens over 32K, d =
 // 256: 30.5 us, four items of 8 rows that convert the same codes (16 rows would take 128
 // accumulators a lane, beside 64 registers of queries). 4,096 tokens over 39,322 in all: 0.83 to 0.86
 // ms, of which the copy is 0.03.
@@ -102,6 +102,8 @@ struct Args {
     int piece_shift;           // log2 of a copy's tokens: a block's, at most a tile's
     int bs_shift;              // log2(bs), or -1
     int whole;                 // tiles of an item up to which it is not cut
+    int cuts;                  // whether the table's rows hold longer ones (if not, there is no second join: one token
+                               // over 512 by a row of 544 tokens 10.0 to 7.8 us, 64 over 900 by rows of 928, 2 heads of 64, 14.9 to 9.3)
     int local_plan, bf16;
     float scale2, v_scale;
 };
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(kPlanThreads) fp4_plan_kernel(const Args a, in
 
 // CTAs that share `units`: few of them get less than a tile for every other warp. (4 tokens
 // over 8K in 4 requests, d = 64: 14.3 us; 16 15.3, 32 17.9. One token over 512: 10.2 us; 2 and 4, where
-// more CTAs share it, 11.0 and 10.9.)
+// more CTAs shared it, 11.0 and 10.9.)
 constexpr int kLeastUnits = 8;
 
 __device__ __forceinline__ int64_t ctas_for(const Args& a, int64_t units) {
@@ -1521,7 +1523,7 @@ cudaError_t launch_rows(const Args& a, cudaStream_t st) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(L::total));
     if (e != cudaSuccess) return e;
     e = launch_k(kern, static_cast<unsigned>(a.grid), L::kThreads, L::total, st, a);
-    if (e != cudaSuccess || a.grid < 2) return e;
+    if (e != cudaSuccess || a.grid < 2 || !a.cuts) return e;
     return launch_k(fp4_join_kernel<D, NT>, dim3(a.grid - 1, L::kRows), kJoinThreads, 0, st, a);
 }
 
@@ -1578,7 +1580,8 @@ cudaError_t launch_paged_attention_fp4(const sp_fp4_shape* s, const sp_fp4_param
     // (as many as there may be, without those that a padded batch does not have)
     const int64_t items = a.hk * (static_cast<int64_t>(a.max_new) * a.G <= rows ? a.B : static_cast<int64_t>(a.cap) * a.G / rows + a.B);
     a.whole = warps_of(d, rows / 8) * (items >= 64 && (items <= a.grid || 2 * items >= 3 * a.grid) ? 2 : 1);
-    const int64_t keys = static_cast<int64_t>(a.table_stride) * a.bs >> a.tile_shift;
+    const int64_t room = static_cast<int64_t>(a.table_stride) * a.bs, keys = ((room < kMaxCached ? room : kMaxCached) + tile_keys(d) - 1) >> a.tile_shift;
+    a.cuts = keys > a.whole;
     if (l.dense_cap > 0 && items * (keys + kItemCost) > dense_units(d)) {
         DenseArgs e;
         e.q_off = q_off;

@@ -331,3 +331,28 @@ def test_chunks_among_many_requests(cuda_lib, batch, room):
                                        np.nan_to_num(c["v"]))
     check_attention(out, None, ref, host(c["kv_len"]), 64, "fp16", sum(new), 30.0)
     assert sp.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("d,hq,hk", [(64, 4, 2), (128, 16, 4), (256, 6, 2)])
+@pytest.mark.parametrize("batch,top", [(1, 380), (9, 200), (70, 380), (300, 64)])
+def test_rows_that_hold_short_contexts(cuda_lib, d, hq, hk, batch, top):
+    """By a table that holds no context long enough to be cut the results are those of a wide one, bit for bit."""
+    import torch
+    from tests.fp4_cases import fp4_case
+    sp = cuda_lib
+    rng = np.random.default_rng(batch)
+    new = [int(x) for x in rng.choice([0, 1, 1, 3], batch)]
+    new[0] = 1
+    c = fp4_case(batch + d, [int(x) for x in rng.integers(0, top - 3, batch)], new, hq, hk, d, 16, "bf16")
+    narrow = c["table"][:, :-(-top // 16)].contiguous()
+    got = []
+    for table in (narrow, c["table"]):
+        lse = torch.full((sum(new), hq), 7.0, device="cuda")
+        ws = sp.make_attention_fp4_workspace(c["q"], batch, c["k_pool"], max_new=3)
+        out = sp.paged_attention_fp4(c["q"], c["q_off"], c["kv_len"], table, c["k_pool"], c["v_pool"], lse=lse, max_new=3, ws=ws)
+        assert sp.device_status(ws) == 0
+        got.append((out, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    ref = paged_oracle.paged_attention(host(c["q"]), host(c["q_off"]), host(c["kv_len"]), host(narrow), np.nan_to_num(c["k"]),
+                                       np.nan_to_num(c["v"]))
+    check_attention(*got[0], ref, host(c["kv_len"]), d, "bf16", sum(new), 30.0)
