@@ -156,7 +156,7 @@ struct AttnArgs {
     int hk_shift, hv_shift;  // rows of a K and of a V box, as powers of two
     uint32_t q_bytes;    // of one 64-element chunk of a query tile
     float scale2;
-    float out_scale;     // factor of the result
+    float out_scale;     // with `only`: factor of the result
 };
 
 // ------------------------------------------------------------ plan
@@ -971,7 +971,8 @@ struct RowEnd {
 // kernel. Not inlined: the softmax loop keeps its registers. (Whole lines after
 // an exchange between quads took 1.4 times as long: the shuffles cost more
 // than the 32 lines of a store.)
-template <int D, bool kBf16>
+// (kScaled: a code of its own, as the factor takes a short call 0.3 us: one token 9.5 to 9.8.)
+template <int D, bool kBf16, bool kScaled>
 __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
     constexpr int kCols = D > 128 ? D / 2 : D;    // columns of a warpgroup
     const bool mine = static_cast<int>(threadIdx.x & 31) < e.rows;
@@ -981,7 +982,7 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
     // the exact ones out is the same to four digits of its error, lse is 0.5e-6 in
     // place of 0.7e-6 off at 8.5, where a step of 32 bits is 1e-6, and a prompt at
     // d = 256 and the mixed batch take 1 % longer)
-    const float inv = split ? 1.0f : none ? 0.0f : __fdividef(1.0f, e.l) * a.out_scale;
+    const float inv = split ? 1.0f : none ? 0.0f : kScaled ? __fdividef(1.0f, e.l) * a.out_scale : __fdividef(1.0f, e.l);
     const float e0 = e.f0 * inv, e1 = e.f1 * inv;
     char* dst = split ? reinterpret_cast<char*>(a.part_o + static_cast<int64_t>(e.part) * D + e.col0)
                       : reinterpret_cast<char*>(a.out + e.t * a.o_st + e.h * a.o_sh + e.col0);
@@ -1354,7 +1355,8 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                 e.m = m;
                 e.l = s.n > 0 ? l : 0.0f;
                 e.join = join;
-                write_rows<D, kBf16>(a, e);
+                if (a.only) write_rows<D, kBf16, true>(a, e);
+                else write_rows<D, kBf16, false>(a, e);
             }
             if (s.n > 0) {
                 tc_fence_before();
@@ -1535,7 +1537,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
         const Row zero{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
         auto write = [&](Place x, const Row& y) {
             const bool none = y.sum == 0.0f;
-            const float inv = none ? 0.0f : 1.0f / y.sum * a.out_scale;
+            float inv = none ? 0.0f : 1.0f / y.sum;
+            if (a.only) inv *= a.out_scale;
             const int tok = x.row / a.G;
             const int64_t t = job.tok0 + x.tile * a.tq + tok;
             const int h = job.g * a.G + x.row - tok * a.G;
