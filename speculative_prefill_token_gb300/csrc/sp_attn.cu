@@ -265,6 +265,10 @@ __device__ __forceinline__ bool bad_request(const AttnArgs& a, int64_t lo, int64
     return hi < lo || hi > a.cap || kv < 0 || kv > kMaxCached || (kv + a.bs - 1) / a.bs > a.table_stride;
 }
 
+// Requests that the caller computes elsewhere. It has looked at their lengths: their
+// contexts may be longer than this call's table holds.
+__device__ __forceinline__ bool left_out(const AttnArgs& a, int b) { return a.only && a.only[b] < 0; }
+
 // Lays out a batch of any size, by one block of its own: items with their
 // costs, and the CTAs' ranges. Bound by the latency of its scans.
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles) {
@@ -280,8 +284,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
         int64_t n = 0;
         if (b < a.B) {
             const int64_t lo = a.q_off[b], hi = a.q_off[b + 1];
-            if (bad_request(a, lo, hi, a.kv_len[b])) bad = 1;
-            else if (!a.only || a.only[b] >= 0) n = (hi - lo + tpi - 1) / tpi;
+            if (!left_out(a, b)) {
+                if (bad_request(a, lo, hi, a.kv_len[b])) bad = 1;
+                else n = (hi - lo + tpi - 1) / tpi;
+            }
         }
         int64_t total;
         const int64_t at = items + block_scan<kPlanThreads>(n, sums, &total);
@@ -344,8 +350,9 @@ __device__ __forceinline__ int local_plan(const AttnArgs& a, int tiles, LocalPla
     int bad = 0, n = 0;
     if (t < a.B) {
         const int lo = a.q_off[t], hi = a.q_off[t + 1], kv = a.kv_len[t];
-        bad = bad_request(a, lo, hi, kv) || (t == 0 && lo != 0);
-        if (!bad && (!a.only || a.only[t] >= 0)) n = (hi - lo + tpi - 1) / tpi;
+        const bool out = left_out(a, t);
+        bad = (!out && bad_request(a, lo, hi, kv)) || (t == 0 && lo != 0);
+        if (!bad && !out) n = (hi - lo + tpi - 1) / tpi;
         p.q0[t] = lo;
         p.nq[t] = hi - lo;
         p.kv[t] = kv;
