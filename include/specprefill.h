@@ -712,7 +712,8 @@ int sp_paged_attention_fp4_workspace(const sp_fp4_shape* shape, size_t* bytes);
  * computed from the 4-bit rows. A request with more new
  * tokens than max_new sets SP_ERR_DEVICE, and nothing is computed.
  * Cached rows that a query is masked from may hold anything, scales that are
- * NaN included. */
+ * NaN included; table entries of blocks that no row sees (behind the request's end,
+ * before the first row's window) are not read. */
 int sp_paged_attention_fp4(const sp_fp4_shape* shape, const sp_fp4_params* params,
                            const int32_t* q_off, const int32_t* kv_len, const int32_t* block_table,
                            const uint16_t* q, const uint8_t* k_pool, const uint8_t* v_pool,

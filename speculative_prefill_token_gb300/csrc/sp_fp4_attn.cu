@@ -1271,10 +1271,14 @@ struct DenseArgs {
     int B, hk, G, d, bs, bs_shift, table_stride, width, tokens, max_new, window, cap;
 };
 
-// First block of 128 tokens that a request's rows see.
-__device__ __forceinline__ int dense_first(const DenseArgs& a, int nq, int kv) {
-    return a.window > 0 ? max(0, kv - nq - a.window + 1) / kDenseBlock : 0;
+// First cached token that a request's rows see: those before it are not read (their blocks
+// may be gone), and their places in the copy hold anything.
+__device__ __forceinline__ int dense_low(const DenseArgs& a, int nq, int kv) {
+    return a.window > 0 ? max(0, kv - nq - a.window + 1) : 0;
 }
+
+// And the block of 128 that it lies in.
+__device__ __forceinline__ int dense_first(const DenseArgs& a, int nq, int kv) { return dense_low(a, nq, kv) / kDenseBlock; }
 
 // Blocks of request b's copy, from `first` on; 0: it is read from the 4-bit rows.
 // Lengths that are out of range are noted, and told by the kernels that follow.
@@ -1388,10 +1392,10 @@ __global__ void __launch_bounds__(kDenseThreads) fp4_dense_kernel(const DenseArg
         } else {
             own = a.owner[blk];
         }
-        const int kv = a.kv_len[own.x];
+        const int kv = a.kv_len[own.x], lo = dense_low(a, a.q_off[own.x + 1] - a.q_off[own.x], kv);
         for (int x = threadIdx.x; x < kDenseBlock * groups; x += kDenseThreads) {
             const int r = x >> shift, g = x & (groups - 1), j = own.y * kDenseBlock + r;
-            if (j >= kv) continue;
+            if (j < lo || j >= kv) continue;
             const int col = a.bs_shift >= 0 ? j >> a.bs_shift : j / a.bs, within = j - col * a.bs;
             int id = a.table[static_cast<int64_t>(own.x) * a.table_stride + col];
             if (id < 0 || id >= a.pool_blocks) {

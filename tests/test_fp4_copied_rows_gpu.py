@@ -42,10 +42,10 @@ def attend(c, copied=(), causal=True, window=0, scale=0.0, max_new=None, kv_toke
     return out, lse, sp.device_status(ws)
 
 
-def check(c, dtype, copied, causal=True, window=0, **more):
+def check(c, dtype, copied, causal=True, window=0, table=None, **more):
     out, lse, status = attend(c, copied, causal, window, **more)
     assert status == 0
-    ref = paged_oracle.paged_attention(host(c["q"]), host(c["q_off"]), host(c["kv_len"]), host(c["table"]),
+    ref = paged_oracle.paged_attention(host(c["q"]), host(c["q_off"]), host(c["kv_len"]), host(c["table"]) if table is None else table,
                                        np.nan_to_num(c["k"]), np.nan_to_num(c["v"]), causal, window)
     check_attention(out, lse, ref, host(c["kv_len"]), c["q"].shape[2], dtype, int(c["q_off"][-1]),
                     float(np.nanmax(np.abs(c["v"]))))
@@ -69,3 +69,21 @@ def test_a_context_longer_than_its_pool_beside_a_chunk(batch, longer, window):
     c["kv_len"][0] = 400 * rounds
     assert 400 * rounds > blocks * bs
     check(c, "bf16", [2], window=window)
+
+
+@pytest.mark.parametrize("batch", [2, 80])
+@pytest.mark.parametrize("d,bs", [(64, 8), (128, 32), (256, 16)])
+def test_blocks_behind_the_window_may_be_gone(batch, d, bs):
+    """Their table entries name no block; the copy does not look at them either."""
+    new = [1] * batch
+    new[-1] = 150
+    ctx = [90 + 7 * i % 300 for i in range(batch)]
+    ctx[-1] = 1000
+    c = fp4_case(d + batch, ctx, new, 4, 1, d, bs, "fp16")
+    window = 150
+    whole = host(c["table"]).copy()     # (the oracle looks every block up before it masks)
+    for b in range(batch):
+        gone = max(0, ctx[b] + 1 - window) // bs        # blocks of tokens that no row sees
+        c["table"][b, :gone] = -1 if b % 2 else 1 << 24
+    assert int(c["table"][-1, (1001 - window) // 128 * 128 // bs]) in (-1, 1 << 24)   # such tokens share the copy's first block
+    check(c, "fp16", [batch - 1], window=window, table=whole)
