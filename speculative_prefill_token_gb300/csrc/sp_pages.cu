@@ -204,8 +204,9 @@ __global__ void __launch_bounds__(kCopyThreads, copy_ctas(kTokens)) copy_kv_kern
             in = from.block * a.sb + part * a.sh;
             out = to.block * a.sb + part * a.sh;
         } else {
-            in = from.block * a.sb + from.row / kFp4Rows * fp4_record(a.d);
-            out = to.block * a.sb + to.row / kFp4Rows * fp4_record(a.d);
+            // (a block may be more than 2^31 bytes)
+            in = from.block * a.sb + static_cast<int64_t>(from.row / kFp4Rows) * fp4_record(a.d);
+            out = to.block * a.sb + static_cast<int64_t>(to.row / kFp4Rows) * fp4_record(a.d);
         }
         if (!live) in = -1;
         const int count = static_cast<int>(min(static_cast<int64_t>(a.per_warp), tasks - (w - p * steps) * a.per_warp));

@@ -282,3 +282,23 @@ def test_strided_pools():
     want[0, 1, :, 0] = old[0, 1, :, 3]
     want[5, 1, :, 7] = old[2, 1, :, 1]
     assert torch.equal(big, want)
+
+
+@pytest.mark.parametrize("d,bs", [(256, 15_000_064), (64, 119_400_064)])
+def test_tokens_of_a_block_of_more_than_31_bits(d, bs):
+    """A pool of one block and one head is one run of rows, whose last lie more than 2^31 bytes (and 2^32) behind
+    the first."""
+    import torch
+
+    import speculative_prefill_token_gb300 as sp
+    assert bs % 128 == 0 and (bs - 20) * (9 * d // 16) > 1 << 31
+    pool = torch.zeros(1, 1, bs // 8, 9 * d // 2, dtype=torch.uint8, device="cuda")
+    pool[0, 0, -2:] = torch.randint(1, 120, pool.shape[3:], dtype=torch.uint8, device="cuda")
+    far, near = np.arange(bs - 12, bs, 3), np.array([0, 9, 18, 30])
+    want = sp.unpack_fp4(pool, slots=i32(far))
+    assert want.any(-1).all()
+    sp.copy_kv([pool], i32(far), i32(near))
+    assert torch.equal(sp.unpack_fp4(pool, slots=i32(near)), want)
+    sp.copy_kv([pool], i32(near), i32(far - 1))
+    assert torch.equal(sp.unpack_fp4(pool, slots=i32(far - 1)), want) and torch.equal(sp.unpack_fp4(pool, slots=i32(far)), want)
+    assert not pool[0, 0, 4:-2].any()
