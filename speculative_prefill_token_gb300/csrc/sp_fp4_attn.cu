@@ -525,8 +525,10 @@ struct Feed {
                 atomicCAS(a.status, 0, static_cast<int32_t>(SP_ERR_DEVICE));
                 id = 0;
             }
-            k_at = static_cast<uint64_t>(id) * a.k_sb + row * (L::kRec / kFp4Rows);
-            v_at = static_cast<uint64_t>(id) * a.v_sb + row * (L::kRec / kFp4Rows);
+            // (a pool of one block and head may be one run of more than 2^32 bytes)
+            const uint64_t in = static_cast<uint64_t>(row) * (L::kRec / kFp4Rows);
+            k_at = static_cast<uint64_t>(id) * a.k_sb + in;
+            v_at = static_cast<uint64_t>(id) * a.v_sb + in;
         }
     }
     // Keys or values of the tile to `dst`, as a group of copies.

@@ -192,3 +192,29 @@ def test_large_offsets():
     from tests.fp4_cases import check_attention
     out = sp.paged_attention_fp4(q, i32(0, 1), i32(bs), table, *pools)
     check_attention(out, None, ref, [bs], d, "bf16", 1, 6.0)
+
+
+@pytest.mark.parametrize("d,bs", [(256, 29_900_160), (64, 119_400_064)])
+def test_a_block_of_more_than_32_bits(d, bs):
+    """A pool of one block and one head is one run of rows: the last of them lie more than 2^32 bytes behind the first."""
+    import torch
+
+    import speculative_prefill_token_gb300 as sp
+    from tests.fp4_cases import check_attention
+    n, tail = 4, 70
+    assert bs % 128 == 0 and (bs - tail) * (9 * d // 16) > 1 << 32
+    pools = [torch.zeros(1, 1, bs // 8, 9 * d // 2, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots = torch.arange(bs - tail, bs, dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    qkv = torch.randn(tail, 4, d, device="cuda", generator=gen).bfloat16()
+    sp.append_kv_fp4(qkv[:, 2:3], qkv[:, 3:], slots, *pools)
+    back = [sp.unpack_fp4(p, slots=slots) for p in pools]
+    assert np.array_equal(host(back[0]), fp4_oracle.decode(*fp4_oracle.encode(host(qkv[:, 2:3]).astype(np.float32))))
+    q = qkv[:n, :2].contiguous()
+    ws = sp.make_attention_fp4_workspace(q, 1, pools[0], kv_tokens=0)
+    out = sp.paged_attention_fp4(q, i32(0, n), i32(bs), i32(0)[None], *pools, window=60, ws=ws)
+    assert sp.device_status(ws) == 0
+    k, v = (host(x)[None] for x in back)
+    ref = paged_oracle.paged_attention(host(q), [0, n], [tail], np.zeros((1, 1), dtype=int), k, v, window=60)
+    check_attention(out, None, ref, [tail], d, "bf16", n, 6.0)
