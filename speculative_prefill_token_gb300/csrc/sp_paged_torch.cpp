@@ -26,6 +26,19 @@ namespace {
 // A Python error is already set.
 struct PythonError {};
 
+// A reference that is dropped at the end of its scope, a refusal's among them.
+struct Owned {
+    PyObject* o;
+    explicit Owned(PyObject* object) : o(object) {}
+    Owned(const Owned&) = delete;
+    ~Owned() { Py_XDECREF(o); }
+    PyObject* release() {
+        PyObject* r = o;
+        o = nullptr;
+        return r;
+    }
+};
+
 const at::Tensor* maybe(PyObject* o, const char* name) {
     if (o == Py_None) return nullptr;
     if (!THPVariable_Check(o)) refuse(std::string(name) + " must be a tensor");
@@ -398,15 +411,11 @@ PyObject* new_unpack_fp4(PyObject* const* a) {
     at::Tensor out;
     if (st) out = at::empty({st->numel(), p.heads, p.d}, pt.options().dtype(type));
     else out = at::empty({p.blocks, p.bs, p.heads, p.d}, pt.options().dtype(type));
-    PyObject* o = THPVariable_Wrap(out);
-    if (!o) throw PythonError();
-    PyObject* args[6] = {a[0], a[1], o, a[3], a[4], Py_None};
+    Owned o{THPVariable_Wrap(out)};
+    if (!o.o) throw PythonError();
+    PyObject* args[6] = {a[0], a[1], o.o, a[3], a[4], Py_None};
     const int rc = call_unpack_fp4(args);
-    if (rc != SP_OK) {
-        Py_DECREF(o);
-        return PyLong_FromLong(rc);
-    }
-    return o;
+    return rc == SP_OK ? o.release() : PyLong_FromLong(rc);
 }
 
 // The shape of an attention call over 4-bit pools (table_stride is left to the
@@ -491,10 +500,7 @@ int64_t call_workspace_fp4(PyObject* const* a) {
 int call_copy_kv(PyObject* const* a) {
     PyObject* list = PySequence_Fast(a[0], "pools must be a sequence of tensors");
     if (!list) throw PythonError();
-    struct Release {
-        PyObject* o;
-        ~Release() { Py_DECREF(o); }
-    } release{list};
+    const Owned release{list};
     const Py_ssize_t n = PySequence_Fast_GET_SIZE(list);
     if (n < 1 || n > SP_MAX_COPY_POOLS) refuse("give 1 to " + std::to_string(SP_MAX_COPY_POOLS) + " pools");
     const at::Tensor& first = need(PySequence_Fast_GET_ITEM(list, 0), "pools");

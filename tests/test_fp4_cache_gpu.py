@@ -218,3 +218,18 @@ def test_a_block_of_more_than_32_bits(d, bs):
     k, v = (host(x)[None] for x in back)
     ref = paged_oracle.paged_attention(host(q), [0, n], [tail], np.zeros((1, 1), dtype=int), k, v, window=60)
     check_attention(out, None, ref, [tail], d, "bf16", n, 6.0)
+
+
+def test_a_refused_read_keeps_no_memory():
+    import torch
+
+    import speculative_prefill_token_gb300 as sp
+    pool = torch.zeros(64, 2, 2, 576, dtype=torch.uint8, device="cuda")
+    slots = torch.zeros(1000, dtype=torch.int64, device="cuda")
+    status = torch.zeros(1, device="cuda")
+    sp.unpack_fp4(pool)
+    before = torch.cuda.memory_allocated()
+    for kw in (dict(slots=slots), dict(status=status), dict(scale="one"), dict(scale=float("inf")), dict(slots=slots[:0].float())):
+        with pytest.raises((ValueError, TypeError, sp.SpecPrefillError)):
+            sp.unpack_fp4(pool, **kw)
+        assert torch.cuda.memory_allocated() == before, kw
