@@ -11,6 +11,8 @@
 
 namespace sp {
 
+constexpr int kMaxForks = 16384;   // forks whose scan fits a CTA's shared memory
+
 cudaError_t launch_append_kv_fp4(const sp_append_fp4_shape* s, const uint16_t* q, const uint16_t* k,
                                  const uint16_t* v, const int32_t* slot_map, const int32_t* positions,
                                  const float* cos_sin, const int32_t* n_new, uint16_t* q_out, uint8_t* k_pool,

@@ -16,8 +16,6 @@
 namespace sp {
 namespace {
 
-constexpr int kMaxForks = 16384;   // forks whose scan fits a CTA's shared memory
-
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 using Pointers = std::initializer_list<const void*>;

@@ -575,9 +575,11 @@ cudaError_t launch_fork_blocks(const sp_pages_shape* s, const int32_t* src, cons
     a.pool_blocks = s->pool_blocks;
     a.free_cap = s->free_capacity;
     const size_t smem = 8 * static_cast<size_t>(a.F) + 4 * ((static_cast<size_t>(a.B) + 31) / 32);
+    // (the limit of the largest call, whatever this one takes: a smaller one set by another
+    // thread between these two calls would have the launch refused)
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(fork_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        constexpr int kMost = 8 * kMaxForks + 4 * ((kMaxTableSeqs + 31) / 32);
+        const cudaError_t e = cudaFuncSetAttribute(fork_blocks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess) return e;
     }
     const int64_t units = static_cast<int64_t>(a.F) * ((a.table_stride + kRun - 1) / kRun);

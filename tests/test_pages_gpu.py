@@ -302,3 +302,40 @@ def test_tokens_of_a_block_of_more_than_31_bits(d, bs):
     sp.copy_kv([pool], i32(near), i32(far - 1))
     assert torch.equal(sp.unpack_fp4(pool, slots=i32(far - 1)), want) and torch.equal(sp.unpack_fp4(pool, slots=i32(far)), want)
     assert not pool[0, 0, 4:-2].any()
+
+
+def test_forks_by_two_threads_at_once():
+    """Calls whose shared memory differs, through the C ABI (which leaves the interpreter's lock)."""
+    import ctypes
+    import threading
+
+    import torch
+
+    import speculative_prefill_token_gb300 as sp
+    from speculative_prefill_token_gb300 import pages
+    lib, failed = sp.load(), []
+
+    def caller(forks, stream):
+        rows, i32z = 8192, lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+        src, ctx, table, shared, free, n_free = i32z(forks) - 1, i32z(rows), i32z(rows * 4), i32z(64), i32z(64), i32z(1)
+        outs = [i32z(rows), i32z(forks), i32z(forks), i32z(1), i32z(1)]
+        torch.cuda.synchronize()
+        shape = pages._PagesShape(n_seqs=rows, n_forks=forks, block_size=16, table_stride=4, pool_blocks=64, free_capacity=64)
+        ptr = [t.data_ptr() for t in (src, src.clone(), ctx, table, shared, free, n_free, *outs)]
+        torch.cuda.synchronize()
+        for _ in range(3000):
+            rc = lib.sp_fork_blocks(ctypes.byref(shape), *ptr, stream.cuda_stream)
+            if rc:
+                failed.append((forks, rc))
+                break
+        stream.synchronize()
+        if int(outs[4]):
+            failed.append((forks, "status"))
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    threads = [threading.Thread(target=caller, args=a) for a in zip((16384, 6500), streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
