@@ -320,9 +320,11 @@ cudaError_t launch_block_tables(const sp_block_shape* s, const int32_t* ctx_len,
     a.pool_blocks = s->pool_blocks;
     a.shift = (a.bs & (a.bs - 1)) == 0 ? __builtin_ctz(a.bs) : -1;
     const size_t smem = (3 * static_cast<size_t>(a.B) + 1) * 4;
+    // (the limit of the largest call, whatever this one takes: a smaller one set by another
+    // thread between these two calls would have the launch refused)
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        constexpr int kMost = (3 * kMaxTableSeqs + 1) * 4;
+        const cudaError_t e = cudaFuncSetAttribute(block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
         if (e != cudaSuccess) return e;
     }
     const int64_t work = a.cap > a.B ? a.cap : a.B;

@@ -339,3 +339,37 @@ def test_forks_by_two_threads_at_once():
     for t in threads:
         t.join()
     assert not failed
+
+
+def test_tables_by_two_threads_at_once():
+    import ctypes
+    import threading
+
+    import torch
+
+    import speculative_prefill_token_gb300 as sp
+    from speculative_prefill_token_gb300 import paged
+    lib, failed = sp.load(), []
+
+    def caller(rows, stream):
+        i32z = lambda n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+        bufs = [i32z(rows), i32z(rows + 1), i32z(16), i32z(1), i32z(rows * 2), i32z(8), i32z(rows), i32z(1), i32z(1)]
+        torch.cuda.synchronize()
+        shape = paged._BlockShape(n_seqs=rows, block_size=16, table_stride=2, n_tokens=8, free_capacity=16, pool_blocks=16)
+        ptr = [t.data_ptr() for t in bufs]
+        for _ in range(3000):
+            rc = lib.sp_block_tables(ctypes.byref(shape), *ptr, stream.cuda_stream)
+            if rc:
+                failed.append((rows, rc))
+                break
+        stream.synchronize()
+        if int(bufs[-1]):
+            failed.append((rows, "status"))
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    threads = [threading.Thread(target=caller, args=a) for a in zip((16384, 4200), streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
