@@ -771,6 +771,8 @@ typedef struct sp_pages_shape {
     int32_t table_stride;  /* >= 1 entries of a table row */
     int32_t pool_blocks;   /* entries of shared; pool_blocks * block_size < 2^31 */
     int32_t free_capacity; /* entries of free_blocks */
+    int32_t alone;         /* sp_free_blocks: 1 refuses cuts inside a block that others hold (below), 0 makes them;
+                              sp_fork_blocks: 0 */
 } sp_pages_shape;
 
 /* Forks requests: row dst[i] of the table becomes a request with the cached
@@ -814,6 +816,13 @@ int sp_fork_blocks(const sp_pages_shape* shape, const int32_t* src, const int32_
  *   free_blocks is too short. The call then frees nothing: counts and list stay,
  *   kv_len is ctx_len, n_left is n_free. A block id outside [0, pool_blocks) also
  *   raises SP_ERR_DEVICE, and is counted nowhere.
+ * A cut may end inside a block that other requests hold as well (a request and its fork
+ * share a block until both have let it go). A request cut like that may be read, cut further
+ * and forked, but not filled further: sp_block_tables takes a begun block for the
+ * request's own, and its next tokens would overwrite those of the others. To go on with it, fork it
+ * into an empty row, which gets the begun block as a copy of its own, and free the row that was cut. With
+ * alone = 1 such a cut counts as a length out of range: SP_ERR_DEVICE, and the call frees
+ * nothing.
  * Outputs may not be inputs or one another (SP_ERR_INVALID_ARG). */
 int sp_free_blocks(const sp_pages_shape* shape, const int32_t* ctx_len, const int32_t* new_len,
                    const int32_t* block_table, int32_t* shared, int32_t* free_blocks,

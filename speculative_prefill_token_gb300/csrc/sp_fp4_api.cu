@@ -88,7 +88,7 @@ int check_fp4(const sp_fp4_shape* s) {
 int check_pages(const sp_pages_shape* s) {
     if (!s) return SP_ERR_INVALID_ARG;
     if (s->n_seqs < 1 || s->block_size < 1 || s->table_stride < 1 || s->pool_blocks < 1 || s->free_capacity < 0 ||
-        static_cast<int64_t>(s->pool_blocks) * s->block_size > INT32_MAX)
+        (s->alone != 0 && s->alone != 1) || static_cast<int64_t>(s->pool_blocks) * s->block_size > INT32_MAX)
         return SP_ERR_INVALID_ARG;
     return s->n_seqs > kMaxTableSeqs ? SP_ERR_UNSUPPORTED : SP_OK;
 }
@@ -229,7 +229,7 @@ int sp_fork_blocks(const sp_pages_shape* s, const int32_t* src, const int32_t* d
                    sp_stream_t stream) {
     const int rc = check_pages(s);
     if (rc != SP_OK) return rc;
-    if (s->n_forks < 1 || !src || !dst || !ctx_len || !block_table || !shared_count || !n_free || !kv_len ||
+    if (s->n_forks < 1 || s->alone != 0 || !src || !dst || !ctx_len || !block_table || !shared_count || !n_free || !kv_len ||
         !copy_src || !copy_dst || !n_left || (s->free_capacity > 0 && !free_blocks))
         return SP_ERR_INVALID_ARG;
     if (s->n_forks > kMaxForks) return SP_ERR_UNSUPPORTED;

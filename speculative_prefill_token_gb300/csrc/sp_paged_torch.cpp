@@ -585,17 +585,19 @@ int call_fork_blocks(PyObject* const* a) {
 }
 
 // (ctx_len, new_len, block_table, shared, free_blocks, n_free, block_size, kv_len,
-//  n_left, status, stream)
+//  n_left, status, alone, stream)
 int call_free_blocks(PyObject* const* a) {
     const at::Tensor &ctx = need(a[0], "ctx_len"), &free = need(a[4], "free_blocks");
     const int dev = device_of(ctx, "ctx_len");
     int32_t *tab, *shared;
-    const sp_pages_shape s = pages_shape(ctx, a[2], a[3], free, a[6], dev, &tab, &shared);
+    sp_pages_shape s = pages_shape(ctx, a[2], a[3], free, a[6], dev, &tab, &shared);
+    s.alone = PyObject_IsTrue(a[10]);
+    if (s.alone < 0) throw PythonError();
     return sp_free_blocks(&s, ints(&ctx, 1, "ctx_len", dev), ints(&need(a[1], "new_len"), s.n_seqs, "new_len", dev), tab, shared,
                           ints(&free, 0, "free_blocks", dev), ints(&need(a[5], "n_free"), 1, "n_free", dev),
                           ints(&need(a[7], "kv_len"), s.n_seqs, "kv_len", dev),
                           ints(&need(a[8], "n_left"), 1, "n_left", dev), ints(maybe(a[9], "status"), 1, "status", dev),
-                          stream_of(a[10], dev));
+                          stream_of(a[11], dev));
 }
 
 PyObject* wrapped(int64_t v) { return PyLong_FromLongLong(v); }
@@ -634,7 +636,7 @@ PyMethodDef methods[] = {
     SP_METHOD("workspace_fp4", int64_t, call_workspace_fp4, 5),
     SP_METHOD("copy_kv", int, call_copy_kv, 9),
     SP_METHOD("fork_blocks", int, call_fork_blocks, 14),
-    SP_METHOD("free_blocks", int, call_free_blocks, 11),
+    SP_METHOD("free_blocks", int, call_free_blocks, 12),
     {nullptr, nullptr, 0, nullptr},
 };
 

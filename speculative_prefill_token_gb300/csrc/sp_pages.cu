@@ -22,8 +22,9 @@
 // requests with lengths out of range alone; a second, one cluster of 8 CTAs, checks all
 // lengths, walks the counts in the order of the ids, each CTA a slice, and puts the
 // blocks at -1 behind the free ones. The order of the list is that of the ids, so it
-// does not depend on timing. After a length out of range, or a count below -1 (a block
-// let go too often), everything is put back.
+// does not depend on timing. After a length out of range, a count below -1 (a block
+// let go too often) or, on request, a cut inside a block that keeps other holders,
+// everything is put back.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -243,7 +244,7 @@ struct PageArgs {
     int32_t* copy_dst;
     int32_t* n_left;
     int32_t* status;
-    int B, F, bs, table_stride, pool_blocks, free_cap;
+    int B, F, bs, table_stride, pool_blocks, free_cap, alone;
 };
 
 __device__ __forceinline__ int blocks_for(int tokens, int bs) { return tokens / bs + (tokens % bs != 0); }
@@ -436,8 +437,15 @@ __global__ void __cluster_dims__(kSweepCtas, 1, 1) __launch_bounds__(kSweepThrea
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_free = *a.n_free;
     bool low = n_free < 0 || n_free > a.free_cap;   // something is wrong
-    for (int b = rank * kSweepThreads + tid; b < a.B; b += kSweepCtas * kSweepThreads)
-        low |= !cut_fits(a, a.ctx_len[b], a.new_len[b]);
+    for (int b = rank * kSweepThreads + tid; b < a.B; b += kSweepCtas * kSweepThreads) {
+        const int ctx = a.ctx_len[b], left = a.new_len[b];
+        if (!cut_fits(a, ctx, left)) {
+            low = true;
+        } else if (a.alone && left < ctx && left % a.bs != 0) {   // (the block that the cut leaves begun)
+            const int id = a.table[static_cast<int64_t>(b) * a.table_stride + left / a.bs];
+            low |= id >= 0 && id < a.pool_blocks && a.shared[id] > 0;
+        }
+    }
     // a slice of whole steps for each CTA
     const int64_t steps = (static_cast<int64_t>(a.pool_blocks) + kSweepPer - 1) / kSweepPer;
     const int64_t first = steps * rank / kSweepCtas, last = steps * (rank + 1) / kSweepCtas;
@@ -608,6 +616,7 @@ cudaError_t launch_free_blocks(const sp_pages_shape* s, const int32_t* ctx_len, 
     a.table_stride = s->table_stride;
     a.pool_blocks = s->pool_blocks;
     a.free_cap = s->free_capacity;
+    a.alone = s->alone;
     const int64_t units = static_cast<int64_t>(a.B) * ((a.table_stride + kRun - 1) / kRun);
     int64_t grid = (units + kDropThreads / 32 - 1) / (kDropThreads / 32);
     const int64_t most = int64_t(2) * device_sms();

@@ -10,6 +10,13 @@ the first. Several continuations of one prompt:
   ...                                                       # steps of the forks; later, where new_len is 0:
   kv_len, n_left = free_blocks(ctx_len, new_len, table, shared, free, n_free, block_size)
 
+A request whose cut ends inside a shared block goes on in another row (``row``, empty before):
+
+  kv_len, n_left = free_blocks(ctx_len, new_len, table, shared, free, n_free, block_size)
+  kv_len, copy_src, copy_dst, n_left = fork_blocks(cut, row, kv_len, table, shared, free, n_left, block_size)
+  copy_kv(pools, copy_src, copy_dst, rows=block_size)
+  kv_len, n_left = free_blocks(kv_len, without_cut, table, shared, free, n_left, block_size)
+
 The kept tokens of a cached prompt moved to blocks of their own (``new_table``
 has a row for each prompt, empty before):
 
@@ -32,7 +39,7 @@ class _CopyShape(ctypes.Structure):
 
 class _PagesShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("n_seqs", "n_forks", "block_size", "table_stride", "pool_blocks",
-                                              "free_capacity")]
+                                              "free_capacity", "alone")]
 
 
 def _bind(lib_):
@@ -88,19 +95,24 @@ def fork_blocks(src, dst, ctx_len, block_table, shared, free_blocks, n_free, blo
 
 
 def free_blocks(ctx_len, new_len, block_table, shared, free_blocks, n_free, block_size: int, kv_len=None, n_left=None,
-                status=None, stream=None):
+                status=None, stream=None, alone: bool = False):
     """(kv_len, n_left): every request cut from ctx_len[b] to new_len[b] cached
     tokens (0: it ends). Blocks that nobody holds any more go behind the n_free
     free ones in ``free_blocks`` (in place), in the order of their ids; ``n_left``
     counts the free ones afterwards. ``status`` as in block_tables: a call that
     fails (a block let go more often than held, a full list) frees nothing,
-    and its kv_len is ctx_len."""
+    and its kv_len is ctx_len.
+
+    A request cut inside a block that others hold as well may be read, but not
+    filled further: its next tokens would overwrite theirs. To go on with it, fork it
+    into an empty row, which gets the begun block as a copy of its own, and free the
+    row that was cut. ``alone=True`` refuses such cuts (status as for a bad length)."""
     if kv_len is None:
         kv_len = _new(ctx_len.numel(), ctx_len.dtype, ctx_len, stream)
     if n_left is None:
         n_left = _new(1, ctx_len.dtype, ctx_len, stream)
     rc = (paged._side or torch_side()).free_blocks(ctx_len, new_len, block_table, shared, free_blocks, n_free,
-                                                   block_size, kv_len, n_left, status, _handle(stream))
+                                                   block_size, kv_len, n_left, status, alone, _handle(stream))
     if rc:
         _check(rc, "sp_free_blocks")
     return kv_len, n_left

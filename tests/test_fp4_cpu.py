@@ -222,6 +222,11 @@ def test_fork_and_free_refusals(lib):
         assert _free(lib, **{n: P + 4096 * 20 + 1}) == 1, n
 
 
+def test_the_refusal_of_cuts_is_a_choice_of_frees_alone(lib):
+    assert _free(lib, dict(alone=2)) == 1 and _free(lib, dict(alone=-1)) == 1
+    assert _fork(lib, dict(alone=1)) == 1
+
+
 def test_pool_sizes():
     pool = sp.make_pool_fp4(3, 24, 2, 128, device="cpu")
     assert pool.shape == (3, 2, 3, 576) and not pool.any()
