@@ -58,7 +58,7 @@
 //                   store in turn. No pipe is full: a prompt of 2,700 tokens, 8 +
 //                   2 heads, has an instruction in 24 % of the issue slots, the
 //                   tensor and exponential pipes busy 15 % each
-//   single rows     latency: 9.5 us for a token over 512
+//   single rows     latency: 9.0 to 9.5 us for a token over 512
 //
 // Every mbarrier wait is bounded; a wait that gives up records SP_ERR_TIMEOUT
 // in the workspace status, and the CTA drains its copies and MMAs in flight
@@ -134,7 +134,7 @@ struct AttnArgs {
     const int32_t* q_off;
     const int32_t* kv_len;
     const int32_t* table;
-    const int32_t* only;   // [B] or null: requests below 0 are left out
+    const int32_t* only;   // with kOver, [B]: requests below 0 are left out
     const uint16_t* q;
     const uint16_t* k;
     const uint16_t* v;
@@ -156,8 +156,12 @@ struct AttnArgs {
     int hk_shift, hv_shift;  // rows of a K and of a V box, as powers of two
     uint32_t q_bytes;    // of one 64-element chunk of a query tile
     float scale2;
-    float out_scale;     // with `only`: factor of the result
+    float out_scale;     // with kOver: factor of the result
 };
+
+// kOver, of the kernels below: called over the 16-bit copy of a 4-bit cache (sp_fp4_attn.cu). Kernels of
+// their own, as the choice at run time took the others 0.2 of 9.5 us for one token over 512
+// and 0.4 of 50.9 for 24 mixed requests.
 
 // ------------------------------------------------------------ plan
 
@@ -260,6 +264,13 @@ __device__ __forceinline__ Start make_start(const AttnArgs& a, const T* pre, int
     return s;
 }
 
+// The same, not inlined: for the list of all starts, which CTA 0 makes beside its work. (The loop's
+// instructions between the start and the streams' loops moved the long chunk at d = 128 from 851 to 864 us.)
+template <typename T>
+__device__ __noinline__ Start listed_start(const AttnArgs& a, const T* pre, int items, T units, int c) {
+    return make_start(a, pre, items, units, c);
+}
+
 // (cache indices stay below 2^30, so that no sum of two of them leaves 31 bits)
 __device__ __forceinline__ bool bad_request(const AttnArgs& a, int64_t lo, int64_t hi, int64_t kv) {
     return hi < lo || hi > a.cap || kv < 0 || kv > kMaxCached || (kv + a.bs - 1) / a.bs > a.table_stride;
@@ -267,10 +278,15 @@ __device__ __forceinline__ bool bad_request(const AttnArgs& a, int64_t lo, int64
 
 // Requests that the caller computes elsewhere. It has looked at their lengths: their
 // contexts may be longer than this call's table holds.
-__device__ __forceinline__ bool left_out(const AttnArgs& a, int b) { return a.only && a.only[b] < 0; }
+template <bool kOver>
+__device__ __forceinline__ bool left_out(const AttnArgs& a, int b) {
+    if constexpr (kOver) return a.only[b] < 0;
+    else return false;
+}
 
 // Lays out a batch of any size, by one block of its own: items with their
 // costs, and the CTAs' ranges. Bound by the latency of its scans.
+template <bool kOver>
 __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, int tiles) {
     __shared__ int64_t sums[32];
     grid_dep_wait();
@@ -284,7 +300,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
         int64_t n = 0;
         if (b < a.B) {
             const int64_t lo = a.q_off[b], hi = a.q_off[b + 1];
-            if (!left_out(a, b)) {
+            if (!left_out<kOver>(a, b)) {
                 if (bad_request(a, lo, hi, a.kv_len[b])) bad = 1;
                 else n = (hi - lo + tpi - 1) / tpi;
             }
@@ -344,13 +360,14 @@ struct alignas(16) Range {
     Start begin, end;
 };
 
+template <bool kOver>
 __device__ __forceinline__ int local_plan(const AttnArgs& a, int tiles, LocalPlan& p, Range* range) {
     const int t = threadIdx.x;
     const int tpi = a.tq * tiles;
     int bad = 0, n = 0;
     if (t < a.B) {
         const int lo = a.q_off[t], hi = a.q_off[t + 1], kv = a.kv_len[t];
-        const bool out = left_out(a, t);
+        const bool out = left_out<kOver>(a, t);
         bad = (!out && bad_request(a, lo, hi, kv)) || (t == 0 && lo != 0);
         if (!bad && !out) n = (hi - lo + tpi - 1) / tpi;
         p.q0[t] = lo;
@@ -385,7 +402,7 @@ __device__ __forceinline__ int local_plan(const AttnArgs& a, int tiles, LocalPla
         else range->end = s;
     }
     if (blockIdx.x == 0) {   // for the list of cut items
-        for (int c = t; c <= a.grid && items > 0; c += kAttnThreads) a.starts[c] = make_start(a, p.pre, items, units, c);
+        for (int c = t; c <= a.grid && items > 0; c += kAttnThreads) a.starts[c] = listed_start(a, p.pre, items, units, c);
         for (int i = t; i <= items; i += kAttnThreads) a.pre[i] = p.pre[i];
         if (t == 0) {
             a.head->items = items;
@@ -974,27 +991,26 @@ struct RowEnd {
     bool join;
 };
 
-// Writes the rows of a warp, one per lane: results, or a part for the join
+// Writes the rows of a warp, one per lane: results, or (kSplit) a part for the join
 // kernel. Not inlined: the softmax loop keeps its registers. (Whole lines after
 // an exchange between quads took 1.4 times as long: the shuffles cost more
-// than the 32 lines of a store.)
-// (kScaled: a code of its own, as the factor takes a short call 0.3 us: one token 9.5 to 9.8.)
-template <int D, bool kBf16, bool kScaled>
+// than the 32 lines of a store. One code for both, with the choice at run time: one token
+// over 512 9.2 us in place of 9.0.)
+template <int D, bool kBf16, bool kOver, bool kSplit>
 __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
     constexpr int kCols = D > 128 ? D / 2 : D;    // columns of a warpgroup
     const bool mine = static_cast<int>(threadIdx.x & 31) < e.rows;
-    const bool split = e.part >= 0;
-    const bool none = e.l == 0.0f && !split;
+    const bool none = e.l == 0.0f && !kSplit;
     // (the approximate reciprocal and, for lse, logarithm are off by 2^-22: with
     // the exact ones out is the same to four digits of its error, lse is 0.5e-6 in
     // place of 0.7e-6 off at 8.5, where a step of 32 bits is 1e-6, and a prompt at
     // d = 256 and the mixed batch take 1 % longer)
-    const float inv = split ? 1.0f : none ? 0.0f : kScaled ? __fdividef(1.0f, e.l) * a.out_scale : __fdividef(1.0f, e.l);
+    const float inv = kSplit ? 1.0f : none ? 0.0f : kOver ? __fdividef(1.0f, e.l) * a.out_scale : __fdividef(1.0f, e.l);
     const float e0 = e.f0 * inv, e1 = e.f1 * inv;
-    char* dst = split ? reinterpret_cast<char*>(a.part_o + static_cast<int64_t>(e.part) * D + e.col0)
+    char* dst = kSplit ? reinterpret_cast<char*>(a.part_o + static_cast<int64_t>(e.part) * D + e.col0)
                       : reinterpret_cast<char*>(a.out + e.t * a.o_st + e.h * a.o_sh + e.col0);
     if (mine && e.col0 == 0) {
-        if (split) a.part_ml[e.part] = make_float2(e.m, e.l);
+        if constexpr (kSplit) a.part_ml[e.part] = make_float2(e.m, e.l);
         else if (a.lse) a.lse[e.t * a.G * a.hk + e.h] = none ? -INFINITY : (e.m - weight_bias(kBf16) + __log2f(e.l)) * kLn2;
     }
 #pragma unroll 1
@@ -1013,7 +1029,7 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
             for (int i = 0; i < 32; ++i) x[i] *= e0;
         }
         if (!mine) continue;
-        if (split) {
+        if constexpr (kSplit) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 store_32b(dst + q * 128 + i * 32, reinterpret_cast<const uint32_t*>(x + 8 * i));
@@ -1044,7 +1060,7 @@ struct RowsAgain {
 // the head dimension over its lanes: for segments in which a row is masked from
 // a value that is infinite or NaN (its zero weight would make the product NaN).
 // Slow, and right for any input.
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kOver>
 __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
     constexpr int E = D / 32;
     constexpr float kBias = weight_bias(kBf16);
@@ -1097,7 +1113,7 @@ __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
             uint16_t* o = a.out + t * a.o_st + h * a.o_sh + lane * E;
 #pragma unroll
             for (int i = 0; i < E; ++i) {
-                const uint32_t w = none ? 0u : pack_pair<kBf16>(acc[i] / l * a.out_scale, 0.0f);
+                const uint32_t w = none ? 0u : pack_pair<kBf16>(kOver ? acc[i] / l * a.out_scale : acc[i] / l, 0.0f);
                 o[i] = static_cast<uint16_t>(w & 0xffffu);
             }
             if (a.lse && lane == 0) a.lse[t * a.G * a.hk + h] = none ? -INFINITY : (m - kBias + __log2f(l)) * kLn2;
@@ -1109,7 +1125,7 @@ __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
 // time grows with the context (0.1 s and more at 40,000 keys), beyond what a
 // bounded wait may last. The segments are found by looking at their values once
 // more (as many flags as a range has segments have no place to stay).
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kOver>
 __device__ __noinline__ void flagged_rows(const AttnArgs& a, const Range* range, int items, int wg) {
     const int warp = threadIdx.x >> 5 & 3, lane = threadIdx.x & 31;
     Walk w(range, items);
@@ -1129,12 +1145,12 @@ __device__ __noinline__ void flagged_rows(const AttnArgs& a, const Range* range,
         e.row0 = warp * 32;
         e.rows = rows;
         e.part = s.split ? ((static_cast<int>(blockIdx.x) * 2 + (s.head ? 0 : 1)) * Smem<D>::kTiles + tile) * kRows : -1;
-        rows_again<D, kBf16>(a, e);
+        rows_again<D, kBf16, kOver>(a, e);
     }
 }
 
 // One warpgroup (index wg) of softmax threads over the CTA's segments.
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kOver>
 __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int items, int wg) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
@@ -1362,8 +1378,8 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                 e.m = m;
                 e.l = s.n > 0 ? l : 0.0f;
                 e.join = join;
-                if (a.only) write_rows<D, kBf16, true>(a, e);
-                else write_rows<D, kBf16, false>(a, e);
+                if (s.split) write_rows<D, kBf16, kOver, true>(a, e);
+                else write_rows<D, kBf16, kOver, false>(a, e);
             }
             if (s.n > 0) {
                 tc_fence_before();
@@ -1383,12 +1399,12 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
         }
     }
     // (this warp has seen the flag of every segment that is looked at)
-    if (ok && reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[2]) flagged_rows<D, kBf16>(a, c.range, items, wg);
+    if (ok && reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[2]) flagged_rows<D, kBf16, kOver>(a, c.range, items, wg);
 }
 
 // ------------------------------------------------------------ kernel
 
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kOver>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                 const __grid_constant__ CUtensorMap mv, const __grid_constant__ AttnArgs a) {
@@ -1447,7 +1463,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (aligned) {
         if (a.local_plan) {
             // the ring is scratch until the first copy into it
-            items = local_plan(a, L::kTiles, *reinterpret_cast<LocalPlan*>(attn_smem + L::ring), range);
+            items = local_plan<kOver>(a, L::kTiles, *reinterpret_cast<LocalPlan*>(attn_smem + L::ring), range);
             fence_proxy_async_smem();
         } else {
             items = a.head->items;
@@ -1473,7 +1489,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        if (work) softmax_rows<D, kBf16>(c, a, tmem, items, warp >> 2);
+        if (work) softmax_rows<D, kBf16, kOver>(c, a, tmem, items, warp >> 2);
     }
     tc_fence_before();
     __syncthreads();
@@ -1491,7 +1507,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // 64 columns of a row with many parts, which the 16 groups of a block share (the
 // L2 latency of 76 parts in turn would be the kernel's time), or of 32 rows with
 // few, two for each group.
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kOver>
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(const AttnArgs a) {
     using L = Smem<D>;
     constexpr float kBias = weight_bias(kBf16);
@@ -1544,8 +1560,7 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(co
         const Row zero{-INFINITY, 0.0f, make_float4(0.0f, 0.0f, 0.0f, 0.0f)};
         auto write = [&](Place x, const Row& y) {
             const bool none = y.sum == 0.0f;
-            float inv = none ? 0.0f : 1.0f / y.sum;
-            if (a.only) inv *= a.out_scale;
+            const float inv = none ? 0.0f : kOver ? 1.0f / y.sum * a.out_scale : 1.0f / y.sum;
             const int tok = x.row / a.G;
             const int64_t t = job.tok0 + x.tile * a.tq + tok;
             const int h = job.g * a.G + x.row - tok * a.G;
@@ -1719,17 +1734,29 @@ Layout layout(const sp_paged_shape* s, int grid) {
     return l;
 }
 
-template <int D>
+template <int D, bool kOver>
 cudaError_t launch_d(const AttnArgs& a, bool bf16, const CUtensorMap& mq, const CUtensorMap& mk,
                      const CUtensorMap& mv, cudaStream_t st) {
-    auto kern = bf16 ? attn_kernel<D, true> : attn_kernel<D, false>;
+    auto kern = bf16 ? attn_kernel<D, true, kOver> : attn_kernel<D, false, kOver>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(Smem<D>::total));
     if (e != cudaSuccess) return e;
     const cudaError_t r = launch_k(kern, static_cast<unsigned>(a.grid), kAttnThreads, Smem<D>::total, st, mq, mk, mv, a);
     if (r != cudaSuccess) return r;
-    return launch_k(bf16 ? attn_join_kernel<D, true> : attn_join_kernel<D, false>,
+    return launch_k(bf16 ? attn_join_kernel<D, true, kOver> : attn_join_kernel<D, false, kOver>,
                     static_cast<unsigned>(kJoinBlocks * a.grid), kJoinThreads, 0, st, a);
+}
+
+template <bool kOver>
+cudaError_t launch_all(const AttnArgs& a, int d, bool bf16, const CUtensorMap& mq, const CUtensorMap& mk,
+                       const CUtensorMap& mv, cudaStream_t st) {
+    if (!a.local_plan) {
+        const cudaError_t e = launch_k(attn_plan_kernel<kOver>, 1, kPlanThreads, 0, st, a, tiles_per_item(d));
+        if (e != cudaSuccess) return e;
+    }
+    return d == 64    ? launch_d<64, kOver>(a, bf16, mq, mk, mv, st)
+           : d == 128 ? launch_d<128, kOver>(a, bf16, mq, mk, mv, st)
+                      : launch_d<256, kOver>(a, bf16, mq, mk, mv, st);
 }
 
 }  // namespace
@@ -1807,13 +1834,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     const int64_t tiles = (static_cast<int64_t>(a.table_stride) * bs + kKeys - 1) / kKeys + a.item_cost;
     a.local_plan = l.items_max <= kLocalItems && a.B <= kLocalItems &&
                    tiles < INT32_MAX / kLocalItems / kMaxCtas / a.hk;
-    if (!a.local_plan) {
-        const cudaError_t e = launch_k(attn_plan_kernel, 1, kPlanThreads, 0, st, a, tiles_per_item(d));
-        if (e != cudaSuccess) return e;
-    }
-    return d == 64    ? launch_d<64>(a, bf16, mq, mk, mv, st)
-           : d == 128 ? launch_d<128>(a, bf16, mq, mk, mv, st)
-                      : launch_d<256>(a, bf16, mq, mk, mv, st);
+    return more ? launch_all<true>(a, d, bf16, mq, mk, mv, st) : launch_all<false>(a, d, bf16, mq, mk, mv, st);
 }
 
 }  // namespace sp
