@@ -707,9 +707,12 @@ int sp_paged_attention_fp4_workspace(const sp_fp4_shape* shape, size_t* bytes);
  * exact for elements down to 2^-31 of the row's largest.
  * Requests whose new tokens make many rows are computed over a 16-bit copy of
  * their cached tokens, in the workspace, as long as those of all such requests
- * of the call fit into dense_tokens (in the requests' order); the others,
- * all decode steps, and calls that n_tokens and the table's rows bound to little work are
- * computed from the 4-bit rows. A request with more new
+ * of the call fit into dense_tokens (in the requests' order: from the first that does not
+ * fit on, none is copied); the others, all decode steps, and calls that n_tokens and the
+ * table's rows bound to little work are computed from the 4-bit rows. The same call gives
+ * the same bits. A request's last bits may change with the requests beside it and with
+ * the table's width: they decide where its context is cut, and whether a chunk's weights
+ * are rounded to fp16 or to the tensors' type. A request with more new
  * tokens than max_new sets SP_ERR_DEVICE, and nothing is computed.
  * Cached rows that a query is masked from may hold anything, scales that are
  * NaN included; table entries of blocks that no row sees (behind the request's end,

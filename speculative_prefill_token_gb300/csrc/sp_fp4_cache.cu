@@ -14,11 +14,11 @@
 // correctly, and no quotient here overflows; one that underflows is far below the
 // smallest code's border).
 //
-// Bound: 39,322 tokens of 16/4 heads of 128 (bf16) are 322 MB of queries and 81 + 23 MB of
-// keys and values; the queries take 54 us (6.0 TB/s, the memory), keys and values 36 us: 17
-// instructions an element and the loads' latency before them (issue slots 55 % busy at 24
-// warps an SM; a thread's elements are under way before its slot and position are known,
-// 93 to 90 us in all; the next row's read ahead as well: no gain). 16 tokens of 8/2 heads of
+// 39,322 tokens of 16/4 heads of 128 (bf16) are 322 MB of queries and 81 + 23 MB of
+// keys and values; the queries take 54 us (6.0 TB/s, the memory), keys and values 36 us, 2.4 times
+// their bytes at a copy's rate: no pipe is full (17 instructions an element, issue slots 55 % busy), the
+// loads in flight wait in registers, 24 warps an SM (a thread's elements are under way before its slot and
+// position are known, 93 to 90 us in all; the next row's read ahead as well: no gain). 16 tokens of 8/2 heads of
 // 256: 2.3 us, a launch and three reads that follow one another.
 //
 // unpack_fp4_kernel. A thread turns 8 bytes of codes and a scale into 32 bytes (39,424 rows of 4 heads

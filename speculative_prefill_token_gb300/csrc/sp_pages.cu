@@ -6,8 +6,10 @@
 // copy_kv_kernel. A warp takes up to 32 tasks of one pool: a task is a row of all heads
 // (or, for whole blocks of a 4-bit pool, one head's records). Its lanes look the tasks'
 // places up side by side, and the warp copies 2 KB of them at a time, every load issued
-// before the first store. Bound by memory: 39,322 rows of 1 KB in two pools, a third of
-// a prompt's, 161 MB, 32.9 us, 4.9 TB/s; rows in order by the same kernel 5.2 TB/s.
+// before the first store. 39,322 rows of 1 KB in two pools, a third of a prompt's, 161 MB:
+// 32.9 us, 4.9 TB/s; whole blocks by the same kernel 5.1 to 5.4. Their tokens in 4 bits, 288 bytes in
+// four pools, 91 MB: 33.1 us, 2.7 TB/s. What bounds it is not shown: the kernels spill 56 to 136
+// bytes a thread, and each 16 bytes cost a division by the run's length.
 //
 // fork_blocks_kernel. With len_i the cached tokens of src_i, full_i = len_i / bs and
 // pre_i the begun blocks of the forks before i,
@@ -15,7 +17,8 @@
 //   table[dst_i][full_i] = free[n_free - 1 - pre_i]          if len_i % bs != 0.
 // Every CTA checks and scans all forks itself (no communication between CTAs),
 // and then takes its share of runs of 256 table entries. Counts go up by atomic
-// additions, whose order changes nothing.
+// additions, whose order changes nothing. (3,200 forks of 400 prompts: 21 us under ncu; each fork adds
+// to every count of its parent's blocks, and every CTA scans all forks.)
 //
 // free_blocks. One kernel takes a holder off every block that a request lets go
 // (shared[id] -= 1, so that a block that nobody holds any more is at -1), leaving

@@ -149,9 +149,11 @@ def make_attention_fp4_workspace(q, n_seqs: int, k_pool, max_new=None, kv_tokens
     the new tokens of a call) of ``n_seqs`` requests over pools like ``k_pool``;
     calls that share one must be ordered. Requests with many new tokens are
     computed over a 16-bit copy of their cached tokens in the workspace:
-    ``kv_tokens`` bounds those tokens (default: as many as the pool has;
-    requests that do not fit are computed from the 4-bit rows, more slowly).
-    With a small ``max_new``, the most new tokens of a request, none is needed."""
+    ``kv_tokens`` bounds those tokens (default: as many as the pool has, so that the
+    workspace is 3.6 times as large as both pools of a layer; one serves all layers).
+    Requests that do not fit are computed from the 4-bit rows, a long chunk several times
+    more slowly, and so is every one behind the first of them. With a small
+    ``max_new``, the most new tokens of a request, none is needed."""
     import torch
     dense = _dense(kv_tokens, k_pool)
     n = torch_side().workspace_fp4(q, n_seqs, k_pool, max_new, dense)
@@ -173,7 +175,7 @@ def paged_attention_fp4(q, q_off, kv_len, block_table, k_pool, v_pool, causal: b
     the same arguments, masks and outputs. ``max_new`` (default: the rows of q) is the most
     new tokens of a request; a decode step that says 1 launches less. ``ws`` from
     make_attention_fp4_workspace, with its status in device_status; without
-    it the call allocates one, whose status is lost."""
+    it the call allocates one (of the default size), whose status is lost."""
     if out is None:
         out = _new(q.shape, q.dtype, q, stream)
     if q.shape[0] == 0:
