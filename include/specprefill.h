@@ -701,8 +701,7 @@ int sp_paged_attention_fp4_workspace(const sp_fp4_shape* shape, size_t* bytes);
 /* sp_paged_attention over 4-bit pools: the same rows, masks, outputs and error
  * behaviour, with s_j = scale k_scale <q, k_j> and out = v_scale sum p v / sum p.
  * Logits, statistics and sums are held in 32 bits; weights are rounded to fp16
- * (scaled so that the largest is 2^6 to 2^14) for the product with the values, or to the
- * tensors' type where the values are read through 16 bits. bf16 queries are
+ * (scaled so that the largest is 2^6 to 2^14) for the product with the values. bf16 queries are
  * scaled by a power of two for each row and head and taken as fp16, which is
  * exact for elements down to 2^-31 of the row's largest.
  * Requests whose new tokens make many rows are computed over a 16-bit copy of
@@ -711,8 +710,7 @@ int sp_paged_attention_fp4_workspace(const sp_fp4_shape* shape, size_t* bytes);
  * fit on, none is copied); the others, all decode steps, and calls that n_tokens and the
  * table's rows bound to little work are computed from the 4-bit rows. The same call gives
  * the same bits. A request's last bits may change with the requests beside it and with
- * the table's width: they decide where its context is cut, and whether a chunk's weights
- * are rounded to fp16 or to the tensors' type. A request with more new
+ * the table's width, which decide where its context is cut and which way a chunk goes. A request with more new
  * tokens than max_new sets SP_ERR_DEVICE, and nothing is computed.
  * Cached rows that a query is masked from may hold anything, scales that are
  * NaN included; table entries of blocks that no row sees (behind the request's end,

@@ -96,6 +96,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // orders below the maximum, and the largest weight is 2^14.
 __host__ __device__ constexpr float weight_bias(bool bf16) { return bf16 ? 0.0f : 6.0f; }
 
+// Whether weights and values are bf16: of bf16 queries, but for the values of a 4-bit cache (kOver),
+// which fp16 holds as exactly and whose weights then keep three bits more (the long chunk's error of 0.0023
+// relative to 64 bits becomes 0.0017, that of the result's own rounding).
+__host__ __device__ constexpr bool bf16_values(bool bf16, bool over) { return bf16 && !over; }
+
 __host__ __device__ constexpr int tiles_per_item(int d) { return d <= 128 ? 2 : 1; }
 // A ring slot holds a whole K or V tile (d = 256: half of one): the MMA warp
 // waits once for each. (16 KB slots at d = 128: a wait before every four MMAs,
@@ -746,7 +751,7 @@ __device__ __forceinline__ bool odd_values(const AttnArgs& a, const Segment& s, 
 // a flagged segment; they take them one by one when their range is done. It
 // costs a prefill at d = 256 4 % of its time; by the softmax warps, from the
 // ring, it was 20 %.
-template <int D, bool kBf16>
+template <int D, bool kBf16V>
 __device__ __forceinline__ void check_values(const Ctx& c, const AttnArgs& a, int items, int lane) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
@@ -756,7 +761,7 @@ __device__ __forceinline__ void check_values(const Ctx& c, const AttnArgs& a, in
     while (w.next(a, s)) {
         if (!looked_at(a, s)) continue;
         if (!__all_sync(kAll, c.wait(L::seen + 8 * (n & 1), (n >> 1 & 1) ^ 1))) return;
-        const bool odd = odd_values<D, kBf16>(a, s, lane);
+        const bool odd = odd_values<D, kBf16V>(a, s, lane);
         if (lane == 0) {
             reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[n & 1] = odd;
             if (odd) reinterpret_cast<volatile uint32_t*>(c.smem + L::odd)[2] = 1;
@@ -776,12 +781,12 @@ __device__ __forceinline__ void check_values(const Ctx& c, const AttnArgs& a, in
 // with V_j and the product of the next keys with its queries. Its barriers are
 // polled together, one per lane: a wait costs some 200 cycles even when it is
 // over, and the MMA queue holds only a few instructions.
-template <int D, bool kBf16>
+template <int D, bool kBf16, bool kBf16V>
 __device__ __forceinline__ void issue_mma(const Ctx& c, const AttnArgs& a, uint32_t tmem_base, int items) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
     constexpr uint32_t kIdQk = idesc_f16_f32(kRows, kKeys, kBf16, false);
-    constexpr uint32_t kIdPv = idesc_f16_f32(kRows, D, kBf16, true);
+    constexpr uint32_t kIdPv = idesc_f16_f32(kRows, D, kBf16V, true);
     constexpr int P = L::kParts, kPer = L::kSlotKeys;
     // lane 0: weights; 1 .. P: V slots; P + 1 .. 2 P: K slots; then the accumulator
     constexpr unsigned kNeedV = ((1u << P) - 1) << 1, kNeedK = kNeedV << P, kNeedO = 1u << (2 * P + 1);
@@ -1011,7 +1016,7 @@ __device__ __noinline__ void write_rows(const AttnArgs& a, RowEnd e) {
                       : reinterpret_cast<char*>(a.out + e.t * a.o_st + e.h * a.o_sh + e.col0);
     if (mine && e.col0 == 0) {
         if constexpr (kSplit) a.part_ml[e.part] = make_float2(e.m, e.l);
-        else if (a.lse) a.lse[e.t * a.G * a.hk + e.h] = none ? -INFINITY : (e.m - weight_bias(kBf16) + __log2f(e.l)) * kLn2;
+        else if (a.lse) a.lse[e.t * a.G * a.hk + e.h] = none ? -INFINITY : (e.m - weight_bias(bf16_values(kBf16, kOver)) + __log2f(e.l)) * kLn2;
     }
 #pragma unroll 1
     for (int q = 0; q < kCols / 32; ++q) {
@@ -1056,6 +1061,15 @@ struct RowsAgain {
     int g, first, n, tok0, row0, rows, part;   // part < 0: the whole item is here
 };
 
+template <bool kBf16, int E>
+__device__ __forceinline__ void load_elements(const uint16_t* p, float (&x)[E]) {
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        if constexpr (kBf16) x[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
+        else x[i] = __half2float(__ushort_as_half(p[i]));
+    }
+}
+
 // The same rows without the tensor cores, by one warp, a row at a time with
 // the head dimension over its lanes: for segments in which a row is masked from
 // a value that is infinite or NaN (its zero weight would make the product NaN).
@@ -1063,15 +1077,8 @@ struct RowsAgain {
 template <int D, bool kBf16, bool kOver>
 __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
     constexpr int E = D / 32;
-    constexpr float kBias = weight_bias(kBf16);
+    constexpr float kBias = weight_bias(bf16_values(kBf16, kOver));
     const int lane = threadIdx.x & 31;
-    auto load = [&](const uint16_t* p, float (&x)[E]) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if constexpr (kBf16) x[i] = __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
-            else x[i] = __half2float(__ushort_as_half(p[i]));
-        }
-    };
     for (int r = e.row0; r < min(e.rows, e.row0 + 32); ++r) {
         const int tok = r / a.G, h = e.g * a.G + r - tok * a.G;
         const int64_t t = e.it.tok0 + e.tok0 + tok;
@@ -1079,7 +1086,7 @@ __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
         int hi = min(a.causal ? min(e.it.khi, pos + 1) : e.it.khi, (e.first + e.n) * kKeys);
         int lo = max(a.window > 0 ? max(pos - a.window + 1, 0) : 0, e.first * kKeys);
         float q[E], acc[E];
-        load(a.q + t * a.q_st + h * a.q_sh + lane * E, q);
+        load_elements<kBf16>(a.q + t * a.q_st + h * a.q_sh + lane * E, q);
 #pragma unroll
         for (int i = 0; i < E; ++i) acc[i] = 0.0f;
         float m = -INFINITY, l = 0.0f;
@@ -1089,7 +1096,7 @@ __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
             int64_t row = static_cast<int64_t>(id) * a.bs;
             row = id < 0 || row + a.bs > a.pool_tokens ? 0 : row + j - blk * a.bs;
             float x[E], y = 0.0f;
-            load(a.k + row * a.k_st + e.g * a.k_sh + lane * E, x);
+            load_elements<kBf16>(a.k + row * a.k_st + e.g * a.k_sh + lane * E, x);
 #pragma unroll
             for (int i = 0; i < E; ++i) y += q[i] * x[i];
 #pragma unroll
@@ -1098,7 +1105,7 @@ __device__ __noinline__ void rows_again(const AttnArgs& a, const RowsAgain e) {
             const float mn = fmaxf(m, y), base = mn == -INFINITY ? 0.0f : mn;
             const float f = mn == m ? 1.0f : exp2_ftz(m - mn), p = exp2_ftz(y - base + kBias);
             l = l * f + p;
-            load(a.v + row * a.v_st + e.g * a.v_sh + lane * E, x);
+            load_elements<bf16_values(kBf16, kOver)>(a.v + row * a.v_st + e.g * a.v_sh + lane * E, x);
 #pragma unroll
             for (int i = 0; i < E; ++i) acc[i] = acc[i] * f + p * x[i];
             m = mn;
@@ -1135,7 +1142,7 @@ __device__ __noinline__ void flagged_rows(const AttnArgs& a, const Range* range,
         const int tile = two ? wg : 0;
         const int rows = min(max(s.it.ntok - tile * a.tq, 0), a.tq) * a.G;
         if (wg == 1 && !two) continue;   // (the first warpgroup's rows)
-        if (warp * 32 >= rows || !looked_at(a, s) || !odd_values<D, kBf16>(a, s, lane)) continue;
+        if (warp * 32 >= rows || !looked_at(a, s) || !odd_values<D, bf16_values(kBf16, kOver)>(a, s, lane)) continue;
         RowsAgain e;
         e.it = s.it;
         e.g = s.g;
@@ -1154,7 +1161,7 @@ template <int D, bool kBf16, bool kOver>
 __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, uint32_t tmem, int items, int wg) {
     using L = Smem<D>;
     constexpr unsigned kAll = 0xffffffffu;
-    constexpr float kBias = weight_bias(kBf16);
+    constexpr float kBias = weight_bias(bf16_values(kBf16, kOver));
     const int warp = threadIdx.x >> 5 & 3, lane = threadIdx.x & 31;
     const int row = warp * 32 + lane;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
@@ -1273,7 +1280,7 @@ __device__ __forceinline__ void softmax_rows(const Ctx& c, const AttnArgs& a, ui
                             x.x = exp2_ftz(x.x);
                             x.y = exp2_ftz(x.y);
                             sum[i & 3] = (q == 0 && i < 4) ? x : add2(sum[i & 3], x);
-                            pk[i] = pack_pair<kBf16>(x.x, x.y);
+                            pk[i] = pack_pair<bf16_values(kBf16, kOver)>(x.x, x.y);
                         }
                         tmem_st_32x32b_x16(st + 16 * q, pk);
                     }
@@ -1480,11 +1487,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (work) {
             if (warp == kLoadWarp) load_keys<D>(c, a, &mk, &mv, items, lane);
-            else if (warp == kMmaWarp) issue_mma<D, kBf16>(c, a, tmem, items);
+            else if (warp == kMmaWarp) issue_mma<D, kBf16, bf16_values(kBf16, kOver)>(c, a, tmem, items);
             else if (warp == kQWarp && lane == 0) load_queries<D>(c, a, &mq, items);
         }
         if (warp == kListWarp) {
-            if (work) check_values<D, kBf16>(c, a, items, lane);
+            if (work) check_values<D, bf16_values(kBf16, kOver)>(c, a, items, lane);
             if (blockIdx.x == 0 && aligned) list_cuts(a, L::kChunks, lane);
         }
     } else {
@@ -1510,7 +1517,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 template <int D, bool kBf16, bool kOver>
 __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_join_kernel(const AttnArgs a) {
     using L = Smem<D>;
-    constexpr float kBias = weight_bias(kBf16);
+    constexpr float kBias = weight_bias(bf16_values(kBf16, kOver));
     __shared__ Job job_s[kMaxCtas];
     __shared__ float2 ml_s[kMaxCtas];
     __shared__ float4 acc_s[kJoinGroups][16];
@@ -1824,7 +1831,7 @@ cudaError_t launch_paged_attention(const sp_paged_shape* s, const sp_attn_params
     if (!make_map(&mq, bf16, q, d, s->n_q_heads, s->q_stride_head, s->n_tokens, s->q_stride_token, a.G, a.tq) ||
         !make_pool_map(&mk, bf16, k_pool, d, s->pool_tokens, s->k_stride_token, a.hk, s->k_stride_head, hk,
                        d / 64 / slots_per_tile(d)) ||
-        !make_pool_map(&mv, bf16, v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, hv,
+        !make_pool_map(&mv, bf16_values(bf16, more != nullptr), v_pool, d, s->pool_tokens, s->v_stride_token, a.hk, s->v_stride_head, hv,
                        d / 64))
         return cudaErrorInvalidValue;
     // (a prompt of 4,916 tokens at d = 256: 102 us with 32-byte stores, 114 with 16)

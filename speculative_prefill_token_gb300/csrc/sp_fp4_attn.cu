@@ -1418,7 +1418,7 @@ __global__ void __launch_bounds__(kDenseThreads) fp4_dense_kernel(const DenseArg
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     o[i] = mul_f16x2(n[i], s);
-                    if constexpr (kBf16) {   // (exact: 6 significant bits)
+                    if (kBf16 && !v) {   // (exact: 6 significant bits; values stay fp16, as their weights are)
                         const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
                         const __nv_bfloat162 w = __floats2bfloat162_rn(f.x, f.y);
                         o[i] = *reinterpret_cast<const uint32_t*>(&w);

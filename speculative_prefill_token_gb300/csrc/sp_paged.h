@@ -35,7 +35,8 @@ cudaError_t launch_append_kv(const sp_append_shape* s, const uint16_t* q, const 
 // Bytes of workspace of the attention (header included).
 size_t attn_workspace(const sp_paged_shape* s);
 
-// What a caller inside the library may ask for besides (sp_fp4_attn.cu).
+// What a caller inside the library may ask for besides (sp_fp4_attn.cu); the values are then fp16,
+// whatever the type of queries, keys and results.
 struct AttnMore {
     const int32_t* only;   // device [B]: requests below 0 are left out
     int32_t* status;       // in place of the workspace's

@@ -8,6 +8,7 @@ import pytest
 from oracle import paged_oracle
 from tests.fp4_cases import attention_bounds, check_attention, dev, fp4_case
 from tests.paged_cases import host
+from tests.test_fp4_rows_gpu import bound_of_fp16_weights
 
 pytestmark = pytest.mark.gpu
 
@@ -178,3 +179,14 @@ def test_captured_chunks_and_steps_share_a_workspace():
         for c, out in zip(cases, outs):
             assert torch.equal(out, attend(dict(c, kv_len=kv), window=300)[0])
     assert sp.device_status(ws) == 0
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_weights_have_11_bits(d):
+    """As they have on the 4-bit rows: a bf16 chunk's error does not depend on the way it goes."""
+    c = fp4_case(d, [3000, 0, 1], [150, 140, 1], 8, 2, d, 32, "bf16", factor=(0.5, 2.0))
+    ref = paged_oracle.paged_attention(host(c["q"]), host(c["q_off"]), host(c["kv_len"]), host(c["table"]),
+                                       np.nan_to_num(c["k"]), np.nan_to_num(c["v"]))
+    out, _, status = attend(c, [0, 1])
+    assert status == 0
+    assert (np.abs(host(out) - ref[0]) <= bound_of_fp16_weights(c, ref)).all()
